@@ -14,6 +14,7 @@ QLORA_OK = 0
 QLORA_OP_FWD, QLORA_OP_BWD, QLORA_OP_GEMV, QLORA_OP_LORA = 0, 1, 2, 3
 QLORA_OP_FWD_FUSED, QLORA_OP_BWD_FUSED = 4, 5
 QLORA_OP_GROUP_FWD, QLORA_OP_GROUP_BWD, QLORA_OP_GROUP_LORA, QLORA_OP_BF16_DX = 6, 7, 8, 9
+QLORA_OP_BWD_DROP, QLORA_OP_I8_FWD, QLORA_OP_I8_BWD = 10, 11, 12
 
 STATUS_NAMES = {
     0: "QLORA_OK", 1: "QLORA_E_NULL", 2: "QLORA_E_ALIGN", 3: "QLORA_E_SHAPE",
@@ -35,6 +36,9 @@ EXPORTS = [
     "qlora_group_dequant", "qlora_group_dequant_t", "qlora_bf16_group_fwd", "qlora_bf16_group_dx",
     "qlora_group_lora_dy_b", "qlora_group_lora_grads",
     "qlora_level_table_id", "qlora_qtensor_header_write", "qlora_qtensor_header_read",
+    "qlora_dropout", "qlora_linear_fwd_drop", "qlora_linear_bwd_drop",
+    "qlora_i8_row_bytes", "qlora_i8_quantize", "qlora_i8_dequant", "qlora_i8_matmul",
+    "qlora_i8_linear_fwd", "qlora_i8_linear_bwd",
 ]
 QLORA_PAGED_LOAD, QLORA_PAGED_STORE = 1, 2
 
@@ -91,6 +95,26 @@ class PagedLayoutDesc(ctypes.Structure):
         ("resident_bytes", ctypes.c_size_t),
         ("chunk", ctypes.c_size_t),
         ("staging_bytes", ctypes.c_size_t),
+    ]
+
+
+class DropDesc(ctypes.Structure):
+    """qlora_drop."""
+    _fields_ = [
+        ("p", ctypes.c_double),
+        ("seed", ctypes.c_uint64),
+        ("offset", ctypes.c_uint64),
+        ("step", ctypes.c_void_p),
+    ]
+
+
+class I8RowsDesc(ctypes.Structure):
+    """qlora_i8_rows."""
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("codes", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
     ]
 
 
@@ -197,6 +221,25 @@ def lib():
     L.qlora_qtensor_header_read.restype = ctypes.c_int
     L.qlora_qtensor_header_read.argtypes = [ctypes.c_char_p, sz, ctypes.POINTER(Nf4WeightDesc),
                                             ctypes.POINTER(ctypes.c_uint64)]
+    D, Q = ctypes.POINTER(DropDesc), ctypes.POINTER(I8RowsDesc)
+    L.qlora_dropout.restype = ctypes.c_int
+    L.qlora_dropout.argtypes = [vp, i64, D, vp, vp]
+    L.qlora_linear_fwd_drop.restype = ctypes.c_int
+    L.qlora_linear_fwd_drop.argtypes = [W, vp, i64, vp, vp, i32, f32, D, vp, vp, vp, sz, vp]
+    L.qlora_linear_bwd_drop.restype = ctypes.c_int
+    L.qlora_linear_bwd_drop.argtypes = [W, vp, vp, i64, vp, vp, i32, f32, vp, D, vp, vp, vp, vp, sz, vp]
+    L.qlora_i8_row_bytes.restype = sz
+    L.qlora_i8_row_bytes.argtypes = [i64]
+    L.qlora_i8_quantize.restype = ctypes.c_int
+    L.qlora_i8_quantize.argtypes = [vp, Q, vp]
+    L.qlora_i8_dequant.restype = ctypes.c_int
+    L.qlora_i8_dequant.argtypes = [Q, vp, vp]
+    L.qlora_i8_matmul.restype = ctypes.c_int
+    L.qlora_i8_matmul.argtypes = [Q, Q, vp, vp]
+    L.qlora_i8_linear_fwd.restype = ctypes.c_int
+    L.qlora_i8_linear_fwd.argtypes = [Q, vp, i64, vp, vp, i32, f32, D, vp, vp, vp, sz, vp]
+    L.qlora_i8_linear_bwd.restype = ctypes.c_int
+    L.qlora_i8_linear_bwd.argtypes = [Q, vp, vp, i64, vp, vp, i32, f32, vp, D, vp, vp, vp, vp, sz, vp]
     _lib = L
     return L
 

@@ -16,6 +16,12 @@
 // times, so it is taken from kStagedMinTokens tokens on, when the workspace
 // holds the bf16 weight.
 //   GEMV        : per job, 128 fp32 for u = A x | the device job table
+//   BWD_DROP, I8_BWD : G as two bf16 parts [M x r] each | U bf16 [M x r] |
+//                 split partials | deq(W)^T bf16 [K x Np] | dY bf16 [M x Np]
+//                 when N % 64 != 0 (Np = N rounded up to 64, zero columns) |
+//                 the dense product's split partials, if it splits
+//   I8_FWD      : X as 8-bit rows [M x i8_row_bytes(K)] | their scales fp32
+//                 [M] | U bf16 [M x r] | split partials of X A^T
 // qlora_linear_fwd_noalloc carves the FWD layout out of `scratch` below
 // instead of a caller workspace.
 #include <hip/hip_runtime.h>
@@ -177,6 +183,93 @@ size_t lora_part_bytes(int64_t M, int64_t N, int64_t K, int32_t r) {
   return align_up(p);
 }
 
+// A dropout specification as the kernels take it.  *active: whether anything
+// is dropped (p may round to 0 in steps of 1/65536).
+qlora_status check_drop(const qlora_drop* d, DropArgs* out, bool* active) {
+  *active = false;
+  if (!d) return QLORA_OK;
+  if (!(d->p >= 0.0 && d->p < 1.0)) return QLORA_E_UNSUPPORTED;   // NaN too
+  if (reinterpret_cast<uintptr_t>(d->step) & 7u) return QLORA_E_ALIGN;
+  const int t = std::min(65535, (int)(65536.0 * d->p + 0.5));
+  out->seed = d->seed;
+  out->offset = d->offset;
+  out->step = d->step;
+  out->thr = t - 32768;
+  out->scale = (float)(65536.0 / (double)(65536 - t));
+  *active = t > 0;
+  return QLORA_OK;
+}
+
+int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
+
+// The backward of an adapter under dropout and of the 8-bit linear: always
+// staged, for any number of tokens (deq(W)^T is written once; below 1024
+// tokens that costs what the fused kernels save, and they have no masked
+// tail).
+struct DropBwdLayout {
+  size_t hi, lo, u, part, wdt, dyp, split, split_bytes, total;
+};
+DropBwdLayout drop_bwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool with_dx) {
+  DropBwdLayout L{};
+  const int64_t np = up64(N);
+  if (r > 0) {
+    const size_t mr = align_up((size_t)M * r * 2);
+    L.lo = mr;
+    L.u = 2 * mr;
+    L.part = 3 * mr;
+    L.total = L.part + lora_part_bytes(M, N, K, r);
+  }
+  if (with_dx) {
+    L.wdt = L.total;
+    L.dyp = L.wdt + align_up((size_t)np * (size_t)K * 2);
+    L.split = L.dyp + (np != N ? align_up((size_t)M * (size_t)np * 2) : 0);
+    L.split_bytes = dense_split_bytes(K, np, M);
+    L.total = L.split + align_up(L.split_bytes);
+  }
+  return L;
+}
+// Np K, M Np below 2^31 elements (32-bit byte offsets), the transposing
+// dequantization's grid rows.
+bool drop_bwd_ok(int64_t M, int64_t N, int64_t K) {
+  const int64_t np = up64(N);
+  return np <= (int64_t)0x7FFFFFFF / K && np <= (int64_t)0x7FFFFFFF / M && np / 64 <= 65535;
+}
+
+struct I8FwdLayout {
+  size_t xq, sx, u, part, total;
+};
+I8FwdLayout i8_fwd_layout(int64_t M, int64_t K, int32_t r) {
+  I8FwdLayout L{};
+  L.sx = align_up((size_t)M * (size_t)i8_row_bytes(K));
+  L.u = L.sx + align_up((size_t)M * sizeof(float));
+  L.part = L.total = L.u;
+  if (r > 0) {
+    L.part = L.u + align_up((size_t)M * r * 2);
+    L.total = L.part + align_up(skinny_partial_bytes(M, r, K, kXAt));
+  }
+  return L;
+}
+
+// A weight (or an input) as rows of 8-bit integers.
+qlora_status check_i8(const qlora_i8_rows* q) {
+  if (!q) return QLORA_E_NULL;
+  if (q->rows <= 0 || q->cols <= 0) return QLORA_E_SHAPE;
+  if (q->cols % 8 != 0 || q->cols > kI8MaxCols) return QLORA_E_UNSUPPORTED;
+  if (q->rows > (int64_t)0x7FFFFFFF / i8_row_bytes(q->cols)) return QLORA_E_UNSUPPORTED;
+  if (!q->codes || !q->scale) return QLORA_E_NULL;
+  if (!aligned16(q->codes) || !aligned16(q->scale)) return QLORA_E_ALIGN;
+  return QLORA_OK;
+}
+// An 8-bit weight in a product with M tokens.
+qlora_status check_i8_product(const qlora_i8_rows* W, int64_t M) {
+  const qlora_status st = check_i8(W);
+  if (st != QLORA_OK) return st;
+  if (W->rows % 8 != 0) return QLORA_E_UNSUPPORTED;
+  if (M <= 0 || M > 0x7FFFFFFF) return QLORA_E_SHAPE;
+  if (M > (int64_t)0x7FFFFFFF / i8_row_bytes(W->cols) || M > (int64_t)0x7FFFFFFF / W->rows) return QLORA_E_UNSUPPORTED;
+  return QLORA_OK;
+}
+
 // Layer-set groups: G weights of one shape N x K read the same input, with
 // the adapters stacked (A [G r x K], B [G N x r]) and the outputs side by
 // side (Y, dY [M x G N]).  Always staged.
@@ -294,7 +387,7 @@ qlora_status check_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, 
 // The forward's launches, on a workspace of the FWD layout.
 qlora_status run_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, const uint16_t* A,
                      const uint16_t* B, int32_t r, float alpha, uint16_t* Y, uint16_t* U_save, void* ws,
-                     bool staged, hipStream_t s) {
+                     bool staged, hipStream_t s, const DropArgs* drop = nullptr) {
   const FwdLayout L = fwd_layout(M, W->rows, W->cols, r, staged);
   const Nf4View v = view(W);
   const bf16_t* U = nullptr;
@@ -303,7 +396,8 @@ qlora_status run_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, co
     sc = (float)((double)alpha / (double)r);  // s = RN32(alpha / r)
     bf16_t* Ud = U_save ? U_save : reinterpret_cast<bf16_t*>(ws_at(ws, L.u));
     float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
-    qlora_status st = hip_status(launch_xat(X, A, M, W->cols, r, part, Ud, nullptr, 1.0f, s));
+    qlora_status st = hip_status(drop ? launch_xat_drop(X, A, M, W->cols, r, drop, part, Ud, s)
+                                      : launch_xat(X, A, M, W->cols, r, part, Ud, nullptr, 1.0f, s));
     if (st != QLORA_OK) return st;
     U = Ud;
   }
@@ -413,6 +507,13 @@ size_t qlora_workspace_bytes(qlora_op op, int64_t M, int64_t N, int64_t K, int32
     case QLORA_OP_BF16_DX:
       if (!group_sizes_ok(M, N, K, r, njobs)) return 0;
       return dense_split_bytes(K, (int64_t)njobs * N, M);
+    case QLORA_OP_BWD_DROP:
+    case QLORA_OP_I8_BWD:
+      if (M <= 0 || N <= 0 || K <= 0 || r < 0 || r > kMaxRank || !drop_bwd_ok(M, N, K)) return 0;
+      return drop_bwd_layout(M, N, K, r, true).total;
+    case QLORA_OP_I8_FWD:
+      if (M <= 0 || K <= 0 || K > kI8MaxCols || M > 0x7FFFFFFF / K || r < 0 || r > kMaxRank) return 0;
+      return i8_fwd_layout(M, K, r).total;
   }
   return 0;
 }
@@ -590,6 +691,203 @@ qlora_status qlora_linear_bwd(const qlora_nf4_weight* W, const uint16_t* X, cons
     if (st != QLORA_OK) return st;
   }
   return hip_status(launch_grads(G, X, dY, N, U, r, M, N, K, r, 1, part, dA, dB, sc, s));
+}
+
+qlora_status qlora_dropout(const uint16_t* x, int64_t n, const qlora_drop* drop, uint16_t* y, void* stream) {
+  if (!x || !y || !drop) return QLORA_E_NULL;
+  if (!aligned16(x) || !aligned16(y)) return QLORA_E_ALIGN;
+  if (n <= 0 || n > ((int64_t)1 << 40)) return QLORA_E_SHAPE;
+  DropArgs d{};
+  bool active;
+  const qlora_status st = check_drop(drop, &d, &active);
+  if (st != QLORA_OK) return st;
+  return hip_status(launch_dropout(x, n, d, y, (hipStream_t)stream));
+}
+
+qlora_status qlora_linear_fwd_drop(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, const uint16_t* A,
+                                   const uint16_t* B, int32_t r, float alpha, const qlora_drop* drop, uint16_t* Y,
+                                   uint16_t* U_save, void* ws, size_t ws_bytes, void* stream) {
+  qlora_status st = check_fwd(W, X, M, A, B, r, Y, U_save);
+  if (st != QLORA_OK) return st;
+  if (r == 0) return QLORA_E_UNSUPPORTED;   // no adapter, nothing to drop
+  if (!drop) return QLORA_E_NULL;
+  DropArgs d{};
+  bool active;
+  if ((st = check_drop(drop, &d, &active)) != QLORA_OK) return st;
+  const bool staged = staged_ok(M, W->rows, W->cols) &&
+                      ws_bytes >= fwd_layout(M, W->rows, W->cols, r, true).total;
+  if ((st = check_ws(ws, ws_bytes, fwd_layout(M, W->rows, W->cols, r, staged).total)) != QLORA_OK) return st;
+  return run_fwd(W, X, M, A, B, r, alpha, Y, U_save, ws, staged, (hipStream_t)stream, active ? &d : nullptr);
+}
+
+namespace {
+
+// Argument checks of the staged backwards, before any workspace is looked at.
+qlora_status check_bwd(int64_t M, int64_t N, int64_t K, const uint16_t* X, const uint16_t* dY, const uint16_t* A,
+                       const uint16_t* B, int32_t r, const uint16_t* U_saved, const uint16_t* dX, const float* dA,
+                       const float* dB) {
+  if (!drop_bwd_ok(M, N, K)) return QLORA_E_UNSUPPORTED;
+  if (!dY) return QLORA_E_NULL;
+  if (!aligned16(dY) || (dX && !aligned16(dX)) || (U_saved && !aligned16(U_saved))) return QLORA_E_ALIGN;
+  const qlora_status st = check_rank(r, A, B);
+  if (st != QLORA_OK) return st;
+  if (r > 0) {
+    if (!dA || !dB || !X) return QLORA_E_NULL;
+    if (!aligned16(dA) || !aligned16(dB) || !aligned16(X)) return QLORA_E_ALIGN;
+    if (!skinny_cols_ok(K) || !skinny_cols_ok(N)) return QLORA_E_UNSUPPORTED;
+  } else if (dA || dB) {
+    return QLORA_E_SHAPE;   // no adapter, no adapter gradients
+  }
+  return QLORA_OK;
+}
+
+// deq(W)^T of either format: out [K x ldo], the columns past N zero.
+qlora_status weight_t(const qlora_nf4_weight* W, const qlora_i8_rows* W8, bf16_t* out, int64_t ldo, hipStream_t s) {
+  if (W8) return hip_status(launch_i8_dequant_t(W8->codes, W8->scale, W8->rows, W8->cols, out, ldo, s));
+  const int64_t N = W->rows, K = W->cols;
+  const qlora_status st = hip_status(
+      launch_dequant_t(W->codes, W->absmax_q, W->group_scale, N, K, W->codebook, W->absmax_format, out, ldo, s));
+  if (st != QLORA_OK || ldo == N) return st;
+  return hip_status(launch_pad_rows(nullptr, K, N, out, ldo, s));
+}
+
+// The staged backward's launches on validated arguments, for the weight W or
+// (not null) W8.
+qlora_status run_bwd(const qlora_nf4_weight* W, const qlora_i8_rows* W8, int64_t M, int64_t N, int64_t K, const uint16_t* X, const uint16_t* dY, const uint16_t* A,
+                     const uint16_t* B, int32_t r, float alpha, const uint16_t* U, const DropArgs* drop, uint16_t* dX,
+                     float* dA, float* dB, void* ws, hipStream_t s) {
+  const DropBwdLayout L = drop_bwd_layout(M, N, K, r, dX != nullptr);
+  const int64_t np = up64(N);
+  qlora_status st;
+  const float sc = r > 0 ? (float)((double)alpha / (double)r) : 0.0f;
+  bf16_t* hi = reinterpret_cast<bf16_t*>(ws_at(ws, L.hi));
+  bf16_t* lo = reinterpret_cast<bf16_t*>(ws_at(ws, L.lo));
+  float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
+  if (r > 0 && !U) {
+    bf16_t* Ud = reinterpret_cast<bf16_t*>(ws_at(ws, L.u));
+    if ((st = hip_status(launch_xat_drop(X, A, M, K, r, drop, part, Ud, s))) != QLORA_OK) return st;
+    U = Ud;
+  }
+  auto run_g = [&]() { return hip_status(launch_dyb_hl(dY, B, M, N, r, part, hi, lo, s)); };
+  if (dX) {
+    bf16_t* WdT = reinterpret_cast<bf16_t*>(ws_at(ws, L.wdt));
+    const bf16_t* g = dY;
+    const bool late = dy_late(M, N);
+    if (r > 0 && !late && (st = run_g()) != QLORA_OK) return st;
+    if ((st = weight_t(W, W8, WdT, np, s)) != QLORA_OK) return st;
+    if (np != N) {
+      bf16_t* dyp = reinterpret_cast<bf16_t*>(ws_at(ws, L.dyp));
+      if ((st = hip_status(launch_pad_rows(dY, M, N, dyp, np, s))) != QLORA_OK) return st;
+      g = dyp;
+    }
+    if (r > 0 && late && (st = run_g()) != QLORA_OK) return st;
+    float* split = reinterpret_cast<float*>(ws_at(ws, L.split));
+    st = hip_status(r > 0 && drop
+                        ? launch_bf16_dx_drop(WdT, K, np, g, M, hi, A, r, sc, *drop, dX, s, split, L.split_bytes)
+                        : launch_bf16_fwd(WdT, K, np, g, M, r > 0 ? hi : nullptr, r > 0 ? A : nullptr, true, r, sc, dX,
+                                          s, split, L.split_bytes));
+    if (st != QLORA_OK) return st;
+  } else if (r > 0 && (st = run_g()) != QLORA_OK) {
+    return st;
+  }
+  if (r == 0) return QLORA_OK;
+  return hip_status(launch_grads_hl(hi, lo, X, dY, U, M, N, K, r, drop, part, dA, dB, sc, s));
+}
+
+}  // namespace
+
+qlora_status qlora_linear_bwd_drop(const qlora_nf4_weight* W, const uint16_t* X, const uint16_t* dY, int64_t M,
+                                   const uint16_t* A, const uint16_t* B, int32_t r, float alpha,
+                                   const uint16_t* U_saved, const qlora_drop* drop, uint16_t* dX, float* dA,
+                                   float* dB, void* ws, size_t ws_bytes, void* stream) {
+  qlora_status st = check_gemm_weight(W);
+  if (st != QLORA_OK) return st;
+  if ((st = check_tokens(M, W)) != QLORA_OK) return st;
+  const int64_t N = W->rows, K = W->cols;
+  if ((st = check_bwd(M, N, K, X, dY, A, B, r, U_saved, dX, dA, dB)) != QLORA_OK) return st;
+  if (r == 0) return QLORA_E_UNSUPPORTED;   // no adapter, nothing to drop
+  if (!drop) return QLORA_E_NULL;
+  DropArgs d{};
+  bool active;
+  if ((st = check_drop(drop, &d, &active)) != QLORA_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, drop_bwd_layout(M, N, K, r, dX != nullptr).total)) != QLORA_OK) return st;
+  return run_bwd(W, nullptr, M, N, K, X, dY, A, B, r, alpha, U_saved, active ? &d : nullptr, dX, dA, dB, ws,
+                 (hipStream_t)stream);
+}
+
+size_t qlora_i8_row_bytes(int64_t cols) { return cols > 0 && cols <= kI8MaxCols ? (size_t)i8_row_bytes(cols) : 0; }
+
+qlora_status qlora_i8_quantize(const uint16_t* X, const qlora_i8_rows* q, void* stream) {
+  const qlora_status st = check_i8(q);
+  if (st != QLORA_OK) return st;
+  if (!X) return QLORA_E_NULL;
+  if (!aligned16(X)) return QLORA_E_ALIGN;
+  return hip_status(launch_quant_rows(X, q->rows, q->cols, q->codes, q->scale, (hipStream_t)stream));
+}
+
+qlora_status qlora_i8_dequant(const qlora_i8_rows* q, uint16_t* out, void* stream) {
+  const qlora_status st = check_i8(q);
+  if (st != QLORA_OK) return st;
+  if (!out) return QLORA_E_NULL;
+  if (!aligned16(out)) return QLORA_E_ALIGN;
+  return hip_status(launch_i8_dequant(q->codes, q->scale, q->rows, q->cols, out, (hipStream_t)stream));
+}
+
+qlora_status qlora_i8_matmul(const qlora_i8_rows* X, const qlora_i8_rows* W, uint16_t* Y, void* stream) {
+  qlora_status st = check_i8(X);
+  if (st != QLORA_OK) return st;
+  if ((st = check_i8_product(W, X->rows)) != QLORA_OK) return st;
+  if (X->cols != W->cols) return QLORA_E_SHAPE;
+  if (!Y) return QLORA_E_NULL;
+  if (!aligned16(Y)) return QLORA_E_ALIGN;
+  const I8Gemm g{W->codes, W->scale, W->rows, W->cols, X->codes, X->scale, X->rows, nullptr, nullptr, 0, 0.0f, Y};
+  return hip_status(launch_i8_gemm(g, (hipStream_t)stream));
+}
+
+qlora_status qlora_i8_linear_fwd(const qlora_i8_rows* W, const uint16_t* X, int64_t M, const uint16_t* A,
+                                 const uint16_t* B, int32_t r, float alpha, const qlora_drop* drop, uint16_t* Y,
+                                 uint16_t* U_save, void* ws, size_t ws_bytes, void* stream) {
+  qlora_status st = check_i8_product(W, M);
+  if (st != QLORA_OK) return st;
+  if (!X || !Y) return QLORA_E_NULL;
+  if (!aligned16(X) || !aligned16(Y) || (U_save && !aligned16(U_save))) return QLORA_E_ALIGN;
+  if ((st = check_rank(r, A, B)) != QLORA_OK) return st;
+  DropArgs d{};
+  bool active;
+  if ((st = check_drop(drop, &d, &active)) != QLORA_OK) return st;
+  if (r == 0 && drop) return QLORA_E_UNSUPPORTED;   // no adapter, nothing to drop
+  const int64_t N = W->rows, K = W->cols;
+  const I8FwdLayout L = i8_fwd_layout(M, K, r);
+  if ((st = check_ws(ws, ws_bytes, L.total)) != QLORA_OK) return st;
+  hipStream_t s = (hipStream_t)stream;
+  int8_t* xq = reinterpret_cast<int8_t*>(ws_at(ws, L.xq));
+  float* sx = reinterpret_cast<float*>(ws_at(ws, L.sx));
+  bf16_t* U = r > 0 ? (U_save ? U_save : reinterpret_cast<bf16_t*>(ws_at(ws, L.u))) : nullptr;
+  if (r > 0) {
+    float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
+    if ((st = hip_status(launch_xat_drop(X, A, M, K, r, active ? &d : nullptr, part, U, s))) != QLORA_OK) return st;
+  }
+  if ((st = hip_status(launch_quant_rows(X, M, K, xq, sx, s))) != QLORA_OK) return st;
+  const float sc = r > 0 ? (float)((double)alpha / (double)r) : 0.0f;
+  const I8Gemm g{W->codes, W->scale, N, K, xq, sx, M, U, B, r, sc, Y};
+  return hip_status(launch_i8_gemm(g, s));
+}
+
+qlora_status qlora_i8_linear_bwd(const qlora_i8_rows* W, const uint16_t* X, const uint16_t* dY, int64_t M,
+                                 const uint16_t* A, const uint16_t* B, int32_t r, float alpha,
+                                 const uint16_t* U_saved, const qlora_drop* drop, uint16_t* dX, float* dA, float* dB,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  qlora_status st = check_i8_product(W, M);
+  if (st != QLORA_OK) return st;
+  const int64_t N = W->rows, K = W->cols;
+  if ((st = check_bwd(M, N, K, X, dY, A, B, r, U_saved, dX, dA, dB)) != QLORA_OK) return st;
+  DropArgs d{};
+  bool active;
+  if ((st = check_drop(drop, &d, &active)) != QLORA_OK) return st;
+  if (r == 0 && drop) return QLORA_E_UNSUPPORTED;
+  if ((st = check_ws(ws, ws_bytes, drop_bwd_layout(M, N, K, r, dX != nullptr).total)) != QLORA_OK) return st;
+  return run_bwd(nullptr, W, M, N, K, X, dY, A, B, r, alpha, U_saved, active ? &d : nullptr, dX, dA, dB, ws,
+                 (hipStream_t)stream);
 }
 
 namespace {

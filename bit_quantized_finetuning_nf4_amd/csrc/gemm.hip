@@ -22,6 +22,7 @@
 #include "device.h"
 #include "kernels.h"
 #include "lds.h"
+#include "rng.h"
 
 namespace qlora {
 
@@ -50,6 +51,9 @@ __device__ __forceinline__ void tr_dma_coords(int q, int lane, int& row, int& co
 // (16-byte chunk c of row m at c ^ ((m >> 2) & 3)).  Q is A [r x C] (QT =
 // false: rows j, read like P) or B [C x r] (QT = true: rows c, read
 // transposed).  Output D[j][m]: a lane holds four consecutive j of one m.
+// DROP: P is drop(P), masked as its fragments are read: a fragment's 16 bytes
+// are eight consecutive columns of one row, one Philox block (rng.h), and no
+// two lanes read the same ones.
 // ---------------------------------------------------------------------------
 template <int RP, bool QT>
 struct RowShape {
@@ -60,12 +64,12 @@ struct RowShape {
   static constexpr int kLoads = 2 + kQDma;                 // all DMA instructions per wave per stage
 };
 
-template <int RP, bool QT>
+template <int RP, bool QT, bool DROP>
 __global__ __launch_bounds__(kThreads, 1) void rskinny_kernel(const bf16_t* __restrict__ P, int64_t M, int64_t C,
                                                               int64_t ldp, int64_t p_gs,
                                                               const bf16_t* __restrict__ Q, int r, int64_t q_gs,
                                                               int stages_per_split, int tiles_m, int ldo,
-                                                              float* __restrict__ part) {
+                                                              float* __restrict__ part, DropArgs drop) {
   using S = RowShape<RP, QT>;
   extern __shared__ __align__(16) char smem[];
   const int tm = blockIdx.x % tiles_m, sp = blockIdx.x / tiles_m, g = blockIdx.y;
@@ -117,6 +121,13 @@ __global__ __launch_bounds__(kThreads, 1) void rskinny_kernel(const bf16_t* __re
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[f][e] = 0.0f;
 
+  [[maybe_unused]] DropKey key;
+  [[maybe_unused]] uint32_t row_block = 0;
+  if constexpr (DROP) {
+    key = drop_key(drop);
+    row_block = (uint32_t)(m0 + 32 * w + lr) * (uint32_t)(C >> 3);
+  }
+
   if (s0 < s1) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) dma(s0 + a, a);
@@ -136,6 +147,8 @@ __global__ __launch_bounds__(kThreads, 1) void rskinny_kernel(const bf16_t* __re
         const int ch = QT ? 2 * kk + h : 2 * h + kk;
         bf16x8_t b = rd16(base + spos(32 * w + lr, ch));
         if (32 * st + 8 * ch >= C) b = bf16x8_t{};   // columns past C (C % 8 == 0)
+        if constexpr (DROP)   // M C < 2^31: block numbers in 32 bits (rows past M: masks of zeros)
+          b = __builtin_bit_cast(bf16x8_t, drop8(__builtin_bit_cast(u32x4_t, b), row_block + (uint32_t)(4 * st + ch), key));
         bf16x8_t a[FJ];
         if constexpr (!QT) {
 #pragma unroll
@@ -177,23 +190,33 @@ __global__ __launch_bounds__(kThreads, 1) void rskinny_kernel(const bf16_t* __re
 // tokens.  Both tiles are rows m, read transposed.  DB = false stores dA
 // [r x C] (A operand = Big, D[c][j]: four consecutive c per lane); DB = true
 // stores dB [C x r] (A operand = Sm, D[j][c]: four consecutive j per lane).
+// HL: the rank side is Sm + Sm2, an fp32 matrix in two bf16 parts, both
+// multiplied into the same sums (dA is fp32: one bf16 G would leave it 2^-9
+// of G's rounding).
+// DROP: Big is drop(Big).  A transposed fragment holds eight tokens of one
+// column, eight different Philox blocks, so the mask is applied in LDS
+// instead: each lane zeroes the dropped elements of the 16-byte pieces that
+// its own wave's DMA brought (one block each), one stage ahead of the one
+// being multiplied; the stage's barrier publishes them.
 // ---------------------------------------------------------------------------
-template <int RP>
+template <int RP, bool HL>
 struct ColShape {
   static constexpr int kBig = 32 * 256;                    // 8 KiB: 32 rows x 128 columns
   static constexpr int kSm = 32 * 2 * RP;                  // 32 rows x RP ranks
-  static constexpr int kStage = kBig + kSm;
+  static constexpr int kStage = kBig + (HL ? 2 : 1) * kSm;
   static constexpr int kSmDma = kSm / 1024 / 4;
-  static constexpr int kLoads = 2 + kSmDma;
+  static constexpr int kLoads = 2 + (HL ? 2 : 1) * kSmDma;
 };
 
-template <int RP, bool DB>
+template <int RP, bool DB, bool HL, bool DROP>
 __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __restrict__ Big, int64_t M, int64_t C,
                                                               int64_t ldb, int64_t big_gs,
                                                               const bf16_t* __restrict__ Sm, int r, int lds,
                                                               int64_t sm_gs, int stages_per_split, int tiles_c,
-                                                              float* __restrict__ part) {
-  using S = ColShape<RP>;
+                                                              float* __restrict__ part,
+                                                              const bf16_t* __restrict__ Sm2, DropArgs drop) {
+  static_assert(!HL || (!DB && RP <= 128), "two-part rank side: dA of one adapter");
+  using S = ColShape<RP, HL>;
   extern __shared__ __align__(16) char smem[];
   const int tc = blockIdx.x % tiles_c, sp = blockIdx.x / tiles_c, g = blockIdx.y;
   const int t = threadIdx.x, w = t >> 6, lane = t & 63, lr = lane & 31, h = lane >> 5;
@@ -205,14 +228,20 @@ __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __re
   // rows past M read as zero
   const rsrc_t br = make_rsrc(Big, (uint32_t)(((M - 1) * ldb + C) * 2));
   const rsrc_t sr = make_rsrc(Sm, (uint32_t)(((M - 1) * lds + r) * 2));
+  [[maybe_unused]] rsrc_t sr2;
+  if constexpr (HL) sr2 = make_rsrc(Sm2, (uint32_t)(((M - 1) * lds + r) * 2));
   uint32_t bo[2], so[S::kSmDma];
   int bl[2], sl[S::kSmDma];
+  [[maybe_unused]] DropKey key;
+  [[maybe_unused]] uint32_t blk[2];   // Philox block of the lane's pieces in stage 0 (M C < 2^31)
+  if constexpr (DROP) key = drop_key(drop);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     int row, col;
     tr_dma_coords<256>(2 * w + q, lane, row, col);
     bo[q] = (uint32_t)(row * ldb * 2 + (c0 + col) * 2);   // columns past C: never stored
     bl[q] = (2 * w + q) * 1024;
+    if constexpr (DROP) blk[q] = (uint32_t)((row * C + c0 + col) >> 3);
   }
 #pragma unroll
   for (int q = 0; q < S::kSmDma; ++q) {
@@ -228,6 +257,22 @@ __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __re
     for (int q = 0; q < 2; ++q) dma16(br, base + bl[q], bo[q], ss * 32u * (uint32_t)ldb * 2u);
 #pragma unroll
     for (int q = 0; q < S::kSmDma; ++q) dma16(sr, base + sl[q], so[q], ss * 32u * (uint32_t)lds * 2u);
+    if constexpr (HL) {
+#pragma unroll
+      for (int q = 0; q < S::kSmDma; ++q)
+        dma16(sr2, base + S::kSm + sl[q], so[q], ss * 32u * (uint32_t)lds * 2u);
+    }
+  };
+  // zero the dropped elements of this lane's pieces of stage st, in slot
+  // `slot` (columns past C: masks of values that are never stored)
+  [[maybe_unused]] auto mask = [&](int st, int slot) __attribute__((always_inline)) {
+    char* base = smem + slot * S::kStage;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      char* p = base + bl[q] + 16 * lane;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(p);
+      *reinterpret_cast<u32x4_t*>(p) = drop8(v, blk[q] + (uint32_t)st * 4u * (uint32_t)C, key);
+    }
   };
 
   constexpr int FJ = RP / 32;
@@ -243,11 +288,19 @@ __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __re
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) dma(s0 + a, a);
     int slot = 0;
-    for (int st = s0; st < s1; ++st) {
+    if constexpr (DROP) {
       QLORA_WAIT((kAhead - 1) * S::kLoads, 0);
+      mask(s0, 0);
+    }
+    for (int st = s0; st < s1; ++st) {
+      // (DROP: stage st + 1 as well, for the mask; it is the wave's own DMA)
+      QLORA_WAIT((kAhead - (DROP ? 2 : 1)) * S::kLoads, 0);
       __builtin_amdgcn_s_barrier();
       dma(st + kAhead, slot == 0 ? kRing - 1 : slot - 1);
       const char* base = smem + slot * S::kStage;
+      if constexpr (DROP) {
+        if (st + 1 < s1) mask(st + 1, slot == kRing - 1 ? 0 : slot + 1);
+      }
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         // transposed reads in asm blocks (see tr_read3): the big tile's
@@ -267,6 +320,14 @@ __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __re
 #pragma unroll
         for (int f = 0; f < FJ; ++f)
           acc[f] = DB ? mfma32x32x16(sm[f], bg, acc[f]) : mfma32x32x16(bg, sm[f], acc[f]);
+        if constexpr (HL) {
+          const char* sb2 = sb + S::kSm;
+#pragma unroll
+          for (int f = 0; f < FJ; f += 2)
+            tr_read2<O, O>(sb2 + tr_off<2 * RP>(f), sb2 + tr_off<2 * RP>(f + 1), sm[f], sm[f + 1]);
+#pragma unroll
+          for (int f = 0; f < FJ; ++f) acc[f] = mfma32x32x16(bg, sm[f], acc[f]);
+        }
       }
       slot = slot == kRing - 1 ? 0 : slot + 1;
     }
@@ -320,13 +381,39 @@ __global__ __launch_bounds__(kThreads) void reduce_kernel(const float* __restric
   }
 }
 
+// hi + lo = scale * the sum of the splits: hi its bf16 rounding, lo the
+// bf16 rounding of what that left, together within 2^-18 of the sum.
+__global__ __launch_bounds__(kThreads) void reduce_hl_kernel(const float* __restrict__ part, int splits, int64_t n,
+                                                             float scale, bf16_t* __restrict__ hi,
+                                                             bf16_t* __restrict__ lo) {
+  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+  if (i >= n) return;
+  float4 acc = *reinterpret_cast<const float4*>(part + i);
+  for (int sp = 1; sp < splits; ++sp) {
+    const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)sp * n + i);
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+  }
+  acc.x *= scale;
+  acc.y *= scale;
+  acc.z *= scale;
+  acc.w *= scale;
+  const uint2 p = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+  *reinterpret_cast<uint2*>(hi + i) = p;
+  *reinterpret_cast<uint2*>(lo + i) =
+      make_uint2(pack_bf16x2(acc.x - bf2f(p.x & 0xFFFFu), acc.y - bf2f(p.x >> 16)),
+                 pack_bf16x2(acc.z - bf2f(p.y & 0xFFFFu), acc.w - bf2f(p.y >> 16)));
+}
+
 // The reductions of dA and dB in one launch: elements [0, n0) of the
 // output are out0 (partials at part0, splits0 of them), the next n1 are out1
 // (part1, splits1); each sums its splits in order, as reduce_kernel does.
 __global__ __launch_bounds__(kThreads) void reduce2_kernel(const float* __restrict__ part0, int splits0, int64_t n0,
                                                            float* __restrict__ out0,
                                                            const float* __restrict__ part1, int splits1, int64_t n1,
-                                                           float* __restrict__ out1, float scale) {
+                                                           float* __restrict__ out1, float scale, float scale1) {
   int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
   const float* part = part0;
   float* out = out0;
@@ -334,7 +421,7 @@ __global__ __launch_bounds__(kThreads) void reduce2_kernel(const float* __restri
   int64_t n = n0;
   if (i >= n0) {
     i -= n0;
-    part = part1, out = out1, splits = splits1, n = n1;
+    part = part1, out = out1, splits = splits1, n = n1, scale = scale1;
   }
   if (i >= n) return;
   float4 acc = *reinterpret_cast<const float4*>(part + i);
@@ -399,17 +486,25 @@ struct RowArgs {
   int G, ldo;
 };
 
-template <int RP, bool QT>
-hipError_t run_rows(const RowArgs& a, float* part, float scale, bf16_t* out, bf16_t* out2, hipStream_t st) {
+template <int RP, bool QT, bool DROP>
+hipError_t row_partials(const RowArgs& a, const DropArgs& drop, float* part, int* splits, hipStream_t st) {
   const Split sp = split_for((a.M + 127) / 128, a.C, 256);
-  auto* fn = &rskinny_kernel<RP, QT>;
+  auto* fn = &rskinny_kernel<RP, QT, DROP>;
   const size_t lds = (size_t)kRing * RowShape<RP, QT>::kStage;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits, a.G), dim3(kThreads), lds, st, a.P, a.M, a.C, a.ldp, a.p_gs, a.Q,
-                     a.r, a.q_gs, sp.sps, sp.tiles, a.ldo, part);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  return reduce(part, sp.splits, a.M * a.ldo, scale, nullptr, out, out2, st);
+                     a.r, a.q_gs, sp.sps, sp.tiles, a.ldo, part, drop);
+  *splits = sp.splits;
+  return hipGetLastError();
+}
+
+template <int RP, bool QT>
+hipError_t run_rows(const RowArgs& a, float* part, float scale, bf16_t* out, bf16_t* out2, hipStream_t st) {
+  int splits = 0;
+  const hipError_t e = row_partials<RP, QT, false>(a, DropArgs{}, part, &splits, st);
+  if (e != hipSuccess) return e;
+  return reduce(part, splits, a.M * a.ldo, scale, nullptr, out, out2, st);
 }
 
 // Token contraction over G groups (grid y): group g reads Big + g big_gs
@@ -426,15 +521,16 @@ struct ColArgs {
 
 // The token-contraction product's partials (no reduction); *splits gets
 // their count.
-template <int RP, bool DB>
-hipError_t run_cols(const ColArgs& a, float* part, int* splits, hipStream_t st) {
+template <int RP, bool DB, bool HL = false, bool DROP = false>
+hipError_t run_cols(const ColArgs& a, float* part, int* splits, hipStream_t st, const bf16_t* Sm2 = nullptr,
+                    const DropArgs& drop = DropArgs{}) {
   const Split sp = split_for((a.C + 127) / 128, a.M, 256);
-  auto* fn = &cskinny_kernel<RP, DB>;
-  const size_t lds = (size_t)kRing * ColShape<RP>::kStage;
+  auto* fn = &cskinny_kernel<RP, DB, HL, DROP>;
+  const size_t lds = (size_t)kRing * ColShape<RP, HL>::kStage;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits, a.G), dim3(kThreads), lds, st, a.Big, a.M, a.C, a.ldb,
-                     a.big_gs, a.Sm, a.r, a.lds, a.sm_gs, sp.sps, sp.tiles, part);
+                     a.big_gs, a.Sm, a.r, a.lds, a.sm_gs, sp.sps, sp.tiles, part, Sm2, drop);
   *splits = sp.splits;
   return hipGetLastError();
 }
@@ -490,7 +586,51 @@ hipError_t launch_grads(const bf16_t* Gm, const bf16_t* X, const bf16_t* dY, int
   if (e != hipSuccess) return e;
   const int64_t na = (int64_t)ra * K, nb = (int64_t)G * N * r;
   hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(((na + nb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
-                     part, sa, na, dA, part_b, sb, nb, dB, scale);
+                     part, sa, na, dA, part_b, sb, nb, dB, scale, scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
+                           float* part, bf16_t* out, hipStream_t st) {
+  if (!drop) return launch_xat(X, A, M, K, r, part, out, nullptr, 1.0f, st);
+  const RowArgs a{X, M, K, K, 0, A, r, 0, 1, r};
+  int splits = 0;
+  const hipError_t e = r <= 64 ? row_partials<64, false, true>(a, *drop, part, &splits, st)
+                               : row_partials<128, false, true>(a, *drop, part, &splits, st);
+  if (e != hipSuccess) return e;
+  return reduce(part, splits, M * r, drop->scale, nullptr, out, nullptr, st);
+}
+
+hipError_t launch_dyb_hl(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* hi,
+                         bf16_t* lo, hipStream_t st) {
+  const RowArgs a{dY, M, N, N, 0, B, r, 0, 1, r};
+  int splits = 0;
+  const hipError_t e = r <= 64 ? row_partials<64, true, false>(a, DropArgs{}, part, &splits, st)
+                               : row_partials<128, true, false>(a, DropArgs{}, part, &splits, st);
+  if (e != hipSuccess) return e;
+  const int64_t n = M * r;
+  hipLaunchKernelGGL(reduce_hl_kernel, dim3((unsigned)((n / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, part,
+                     splits, n, 1.0f, hi, lo);
+  return hipGetLastError();
+}
+
+hipError_t launch_grads_hl(const bf16_t* hi, const bf16_t* lo, const bf16_t* X, const bf16_t* dY, const bf16_t* U,
+                           int64_t M, int64_t N, int64_t K, int r, const DropArgs* drop, float* part, float* dA,
+                           float* dB, float scale, hipStream_t st) {
+  const ColArgs a{X, M, K, K, 0, hi, r, r, 0, 1};
+  int sa = 0, sb = 0;
+  hipError_t e = drop ? (r <= 64 ? run_cols<64, false, true, true>(a, part, &sa, st, lo, *drop)
+                                 : run_cols<128, false, true, true>(a, part, &sa, st, lo, *drop))
+                      : (r <= 64 ? run_cols<64, false, true>(a, part, &sa, st, lo)
+                                 : run_cols<128, false, true>(a, part, &sa, st, lo));
+  if (e != hipSuccess) return e;
+  float* part_b = part + (skinny_partial_bytes(r, K, M, kGtX) + 255) / 256 * 256 / sizeof(float);
+  const ColArgs b{dY, M, N, N, 0, U, r, r, 0, 1};
+  e = r <= 64 ? run_cols<64, true>(b, part_b, &sb, st) : run_cols<128, true>(b, part_b, &sb, st);
+  if (e != hipSuccess) return e;
+  const int64_t na = (int64_t)r * K, nb = N * r;
+  hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(((na + nb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
+                     part, sa, na, dA, part_b, sb, nb, dB, drop ? scale * drop->scale : scale, scale);
   return hipGetLastError();
 }
 

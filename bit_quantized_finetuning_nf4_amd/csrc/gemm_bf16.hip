@@ -16,281 +16,79 @@
 //
 //   dX        the same kernel on deq(W)^T: dX = dY (W^T)^T + s G (A^T)^T,
 //             with A read column-wise in the LoRA tail;
+//   dX under dropout   the adapter branch saw drop(X), so its product is
+//             masked like X before it joins: dX = dY (W^T)^T + s drop'(G A);
 //   groups    weight rows in groups of gn, each with its own adapter (the
 //             stacked q/k/v or gate/up weights of one layer).
 #include <algorithm>
 
-#include "gemm_common.h"
+#include "dense_tile.h"
+#include "rng.h"
 
 namespace qlora {
 namespace {
 
-constexpr int kPairOp = kTile * 128;                    // 32 KiB: 256 rows x 64 bf16 (two stages)
-constexpr int kPairSlot = 2 * kPairOp;                  // weight rows at 0, token rows at kPairOp
-constexpr size_t kLdsPairs = 2 * (size_t)kPairSlot;     // 128 KiB: two pair slots
-constexpr size_t kLdsDense = kLdsPairs + 2 * kOp;       // + 32 KiB: the first LoRA tail chunk
-constexpr int kDGroup = 4;                              // token tiles per tile group (tile order)
-
-// Pair slots hold two consecutive 32-wide stages (one 64-wide stage): rows of
-// 128 bytes, 16-byte chunk c of row r at position c ^ ((r >> 1) & 7), so the
-// 16 lanes of one read quarter (16 consecutive rows, one chunk) and a DMA
-// instruction's 64 lanes (8 whole rows) cover all 64 LDS banks.  Chunks
-// 0..3 are the even stage, 4..7 the odd one.
-__device__ __forceinline__ int pos128(int r, int c) { return r * 128 + 16 * (c ^ ((r >> 1) & 7)); }
-
-// Tile order of the dense GEMMs.  The eight XCDs receive contiguous ranges of
-// tile ids (the hardware hands workgroups to XCDs round robin); ids run over
-// groups of kDGroup token tiles, each group column-tile-major, so that the
-// tiles one XCD holds at a time share a few token tiles and a few weight
-// tiles and both stream through its L2.
-// With the contraction split, ids run split-major: the tiles of one split
-// (which share its column range of both operands) sit on the same XCDs.
-__device__ __forceinline__ int xcd_tile_id() {
-  const int nwg = (int)gridDim.x;
-  int id = blockIdx.x;
-  if ((nwg & 7) == 0) id = (id & 7) * (nwg >> 3) + (id >> 3);
-  return id;
-}
-// With 16 token tiles or more a group holds 8 of them, so each weight tile
-// streams through an XCD's L2 half as often (the weight is the larger
-// operand of these products): at 4096 tokens the 65B products ran 1.4 %
-// faster than with 4; at 2048 tokens (8 token tiles) 4 stays slightly ahead.
-__device__ __forceinline__ void map_tile_grouped(int id, int tiles_c, int tiles_r, int& tc, int& tr) {
-  const int grp = tiles_r >= 16 ? 2 * kDGroup : kDGroup;
-  const int per_group = grp * tiles_c;
-  const int g = id / per_group, first = g * grp;
-  const int size = min(grp, tiles_r - first);
-  const int local = id - g * per_group;
-  tr = first + local % size;
-  tc = local / size;
-}
-
-struct DenseOps {
-  rsrc_t wr_, xr;           // weight rows, token rows
-  uint32_t wo[8], xo[8];    // lane offsets of the eight DMA instructions per operand (pair 0)
-  int npair, w;
-};
-
-// DMA of pair `pair` (64 columns of every row) of both operands into pair
-// slot `dst`: weight instruction q < 2 FI and token instruction q < 8 of
-// wave w fill rows 8 (4 q + w) .. +7 of their tile, 128 bytes each (lane j:
-// row + (j >> 3), position j & 7).  DMA d of a pair is weight instruction d
-// for d < 2 FI, token instruction d - 2 FI after.  Past the last pair the last
-// one is re-loaded (never read).
-template <int FI>
-__device__ __forceinline__ void pair_dma(char* dst, const DenseOps& f, int pair, int d) {
-  const uint32_t soff = (uint32_t)min(pair, f.npair - 1) * 128u;
-  const bool wrow = d < 2 * FI;
-  const int q = wrow ? d : d - 2 * FI;
-  char* dd = dst + (wrow ? 0 : kPairOp) + 8 * (4 * q + f.w) * 128;
-  if (wrow)
-    dma16(f.wr_, dd, f.wo[q], soff);
-  else
-    dma16(f.xr, dd, f.xo[q], soff);
-}
-
-// Read offsets of the lane within a pair slot: stage half hf, k16 step kk ->
-// chunk 4 hf + 2 kk + h of row lr.
-struct PairOffs {
-  int o[2][2];
-};
-
-// MFMA slot X (0 .. 8 FI - 1) of substep s: X = 4 FI kk + 4 i + j is
-// fragment pair (i, j) of k16 step kk (FI weight fragments of 32 rows, four
-// token fragments).  Stage s is half HF of the pair slot at cur; stage s+1 is
-// the other half of cur (HF = 0) or half 0 of the next slot (HF = 1).
-//   LDS reads   read q (fragments A0, B0, B1, B2, B3, A1, .., A(FI-1) in
-//               that order) in slot rd_slot(q): step 1 of stage s; in slot
-//               4 FI + rd_slot(q): step 0 of stage s+1, into the registers
-//               step 0 of stage s has finished with.
-//   barrier     odd substeps, before slot 4 FI: this wave's DMAs of the next
-//               pair have landed and its reads of this pair have completed;
-//               after it the next pair is visible to every wave and no wave
-//               reads this pair's slot any more.
-//   DMA         the pair after next into this pair's slot (2 FI weight-row,
-//               then 8 token-row instructions of 8 whole 128-byte rows each):
-//               the first FI + 4 in the odd substep's slots 4 FI .., every
-//               other slot; the other FI + 4 in the next pair's even substep,
-//               one every fourth slot.  Issued all in the odd substep's
-//               second half, 16 instructions per wave in 16 MFMA slots
-//               overran the texture address queue (its FIFO full about 10 %
-//               of the cycles) and stalled issue; split, the product ran
-//               about 7 % faster.
-template <int FI>
-constexpr int rd_slot(int q) { return q * 4 * FI / (FI + 4); }
-template <int FI>
-constexpr int dma_half = FI + 4;   // DMAs of a pair issued in its odd substep
-template <int FI>
-constexpr int dma_slot_a(int d) { return 4 * FI + d * 4 * FI / dma_half<FI>; }
-template <int FI>
-constexpr int dma_slot_b(int d) { return (d - dma_half<FI>) * 8 * FI / dma_half<FI>; }
-
-template <int FI, int X, int HF>
-__device__ __forceinline__ void dense_slot(const char* cur, const char* nxt, char* fill, const DenseOps& f,
-                                           int pair, f32x16_t (&acc)[FI][4], Frags& F, int am, int bm,
-                                           const PairOffs& po) {
-  constexpr int H = 4 * FI;   // slots per k16 step
-  constexpr int kk = X / H, y = X % H, i = y >> 2, j = y & 3;
-  if constexpr (HF == 1 && X == H) {
-    QLORA_WAIT(0, 0);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  if constexpr (kk == 0)
-    acc[i][j] = mfma32x32x16(F.a0[i], F.b0[j], acc[i][j]);
-  else
-    acc[i][j] = mfma32x32x16(F.a1[i], F.b1[j], acc[i][j]);
-#pragma unroll
-  for (int q = 0; q < FI + 4; ++q) {
-    if (rd_slot<FI>(q) != y) continue;
-    const bool isA = q == 0 || q >= 5;
-    const int fr = q == 0 ? 0 : q >= 5 ? q - 4 : q - 1;   // fragment index
-    // step 1 of stage s (half HF of cur), or step 0 of stage s+1
-    const char* slot = kk == 0 ? cur : (HF == 0 ? cur : nxt);
-    const int o = kk == 0 ? po.o[HF][1] : po.o[HF ^ 1][0];
-    const char* base = slot + (isA ? am : kPairOp + bm) + fr * 32 * 128 + o;
-    if (isA) {
-      if (kk == 0) F.a1[fr] = rd16(base); else F.a0[fr] = rd16(base);
-    } else {
-      if (kk == 0) F.b1[fr] = rd16(base); else F.b0[fr] = rd16(base);
-    }
-  }
-  if constexpr (HF == 1 && kk == 1) {
-#pragma unroll
-    for (int d = 0; d < dma_half<FI>; ++d)
-      if (dma_slot_a<FI>(d) == X) pair_dma<FI>(fill, f, pair + 2, d);
-  }
-  if constexpr (HF == 0) {
-    // the rest of pair + 1's DMAs into nxt, which no wave reads before the
-    // barrier of this pair (in the first pair they re-load what the
-    // prologue loaded: the same bytes to the same place)
-#pragma unroll
-    for (int d = dma_half<FI>; d < 2 * FI + 8; ++d)
-      if (dma_slot_b<FI>(d) == X) pair_dma<FI>(const_cast<char*>(nxt), f, pair + 1, d);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-}
-
-template <int FI, int HF, int X>
-__device__ __forceinline__ void dense_slots(const char* cur, const char* nxt, char* fill, const DenseOps& f,
-                                            int pair, f32x16_t (&acc)[FI][4], Frags& F, int am, int bm,
-                                            const PairOffs& po) {
-  if constexpr (X < 8 * FI) {
-    dense_slot<FI, X, HF>(cur, nxt, fill, f, pair, acc, F, am, bm, po);
-    dense_slots<FI, HF, X + 1>(cur, nxt, fill, f, pair, acc, F, am, bm, po);
-  }
-}
-
-// One 32-wide chunk of the LoRA tail, in registers: the weight half
-// B'[row0 + row, j0 ..] (zero past the rank, and for rows outside [lo, hi))
-// and the token half T[trow0 + row, j0 + 8 c ..] (T is trows x rank with
-// row stride ld; zero past the rank and the last row).  Token half: thread t
-// holds row (t + 256 e) >> 2, 16-byte chunk (t + 256 e) & 3.  Weight half:
-// B' is B [rows x r], held like the tokens; or, with b_trans, the transpose
-// of B [r x rows], read along its rows (coalesced): thread t holds B[j0 +
-// (i >> 5)][row0 + 8 (i & 31) ..] for i = t + 256 e.
-struct TailRegs {
-  uint4 w[4], t[4];
-};
-__device__ __forceinline__ void tail_load(TailRegs& R, const bf16_t* Bm, bool b_trans, int64_t rows, int r,
-                                          int64_t row0, int j0, int64_t lo, int64_t hi, const bf16_t* T,
-                                          int64_t ld, int64_t trows, int64_t trow0) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int idx = threadIdx.x + kThreads * e;
-    const int row = idx >> 2, c = idx & 3, col = j0 + 8 * c;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (!b_trans) {
-      if (col < r && row0 + row >= lo && row0 + row < hi)
-        v = *reinterpret_cast<const uint4*>(Bm + (row0 + row) * r + col);
-    } else {
-      // rows % 8 == 0 and lo, hi multiples of 8: the 8 rows are all in or all out
-      const int j = j0 + (idx >> 5);
-      const int64_t rr = row0 + 8 * (idx & 31);
-      if (j < r && rr >= lo && rr < hi) v = *reinterpret_cast<const uint4*>(Bm + (int64_t)j * rows + rr);
-    }
-    R.w[e] = v;
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (col < r && trow0 + row < trows) u = *reinterpret_cast<const uint4*>(T + (trow0 + row) * ld + col);
-    R.t[e] = u;
-  }
-}
-// The chunk into LDS: s T as a 64-byte-row tile at dst + kOp; the weights
-// at dst, as a 64-byte-row tile or, with b_trans, as a tile of 32 rank rows
-// x 256 weight rows (512-byte rows, 32-byte block b of rank row n at
-// b ^ (n & 3)) for transposed fragment reads.
-__device__ __forceinline__ void tail_store(char* dst, const TailRegs& R, bool b_trans, float s) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int idx = threadIdx.x + kThreads * e;
-    const int row = idx >> 2, c = idx & 3;
-    if (!b_trans) {
-      wr16(dst + spos(row, c), R.w[e]);
-    } else {
-      const int n = idx >> 5, sg = idx & 31;
-      wr16(dst + n * 512 + 32 * ((sg >> 1) ^ (n & 3)) + 16 * (sg & 1), R.w[e]);
-    }
-    wr16(dst + kOp + spos(row, c), scale16(R.t[e], s));
-  }
-}
-
-// The LoRA tail by DMA, for tiles inside one adapter group with the rank in
-// whole 32-wide chunks.  A chunk takes 32 KiB of LDS in the layouts of
-// tail_store, but the token half holds T itself (unscaled): s is applied to
-// each fragment as it is read, which rounds exactly as tail_store does.
-struct TailSrc {
-  rsrc_t wr, tr;         // weight half (B, or A with b_trans), token half (T)
-  int64_t n0, m0, rows;  // first weight row, first token row, weight rows (N)
-  int r, ld, col0;       // rank, T's row stride, T's first column (the group's)
-  bool bt;
-};
-// DMA of chunk c (ranks 32 c ..) into dst: per wave 4 token and 4 weight
-// instructions of 1 KiB.  Token rows / weight rows (no b_trans): the
-// 256-row x 64-byte pattern of dma_row / dma_chunk.  With b_trans: rank rows
-// n = 2 (4 w + q) + (lane >> 5) of 512 bytes, lane position pc = lane & 31
-// holding 32-byte block (pc >> 1) ^ (n & 3), half pc & 1.  Rows past the
-// arrays read zero (buffer range) or another row's finite values, which only
-// reach outputs past M or N.
-__device__ __forceinline__ void tail_dma(char* dst, const TailSrc& S, int c, int w, int lane) {
-  const int j0 = 32 * c;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int row = dma_row(q, w, lane), ch = dma_chunk(lane);
-    dma16(S.tr, dst + kOp + (64 * q + 16 * w) * 64,
-          (uint32_t)(((S.m0 + row) * S.ld + S.col0 + j0 + 8 * ch) * 2), 0u);
-    if (!S.bt) {
-      dma16(S.wr, dst + (64 * q + 16 * w) * 64, (uint32_t)(((S.n0 + row) * S.r + j0 + 8 * ch) * 2), 0u);
-    } else {
-      const int n = 2 * (4 * w + q) + (lane >> 5), pc = lane & 31;
-      const int e = 8 * (2 * ((pc >> 1) ^ (n & 3)) + (pc & 1));
-      dma16(S.wr, dst + 1024 * (4 * w + q), (uint32_t)(((int64_t)(j0 + n) * S.rows + S.n0 + e) * 2), 0u);
-    }
-  }
-}
-__device__ __forceinline__ bf16x8_t scale_frag(bf16x8_t v, float s) {
-  return __builtin_bit_cast(bf16x8_t, scale16(__builtin_bit_cast(uint4, v), s));
-}
-
-// fp32 sums of the tile (the lane layout of store_tile_lds): lane (lr, h) of
-// wave (wr, wc) holds token row0 + 128 wr + 32 j + lr, columns col0 + 32 FI
-// wc + 32 i + 8 q + 4 h + 0..3, stored as one 16-byte piece (cols % 4 == 0).
-template <int FI>
-__device__ __forceinline__ void store_tile_f32(const f32x16_t (&acc)[FI][4], float* out, int64_t ld, int64_t rows,
-                                               int64_t cols, int64_t row0, int64_t col0) {
+// The masked LoRA tail of a tile: acc += s drop'(T A) over tokens row0 .. and
+// columns col0 .., A [r x cols] read transposed, T [M x r], r <= 128.  All
+// chunks of the rank are in LDS (chunk c at 2 kOp c), so a 32 x 32 block's
+// product is summed in 16 registers of its own, masked, and added: the tile
+// keeps one set of accumulators.
+//
+// A lane holds four consecutive columns of a token, half of a Philox block's
+// eight; its two lane halves hold the block's two halves.  So the lower half
+// computes the block of column group 2 p, the upper half that of 2 p + 1, and
+// v_permlane32_swap hands each half its four columns of both.
+template <int FI, int NT>
+__device__ __forceinline__ void masked_tail(f32x16_t (&acc)[FI][4], const char* smem, float s,
+                                            const DropKey& key, int64_t cols, int64_t row0, int64_t col0) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1, lr = lane & 31, h = lane >> 5;
+  const FragOffs fo = frag_offs(lane);
+  const int bm64 = wr * 128 * 64;
 #pragma unroll
-  for (int i = 0; i < FI; ++i)
+  for (int j = 0; j < 4; ++j) {
+    bf16x8_t b[2 * NT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t row = row0 + 128 * wr + 32 * j + lr;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t col = col0 + 32 * FI * wc + 32 * i + 8 * q + 4 * h;
-        if (row < rows && col < cols)
-          *reinterpret_cast<float4*>(out + row * ld + col) =
-              make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-      }
+    for (int c = 0; c < NT; ++c) {
+      const char* tok = smem + c * 2 * kOp + kOp + bm64 + j * 2048;
+      b[2 * c] = rd16(tok + fo.o0);
+      b[2 * c + 1] = rd16(tok + fo.o1);
     }
+    // Philox block of column col0 + 32 FI wc of the lane's token, M cols < 2^31
+    const uint32_t row_block =
+        (uint32_t)(row0 + 128 * wr + 32 * j + lr) * (uint32_t)(cols >> 3) + (uint32_t)((col0 + 32 * FI * wc) >> 3);
+#pragma unroll
+    for (int i = 0; i < FI; ++i) {
+      f32x16_t t;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) t[e] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        const char* a0 = smem + c * 2 * kOp + tr_off<512>(wc * FI + i);
+        bf16x8_t f0, f1;
+        tr_read2<2048, 2048>(a0, a0 + 16 * 512, f0, f1);
+        t = mfma32x32x16(f0, b[2 * c], t);
+        t = mfma32x32x16(f1, b[2 * c + 1], t);
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const u32x4_t x = philox(row_block + (uint32_t)(4 * i + 2 * p + h), key);
+        const auto x0 = __builtin_amdgcn_permlane32_swap(x.x, x.z, false, false);
+        const auto x1 = __builtin_amdgcn_permlane32_swap(x.y, x.w, false, false);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {   // column group 2 p + g: elements 8 p + 4 g ..
+          const int wd[2] = {(int)x0[g], (int)x1[g]};
+          const int thr = key.thr << 16;   // a half, as a signed number in the high bits
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            const int e = 8 * p + 4 * g + 2 * d;
+            acc[i][j][e] += (wd[d] << 16) >= thr ? s * t[e] : 0.0f;
+            acc[i][j][e + 1] += wd[d] >= thr ? s * t[e + 1] : 0.0f;
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
+    }
+  }
 }
 
 // FI: weight fragments per wave, so the tile is 64 FI weight rows x 256
@@ -299,14 +97,15 @@ __device__ __forceinline__ void store_tile_f32(const f32x16_t (&acc)[FI][4], flo
 // split p takes contraction pairs p pps .. (64-column pairs), split 0 alone
 // adds the LoRA tail, and each split stores its fp32 sums at part + p M N
 // ([M x N], row stride N) instead of Y.
-template <int FI, bool TD>
+// DR: the LoRA tail masked by `drop` (dX: b_trans, one adapter, gn = N).
+template <int FI, bool TD, bool DR>
 __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __restrict__ Wd, int64_t N, int64_t K,
                                                                const bf16_t* __restrict__ X, int64_t M,
                                                                const bf16_t* __restrict__ U,
                                                                const bf16_t* __restrict__ Bl, int b_trans, int r,
                                                                int ldu, int64_t gn, float s, bf16_t* __restrict__ Y,
                                                                int64_t n_begin, int tiles_n, int tiles_m, int pps,
-                                                               float* __restrict__ part) {
+                                                               float* __restrict__ part, DropArgs drop) {
   extern __shared__ __align__(16) char smem[];
   int tn, tm;
   int id = xcd_tile_id();
@@ -357,7 +156,7 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
   // arrays fit 32-bit byte offsets); otherwise through registers
   const int64_t g0 = n0 / gn;
   const bool tail = r > 0 && split == 0;
-  const bool tdma = TD && tail;
+  const bool tdma = TD && !DR && tail;
   // (built where used, so nothing of it stays live through the main loop)
   auto tail_src = [&]() __attribute__((always_inline)) {
     TailSrc ts;
@@ -392,9 +191,9 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
     char* cur = smem + (pr & 1) * kPairSlot;
     char* nxt = smem + ((pr & 1) ^ 1) * kPairSlot;
     __builtin_amdgcn_sched_barrier(0);
-    dense_slots<FI, 0, 0>(cur, nxt, cur, f, pr, acc, F, am, bm, po);
+    dense_slots<MmBf16, FI, 0, 0>(cur, nxt, cur, f, pr, acc, F, am, bm, po);
     __builtin_amdgcn_sched_barrier(0);
-    dense_slots<FI, 1, 0>(cur, nxt, cur, f, pr, acc, F, am, bm, po);
+    dense_slots<MmBf16, FI, 1, 0>(cur, nxt, cur, f, pr, acc, F, am, bm, po);
   }
   // drain the DMAs still in flight (clamped re-loads) before reusing LDS
   QLORA_WAIT(0, 0);
@@ -436,7 +235,30 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
         for (int j = 0; j < 4; ++j) acc[i][j] = mfma32x32x16(F.a0[i], F.b0[j], acc[i][j]);
     }
   };
-  if constexpr (TD) {
+  if constexpr (DR) {
+    if (tail) {
+      const int nt = r <= 32 ? 1 : r <= 64 ? 2 : 4;
+      if constexpr (TD) {
+        const TailSrc ts = tail_src();
+        for (int c = 0; c < nt; ++c) tail_dma(smem + c * 2 * kOp, ts, c, f.w, lane);
+      } else {
+        for (int c = 0; c < nt; ++c) {
+          TailRegs R;
+          tail_load(R, Bl, true, N, r, n0, 32 * c, 0, N, U, ldu, M, m0);
+          tail_store(smem + c * 2 * kOp, R, true, 1.0f);
+        }
+      }
+      QLORA_WAIT(0, 0);
+      __syncthreads();
+      const DropKey key = drop_key(drop);
+      if (nt == 1)
+        masked_tail<FI, 1>(acc, smem, s, key, N, m0, n0);
+      else if (nt == 2)
+        masked_tail<FI, 2>(acc, smem, s, key, N, m0, n0);
+      else
+        masked_tail<FI, 4>(acc, smem, s, key, N, m0, n0);
+    }
+  } else if constexpr (TD) {
     if (tdma) {
       // chunk 0 landed before the drain above; chunks 1 .. go four at a time
       // into the pair slots, the first four while chunk 0 is multiplied
@@ -515,18 +337,20 @@ bool tail_by_dma(int64_t N, int64_t M, int r, int ldu, int64_t gn, int64_t n_beg
 template <int FI>
 hipError_t launch_fi(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* U,
                      const bf16_t* B, bool b_trans, int r, int ldu, int64_t gn, float s, bf16_t* Y, int64_t n_begin,
-                     int64_t n_rows, hipStream_t st, int splits = 1, float* part = nullptr) {
+                     int64_t n_rows, hipStream_t st, const DropArgs* drop, int splits = 1, float* part = nullptr) {
   const int tiles_n = (int)((n_rows + 64 * FI - 1) / (64 * FI));
   const int tiles_m = (int)((M + kTile - 1) / kTile);
   const bool td = tail_by_dma(N, M, r, ldu, gn, n_begin, tiles_n, 64 * FI);
-  auto* fn = td ? &bf16_fwd_kernel<FI, true> : &bf16_fwd_kernel<FI, false>;
-  const size_t lds = td ? kLdsDense : kLdsPairs;
+  auto* fn = drop ? (td ? &bf16_fwd_kernel<FI, true, true> : &bf16_fwd_kernel<FI, false, true>)
+                  : (td ? &bf16_fwd_kernel<FI, true, false> : &bf16_fwd_kernel<FI, false, false>);
+  const size_t lds = td && !drop ? kLdsDense : kLdsPairs;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
   if (e != hipSuccess) return e;
   const int npair = (int)(K >> 6);
   const int pps = splits > 1 ? (npair + splits - 1) / splits : npair;
   hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_m * splits), dim3(kThreads), lds, st, Wd, N, K, X, M, U, B,
-                     (int)b_trans, r, ldu, gn, s, Y, n_begin, tiles_n, tiles_m, pps, splits > 1 ? part : nullptr);
+                     (int)b_trans, r, ldu, gn, s, Y, n_begin, tiles_n, tiles_m, pps, splits > 1 ? part : nullptr,
+                     drop ? *drop : DropArgs{});
   return hipGetLastError();
 }
 
@@ -564,11 +388,11 @@ int best_fi(int64_t rows, int64_t tiles_m, int cus) {
 
 hipError_t launch_rows(int fi, const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M,
                        const bf16_t* U, const bf16_t* B, bool b_trans, int r, int ldu, int64_t gn, float s,
-                       bf16_t* Y, int64_t n_begin, hipStream_t st) {
+                       bf16_t* Y, int64_t n_begin, hipStream_t st, const DropArgs* drop) {
   const int64_t n_rows = N - n_begin;
-  if (fi == 3) return launch_fi<3>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_begin, n_rows, st);
-  if (fi == 2) return launch_fi<2>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_begin, n_rows, st);
-  return launch_fi<4>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_begin, n_rows, st);
+  if (fi == 3) return launch_fi<3>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_begin, n_rows, st, drop);
+  if (fi == 2) return launch_fi<2>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_begin, n_rows, st, drop);
+  return launch_fi<4>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_begin, n_rows, st, drop);
 }
 
 }  // namespace
@@ -596,15 +420,17 @@ size_t dense_split_bytes(int64_t N, int64_t K, int64_t M) {
 // fills whole rounds of 256-row tiles and a remainder, whose tile width (256,
 // 192 or 128 rows) minimizes its time; a shape with fewer 256-row tiles than
 // CUs is all remainder, or a split contraction (above) when part has room.
-hipError_t launch_bf16_group(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* U,
-                             int ldu, const bf16_t* B, bool b_trans, int r, int64_t gn, float s, bf16_t* Y,
-                             hipStream_t st, float* part, size_t part_bytes) {
+namespace {
+
+hipError_t launch_dense(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* U,
+                        int ldu, const bf16_t* B, bool b_trans, int r, int64_t gn, float s, bf16_t* Y,
+                        hipStream_t st, float* part, size_t part_bytes, const DropArgs* drop) {
   const int cus = device_cu_count();
   const int64_t tiles_m = (M + kTile - 1) / kTile;
   const int64_t tiles_n = (N + kTile - 1) / kTile;
   const int sp = dense_splits(N, K, M, cus);
   if (sp > 1 && part != nullptr && part_bytes >= (size_t)sp * (size_t)M * (size_t)N * sizeof(float)) {
-    hipError_t e = launch_fi<4>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, 0, N, st, sp, part);
+    hipError_t e = launch_fi<4>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, 0, N, st, drop, sp, part);
     if (e != hipSuccess) return e;
     const int64_t n = M * N;
     hipLaunchKernelGGL(split_sum_kernel, dim3((unsigned)((n / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
@@ -620,13 +446,27 @@ hipError_t launch_bf16_group(const bf16_t* Wd, int64_t N, int64_t K, const bf16_
       n_split = 0;   // nothing left over, or the remainder gains nothing from narrower tiles: one launch
   }
   if (n_split > 0) {
-    hipError_t e = launch_fi<4>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, 0, n_split, st);
+    hipError_t e = launch_fi<4>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, 0, n_split, st, drop);
     if (e != hipSuccess) return e;
     // the remainder's tiles address rows from n_split on, in the same arrays
     return launch_rows(best_fi(N - n_split, tiles_m, cus), Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_split,
-                       st);
+                       st, drop);
   }
-  return launch_rows(best_fi(N, tiles_m, cus), Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, 0, st);
+  return launch_rows(best_fi(N, tiles_m, cus), Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, 0, st, drop);
+}
+
+}  // namespace
+
+hipError_t launch_bf16_group(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* U,
+                             int ldu, const bf16_t* B, bool b_trans, int r, int64_t gn, float s, bf16_t* Y,
+                             hipStream_t st, float* part, size_t part_bytes) {
+  return launch_dense(Wd, N, K, X, M, U, ldu, B, b_trans, r, gn, s, Y, st, part, part_bytes, nullptr);
+}
+
+hipError_t launch_bf16_dx_drop(const bf16_t* WdT, int64_t K, int64_t N, const bf16_t* dY, int64_t M, const bf16_t* G,
+                               const bf16_t* A, int r, float s, const DropArgs& drop, bf16_t* dX, hipStream_t st,
+                               float* part, size_t part_bytes) {
+  return launch_dense(WdT, K, N, dY, M, G, r, A, true, r, K, s * drop.scale, dX, st, part, part_bytes, &drop);
 }
 
 hipError_t launch_bf16_fwd(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* U,

@@ -20,6 +20,18 @@ struct Nf4View {
   int absfmt;    // second-level format (the values of qlora_absmax_format)
 };
 
+// Dropout of one call: the mask's key and counter offset, the threshold on
+// signed 16-bit halves and the factor 1 / (1 - p) of what is kept (rng.h).
+struct DropArgs {
+  uint64_t seed, offset;
+  const uint64_t* step;   // device memory, may be null: added to offset
+  int thr;
+  float scale;
+};
+
+// y = drop(x) over n bf16 values (16-byte aligned; y may be x).
+hipError_t launch_dropout(const bf16_t* x, int64_t n, const DropArgs& d, bf16_t* y, hipStream_t st);
+
 // Compute units of the current device (256 if the query fails).
 int device_cu_count();
 
@@ -104,6 +116,57 @@ size_t grads_partial_bytes(int64_t M, int64_t N, int64_t K, int r, int G);
 hipError_t launch_grads(const bf16_t* Gm, const bf16_t* X, const bf16_t* dY, int64_t ldy, const bf16_t* U, int ldu,
                         int64_t M, int64_t N, int64_t K, int r, int G, float* part, float* dA, float* dB, float scale,
                         hipStream_t st);
+
+// The same products for an adapter under dropout and for callers that need
+// fp32-accurate gradients: drop may be null (no mask).
+// out [M x r] = drop(X) A^T; partials as launch_xat.
+hipError_t launch_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
+                           float* part, bf16_t* out, hipStream_t st);
+// hi + lo [M x r each] = dY B to about 16 bits; partials as launch_dyb.
+hipError_t launch_dyb_hl(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* hi,
+                         bf16_t* lo, hipStream_t st);
+// dA [r x K] = scale (hi + lo)^T drop(X), dB [N x r] = scale dY^T U;
+// partials: grads_partial_bytes(M, N, K, r, 1).
+hipError_t launch_grads_hl(const bf16_t* hi, const bf16_t* lo, const bf16_t* X, const bf16_t* dY, const bf16_t* U,
+                           int64_t M, int64_t N, int64_t K, int r, const DropArgs* drop, float* part, float* dA,
+                           float* dB, float scale, hipStream_t st);
+
+// dX [M x K] = dY WdT^T + s drop'(G A): the dense product on WdT [K x N]
+// (K weight rows, contraction N % 64 == 0) with the adapter's product masked
+// as the M x K tensor X was.
+hipError_t launch_bf16_dx_drop(const bf16_t* WdT, int64_t K, int64_t N, const bf16_t* dY, int64_t M, const bf16_t* G,
+                               const bf16_t* A, int r, float s, const DropArgs& drop, bf16_t* dX, hipStream_t st,
+                               float* part, size_t part_bytes);
+
+// Rows of 8-bit integers with one scale each (i8.hip): bytes from one row to
+// the next, and the passes over them.
+inline int64_t i8_row_bytes(int64_t cols) { return (cols + 127) / 128 * 128; }
+constexpr int64_t kI8MaxCols = 131072;   // 127^2 cols fits a 32-bit sum
+// Q [M x i8_row_bytes(K)], scale [M] from X [M x K], K % 8 == 0.
+hipError_t launch_quant_rows(const bf16_t* X, int64_t M, int64_t K, int8_t* Q, float* scale, hipStream_t st);
+hipError_t launch_i8_dequant(const int8_t* Q, const float* scale, int64_t N, int64_t K, bf16_t* out, hipStream_t st);
+// out [K x ldo] = deq^T, ldo = N rounded up to 64, the columns past N zero.
+hipError_t launch_i8_dequant_t(const int8_t* Q, const float* scale, int64_t N, int64_t K, bf16_t* out, int64_t ldo,
+                               hipStream_t st);
+// out [rows x ldo]: in [rows x cols] (null: nothing copied) and zero columns
+// cols .. ldo - 1.
+hipError_t launch_pad_rows(const bf16_t* in, int64_t rows, int64_t cols, bf16_t* out, int64_t ldo, hipStream_t st);
+
+// Y [M x N] = sx sw^T o (Xq Wq^T) + s U B^T (r may be 0).
+struct I8Gemm {
+  const int8_t* Wq;
+  const float* sw;
+  int64_t N, K;
+  const int8_t* Xq;
+  const float* sx;
+  int64_t M;
+  const bf16_t* U;
+  const bf16_t* B;
+  int r;
+  float s;
+  bf16_t* Y;
+};
+hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st);
 
 // The paged optimizer's layout and step (paged.hip).
 bool paged_plan(const qlora_paged_tensor* t, int nt, size_t dev_bytes, qlora_paged_layout* L);

@@ -13,6 +13,7 @@ import torch
 
 from . import _lib
 from . import debug as _debug
+from ._lib import DropDesc, I8RowsDesc
 from ._lib import GemvJobDesc, GemvPlanDesc, Nf4WeightDesc, PagedLayoutDesc, PagedTensorDesc, lib
 from ._lib import check as _check_status
 
@@ -217,6 +218,75 @@ def dequant_t(q: QuantizedWeight, out: Optional[torch.Tensor] = None) -> torch.T
     return out
 
 
+@dataclass
+class Dropout:
+    """Dropout of an adapter's input: keep with probability 1 - p, from a
+    counter-based generator; the same seed and offset give the same mask in
+    the forward and the backward pass.  Give every layer and step its own
+    offset.  step, when given, is an int64 or uint64 GPU tensor of one element
+    that is added to the offset when the kernels run (for captured graphs)."""
+    p: float
+    seed: int
+    offset: int = 0
+    step: Optional[torch.Tensor] = None
+
+    def desc(self, device) -> DropDesc:
+        step = None
+        if self.step is not None:
+            if self.step.dtype not in (torch.int64, torch.uint64) or self.step.numel() != 1:
+                raise ValueError("step must be an int64 or uint64 tensor of one element")
+            if self.step.device != device:
+                raise ValueError(f"step must be on {device}")
+            step = self.step.data_ptr()
+        return DropDesc(float(self.p), self.seed & _U64, self.offset & _U64, step)
+
+
+_U64 = (1 << 64) - 1
+
+
+def _on_current(device):
+    """The current stream belongs to the current device: a call on another
+    device's tensors is refused."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _beside(t, like, name):
+    if t is not None and t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    return t
+
+
+def _out(t, shape, dtype, like, name):
+    """The caller's output checked, or a new one."""
+    if t is None:
+        return _empty(shape, dtype=dtype, device=like.device)
+    return _beside(_need(t, dtype, name, shape), like, name)
+
+
+def _ws_for(ws, nbytes, like):
+    if ws is None:
+        return workspace(nbytes, like.device)
+    return _beside(_need(ws, torch.uint8, "ws"), like, "ws")
+
+
+def _ws_args(ws):
+    return _ptr(ws), 0 if ws is None else ws.numel()
+
+
+def dropout(x: torch.Tensor, drop: Dropout, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """drop(x), bf16, of any contiguous shape; out may be x.  The gradient is
+    dropout(dy, drop)."""
+    _need(x, torch.bfloat16, "x")
+    _on_current(x.device)
+    out = _out(out, x.shape, torch.bfloat16, x, "out")
+    if x.numel() == 0:
+        return out
+    d = drop.desc(x.device)
+    check(lib().qlora_dropout(_ptr(x), x.numel(), ctypes.byref(d), _ptr(out), _stream()), "qlora_dropout")
+    return out
+
+
 PATHS = ("auto", "fused")
 
 
@@ -227,8 +297,10 @@ def _op(path, staged_op, fused_op):
 
 
 def linear_fwd(q: QuantizedWeight, X: torch.Tensor, A=None, B=None, alpha: float = 0.0,
-               save_u: bool = False, out=None, u_out=None, ws=None, path: str = "auto"):
+               save_u: bool = False, out=None, u_out=None, ws=None, path: str = "auto",
+               drop: Optional[Dropout] = None):
     """Y = X deq(W)^T + (alpha/r) (X A^T) B^T.  Returns Y, or (Y, U) with save_u.
+    With drop, U = drop(X) A^T.
 
     path "auto" sizes the workspace for the staged path (the library takes it
     from 1024 tokens on: W dequantized once, then the dense bf16 product);
@@ -249,6 +321,13 @@ def linear_fwd(q: QuantizedWeight, X: torch.Tensor, A=None, B=None, alpha: float
     elif ws.numel() > nbytes:
         ws = ws[:nbytes]
     d = q.desc()
+    if drop is not None:
+        _on_current(X.device)
+        dd = drop.desc(X.device)
+        check(lib().qlora_linear_fwd_drop(ctypes.byref(d), _ptr(X), M, _ptr(A), _ptr(B), r, float(alpha),
+                                          ctypes.byref(dd), _ptr(Y), _ptr(U), *_ws_args(ws), _stream()),
+              "qlora_linear_fwd_drop")
+        return (Y, U) if save_u else Y
     check(lib().qlora_linear_fwd(ctypes.byref(d), _ptr(X), M, _ptr(A), _ptr(B), r, float(alpha), _ptr(Y),
                                  _ptr(U), _ptr(ws), 0 if ws is None else ws.numel(), _stream()),
           "qlora_linear_fwd")
@@ -280,10 +359,18 @@ def linear_fwd_noalloc(q: QuantizedWeight, X: torch.Tensor, A=None, B=None, alph
 
 def linear_bwd(q: QuantizedWeight, X: torch.Tensor, dY: torch.Tensor, A=None, B=None, alpha: float = 0.0,
                U: Optional[torch.Tensor] = None, need_dx: bool = True, dX=None, dA=None, dB=None, ws=None,
-               path: str = "auto"):
+               path: str = "auto", drop: Optional[Dropout] = None):
     """Returns (dX, dA, dB): dX bf16 [M x K] (or None), dA [r x K] and dB [N x r] fp32 (or None).
-    path as in linear_fwd."""
+    path as in linear_fwd.  With drop (the forward's), the adapter's gradients
+    are those under its mask; that backward is always staged (ws sized by
+    QLORA_OP_BWD_DROP)."""
     _need(dY, torch.bfloat16, "dY")
+    if drop is not None:
+        if path != "auto":
+            raise ValueError("the backward under dropout has no fused path")
+        d = q.desc()
+        return _staged_bwd("qlora_linear_bwd_drop", _lib.QLORA_OP_BWD_DROP, d, q.rows, q.cols, X, dY, A, B, alpha, U,
+                           drop, need_dx, dX, dA, dB, ws)
     M = dY.shape[0]
     r = 0 if A is None else A.shape[0]
     if r:
@@ -309,6 +396,130 @@ def linear_bwd(q: QuantizedWeight, X: torch.Tensor, dY: torch.Tensor, A=None, B=
                                  0 if ws is None else ws.numel(), _stream()),
           "qlora_linear_bwd")
     return dX, dA, dB
+
+
+def _staged_bwd(name, op, d, N, K, X, dY, A, B, alpha, U, drop, need_dx, dX, dA, dB, ws):
+    _on_current(dY.device)
+    M = dY.shape[0]
+    _need(dY, torch.bfloat16, "dY", (M, N))
+    r = 0 if A is None else A.shape[0]
+    if r:
+        _beside(_need(X, torch.bfloat16, "X", (M, K)), dY, "X")
+        _beside(_need(A, torch.bfloat16, "A", (r, K)), dY, "A")
+        _beside(_need(B, torch.bfloat16, "B", (N, r)), dY, "B")
+        if U is not None:
+            _beside(_need(U, torch.bfloat16, "U", (M, r)), dY, "U")
+        dA = _out(dA, (r, K), torch.float32, dY, "dA")
+        dB = _out(dB, (N, r), torch.float32, dY, "dB")
+    else:
+        X = U = dA = dB = None
+    dX = _out(dX, (M, K), torch.bfloat16, dY, "dX") if need_dx else None
+    ws = _ws_for(ws, workspace_bytes(op, M, N, K, r), dY)
+    dd = None if drop is None else ctypes.byref(drop.desc(dY.device))
+    check(getattr(lib(), name)(ctypes.byref(d), _ptr(X), _ptr(dY), M, _ptr(A), _ptr(B), r, float(alpha), _ptr(U), dd,
+                               _ptr(dX), _ptr(dA), _ptr(dB), *_ws_args(ws), _stream()), name)
+    return dX, dA, dB
+
+
+@dataclass
+class Int8Weight:
+    """Rows of 8-bit integers with one fp32 scale each: a frozen weight
+    [rows x cols] (one scale per output channel) or quantized inputs (one per
+    token).  codes [rows x i8_row_bytes(cols)], zero past cols."""
+    rows: int
+    cols: int
+    codes: torch.Tensor        # int8
+    scale: torch.Tensor        # float32 [rows]
+
+    def desc(self) -> I8RowsDesc:
+        _need(self.codes, torch.int8, "codes", (self.rows, i8_row_bytes(self.cols)))
+        _beside(_need(self.scale, torch.float32, "scale", (self.rows,)), self.codes, "scale")
+        return I8RowsDesc(self.rows, self.cols, self.codes.data_ptr(), self.scale.data_ptr())
+
+    @staticmethod
+    def empty(rows, cols, device):
+        return Int8Weight(rows, cols, _empty(rows, i8_row_bytes(cols), dtype=torch.int8, device=device),
+                          _empty(rows, dtype=torch.float32, device=device))
+
+    def nbytes(self):
+        return self.codes.numel() + 4 * self.scale.numel()
+
+
+def i8_row_bytes(cols):
+    """Bytes of one row of codes (cols rounded up to 128)."""
+    return int(lib().qlora_i8_row_bytes(cols))
+
+
+def i8_quantize(X: torch.Tensor, out: Optional[Int8Weight] = None) -> Int8Weight:
+    """bf16 rows -> 8-bit integers with one scale per row (a weight's output
+    channels, an input's tokens)."""
+    _need(X, torch.bfloat16, "X")
+    if X.dim() != 2:
+        raise ValueError(f"X must be a matrix, got shape {tuple(X.shape)}")
+    _on_current(X.device)
+    q = out if out is not None else Int8Weight.empty(X.shape[0], X.shape[1], X.device)
+    if (q.rows, q.cols) != tuple(X.shape):
+        raise ValueError(f"out is {q.rows} x {q.cols}, X is {tuple(X.shape)}")
+    _beside(q.codes, X, "out")
+    d = q.desc()
+    check(lib().qlora_i8_quantize(_ptr(X), ctypes.byref(d), _stream()), "qlora_i8_quantize")
+    return q
+
+
+def i8_dequant(q: Int8Weight, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """bf16 [rows x cols] of the codes times their row's scale."""
+    d = q.desc()
+    _on_current(q.codes.device)
+    out = _out(out, (q.rows, q.cols), torch.bfloat16, q.codes, "out")
+    check(lib().qlora_i8_dequant(ctypes.byref(d), _ptr(out), _stream()), "qlora_i8_dequant")
+    return out
+
+
+def i8_matmul(xq: Int8Weight, w: Int8Weight, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = X W^T of quantized rows (bf16 [tokens x channels]): an input
+    quantized once by i8_quantize, times one of the weights that read it."""
+    dx, dw = xq.desc(), w.desc()
+    _on_current(w.codes.device)
+    _beside(xq.codes, w.codes, "xq")
+    Y = _out(out, (xq.rows, w.rows), torch.bfloat16, w.codes, "out")
+    check(lib().qlora_i8_matmul(ctypes.byref(dx), ctypes.byref(dw), _ptr(Y), _stream()), "qlora_i8_matmul")
+    return Y
+
+
+def i8_linear_fwd(w: Int8Weight, X: torch.Tensor, A=None, B=None, alpha: float = 0.0, save_u: bool = False, out=None,
+                  u_out=None, ws=None, drop: Optional[Dropout] = None):
+    """Y = Xq W^T + (alpha/r) U B^T with X quantized per token and U = drop(X)
+    A^T (X A^T without drop), for any number of tokens.  Returns Y, or (Y, U)
+    with save_u."""
+    _need(X, torch.bfloat16, "X")
+    _on_current(X.device)
+    M = X.shape[0]
+    _need(X, torch.bfloat16, "X", (M, w.cols))
+    _beside(w.codes, X, "w")
+    r = 0 if A is None else A.shape[0]
+    if r:
+        _beside(_need(A, torch.bfloat16, "A", (r, w.cols)), X, "A")
+        _beside(_need(B, torch.bfloat16, "B", (w.rows, r)), X, "B")
+    Y = _out(out, (M, w.rows), torch.bfloat16, X, "out")
+    U = _out(u_out, (M, r), torch.bfloat16, X, "u_out") if save_u and r else None
+    ws = _ws_for(ws, workspace_bytes(_lib.QLORA_OP_I8_FWD, M, w.rows, w.cols, r), X)
+    d = w.desc()
+    dd = None if drop is None else ctypes.byref(drop.desc(X.device))
+    check(lib().qlora_i8_linear_fwd(ctypes.byref(d), _ptr(X), M, _ptr(A), _ptr(B), r, float(alpha), dd, _ptr(Y),
+                                    _ptr(U), *_ws_args(ws), _stream()), "qlora_i8_linear_fwd")
+    return (Y, U) if save_u else Y
+
+
+def i8_linear_bwd(w: Int8Weight, X, dY: torch.Tensor, A=None, B=None, alpha: float = 0.0,
+                  U: Optional[torch.Tensor] = None, need_dx: bool = True, dX=None, dA=None, dB=None, ws=None,
+                  drop: Optional[Dropout] = None):
+    """Backward of i8_linear_fwd, the gradient in 16 bits through the
+    dequantized weight.  Returns (dX, dA, dB) as linear_bwd."""
+    _need(dY, torch.bfloat16, "dY")
+    d = w.desc()
+    _beside(w.codes, dY, "w")
+    return _staged_bwd("qlora_i8_linear_bwd", _lib.QLORA_OP_I8_BWD, d, w.rows, w.cols, X, dY, A, B, alpha, U, drop,
+                       need_dx, dX, dA, dB, ws)
 
 
 def _group_descs(qs: Sequence[QuantizedWeight]):

@@ -93,9 +93,12 @@ typedef enum {
                               qlora_lora_down at rank G r,
                               qlora_group_lora_dy_b, qlora_group_lora_grads
                               (njobs = G)                                    */
-  QLORA_OP_BF16_DX = 9     /* the split contraction of qlora_bf16_dx
+  QLORA_OP_BF16_DX = 9,    /* the split contraction of qlora_bf16_dx
                               (njobs = 1) and qlora_bf16_group_dx (njobs = G):
                               0 for shapes that do not split                 */
+  QLORA_OP_BWD_DROP = 10,  /* qlora_linear_bwd_drop                          */
+  QLORA_OP_I8_FWD = 11,    /* qlora_i8_linear_fwd                            */
+  QLORA_OP_I8_BWD = 12     /* qlora_i8_linear_bwd                            */
 } qlora_op;
 
 /* A quantized weight: host struct holding device pointers.
@@ -522,6 +525,111 @@ qlora_status qlora_gemv_prepare(const qlora_gemv_job* jobs, int32_t njobs, void*
  * be ordered after it by the caller.  QLORA_E_SHAPE for a plan that
  * qlora_gemv_prepare did not fill. */
 qlora_status qlora_gemv_run(const qlora_gemv_plan* plan, void* stream);
+
+/* ---- Dropout --------------------------------------------------------------
+ * LoRA training drops inputs of the adapter branch: the adapter sees
+ * drop(X), which keeps each element with probability 1 - p and divides what
+ * it keeps by 1 - p, while the frozen product sees X.  No mask is stored: the
+ * bits are a function of the seed, an offset and the element's position, and
+ * the backward pass computes them again.
+ *
+ * Generator: Philox-4x32 with 7 rounds (Salmon, Moraes, Dror and Shaw,
+ * "Parallel random numbers: as easy as 1, 2, 3", SC 2011).  Element e of the
+ * row-major tensor takes 16-bit half e mod 8 (word (e mod 8) / 2, low half
+ * first) of the block with counter words {lo, hi of e / 8, lo, hi of the
+ * offset} and key {lo, hi of the seed}.  With t = min(65535, floor(65536 p +
+ * 1/2)) the element is kept where the half, read as a signed number, is at
+ * least t - 32768, and scaled by 65536 / (65536 - t); a dropped element is 0
+ * whatever it held (infinities and NaN included).  Two calls use the same
+ * mask if and only if seed and offset (and the position) agree: give each
+ * layer and step its own offset. */
+typedef struct {
+  double p;              /* probability of dropping, in [0, 1)               */
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* step;  /* nullable DEVICE pointer (8-byte aligned), read when
+                            the kernels run: the offset is offset + *step, so
+                            a captured graph draws new masks on each replay */
+} qlora_drop;
+
+/* y = drop(x) over n bf16 values, rounded once; y may be x.  The gradient is
+ * the same call on dy.  QLORA_E_UNSUPPORTED for p outside [0, 1). */
+qlora_status qlora_dropout(const uint16_t* x, int64_t n, const qlora_drop* drop, uint16_t* y, void* stream);
+
+/* qlora_linear_fwd with the adapter under dropout:
+ *   Y = X deq(W)^T + s U B^T,  U = drop(X) A^T,  drop over X [M x K].
+ * Arguments, paths, workspace (QLORA_OP_FWD / _FWD_FUSED) and errors as
+ * qlora_linear_fwd; r > 0 and drop not NULL.  At p = 0 the result is
+ * qlora_linear_fwd's. */
+qlora_status qlora_linear_fwd_drop(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, const uint16_t* A,
+                                   const uint16_t* B, int32_t r, float alpha, const qlora_drop* drop, uint16_t* Y,
+                                   uint16_t* U_save, void* ws, size_t ws_bytes, void* stream);
+
+/* Its backward, under the forward's seed and offset (and step):
+ *   dX = dY deq(W) + s drop'(G A),  G = dY B,  drop'(Z) masked and scaled as
+ *                                   X was (NULL dX skips it);
+ *   dA = s G^T drop(X),  dB = s dY^T U.
+ * U_saved is the forward's U; NULL computes it again.  G is kept to 16 bits
+ * of mantissa for dA (two bf16 parts), to bf16 for dX.  Always staged, for
+ * any M: workspace qlora_workspace_bytes(QLORA_OP_BWD_DROP, M, N, K, r, 0),
+ * which holds deq(W)^T.  K % 64 == 0, N % 8 == 0; with Np = N rounded up to
+ * 64, Np K and M Np below 2^31 (QLORA_E_UNSUPPORTED otherwise). */
+qlora_status qlora_linear_bwd_drop(const qlora_nf4_weight* W, const uint16_t* X, const uint16_t* dY, int64_t M,
+                                   const uint16_t* A, const uint16_t* B, int32_t r, float alpha,
+                                   const uint16_t* U_saved, const qlora_drop* drop, uint16_t* dX, float* dA,
+                                   float* dB, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- 8-bit linears ---------------------------------------------------------
+ * A frozen weight as 8-bit integers with one fp32 scale per output channel,
+ * multiplied with inputs quantized the same way per token: twice the bytes of
+ * NF4, integer products at twice the bf16 rate, and the same adapter.
+ *
+ * Rows of 8-bit integers: scale_m = RN32(amax_m / 127) with amax_m the row's
+ * largest magnitude, and code = the integer nearest 127 x / amax_m, ties to
+ * even, in [-127, 127].  A row of zeros has scale 0; a row that holds an
+ * infinity or a NaN has scale NaN and codes 0 (its products are NaN, other
+ * rows' are not touched). */
+typedef struct {
+  int64_t rows;    /* output channels of a weight, tokens of an input        */
+  int64_t cols;    /* K: K % 8 == 0, K <= 131072                             */
+  int8_t* codes;   /* rows of qlora_i8_row_bytes(cols) bytes, codes past cols
+                      zero; 16-byte aligned                                  */
+  float* scale;    /* [rows], 16-byte aligned                                */
+} qlora_i8_rows;
+
+/* Bytes from one row of codes to the next: cols rounded up to 128; 0 for
+ * cols <= 0 or > 131072. */
+size_t qlora_i8_row_bytes(int64_t cols);
+
+/* Quantize bf16 X [rows x cols] into q: codes (the zeros past cols
+ * included) and scales are overwritten.  rows * row bytes below 2^31. */
+qlora_status qlora_i8_quantize(const uint16_t* X, const qlora_i8_rows* q, void* stream);
+
+/* out [rows x cols] = RNE_bf16(RN32(scale code)). */
+qlora_status qlora_i8_dequant(const qlora_i8_rows* q, uint16_t* out, void* stream);
+
+/* Y [M x N] = the product of quantized rows: bf16 of sx_m sw_n sum_k x w,
+ * the sum in 32-bit integers.  For callers that quantize an input once and
+ * multiply it by several weights.  W->rows % 8 == 0, M N below 2^31. */
+qlora_status qlora_i8_matmul(const qlora_i8_rows* X, const qlora_i8_rows* W, uint16_t* Y, void* stream);
+
+/* Forward: Y [M x N] = Xq W^T (as qlora_i8_matmul, with X quantized per token
+ * into the workspace) + s U B^T, U = drop(X) A^T (drop NULL: X A^T).  A, B,
+ * r, alpha, U_save as for qlora_linear_fwd; r == 0 gives the frozen layer
+ * alone (drop must be NULL).  Any M >= 1; N % 8 == 0, K % 8 == 0.
+ * Workspace: qlora_workspace_bytes(QLORA_OP_I8_FWD, M, N, K, r, 0). */
+qlora_status qlora_i8_linear_fwd(const qlora_i8_rows* W, const uint16_t* X, int64_t M, const uint16_t* A,
+                                 const uint16_t* B, int32_t r, float alpha, const qlora_drop* drop, uint16_t* Y,
+                                 uint16_t* U_save, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward, with the gradient in 16 bits: dX [M x K] = dY deq(W) + s drop'(G
+ * A) with deq(W) as qlora_i8_dequant gives it, dA and dB as
+ * qlora_linear_bwd_drop (drop NULL: no mask).  r == 0: dA and dB NULL.
+ * Workspace: qlora_workspace_bytes(QLORA_OP_I8_BWD, M, N, K, r, 0). */
+qlora_status qlora_i8_linear_bwd(const qlora_i8_rows* W, const uint16_t* X, const uint16_t* dY, int64_t M,
+                                 const uint16_t* A, const uint16_t* B, int32_t r, float alpha,
+                                 const uint16_t* U_saved, const qlora_drop* drop, uint16_t* dX, float* dA, float* dB,
+                                 void* ws, size_t ws_bytes, void* stream);
 
 /* ---- Serialized quantized weights -------------------------------------
  * An adapter is trained against one exact quantized base weight: the pages
