@@ -863,11 +863,15 @@ qlora_status qlora_i8_linear_fwd(const qlora_i8_rows* W, const uint16_t* X, int6
   int8_t* xq = reinterpret_cast<int8_t*>(ws_at(ws, L.xq));
   float* sx = reinterpret_cast<float*>(ws_at(ws, L.sx));
   bf16_t* U = r > 0 ? (U_save ? U_save : reinterpret_cast<bf16_t*>(ws_at(ws, L.u))) : nullptr;
-  if (r > 0) {
+  const DropArgs* dp = active ? &d : nullptr;
+  if (i8_prep_ok(M, K)) {
+    st = hip_status(launch_i8_prep(X, M, K, A, r, dp, U, xq, sx, s));
+  } else {
     float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
-    if ((st = hip_status(launch_xat_drop(X, A, M, K, r, active ? &d : nullptr, part, U, s))) != QLORA_OK) return st;
+    if (r > 0 && (st = hip_status(launch_xat_drop(X, A, M, K, r, dp, part, U, s))) != QLORA_OK) return st;
+    st = hip_status(launch_quant_rows(X, M, K, xq, sx, s));
   }
-  if ((st = hip_status(launch_quant_rows(X, M, K, xq, sx, s))) != QLORA_OK) return st;
+  if (st != QLORA_OK) return st;
   const float sc = r > 0 ? (float)((double)alpha / (double)r) : 0.0f;
   const I8Gemm g{W->codes, W->scale, N, K, xq, sx, M, U, B, r, sc, Y};
   return hip_status(launch_i8_gemm(g, s));

@@ -45,6 +45,7 @@ __device__ __forceinline__ void scale_tile(const i32x16_t (&acc)[FI][4], f32x16_
         out[i][j][4 * q + 2] = (float)acc[i][j][4 * q + 2] * (x[j] * v.z);
         out[i][j][4 * q + 3] = (float)acc[i][j][4 * q + 3] * (x[j] * v.w);
       }
+      __builtin_amdgcn_sched_barrier(0);   // one quarter's scales at a time
     }
 }
 
@@ -159,6 +160,274 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
   store_tile_lds<FI>(out, Y, N, M, N, m0, n0, smem);
 }
 
+// ---------------------------------------------------------------------------
+// Few tokens (M <= 16 MT): the weight is streamed once, straight into the
+// MFMA layout, and nothing else matters.  A workgroup of 8 waves takes 16 R
+// channels; the waves take the 128-byte lines of a row in turn, so all eight
+// stream the same rows, and their integer sums meet in LDS (exact in any
+// order).  16x16x64 MFMA: lane (l = lane & 15, g = lane >> 4) holds 16 bytes
+// of channel l (A) or token l (B); a load instruction takes 64 contiguous
+// bytes of 16 rows, the next one the other half of the same lines.  The
+// tokens come from L2 in the same layout.  Loads run one batch of kUp lines
+// ahead of the products.
+// ---------------------------------------------------------------------------
+constexpr int kSkWaves = 8;
+
+__device__ __forceinline__ i32x4_t ld16(const int8_t* p) { return *reinterpret_cast<const i32x4_t*>(p); }
+
+template <int R, int MT>
+struct SkinnyBatch {
+  i32x4_t a[R][2], b[MT][2];
+};
+
+template <int R, int MT, int UP>
+__global__ __launch_bounds__(kSkWaves * 64, 1) void i8_skinny_kernel(const int8_t* __restrict__ Wq,
+                                                                     const float* __restrict__ sw, int64_t N,
+                                                                     int64_t ld, const int8_t* __restrict__ Xq,
+                                                                     const float* __restrict__ sx, int64_t M,
+                                                                     const bf16_t* __restrict__ U,
+                                                                     const bf16_t* __restrict__ B, int r, float s,
+                                                                     bf16_t* __restrict__ Y) {
+  __shared__ __align__(16) i32x4_t red[kSkWaves][R * MT][64];
+  // the wave's number as a scalar: its branches must not mask lanes, which an
+  // MFMA would ignore
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * R;
+  const int8_t* wp[R];
+  const int8_t* xp[MT];
+#pragma unroll
+  for (int i = 0; i < R; ++i) wp[i] = Wq + min(n0 + 16 * i + l, N - 1) * ld + 16 * g;   // rows past the end: never stored
+#pragma unroll
+  for (int j = 0; j < MT; ++j) xp[j] = Xq + min((int64_t)(16 * j + l), M - 1) * ld + 16 * g;
+  const int lines = (int)(ld >> 7);
+
+  i32x4_t acc[R][MT];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+
+  typedef SkinnyBatch<R, MT> Line;
+  auto load = [&](Line& v, int line) __attribute__((always_inline)) {   // a line past the end re-loads the last one
+    const int64_t o = (int64_t)min(line, lines - 1) * 128;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) v.a[i][c] = ld16(wp[i] + o + 64 * c);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) v.b[j][c] = ld16(xp[j] + o + 64 * c);
+    }
+  };
+  auto mul = [&](const Line& v) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v.a[i][c], v.b[j][c], acc[i][j], 0, 0, 0);
+  };
+  Line cur[UP], nxt[UP];
+#pragma unroll
+  for (int u = 0; u < UP; ++u) load(cur[u], w + kSkWaves * u);
+  for (int base = w; base < lines; base += kSkWaves * UP) {
+    const bool more = base + kSkWaves * UP < lines;
+    if (more) {
+#pragma unroll
+      for (int u = 0; u < UP; ++u) load(nxt[u], base + kSkWaves * (UP + u));
+    }
+#pragma unroll
+    for (int u = 0; u < UP; ++u)
+      if (base + kSkWaves * u < lines) mul(cur[u]);
+    if (more) {
+#pragma unroll
+      for (int u = 0; u < UP; ++u) cur[u] = nxt[u];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) red[w][i * MT + j][lane] = acc[i][j];
+  __syncthreads();
+  // wave b < R MT finishes block b: D[channel][token], lane: token l, channels 4 g ..
+#pragma unroll
+  for (int b = 0; b < R * MT; b += kSkWaves) {
+    const int blk = b + w;
+    if (blk >= R * MT) break;
+    const int i = blk / MT, j = blk % MT;
+    i32x4_t t = red[0][blk][lane];
+#pragma unroll
+    for (int v = 1; v < kSkWaves; ++v) t += red[v][blk][lane];
+    const int64_t m = 16 * j + l, nrow = n0 + 16 * i, n = nrow + 4 * g;
+    f32x4_t lo = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < r; c += 32) {   // adapter: 16 channels x 16 tokens over the rank
+      const int k = c + 8 * g;
+      bf16x8_t fb{}, fu{};
+      if (k < r && nrow + l < N) fb = *reinterpret_cast<const bf16x8_t*>(B + (nrow + l) * r + k);
+      if (k < r && m < M) fu = *reinterpret_cast<const bf16x8_t*>(U + m * r + k);
+      lo = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fu, lo, 0, 0, 0);
+    }
+    if (m < M && n < N) {   // N % 8 == 0
+      const float4 sc = *reinterpret_cast<const float4*>(sw + n);
+      const float x = sx[m];
+      const float y0 = fmaf(s, lo[0], (float)t[0] * (x * sc.x)), y1 = fmaf(s, lo[1], (float)t[1] * (x * sc.y)),
+                  y2 = fmaf(s, lo[2], (float)t[2] * (x * sc.z)), y3 = fmaf(s, lo[3], (float)t[3] * (x * sc.w));
+      *reinterpret_cast<uint2*>(Y + m * N + n) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
+    }
+  }
+}
+
+template <int R, int MT, int UP>
+hipError_t launch_skinny(const I8Gemm& g, hipStream_t st) {
+  hipLaunchKernelGGL((i8_skinny_kernel<R, MT, UP>), dim3((unsigned)((g.N + 16 * R - 1) / (16 * R))),
+                     dim3(kSkWaves * 64), 0, st, g.Wq, g.sw, g.N, i8_row_bytes(g.K), g.Xq, g.sx, g.M, g.U, g.B, g.r,
+                     g.s, g.Y);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// A middling number of tokens: TM tokens x TN channels per workgroup, waves
+// 2 x 2 over the tile, a ring of NS stages of 128 bytes of all its rows.
+// Smaller tiles than the 256 x 256 kernel's read LDS more per product, but
+// there are enough of them for the whole card.
+//
+// The fragments of a 32-byte step are read one step ahead of their MFMAs.
+// The stage's barrier stands before its last step's MFMAs, which hide the
+// first reads of the next stage: there every wave has read all of the stage,
+// so the DMA of stage st + NS goes into its slot at once.
+// ---------------------------------------------------------------------------
+template <int TM, int TN, int NS>
+__global__ __launch_bounds__(kThreads, 1) void i8_tile_kernel(const int8_t* __restrict__ Wq,
+                                                              const float* __restrict__ sw, int64_t N, int64_t ld,
+                                                              const int8_t* __restrict__ Xq,
+                                                              const float* __restrict__ sx, int64_t M,
+                                                              const bf16_t* __restrict__ U,
+                                                              const bf16_t* __restrict__ B, int r, float s,
+                                                              bf16_t* __restrict__ Y, int64_t n_begin, int tiles_n,
+                                                              int tiles_m) {
+  constexpr int FI = TN / 64, FJ = TM / 64;         // 32-row fragments per wave
+  constexpr int kRows = TM + TN, kSlot = kRows * 128, kDma = kRows / 32;   // DMA instructions per wave and stage
+  extern __shared__ __align__(16) char smem[];
+  int tn, tm;
+  map_tile_grouped(xcd_tile_id(), tiles_n, tiles_m, tn, tm);
+  const int64_t n0 = n_begin + (int64_t)tn * TN, m0 = (int64_t)tm * TM;
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), wr = w >> 1, wc = w & 1;
+  const int lr = lane & 31, h = lane >> 5;
+  const int nst = (int)(ld >> 7);
+  // weight rows 0 .. TN - 1, then token rows; instruction q of wave w brings
+  // rows 8 (4 q + w) .. + 7
+  const rsrc_t wres = make_rsrc(Wq, (uint32_t)(N * ld)), xres = make_rsrc(Xq, (uint32_t)(M * ld));
+  uint32_t off[kDma];
+#pragma unroll
+  for (int q = 0; q < kDma; ++q) {
+    const int row = 8 * (4 * q + w) + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+    const int64_t src = q < TN / 32 ? min(n0 + row, N - 1) : min(m0 + row - TN, M - 1);
+    off[q] = (uint32_t)(src * ld + 16 * c);
+  }
+  auto dma = [&](char* slot, int st, int q) __attribute__((always_inline)) {
+    // past the end: re-loads the last stage, never read
+    dma16(q < TN / 32 ? wres : xres, slot + 8 * (4 * q + w) * 128, off[q], (uint32_t)min(st, nst - 1) * 128u);
+  };
+  i32x16_t acc[FI][FJ];
+#pragma unroll
+  for (int i = 0; i < FI; ++i)
+#pragma unroll
+    for (int j = 0; j < FJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+#pragma unroll
+  for (int a = 0; a < NS; ++a)
+#pragma unroll
+    for (int q = 0; q < kDma; ++q) dma(smem + a * kSlot, a, q);
+  int o[4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) o[kk] = pos128(lr, 2 * kk + h);
+  const int am = wc * 32 * FI * 128, bm = (TN + wr * 32 * FJ) * 128;
+  bf16x8_t a[2][FI], b[2][FJ];
+  auto read = [&](const char* base, int kk, int set) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < FI; ++i) a[set][i] = rd16(base + am + i * 32 * 128 + o[kk]);
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) b[set][j] = rd16(base + bm + j * 32 * 128 + o[kk]);
+  };
+  QLORA_WAIT((NS - 1) * kDma, 0);
+  __builtin_amdgcn_s_barrier();
+  read(smem, 0, 0);
+  int slot = 0;
+  for (int st = 0; st < nst; ++st) {
+    char* cur = smem + slot * kSlot;
+    slot = slot == NS - 1 ? 0 : slot + 1;
+#pragma unroll
+    for (int kk = 0; kk < 3; ++kk) {
+      read(cur, kk + 1, (kk + 1) & 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) acc[i][j] = MmI8::mma(a[kk & 1][i], b[kk & 1][j], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    QLORA_WAIT((NS - 2) * kDma, 0);   // stage st + 1 has landed; this wave has read all of stage st
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read(smem + slot * kSlot, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int x = 0; x < FI * FJ; ++x) {
+      acc[x / FJ][x % FJ] = MmI8::mma(a[1][x / FJ], b[1][x % FJ], acc[x / FJ][x % FJ]);
+#pragma unroll
+      for (int q = 0; q < kDma; ++q)
+        if (q * FI * FJ / kDma == x) dma(cur, st + NS, q);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  QLORA_WAIT(0, 0);
+  // D[channel][token]: lane (lr, h): token lr, channels 8 q + 4 h .. of a block
+#pragma unroll
+  for (int j = 0; j < FJ; ++j) {
+    const int64_t m = m0 + 32 * (FJ * wr + j) + lr;
+    const float x = m < M ? sx[m] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < FI; ++i) {
+      const int64_t nb = n0 + 32 * (FI * wc + i);
+      f32x16_t y;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] = 0.0f;
+      for (int c = 0; c < r; c += 16) {   // 32x32x16: 8 ranks per lane half
+        const int k = c + 8 * h;
+        bf16x8_t fb{}, fu{};
+        if (k < r && nb + lr < N) fb = *reinterpret_cast<const bf16x8_t*>(B + (nb + lr) * r + k);
+        if (k < r && m < M) fu = *reinterpret_cast<const bf16x8_t*>(U + m * r + k);
+        y = mfma32x32x16(fb, fu, y);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t n = nb + 8 * q + 4 * h;
+        if (m < M && n < N) {
+          const float4 sc = *reinterpret_cast<const float4*>(sw + n);
+          const float y0 = fmaf(s, y[4 * q], (float)acc[i][j][4 * q] * (x * sc.x)),
+                      y1 = fmaf(s, y[4 * q + 1], (float)acc[i][j][4 * q + 1] * (x * sc.y)),
+                      y2 = fmaf(s, y[4 * q + 2], (float)acc[i][j][4 * q + 2] * (x * sc.z)),
+                      y3 = fmaf(s, y[4 * q + 3], (float)acc[i][j][4 * q + 3] * (x * sc.w));
+          *reinterpret_cast<uint2*>(Y + m * N + n) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
+        }
+      }
+    }
+  }
+}
+
+template <int TM, int TN, int NS>
+hipError_t launch_tile(const I8Gemm& g, int64_t n_begin, int64_t n_rows, hipStream_t st) {
+  const int tiles_n = (int)((n_rows + TN - 1) / TN), tiles_m = (int)((g.M + TM - 1) / TM);
+  auto* fn = &i8_tile_kernel<TM, TN, NS>;
+  constexpr int lds = NS * (TM + TN) * 128;
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_m), dim3(kThreads), lds, st, g.Wq, g.sw, g.N, i8_row_bytes(g.K), g.Xq,
+                     g.sx, g.M, g.U, g.B, g.r, g.s, g.Y, n_begin, tiles_n, tiles_m);
+  return hipGetLastError();
+}
+
 template <int FI>
 hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, hipStream_t st) {
   const int tiles_n = (int)((n_rows + 64 * FI - 1) / (64 * FI)), tiles_m = (int)((g.M + kTile - 1) / kTile);
@@ -172,6 +441,75 @@ hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, hipStream
 
 }  // namespace
 
-hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st) { return launch_fi<4>(g, 0, g.N, st); }
+namespace {
+
+// Tiles of TM tokens x TN channels.  What bounds every tile kernel here is
+// the compute unit's DMA: about 90 cache lines in flight, so 17-22 bytes a
+// clock at the latencies of a product whose operands come from beyond L2
+// (52 from L2 alone), whatever the depth of the LDS ring.  Its time is
+// therefore the bytes that the busiest CU brings: rounds x (TM + TN) rows.
+// Measured in us (tokens x channels x K; the tile sizes with their rounds x
+// rows):
+//   128 x 8192 x 8192    64x64 128: 24   64x128 192: 35   128x128 256: 45
+//   512 x 8192 x 22016   128x128 256: 115   192x128 320: 130
+//                        256x128 384: 177   64x64 512: 172
+//   333 x 11008 x 4096   192x128 320: 34   256x128 384: 39   256x192 448: 45
+//                        256x256 512: 50
+//   768 x 11008 x 4096   256x192 448: 50   256x256 512: 53   192x128 640: 67
+// Rings of two stages lose (151 us against 115 with four, 128 x 128 at 512 x
+// 8192 x 22016); past three or four nothing changes.
+struct Shape {
+  int tm, tn;
+};
+constexpr Shape kShapes[] = {{64, 64}, {64, 128}, {128, 128}, {192, 128}, {256, 128}, {256, 192}, {256, 256}};
+int64_t shape_tiles(Shape t, int64_t M, int64_t rows) { return (M + t.tm - 1) / t.tm * ((rows + t.tn - 1) / t.tn); }
+int64_t shape_cost(Shape t, int64_t M, int64_t rows, int cus) {
+  return (shape_tiles(t, M, rows) + cus - 1) / cus * (t.tm + t.tn);
+}
+// The cheapest shape; of equals the one with larger tiles (fewer LDS reads).
+Shape best_shape(int64_t M, int64_t rows, int cus) {
+  Shape best = kShapes[0];
+  for (const Shape& t : kShapes)
+    if (shape_cost(t, M, rows, cus) <= shape_cost(best, M, rows, cus)) best = t;
+  return best;
+}
+hipError_t launch_shape(Shape t, const I8Gemm& g, int64_t n_begin, int64_t n_rows, hipStream_t st) {
+  if (t.tm == 256)
+    return t.tn == 256   ? launch_fi<4>(g, n_begin, n_rows, st)
+           : t.tn == 192 ? launch_fi<3>(g, n_begin, n_rows, st)
+                         : launch_fi<2>(g, n_begin, n_rows, st);
+  if (t.tm == 192) return launch_tile<192, 128, 3>(g, n_begin, n_rows, st);
+  if (t.tm == 128) return launch_tile<128, 128, 4>(g, n_begin, n_rows, st);
+  return t.tn == 128 ? launch_tile<64, 128, 3>(g, n_begin, n_rows, st) : launch_tile<64, 64, 4>(g, n_begin, n_rows, st);
+}
+
+}  // namespace
+
+// Up to 16 tokens: the streaming kernel, 16 channels per workgroup, or 32
+// where that still fills the card and there are enough tokens for their
+// second reading to cost (16 x 8192 x 8192: 17.8 against 19.9 us, 16 x 22016 x
+// 8192: 41 against 47; one token at 22016 x 8192: 37 against 34).  17 to 32
+// tokens: the same with two token groups, below 16384 channels (32 x 8192 x
+// 8192: 19.8 against 21.3 us on 64 x 64 tiles, 32 x 22016 x 8192: 54 against
+// 45).  More: tiles (64 x 4096 x 4096: 10.6 against 12.1 us).
+hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st) {
+  if (g.M <= 16) return g.M > 8 && g.N >= 8192 ? launch_skinny<2, 1, 2>(g, st) : launch_skinny<1, 1, 2>(g, st);
+  if (g.M <= 32 && g.N < 16384) return g.N < 8192 ? launch_skinny<1, 2, 4>(g, st) : launch_skinny<2, 2, 2>(g, st);
+  const int cus = device_cu_count();
+  const Shape one = best_shape(g.M, g.N, cus);
+  // or: whole rounds of 256 x 256 tiles, and the rest of the channels apart
+  const int64_t tiles_m = (g.M + 255) / 256, tiles = tiles_m * ((g.N + 255) / 256);
+  if (tiles > cus && cus % tiles_m == 0) {
+    const int64_t rounds = tiles / cus, n_full = rounds * (cus / tiles_m) * 256;
+    if (n_full < g.N) {
+      const Shape rest = best_shape(g.M, g.N - n_full, cus);
+      if (rounds * 512 + shape_cost(rest, g.M, g.N - n_full, cus) < shape_cost(one, g.M, g.N, cus)) {
+        const hipError_t e = launch_fi<4>(g, 0, n_full, st);
+        return e != hipSuccess ? e : launch_shape(rest, g, n_full, g.N - n_full, st);
+      }
+    }
+  }
+  return launch_shape(one, g, 0, g.N, st);
+}
 
 }  // namespace qlora

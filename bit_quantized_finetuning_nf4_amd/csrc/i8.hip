@@ -8,7 +8,8 @@
 // scale NaN and codes 0, so that it poisons its own products and no others.
 // Rows are padded with zeros to whole 128-byte lines (i8_row_bytes), which
 // the product kernels stream.
-#include "dense_tile.h"
+#include "lds.h"
+#include "rng.h"
 
 namespace qlora {
 namespace {
@@ -67,17 +68,14 @@ __device__ __forceinline__ RowScale row_scale(uint32_t bits) {
   return r;
 }
 
-// TPR threads (a wave, or the whole workgroup) per row, 16 elements per
-// thread and chunk, NCH chunks held in registers so that the row is read
-// once; NCH = 0: longer rows, read twice (the second time mostly from cache).
+// Row m by TPR threads (a wave, or the whole workgroup), thread t of them; 16
+// elements per thread and chunk, NCH chunks held in registers so that the row
+// is read once; NCH = 0: longer rows, read twice (the second time mostly from
+// cache).  wmax: four words of LDS (TPR == 256).
 template <int TPR, int NCH>
-__global__ __launch_bounds__(256) void quant_rows_kernel(const bf16_t* __restrict__ X, int64_t M, int64_t K,
-                                                         int64_t ld, int8_t* __restrict__ Q,
-                                                         float* __restrict__ scale) {
-  __shared__ uint32_t wmax[4];
-  const int t = threadIdx.x % TPR, lane = threadIdx.x & 63;
-  const int64_t m = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
-  if (TPR == 64 && m >= M) return;   // whole waves; no barrier below for TPR == 64
+__device__ __forceinline__ void quant_row(const bf16_t* __restrict__ X, int64_t m, int t, int64_t K, int64_t ld,
+                                          int8_t* __restrict__ Q, float* __restrict__ scale, uint32_t* wmax) {
+  const int lane = threadIdx.x & 63;
   const bf16_t* x = X + m * K;
   int8_t* q = Q + m * ld;
   const int64_t groups = K >> 3;     // K % 8 == 0
@@ -120,6 +118,76 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const bf16_t* __restric
     for (int c = 0; c < NCH; ++c) store(2 * ((int64_t)c * TPR + t), v[2 * c], v[2 * c + 1]);
   } else {
     for (int64_t g = 2 * t; 8 * g < ld; g += 2 * TPR) store(g, load(g), load(g + 1));
+  }
+}
+
+template <int TPR, int NCH>
+__global__ __launch_bounds__(256) void quant_rows_kernel(const bf16_t* __restrict__ X, int64_t M, int64_t K,
+                                                         int64_t ld, int8_t* __restrict__ Q,
+                                                         float* __restrict__ scale) {
+  __shared__ uint32_t wmax[4];
+  const int64_t m = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  if (TPR == 64 && m >= M) return;   // whole waves; TPR == 64 meets no barrier
+  quant_row<TPR, NCH>(X, m, threadIdx.x % TPR, K, ld, Q, scale, wmax);
+}
+
+// What a product of few tokens needs first, in one launch: workgroups 0 ..
+// nu - 1 compute U = drop(X) A^T, one rank row and up to 16 tokens each (as
+// fp32 dot products: A is read once), the others quantize one token each.
+// With M <= 64 either part alone would leave most of the card idle.
+constexpr int kPrepTokens = 16;
+template <int NCH, bool DROP>
+__global__ __launch_bounds__(256) void i8_prep_kernel(const bf16_t* __restrict__ X, int64_t M, int64_t K, int64_t ld,
+                                                      const bf16_t* __restrict__ A, int r, int nu,
+                                                      bf16_t* __restrict__ U, int8_t* __restrict__ Q,
+                                                      float* __restrict__ scale, DropArgs drop) {
+  __shared__ uint32_t wmax[4];
+  __shared__ float part[4][kPrepTokens];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  if ((int)blockIdx.x >= nu) {
+    quant_row<256, NCH>(X, (int)blockIdx.x - nu, t, K, ld, Q, scale, wmax);
+    return;
+  }
+  const int j = blockIdx.x % r, m0 = (int)blockIdx.x / r * kPrepTokens;
+  const int mt = min(kPrepTokens, (int)M - m0);
+  const int groups = (int)(K >> 3);
+  [[maybe_unused]] DropKey key;
+  if constexpr (DROP) key = drop_key(drop);
+  float sum[kPrepTokens];
+#pragma unroll
+  for (int i = 0; i < kPrepTokens; ++i) sum[i] = 0.0f;
+  for (int g = t; g < groups; g += 256) {
+    const uint4 a = reinterpret_cast<const uint4*>(A + (int64_t)j * K)[g];
+    const float a0 = bf2f(a.x & 0xFFFFu), a1 = bf2f(a.x >> 16), a2 = bf2f(a.y & 0xFFFFu), a3 = bf2f(a.y >> 16),
+                a4 = bf2f(a.z & 0xFFFFu), a5 = bf2f(a.z >> 16), a6 = bf2f(a.w & 0xFFFFu), a7 = bf2f(a.w >> 16);
+#pragma unroll
+    for (int i = 0; i < kPrepTokens; ++i)
+      if (i < mt) {
+        u32x4_t x = *reinterpret_cast<const u32x4_t*>(X + (m0 + i) * K + 8 * g);
+        if constexpr (DROP) x = drop8(x, (uint32_t)(m0 + i) * (uint32_t)groups + (uint32_t)g, key);
+        float v = sum[i];
+        v = fmaf(a0, bf2f(x.x & 0xFFFFu), v);
+        v = fmaf(a1, bf2f(x.x >> 16), v);
+        v = fmaf(a2, bf2f(x.y & 0xFFFFu), v);
+        v = fmaf(a3, bf2f(x.y >> 16), v);
+        v = fmaf(a4, bf2f(x.z & 0xFFFFu), v);
+        v = fmaf(a5, bf2f(x.z >> 16), v);
+        v = fmaf(a6, bf2f(x.w & 0xFFFFu), v);
+        sum[i] = fmaf(a7, bf2f(x.w >> 16), v);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < kPrepTokens; ++i)
+    if (i < mt) {
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) sum[i] += __shfl_xor(sum[i], o);
+      if (lane == 0) part[w][i] = sum[i];
+    }
+  __syncthreads();
+  if (t < mt) {
+    float v = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
+    if constexpr (DROP) v *= drop.scale;
+    U[(int64_t)(m0 + t) * r + j] = (bf16_t)pack_bf16x2(v, 0.0f);
   }
 }
 
@@ -208,6 +276,27 @@ hipError_t launch_quant_rows(const bf16_t* X, int64_t M, int64_t K, int8_t* Q, f
     go(&quant_rows_kernel<256, 8>, 1);
   else
     go(&quant_rows_kernel<256, 0>, 1);
+  return hipGetLastError();
+}
+
+bool i8_prep_ok(int64_t M, int64_t K) { return M <= 64 && i8_row_bytes(K) <= 32768; }
+
+hipError_t launch_i8_prep(const bf16_t* X, int64_t M, int64_t K, const bf16_t* A, int r, const DropArgs* drop,
+                          bf16_t* U, int8_t* Q, float* scale, hipStream_t st) {
+  const int64_t ld = i8_row_bytes(K);
+  const int nu = r * (int)((M + kPrepTokens - 1) / kPrepTokens);
+  auto go = [&](auto* fn) {
+    hipLaunchKernelGGL(fn, dim3((unsigned)(nu + M)), dim3(256), 0, st, X, M, K, ld, A, r, nu, U, Q, scale,
+                       drop ? *drop : DropArgs{});
+  };
+  if (ld <= 4096)
+    drop ? go(&i8_prep_kernel<1, true>) : go(&i8_prep_kernel<1, false>);
+  else if (ld <= 8192)
+    drop ? go(&i8_prep_kernel<2, true>) : go(&i8_prep_kernel<2, false>);
+  else if (ld <= 16384)
+    drop ? go(&i8_prep_kernel<4, true>) : go(&i8_prep_kernel<4, false>);
+  else
+    drop ? go(&i8_prep_kernel<8, true>) : go(&i8_prep_kernel<8, false>);
   return hipGetLastError();
 }
 

@@ -78,6 +78,12 @@ SHAPES = [
     (32, 256, 8192, 64), (33, 136, 640, 96), (48, 1032, 1088, 16), (64, 4096, 4096, 64), (65, 320, 2056, 128),
     (100, 776, 576, 8), (128, 264, 1024, 0), (200, 4104, 1024, 16), (256, 1024, 1024, 8), (333, 1376, 4096, 16),
     (513, 264, 320, 128), (1100, 1000, 584, 24), (2048, 5120, 256, 64), (4300, 360, 136, 16),
+    # one shape at least for each kernel and launch: lines left over in the streaming kernel's batches, its two
+    # widths, two token groups in both widths, 64 x 128, 128 x 128, 192 x 128, 256 x 128 and 256 x 192 tiles, whole
+    # rounds of 256 x 256 with the rest apart
+    (1, 264, 22016, 8), (9, 8200, 1160, 16), (16, 8192, 384, 0), (4, 22016, 136, 16), (20, 8200, 264, 24),
+    (30, 4104, 2056, 8), (200, 4104, 1024, 128), (512, 8192, 256, 16), (333, 11008, 136, 40), (1000, 8192, 128, 64),
+    (768, 11008, 128, 8), (2048, 11008, 128, 16), (2000, 11000, 264, 64),
 ]
 
 
