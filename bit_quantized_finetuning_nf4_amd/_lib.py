@@ -14,7 +14,7 @@ QLORA_OK = 0
 QLORA_OP_FWD, QLORA_OP_BWD, QLORA_OP_GEMV, QLORA_OP_LORA = 0, 1, 2, 3
 QLORA_OP_FWD_FUSED, QLORA_OP_BWD_FUSED = 4, 5
 QLORA_OP_GROUP_FWD, QLORA_OP_GROUP_BWD, QLORA_OP_GROUP_LORA, QLORA_OP_BF16_DX = 6, 7, 8, 9
-QLORA_OP_BWD_DROP, QLORA_OP_I8_FWD, QLORA_OP_I8_BWD = 10, 11, 12
+QLORA_OP_BWD_DROP, QLORA_OP_I8_FWD, QLORA_OP_I8_BWD, QLORA_OP_FWD_DROP = 10, 11, 12, 13
 
 STATUS_NAMES = {
     0: "QLORA_OK", 1: "QLORA_E_NULL", 2: "QLORA_E_ALIGN", 3: "QLORA_E_SHAPE",

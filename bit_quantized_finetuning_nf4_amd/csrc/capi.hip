@@ -16,7 +16,7 @@
 // times, so it is taken from kStagedMinTokens tokens on, when the workspace
 // holds the bf16 weight.
 //   GEMV        : per job, 128 fp32 for u = A x | the device job table
-//   BWD_DROP, I8_BWD : G as two bf16 parts [M x r] each | U bf16 [M x r] |
+//   BWD_DROP, I8_BWD : G as three bf16 parts [M x r] each | U bf16 [M x r] |
 //                 split partials | deq(W)^T bf16 [K x Np] | dY bf16 [M x Np]
 //                 when N % 64 != 0 (Np = N rounded up to 64, zero columns) |
 //                 the dense product's split partials, if it splits
@@ -134,18 +134,23 @@ bool staged_bwd_ok(int64_t M, int64_t N, int64_t K) { return staged_ok(M, N, K) 
 struct FwdLayout {
   size_t u, part, wd, total;
 };
-FwdLayout fwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool staged) {
+FwdLayout fwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool staged, bool drop = false) {
   FwdLayout L{0, 0, 0, 0};
   if (r > 0) {
     L.u = 0;
     L.part = align_up((size_t)M * r * 2);
-    L.total = L.part + align_up(skinny_partial_bytes(M, r, K, kXAt));
+    L.total = L.part + align_up(drop ? u_part_bytes(M, K, r) : skinny_partial_bytes(M, r, K, kXAt));
   }
   if (staged) {
     L.wd = L.total;
     L.total += align_up((size_t)N * (size_t)K * 2);
   }
   return L;
+}
+
+// What the forward under dropout needs whether or not anything is dropped.
+size_t fwd_drop_bytes(int64_t M, int64_t N, int64_t K, int32_t r, bool staged) {
+  return std::max(fwd_layout(M, N, K, r, staged, true).total, fwd_layout(M, N, K, r, staged).total);
 }
 
 size_t lora_part_bytes(int64_t M, int64_t N, int64_t K, int32_t r);
@@ -207,17 +212,15 @@ int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 // tokens that costs what the fused kernels save, and they have no masked
 // tail).
 struct DropBwdLayout {
-  size_t hi, lo, u, part, wdt, dyp, split, split_bytes, total;
+  size_t g, u, part, wdt, dyp, split, split_bytes, total;
 };
 DropBwdLayout drop_bwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool with_dx) {
   DropBwdLayout L{};
   const int64_t np = up64(N);
   if (r > 0) {
-    const size_t mr = align_up((size_t)M * r * 2);
-    L.lo = mr;
-    L.u = 2 * mr;
-    L.part = 3 * mr;
-    L.total = L.part + lora_part_bytes(M, N, K, r);
+    L.u = align_up((size_t)M * r * 3 * 2);
+    L.part = L.u + align_up((size_t)M * r * 2);
+    L.total = L.part + align_up(adapter_part_bytes(M, N, K, r));
   }
   if (with_dx) {
     L.wdt = L.total;
@@ -245,7 +248,7 @@ I8FwdLayout i8_fwd_layout(int64_t M, int64_t K, int32_t r) {
   L.part = L.total = L.u;
   if (r > 0) {
     L.part = L.u + align_up((size_t)M * r * 2);
-    L.total = L.part + align_up(skinny_partial_bytes(M, r, K, kXAt));
+    L.total = L.part + align_up(u_part_bytes(M, K, r));
   }
   return L;
 }
@@ -388,7 +391,7 @@ qlora_status check_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, 
 qlora_status run_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, const uint16_t* A,
                      const uint16_t* B, int32_t r, float alpha, uint16_t* Y, uint16_t* U_save, void* ws,
                      bool staged, hipStream_t s, const DropArgs* drop = nullptr) {
-  const FwdLayout L = fwd_layout(M, W->rows, W->cols, r, staged);
+  const FwdLayout L = fwd_layout(M, W->rows, W->cols, r, staged, drop != nullptr);
   const Nf4View v = view(W);
   const bf16_t* U = nullptr;
   float sc = 0.0f;
@@ -507,6 +510,9 @@ size_t qlora_workspace_bytes(qlora_op op, int64_t M, int64_t N, int64_t K, int32
     case QLORA_OP_BF16_DX:
       if (!group_sizes_ok(M, N, K, r, njobs)) return 0;
       return dense_split_bytes(K, (int64_t)njobs * N, M);
+    case QLORA_OP_FWD_DROP:
+      if (M <= 0 || N <= 0 || K <= 0 || r <= 0 || r > kMaxRank) return 0;
+      return fwd_drop_bytes(M, N, K, r, staged_ok(M, N, K));
     case QLORA_OP_BWD_DROP:
     case QLORA_OP_I8_BWD:
       if (M <= 0 || N <= 0 || K <= 0 || r < 0 || r > kMaxRank || !drop_bwd_ok(M, N, K)) return 0;
@@ -714,9 +720,9 @@ qlora_status qlora_linear_fwd_drop(const qlora_nf4_weight* W, const uint16_t* X,
   DropArgs d{};
   bool active;
   if ((st = check_drop(drop, &d, &active)) != QLORA_OK) return st;
-  const bool staged = staged_ok(M, W->rows, W->cols) &&
-                      ws_bytes >= fwd_layout(M, W->rows, W->cols, r, true).total;
-  if ((st = check_ws(ws, ws_bytes, fwd_layout(M, W->rows, W->cols, r, staged).total)) != QLORA_OK) return st;
+  const int64_t N = W->rows, K = W->cols;
+  const bool staged = staged_ok(M, N, K) && ws_bytes >= fwd_drop_bytes(M, N, K, r, true);
+  if ((st = check_ws(ws, ws_bytes, fwd_drop_bytes(M, N, K, r, staged))) != QLORA_OK) return st;
   return run_fwd(W, X, M, A, B, r, alpha, Y, U_save, ws, staged, (hipStream_t)stream, active ? &d : nullptr);
 }
 
@@ -760,15 +766,14 @@ qlora_status run_bwd(const qlora_nf4_weight* W, const qlora_i8_rows* W8, int64_t
   const int64_t np = up64(N);
   qlora_status st;
   const float sc = r > 0 ? (float)((double)alpha / (double)r) : 0.0f;
-  bf16_t* hi = reinterpret_cast<bf16_t*>(ws_at(ws, L.hi));
-  bf16_t* lo = reinterpret_cast<bf16_t*>(ws_at(ws, L.lo));
+  bf16_t* G = reinterpret_cast<bf16_t*>(ws_at(ws, L.g));   // its first part is G rounded to bf16
   float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
   if (r > 0 && !U) {
     bf16_t* Ud = reinterpret_cast<bf16_t*>(ws_at(ws, L.u));
     if ((st = hip_status(launch_xat_drop(X, A, M, K, r, drop, part, Ud, s))) != QLORA_OK) return st;
     U = Ud;
   }
-  auto run_g = [&]() { return hip_status(launch_dyb_hl(dY, B, M, N, r, part, hi, lo, s)); };
+  auto run_g = [&]() { return hip_status(launch_dyb_parts(dY, B, M, N, r, part, G, s)); };
   if (dX) {
     bf16_t* WdT = reinterpret_cast<bf16_t*>(ws_at(ws, L.wdt));
     const bf16_t* g = dY;
@@ -783,15 +788,15 @@ qlora_status run_bwd(const qlora_nf4_weight* W, const qlora_i8_rows* W8, int64_t
     if (r > 0 && late && (st = run_g()) != QLORA_OK) return st;
     float* split = reinterpret_cast<float*>(ws_at(ws, L.split));
     st = hip_status(r > 0 && drop
-                        ? launch_bf16_dx_drop(WdT, K, np, g, M, hi, A, r, sc, *drop, dX, s, split, L.split_bytes)
-                        : launch_bf16_fwd(WdT, K, np, g, M, r > 0 ? hi : nullptr, r > 0 ? A : nullptr, true, r, sc, dX,
+                        ? launch_bf16_dx_drop(WdT, K, np, g, M, G, A, r, sc, *drop, dX, s, split, L.split_bytes)
+                        : launch_bf16_fwd(WdT, K, np, g, M, r > 0 ? G : nullptr, r > 0 ? A : nullptr, true, r, sc, dX,
                                           s, split, L.split_bytes));
     if (st != QLORA_OK) return st;
   } else if (r > 0 && (st = run_g()) != QLORA_OK) {
     return st;
   }
   if (r == 0) return QLORA_OK;
-  return hip_status(launch_grads_hl(hi, lo, X, dY, U, M, N, K, r, drop, part, dA, dB, sc, s));
+  return hip_status(launch_adapter_grads(G, X, dY, U, M, N, K, r, drop, part, dA, dB, sc, s));
 }
 
 }  // namespace

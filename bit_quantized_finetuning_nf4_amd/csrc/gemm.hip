@@ -19,6 +19,8 @@
 // sums and reduce_kernel adds them in a fixed order, so results do not
 // depend on timing.  The rank side is padded to RP = 64 or 128 with values
 // that only reach output columns >= r, which are never stored.
+#include <algorithm>
+
 #include "device.h"
 #include "kernels.h"
 #include "lds.h"
@@ -190,33 +192,39 @@ __global__ __launch_bounds__(kThreads, 1) void rskinny_kernel(const bf16_t* __re
 // tokens.  Both tiles are rows m, read transposed.  DB = false stores dA
 // [r x C] (A operand = Big, D[c][j]: four consecutive c per lane); DB = true
 // stores dB [C x r] (A operand = Sm, D[j][c]: four consecutive j per lane).
-// HL: the rank side is Sm + Sm2, an fp32 matrix in two bf16 parts, both
-// multiplied into the same sums (dA is fp32: one bf16 G would leave it 2^-9
-// of G's rounding).
+// PARTS = 3: the rank side is an fp32 matrix as a sum of three bf16 ones,
+// sm_part elements apart, all multiplied into the same sums (dA is fp32: one
+// bf16 G would leave it G's rounding of 2^-9, two 2^-18, above the sum's own
+// error).
 // DROP: Big is drop(Big).  A transposed fragment holds eight tokens of one
 // column, eight different Philox blocks, so the mask is applied in LDS
 // instead: each lane zeroes the dropped elements of the 16-byte pieces that
 // its own wave's DMA brought (one block each), one stage ahead of the one
 // being multiplied; the stage's barrier publishes them.
 // ---------------------------------------------------------------------------
-template <int RP, bool HL>
+template <int RP, int PARTS>
 struct ColShape {
   static constexpr int kBig = 32 * 256;                    // 8 KiB: 32 rows x 128 columns
   static constexpr int kSm = 32 * 2 * RP;                  // 32 rows x RP ranks
-  static constexpr int kStage = kBig + (HL ? 2 : 1) * kSm;
+  static constexpr int kStage = kBig + PARTS * kSm;
   static constexpr int kSmDma = kSm / 1024 / 4;
-  static constexpr int kLoads = 2 + (HL ? 2 : 1) * kSmDma;
+  static constexpr int kLoads = 2 + PARTS * kSmDma;
+  // three parts: a shorter ring, so that two workgroups of a rank up to 64
+  // share a CU (a CU keeps about 11 KiB of loads in flight whatever the ring)
+  static constexpr int kRing = PARTS == 1 ? qlora::kRing : 4;
+  static constexpr int kAhead = kRing - 1;
 };
 
-template <int RP, bool DB, bool HL, bool DROP>
+template <int RP, bool DB, int PARTS, bool DROP>
 __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __restrict__ Big, int64_t M, int64_t C,
                                                               int64_t ldb, int64_t big_gs,
                                                               const bf16_t* __restrict__ Sm, int r, int lds,
                                                               int64_t sm_gs, int stages_per_split, int tiles_c,
                                                               float* __restrict__ part,
-                                                              const bf16_t* __restrict__ Sm2, DropArgs drop) {
-  static_assert(!HL || (!DB && RP <= 128), "two-part rank side: dA of one adapter");
-  using S = ColShape<RP, HL>;
+                                                              int64_t sm_part, DropArgs drop) {
+  static_assert(PARTS == 1 || (PARTS == 3 && !DB && RP <= 128), "three-part rank side: dA of one adapter");
+  using S = ColShape<RP, PARTS>;
+  constexpr int kRing = S::kRing, kAhead = S::kAhead;
   extern __shared__ __align__(16) char smem[];
   const int tc = blockIdx.x % tiles_c, sp = blockIdx.x / tiles_c, g = blockIdx.y;
   const int t = threadIdx.x, w = t >> 6, lane = t & 63, lr = lane & 31, h = lane >> 5;
@@ -227,9 +235,9 @@ __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __re
   Sm += g * sm_gs;
   // rows past M read as zero
   const rsrc_t br = make_rsrc(Big, (uint32_t)(((M - 1) * ldb + C) * 2));
-  const rsrc_t sr = make_rsrc(Sm, (uint32_t)(((M - 1) * lds + r) * 2));
-  [[maybe_unused]] rsrc_t sr2;
-  if constexpr (HL) sr2 = make_rsrc(Sm2, (uint32_t)(((M - 1) * lds + r) * 2));
+  rsrc_t sr[PARTS];
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) sr[p] = make_rsrc(Sm + p * sm_part, (uint32_t)(((M - 1) * lds + r) * 2));
   uint32_t bo[2], so[S::kSmDma];
   int bl[2], sl[S::kSmDma];
   [[maybe_unused]] DropKey key;
@@ -256,12 +264,10 @@ __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __re
 #pragma unroll
     for (int q = 0; q < 2; ++q) dma16(br, base + bl[q], bo[q], ss * 32u * (uint32_t)ldb * 2u);
 #pragma unroll
-    for (int q = 0; q < S::kSmDma; ++q) dma16(sr, base + sl[q], so[q], ss * 32u * (uint32_t)lds * 2u);
-    if constexpr (HL) {
+    for (int p = 0; p < PARTS; ++p)
 #pragma unroll
       for (int q = 0; q < S::kSmDma; ++q)
-        dma16(sr2, base + S::kSm + sl[q], so[q], ss * 32u * (uint32_t)lds * 2u);
-    }
+        dma16(sr[p], base + p * S::kSm + sl[q], so[q], ss * 32u * (uint32_t)lds * 2u);
   };
   // zero the dropped elements of this lane's pieces of stage st, in slot
   // `slot` (columns past C: masks of values that are never stored)
@@ -320,11 +326,12 @@ __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __re
 #pragma unroll
         for (int f = 0; f < FJ; ++f)
           acc[f] = DB ? mfma32x32x16(sm[f], bg, acc[f]) : mfma32x32x16(bg, sm[f], acc[f]);
-        if constexpr (HL) {
-          const char* sb2 = sb + S::kSm;
+#pragma unroll
+        for (int p = 1; p < PARTS; ++p) {
+          const char* sp2 = sb + p * S::kSm;
 #pragma unroll
           for (int f = 0; f < FJ; f += 2)
-            tr_read2<O, O>(sb2 + tr_off<2 * RP>(f), sb2 + tr_off<2 * RP>(f + 1), sm[f], sm[f + 1]);
+            tr_read2<O, O>(sp2 + tr_off<2 * RP>(f), sp2 + tr_off<2 * RP>(f + 1), sm[f], sm[f + 1]);
 #pragma unroll
           for (int f = 0; f < FJ; ++f) acc[f] = mfma32x32x16(bg, sm[f], acc[f]);
         }
@@ -355,13 +362,12 @@ __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __re
     }
 }
 
-__global__ __launch_bounds__(kThreads) void reduce_kernel(const float* __restrict__ part, int splits, int64_t n,
-                                                          float scale, float* __restrict__ out_f32,
-                                                          bf16_t* __restrict__ out_bf16,
-                                                          bf16_t* __restrict__ out_bf16_2) {
-  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-  if (i >= n) return;
+// Elements i .. i + 3 of the splits' partials, summed in split order, times
+// scale; the loads of eight splits are issued together.
+__device__ __forceinline__ float4 sum_splits(const float* __restrict__ part, int splits, int64_t n, int64_t i,
+                                             float scale) {
   float4 acc = *reinterpret_cast<const float4*>(part + i);
+#pragma unroll 8
   for (int sp = 1; sp < splits; ++sp) {
     const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)sp * n + i);
     acc.x += v.x;
@@ -369,10 +375,16 @@ __global__ __launch_bounds__(kThreads) void reduce_kernel(const float* __restric
     acc.z += v.z;
     acc.w += v.w;
   }
-  acc.x *= scale;
-  acc.y *= scale;
-  acc.z *= scale;
-  acc.w *= scale;
+  return make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
+}
+
+__global__ __launch_bounds__(kThreads) void reduce_kernel(const float* __restrict__ part, int splits, int64_t n,
+                                                          float scale, float* __restrict__ out_f32,
+                                                          bf16_t* __restrict__ out_bf16,
+                                                          bf16_t* __restrict__ out_bf16_2) {
+  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+  if (i >= n) return;
+  const float4 acc = sum_splits(part, splits, n, i, scale);
   if (out_f32) *reinterpret_cast<float4*>(out_f32 + i) = acc;
   if (out_bf16 || out_bf16_2) {
     const uint2 p = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
@@ -381,30 +393,19 @@ __global__ __launch_bounds__(kThreads) void reduce_kernel(const float* __restric
   }
 }
 
-// hi + lo = scale * the sum of the splits: hi its bf16 rounding, lo the
-// bf16 rounding of what that left, together within 2^-18 of the sum.
-__global__ __launch_bounds__(kThreads) void reduce_hl_kernel(const float* __restrict__ part, int splits, int64_t n,
-                                                             float scale, bf16_t* __restrict__ hi,
-                                                             bf16_t* __restrict__ lo) {
+// The sum of the splits as three bf16 parts, n elements apart: each the bf16
+// rounding of what the parts before it left, together the fp32 sum.
+__global__ __launch_bounds__(kThreads) void reduce_parts_kernel(const float* __restrict__ part, int splits, int64_t n,
+                                                                bf16_t* __restrict__ out) {
   const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
   if (i >= n) return;
-  float4 acc = *reinterpret_cast<const float4*>(part + i);
-  for (int sp = 1; sp < splits; ++sp) {
-    const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)sp * n + i);
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
+  float4 v = sum_splits(part, splits, n, i, 1.0f);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const uint2 p = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    *reinterpret_cast<uint2*>(out + k * n + i) = p;
+    v = make_float4(v.x - bf2f(p.x & 0xFFFFu), v.y - bf2f(p.x >> 16), v.z - bf2f(p.y & 0xFFFFu), v.w - bf2f(p.y >> 16));
   }
-  acc.x *= scale;
-  acc.y *= scale;
-  acc.z *= scale;
-  acc.w *= scale;
-  const uint2 p = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-  *reinterpret_cast<uint2*>(hi + i) = p;
-  *reinterpret_cast<uint2*>(lo + i) =
-      make_uint2(pack_bf16x2(acc.x - bf2f(p.x & 0xFFFFu), acc.y - bf2f(p.x >> 16)),
-                 pack_bf16x2(acc.z - bf2f(p.y & 0xFFFFu), acc.w - bf2f(p.y >> 16)));
 }
 
 // The reductions of dA and dB in one launch: elements [0, n0) of the
@@ -424,18 +425,7 @@ __global__ __launch_bounds__(kThreads) void reduce2_kernel(const float* __restri
     part = part1, out = out1, splits = splits1, n = n1, scale = scale1;
   }
   if (i >= n) return;
-  float4 acc = *reinterpret_cast<const float4*>(part + i);
-  for (int sp = 1; sp < splits; ++sp) {
-    const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)sp * n + i);
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
-  }
-  acc.x *= scale;
-  acc.y *= scale;
-  acc.z *= scale;
-  acc.w *= scale;
+  const float4 acc = sum_splits(part, splits, n, i, scale);
   *reinterpret_cast<float4*>(out + i) = acc;
 }
 
@@ -487,24 +477,22 @@ struct RowArgs {
 };
 
 template <int RP, bool QT, bool DROP>
-hipError_t row_partials(const RowArgs& a, const DropArgs& drop, float* part, int* splits, hipStream_t st) {
-  const Split sp = split_for((a.M + 127) / 128, a.C, 256);
+hipError_t row_partials(const RowArgs& a, const Split& sp, const DropArgs& drop, float* part, hipStream_t st) {
   auto* fn = &rskinny_kernel<RP, QT, DROP>;
   const size_t lds = (size_t)kRing * RowShape<RP, QT>::kStage;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits, a.G), dim3(kThreads), lds, st, a.P, a.M, a.C, a.ldp, a.p_gs, a.Q,
                      a.r, a.q_gs, sp.sps, sp.tiles, a.ldo, part, drop);
-  *splits = sp.splits;
   return hipGetLastError();
 }
 
 template <int RP, bool QT>
 hipError_t run_rows(const RowArgs& a, float* part, float scale, bf16_t* out, bf16_t* out2, hipStream_t st) {
-  int splits = 0;
-  const hipError_t e = row_partials<RP, QT, false>(a, DropArgs{}, part, &splits, st);
+  const Split sp = split_for((a.M + 127) / 128, a.C, 256);
+  const hipError_t e = row_partials<RP, QT, false>(a, sp, DropArgs{}, part, st);
   if (e != hipSuccess) return e;
-  return reduce(part, splits, a.M * a.ldo, scale, nullptr, out, out2, st);
+  return reduce(part, sp.splits, a.M * a.ldo, scale, nullptr, out, out2, st);
 }
 
 // Token contraction over G groups (grid y): group g reads Big + g big_gs
@@ -521,18 +509,22 @@ struct ColArgs {
 
 // The token-contraction product's partials (no reduction); *splits gets
 // their count.
-template <int RP, bool DB, bool HL = false, bool DROP = false>
-hipError_t run_cols(const ColArgs& a, float* part, int* splits, hipStream_t st, const bf16_t* Sm2 = nullptr,
-                    const DropArgs& drop = DropArgs{}) {
-  const Split sp = split_for((a.C + 127) / 128, a.M, 256);
-  auto* fn = &cskinny_kernel<RP, DB, HL, DROP>;
-  const size_t lds = (size_t)kRing * ColShape<RP, HL>::kStage;
+template <int RP, bool DB, int PARTS = 1, bool DROP = false>
+hipError_t col_partials(const ColArgs& a, const Split& sp, float* part, hipStream_t st, int64_t sm_part = 0,
+                        const DropArgs& drop = DropArgs{}) {
+  auto* fn = &cskinny_kernel<RP, DB, PARTS, DROP>;
+  const size_t lds = (size_t)ColShape<RP, PARTS>::kRing * ColShape<RP, PARTS>::kStage;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits, a.G), dim3(kThreads), lds, st, a.Big, a.M, a.C, a.ldb,
-                     a.big_gs, a.Sm, a.r, a.lds, a.sm_gs, sp.sps, sp.tiles, part, Sm2, drop);
-  *splits = sp.splits;
+                     a.big_gs, a.Sm, a.r, a.lds, a.sm_gs, sp.sps, sp.tiles, part, sm_part, drop);
   return hipGetLastError();
+}
+template <int RP, bool DB>
+hipError_t run_cols(const ColArgs& a, float* part, int* splits, hipStream_t st) {
+  const Split sp = split_for((a.C + 127) / 128, a.M, 256);
+  *splits = sp.splits;
+  return col_partials<RP, DB>(a, sp, part, st);
 }
 
 }  // namespace
@@ -590,47 +582,85 @@ hipError_t launch_grads(const bf16_t* Gm, const bf16_t* X, const bf16_t* dY, int
   return hipGetLastError();
 }
 
-hipError_t launch_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
-                           float* part, bf16_t* out, hipStream_t st) {
-  if (!drop) return launch_xat(X, A, M, K, r, part, out, nullptr, 1.0f, st);
-  const RowArgs a{X, M, K, K, 0, A, r, 0, 1, r};
-  int splits = 0;
-  const hipError_t e = r <= 64 ? row_partials<64, false, true>(a, *drop, part, &splits, st)
-                               : row_partials<128, false, true>(a, *drop, part, &splits, st);
-  if (e != hipSuccess) return e;
-  return reduce(part, splits, M * r, drop->scale, nullptr, out, nullptr, st);
+// Splits of the products of an adapter under dropout and of the 8-bit linear.
+// The masked stages are longer (two Philox blocks per wave and stage of 32),
+// and the smaller layers have few tiles, so these products fill 512
+// workgroups (two per CU) by splits of four stages or more: the split count
+// whose rounds x (stages + 6 to fill the ring), plus a stage's time for each
+// split's partials, is least.  dA of 2048 x 4096 at rank 64: 64 workgroups
+// took 26 us, 256 take 13 us.  No device query, so that the workspace does
+// not depend on the device.
+namespace {
+
+Split fill_split(int64_t tiles, int64_t contraction) {
+  const int nst = (int)((contraction + 31) / 32);
+  Split best{(int)tiles, nst, 1};
+  int64_t best_cost = INT64_MAX;
+  for (int want = 1; want <= 32 && (want == 1 || want * 4 <= nst); ++want) {
+    const int sps = (nst + want - 1) / want, splits = (nst + sps - 1) / sps;
+    const int64_t cost = (tiles * splits + 511) / 512 * (sps + 6) + splits;
+    if (cost < best_cost) best_cost = cost, best = Split{(int)tiles, sps, splits};
+  }
+  return best;
+}
+Split rows_split(int64_t M, int64_t C) { return fill_split((M + 127) / 128, C); }
+Split cols_split(int64_t C, int64_t M) { return fill_split((C + 127) / 128, M); }
+size_t part_bytes(const Split& s, int64_t n) { return (size_t)s.splits * (size_t)n * sizeof(float); }
+
+}  // namespace
+
+size_t adapter_part_bytes(int64_t M, int64_t N, int64_t K, int r) {
+  const size_t u = part_bytes(rows_split(M, K), M * r), g = part_bytes(rows_split(M, N), M * r);
+  const size_t da = part_bytes(cols_split(K, M), (int64_t)r * K), db = part_bytes(cols_split(N, M), N * r);
+  return std::max(std::max(u, g), (da + 255) / 256 * 256 + db);
 }
 
-hipError_t launch_dyb_hl(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* hi,
-                         bf16_t* lo, hipStream_t st) {
+size_t u_part_bytes(int64_t M, int64_t K, int r) { return part_bytes(rows_split(M, K), M * r); }
+
+hipError_t launch_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
+                           float* part, bf16_t* out, hipStream_t st) {
+  const RowArgs a{X, M, K, K, 0, A, r, 0, 1, r};
+  const Split sp = rows_split(M, K);
+  const DropArgs d = drop ? *drop : DropArgs{};
+  const hipError_t e = drop ? (r <= 64 ? row_partials<64, false, true>(a, sp, d, part, st)
+                                       : row_partials<128, false, true>(a, sp, d, part, st))
+                            : (r <= 64 ? row_partials<64, false, false>(a, sp, d, part, st)
+                                       : row_partials<128, false, false>(a, sp, d, part, st));
+  if (e != hipSuccess) return e;
+  return reduce(part, sp.splits, M * r, drop ? drop->scale : 1.0f, nullptr, out, nullptr, st);
+}
+
+hipError_t launch_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* out,
+                            hipStream_t st) {
   const RowArgs a{dY, M, N, N, 0, B, r, 0, 1, r};
-  int splits = 0;
-  const hipError_t e = r <= 64 ? row_partials<64, true, false>(a, DropArgs{}, part, &splits, st)
-                               : row_partials<128, true, false>(a, DropArgs{}, part, &splits, st);
+  const Split sp = rows_split(M, N);
+  const hipError_t e = r <= 64 ? row_partials<64, true, false>(a, sp, DropArgs{}, part, st)
+                               : row_partials<128, true, false>(a, sp, DropArgs{}, part, st);
   if (e != hipSuccess) return e;
   const int64_t n = M * r;
-  hipLaunchKernelGGL(reduce_hl_kernel, dim3((unsigned)((n / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, part,
-                     splits, n, 1.0f, hi, lo);
+  hipLaunchKernelGGL(reduce_parts_kernel, dim3((unsigned)((n / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
+                     part, sp.splits, n, out);
   return hipGetLastError();
 }
 
-hipError_t launch_grads_hl(const bf16_t* hi, const bf16_t* lo, const bf16_t* X, const bf16_t* dY, const bf16_t* U,
-                           int64_t M, int64_t N, int64_t K, int r, const DropArgs* drop, float* part, float* dA,
-                           float* dB, float scale, hipStream_t st) {
-  const ColArgs a{X, M, K, K, 0, hi, r, r, 0, 1};
-  int sa = 0, sb = 0;
-  hipError_t e = drop ? (r <= 64 ? run_cols<64, false, true, true>(a, part, &sa, st, lo, *drop)
-                                 : run_cols<128, false, true, true>(a, part, &sa, st, lo, *drop))
-                      : (r <= 64 ? run_cols<64, false, true>(a, part, &sa, st, lo)
-                                 : run_cols<128, false, true>(a, part, &sa, st, lo));
-  if (e != hipSuccess) return e;
-  float* part_b = part + (skinny_partial_bytes(r, K, M, kGtX) + 255) / 256 * 256 / sizeof(float);
-  const ColArgs b{dY, M, N, N, 0, U, r, r, 0, 1};
-  e = r <= 64 ? run_cols<64, true>(b, part_b, &sb, st) : run_cols<128, true>(b, part_b, &sb, st);
+hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t* dY, const bf16_t* U, int64_t M,
+                                int64_t N, int64_t K, int r, const DropArgs* drop, float* part, float* dA, float* dB,
+                                float scale, hipStream_t st) {
+  const ColArgs a{X, M, K, K, 0, G3, r, r, 0, 1};
+  const Split sa = cols_split(K, M), sb = cols_split(N, M);
+  const DropArgs d = drop ? *drop : DropArgs{};
+  hipError_t e = drop ? (r <= 64 ? col_partials<64, false, 3, true>(a, sa, part, st, M * r, d)
+                                 : col_partials<128, false, 3, true>(a, sa, part, st, M * r, d))
+                      : (r <= 64 ? col_partials<64, false, 3>(a, sa, part, st, M * r)
+                                 : col_partials<128, false, 3>(a, sa, part, st, M * r));
   if (e != hipSuccess) return e;
   const int64_t na = (int64_t)r * K, nb = N * r;
+  float* part_b = part + (part_bytes(sa, na) + 255) / 256 * 256 / sizeof(float);
+  const ColArgs b{dY, M, N, N, 0, U, r, r, 0, 1};
+  e = r <= 64 ? col_partials<64, true>(b, sb, part_b, st) : col_partials<128, true>(b, sb, part_b, st);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(((na + nb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
-                     part, sa, na, dA, part_b, sb, nb, dB, drop ? scale * drop->scale : scale, scale);
+                     part, sa.splits, na, dA, part_b, sb.splits, nb, dB, drop ? scale * drop->scale : scale, scale);
   return hipGetLastError();
 }
 

@@ -118,18 +118,20 @@ hipError_t launch_grads(const bf16_t* Gm, const bf16_t* X, const bf16_t* dY, int
                         hipStream_t st);
 
 // The same products for an adapter under dropout and for callers that need
-// fp32-accurate gradients: drop may be null (no mask).
-// out [M x r] = drop(X) A^T; partials as launch_xat.
+// fp32-accurate gradients: drop may be null (no mask); r <= 128.  Partials:
+// u_part_bytes for the first alone, adapter_part_bytes for all of them.
+size_t u_part_bytes(int64_t M, int64_t K, int r);
+size_t adapter_part_bytes(int64_t M, int64_t N, int64_t K, int r);
+// out [M x r] = drop(X) A^T.
 hipError_t launch_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
                            float* part, bf16_t* out, hipStream_t st);
-// hi + lo [M x r each] = dY B to about 16 bits; partials as launch_dyb.
-hipError_t launch_dyb_hl(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* hi,
-                         bf16_t* lo, hipStream_t st);
-// dA [r x K] = scale (hi + lo)^T drop(X), dB [N x r] = scale dY^T U;
-// partials: grads_partial_bytes(M, N, K, r, 1).
-hipError_t launch_grads_hl(const bf16_t* hi, const bf16_t* lo, const bf16_t* X, const bf16_t* dY, const bf16_t* U,
-                           int64_t M, int64_t N, int64_t K, int r, const DropArgs* drop, float* part, float* dA,
-                           float* dB, float scale, hipStream_t st);
+// G = dY B as the sum of three bf16 matrices [M x r], one after the other.
+hipError_t launch_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* out,
+                            hipStream_t st);
+// dA [r x K] = scale G^T drop(X) with G3 as above, dB [N x r] = scale dY^T U.
+hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t* dY, const bf16_t* U, int64_t M,
+                                int64_t N, int64_t K, int r, const DropArgs* drop, float* part, float* dA, float* dB,
+                                float scale, hipStream_t st);
 
 // dX [M x K] = dY WdT^T + s drop'(G A): the dense product on WdT [K x N]
 // (K weight rows, contraction N % 64 == 0) with the adapter's product masked

@@ -315,19 +315,24 @@ def linear_fwd(q: QuantizedWeight, X: torch.Tensor, A=None, B=None, alpha: float
     U = None
     if save_u and r:
         U = u_out if u_out is not None else _empty(M, r, dtype=torch.bfloat16, device=X.device)
+    if drop is not None:
+        if path != "auto":
+            raise ValueError("the forward under dropout takes the path that the library chooses")
+        _on_current(X.device)
+        _need(X, torch.bfloat16, "X", (M, q.cols))
+        d = q.desc()
+        ws = _ws_for(ws, workspace_bytes(_lib.QLORA_OP_FWD_DROP, M, q.rows, q.cols, r), X)
+        dd = drop.desc(X.device)
+        check(lib().qlora_linear_fwd_drop(ctypes.byref(d), _ptr(X), M, _ptr(A), _ptr(B), r, float(alpha),
+                                          ctypes.byref(dd), _ptr(Y), _ptr(U), *_ws_args(ws), _stream()),
+              "qlora_linear_fwd_drop")
+        return (Y, U) if save_u else Y
     nbytes = workspace_bytes(_op(path, _lib.QLORA_OP_FWD, _lib.QLORA_OP_FWD_FUSED), M, q.rows, q.cols, r)
     if ws is None:
         ws = workspace(nbytes, X.device)
     elif ws.numel() > nbytes:
         ws = ws[:nbytes]
     d = q.desc()
-    if drop is not None:
-        _on_current(X.device)
-        dd = drop.desc(X.device)
-        check(lib().qlora_linear_fwd_drop(ctypes.byref(d), _ptr(X), M, _ptr(A), _ptr(B), r, float(alpha),
-                                          ctypes.byref(dd), _ptr(Y), _ptr(U), *_ws_args(ws), _stream()),
-              "qlora_linear_fwd_drop")
-        return (Y, U) if save_u else Y
     check(lib().qlora_linear_fwd(ctypes.byref(d), _ptr(X), M, _ptr(A), _ptr(B), r, float(alpha), _ptr(Y),
                                  _ptr(U), _ptr(ws), 0 if ws is None else ws.numel(), _stream()),
           "qlora_linear_fwd")

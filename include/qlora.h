@@ -98,7 +98,8 @@ typedef enum {
                               0 for shapes that do not split                 */
   QLORA_OP_BWD_DROP = 10,  /* qlora_linear_bwd_drop                          */
   QLORA_OP_I8_FWD = 11,    /* qlora_i8_linear_fwd                            */
-  QLORA_OP_I8_BWD = 12     /* qlora_i8_linear_bwd                            */
+  QLORA_OP_I8_BWD = 12,    /* qlora_i8_linear_bwd                            */
+  QLORA_OP_FWD_DROP = 13   /* qlora_linear_fwd_drop (room for the staged path) */
 } qlora_op;
 
 /* A quantized weight: host struct holding device pointers.
@@ -558,9 +559,10 @@ qlora_status qlora_dropout(const uint16_t* x, int64_t n, const qlora_drop* drop,
 
 /* qlora_linear_fwd with the adapter under dropout:
  *   Y = X deq(W)^T + s U B^T,  U = drop(X) A^T,  drop over X [M x K].
- * Arguments, paths, workspace (QLORA_OP_FWD / _FWD_FUSED) and errors as
- * qlora_linear_fwd; r > 0 and drop not NULL.  At p = 0 the result is
- * qlora_linear_fwd's. */
+ * Arguments, paths and errors as qlora_linear_fwd; r > 0 and drop not NULL.
+ * Workspace: qlora_workspace_bytes(QLORA_OP_FWD_DROP, M, N, K, r, 0); the
+ * staged path, where it applies, is taken if the workspace holds it.  At
+ * p = 0 the result is qlora_linear_fwd's. */
 qlora_status qlora_linear_fwd_drop(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, const uint16_t* A,
                                    const uint16_t* B, int32_t r, float alpha, const qlora_drop* drop, uint16_t* Y,
                                    uint16_t* U_save, void* ws, size_t ws_bytes, void* stream);
@@ -569,8 +571,8 @@ qlora_status qlora_linear_fwd_drop(const qlora_nf4_weight* W, const uint16_t* X,
  *   dX = dY deq(W) + s drop'(G A),  G = dY B,  drop'(Z) masked and scaled as
  *                                   X was (NULL dX skips it);
  *   dA = s G^T drop(X),  dB = s dY^T U.
- * U_saved is the forward's U; NULL computes it again.  G is kept to 16 bits
- * of mantissa for dA (two bf16 parts), to bf16 for dX.  Always staged, for
+ * U_saved is the forward's U; NULL computes it again.  G is kept in fp32 for
+ * dA (as three bf16 parts), in bf16 for dX.  Always staged, for
  * any M: workspace qlora_workspace_bytes(QLORA_OP_BWD_DROP, M, N, K, r, 0),
  * which holds deq(W)^T.  K % 64 == 0, N % 8 == 0; with Np = N rounded up to
  * 64, Np K and M Np below 2^31 (QLORA_E_UNSUPPORTED otherwise). */

@@ -37,7 +37,7 @@ def within(got, ref, tol, name):
 def adapter_bounds(X, dY, A, B, Wd, s, D, U):
     """(dX, dA, dB) and their bounds; D: the kept scale of every element of X
     (0 where dropped), U: the bf16 values handed to the backward.  G is bf16
-    in dX, two bf16 parts (E^2) in dA, plus its own sum's error."""
+    in dX, fp32 (three bf16 parts, 2^-24) in dA, plus its own sum's error."""
     M, N, K, r = X.shape[0], dY.shape[1], X.shape[1], A.shape[0]
     G = dY @ B
     Gm = np.abs(dY) @ np.abs(B)
@@ -48,7 +48,7 @@ def adapter_bounds(X, dY, A, B, Wd, s, D, U):
     dX_tol = 1.01 * (E * np.abs(dX) + N * F * (np.abs(dY) @ np.abs(Wd)) + tail)
     XD = D * X
     dA = s * (G.T @ XD)
-    dA_tol = 1.01 * s * ((E * E * np.abs(G) + g_err).T @ np.abs(XD) + 2 * M * F * (np.abs(G).T @ np.abs(XD)))
+    dA_tol = 1.01 * s * ((2.0**-24 * np.abs(G) + g_err).T @ np.abs(XD) + 3 * M * F * (np.abs(G).T @ np.abs(XD)))
     dB = s * (dY.T @ U)
     dB_tol = 1.01 * s * M * F * (np.abs(dY).T @ np.abs(U))
     return (dX, dX_tol), (dA, dA_tol), (dB, dB_tol)
@@ -257,6 +257,8 @@ def test_refusals():
         ops.linear_bwd(q, X, d["dY"], drop=ops.Dropout(0.1, 1))
     with pytest.raises(ValueError):
         ops.linear_bwd(q, X, d["dY"], A, B, 16.0, drop=ops.Dropout(0.1, 1), path="fused")
+    with pytest.raises(ValueError):
+        ops.linear_fwd(q, X, A, B, 16.0, drop=ops.Dropout(0.1, 1), path="fused")
     with pytest.raises(ValueError):
         ops.dropout(X.t(), ops.Dropout(0.1, 1))                              # strided
     with pytest.raises(ValueError):
