@@ -21,7 +21,8 @@
 //                 when N % 64 != 0 (Np = N rounded up to 64, zero columns) |
 //                 the dense product's split partials, if it splits
 //   I8_FWD      : X as 8-bit rows [M x i8_row_bytes(K)] | their scales fp32
-//                 [M] | U bf16 [M x r] | split partials of X A^T
+//                 [M] | U bf16 [M x r] | split partials of X A^T, then of
+//                 the product
 // qlora_linear_fwd_noalloc carves the FWD layout out of `scratch` below
 // instead of a caller workspace.
 #include <hip/hip_runtime.h>
@@ -134,12 +135,12 @@ bool staged_bwd_ok(int64_t M, int64_t N, int64_t K) { return staged_ok(M, N, K) 
 struct FwdLayout {
   size_t u, part, wd, total;
 };
-FwdLayout fwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool staged, bool drop = false) {
+FwdLayout fwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool staged) {
   FwdLayout L{0, 0, 0, 0};
   if (r > 0) {
     L.u = 0;
     L.part = align_up((size_t)M * r * 2);
-    L.total = L.part + align_up(drop ? u_part_bytes(M, K, r) : skinny_partial_bytes(M, r, K, kXAt));
+    L.total = L.part + align_up(skinny_partial_bytes(M, r, K, kXAt));
   }
   if (staged) {
     L.wd = L.total;
@@ -148,9 +149,30 @@ FwdLayout fwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool staged, bo
   return L;
 }
 
-// What the forward under dropout needs whether or not anything is dropped.
-size_t fwd_drop_bytes(int64_t M, int64_t N, int64_t K, int32_t r, bool staged) {
-  return std::max(fwd_layout(M, N, K, r, staged, true).total, fwd_layout(M, N, K, r, staged).total);
+// The forward under dropout: U | split partials of U, then of the staged
+// product | deq(W), if staged.  It is staged from kStagedMinTokens tokens on,
+// and below where the estimate says so: the fused kernel takes about 26 ns a
+// column of K and round of 256 x 256 tiles (256 x 1024 x 1024: 31 us on four
+// workgroups, against 3 us to dequantize and 12 for 64 x 64 tiles; 263 x 16576
+// x 3968: about 100 us, against 35 and 80), the dequantization 2.5 bytes a
+// weight at 4.4 TB/s.  (Fixed rates, so that the workspace does not depend on
+// the device.)
+bool drop_fwd_staged(int64_t M, int64_t N, int64_t K) {
+  if (N > (int64_t)0x7FFFFFFF / K) return false;
+  if (staged_ok(M, N, K)) return true;
+  const double rounds = (double)(((M + 255) / 256 * ((N + 255) / 256) + 255) / 256);
+  return 4.0 + (double)N * (double)K * 2.5 / 4.4e6 + staged_cost(N, K, M) < 5.0 + rounds * 0.026 * (double)K;
+}
+struct DropFwdLayout {
+  size_t u, part, part_bytes, wd, total;
+};
+DropFwdLayout drop_fwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool staged) {
+  DropFwdLayout L{};
+  L.part = align_up((size_t)M * r * 2);
+  L.part_bytes = std::max(u_part_bytes(M, K, r), staged ? staged_part_bytes(N, K, M) : 0);
+  L.wd = L.part + align_up(L.part_bytes);
+  L.total = L.wd + (staged ? align_up((size_t)N * (size_t)K * 2) : 0);
+  return L;
 }
 
 size_t lora_part_bytes(int64_t M, int64_t N, int64_t K, int32_t r);
@@ -226,7 +248,7 @@ DropBwdLayout drop_bwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool w
     L.wdt = L.total;
     L.dyp = L.wdt + align_up((size_t)np * (size_t)K * 2);
     L.split = L.dyp + (np != N ? align_up((size_t)M * (size_t)np * 2) : 0);
-    L.split_bytes = dense_split_bytes(K, np, M);
+    L.split_bytes = staged_part_bytes(K, np, M);
     L.total = L.split + align_up(L.split_bytes);
   }
   return L;
@@ -239,17 +261,16 @@ bool drop_bwd_ok(int64_t M, int64_t N, int64_t K) {
 }
 
 struct I8FwdLayout {
-  size_t xq, sx, u, part, total;
+  size_t xq, sx, u, part, part_bytes, total;
 };
-I8FwdLayout i8_fwd_layout(int64_t M, int64_t K, int32_t r) {
+I8FwdLayout i8_fwd_layout(int64_t M, int64_t N, int64_t K, int32_t r) {
   I8FwdLayout L{};
   L.sx = align_up((size_t)M * (size_t)i8_row_bytes(K));
   L.u = L.sx + align_up((size_t)M * sizeof(float));
-  L.part = L.total = L.u;
-  if (r > 0) {
-    L.part = L.u + align_up((size_t)M * r * 2);
-    L.total = L.part + align_up(u_part_bytes(M, K, r));
-  }
+  L.part = L.u + align_up((size_t)M * r * 2);
+  // the partials of U, then those of the product
+  L.part_bytes = std::max(r > 0 ? u_part_bytes(M, K, r) : 0, i8_gemm_part_bytes(M, N, K));
+  L.total = L.part + align_up(L.part_bytes);
   return L;
 }
 
@@ -390,8 +411,8 @@ qlora_status check_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, 
 // The forward's launches, on a workspace of the FWD layout.
 qlora_status run_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, const uint16_t* A,
                      const uint16_t* B, int32_t r, float alpha, uint16_t* Y, uint16_t* U_save, void* ws,
-                     bool staged, hipStream_t s, const DropArgs* drop = nullptr) {
-  const FwdLayout L = fwd_layout(M, W->rows, W->cols, r, staged, drop != nullptr);
+                     bool staged, hipStream_t s) {
+  const FwdLayout L = fwd_layout(M, W->rows, W->cols, r, staged);
   const Nf4View v = view(W);
   const bf16_t* U = nullptr;
   float sc = 0.0f;
@@ -399,8 +420,7 @@ qlora_status run_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, co
     sc = (float)((double)alpha / (double)r);  // s = RN32(alpha / r)
     bf16_t* Ud = U_save ? U_save : reinterpret_cast<bf16_t*>(ws_at(ws, L.u));
     float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
-    qlora_status st = hip_status(drop ? launch_xat_drop(X, A, M, W->cols, r, drop, part, Ud, s)
-                                      : launch_xat(X, A, M, W->cols, r, part, Ud, nullptr, 1.0f, s));
+    qlora_status st = hip_status(launch_xat(X, A, M, W->cols, r, part, Ud, nullptr, 1.0f, s));
     if (st != QLORA_OK) return st;
     U = Ud;
   }
@@ -512,14 +532,18 @@ size_t qlora_workspace_bytes(qlora_op op, int64_t M, int64_t N, int64_t K, int32
       return dense_split_bytes(K, (int64_t)njobs * N, M);
     case QLORA_OP_FWD_DROP:
       if (M <= 0 || N <= 0 || K <= 0 || r <= 0 || r > kMaxRank) return 0;
-      return fwd_drop_bytes(M, N, K, r, staged_ok(M, N, K));
+      if (M > 0x7FFFFFFF / K || M > 0x7FFFFFFF / N) return 0;
+      return std::max(drop_fwd_layout(M, N, K, r, drop_fwd_staged(M, N, K)).total,
+                      fwd_layout(M, N, K, r, staged_ok(M, N, K)).total);
     case QLORA_OP_BWD_DROP:
     case QLORA_OP_I8_BWD:
       if (M <= 0 || N <= 0 || K <= 0 || r < 0 || r > kMaxRank || !drop_bwd_ok(M, N, K)) return 0;
       return drop_bwd_layout(M, N, K, r, true).total;
     case QLORA_OP_I8_FWD:
-      if (M <= 0 || K <= 0 || K > kI8MaxCols || M > 0x7FFFFFFF / K || r < 0 || r > kMaxRank) return 0;
-      return i8_fwd_layout(M, K, r).total;
+      if (M <= 0 || N <= 0 || K <= 0 || K > kI8MaxCols || M > 0x7FFFFFFF / K || N > 0x7FFFFFFF / M || r < 0 ||
+          r > kMaxRank)
+        return 0;
+      return i8_fwd_layout(M, N, K, r).total;
   }
   return 0;
 }
@@ -720,10 +744,22 @@ qlora_status qlora_linear_fwd_drop(const qlora_nf4_weight* W, const uint16_t* X,
   DropArgs d{};
   bool active;
   if ((st = check_drop(drop, &d, &active)) != QLORA_OK) return st;
+  if (!active)   // the plain forward, bit for bit
+    return qlora_linear_fwd(W, X, M, A, B, r, alpha, Y, U_save, ws, ws_bytes, stream);
   const int64_t N = W->rows, K = W->cols;
-  const bool staged = staged_ok(M, N, K) && ws_bytes >= fwd_drop_bytes(M, N, K, r, true);
-  if ((st = check_ws(ws, ws_bytes, fwd_drop_bytes(M, N, K, r, staged))) != QLORA_OK) return st;
-  return run_fwd(W, X, M, A, B, r, alpha, Y, U_save, ws, staged, (hipStream_t)stream, active ? &d : nullptr);
+  const bool staged = drop_fwd_staged(M, N, K) && ws_bytes >= drop_fwd_layout(M, N, K, r, true).total;
+  const DropFwdLayout L = drop_fwd_layout(M, N, K, r, staged);
+  if ((st = check_ws(ws, ws_bytes, L.total)) != QLORA_OK) return st;
+  hipStream_t s = (hipStream_t)stream;
+  const float sc = (float)((double)alpha / (double)r);
+  bf16_t* U = U_save ? U_save : reinterpret_cast<bf16_t*>(ws_at(ws, L.u));
+  float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
+  if ((st = hip_status(launch_xat_drop(X, A, M, K, r, &d, part, U, s))) != QLORA_OK) return st;
+  if (!staged) return hip_status(launch_fwd(view(W), X, M, U, B, r, sc, Y, s));
+  bf16_t* Wd = reinterpret_cast<bf16_t*>(ws_at(ws, L.wd));
+  st = hip_status(launch_dequant(W->codes, W->absmax_q, W->group_scale, N * K, W->codebook, W->absmax_format, Wd, s));
+  if (st != QLORA_OK) return st;
+  return hip_status(launch_staged(Wd, N, K, X, M, U, B, false, r, sc, nullptr, Y, s, part, L.part_bytes));
 }
 
 namespace {
@@ -787,10 +823,8 @@ qlora_status run_bwd(const qlora_nf4_weight* W, const qlora_i8_rows* W8, int64_t
     }
     if (r > 0 && late && (st = run_g()) != QLORA_OK) return st;
     float* split = reinterpret_cast<float*>(ws_at(ws, L.split));
-    st = hip_status(r > 0 && drop
-                        ? launch_bf16_dx_drop(WdT, K, np, g, M, G, A, r, sc, *drop, dX, s, split, L.split_bytes)
-                        : launch_bf16_fwd(WdT, K, np, g, M, r > 0 ? G : nullptr, r > 0 ? A : nullptr, true, r, sc, dX,
-                                          s, split, L.split_bytes));
+    st = hip_status(launch_staged(WdT, K, np, g, M, r > 0 ? G : nullptr, r > 0 ? A : nullptr, true, r, sc,
+                                  r > 0 ? drop : nullptr, dX, s, split, L.split_bytes));
     if (st != QLORA_OK) return st;
   } else if (r > 0 && (st = run_g()) != QLORA_OK) {
     return st;
@@ -846,7 +880,7 @@ qlora_status qlora_i8_matmul(const qlora_i8_rows* X, const qlora_i8_rows* W, uin
   if (!Y) return QLORA_E_NULL;
   if (!aligned16(Y)) return QLORA_E_ALIGN;
   const I8Gemm g{W->codes, W->scale, W->rows, W->cols, X->codes, X->scale, X->rows, nullptr, nullptr, 0, 0.0f, Y};
-  return hip_status(launch_i8_gemm(g, (hipStream_t)stream));
+  return hip_status(launch_i8_gemm(g, (hipStream_t)stream, nullptr, 0));
 }
 
 qlora_status qlora_i8_linear_fwd(const qlora_i8_rows* W, const uint16_t* X, int64_t M, const uint16_t* A,
@@ -862,24 +896,24 @@ qlora_status qlora_i8_linear_fwd(const qlora_i8_rows* W, const uint16_t* X, int6
   if ((st = check_drop(drop, &d, &active)) != QLORA_OK) return st;
   if (r == 0 && drop) return QLORA_E_UNSUPPORTED;   // no adapter, nothing to drop
   const int64_t N = W->rows, K = W->cols;
-  const I8FwdLayout L = i8_fwd_layout(M, K, r);
+  const I8FwdLayout L = i8_fwd_layout(M, N, K, r);
   if ((st = check_ws(ws, ws_bytes, L.total)) != QLORA_OK) return st;
   hipStream_t s = (hipStream_t)stream;
   int8_t* xq = reinterpret_cast<int8_t*>(ws_at(ws, L.xq));
   float* sx = reinterpret_cast<float*>(ws_at(ws, L.sx));
   bf16_t* U = r > 0 ? (U_save ? U_save : reinterpret_cast<bf16_t*>(ws_at(ws, L.u))) : nullptr;
   const DropArgs* dp = active ? &d : nullptr;
+  float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
   if (i8_prep_ok(M, K)) {
     st = hip_status(launch_i8_prep(X, M, K, A, r, dp, U, xq, sx, s));
   } else {
-    float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
     if (r > 0 && (st = hip_status(launch_xat_drop(X, A, M, K, r, dp, part, U, s))) != QLORA_OK) return st;
     st = hip_status(launch_quant_rows(X, M, K, xq, sx, s));
   }
   if (st != QLORA_OK) return st;
   const float sc = r > 0 ? (float)((double)alpha / (double)r) : 0.0f;
   const I8Gemm g{W->codes, W->scale, N, K, xq, sx, M, U, B, r, sc, Y};
-  return hip_status(launch_i8_gemm(g, s));
+  return hip_status(launch_i8_gemm(g, s, part, L.part_bytes));
 }
 
 qlora_status qlora_i8_linear_bwd(const qlora_i8_rows* W, const uint16_t* X, const uint16_t* dY, int64_t M,

@@ -33,15 +33,10 @@ namespace {
 // chunks of the rank are in LDS (chunk c at 2 kOp c), so a 32 x 32 block's
 // product is summed in 16 registers of its own, masked, and added: the tile
 // keeps one set of accumulators.
-//
-// A lane holds four consecutive columns of a token, half of a Philox block's
-// eight; its two lane halves hold the block's two halves.  So the lower half
-// computes the block of column group 2 p, the upper half that of 2 p + 1, and
-// v_permlane32_swap hands each half its four columns of both.
 template <int FI, int NT>
 __device__ __forceinline__ void masked_tail(f32x16_t (&acc)[FI][4], const char* smem, float s,
                                             const DropKey& key, int64_t cols, int64_t row0, int64_t col0) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1, lr = lane & 31, h = lane >> 5;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1, lr = lane & 31;
   const FragOffs fo = frag_offs(lane);
   const int bm64 = wr * 128 * 64;
 #pragma unroll
@@ -69,23 +64,9 @@ __device__ __forceinline__ void masked_tail(f32x16_t (&acc)[FI][4], const char* 
         t = mfma32x32x16(f0, b[2 * c], t);
         t = mfma32x32x16(f1, b[2 * c + 1], t);
       }
+      mask_block(t, row_block + 4u * i, key);
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const u32x4_t x = philox(row_block + (uint32_t)(4 * i + 2 * p + h), key);
-        const auto x0 = __builtin_amdgcn_permlane32_swap(x.x, x.z, false, false);
-        const auto x1 = __builtin_amdgcn_permlane32_swap(x.y, x.w, false, false);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {   // column group 2 p + g: elements 8 p + 4 g ..
-          const int wd[2] = {(int)x0[g], (int)x1[g]};
-          const int thr = key.thr << 16;   // a half, as a signed number in the high bits
-#pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            const int e = 8 * p + 4 * g + 2 * d;
-            acc[i][j][e] += (wd[d] << 16) >= thr ? s * t[e] : 0.0f;
-            acc[i][j][e + 1] += wd[d] >= thr ? s * t[e + 1] : 0.0f;
-          }
-        }
-      }
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(s, t[e], acc[i][j][e]);
       __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
     }
   }
@@ -463,16 +444,38 @@ hipError_t launch_bf16_group(const bf16_t* Wd, int64_t N, int64_t K, const bf16_
   return launch_dense(Wd, N, K, X, M, U, ldu, B, b_trans, r, gn, s, Y, st, part, part_bytes, nullptr);
 }
 
-hipError_t launch_bf16_dx_drop(const bf16_t* WdT, int64_t K, int64_t N, const bf16_t* dY, int64_t M, const bf16_t* G,
-                               const bf16_t* A, int r, float s, const DropArgs& drop, bf16_t* dX, hipStream_t st,
-                               float* part, size_t part_bytes) {
-  return launch_dense(WdT, K, N, dY, M, G, r, A, true, r, K, s * drop.scale, dX, st, part, part_bytes, &drop);
-}
-
 hipError_t launch_bf16_fwd(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* U,
                            const bf16_t* B, bool b_trans, int r, float s, bf16_t* Y, hipStream_t st, float* part,
                            size_t part_bytes) {
   return launch_bf16_group(Wd, N, K, X, M, U, r, B, b_trans, r, N, s, Y, st, part, part_bytes);
+}
+
+hipError_t launch_split_sum(const float* part, int splits, int64_t n, bf16_t* Y, hipStream_t st) {
+  hipLaunchKernelGGL(split_sum_kernel, dim3((unsigned)((n / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, part,
+                     splits, n, Y);
+  return hipGetLastError();
+}
+
+size_t staged_part_bytes(int64_t N, int64_t K, int64_t M) {
+  return std::max(tile_part_bytes(M, N, K / 64), dense_split_bytes(N, K, M));
+}
+
+double staged_cost(int64_t N, int64_t K, int64_t M) { return choose_tile(M, N, K / 64, kSplitCus, (size_t)1 << 62).cost; }
+
+hipError_t launch_staged(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* T,
+                         const bf16_t* B, bool b_trans, int r, float s, const DropArgs* drop, bf16_t* Y, hipStream_t st,
+                         float* part, size_t part_bytes) {
+  const float sc = drop ? s * drop->scale : s;
+  const TileChoice c = choose_tile(M, N, K / 64, device_cu_count(), part ? part_bytes : 0);
+  if (c.tm < 256) {
+    TileGemm t{};
+    t.W = Wd, t.X = X, t.N = N, t.row_bytes = 2 * K, t.M = M, t.T = T, t.B = B, t.r = r, t.s = sc, t.b_trans = b_trans;
+    t.dropped = drop != nullptr;
+    if (drop) t.drop = *drop;
+    t.Y = Y, t.part = part;
+    return launch_tile(t, c, 0, N, st);
+  }
+  return launch_dense(Wd, N, K, X, M, T, r, B, b_trans, r, N, sc, Y, st, part, part_bytes, drop);
 }
 
 }  // namespace qlora

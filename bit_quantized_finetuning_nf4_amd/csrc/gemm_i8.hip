@@ -285,149 +285,6 @@ hipError_t launch_skinny(const I8Gemm& g, hipStream_t st) {
   return hipGetLastError();
 }
 
-// ---------------------------------------------------------------------------
-// A middling number of tokens: TM tokens x TN channels per workgroup, waves
-// 2 x 2 over the tile, a ring of NS stages of 128 bytes of all its rows.
-// Smaller tiles than the 256 x 256 kernel's read LDS more per product, but
-// there are enough of them for the whole card.
-//
-// The fragments of a 32-byte step are read one step ahead of their MFMAs.
-// The stage's barrier stands before its last step's MFMAs, which hide the
-// first reads of the next stage: there every wave has read all of the stage,
-// so the DMA of stage st + NS goes into its slot at once.
-// ---------------------------------------------------------------------------
-template <int TM, int TN, int NS>
-__global__ __launch_bounds__(kThreads, 1) void i8_tile_kernel(const int8_t* __restrict__ Wq,
-                                                              const float* __restrict__ sw, int64_t N, int64_t ld,
-                                                              const int8_t* __restrict__ Xq,
-                                                              const float* __restrict__ sx, int64_t M,
-                                                              const bf16_t* __restrict__ U,
-                                                              const bf16_t* __restrict__ B, int r, float s,
-                                                              bf16_t* __restrict__ Y, int64_t n_begin, int tiles_n,
-                                                              int tiles_m) {
-  constexpr int FI = TN / 64, FJ = TM / 64;         // 32-row fragments per wave
-  constexpr int kRows = TM + TN, kSlot = kRows * 128, kDma = kRows / 32;   // DMA instructions per wave and stage
-  extern __shared__ __align__(16) char smem[];
-  int tn, tm;
-  map_tile_grouped(xcd_tile_id(), tiles_n, tiles_m, tn, tm);
-  const int64_t n0 = n_begin + (int64_t)tn * TN, m0 = (int64_t)tm * TM;
-  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), wr = w >> 1, wc = w & 1;
-  const int lr = lane & 31, h = lane >> 5;
-  const int nst = (int)(ld >> 7);
-  // weight rows 0 .. TN - 1, then token rows; instruction q of wave w brings
-  // rows 8 (4 q + w) .. + 7
-  const rsrc_t wres = make_rsrc(Wq, (uint32_t)(N * ld)), xres = make_rsrc(Xq, (uint32_t)(M * ld));
-  uint32_t off[kDma];
-#pragma unroll
-  for (int q = 0; q < kDma; ++q) {
-    const int row = 8 * (4 * q + w) + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
-    const int64_t src = q < TN / 32 ? min(n0 + row, N - 1) : min(m0 + row - TN, M - 1);
-    off[q] = (uint32_t)(src * ld + 16 * c);
-  }
-  auto dma = [&](char* slot, int st, int q) __attribute__((always_inline)) {
-    // past the end: re-loads the last stage, never read
-    dma16(q < TN / 32 ? wres : xres, slot + 8 * (4 * q + w) * 128, off[q], (uint32_t)min(st, nst - 1) * 128u);
-  };
-  i32x16_t acc[FI][FJ];
-#pragma unroll
-  for (int i = 0; i < FI; ++i)
-#pragma unroll
-    for (int j = 0; j < FJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
-#pragma unroll
-  for (int a = 0; a < NS; ++a)
-#pragma unroll
-    for (int q = 0; q < kDma; ++q) dma(smem + a * kSlot, a, q);
-  int o[4];
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) o[kk] = pos128(lr, 2 * kk + h);
-  const int am = wc * 32 * FI * 128, bm = (TN + wr * 32 * FJ) * 128;
-  bf16x8_t a[2][FI], b[2][FJ];
-  auto read = [&](const char* base, int kk, int set) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < FI; ++i) a[set][i] = rd16(base + am + i * 32 * 128 + o[kk]);
-#pragma unroll
-    for (int j = 0; j < FJ; ++j) b[set][j] = rd16(base + bm + j * 32 * 128 + o[kk]);
-  };
-  QLORA_WAIT((NS - 1) * kDma, 0);
-  __builtin_amdgcn_s_barrier();
-  read(smem, 0, 0);
-  int slot = 0;
-  for (int st = 0; st < nst; ++st) {
-    char* cur = smem + slot * kSlot;
-    slot = slot == NS - 1 ? 0 : slot + 1;
-#pragma unroll
-    for (int kk = 0; kk < 3; ++kk) {
-      read(cur, kk + 1, (kk + 1) & 1);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < FI; ++i)
-#pragma unroll
-        for (int j = 0; j < FJ; ++j) acc[i][j] = MmI8::mma(a[kk & 1][i], b[kk & 1][j], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    QLORA_WAIT((NS - 2) * kDma, 0);   // stage st + 1 has landed; this wave has read all of stage st
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    read(smem + slot * kSlot, 0, 0);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int x = 0; x < FI * FJ; ++x) {
-      acc[x / FJ][x % FJ] = MmI8::mma(a[1][x / FJ], b[1][x % FJ], acc[x / FJ][x % FJ]);
-#pragma unroll
-      for (int q = 0; q < kDma; ++q)
-        if (q * FI * FJ / kDma == x) dma(cur, st + NS, q);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-  QLORA_WAIT(0, 0);
-  // D[channel][token]: lane (lr, h): token lr, channels 8 q + 4 h .. of a block
-#pragma unroll
-  for (int j = 0; j < FJ; ++j) {
-    const int64_t m = m0 + 32 * (FJ * wr + j) + lr;
-    const float x = m < M ? sx[m] : 0.0f;
-#pragma unroll
-    for (int i = 0; i < FI; ++i) {
-      const int64_t nb = n0 + 32 * (FI * wc + i);
-      f32x16_t y;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = 0.0f;
-      for (int c = 0; c < r; c += 16) {   // 32x32x16: 8 ranks per lane half
-        const int k = c + 8 * h;
-        bf16x8_t fb{}, fu{};
-        if (k < r && nb + lr < N) fb = *reinterpret_cast<const bf16x8_t*>(B + (nb + lr) * r + k);
-        if (k < r && m < M) fu = *reinterpret_cast<const bf16x8_t*>(U + m * r + k);
-        y = mfma32x32x16(fb, fu, y);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t n = nb + 8 * q + 4 * h;
-        if (m < M && n < N) {
-          const float4 sc = *reinterpret_cast<const float4*>(sw + n);
-          const float y0 = fmaf(s, y[4 * q], (float)acc[i][j][4 * q] * (x * sc.x)),
-                      y1 = fmaf(s, y[4 * q + 1], (float)acc[i][j][4 * q + 1] * (x * sc.y)),
-                      y2 = fmaf(s, y[4 * q + 2], (float)acc[i][j][4 * q + 2] * (x * sc.z)),
-                      y3 = fmaf(s, y[4 * q + 3], (float)acc[i][j][4 * q + 3] * (x * sc.w));
-          *reinterpret_cast<uint2*>(Y + m * N + n) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
-        }
-      }
-    }
-  }
-}
-
-template <int TM, int TN, int NS>
-hipError_t launch_tile(const I8Gemm& g, int64_t n_begin, int64_t n_rows, hipStream_t st) {
-  const int tiles_n = (int)((n_rows + TN - 1) / TN), tiles_m = (int)((g.M + TM - 1) / TM);
-  auto* fn = &i8_tile_kernel<TM, TN, NS>;
-  constexpr int lds = NS * (TM + TN) * 128;
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_m), dim3(kThreads), lds, st, g.Wq, g.sw, g.N, i8_row_bytes(g.K), g.Xq,
-                     g.sx, g.M, g.U, g.B, g.r, g.s, g.Y, n_begin, tiles_n, tiles_m);
-  return hipGetLastError();
-}
-
 template <int FI>
 hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, hipStream_t st) {
   const int tiles_n = (int)((n_rows + 64 * FI - 1) / (64 * FI)), tiles_m = (int)((g.M + kTile - 1) / kTile);
@@ -441,75 +298,47 @@ hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, hipStream
 
 }  // namespace
 
-namespace {
-
-// Tiles of TM tokens x TN channels.  What bounds every tile kernel here is
-// the compute unit's DMA: about 90 cache lines in flight, so 17-22 bytes a
-// clock at the latencies of a product whose operands come from beyond L2
-// (52 from L2 alone), whatever the depth of the LDS ring.  Its time is
-// therefore the bytes that the busiest CU brings: rounds x (TM + TN) rows.
-// Measured in us (tokens x channels x K; the tile sizes with their rounds x
-// rows):
-//   128 x 8192 x 8192    64x64 128: 24   64x128 192: 35   128x128 256: 45
-//   512 x 8192 x 22016   128x128 256: 115   192x128 320: 130
-//                        256x128 384: 177   64x64 512: 172
-//   333 x 11008 x 4096   192x128 320: 34   256x128 384: 39   256x192 448: 45
-//                        256x256 512: 50
-//   768 x 11008 x 4096   256x192 448: 50   256x256 512: 53   192x128 640: 67
-// Rings of two stages lose (151 us against 115 with four, 128 x 128 at 512 x
-// 8192 x 22016); past three or four nothing changes.
-struct Shape {
-  int tm, tn;
-};
-constexpr Shape kShapes[] = {{64, 64}, {64, 128}, {128, 128}, {192, 128}, {256, 128}, {256, 192}, {256, 256}};
-int64_t shape_tiles(Shape t, int64_t M, int64_t rows) { return (M + t.tm - 1) / t.tm * ((rows + t.tn - 1) / t.tn); }
-int64_t shape_cost(Shape t, int64_t M, int64_t rows, int cus) {
-  return (shape_tiles(t, M, rows) + cus - 1) / cus * (t.tm + t.tn);
-}
-// The cheapest shape; of equals the one with larger tiles (fewer LDS reads).
-Shape best_shape(int64_t M, int64_t rows, int cus) {
-  Shape best = kShapes[0];
-  for (const Shape& t : kShapes)
-    if (shape_cost(t, M, rows, cus) <= shape_cost(best, M, rows, cus)) best = t;
-  return best;
-}
-hipError_t launch_shape(Shape t, const I8Gemm& g, int64_t n_begin, int64_t n_rows, hipStream_t st) {
-  if (t.tm == 256)
-    return t.tn == 256   ? launch_fi<4>(g, n_begin, n_rows, st)
-           : t.tn == 192 ? launch_fi<3>(g, n_begin, n_rows, st)
-                         : launch_fi<2>(g, n_begin, n_rows, st);
-  if (t.tm == 192) return launch_tile<192, 128, 3>(g, n_begin, n_rows, st);
-  if (t.tm == 128) return launch_tile<128, 128, 4>(g, n_begin, n_rows, st);
-  return t.tn == 128 ? launch_tile<64, 128, 3>(g, n_begin, n_rows, st) : launch_tile<64, 64, 4>(g, n_begin, n_rows, st);
-}
-
-}  // namespace
-
 // Up to 16 tokens: the streaming kernel, 16 channels per workgroup, or 32
 // where that still fills the card and there are enough tokens for their
 // second reading to cost (16 x 8192 x 8192: 17.8 against 19.9 us, 16 x 22016 x
 // 8192: 41 against 47; one token at 22016 x 8192: 37 against 34).  17 to 32
 // tokens: the same with two token groups, below 16384 channels (32 x 8192 x
 // 8192: 19.8 against 21.3 us on 64 x 64 tiles, 32 x 22016 x 8192: 54 against
-// 45).  More: tiles (64 x 4096 x 4096: 10.6 against 12.1 us).
-hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st) {
+// 45).  More: tiles (64 x 4096 x 4096: 10.6 against 12.1 us), the small ones or
+// 256 x 64 FI; or whole rounds of 256 x 256 tiles and the rest of the channels
+// apart.
+hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, float* part, size_t part_bytes) {
   if (g.M <= 16) return g.M > 8 && g.N >= 8192 ? launch_skinny<2, 1, 2>(g, st) : launch_skinny<1, 1, 2>(g, st);
   if (g.M <= 32 && g.N < 16384) return g.N < 8192 ? launch_skinny<1, 2, 4>(g, st) : launch_skinny<2, 2, 2>(g, st);
   const int cus = device_cu_count();
-  const Shape one = best_shape(g.M, g.N, cus);
-  // or: whole rounds of 256 x 256 tiles, and the rest of the channels apart
+  const int64_t lines = i8_row_bytes(g.K) / 128;
+  auto part_of = [&](const TileChoice& c, int64_t n_begin, int64_t n_rows) {
+    if (c.tm == 256)
+      return c.tn == 256   ? launch_fi<4>(g, n_begin, n_rows, st)
+             : c.tn == 192 ? launch_fi<3>(g, n_begin, n_rows, st)
+                           : launch_fi<2>(g, n_begin, n_rows, st);
+    TileGemm t{};
+    t.W = g.Wq, t.X = g.Xq, t.sw = g.sw, t.sx = g.sx, t.N = g.N, t.row_bytes = i8_row_bytes(g.K), t.M = g.M;
+    t.T = g.U, t.B = g.B, t.r = g.r, t.s = g.s, t.Y = g.Y, t.part = part;
+    return launch_tile(t, c, n_begin, n_rows, st);
+  };
+  const TileChoice one = choose_tile(g.M, g.N, lines, cus, part ? part_bytes : 0);
   const int64_t tiles_m = (g.M + 255) / 256, tiles = tiles_m * ((g.N + 255) / 256);
   if (tiles > cus && cus % tiles_m == 0) {
     const int64_t rounds = tiles / cus, n_full = rounds * (cus / tiles_m) * 256;
     if (n_full < g.N) {
-      const Shape rest = best_shape(g.M, g.N - n_full, cus);
-      if (rounds * 512 + shape_cost(rest, g.M, g.N - n_full, cus) < shape_cost(one, g.M, g.N, cus)) {
+      const TileChoice rest = choose_tile(g.M, g.N - n_full, lines, cus, 0);
+      if ((double)rounds * tile_round_cost(256, 256, lines) + rest.cost < one.cost) {
         const hipError_t e = launch_fi<4>(g, 0, n_full, st);
-        return e != hipSuccess ? e : launch_shape(rest, g, n_full, g.N - n_full, st);
+        return e != hipSuccess ? e : part_of(rest, n_full, g.N - n_full);
       }
     }
   }
-  return launch_shape(one, g, 0, g.N, st);
+  return part_of(one, 0, g.N);
+}
+
+size_t i8_gemm_part_bytes(int64_t M, int64_t N, int64_t K) {
+  return M <= 32 ? 0 : tile_part_bytes(M, N, i8_row_bytes(K) / 128);
 }
 
 }  // namespace qlora

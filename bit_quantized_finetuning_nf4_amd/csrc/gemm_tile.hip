@@ -1,0 +1,268 @@
+// gemm_tile.hip -- the products of a middling number of tokens, or of few
+// channels: Y = X W^T and the adapter's term, in tiles small enough to reach
+// every CU, for bf16 and for 8-bit operands.
+//
+//   forward   Y = X W^T + s U B^T           (B [N x r])
+//   dX        Y = X W^T + s (G A)           (A [r x N], W a transposed weight)
+//   dX under dropout                        (s G A masked as Y's own shape)
+//
+// TM tokens x TN channels per workgroup, waves 2 x 2 over the tile, a ring of
+// NS stages of 128 bytes of all its rows, brought by buffer->LDS DMA.  The
+// fragments of a 32-byte step are read one step ahead of their MFMAs.  The
+// stage's barrier stands before its last step's MFMAs, which hide the first
+// reads of the next stage: there every wave has read all of the stage, so the
+// DMA of stage st + NS goes into its slot at once.
+//
+// What bounds it is the compute unit's DMA: about 90 cache lines in flight, so
+// 17-22 bytes a clock at the latencies of operands that come from beyond L2
+// (57 from L2 alone), whatever the depth of the ring; without its MFMAs and
+// LDS reads the loop takes the same time.  So the tile is chosen by the bytes
+// that the busiest CU brings (choose_tile), and where even the smallest tiles
+// leave CUs idle the contraction is split, the fp32 parts added in order.
+#include <algorithm>
+#include <type_traits>
+
+#include "dense_tile.h"
+#include "rng.h"
+
+namespace qlora {
+namespace {
+
+enum Tail : int { kTailFwd = 0, kTailDx = 1, kTailDxDrop = 2 };
+
+struct TileArgs {
+  TileGemm g;
+  int64_t n_begin;
+  int tiles_n, tiles_m, sps;   // sps: stages per split of the contraction
+};
+
+template <class MM, int TM, int TN, int NS, int TAIL>
+__global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
+  constexpr bool kI8 = std::is_same<MM, MmI8>::value;
+  constexpr int FI = TN / 64, FJ = TM / 64;         // 32-row fragments per wave
+  constexpr int kRows = TM + TN, kSlot = kRows * 128, kDma = kRows / 32;   // DMA instructions per wave and stage
+  extern __shared__ __align__(16) char smem[];
+  const TileGemm& g = p.g;
+  int tn, tm;
+  int id = xcd_tile_id();
+  const int split = id / (p.tiles_n * p.tiles_m);
+  map_tile_grouped(id - split * p.tiles_n * p.tiles_m, p.tiles_n, p.tiles_m, tn, tm);
+  const int64_t M = g.M, N = g.N, ld = g.row_bytes;
+  const int64_t n0 = p.n_begin + (int64_t)tn * TN, m0 = (int64_t)tm * TM;
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), wr = w >> 1, wc = w & 1;
+  const int lr = lane & 31, h = lane >> 5;
+  const int s0 = split * p.sps, nst = min((int)(ld >> 7) - s0, p.sps);
+  // weight rows 0 .. TN - 1, then token rows; instruction q of wave w brings
+  // rows 8 (4 q + w) .. + 7; rows past the end re-read the last one, never
+  // stored
+  const rsrc_t wres = make_rsrc(g.W, (uint32_t)(N * ld)), xres = make_rsrc(g.X, (uint32_t)(M * ld));
+  uint32_t off[kDma];
+#pragma unroll
+  for (int q = 0; q < kDma; ++q) {
+    const int row = 8 * (4 * q + w) + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+    const int64_t src = q < TN / 32 ? min(n0 + row, N - 1) : min(m0 + row - TN, M - 1);
+    off[q] = (uint32_t)(src * ld + 16 * c);
+  }
+  auto dma = [&](char* slot, int st, int q) __attribute__((always_inline)) {
+    // past the end: re-loads the last stage, never read
+    dma16(q < TN / 32 ? wres : xres, slot + 8 * (4 * q + w) * 128, off[q], (uint32_t)(s0 + min(st, nst - 1)) * 128u);
+  };
+  typename MM::acc_t acc[FI][FJ];
+#pragma unroll
+  for (int i = 0; i < FI; ++i)
+#pragma unroll
+    for (int j = 0; j < FJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+#pragma unroll
+  for (int a = 0; a < NS; ++a)
+#pragma unroll
+    for (int q = 0; q < kDma; ++q) dma(smem + a * kSlot, a, q);
+  int o[4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) o[kk] = pos128(lr, 2 * kk + h);
+  const int am = wc * 32 * FI * 128, bm = (TN + wr * 32 * FJ) * 128;
+  bf16x8_t a[2][FI], b[2][FJ];
+  auto read = [&](const char* base, int kk, int set) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < FI; ++i) a[set][i] = rd16(base + am + i * 32 * 128 + o[kk]);
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) b[set][j] = rd16(base + bm + j * 32 * 128 + o[kk]);
+  };
+  QLORA_WAIT((NS - 1) * kDma, 0);
+  __builtin_amdgcn_s_barrier();
+  read(smem, 0, 0);
+  int slot = 0;
+  for (int st = 0; st < nst; ++st) {
+    char* cur = smem + slot * kSlot;
+    slot = slot == NS - 1 ? 0 : slot + 1;
+#pragma unroll
+    for (int kk = 0; kk < 3; ++kk) {
+      read(cur, kk + 1, (kk + 1) & 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) acc[i][j] = MM::mma(a[kk & 1][i], b[kk & 1][j], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    QLORA_WAIT((NS - 2) * kDma, 0);   // stage st + 1 has landed; this wave has read all of stage st
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read(smem + slot * kSlot, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int x = 0; x < FI * FJ; ++x) {
+      acc[x / FJ][x % FJ] = MM::mma(a[1][x / FJ], b[1][x % FJ], acc[x / FJ][x % FJ]);
+#pragma unroll
+      for (int q = 0; q < kDma; ++q)
+        if (q * FI * FJ / kDma == x) dma(cur, st + NS, q);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  QLORA_WAIT(0, 0);   // no DMA still in flight when the workgroup ends
+
+  // D[channel][token]: lane (lr, h): token lr, channels 8 q + 4 h .. of a
+  // block.  The adapter's product of a block is summed on its own, from
+  // global memory: 8 ranks per lane half and MFMA.
+  [[maybe_unused]] DropKey key;
+  if constexpr (TAIL == kTailDxDrop) key = drop_key(g.drop);
+  const int r = split == 0 ? g.r : 0;
+#pragma unroll
+  for (int j = 0; j < FJ; ++j) {
+    const int64_t m = m0 + 32 * (FJ * wr + j) + lr;
+    [[maybe_unused]] float x = 1.0f;
+    if constexpr (kI8) x = m < M ? g.sx[m] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < FI; ++i) {
+      const int64_t nb = n0 + 32 * (FI * wc + i);
+      f32x16_t y;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] = 0.0f;
+      for (int c = 0; c < r; c += 16) {
+        const int k = c + 8 * h;
+        bf16x8_t fb{}, fu{};
+        if (k < r && nb + lr < N) {
+          if constexpr (TAIL == kTailFwd) {
+            fb = *reinterpret_cast<const bf16x8_t*>(g.B + (nb + lr) * g.r + k);
+          } else {   // A's rows: eight ranks of one column
+            uint32_t v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = g.B[(int64_t)(k + e) * N + nb + lr];
+            fb = __builtin_bit_cast(bf16x8_t, u32x4_t{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
+                                                      v[6] | v[7] << 16});
+          }
+        }
+        if (k < r && m < M) fu = *reinterpret_cast<const bf16x8_t*>(g.T + m * g.r + k);
+        y = mfma32x32x16(fb, fu, y);
+      }
+      if constexpr (TAIL == kTailDxDrop) {
+        if (r > 0) mask_block(y, (uint32_t)m * (uint32_t)(N >> 3) + (uint32_t)(nb >> 3), key);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t n = nb + 8 * q + 4 * h;   // N % 8 == 0
+        if (m < M && n < N) {
+          float4 sc = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+          if constexpr (kI8) sc = *reinterpret_cast<const float4*>(g.sw + n);
+          const float y0 = fmaf(g.s, y[4 * q], (float)acc[i][j][4 * q] * (x * sc.x)),
+                      y1 = fmaf(g.s, y[4 * q + 1], (float)acc[i][j][4 * q + 1] * (x * sc.y)),
+                      y2 = fmaf(g.s, y[4 * q + 2], (float)acc[i][j][4 * q + 2] * (x * sc.z)),
+                      y3 = fmaf(g.s, y[4 * q + 3], (float)acc[i][j][4 * q + 3] * (x * sc.w));
+          if (g.part)
+            *reinterpret_cast<float4*>(g.part + ((int64_t)split * M + m) * N + n) = make_float4(y0, y1, y2, y3);
+          else
+            *reinterpret_cast<uint2*>(g.Y + m * N + n) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
+        }
+      }
+    }
+  }
+}
+
+template <class MM, int TM, int TN, int NS, int TAIL>
+hipError_t launch(TileGemm g, int splits, int64_t n_begin, int64_t n_rows, hipStream_t st) {
+  auto* fn = &tile_kernel<MM, TM, TN, NS, TAIL>;
+  constexpr int lds = NS * (TM + TN) * 128;
+  hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
+  if (e != hipSuccess) return e;
+  TileArgs p{g, n_begin, (int)((n_rows + TN - 1) / TN), (int)((g.M + TM - 1) / TM), 0};
+  const int lines = (int)(g.row_bytes / 128);
+  p.sps = (lines + splits - 1) / splits;
+  if (splits == 1) p.g.part = nullptr;
+  hipLaunchKernelGGL(fn, dim3(p.tiles_n * p.tiles_m * splits), dim3(kThreads), lds, st, p);
+  if ((e = hipGetLastError()) != hipSuccess || splits == 1) return e;
+  return launch_split_sum(g.part, splits, g.M * g.N, g.Y, st);
+}
+
+template <class MM, int TAIL>
+hipError_t launch_shape(const TileGemm& g, const TileChoice& c, int64_t n_begin, int64_t n_rows, hipStream_t st) {
+  if (c.tm == 192) return launch<MM, 192, 128, 3, TAIL>(g, c.splits, n_begin, n_rows, st);
+  if (c.tm == 128) return launch<MM, 128, 128, 4, TAIL>(g, c.splits, n_begin, n_rows, st);
+  if (c.tn == 128) return launch<MM, 64, 128, 3, TAIL>(g, c.splits, n_begin, n_rows, st);
+  return launch<MM, 64, 64, 4, TAIL>(g, c.splits, n_begin, n_rows, st);
+}
+
+struct Shape {
+  int tm, tn;
+};
+constexpr Shape kShapes[] = {{64, 64}, {64, 128}, {128, 128}, {192, 128}, {256, 128}, {256, 192}, {256, 256}};
+constexpr int kMaxSplits = 32;
+constexpr int kMinLines = 4;   // stages of a split, at least
+
+}  // namespace
+
+// One round of tiles in us: the tile's rows at 46 bytes per ns and CU, and
+// what a round costs beside its loop (prologue, epilogue and, for the 256-row
+// kernels, the tile's way out through LDS).
+double tile_round_cost(int tm, int tn, int64_t lines) {
+  return (double)(tm + tn) * 128.0 * (double)lines / 46e3 + (tm == 256 ? 8.0 : 3.0);
+}
+
+// The shape, and for the small ones the split of the contraction, with the
+// least time.  Measured in us for 8-bit operands (tokens x channels x K; the
+// shapes with rounds x rows):
+//   128 x 8192 x 8192    64x64 128: 24   64x128 192: 35   128x128 256: 45
+//   512 x 8192 x 22016   128x128 256: 115   192x128 320: 130
+//                        256x128 384: 177   64x64 512: 172
+//   333 x 11008 x 4096   192x128 320: 34   256x128 384: 39   256x192 448: 45
+//                        256x256 512: 50
+//   768 x 11008 x 4096   256x192 448: 50   256x256 512: 53   192x128 640: 67
+// Rings of two stages lose (151 us against 115 with four, 128 x 128 at 512 x
+// 8192 x 22016); past three or four nothing changes.  A split adds its fp32
+// parts' way through memory and a launch.
+TileChoice choose_tile(int64_t M, int64_t N, int64_t lines, int cus, size_t part_bytes) {
+  TileChoice best{0, 0, 1, 1e30};
+  for (const Shape& t : kShapes) {
+    const int64_t tiles = (M + t.tm - 1) / t.tm * ((N + t.tn - 1) / t.tn);
+    for (int want = 1; want <= (t.tm == 256 ? 1 : kMaxSplits); ++want) {
+      if (want > 1 && (int64_t)want * kMinLines > lines) break;
+      const int64_t sps = (lines + want - 1) / want;
+      const int splits = (int)((lines + sps - 1) / sps);   // no split is empty
+      if (splits != want) continue;
+      const size_t bytes = (size_t)splits * (size_t)M * (size_t)N * sizeof(float);
+      if (splits > 1 && bytes > part_bytes) break;
+      double cost = (double)((tiles * splits + cus - 1) / cus) * tile_round_cost(t.tm, t.tn, sps);
+      if (splits > 1) cost += 3.0 + (double)bytes * 2.0 / 4e6;
+      if (cost <= best.cost) best = TileChoice{t.tm, t.tn, splits, cost};
+    }
+  }
+  return best;
+}
+
+// Room for the split that choose_tile would take with room enough, on a card
+// of kSplitCus CUs, so that the size does not depend on the device; with
+// less, or with more CUs, it takes what fits.
+constexpr int kSplitCus = 256;
+size_t tile_part_bytes(int64_t M, int64_t N, int64_t lines) {
+  const TileChoice c = choose_tile(M, N, lines, kSplitCus, (size_t)1 << 62);
+  return c.splits > 1 ? (size_t)c.splits * (size_t)M * (size_t)N * sizeof(float) : 0;
+}
+
+hipError_t launch_tile(const TileGemm& g, const TileChoice& c, int64_t n_begin, int64_t n_rows, hipStream_t st) {
+  if (g.sw) return launch_shape<MmI8, kTailFwd>(g, c, n_begin, n_rows, st);
+  if (!g.b_trans) return launch_shape<MmBf16, kTailFwd>(g, c, n_begin, n_rows, st);
+  return g.dropped ? launch_shape<MmBf16, kTailDxDrop>(g, c, n_begin, n_rows, st)
+                   : launch_shape<MmBf16, kTailDx>(g, c, n_begin, n_rows, st);
+}
+
+}  // namespace qlora

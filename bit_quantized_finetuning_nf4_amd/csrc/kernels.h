@@ -133,12 +133,15 @@ hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t*
                                 int64_t N, int64_t K, int r, const DropArgs* drop, float* part, float* dA, float* dB,
                                 float scale, hipStream_t st);
 
-// dX [M x K] = dY WdT^T + s drop'(G A): the dense product on WdT [K x N]
-// (K weight rows, contraction N % 64 == 0) with the adapter's product masked
-// as the M x K tensor X was.
-hipError_t launch_bf16_dx_drop(const bf16_t* WdT, int64_t K, int64_t N, const bf16_t* dY, int64_t M, const bf16_t* G,
-                               const bf16_t* A, int r, float s, const DropArgs& drop, bf16_t* dX, hipStream_t st,
-                               float* part, size_t part_bytes);
+// launch_bf16_fwd on the small tiles or the 256-token kernels, whichever is
+// estimated faster: Y [M x N] = X Wd^T + s T B'^T, with b_trans and drop (may
+// be null) the adapter's term masked as the M x N tensor was (dX).  K % 64 ==
+// 0; part as for launch_bf16_fwd, staged_part_bytes are enough.
+size_t staged_part_bytes(int64_t N, int64_t K, int64_t M);
+double staged_cost(int64_t N, int64_t K, int64_t M);   // us, estimated
+hipError_t launch_staged(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* T,
+                         const bf16_t* B, bool b_trans, int r, float s, const DropArgs* drop, bf16_t* Y, hipStream_t st,
+                         float* part, size_t part_bytes);
 
 // Rows of 8-bit integers with one scale each (i8.hip): bytes from one row to
 // the next, and the passes over them.
@@ -173,7 +176,40 @@ struct I8Gemm {
   float s;
   bf16_t* Y;
 };
-hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st);
+// part (part_bytes of fp32 scratch, may be null) lets shapes of few tiles split
+// their contraction; i8_gemm_part_bytes is enough.
+size_t i8_gemm_part_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, float* part, size_t part_bytes);
+
+// Tiles of a middling product (gemm_tile.hip).  Rows of W [N] and X [M] are
+// row_bytes apart, whole 128-byte lines; sw and sx: 8-bit operands.  The
+// adapter's term: T [M x r] with B [N x r], or with b_trans A [r x N], masked
+// by `drop` if `dropped`.
+struct TileGemm {
+  const void* W;
+  const void* X;
+  const float* sw;
+  const float* sx;
+  int64_t N, row_bytes, M;
+  const bf16_t* T;
+  const bf16_t* B;
+  int r;
+  float s;
+  bool b_trans, dropped;
+  DropArgs drop;
+  bf16_t* Y;
+  float* part;
+};
+struct TileChoice {
+  int tm, tn, splits;   // tm == 256: one of the 256-token kernels
+  double cost;          // us, estimated
+};
+double tile_round_cost(int tm, int tn, int64_t lines);
+TileChoice choose_tile(int64_t M, int64_t N, int64_t lines, int cus, size_t part_bytes);
+size_t tile_part_bytes(int64_t M, int64_t N, int64_t lines);
+hipError_t launch_tile(const TileGemm& g, const TileChoice& c, int64_t n_begin, int64_t n_rows, hipStream_t st);
+// Y [n] bf16 = the sum of the splits' fp32 parts, in order.
+hipError_t launch_split_sum(const float* part, int splits, int64_t n, bf16_t* Y, hipStream_t st);
 
 // The paged optimizer's layout and step (paged.hip).
 bool paged_plan(const qlora_paged_tensor* t, int nt, size_t dev_bytes, qlora_paged_layout* L);
