@@ -6,7 +6,7 @@ import math
 
 import pytest
 
-from bit_quantized_finetuning_nf4_amd import _lib
+from bit_quantized_finetuning_nf4_amd import _lib, ops
 from bit_quantized_finetuning_nf4_amd._lib import DropDesc, I8RowsDesc, Nf4WeightDesc
 
 NULL, ALIGN, SHAPE, UNSUPPORTED, WORKSPACE = 1, 2, 3, 4, 5
@@ -72,7 +72,8 @@ def test_workspace_queries(L):
 
 def test_i8(L):
     rb = L.qlora_i8_row_bytes
-    assert [rb(c) for c in (-8, 0, 8, 128, 136, 131072, 131080)] == [0, 0, 128, 128, 256, 131072, 0]
+    sizes = (-8, 0, 8, 128, 136, 131072, 131080)
+    assert [rb(c) for c in sizes] == [ops.i8_row_bytes(c) for c in sizes] == [0, 0, 128, 128, 256, 131072, 0]
     rows = lambda n=64, k=256, c=P[0].value, s=P[1].value: I8RowsDesc(n, k, c, s)
     for call in (lambda q: L.qlora_i8_quantize(P[2], ref(q), None), lambda q: L.qlora_i8_dequant(ref(q), P[2], None),
                  lambda q: L.qlora_i8_matmul(ref(rows(4)), ref(q), P[2], None),
