@@ -24,7 +24,7 @@
 #include "device.h"
 #include "kernels.h"
 #include "lds.h"
-#include "rng.h"
+#include "urows.h"
 
 namespace qlora {
 
@@ -615,10 +615,28 @@ size_t adapter_part_bytes(int64_t M, int64_t N, int64_t K, int r) {
   return std::max(std::max(u, g), (da + 255) / 256 * 256 + db);
 }
 
-size_t u_part_bytes(int64_t M, int64_t K, int r) { return part_bytes(rows_split(M, K), M * r); }
+size_t u_part_bytes(int64_t M, int64_t K, int r) {
+  return u_rows_ok(M, r) ? 0 : part_bytes(rows_split(M, K), M * r);
+}
+
+namespace {
+
+template <bool DROP>
+__global__ __launch_bounds__(256) void u_rows_kernel(const bf16_t* __restrict__ X, int64_t M, int64_t K,
+                                                     const bf16_t* __restrict__ A, int r, bf16_t* __restrict__ U,
+                                                     DropArgs drop) {
+  u_rows<DROP>(X, M, K, A, r, blockIdx.x, U, drop);
+}
+
+}  // namespace
 
 hipError_t launch_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
                            float* part, bf16_t* out, hipStream_t st) {
+  if (u_rows_ok(M, r)) {
+    hipLaunchKernelGGL((drop ? &u_rows_kernel<true> : &u_rows_kernel<false>), dim3((unsigned)u_rows_blocks(M, r)),
+                       dim3(256), 0, st, X, M, K, A, r, out, drop ? *drop : DropArgs{});
+    return hipGetLastError();
+  }
   const RowArgs a{X, M, K, K, 0, A, r, 0, 1, r};
   const Split sp = rows_split(M, K);
   const DropArgs d = drop ? *drop : DropArgs{};

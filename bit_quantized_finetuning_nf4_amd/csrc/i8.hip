@@ -9,7 +9,7 @@
 // Rows are padded with zeros to whole 128-byte lines (i8_row_bytes), which
 // the product kernels stream.
 #include "lds.h"
-#include "rng.h"
+#include "urows.h"
 
 namespace qlora {
 namespace {
@@ -131,64 +131,19 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const bf16_t* __restric
   quant_row<TPR, NCH>(X, m, threadIdx.x % TPR, K, ld, Q, scale, wmax);
 }
 
-// What a product of few tokens needs first, in one launch: workgroups 0 ..
-// nu - 1 compute U = drop(X) A^T, one rank row and up to 16 tokens each (as
-// fp32 dot products: A is read once), the others quantize one token each.
-// With M <= 64 either part alone would leave most of the card idle.
-constexpr int kPrepTokens = 16;
+// What the product needs first, in one launch where U is small: workgroups
+// 0 .. nu - 1 compute U = drop(X) A^T (urows.h), the others quantize one token
+// each.  Either part alone would leave most of the card idle.
 template <int NCH, bool DROP>
 __global__ __launch_bounds__(256) void i8_prep_kernel(const bf16_t* __restrict__ X, int64_t M, int64_t K, int64_t ld,
                                                       const bf16_t* __restrict__ A, int r, int nu,
                                                       bf16_t* __restrict__ U, int8_t* __restrict__ Q,
                                                       float* __restrict__ scale, DropArgs drop) {
   __shared__ uint32_t wmax[4];
-  __shared__ float part[4][kPrepTokens];
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  if ((int)blockIdx.x >= nu) {
-    quant_row<256, NCH>(X, (int)blockIdx.x - nu, t, K, ld, Q, scale, wmax);
-    return;
-  }
-  const int j = blockIdx.x % r, m0 = (int)blockIdx.x / r * kPrepTokens;
-  const int mt = min(kPrepTokens, (int)M - m0);
-  const int groups = (int)(K >> 3);
-  [[maybe_unused]] DropKey key;
-  if constexpr (DROP) key = drop_key(drop);
-  float sum[kPrepTokens];
-#pragma unroll
-  for (int i = 0; i < kPrepTokens; ++i) sum[i] = 0.0f;
-  for (int g = t; g < groups; g += 256) {
-    const uint4 a = reinterpret_cast<const uint4*>(A + (int64_t)j * K)[g];
-    const float a0 = bf2f(a.x & 0xFFFFu), a1 = bf2f(a.x >> 16), a2 = bf2f(a.y & 0xFFFFu), a3 = bf2f(a.y >> 16),
-                a4 = bf2f(a.z & 0xFFFFu), a5 = bf2f(a.z >> 16), a6 = bf2f(a.w & 0xFFFFu), a7 = bf2f(a.w >> 16);
-#pragma unroll
-    for (int i = 0; i < kPrepTokens; ++i)
-      if (i < mt) {
-        u32x4_t x = *reinterpret_cast<const u32x4_t*>(X + (m0 + i) * K + 8 * g);
-        if constexpr (DROP) x = drop8(x, (uint32_t)(m0 + i) * (uint32_t)groups + (uint32_t)g, key);
-        float v = sum[i];
-        v = fmaf(a0, bf2f(x.x & 0xFFFFu), v);
-        v = fmaf(a1, bf2f(x.x >> 16), v);
-        v = fmaf(a2, bf2f(x.y & 0xFFFFu), v);
-        v = fmaf(a3, bf2f(x.y >> 16), v);
-        v = fmaf(a4, bf2f(x.z & 0xFFFFu), v);
-        v = fmaf(a5, bf2f(x.z >> 16), v);
-        v = fmaf(a6, bf2f(x.w & 0xFFFFu), v);
-        sum[i] = fmaf(a7, bf2f(x.w >> 16), v);
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < kPrepTokens; ++i)
-    if (i < mt) {
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) sum[i] += __shfl_xor(sum[i], o);
-      if (lane == 0) part[w][i] = sum[i];
-    }
-  __syncthreads();
-  if (t < mt) {
-    float v = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
-    if constexpr (DROP) v *= drop.scale;
-    U[(int64_t)(m0 + t) * r + j] = (bf16_t)pack_bf16x2(v, 0.0f);
-  }
+  if ((int)blockIdx.x >= nu)
+    quant_row<256, NCH>(X, (int)blockIdx.x - nu, threadIdx.x, K, ld, Q, scale, wmax);
+  else
+    u_rows<DROP>(X, M, K, A, r, blockIdx.x, U, drop);
 }
 
 // deq = RNE_bf16(RN32(scale q)).
@@ -279,12 +234,12 @@ hipError_t launch_quant_rows(const bf16_t* X, int64_t M, int64_t K, int8_t* Q, f
   return hipGetLastError();
 }
 
-bool i8_prep_ok(int64_t M, int64_t K) { return M <= 64 && i8_row_bytes(K) <= 32768; }
+bool i8_prep_ok(int64_t M, int64_t K, int r) { return u_rows_ok(M, r) && i8_row_bytes(K) <= 32768; }
 
 hipError_t launch_i8_prep(const bf16_t* X, int64_t M, int64_t K, const bf16_t* A, int r, const DropArgs* drop,
                           bf16_t* U, int8_t* Q, float* scale, hipStream_t st) {
   const int64_t ld = i8_row_bytes(K);
-  const int nu = r * (int)((M + kPrepTokens - 1) / kPrepTokens);
+  const int nu = u_rows_blocks(M, r);
   auto go = [&](auto* fn) {
     hipLaunchKernelGGL(fn, dim3((unsigned)(nu + M)), dim3(256), 0, st, X, M, K, ld, A, r, nu, U, Q, scale,
                        drop ? *drop : DropArgs{});

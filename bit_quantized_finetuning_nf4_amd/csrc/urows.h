@@ -1,0 +1,71 @@
+// urows.h -- U = drop(X) A^T for few tokens or a small rank, without partial
+// sums: a workgroup takes one rank row and up to four tokens and forms their
+// fp32 dot products, each thread over every 256th group of eight columns.  A
+// is read once per four tokens and X r times (from L2), so it pays while M r
+// is small; past that the MFMA product with split partials does (gemm.hip),
+// which is two launches.  Four tokens: with 16 a workgroup brings 256 KiB at K
+// = 8192 (16 tokens at rank 64 with their quantization and product: 15.8 us
+// with four, 19.1 with eight, 26 with 16, 22.6 by MFMA).
+#pragma once
+#include "rng.h"
+
+namespace qlora {
+
+constexpr int kURowTokens = 4;
+
+template <bool DROP>
+__device__ __forceinline__ void u_rows(const bf16_t* __restrict__ X, int64_t M, int64_t K, const bf16_t* __restrict__ A,
+                                       int r, int block, bf16_t* __restrict__ U, const DropArgs& drop) {
+  __shared__ float part[4][kURowTokens];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  const int j = block % r, m0 = block / r * kURowTokens;
+  const int mt = min(kURowTokens, (int)M - m0);
+  const int groups = (int)(K >> 3);
+  [[maybe_unused]] DropKey key;
+  if constexpr (DROP) key = drop_key(drop);
+  float sum[kURowTokens];
+#pragma unroll
+  for (int i = 0; i < kURowTokens; ++i) sum[i] = 0.0f;
+  for (int g = t; g < groups; g += 256) {
+    const uint4 a = reinterpret_cast<const uint4*>(A + (int64_t)j * K)[g];
+    const float a0 = bf2f(a.x & 0xFFFFu), a1 = bf2f(a.x >> 16), a2 = bf2f(a.y & 0xFFFFu), a3 = bf2f(a.y >> 16),
+                a4 = bf2f(a.z & 0xFFFFu), a5 = bf2f(a.z >> 16), a6 = bf2f(a.w & 0xFFFFu), a7 = bf2f(a.w >> 16);
+#pragma unroll
+    for (int i = 0; i < kURowTokens; ++i)
+      if (i < mt) {
+        u32x4_t x = *reinterpret_cast<const u32x4_t*>(X + (m0 + i) * K + 8 * g);
+        if constexpr (DROP) x = drop8(x, (uint32_t)(m0 + i) * (uint32_t)groups + (uint32_t)g, key);   // M K < 2^31
+        float v = sum[i];
+        v = fmaf(a0, bf2f(x.x & 0xFFFFu), v);
+        v = fmaf(a1, bf2f(x.x >> 16), v);
+        v = fmaf(a2, bf2f(x.y & 0xFFFFu), v);
+        v = fmaf(a3, bf2f(x.y >> 16), v);
+        v = fmaf(a4, bf2f(x.z & 0xFFFFu), v);
+        v = fmaf(a5, bf2f(x.z >> 16), v);
+        v = fmaf(a6, bf2f(x.w & 0xFFFFu), v);
+        sum[i] = fmaf(a7, bf2f(x.w >> 16), v);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < kURowTokens; ++i)
+    if (i < mt) {
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) sum[i] += __shfl_xor(sum[i], o);
+      if (lane == 0) part[w][i] = sum[i];
+    }
+  __syncthreads();
+  if (t < mt) {
+    float v = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
+    if constexpr (DROP) v *= drop.scale;
+    U[(int64_t)(m0 + t) * r + j] = (bf16_t)pack_bf16x2(v, 0.0f);
+  }
+}
+
+inline int u_rows_blocks(int64_t M, int r) { return r * (int)((M + kURowTokens - 1) / kURowTokens); }
+// U with the tokens' quantization and a small product, in us, here and by
+// MFMA: 128 x 4096 at rank 64 15.2 and 20.0, 64 x 8192 at rank 128 21.1 and 27.7,
+// 512 x 4096 at rank 16 17.6 and 19.4; but 1024 x 4096 at rank 8 23.1 and 20.9,
+// 256 x 4096 at rank 64 under the mask 27.1 and 22.7.
+inline bool u_rows_ok(int64_t M, int r) { return M * r <= 8192 && M <= 512; }
+
+}  // namespace qlora
