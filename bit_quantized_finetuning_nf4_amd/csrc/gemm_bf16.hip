@@ -475,6 +475,10 @@ hipError_t launch_staged(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X
     t.Y = Y, t.part = part;
     return launch_tile(t, c, 0, N, st);
   }
+  if (c.splits > 1) {
+    const hipError_t e = launch_fi<4>(Wd, N, K, X, M, T, B, b_trans, r, r, N, sc, Y, 0, N, st, drop, c.splits, part);
+    return e != hipSuccess ? e : launch_split_sum(part, c.splits, M * N, Y, st);
+  }
   return launch_dense(Wd, N, K, X, M, T, r, B, b_trans, r, N, sc, Y, st, part, part_bytes, drop);
 }
 

@@ -78,8 +78,10 @@ __device__ __forceinline__ void lora_tail(f32x16_t (&acc)[FI][4], const bf16_t* 
   }
 }
 
-// Xq [M x ld], Wq [N x ld] bytes, ld = 128 npair_all; tiles of 64 FI channels
-// x 256 tokens from channel n_begin on.
+// Xq [M x ld], Wq [N x ld] bytes, whole 128-byte pairs; tiles of 64 FI channels
+// x 256 tokens from channel n_begin on.  part != null: the grid holds the tiles
+// once per split of the contraction, pps pairs each, split 0 with the adapter's
+// term, and their fp32 values go to part + split M N instead of Y.
 template <int FI>
 __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __restrict__ Wq,
                                                               const float* __restrict__ sw, int64_t N, int64_t ld,
@@ -88,17 +90,18 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
                                                               const bf16_t* __restrict__ U,
                                                               const bf16_t* __restrict__ B, int r, float s,
                                                               bf16_t* __restrict__ Y, int64_t n_begin, int tiles_n,
-                                                              int tiles_m) {
+                                                              int tiles_m, int pps, float* __restrict__ part) {
   extern __shared__ __align__(16) char smem[];
   int tn, tm;
-  map_tile_grouped(xcd_tile_id(), tiles_n, tiles_m, tn, tm);
+  const int id = xcd_tile_id(), split = id / (tiles_n * tiles_m), p0 = split * pps;
+  map_tile_grouped(id - split * tiles_n * tiles_m, tiles_n, tiles_m, tn, tm);
   const int64_t n0 = n_begin + (int64_t)tn * 64 * FI, m0 = (int64_t)tm * kTile;
   const int t = threadIdx.x, lane = t & 63, wv = t >> 6, wr = wv >> 1, wc = wv & 1;
 
   DenseOps f;
   f.w = __builtin_amdgcn_readfirstlane(wv);
   __builtin_assume(f.w >= 0 && f.w < 4);
-  f.npair = (int)(ld >> 7);
+  f.npair = min((int)(ld >> 7) - p0, pps);
   f.wr_ = make_rsrc(Wq, (uint32_t)(N * ld));
   f.xr = make_rsrc(Xq, (uint32_t)(M * ld));
   {
@@ -107,8 +110,8 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
     for (int q = 0; q < 8; ++q) {
       // rows past the end re-read the last row, never stored
       const int row = 8 * (4 * q + f.w) + (lane >> 3);
-      if (q < 2 * FI) f.wo[q] = (uint32_t)(min(n0 + row, N - 1) * ld + c * 16);
-      f.xo[q] = (uint32_t)(min(m0 + row, M - 1) * ld + c * 16);
+      if (q < 2 * FI) f.wo[q] = (uint32_t)(min(n0 + row, N - 1) * ld + p0 * 128 + c * 16);
+      f.xo[q] = (uint32_t)(min(m0 + row, M - 1) * ld + p0 * 128 + c * 16);
     }
   }
   PairOffs po;
@@ -156,8 +159,11 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
 
   f32x16_t out[FI][4];
   scale_tile<FI>(acc, out, sx, sw, M, N, m0, n0);
-  if (r > 0) lora_tail<FI>(out, B, U, r, s, M, N, m0, n0, smem);
-  store_tile_lds<FI>(out, Y, N, M, N, m0, n0, smem);
+  if (r > 0 && split == 0) lora_tail<FI>(out, B, U, r, s, M, N, m0, n0, smem);
+  if (part != nullptr)
+    store_tile_f32<FI>(out, part + (int64_t)split * M * N, N, M, N, m0, n0);
+  else
+    store_tile_lds<FI>(out, Y, N, M, N, m0, n0, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -286,14 +292,17 @@ hipError_t launch_skinny(const I8Gemm& g, hipStream_t st) {
 }
 
 template <int FI>
-hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, hipStream_t st) {
+hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, int splits, float* part, hipStream_t st) {
   const int tiles_n = (int)((n_rows + 64 * FI - 1) / (64 * FI)), tiles_m = (int)((g.M + kTile - 1) / kTile);
   auto* fn = &i8_gemm_kernel<FI>;
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)kLdsPairs);
+  hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)kLdsPairs);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_m), dim3(kThreads), kLdsPairs, st, g.Wq, g.sw, g.N, i8_row_bytes(g.K),
-                     g.Xq, g.sx, g.M, g.U, g.B, g.r, g.s, g.Y, n_begin, tiles_n, tiles_m);
-  return hipGetLastError();
+  const int npair = (int)(i8_row_bytes(g.K) / 128);
+  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_m * splits), dim3(kThreads), kLdsPairs, st, g.Wq, g.sw, g.N,
+                     i8_row_bytes(g.K), g.Xq, g.sx, g.M, g.U, g.B, g.r, g.s, g.Y, n_begin, tiles_n, tiles_m,
+                     (npair + splits - 1) / splits, splits > 1 ? part : nullptr);
+  if ((e = hipGetLastError()) != hipSuccess || splits == 1) return e;
+  return launch_split_sum(part, splits, g.M * g.N, g.Y, st);
 }
 
 }  // namespace
@@ -314,9 +323,9 @@ hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, float* part, size_t p
   const int64_t lines = i8_row_bytes(g.K) / 128;
   auto part_of = [&](const TileChoice& c, int64_t n_begin, int64_t n_rows) {
     if (c.tm == 256)
-      return c.tn == 256   ? launch_fi<4>(g, n_begin, n_rows, st)
-             : c.tn == 192 ? launch_fi<3>(g, n_begin, n_rows, st)
-                           : launch_fi<2>(g, n_begin, n_rows, st);
+      return c.tn == 256   ? launch_fi<4>(g, n_begin, n_rows, c.splits, part, st)
+             : c.tn == 192 ? launch_fi<3>(g, n_begin, n_rows, 1, nullptr, st)
+                           : launch_fi<2>(g, n_begin, n_rows, 1, nullptr, st);
     TileGemm t{};
     t.W = g.Wq, t.X = g.Xq, t.sw = g.sw, t.sx = g.sx, t.N = g.N, t.row_bytes = i8_row_bytes(g.K), t.M = g.M;
     t.T = g.U, t.B = g.B, t.r = g.r, t.s = g.s, t.Y = g.Y, t.part = part;
@@ -328,8 +337,8 @@ hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, float* part, size_t p
     const int64_t rounds = tiles / cus, n_full = rounds * (cus / tiles_m) * 256;
     if (n_full < g.N) {
       const TileChoice rest = choose_tile(g.M, g.N - n_full, lines, cus, 0);
-      if ((double)rounds * tile_round_cost(256, 256, lines) + rest.cost < one.cost) {
-        const hipError_t e = launch_fi<4>(g, 0, n_full, st);
+      if ((double)rounds * full_round_cost(lines) + rest.cost < one.cost) {
+        const hipError_t e = launch_fi<4>(g, 0, n_full, 1, nullptr, st);
         return e != hipSuccess ? e : part_of(rest, n_full, g.N - n_full);
       }
     }

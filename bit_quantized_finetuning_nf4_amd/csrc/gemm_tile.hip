@@ -202,24 +202,29 @@ hipError_t launch_shape(const TileGemm& g, const TileChoice& c, int64_t n_begin,
   return launch<MM, 64, 64, 4, TAIL>(g, c.splits, n_begin, n_rows, st);
 }
 
+// A round of tiles of tm tokens x tn channels: the bytes of the tile's rows
+// that a CU brings in a ns, and what a round costs beside them, in us.  Fitted
+// to the 8-bit product's times at 34 sizes (33 to 4096 tokens, 512 to 22016
+// channels and columns, seven shapes each; 10-14 % rms), where the shape that
+// they choose is within 0.7 % of the fastest on the mean and 13 % at most.
 struct Shape {
   int tm, tn;
+  double rate, fixed;
 };
-constexpr Shape kShapes[] = {{64, 64}, {64, 128}, {128, 128}, {192, 128}, {256, 128}, {256, 192}, {256, 256}};
+constexpr Shape kShapes[] = {{64, 64, 68e3, 2.5},   {64, 128, 67e3, 4.0},   {128, 128, 70e3, 8.8}, {192, 128, 65e3, 10.2},
+                             {256, 128, 58e3, 6.7}, {256, 192, 60e3, 9.4},  {256, 256, 56e3, 14.0}};
+double round_cost(const Shape& t, int64_t lines) {
+  return (double)(t.tm + t.tn) * 128.0 * (double)lines / t.rate + t.fixed;
+}
 constexpr int kMaxSplits = 32;
 constexpr int kMinLines = 4;   // stages of a split, at least
 
 }  // namespace
 
-// One round of tiles in us: the tile's rows at 46 bytes per ns and CU, and
-// what a round costs beside its loop (prologue, epilogue and, for the 256-row
-// kernels, the tile's way out through LDS).
-double tile_round_cost(int tm, int tn, int64_t lines) {
-  return (double)(tm + tn) * 128.0 * (double)lines / 46e3 + (tm == 256 ? 8.0 : 3.0);
-}
+double full_round_cost(int64_t lines) { return round_cost(kShapes[6], lines); }
 
-// The shape, and for the small ones the split of the contraction, with the
-// least time.  Measured in us for 8-bit operands (tokens x channels x K; the
+// The shape, and the split of the contraction, with the least time (256 x 192
+// and 256 x 128 tiles are not split: where they would be, another shape is).  Measured in us for 8-bit operands (tokens x channels x K; the
 // shapes with rounds x rows):
 //   128 x 8192 x 8192    64x64 128: 24   64x128 192: 35   128x128 256: 45
 //   512 x 8192 x 22016   128x128 256: 115   192x128 320: 130
@@ -228,21 +233,23 @@ double tile_round_cost(int tm, int tn, int64_t lines) {
 //                        256x256 512: 50
 //   768 x 11008 x 4096   256x192 448: 50   256x256 512: 53   192x128 640: 67
 // Rings of two stages lose (151 us against 115 with four, 128 x 128 at 512 x
-// 8192 x 22016); past three or four nothing changes.  A split adds its fp32
-// parts' way through memory and a launch.
+// 8192 x 22016); past three or four nothing changes.  A split adds a launch and
+// its fp32 parts' way through memory (mostly the last-level cache): 2048 x 4096
+// x 22016 takes 170 us on 256x256 tiles in two splits, 228 unsplit and 215 on
+// 128x128; 40 x 840 x 19840 12 us on 64x64 in eight, 36 unsplit.
 TileChoice choose_tile(int64_t M, int64_t N, int64_t lines, int cus, size_t part_bytes) {
   TileChoice best{0, 0, 1, 1e30};
   for (const Shape& t : kShapes) {
     const int64_t tiles = (M + t.tm - 1) / t.tm * ((N + t.tn - 1) / t.tn);
-    for (int want = 1; want <= (t.tm == 256 ? 1 : kMaxSplits); ++want) {
+    for (int want = 1; want <= (t.tm == 256 && t.tn != 256 ? 1 : kMaxSplits); ++want) {
       if (want > 1 && (int64_t)want * kMinLines > lines) break;
       const int64_t sps = (lines + want - 1) / want;
       const int splits = (int)((lines + sps - 1) / sps);   // no split is empty
       if (splits != want) continue;
       const size_t bytes = (size_t)splits * (size_t)M * (size_t)N * sizeof(float);
       if (splits > 1 && bytes > part_bytes) break;
-      double cost = (double)((tiles * splits + cus - 1) / cus) * tile_round_cost(t.tm, t.tn, sps);
-      if (splits > 1) cost += 3.0 + (double)bytes * 2.0 / 4e6;
+      double cost = (double)((tiles * splits + cus - 1) / cus) * round_cost(t, sps);
+      if (splits > 1) cost += 2.0 + 0.2 * splits + (double)bytes / 4e6;
       if (cost <= best.cost) best = TileChoice{t.tm, t.tn, splits, cost};
     }
   }

@@ -204,7 +204,7 @@ struct TileChoice {
   int tm, tn, splits;   // tm == 256: one of the 256-token kernels
   double cost;          // us, estimated
 };
-double tile_round_cost(int tm, int tn, int64_t lines);
+double full_round_cost(int64_t lines);   // of 256 x 256 tiles
 TileChoice choose_tile(int64_t M, int64_t N, int64_t lines, int cus, size_t part_bytes);
 size_t tile_part_bytes(int64_t M, int64_t N, int64_t lines);
 hipError_t launch_tile(const TileGemm& g, const TileChoice& c, int64_t n_begin, int64_t n_rows, hipStream_t st);
