@@ -309,31 +309,39 @@ __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __re
       }
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
-        // transposed reads in asm blocks (see tr_read3): the big tile's
-        // fragment and the first two rank fragments, then three at a time
-        constexpr int O = 4 * 2 * RP;
-        const char* sb = base + S::kBig + kk * 16 * 2 * RP;
-        bf16x8_t bg, sm[FJ];
-        tr_read3<4 * 256, O, O>(base + kk * 16 * 256 + bo_frag, sb + tr_off<2 * RP>(0), sb + tr_off<2 * RP>(1), bg,
-                                sm[0], sm[1]);
-        if constexpr (FJ == 4) tr_read2<O, O>(sb + tr_off<2 * RP>(2), sb + tr_off<2 * RP>(3), sm[2], sm[3]);
-        if constexpr (FJ == 8) {
+        if constexpr (PARTS == 3) {
+          // fourteen transposed reads per asm block (see tr_read7): the big
+          // tile's fragment and two rank fragments of each part
+          constexpr int O = 4 * 2 * RP;
+          const char* sb = base + S::kBig + kk * 16 * 2 * RP;
 #pragma unroll
-          for (int f = 2; f < 8; f += 3)
-            tr_read3<O, O, O>(sb + tr_off<2 * RP>(f), sb + tr_off<2 * RP>(f + 1), sb + tr_off<2 * RP>(f + 2), sm[f],
-                              sm[f + 1], sm[f + 2]);
-        }
+          for (int f = 0; f < FJ; f += 2) {
+            bf16x8_t bg, sm[3][2];
+            tr_read7<4 * 256, S::kSm, O>(base + kk * 16 * 256 + bo_frag, sb + tr_off<2 * RP>(f),
+                                         sb + tr_off<2 * RP>(f + 1), bg, sm);
 #pragma unroll
-        for (int f = 0; f < FJ; ++f)
-          acc[f] = DB ? mfma32x32x16(sm[f], bg, acc[f]) : mfma32x32x16(bg, sm[f], acc[f]);
+            for (int p = 0; p < 3; ++p)
 #pragma unroll
-        for (int p = 1; p < PARTS; ++p) {
-          const char* sp2 = sb + p * S::kSm;
+              for (int e = 0; e < 2; ++e) acc[f + e] = mfma32x32x16(bg, sm[p][e], acc[f + e]);
+          }
+        } else {
+          // transposed reads in asm blocks (see tr_read3): the big tile's
+          // fragment and the first two rank fragments, then three at a time
+          constexpr int O = 4 * 2 * RP;
+          const char* sb = base + S::kBig + kk * 16 * 2 * RP;
+          bf16x8_t bg, sm[FJ];
+          tr_read3<4 * 256, O, O>(base + kk * 16 * 256 + bo_frag, sb + tr_off<2 * RP>(0), sb + tr_off<2 * RP>(1), bg,
+                                  sm[0], sm[1]);
+          if constexpr (FJ == 4) tr_read2<O, O>(sb + tr_off<2 * RP>(2), sb + tr_off<2 * RP>(3), sm[2], sm[3]);
+          if constexpr (FJ == 8) {
 #pragma unroll
-          for (int f = 0; f < FJ; f += 2)
-            tr_read2<O, O>(sp2 + tr_off<2 * RP>(f), sp2 + tr_off<2 * RP>(f + 1), sm[f], sm[f + 1]);
+            for (int f = 2; f < 8; f += 3)
+              tr_read3<O, O, O>(sb + tr_off<2 * RP>(f), sb + tr_off<2 * RP>(f + 1), sb + tr_off<2 * RP>(f + 2), sm[f],
+                                sm[f + 1], sm[f + 2]);
+          }
 #pragma unroll
-          for (int f = 0; f < FJ; ++f) acc[f] = mfma32x32x16(bg, sm[f], acc[f]);
+          for (int f = 0; f < FJ; ++f)
+            acc[f] = DB ? mfma32x32x16(sm[f], bg, acc[f]) : mfma32x32x16(bg, sm[f], acc[f]);
         }
       }
       slot = slot == kRing - 1 ? 0 : slot + 1;
@@ -582,29 +590,29 @@ hipError_t launch_grads(const bf16_t* Gm, const bf16_t* X, const bf16_t* dY, int
   return hipGetLastError();
 }
 
-// Splits of the products of an adapter under dropout and of the 8-bit linear.
-// The masked stages are longer (two Philox blocks per wave and stage of 32),
-// and the smaller layers have few tiles, so these products fill 512
-// workgroups (two per CU) by splits of four stages or more: the split count
-// whose rounds x (stages + 6 to fill the ring), plus a stage's time for each
-// split's partials, is least.  dA of 2048 x 4096 at rank 64: 64 workgroups
-// took 26 us, 256 take 13 us.  No device query, so that the workspace does
-// not depend on the device.
+// Splits of the products of an adapter under dropout and of the 8-bit linear:
+// four stages or more, and the count whose rounds x stages, with 6 stages to
+// fill the ring and one for each split's partials, are least.  dA of 2048 x
+// 4096 at rank 64: 64 workgroups took 26 us, 256 take 13 us.  Masked dA waits
+// for its LDS passes as much as for its loads, so two workgroups share a CU
+// (512); U and G are bound by the CU's loads, and one does (U of 4096 x 8192
+// under the mask: 25.5 us on 256 workgroups, 29.6 on 512).  No device query, so
+// that the workspace does not depend on the device.
 namespace {
 
-Split fill_split(int64_t tiles, int64_t contraction) {
+Split fill_split(int64_t tiles, int64_t contraction, int slots) {
   const int nst = (int)((contraction + 31) / 32);
   Split best{(int)tiles, nst, 1};
   int64_t best_cost = INT64_MAX;
   for (int want = 1; want <= 32 && (want == 1 || want * 4 <= nst); ++want) {
     const int sps = (nst + want - 1) / want, splits = (nst + sps - 1) / sps;
-    const int64_t cost = (tiles * splits + 511) / 512 * (sps + 6) + splits;
+    const int64_t cost = (tiles * splits + slots - 1) / slots * sps + 6 + splits;
     if (cost < best_cost) best_cost = cost, best = Split{(int)tiles, sps, splits};
   }
   return best;
 }
-Split rows_split(int64_t M, int64_t C) { return fill_split((M + 127) / 128, C); }
-Split cols_split(int64_t C, int64_t M) { return fill_split((C + 127) / 128, M); }
+Split rows_split(int64_t M, int64_t C) { return fill_split((M + 127) / 128, C, 256); }
+Split cols_split(int64_t C, int64_t M) { return fill_split((C + 127) / 128, M, 512); }
 size_t part_bytes(const Split& s, int64_t n) { return (size_t)s.splits * (size_t)n * sizeof(float); }
 
 }  // namespace

@@ -119,6 +119,40 @@ __device__ __forceinline__ void tr_read3(const char* p0, const char* p1, const c
   f2 = cat_frag(c0, c1);
 }
 
+// One fragment (second half O0 further) and, of each of three parts P bytes
+// apart, two fragments f0 and f1 (second halves O bytes further): fourteen
+// reads in flight at once.
+template <int O0, int P, int O>
+__device__ __forceinline__ void tr_read7(const char* p, const char* q0, const char* q1, bf16x8_t& f, bf16x8_t (&g)[3][2]) {
+  u32x2_t a[14];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %14\n\t"
+      "ds_read_b64_tr_b16 %1, %14 offset:%17\n\t"
+      "ds_read_b64_tr_b16 %2, %15\n\t"
+      "ds_read_b64_tr_b16 %3, %15 offset:%18\n\t"
+      "ds_read_b64_tr_b16 %4, %16\n\t"
+      "ds_read_b64_tr_b16 %5, %16 offset:%18\n\t"
+      "ds_read_b64_tr_b16 %6, %15 offset:%19\n\t"
+      "ds_read_b64_tr_b16 %7, %15 offset:%20\n\t"
+      "ds_read_b64_tr_b16 %8, %16 offset:%19\n\t"
+      "ds_read_b64_tr_b16 %9, %16 offset:%20\n\t"
+      "ds_read_b64_tr_b16 %10, %15 offset:%21\n\t"
+      "ds_read_b64_tr_b16 %11, %15 offset:%22\n\t"
+      "ds_read_b64_tr_b16 %12, %16 offset:%21\n\t"
+      "ds_read_b64_tr_b16 %13, %16 offset:%22\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(a[0]), "=&v"(a[1]), "=&v"(a[2]), "=&v"(a[3]), "=&v"(a[4]), "=&v"(a[5]), "=&v"(a[6]), "=&v"(a[7]),
+        "=&v"(a[8]), "=&v"(a[9]), "=&v"(a[10]), "=&v"(a[11]), "=&v"(a[12]), "=&v"(a[13])
+      : "v"(lds_addr(p)), "v"(lds_addr(q0)), "v"(lds_addr(q1)), "i"(O0), "i"(O), "i"(P), "i"(P + O), "i"(2 * P),
+        "i"(2 * P + O));
+  f = cat_frag(a[0], a[1]);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    g[k][0] = cat_frag(a[2 + 4 * k], a[3 + 4 * k]);
+    g[k][1] = cat_frag(a[4 + 4 * k], a[5 + 4 * k]);
+  }
+}
+
 // Position of 16-byte chunk c of row r in a 64-byte-row tile.
 __device__ __forceinline__ int spos(int r, int c) { return r * 64 + 16 * (c ^ ((r >> 2) & 3)); }
 
