@@ -18,45 +18,76 @@
 namespace qlora {
 namespace {
 
+// The scales of the tile's channels (1 KiB) and tokens (1 KiB) lie past the
+// pair slots, DMA'd in the prologue, 0 past the end.
+constexpr int kLdsScales = 2048;
+__device__ __forceinline__ void scales_dma(char* dst, const float* sx, const float* sw, int64_t M, int64_t N, int64_t m0,
+                                           int64_t n0, int w, int lane) {
+  if (w == 0) dma16(make_rsrc(sw, (uint32_t)(N * 4)), dst, (uint32_t)((n0 + 4 * lane) * 4), 0u);
+  if (w == 1) dma16(make_rsrc(sx, (uint32_t)(M * 4)), dst + 1024, (uint32_t)((m0 + 4 * lane) * 4), 0u);
+}
 // Integer sums of the tile to fp32, times both scales (lane layout of
-// store_tile_lds).  Tokens and channels past the end take scale 0.
+// store_tile_lds).
 template <int FI>
-__device__ __forceinline__ void scale_tile(const i32x16_t (&acc)[FI][4], f32x16_t (&out)[FI][4],
-                                           const float* __restrict__ sx, const float* __restrict__ sw, int64_t M,
-                                           int64_t N, int64_t m0, int64_t n0) {
+__device__ __forceinline__ void scale_tile(const i32x16_t (&acc)[FI][4], f32x16_t (&out)[FI][4], const char* scales) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1, lr = lane & 31, h = lane >> 5;
+  const float* sw = reinterpret_cast<const float*>(scales);
+  const float* sx = reinterpret_cast<const float*>(scales + 1024);
   float x[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t m = m0 + 128 * wr + 32 * j + lr;
-    x[j] = m < M ? sx[m] : 0.0f;
-  }
+  for (int j = 0; j < 4; ++j) x[j] = sx[128 * wr + 32 * j + lr];
 #pragma unroll
-  for (int i = 0; i < FI; ++i)
+  for (int i = 0; i < FI; ++i) {
+    f32x4_t v[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t n = n0 + 32 * FI * wc + 32 * i + 8 * q + 4 * h;   // N % 8 == 0
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (n < N) v = *reinterpret_cast<const float4*>(sw + n);
+    for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const f32x4_t*>(sw + 32 * FI * wc + 32 * i + 8 * q + 4 * h);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        out[i][j][4 * q] = (float)acc[i][j][4 * q] * (x[j] * v.x);
-        out[i][j][4 * q + 1] = (float)acc[i][j][4 * q + 1] * (x[j] * v.y);
-        out[i][j][4 * q + 2] = (float)acc[i][j][4 * q + 2] * (x[j] * v.z);
-        out[i][j][4 * q + 3] = (float)acc[i][j][4 * q + 3] * (x[j] * v.w);
+    for (int j = 0; j < 4; ++j) {
+      // through 16 vector registers, back into the accumulator registers that
+      // held the sums: without the moves the compiler keeps the values in
+      // vector registers, which spills
+      float f[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) f[e] = (float)acc[i][j][e] * (x[j] * v[e >> 2][e & 3]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float t;
+        asm volatile("v_accvgpr_write_b32 %0, %1" : "=a"(t) : "v"(f[e]));
+        out[i][j][e] = t;
       }
-      __builtin_amdgcn_sched_barrier(0);   // one quarter's scales at a time
+      __builtin_amdgcn_sched_barrier(0);
     }
+  }
 }
 
-// out += B (s U)^T over the rank, 32 at a time through 64-byte-row tiles, one
+// acc += the chunk at buf (weights at buf, tokens at buf + kOp; the tokens
+// scaled by s as they are read when `raw`).
+template <int FI>
+__device__ __forceinline__ void tail_mul(f32x16_t (&acc)[FI][4], const char* buf, bool raw, float s) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1;
+  const FragOffs fo = frag_offs(lane);
+  const int am64 = wc * 32 * FI * 64, bm64 = wr * 128 * 64;
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    const int o = kk ? fo.o1 : fo.o0;
+    bf16x8_t a[FI], b[4];
+#pragma unroll
+    for (int i = 0; i < FI; ++i) a[i] = rd16(buf + am64 + i * 2048 + o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      b[i] = rd16(buf + kOp + bm64 + i * 2048 + o);
+      if (raw) b[i] = scale_frag(b[i], s);
+    }
+    mfma_block<FI, 4>(acc, a, b);
+  }
+}
+
+// acc += B (s U)^T over the rank, 32 at a time through 64-byte-row tiles, one
 // chunk loaded into registers while the one before is multiplied.
 template <int FI>
 __device__ __forceinline__ void lora_tail(f32x16_t (&acc)[FI][4], const bf16_t* B, const bf16_t* U, int r, float s,
                                           int64_t M, int64_t N, int64_t m0, int64_t n0, char* smem) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1;
-  const FragOffs fo = frag_offs(lane);
-  const int am64 = wc * 32 * FI * 64, bm64 = wr * 128 * 64;
   const int nt = (r + 31) / 32;
   TailRegs R;
   tail_load(R, B, false, N, r, n0, 0, 0, N, U, r, M, m0);
@@ -65,16 +96,7 @@ __device__ __forceinline__ void lora_tail(f32x16_t (&acc)[FI][4], const bf16_t* 
     tail_store(buf, R, false, s);
     if (c + 1 < nt) tail_load(R, B, false, N, r, n0, 32 * (c + 1), 0, N, U, r, M, m0);
     __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int o = kk ? fo.o1 : fo.o0;
-      bf16x8_t a[FI], b[4];
-#pragma unroll
-      for (int i = 0; i < FI; ++i) a[i] = rd16(buf + am64 + i * 2048 + o);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = rd16(buf + kOp + bm64 + i * 2048 + o);
-      mfma_block<FI, 4>(acc, a, b);
-    }
+    tail_mul<FI>(acc, buf, false, s);
   }
 }
 
@@ -82,7 +104,8 @@ __device__ __forceinline__ void lora_tail(f32x16_t (&acc)[FI][4], const bf16_t* 
 // x 256 tokens from channel n_begin on.  part != null: the grid holds the tiles
 // once per split of the contraction, pps pairs each, split 0 with the adapter's
 // term, and their fp32 values go to part + split M N instead of Y.
-template <int FI>
+// TD: the LoRA tail by DMA.
+template <int FI, bool TD>
 __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __restrict__ Wq,
                                                               const float* __restrict__ sw, int64_t N, int64_t ld,
                                                               const int8_t* __restrict__ Xq,
@@ -132,6 +155,8 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
+  const bool tail = r > 0 && split == 0;
+  scales_dma(smem + kLdsPairs, sx, sw, M, N, m0, n0, f.w, lane);
 #pragma unroll
   for (int d = 0; d < 2 * FI + 8; ++d) {
     pair_dma<FI>(smem, f, 0, d);
@@ -156,10 +181,31 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
   // drain the DMAs still in flight (clamped re-loads) before reusing LDS
   QLORA_WAIT(0, 0);
   __builtin_amdgcn_s_barrier();
-
+  // TD: the rank's chunks (32 each, at most four) come into the pair slots
+  // while the sums become fp32
+  if (TD && tail) {
+    TailSrc ts;
+    ts.wr = make_rsrc(B, (uint32_t)(N * r * 2));
+    ts.tr = make_rsrc(U, (uint32_t)(M * r * 2));
+    ts.n0 = n0;
+    ts.m0 = m0;
+    ts.rows = N;
+    ts.r = ts.ld = r;
+    ts.col0 = 0;
+    ts.bt = false;
+    for (int c = 0; c < r / 32; ++c) tail_dma(smem + c * 2 * kOp, ts, c, f.w, lane);
+  }
   f32x16_t out[FI][4];
-  scale_tile<FI>(acc, out, sx, sw, M, N, m0, n0);
-  if (r > 0 && split == 0) lora_tail<FI>(out, B, U, r, s, M, N, m0, n0, smem);
+  scale_tile<FI>(acc, out, smem + kLdsPairs);
+  if (tail) {
+    if constexpr (TD) {
+      QLORA_WAIT(0, 0);
+      __builtin_amdgcn_s_barrier();
+      for (int c = 0; c < r / 32; ++c) tail_mul<FI>(out, smem + c * 2 * kOp, true, s);
+    } else {
+      lora_tail<FI>(out, B, U, r, s, M, N, m0, n0, smem);
+    }
+  }
   if (part != nullptr)
     store_tile_f32<FI>(out, part + (int64_t)split * M * N, N, M, N, m0, n0);
   else
@@ -294,11 +340,14 @@ hipError_t launch_skinny(const I8Gemm& g, hipStream_t st) {
 template <int FI>
 hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, int splits, float* part, hipStream_t st) {
   const int tiles_n = (int)((n_rows + 64 * FI - 1) / (64 * FI)), tiles_m = (int)((g.M + kTile - 1) / kTile);
-  auto* fn = &i8_gemm_kernel<FI>;
-  hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)kLdsPairs);
+  // the rank in whole chunks, U and B within 32-bit byte offsets
+  const bool td = g.r > 0 && g.r % 32 == 0 && g.M * g.r < ((int64_t)1 << 30) && g.N * g.r < ((int64_t)1 << 30);
+  auto* fn = td ? &i8_gemm_kernel<FI, true> : &i8_gemm_kernel<FI, false>;
+  constexpr size_t lds = kLdsPairs + kLdsScales;
+  hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
   if (e != hipSuccess) return e;
   const int npair = (int)(i8_row_bytes(g.K) / 128);
-  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_m * splits), dim3(kThreads), kLdsPairs, st, g.Wq, g.sw, g.N,
+  hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_m * splits), dim3(kThreads), lds, st, g.Wq, g.sw, g.N,
                      i8_row_bytes(g.K), g.Xq, g.sx, g.M, g.U, g.B, g.r, g.s, g.Y, n_begin, tiles_n, tiles_m,
                      (npair + splits - 1) / splits, splits > 1 ? part : nullptr);
   if ((e = hipGetLastError()) != hipSuccess || splits == 1) return e;
