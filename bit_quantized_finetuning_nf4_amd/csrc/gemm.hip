@@ -53,9 +53,6 @@ __device__ __forceinline__ void tr_dma_coords(int q, int lane, int& row, int& co
 // (16-byte chunk c of row m at c ^ ((m >> 2) & 3)).  Q is A [r x C] (QT =
 // false: rows j, read like P) or B [C x r] (QT = true: rows c, read
 // transposed).  Output D[j][m]: a lane holds four consecutive j of one m.
-// DROP: P is drop(P), masked as its fragments are read: a fragment's 16 bytes
-// are eight consecutive columns of one row, one Philox block (rng.h), and no
-// two lanes read the same ones.
 // ---------------------------------------------------------------------------
 template <int RP, bool QT>
 struct RowShape {
@@ -66,12 +63,12 @@ struct RowShape {
   static constexpr int kLoads = 2 + kQDma;                 // all DMA instructions per wave per stage
 };
 
-template <int RP, bool QT, bool DROP>
+template <int RP, bool QT>
 __global__ __launch_bounds__(kThreads, 1) void rskinny_kernel(const bf16_t* __restrict__ P, int64_t M, int64_t C,
                                                               int64_t ldp, int64_t p_gs,
                                                               const bf16_t* __restrict__ Q, int r, int64_t q_gs,
                                                               int stages_per_split, int tiles_m, int ldo,
-                                                              float* __restrict__ part, DropArgs drop) {
+                                                              float* __restrict__ part) {
   using S = RowShape<RP, QT>;
   extern __shared__ __align__(16) char smem[];
   const int tm = blockIdx.x % tiles_m, sp = blockIdx.x / tiles_m, g = blockIdx.y;
@@ -123,13 +120,6 @@ __global__ __launch_bounds__(kThreads, 1) void rskinny_kernel(const bf16_t* __re
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[f][e] = 0.0f;
 
-  [[maybe_unused]] DropKey key;
-  [[maybe_unused]] uint32_t row_block = 0;
-  if constexpr (DROP) {
-    key = drop_key(drop);
-    row_block = (uint32_t)(m0 + 32 * w + lr) * (uint32_t)(C >> 3);
-  }
-
   if (s0 < s1) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) dma(s0 + a, a);
@@ -149,8 +139,6 @@ __global__ __launch_bounds__(kThreads, 1) void rskinny_kernel(const bf16_t* __re
         const int ch = QT ? 2 * kk + h : 2 * h + kk;
         bf16x8_t b = rd16(base + spos(32 * w + lr, ch));
         if (32 * st + 8 * ch >= C) b = bf16x8_t{};   // columns past C (C % 8 == 0)
-        if constexpr (DROP)   // M C < 2^31: block numbers in 32 bits (rows past M: masks of zeros)
-          b = __builtin_bit_cast(bf16x8_t, drop8(__builtin_bit_cast(u32x4_t, b), row_block + (uint32_t)(4 * st + ch), key));
         bf16x8_t a[FJ];
         if constexpr (!QT) {
 #pragma unroll
@@ -181,6 +169,136 @@ __global__ __launch_bounds__(kThreads, 1) void rskinny_kernel(const bf16_t* __re
         const int j = 32 * f + 8 * q + 4 * h;
         if (j < r)
           *reinterpret_cast<float4*>(out + m * ldo + j) =
+              make_float4(acc[f][4 * q], acc[f][4 * q + 1], acc[f][4 * q + 2], acc[f][4 * q + 3]);
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The row contraction of one adapter by whole lines: stages of 64 columns, one
+// 128-byte line of every row of P (a CU keeps about 90 lines in flight, and a
+// request for half a line takes a place like a whole one: with 64-byte rows U
+// of 4096 x 8192 at rank 64 took 26 us).  Rows in the layout of pos128; a ring
+// of four stages.  Q is A [r x C], read like P, or (QT) B [C x r], 64 rows c a
+// stage, read transposed.  DROP: P is drop(P), masked as its fragments are
+// read: a fragment's 16 bytes are eight consecutive columns of one row, one
+// Philox block (rng.h), and no two lanes read the same ones.
+// ---------------------------------------------------------------------------
+constexpr int kWideRing = 4, kWideAhead = kWideRing - 1;
+
+template <int RP>
+struct WideShape {
+  static constexpr int kP = 128 * 128;                     // 16 KiB of P per stage
+  static constexpr int kQ = RP * 128;                      // RP rows x 128 B, or 64 rows x 2 RP B
+  static constexpr int kStage = kP + kQ;
+  static constexpr int kQDma = kQ / 1024 / 4;
+  static constexpr int kLoads = 4 + kQDma;                 // DMA instructions per wave and stage
+};
+
+__device__ __forceinline__ int pos_line(int r, int c) { return r * 128 + 16 * (c ^ ((r >> 1) & 7)); }
+
+template <int RP, bool QT, bool DROP>
+__global__ __launch_bounds__(kThreads, 1) void rwide_kernel(const bf16_t* __restrict__ P, int64_t M, int64_t C,
+                                                            const bf16_t* __restrict__ Q, int r, int stages_per_split,
+                                                            int tiles_m, float* __restrict__ part, DropArgs drop) {
+  using S = WideShape<RP>;
+  extern __shared__ __align__(16) char smem[];
+  const int tm = blockIdx.x % tiles_m, sp = blockIdx.x / tiles_m;
+  const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, h = lane >> 5;
+  const int64_t m0 = (int64_t)tm * 128;
+  const int nst = (int)((C + 63) / 64);
+  const int s0 = sp * stages_per_split, s1 = min(nst, s0 + stages_per_split);   // no split is empty
+  // P rows of this tile only (rows past M read as zero); Q whole
+  const rsrc_t pr = make_rsrc(P + m0 * C, (uint32_t)(min((int64_t)128, M - m0) * C * 2));
+  const rsrc_t qr = make_rsrc(Q, (uint32_t)((int64_t)r * C * 2));
+  uint32_t po[4], qo[S::kQDma];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {   // instruction q of wave w: rows 8 (4 w + q) .. + 7 of P
+    const int row = 8 * (4 * w + q) + (lane >> 3);
+    po[q] = (uint32_t)(row * C * 2 + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+  }
+#pragma unroll
+  for (int q = 0; q < S::kQDma; ++q) {
+    const int gi = S::kQDma * w + q;   // 1 KiB piece of the stage's Q tile
+    if constexpr (!QT) {               // rows j of A (past r: never stored)
+      const int row = 8 * gi + (lane >> 3);
+      qo[q] = (uint32_t)(row * C * 2 + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+    } else {                           // rows c of B
+      int row, col;
+      tr_dma_coords<2 * RP>(gi, lane, row, col);
+      qo[q] = (uint32_t)(row * r * 2 + col * 2);
+    }
+  }
+  auto dma = [&](int st, int slot) __attribute__((always_inline)) {
+    const int ss = min(st, s1 - 1);    // past the split: re-load its last stage (never read)
+    char* base = smem + slot * S::kStage;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) dma16(pr, base + (4 * w + q) * 1024, po[q], (uint32_t)ss * 128u);
+#pragma unroll
+    for (int q = 0; q < S::kQDma; ++q)
+      dma16(qr, base + S::kP + (S::kQDma * w + q) * 1024, qo[q],
+            QT ? (uint32_t)ss * 64u * (uint32_t)r * 2u : (uint32_t)ss * 128u);
+  };
+  constexpr int FJ = RP / 32;
+  f32x16_t acc[FJ];
+#pragma unroll
+  for (int f = 0; f < FJ; ++f)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[f][e] = 0.0f;
+  [[maybe_unused]] DropKey key;
+  [[maybe_unused]] uint32_t row_block = 0;   // M C < 2^31: block numbers in 32 bits
+  if constexpr (DROP) {
+    key = drop_key(drop);
+    row_block = (uint32_t)(m0 + 32 * w + lr) * (uint32_t)(C >> 3);
+  }
+#pragma unroll
+  for (int a = 0; a < kWideAhead; ++a) dma(s0 + a, a);
+  int slot = 0;
+  for (int st = s0; st < s1; ++st) {
+    QLORA_WAIT((kWideAhead - 1) * S::kLoads, 0);
+    __builtin_amdgcn_s_barrier();
+    dma(st + kWideAhead, slot == 0 ? kWideRing - 1 : slot - 1);   // the slot stage st - 1 used
+    const char* base = smem + slot * S::kStage;
+    const bool ragged = 64 * (st + 1) > C;   // columns past C (C % 8 == 0)
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const int ch = 2 * kk + h;   // both operands: columns 16 kk + 8 h ..
+      bf16x8_t b = rd16(base + pos_line(32 * w + lr, ch));
+      bf16x8_t a[FJ];
+      if constexpr (!QT) {
+#pragma unroll
+        for (int f = 0; f < FJ; ++f) a[f] = rd16(base + S::kP + pos_line(32 * f + lr, ch));
+      } else {
+        // transposed reads in asm blocks (see tr_read2)
+        constexpr int O = 4 * 2 * RP;
+        const char* qb = base + S::kP + kk * 16 * 2 * RP;
+#pragma unroll
+        for (int f = 0; f < FJ; f += 2) tr_read2<O, O>(qb + tr_off<2 * RP>(f), qb + tr_off<2 * RP>(f + 1), a[f], a[f + 1]);
+      }
+      if (ragged && 64 * st + 8 * ch >= C) {   // the next row's: neither operand may bring its infinities
+        b = bf16x8_t{};
+#pragma unroll
+        for (int f = 0; f < FJ; ++f) a[f] = bf16x8_t{};
+      }
+      if constexpr (DROP)
+        b = __builtin_bit_cast(bf16x8_t, drop8(__builtin_bit_cast(u32x4_t, b), row_block + (uint32_t)(8 * st + ch), key));
+#pragma unroll
+      for (int f = 0; f < FJ; ++f) acc[f] = mfma32x32x16(a[f], b, acc[f]);
+    }
+    slot = slot == kWideRing - 1 ? 0 : slot + 1;
+  }
+  QLORA_WAIT(0, 0);
+  // D[j][m]: lane (lr, h) holds m = m0 + 32 w + lr, j = 32 f + 8 q + 4 h + 0..3
+  float* out = part + (int64_t)sp * M * r;
+  const int64_t m = m0 + 32 * w + lr;
+  if (m < M) {
+#pragma unroll
+    for (int f = 0; f < FJ; ++f)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int j = 32 * f + 8 * q + 4 * h;
+        if (j < r)
+          *reinterpret_cast<float4*>(out + m * r + j) =
               make_float4(acc[f][4 * q], acc[f][4 * q + 1], acc[f][4 * q + 2], acc[f][4 * q + 3]);
       }
   }
@@ -484,22 +602,16 @@ struct RowArgs {
   int G, ldo;
 };
 
-template <int RP, bool QT, bool DROP>
-hipError_t row_partials(const RowArgs& a, const Split& sp, const DropArgs& drop, float* part, hipStream_t st) {
-  auto* fn = &rskinny_kernel<RP, QT, DROP>;
+template <int RP, bool QT>
+hipError_t run_rows(const RowArgs& a, float* part, float scale, bf16_t* out, bf16_t* out2, hipStream_t st) {
+  const Split sp = split_for((a.M + 127) / 128, a.C, 256);
+  auto* fn = &rskinny_kernel<RP, QT>;
   const size_t lds = (size_t)kRing * RowShape<RP, QT>::kStage;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits, a.G), dim3(kThreads), lds, st, a.P, a.M, a.C, a.ldp, a.p_gs, a.Q,
-                     a.r, a.q_gs, sp.sps, sp.tiles, a.ldo, part, drop);
-  return hipGetLastError();
-}
-
-template <int RP, bool QT>
-hipError_t run_rows(const RowArgs& a, float* part, float scale, bf16_t* out, bf16_t* out2, hipStream_t st) {
-  const Split sp = split_for((a.M + 127) / 128, a.C, 256);
-  const hipError_t e = row_partials<RP, QT, false>(a, sp, DropArgs{}, part, st);
-  if (e != hipSuccess) return e;
+                     a.r, a.q_gs, sp.sps, sp.tiles, a.ldo, part);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   return reduce(part, sp.splits, a.M * a.ldo, scale, nullptr, out, out2, st);
 }
 
@@ -591,28 +703,27 @@ hipError_t launch_grads(const bf16_t* Gm, const bf16_t* X, const bf16_t* dY, int
 }
 
 // Splits of the products of an adapter under dropout and of the 8-bit linear:
-// four stages or more, and the count whose rounds x stages, with 6 stages to
-// fill the ring and one for each split's partials, are least.  dA of 2048 x
-// 4096 at rank 64: 64 workgroups took 26 us, 256 take 13 us.  Masked dA waits
-// for its LDS passes as much as for its loads, so two workgroups share a CU
-// (512); U and G are bound by the CU's loads, and one does (U of 4096 x 8192
-// under the mask: 25.5 us on 256 workgroups, 29.6 on 512).  No device query, so
-// that the workspace does not depend on the device.
+// the count whose rounds x columns (or tokens) of a split, with 160 to fill the
+// ring and 32 for each split's partials, are least.  dA of 2048 x 4096 at rank
+// 64: 64 workgroups took 26 us, 256 take 12 us.  Masked dA waits for its LDS
+// passes as much as for its loads, so two workgroups share a CU (512); U and G
+// are bound by the CU's loads, and one does.  No device query, so that the
+// workspace does not depend on the device.
 namespace {
 
-Split fill_split(int64_t tiles, int64_t contraction, int slots) {
-  const int nst = (int)((contraction + 31) / 32);
+Split fill_split(int64_t tiles, int64_t contraction, int stage, int min_stages, int slots) {
+  const int nst = (int)((contraction + stage - 1) / stage);
   Split best{(int)tiles, nst, 1};
   int64_t best_cost = INT64_MAX;
-  for (int want = 1; want <= 32 && (want == 1 || want * 4 <= nst); ++want) {
+  for (int want = 1; want <= 32 && (want == 1 || want * min_stages <= nst); ++want) {
     const int sps = (nst + want - 1) / want, splits = (nst + sps - 1) / sps;
-    const int64_t cost = (tiles * splits + slots - 1) / slots * sps + 6 + splits;
+    const int64_t cost = (tiles * splits + slots - 1) / slots * sps * stage + 160 + 32 * splits;
     if (cost < best_cost) best_cost = cost, best = Split{(int)tiles, sps, splits};
   }
   return best;
 }
-Split rows_split(int64_t M, int64_t C) { return fill_split((M + 127) / 128, C, 256); }
-Split cols_split(int64_t C, int64_t M) { return fill_split((C + 127) / 128, M, 512); }
+Split rows_split(int64_t M, int64_t C) { return fill_split((M + 127) / 128, C, 64, 2, 256); }
+Split cols_split(int64_t C, int64_t M) { return fill_split((C + 127) / 128, M, 32, 4, 512); }
 size_t part_bytes(const Split& s, int64_t n) { return (size_t)s.splits * (size_t)n * sizeof(float); }
 
 }  // namespace
@@ -638,6 +749,22 @@ __global__ __launch_bounds__(256) void u_rows_kernel(const bf16_t* __restrict__ 
 
 }  // namespace
 
+namespace {
+
+template <int RP, bool QT, bool DROP>
+hipError_t wide_partials(const bf16_t* P, int64_t M, int64_t C, const bf16_t* Q, int r, const DropArgs& drop,
+                         const Split& sp, float* part, hipStream_t st) {
+  auto* fn = &rwide_kernel<RP, QT, DROP>;
+  const size_t lds = (size_t)kWideRing * WideShape<RP>::kStage;
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits), dim3(kThreads), lds, st, P, M, C, Q, r, sp.sps, sp.tiles, part,
+                     drop);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
                            float* part, bf16_t* out, hipStream_t st) {
   if (u_rows_ok(M, r)) {
@@ -645,23 +772,21 @@ hipError_t launch_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t 
                        dim3(256), 0, st, X, M, K, A, r, out, drop ? *drop : DropArgs{});
     return hipGetLastError();
   }
-  const RowArgs a{X, M, K, K, 0, A, r, 0, 1, r};
   const Split sp = rows_split(M, K);
   const DropArgs d = drop ? *drop : DropArgs{};
-  const hipError_t e = drop ? (r <= 64 ? row_partials<64, false, true>(a, sp, d, part, st)
-                                       : row_partials<128, false, true>(a, sp, d, part, st))
-                            : (r <= 64 ? row_partials<64, false, false>(a, sp, d, part, st)
-                                       : row_partials<128, false, false>(a, sp, d, part, st));
+  const hipError_t e = drop ? (r <= 64 ? wide_partials<64, false, true>(X, M, K, A, r, d, sp, part, st)
+                                       : wide_partials<128, false, true>(X, M, K, A, r, d, sp, part, st))
+                            : (r <= 64 ? wide_partials<64, false, false>(X, M, K, A, r, d, sp, part, st)
+                                       : wide_partials<128, false, false>(X, M, K, A, r, d, sp, part, st));
   if (e != hipSuccess) return e;
   return reduce(part, sp.splits, M * r, drop ? drop->scale : 1.0f, nullptr, out, nullptr, st);
 }
 
 hipError_t launch_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* out,
                             hipStream_t st) {
-  const RowArgs a{dY, M, N, N, 0, B, r, 0, 1, r};
   const Split sp = rows_split(M, N);
-  const hipError_t e = r <= 64 ? row_partials<64, true, false>(a, sp, DropArgs{}, part, st)
-                               : row_partials<128, true, false>(a, sp, DropArgs{}, part, st);
+  const hipError_t e = r <= 64 ? wide_partials<64, true, false>(dY, M, N, B, r, DropArgs{}, sp, part, st)
+                               : wide_partials<128, true, false>(dY, M, N, B, r, DropArgs{}, sp, part, st);
   if (e != hipSuccess) return e;
   const int64_t n = M * r;
   hipLaunchKernelGGL(reduce_parts_kernel, dim3((unsigned)((n / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
