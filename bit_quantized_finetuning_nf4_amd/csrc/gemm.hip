@@ -179,26 +179,29 @@ __global__ __launch_bounds__(kThreads, 1) void rskinny_kernel(const bf16_t* __re
 // 128-byte line of every row of P (a CU keeps about 90 lines in flight, and a
 // request for half a line takes a place like a whole one: with 64-byte rows U
 // of 4096 x 8192 at rank 64 took 26 us).  Rows in the layout of pos128; a ring
-// of four stages.  Q is A [r x C], read like P, or (QT) B [C x r], 64 rows c a
+// of four stages.  A fifth wave issues the DMAs: their issue stalls while the
+// lines in flight are at their limit, and would hold up the wave's masks and
+// products.  Q is A [r x C], read like P, or (QT) B [C x r], 64 rows c a
 // stage, read transposed.  DROP: P is drop(P), masked as its fragments are
 // read: a fragment's 16 bytes are eight consecutive columns of one row, one
 // Philox block (rng.h), and no two lanes read the same ones.
 // ---------------------------------------------------------------------------
-constexpr int kWideRing = 4, kWideAhead = kWideRing - 1;
+constexpr int kWideRing = 4, kWideAhead = kWideRing - 1, kWideThreads = kThreads + 64;
 
 template <int RP>
 struct WideShape {
   static constexpr int kP = 128 * 128;                     // 16 KiB of P per stage
   static constexpr int kQ = RP * 128;                      // RP rows x 128 B, or 64 rows x 2 RP B
   static constexpr int kStage = kP + kQ;
-  static constexpr int kQDma = kQ / 1024 / 4;
-  static constexpr int kLoads = 4 + kQDma;                 // DMA instructions per wave and stage
+  static constexpr int kQDma = kQ / 1024;                  // DMA instructions per stage
+  // all but two stages have landed (the counter holds 63 at most)
+  static constexpr int kWait = (kWideAhead - 1) * (16 + kQDma) < 63 ? (kWideAhead - 1) * (16 + kQDma) : 63;
 };
 
 __device__ __forceinline__ int pos_line(int r, int c) { return r * 128 + 16 * (c ^ ((r >> 1) & 7)); }
 
 template <int RP, bool QT, bool DROP>
-__global__ __launch_bounds__(kThreads, 1) void rwide_kernel(const bf16_t* __restrict__ P, int64_t M, int64_t C,
+__global__ __launch_bounds__(kWideThreads, 1) void rwide_kernel(const bf16_t* __restrict__ P, int64_t M, int64_t C,
                                                             const bf16_t* __restrict__ Q, int r, int stages_per_split,
                                                             int tiles_m, float* __restrict__ part, DropArgs drop) {
   using S = WideShape<RP>;
@@ -211,34 +214,45 @@ __global__ __launch_bounds__(kThreads, 1) void rwide_kernel(const bf16_t* __rest
   // P rows of this tile only (rows past M read as zero); Q whole
   const rsrc_t pr = make_rsrc(P + m0 * C, (uint32_t)(min((int64_t)128, M - m0) * C * 2));
   const rsrc_t qr = make_rsrc(Q, (uint32_t)((int64_t)r * C * 2));
-  uint32_t po[4], qo[S::kQDma];
+  if (w == 4) {   // the wave that brings the stages
+    uint32_t po[16], qo[S::kQDma];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {   // instruction q of wave w: rows 8 (4 w + q) .. + 7 of P
-    const int row = 8 * (4 * w + q) + (lane >> 3);
-    po[q] = (uint32_t)(row * C * 2 + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
-  }
-#pragma unroll
-  for (int q = 0; q < S::kQDma; ++q) {
-    const int gi = S::kQDma * w + q;   // 1 KiB piece of the stage's Q tile
-    if constexpr (!QT) {               // rows j of A (past r: never stored)
-      const int row = 8 * gi + (lane >> 3);
-      qo[q] = (uint32_t)(row * C * 2 + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
-    } else {                           // rows c of B
-      int row, col;
-      tr_dma_coords<2 * RP>(gi, lane, row, col);
-      qo[q] = (uint32_t)(row * r * 2 + col * 2);
+    for (int q = 0; q < 16; ++q) {   // rows 8 q .. + 7 of P
+      const int row = 8 * q + (lane >> 3);
+      po[q] = (uint32_t)(row * C * 2 + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
     }
+#pragma unroll
+    for (int q = 0; q < S::kQDma; ++q) {   // 1 KiB pieces of the stage's Q tile
+      if constexpr (!QT) {                 // rows j of A (past r: never stored)
+        const int row = 8 * q + (lane >> 3);
+        qo[q] = (uint32_t)(row * C * 2 + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+      } else {                             // rows c of B
+        int row, col;
+        tr_dma_coords<2 * RP>(q, lane, row, col);
+        qo[q] = (uint32_t)(row * r * 2 + col * 2);
+      }
+    }
+    auto dma = [&](int st, int slot) __attribute__((always_inline)) {
+      const int ss = min(st, s1 - 1);    // past the split: re-load its last stage (never read)
+      char* base = smem + slot * S::kStage;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) dma16(pr, base + q * 1024, po[q], (uint32_t)ss * 128u);
+#pragma unroll
+      for (int q = 0; q < S::kQDma; ++q)
+        dma16(qr, base + S::kP + q * 1024, qo[q], QT ? (uint32_t)ss * 64u * (uint32_t)r * 2u : (uint32_t)ss * 128u);
+    };
+#pragma unroll
+    for (int a = 0; a < kWideAhead; ++a) dma(s0 + a, a);
+    int slot = kWideRing - 1;
+    for (int st = s0; st < s1; ++st) {
+      QLORA_WAIT(S::kWait, 0);
+      __builtin_amdgcn_s_barrier();   // stage st has landed, and stage st - 1 has been read
+      dma(st + kWideAhead, slot);     // the slot stage st - 1 used
+      slot = slot == kWideRing - 1 ? 0 : slot + 1;
+    }
+    QLORA_WAIT(0, 0);
+    return;
   }
-  auto dma = [&](int st, int slot) __attribute__((always_inline)) {
-    const int ss = min(st, s1 - 1);    // past the split: re-load its last stage (never read)
-    char* base = smem + slot * S::kStage;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) dma16(pr, base + (4 * w + q) * 1024, po[q], (uint32_t)ss * 128u);
-#pragma unroll
-    for (int q = 0; q < S::kQDma; ++q)
-      dma16(qr, base + S::kP + (S::kQDma * w + q) * 1024, qo[q],
-            QT ? (uint32_t)ss * 64u * (uint32_t)r * 2u : (uint32_t)ss * 128u);
-  };
   constexpr int FJ = RP / 32;
   f32x16_t acc[FJ];
 #pragma unroll
@@ -251,13 +265,10 @@ __global__ __launch_bounds__(kThreads, 1) void rwide_kernel(const bf16_t* __rest
     key = drop_key(drop);
     row_block = (uint32_t)(m0 + 32 * w + lr) * (uint32_t)(C >> 3);
   }
-#pragma unroll
-  for (int a = 0; a < kWideAhead; ++a) dma(s0 + a, a);
   int slot = 0;
   for (int st = s0; st < s1; ++st) {
-    QLORA_WAIT((kWideAhead - 1) * S::kLoads, 0);
+    QLORA_WAIT(63, 0);   // this wave's reads of stage st - 1
     __builtin_amdgcn_s_barrier();
-    dma(st + kWideAhead, slot == 0 ? kWideRing - 1 : slot - 1);   // the slot stage st - 1 used
     const char* base = smem + slot * S::kStage;
     const bool ragged = 64 * (st + 1) > C;   // columns past C (C % 8 == 0)
 #pragma unroll
@@ -287,7 +298,6 @@ __global__ __launch_bounds__(kThreads, 1) void rwide_kernel(const bf16_t* __rest
     }
     slot = slot == kWideRing - 1 ? 0 : slot + 1;
   }
-  QLORA_WAIT(0, 0);
   // D[j][m]: lane (lr, h) holds m = m0 + 32 w + lr, j = 32 f + 8 q + 4 h + 0..3
   float* out = part + (int64_t)sp * M * r;
   const int64_t m = m0 + 32 * w + lr;
@@ -758,8 +768,8 @@ hipError_t wide_partials(const bf16_t* P, int64_t M, int64_t C, const bf16_t* Q,
   const size_t lds = (size_t)kWideRing * WideShape<RP>::kStage;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits), dim3(kThreads), lds, st, P, M, C, Q, r, sp.sps, sp.tiles, part,
-                     drop);
+  hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits), dim3(kWideThreads), lds, st, P, M, C, Q, r, sp.sps, sp.tiles,
+                     part, drop);
   return hipGetLastError();
 }
 
