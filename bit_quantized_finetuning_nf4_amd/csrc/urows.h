@@ -26,25 +26,41 @@ __device__ __forceinline__ void u_rows(const bf16_t* __restrict__ X, int64_t M, 
   float sum[kURowTokens];
 #pragma unroll
   for (int i = 0; i < kURowTokens; ++i) sum[i] = 0.0f;
-  for (int g = t; g < groups; g += 256) {
-    const uint4 a = reinterpret_cast<const uint4*>(A + (int64_t)j * K)[g];
-    const float a0 = bf2f(a.x & 0xFFFFu), a1 = bf2f(a.x >> 16), a2 = bf2f(a.y & 0xFFFFu), a3 = bf2f(a.y >> 16),
-                a4 = bf2f(a.z & 0xFFFFu), a5 = bf2f(a.z >> 16), a6 = bf2f(a.w & 0xFFFFu), a7 = bf2f(a.w >> 16);
+  // two groups of columns a turn, all their loads issued together
+  for (int g0 = t; g0 < groups; g0 += 512) {
+    uint4 a[2];
+    u32x4_t x[2][kURowTokens];
 #pragma unroll
-    for (int i = 0; i < kURowTokens; ++i)
-      if (i < mt) {
-        u32x4_t x = *reinterpret_cast<const u32x4_t*>(X + (m0 + i) * K + 8 * g);
-        if constexpr (DROP) x = drop8(x, (uint32_t)(m0 + i) * (uint32_t)groups + (uint32_t)g, key);   // M K < 2^31
-        float v = sum[i];
-        v = fmaf(a0, bf2f(x.x & 0xFFFFu), v);
-        v = fmaf(a1, bf2f(x.x >> 16), v);
-        v = fmaf(a2, bf2f(x.y & 0xFFFFu), v);
-        v = fmaf(a3, bf2f(x.y >> 16), v);
-        v = fmaf(a4, bf2f(x.z & 0xFFFFu), v);
-        v = fmaf(a5, bf2f(x.z >> 16), v);
-        v = fmaf(a6, bf2f(x.w & 0xFFFFu), v);
-        sum[i] = fmaf(a7, bf2f(x.w >> 16), v);
-      }
+    for (int u = 0; u < 2; ++u) {
+      const int g = min(g0 + 256 * u, groups - 1);
+      a[u] = reinterpret_cast<const uint4*>(A + (int64_t)j * K)[g];
+#pragma unroll
+      for (int i = 0; i < kURowTokens; ++i)
+        x[u][i] = *reinterpret_cast<const u32x4_t*>(X + min((int64_t)m0 + i, M - 1) * K + 8 * g);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int g = g0 + 256 * u;
+      if (g >= groups) break;
+      const float a0 = bf2f(a[u].x & 0xFFFFu), a1 = bf2f(a[u].x >> 16), a2 = bf2f(a[u].y & 0xFFFFu),
+                  a3 = bf2f(a[u].y >> 16), a4 = bf2f(a[u].z & 0xFFFFu), a5 = bf2f(a[u].z >> 16),
+                  a6 = bf2f(a[u].w & 0xFFFFu), a7 = bf2f(a[u].w >> 16);
+#pragma unroll
+      for (int i = 0; i < kURowTokens; ++i)
+        if (i < mt) {
+          u32x4_t v = x[u][i];
+          if constexpr (DROP) v = drop8(v, (uint32_t)(m0 + i) * (uint32_t)groups + (uint32_t)g, key);   // M K < 2^31
+          float y = sum[i];
+          y = fmaf(a0, bf2f(v.x & 0xFFFFu), y);
+          y = fmaf(a1, bf2f(v.x >> 16), y);
+          y = fmaf(a2, bf2f(v.y & 0xFFFFu), y);
+          y = fmaf(a3, bf2f(v.y >> 16), y);
+          y = fmaf(a4, bf2f(v.z & 0xFFFFu), y);
+          y = fmaf(a5, bf2f(v.z >> 16), y);
+          y = fmaf(a6, bf2f(v.w & 0xFFFFu), y);
+          sum[i] = fmaf(a7, bf2f(v.w >> 16), y);
+        }
+    }
   }
 #pragma unroll
   for (int i = 0; i < kURowTokens; ++i)
