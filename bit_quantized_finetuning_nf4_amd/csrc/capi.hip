@@ -726,7 +726,7 @@ qlora_status qlora_linear_bwd(const qlora_nf4_weight* W, const uint16_t* X, cons
 qlora_status qlora_dropout(const uint16_t* x, int64_t n, const qlora_drop* drop, uint16_t* y, void* stream) {
   if (!x || !y || !drop) return QLORA_E_NULL;
   if (!aligned16(x) || !aligned16(y)) return QLORA_E_ALIGN;
-  if (n <= 0 || n > ((int64_t)1 << 40)) return QLORA_E_SHAPE;
+  if (n <= 0 || n > ((int64_t)1 << 36)) return QLORA_E_SHAPE;   // the launch's thread count below 2^32
   DropArgs d{};
   bool active;
   const qlora_status st = check_drop(drop, &d, &active);

@@ -554,7 +554,8 @@ typedef struct {
 } qlora_drop;
 
 /* y = drop(x) over n bf16 values, rounded once; y may be x.  The gradient is
- * the same call on dy.  QLORA_E_UNSUPPORTED for p outside [0, 1). */
+ * the same call on dy.  0 < n <= 2^36; QLORA_E_UNSUPPORTED for p outside
+ * [0, 1). */
 qlora_status qlora_dropout(const uint16_t* x, int64_t n, const qlora_drop* drop, uint16_t* y, void* stream);
 
 /* qlora_linear_fwd with the adapter under dropout:

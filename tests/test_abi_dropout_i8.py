@@ -28,7 +28,7 @@ def test_dropout(L):
     f = lambda x=P[0], n=64, drop=d, y=P[1]: L.qlora_dropout(x, n, ref(drop), y, None)
     assert f(x=None) == NULL and f(y=None) == NULL and f(drop=None) == NULL
     assert f(x=ODD) == ALIGN and f(y=ODD) == ALIGN
-    assert f(n=0) == SHAPE and f(n=-1) == SHAPE and f(n=(1 << 40) + 1) == SHAPE
+    assert f(n=0) == SHAPE and f(n=-1) == SHAPE and f(n=(1 << 36) + 1) == SHAPE
     for p in (-1e-9, 1.0, 7.0, math.nan, math.inf):
         assert f(drop=DropDesc(p, 1, 2, None)) == UNSUPPORTED
     assert f(drop=DropDesc(0.1, 1, 2, 0x10004)) == ALIGN
