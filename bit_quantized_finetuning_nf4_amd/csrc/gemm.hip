@@ -343,18 +343,16 @@ struct ColShape {
   static constexpr int kAhead = kRing - 1;
 };
 
+// Workgroup `block` of group g (of `groups`).
 template <int RP, bool DB, int PARTS, bool DROP>
-__global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __restrict__ Big, int64_t M, int64_t C,
-                                                              int64_t ldb, int64_t big_gs,
-                                                              const bf16_t* __restrict__ Sm, int r, int lds,
-                                                              int64_t sm_gs, int stages_per_split, int tiles_c,
-                                                              float* __restrict__ part,
-                                                              int64_t sm_part, DropArgs drop) {
+__device__ __forceinline__ void cskinny(int block, int g, int groups, char* smem, const bf16_t* __restrict__ Big, int64_t M,
+                                        int64_t C, int64_t ldb, int64_t big_gs, const bf16_t* __restrict__ Sm, int r,
+                                        int lds, int64_t sm_gs, int stages_per_split, int tiles_c,
+                                        float* __restrict__ part, int64_t sm_part, const DropArgs& drop) {
   static_assert(PARTS == 1 || (PARTS == 3 && !DB && RP <= 128), "three-part rank side: dA of one adapter");
   using S = ColShape<RP, PARTS>;
   constexpr int kRing = S::kRing, kAhead = S::kAhead;
-  extern __shared__ __align__(16) char smem[];
-  const int tc = blockIdx.x % tiles_c, sp = blockIdx.x / tiles_c, g = blockIdx.y;
+  const int tc = block % tiles_c, sp = block / tiles_c;
   const int t = threadIdx.x, w = t >> 6, lane = t & 63, lr = lane & 31, h = lane >> 5;
   const int64_t c0 = (int64_t)tc * 128;
   const int nst = (int)((M + 31) / 32);
@@ -477,7 +475,7 @@ __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __re
     QLORA_WAIT(0, 0);
   }
   // the split's partial holds all groups' outputs, group g at g C r
-  float* out = part + ((int64_t)sp * gridDim.y + g) * C * r;
+  float* out = part + ((int64_t)sp * groups + g) * C * r;
 #pragma unroll
   for (int f = 0; f < FJ; ++f)
 #pragma unroll
@@ -498,18 +496,57 @@ __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __re
     }
 }
 
+template <int RP, bool DB>
+__global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __restrict__ Big, int64_t M, int64_t C,
+                                                              int64_t ldb, int64_t big_gs,
+                                                              const bf16_t* __restrict__ Sm, int r, int lds,
+                                                              int64_t sm_gs, int stages_per_split, int tiles_c,
+                                                              float* __restrict__ part) {
+  extern __shared__ __align__(16) char smem[];
+  cskinny<RP, DB, 1, false>(blockIdx.x, blockIdx.y, gridDim.y, smem, Big, M, C, ldb, big_gs, Sm, r, lds, sm_gs,
+                            stages_per_split, tiles_c, part, 0, DropArgs{});
+}
+
+// Both gradients of one adapter in one launch, dA's workgroups first: apart
+// they leave the card half idle at their starts and ends (2048 x 4096 x 4096
+// at rank 64: 12.5 and 7.5 us).
+struct GradArgs {
+  const bf16_t *X, *dY, *G3, *U;
+  int64_t M, N, K;
+  int r, sps_a, tiles_a, blocks_a, sps_b, tiles_b;
+  float *part_a, *part_b;
+  DropArgs drop;
+};
+template <int RP, bool DROP>
+__global__ __launch_bounds__(kThreads, 1) void adapter_grads_kernel(GradArgs p) {
+  extern __shared__ __align__(16) char smem[];
+  const int id = blockIdx.x;
+  if (id < p.blocks_a)
+    cskinny<RP, false, 3, DROP>(id, 0, 1, smem, p.X, p.M, p.K, p.K, 0, p.G3, p.r, p.r, 0, p.sps_a, p.tiles_a, p.part_a,
+                                p.M * p.r, p.drop);
+  else
+    cskinny<RP, true, 1, false>(id - p.blocks_a, 0, 1, smem, p.dY, p.M, p.N, p.N, 0, p.U, p.r, p.r, 0, p.sps_b,
+                                p.tiles_b, p.part_b, 0, p.drop);
+}
+
 // Elements i .. i + 3 of the splits' partials, summed in split order, times
 // scale; the loads of eight splits are issued together.
 __device__ __forceinline__ float4 sum_splits(const float* __restrict__ part, int splits, int64_t n, int64_t i,
                                              float scale) {
   float4 acc = *reinterpret_cast<const float4*>(part + i);
-#pragma unroll 8
-  for (int sp = 1; sp < splits; ++sp) {
-    const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)sp * n + i);
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
+  for (int s0 = 1; s0 < splits; s0 += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      v[k] = *reinterpret_cast<const float4*>(part + (int64_t)min(s0 + k, splits - 1) * n + i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool in = s0 + k < splits;   // selects, not branches: a branch would sink its load
+      acc.x = in ? acc.x + v[k].x : acc.x;
+      acc.y = in ? acc.y + v[k].y : acc.y;
+      acc.z = in ? acc.z + v[k].z : acc.z;
+      acc.w = in ? acc.w + v[k].w : acc.w;
+    }
   }
   return make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
 }
@@ -639,22 +676,17 @@ struct ColArgs {
 
 // The token-contraction product's partials (no reduction); *splits gets
 // their count.
-template <int RP, bool DB, int PARTS = 1, bool DROP = false>
-hipError_t col_partials(const ColArgs& a, const Split& sp, float* part, hipStream_t st, int64_t sm_part = 0,
-                        const DropArgs& drop = DropArgs{}) {
-  auto* fn = &cskinny_kernel<RP, DB, PARTS, DROP>;
-  const size_t lds = (size_t)ColShape<RP, PARTS>::kRing * ColShape<RP, PARTS>::kStage;
-  hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits, a.G), dim3(kThreads), lds, st, a.Big, a.M, a.C, a.ldb,
-                     a.big_gs, a.Sm, a.r, a.lds, a.sm_gs, sp.sps, sp.tiles, part, sm_part, drop);
-  return hipGetLastError();
-}
 template <int RP, bool DB>
 hipError_t run_cols(const ColArgs& a, float* part, int* splits, hipStream_t st) {
   const Split sp = split_for((a.C + 127) / 128, a.M, 256);
+  auto* fn = &cskinny_kernel<RP, DB>;
+  const size_t lds = (size_t)kRing * ColShape<RP, 1>::kStage;
+  hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits, a.G), dim3(kThreads), lds, st, a.Big, a.M, a.C, a.ldb,
+                     a.big_gs, a.Sm, a.r, a.lds, a.sm_gs, sp.sps, sp.tiles, part);
   *splits = sp.splits;
-  return col_partials<RP, DB>(a, sp, part, st);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -804,22 +836,29 @@ hipError_t launch_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_
   return hipGetLastError();
 }
 
+namespace {
+
+template <int RP>
+constexpr int grads_lds() {
+  return std::max(ColShape<RP, 3>::kRing * ColShape<RP, 3>::kStage, ColShape<RP, 1>::kRing * ColShape<RP, 1>::kStage);
+}
+
+}  // namespace
+
 hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t* dY, const bf16_t* U, int64_t M,
                                 int64_t N, int64_t K, int r, const DropArgs* drop, float* part, float* dA, float* dB,
                                 float scale, hipStream_t st) {
-  const ColArgs a{X, M, K, K, 0, G3, r, r, 0, 1};
   const Split sa = cols_split(K, M), sb = cols_split(N, M);
-  const DropArgs d = drop ? *drop : DropArgs{};
-  hipError_t e = drop ? (r <= 64 ? col_partials<64, false, 3, true>(a, sa, part, st, M * r, d)
-                                 : col_partials<128, false, 3, true>(a, sa, part, st, M * r, d))
-                      : (r <= 64 ? col_partials<64, false, 3>(a, sa, part, st, M * r)
-                                 : col_partials<128, false, 3>(a, sa, part, st, M * r));
-  if (e != hipSuccess) return e;
   const int64_t na = (int64_t)r * K, nb = N * r;
   float* part_b = part + (part_bytes(sa, na) + 255) / 256 * 256 / sizeof(float);
-  const ColArgs b{dY, M, N, N, 0, U, r, r, 0, 1};
-  e = r <= 64 ? col_partials<64, true>(b, sb, part_b, st) : col_partials<128, true>(b, sb, part_b, st);
+  const GradArgs p{X, dY, G3, U, M, N, K, r, sa.sps, sa.tiles, sa.tiles * sa.splits, sb.sps, sb.tiles, part, part_b,
+                   drop ? *drop : DropArgs{}};
+  auto* fn = r <= 64 ? (drop ? &adapter_grads_kernel<64, true> : &adapter_grads_kernel<64, false>)
+                     : (drop ? &adapter_grads_kernel<128, true> : &adapter_grads_kernel<128, false>);
+  const int lds = r <= 64 ? grads_lds<64>() : grads_lds<128>();
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
   if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(fn, dim3(p.blocks_a + sb.tiles * sb.splits), dim3(kThreads), lds, st, p);
   hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(((na + nb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
                      part, sa.splits, na, dA, part_b, sb.splits, nb, dB, drop ? scale * drop->scale : scale, scale);
   return hipGetLastError();
