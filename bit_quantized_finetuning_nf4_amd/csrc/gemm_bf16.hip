@@ -321,7 +321,10 @@ hipError_t launch_fi(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, in
                      int64_t n_rows, hipStream_t st, const DropArgs* drop, int splits = 1, float* part = nullptr) {
   const int tiles_n = (int)((n_rows + 64 * FI - 1) / (64 * FI));
   const int tiles_m = (int)((M + kTile - 1) / kTile);
-  const bool td = tail_by_dma(N, M, r, ldu, gn, n_begin, tiles_n, 64 * FI);
+  // masked_tail takes 1, 2 or 4 chunks: the fourth of rank 96 is zeroed through
+  // registers (by DMA its tokens would be the next rows', whose infinities times
+  // the weight side's zeros are NaN)
+  const bool td = tail_by_dma(N, M, r, ldu, gn, n_begin, tiles_n, 64 * FI) && !(drop && r == 96);
   auto* fn = drop ? (td ? &bf16_fwd_kernel<FI, true, true> : &bf16_fwd_kernel<FI, false, true>)
                   : (td ? &bf16_fwd_kernel<FI, true, false> : &bf16_fwd_kernel<FI, false, false>);
   const size_t lds = td && !drop ? kLdsDense : kLdsPairs;

@@ -100,3 +100,22 @@ def test_nf4_forward_under_dropout(name):
     tol = (E * np.abs(ref) + (K + 34) * F * (np.abs(Xr) @ np.abs(Wd).T)
            + s * ((2.01 * E * np.abs(Ur) + 2 * u_err) @ np.abs(Br).T + (r + 34) * F * (np.abs(Ur) @ np.abs(Br).T)))
     within(Y, ref, 1.01 * tol, "Y")
+
+
+@pytest.mark.parametrize("name", ["64x64", "256x128", "256x192", "256x256", "256x256 split"])
+@pytest.mark.parametrize("r", [40, 64, 96, 128])
+def test_an_infinite_gradient_stays_in_its_row(name, r):
+    M, K, lines = SIZES[name]
+    N = 64 * lines
+    print(f"[tiles inf] {name} M{M} N{N} K{K} r{r}", flush=True)
+    rng = np.random.default_rng(M + r)
+    w = ops.i8_quantize(bf16(rng, (N, K), 0.02)[0])
+    X, A, B = bf16(rng, (M, K))[0], bf16(rng, (r, K), 0.1)[0], bf16(rng, (N, r), 0.1)[0]
+    dY = bf16(rng, (M, N))[0]
+    drop = ops.Dropout(0.3, 31, 7)
+    want = ops.i8_linear_bwd(w, X, dY, A, B, 16.0, drop=drop)[0]
+    dY[7, 0] = float("inf")
+    got = ops.i8_linear_bwd(w, X, dY, A, B, 16.0, drop=drop)[0]
+    rest = [i for i in range(M) if i != 7]
+    assert torch.equal(got[rest], want[rest])
+    assert not got[7].isfinite().any()
