@@ -566,6 +566,11 @@ __global__ __launch_bounds__(kThreads) void reduce_kernel(const float* __restric
   }
 }
 
+// What the bf16 h leaves of v; nothing where h is not finite (an infinity minus
+// itself would make the gradient NaN where its sum is infinite).
+__device__ __forceinline__ float rest_of(float v, uint32_t h) {
+  return (h & 0x7F80u) == 0x7F80u ? 0.0f : v - bf2f(h);
+}
 // The sum of the splits as three bf16 parts, n elements apart: each the bf16
 // rounding of what the parts before it left, together the fp32 sum.
 __global__ __launch_bounds__(kThreads) void reduce_parts_kernel(const float* __restrict__ part, int splits, int64_t n,
@@ -577,7 +582,8 @@ __global__ __launch_bounds__(kThreads) void reduce_parts_kernel(const float* __r
   for (int k = 0; k < 3; ++k) {
     const uint2 p = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     *reinterpret_cast<uint2*>(out + k * n + i) = p;
-    v = make_float4(v.x - bf2f(p.x & 0xFFFFu), v.y - bf2f(p.x >> 16), v.z - bf2f(p.y & 0xFFFFu), v.w - bf2f(p.y >> 16));
+    v = make_float4(rest_of(v.x, p.x & 0xFFFFu), rest_of(v.y, p.x >> 16), rest_of(v.z, p.y & 0xFFFFu),
+                    rest_of(v.w, p.y >> 16));
   }
 }
 

@@ -167,6 +167,24 @@ def test_a_poisoned_token_stays_alone():
     assert torch.equal(got[rest], want[rest])
 
 
+@pytest.mark.parametrize("M,N,K,r", [(40, 72, 512, 16), (300, 256, 1088, 128)])
+def test_an_infinite_gradient_gives_infinite_adapter_gradients(M, N, K, r):
+    rng = np.random.default_rng(M)
+    w = ops.i8_quantize(bf16(rng, (N, K), 0.02)[0])
+    # no zeros: an infinity times any of these is an infinity
+    away = lambda shape: bf16(rng, shape)[0].sign().add(0.25)
+    X, A, B, dY = away((M, K)), away((r, K)), away((N, r)), away((M, N))
+    U = away((M, r))
+    dY[7, 3] = float("inf")
+    dX, dA, dB = ops.i8_linear_bwd(w, X, dY, A, B, 16.0, U=U)
+    G, Xr, Ur = torch_to_f64(dY) @ torch_to_f64(B), torch_to_f64(X), torch_to_f64(U)
+    inf_a, inf_b = G.T @ Xr, torch_to_f64(dY).T @ Ur
+    assert np.isinf(inf_a).all() and np.array_equal(torch_to_f64(dA), inf_a)
+    assert np.isinf(inf_b[3]).all() and np.array_equal(torch_to_f64(dB)[3], inf_b[3])
+    rest = [i for i in range(N) if i != 3]
+    assert dB[rest].isfinite().all() and dX[:7].isfinite().all() and dX[8:].isfinite().all()
+
+
 def test_outputs_stay_inside_their_buffers_and_zero_tokens():
     rng = np.random.default_rng(3)
     M, N, K, r = 37, 136, 264, 8
