@@ -274,6 +274,11 @@ I8FwdLayout i8_fwd_layout(int64_t M, int64_t N, int64_t K, int32_t r) {
   return L;
 }
 
+// U and G [M x r], B [N x r] and A [r x K] within 32-bit byte offsets.
+bool adapter_ok(int64_t M, int64_t N, int64_t K, int32_t r) {
+  return r == 0 || std::max(M, std::max(N, K)) <= (int64_t)0x7FFFFFFF / r;
+}
+
 // A weight (or an input) as rows of 8-bit integers.
 qlora_status check_i8(const qlora_i8_rows* q) {
   if (!q) return QLORA_E_NULL;
@@ -740,6 +745,7 @@ qlora_status qlora_linear_fwd_drop(const qlora_nf4_weight* W, const uint16_t* X,
   qlora_status st = check_fwd(W, X, M, A, B, r, Y, U_save);
   if (st != QLORA_OK) return st;
   if (r == 0) return QLORA_E_UNSUPPORTED;   // no adapter, nothing to drop
+  if (!adapter_ok(M, W->rows, W->cols, r)) return QLORA_E_UNSUPPORTED;
   if (!drop) return QLORA_E_NULL;
   DropArgs d{};
   bool active;
@@ -776,7 +782,7 @@ qlora_status check_bwd(int64_t M, int64_t N, int64_t K, const uint16_t* X, const
   if (r > 0) {
     if (!dA || !dB || !X) return QLORA_E_NULL;
     if (!aligned16(dA) || !aligned16(dB) || !aligned16(X)) return QLORA_E_ALIGN;
-    if (!skinny_cols_ok(K) || !skinny_cols_ok(N)) return QLORA_E_UNSUPPORTED;
+    if (!skinny_cols_ok(K) || !skinny_cols_ok(N) || !adapter_ok(M, N, K, r)) return QLORA_E_UNSUPPORTED;
   } else if (dA || dB) {
     return QLORA_E_SHAPE;   // no adapter, no adapter gradients
   }
@@ -795,9 +801,10 @@ qlora_status weight_t(const qlora_nf4_weight* W, const qlora_i8_rows* W8, bf16_t
 
 // The staged backward's launches on validated arguments, for the weight W or
 // (not null) W8.
-qlora_status run_bwd(const qlora_nf4_weight* W, const qlora_i8_rows* W8, int64_t M, int64_t N, int64_t K, const uint16_t* X, const uint16_t* dY, const uint16_t* A,
-                     const uint16_t* B, int32_t r, float alpha, const uint16_t* U, const DropArgs* drop, uint16_t* dX,
-                     float* dA, float* dB, void* ws, hipStream_t s) {
+qlora_status run_bwd(const qlora_nf4_weight* W, const qlora_i8_rows* W8, int64_t M, int64_t N, int64_t K,
+                     const uint16_t* X, const uint16_t* dY, const uint16_t* A, const uint16_t* B, int32_t r, float alpha,
+                     const uint16_t* U, const DropArgs* drop, uint16_t* dX, float* dA, float* dB, void* ws,
+                     hipStream_t s) {
   const DropBwdLayout L = drop_bwd_layout(M, N, K, r, dX != nullptr);
   const int64_t np = up64(N);
   qlora_status st;

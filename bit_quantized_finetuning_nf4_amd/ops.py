@@ -321,6 +321,8 @@ def linear_fwd(q: QuantizedWeight, X: torch.Tensor, A=None, B=None, alpha: float
             raise ValueError("the forward under dropout takes the path that the library chooses")
         _on_current(X.device)
         _need(X, torch.bfloat16, "X", (M, q.cols))
+        for t, name in ((q.codes, "q"), (A, "A"), (B, "B"), (Y, "out"), (U, "u_out")):
+            _beside(t, X, name)
         d = q.desc()
         ws = _ws_for(ws, workspace_bytes(_lib.QLORA_OP_FWD_DROP, M, q.rows, q.cols, r), X)
         dd = drop.desc(X.device)
@@ -375,6 +377,7 @@ def linear_bwd(q: QuantizedWeight, X: torch.Tensor, dY: torch.Tensor, A=None, B=
         if path != "auto":
             raise ValueError("the backward under dropout has no fused path")
         d = q.desc()
+        _beside(q.codes, dY, "q")
         return _staged_bwd("qlora_linear_bwd_drop", _lib.QLORA_OP_BWD_DROP, d, q.rows, q.cols, X, dY, A, B, alpha, U,
                            drop, need_dx, dX, dA, dB, ws)
     M = dY.shape[0]

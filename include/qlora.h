@@ -560,7 +560,9 @@ qlora_status qlora_dropout(const uint16_t* x, int64_t n, const qlora_drop* drop,
 
 /* qlora_linear_fwd with the adapter under dropout:
  *   Y = X deq(W)^T + s U B^T,  U = drop(X) A^T,  drop over X [M x K].
- * Arguments, paths and errors as qlora_linear_fwd; r > 0 and drop not NULL.
+ * Arguments, paths and errors as qlora_linear_fwd; r > 0 and drop not NULL;
+ * M r, N r and r K below 2^31 (QLORA_E_UNSUPPORTED otherwise, here and in the
+ * backward).
  * Workspace: qlora_workspace_bytes(QLORA_OP_FWD_DROP, M, N, K, r, 0); the
  * staged path, where it applies, is taken if the workspace holds it.  At
  * p = 0 the result is qlora_linear_fwd's. */

@@ -104,3 +104,13 @@ def test_i8(L):
     assert bwd(dY=None) == NULL and bwd(X=None) == NULL and bwd(dA=None) == NULL and bwd(n=100) == WORKSPACE
     assert bwd(r=0, A=None, B=None) == SHAPE      # gradients asked of no adapter
     assert bwd(r=0, A=None, B=None, dA=None, dB=None, drop=DropDesc(0.1, 1, 1, None)) == UNSUPPORTED
+
+
+def test_adapters_past_32_bit_offsets(L):
+    """M r or N r of 2^31 where M K, N K and M N are below it."""
+    d = DropDesc(0.1, 1, 2, None)
+    for m, n, want in ((1 << 24, 8, UNSUPPORTED), ((1 << 24) - 1, 8, WORKSPACE), (8, 1 << 24, UNSUPPORTED)):
+        w = Nf4WeightDesc(n, 64, 64, 256, P[0].value, P[1].value, P[2].value, 0, 0)
+        assert L.qlora_linear_fwd_drop(ref(w), P[3], m, P[4], P[5], 128, 16.0, ref(d), P[6], None, P[7], 0, None) == want
+        assert L.qlora_linear_bwd_drop(ref(w), P[3], P[8], m, P[4], P[5], 128, 16.0, None, ref(d), P[6], P[9], P[10],
+                                       P[7], 0, None) == want
