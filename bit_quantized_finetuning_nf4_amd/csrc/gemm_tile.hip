@@ -120,69 +120,141 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  QLORA_WAIT(0, 0);   // no DMA still in flight when the workgroup ends
+  QLORA_WAIT(0, 0);   // no DMA still in flight, and
+  __builtin_amdgcn_s_barrier();   // no wave still reads the ring: the results pass through it
 
   // D[channel][token]: lane (lr, h): token lr, channels 8 q + 4 h .. of a
-  // block.  The adapter's product of a block is summed on its own, from
-  // global memory: 8 ranks per lane half and MFMA.
-  [[maybe_unused]] DropKey key;
-  if constexpr (TAIL == kTailDxDrop) key = drop_key(g.drop);
+  // block.  The adapter's product is summed on its own (it is masked, or added
+  // to scaled integer sums), from global memory: 8 ranks per lane half and MFMA,
+  // the loads of the next 16 ranks of all blocks in flight meanwhile.
   const int r = split == 0 ? g.r : 0;
+  [[maybe_unused]] float x[FJ];
+  [[maybe_unused]] float4 sc[FI][4];
+  if constexpr (kI8) {
 #pragma unroll
-  for (int j = 0; j < FJ; ++j) {
-    const int64_t m = m0 + 32 * (FJ * wr + j) + lr;
-    [[maybe_unused]] float x = 1.0f;
-    if constexpr (kI8) x = m < M ? g.sx[m] : 0.0f;
+    for (int j = 0; j < FJ; ++j) x[j] = g.sx[min(m0 + 32 * (FJ * wr + j) + lr, M - 1)];
 #pragma unroll
-    for (int i = 0; i < FI; ++i) {
-      const int64_t nb = n0 + 32 * (FI * wc + i);
-      f32x16_t y;
+    for (int i = 0; i < FI; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = 0.0f;
-      for (int c = 0; c < r; c += 16) {
-        const int k = c + 8 * h;
-        bf16x8_t fb{}, fu{};
-        if (k < r && nb + lr < N) {
-          if constexpr (TAIL == kTailFwd) {
-            fb = *reinterpret_cast<const bf16x8_t*>(g.B + (nb + lr) * g.r + k);
-          } else {   // A's rows: eight ranks of one column
-            uint32_t v[8];
+      for (int q = 0; q < 4; ++q)   // N % 8 == 0
+        sc[i][q] = *reinterpret_cast<const float4*>(g.sw + min(n0 + 32 * (FI * wc + i) + 8 * q + 4 * h, N - 4));
+  }
+  f32x16_t y[FI][FJ];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = g.B[(int64_t)(k + e) * N + nb + lr];
-            fb = __builtin_bit_cast(bf16x8_t, u32x4_t{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
-                                                      v[6] | v[7] << 16});
-          }
+  for (int i = 0; i < FI; ++i)
+#pragma unroll
+    for (int j = 0; j < FJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[i][j][e] = 0.0f;
+  if (r > 0) {
+    constexpr int kB = TAIL == kTailFwd ? 4 : 8;   // words of a weight fragment as loaded
+    uint32_t fb[2][FI][kB];
+    u32x4_t fu[2][FJ];
+    auto load = [&](int c, int set) __attribute__((always_inline)) {
+      const int k = c + 8 * h;   // past the rank (r % 8 == 0), or the rows: zero
+#pragma unroll
+      for (int i = 0; i < FI; ++i) {
+        const int64_t n = n0 + 32 * (FI * wc + i) + lr;
+        const bool in = k < r && n < N;
+        if constexpr (TAIL == kTailFwd) {
+          u32x4_t v = {0u, 0u, 0u, 0u};
+          if (in) v = *reinterpret_cast<const u32x4_t*>(g.B + n * g.r + k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) fb[set][i][e] = v[e];
+        } else {   // A's rows: eight ranks of one column
+#pragma unroll
+          for (int e = 0; e < 8; ++e) fb[set][i][e] = in ? g.B[(int64_t)(k + e) * N + n] : 0u;
         }
-        if (k < r && m < M) fu = *reinterpret_cast<const bf16x8_t*>(g.T + m * g.r + k);
-        y = mfma32x32x16(fb, fu, y);
-      }
-      if constexpr (TAIL == kTailDxDrop) {
-        if (r > 0) mask_block(y, (uint32_t)m * (uint32_t)(N >> 3) + (uint32_t)(nb >> 3), key);
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t n = nb + 8 * q + 4 * h;   // N % 8 == 0
-        if (m < M && n < N) {
-          float4 sc = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-          if constexpr (kI8) sc = *reinterpret_cast<const float4*>(g.sw + n);
-          const float y0 = fmaf(g.s, y[4 * q], (float)acc[i][j][4 * q] * (x * sc.x)),
-                      y1 = fmaf(g.s, y[4 * q + 1], (float)acc[i][j][4 * q + 1] * (x * sc.y)),
-                      y2 = fmaf(g.s, y[4 * q + 2], (float)acc[i][j][4 * q + 2] * (x * sc.z)),
-                      y3 = fmaf(g.s, y[4 * q + 3], (float)acc[i][j][4 * q + 3] * (x * sc.w));
-          if (g.part)
-            *reinterpret_cast<float4*>(g.part + ((int64_t)split * M + m) * N + n) = make_float4(y0, y1, y2, y3);
+      for (int j = 0; j < FJ; ++j) {
+        const int64_t m = m0 + 32 * (FJ * wr + j) + lr;
+        fu[set][j] = u32x4_t{0u, 0u, 0u, 0u};
+        if (k < r && m < M) fu[set][j] = *reinterpret_cast<const u32x4_t*>(g.T + m * g.r + k);
+      }
+    };
+    auto mul = [&](int set) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < FI; ++i) {
+        u32x4_t v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (TAIL == kTailFwd)
+            v[e] = fb[set][i][e];
           else
-            *reinterpret_cast<uint2*>(g.Y + m * N + n) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
+            v[e] = fb[set][i][2 * e] | fb[set][i][2 * e + 1] << 16;
         }
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+          y[i][j] = mfma32x32x16(__builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, fu[set][j]), y[i][j]);
       }
+    };
+    load(0, 0);
+    for (int c = 0; c < r; c += 32) {
+      load(c + 16, 1);
+      mul(0);
+      load(c + 32, 0);
+      mul(1);
     }
   }
+  if constexpr (TAIL == kTailDxDrop) {
+    if (r > 0) {
+      const DropKey key = drop_key(g.drop);
+#pragma unroll
+      for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) {
+          const uint32_t m = (uint32_t)(m0 + 32 * (FJ * wr + j) + lr);
+          mask_block(y[i][j], m * (uint32_t)(N >> 3) + (uint32_t)((n0 + 32 * (FI * wc + i)) >> 3), key);
+        }
+    }
+  }
+  // through LDS, so that whole lines of a token's row are stored: rows of TN
+  // values and 16 bytes (a store of four channels of 32 tokens from the
+  // registers is 64 pieces of lines, which L2 takes one at a time: with those,
+  // and the adapter's loads a block at a time, 333 x 11008 x 4096 took 35.1 us
+  // at rank 16 and 39.2 at rank 64, 30.4 and 31.3 this way)
+  auto out = [&](auto* dst, int64_t row0, auto pack) __attribute__((always_inline)) {
+    constexpr int kSize = (int)sizeof(*dst), kPitch = TN * kSize + 16, kRow = TN * kSize / 16;
+#pragma unroll
+    for (int j = 0; j < FJ; ++j)
+#pragma unroll
+      for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float a = (float)acc[i][j][4 * q + e];
+            if constexpr (kI8) a *= x[j] * (e == 0 ? sc[i][q].x : e == 1 ? sc[i][q].y : e == 2 ? sc[i][q].z : sc[i][q].w);
+            v[e] = fmaf(g.s, y[i][j][4 * q + e], a);
+          }
+          pack(smem + (32 * (FJ * wr + j) + lr) * kPitch + (32 * (FI * wc + i) + 8 * q + 4 * h) * kSize, v);
+        }
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < TM * kRow / kThreads; ++p) {
+      const int id = t + kThreads * p, row = id / kRow, c = id % kRow;
+      const int64_t n = n0 + c * (16 / kSize);
+      if (m0 + row < M && n < N)
+        *reinterpret_cast<uint4*>(dst + (row0 + row) * N + n) = *reinterpret_cast<const uint4*>(smem + row * kPitch + 16 * c);
+    }
+  };
+  if (g.part)
+    out(g.part, (int64_t)split * M + m0, [](char* p, const float (&v)[4]) {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    });
+  else
+    out(g.Y, m0, [](char* p, const float (&v)[4]) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    });
 }
 
 template <class MM, int TM, int TN, int NS, int TAIL>
 hipError_t launch(TileGemm g, int splits, int64_t n_begin, int64_t n_rows, hipStream_t st) {
   auto* fn = &tile_kernel<MM, TM, TN, NS, TAIL>;
   constexpr int lds = NS * (TM + TN) * 128;
+  static_assert(lds >= TM * (TN * 4 + 16), "the results pass through the ring");
   hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
   if (e != hipSuccess) return e;
   TileArgs p{g, n_begin, (int)((n_rows + TN - 1) / TN), (int)((g.M + TM - 1) / TM), 0};
