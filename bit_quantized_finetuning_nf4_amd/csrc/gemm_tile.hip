@@ -277,14 +277,14 @@ hipError_t launch_shape(const TileGemm& g, const TileChoice& c, int64_t n_begin,
 // A round of tiles of tm tokens x tn channels: the bytes of the tile's rows
 // that a CU brings in a ns, and what a round costs beside them, in us.  Fitted
 // to the 8-bit product's times at 34 sizes (33 to 4096 tokens, 512 to 22016
-// channels and columns, seven shapes each; 10-14 % rms), where the shape that
-// they choose is within 0.7 % of the fastest on the mean and 13 % at most.
+// channels and columns, seven shapes each; 8-19 % rms), where the shape that
+// they choose is within 0.3 % of the fastest on the mean and 7 % at most.
 struct Shape {
   int tm, tn;
   double rate, fixed;
 };
-constexpr Shape kShapes[] = {{64, 64, 68e3, 2.5},   {64, 128, 67e3, 4.0},   {128, 128, 70e3, 8.8}, {192, 128, 65e3, 10.2},
-                             {256, 128, 58e3, 6.7}, {256, 192, 60e3, 9.4},  {256, 256, 56e3, 14.0}};
+constexpr Shape kShapes[] = {{64, 64, 71e3, 2.2},   {64, 128, 70e3, 3.2},  {128, 128, 69e3, 5.5}, {192, 128, 66e3, 5.5},
+                             {256, 128, 59e3, 6.0}, {256, 192, 61e3, 8.8}, {256, 256, 58e3, 10.5}};
 double round_cost(const Shape& t, int64_t lines) {
   return (double)(t.tm + t.tn) * 128.0 * (double)lines / t.rate + t.fixed;
 }
@@ -296,19 +296,19 @@ constexpr int kMinLines = 4;   // stages of a split, at least
 double full_round_cost(int64_t lines) { return round_cost(kShapes[6], lines); }
 
 // The shape, and the split of the contraction, with the least time (256 x 192
-// and 256 x 128 tiles are not split: where they would be, another shape is).  Measured in us for 8-bit operands (tokens x channels x K; the
-// shapes with rounds x rows):
-//   128 x 8192 x 8192    64x64 128: 24   64x128 192: 35   128x128 256: 45
-//   512 x 8192 x 22016   128x128 256: 115   192x128 320: 130
-//                        256x128 384: 177   64x64 512: 172
-//   333 x 11008 x 4096   192x128 320: 34   256x128 384: 39   256x192 448: 45
-//                        256x256 512: 50
-//   768 x 11008 x 4096   256x192 448: 50   256x256 512: 53   192x128 640: 67
+// and 256 x 128 tiles are not split: where they would be, another shape is).
+// Measured in us for 8-bit operands (tokens x channels x K):
+//   128 x 8192 x 8192    64x64 24   64x128 32   128x128 40
+//                        128x128 in four splits 23.5, in two 29
+//   512 x 8192 x 22016   128x128 112   192x128 126   64x64 175
+//                        256x256 in four splits 102, unsplit 231
+//   333 x 11008 x 4096   192x128 29   256x128 39   128x128 41   256x256 49
+//   768 x 11008 x 4096   256x192 49   256x256 52   192x128 58   64x64 69
+//   2048 x 4096 x 22016  256x256 in two splits 161   256x128 186   128x128 209
+//   40 x 840 x 19840     64x64 in eight splits 11.3, unsplit 34
 // Rings of two stages lose (151 us against 115 with four, 128 x 128 at 512 x
 // 8192 x 22016); past three or four nothing changes.  A split adds a launch and
-// its fp32 parts' way through memory (mostly the last-level cache): 2048 x 4096
-// x 22016 takes 170 us on 256x256 tiles in two splits, 228 unsplit and 215 on
-// 128x128; 40 x 840 x 19840 12 us on 64x64 in eight, 36 unsplit.
+// its fp32 parts' way through memory (mostly the last-level cache).
 TileChoice choose_tile(int64_t M, int64_t N, int64_t lines, int cus, size_t part_bytes) {
   TileChoice best{0, 0, 1, 1e30};
   for (const Shape& t : kShapes) {
@@ -321,7 +321,7 @@ TileChoice choose_tile(int64_t M, int64_t N, int64_t lines, int cus, size_t part
       const size_t bytes = (size_t)splits * (size_t)M * (size_t)N * sizeof(float);
       if (splits > 1 && bytes > part_bytes) break;
       double cost = (double)((tiles * splits + cus - 1) / cus) * round_cost(t, sps);
-      if (splits > 1) cost += 2.0 + 0.2 * splits + (double)bytes / 4e6;
+      if (splits > 1) cost += 1.0 + 0.3 * splits + (double)bytes / 3.3e6;
       if (cost <= best.cost) best = TileChoice{t.tm, t.tn, splits, cost};
     }
   }

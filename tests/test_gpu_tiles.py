@@ -20,7 +20,8 @@ pytestmark = pytest.mark.gpu
 SIZES = {
     "64x64": (49, 64, 1), "64x64 split": (43, 64, 16), "64x128": (66, 9024, 1), "64x128 split": (67, 2816, 55),
     "128x128": (135, 11392, 6), "128x128 split": (65, 9280, 45), "192x128": (324, 11456, 17),
-    "192x128 split": (129, 5696, 54), "256x128": (271, 6656, 1), "256x192": (548, 11008, 1),
+    "192x128 split": (129, 5696, 54), "256x128": (386, 10944, 1), "128x128 of one line": (271, 6656, 1),
+    "256x192": (548, 11008, 1),
     "256x256": (1062, 10560, 2), "256x256 split": (195, 8512, 71),
 }
 
