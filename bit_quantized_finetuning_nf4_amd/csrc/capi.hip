@@ -760,11 +760,14 @@ qlora_status qlora_linear_fwd_drop(const qlora_nf4_weight* W, const uint16_t* X,
   const float sc = (float)((double)alpha / (double)r);
   bf16_t* U = U_save ? U_save : reinterpret_cast<bf16_t*>(ws_at(ws, L.u));
   float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
-  if ((st = hip_status(launch_xat_drop(X, A, M, K, r, &d, part, U, s))) != QLORA_OK) return st;
-  if (!staged) return hip_status(launch_fwd(view(W), X, M, U, B, r, sc, Y, s));
+  Ride rest;
+  if ((st = hip_status(start_xat_drop(X, A, M, K, r, &d, part, U, &rest, s))) != QLORA_OK) return st;
+  if (!staged) {
+    if ((st = hip_status(launch_ride(rest, s))) != QLORA_OK) return st;
+    return hip_status(launch_fwd(view(W), X, M, U, B, r, sc, Y, s));
+  }
   bf16_t* Wd = reinterpret_cast<bf16_t*>(ws_at(ws, L.wd));
-  st = hip_status(launch_dequant(W->codes, W->absmax_q, W->group_scale, N * K, W->codebook, W->absmax_format, Wd, s));
-  if (st != QLORA_OK) return st;
+  if ((st = hip_status(launch_dequant_ride(view(W), Wd, rest, s))) != QLORA_OK) return st;
   return hip_status(launch_staged(Wd, N, K, X, M, U, B, false, r, sc, nullptr, Y, s, part, L.part_bytes));
 }
 
@@ -789,12 +792,15 @@ qlora_status check_bwd(int64_t M, int64_t N, int64_t K, const uint16_t* X, const
   return QLORA_OK;
 }
 
-// deq(W)^T of either format: out [K x ldo], the columns past N zero.
-qlora_status weight_t(const qlora_nf4_weight* W, const qlora_i8_rows* W8, bf16_t* out, int64_t ldo, hipStream_t s) {
-  if (W8) return hip_status(launch_i8_dequant_t(W8->codes, W8->scale, W8->rows, W8->cols, out, ldo, s));
+// deq(W)^T of either format: out [K x ldo], the columns past N zero; with G's
+// last step if there is one.
+qlora_status weight_t(const qlora_nf4_weight* W, const qlora_i8_rows* W8, bf16_t* out, int64_t ldo, const Ride* rest,
+                      hipStream_t s) {
+  if (W8) return hip_status(launch_i8_dequant_t(W8->codes, W8->scale, W8->rows, W8->cols, out, ldo, rest, s));
   const int64_t N = W->rows, K = W->cols;
   const qlora_status st = hip_status(
-      launch_dequant_t(W->codes, W->absmax_q, W->group_scale, N, K, W->codebook, W->absmax_format, out, ldo, s));
+      rest ? launch_dequant_t_ride(view(W), out, ldo, *rest, s)
+           : launch_dequant_t(W->codes, W->absmax_q, W->group_scale, N, K, W->codebook, W->absmax_format, out, ldo, s));
   if (st != QLORA_OK || ldo == N) return st;
   return hip_status(launch_pad_rows(nullptr, K, N, out, ldo, s));
 }
@@ -813,16 +819,25 @@ qlora_status run_bwd(const qlora_nf4_weight* W, const qlora_i8_rows* W8, int64_t
   float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
   if (r > 0 && !U) {
     bf16_t* Ud = reinterpret_cast<bf16_t*>(ws_at(ws, L.u));
-    if ((st = hip_status(launch_xat_drop(X, A, M, K, r, drop, part, Ud, s))) != QLORA_OK) return st;
+    Ride rest;
+    if ((st = hip_status(start_xat_drop(X, A, M, K, r, drop, part, Ud, &rest, s))) != QLORA_OK) return st;
+    if ((st = hip_status(launch_ride(rest, s))) != QLORA_OK) return st;
     U = Ud;
   }
-  auto run_g = [&]() { return hip_status(launch_dyb_parts(dY, B, M, N, r, part, G, s)); };
+  Ride rest;
+  auto start_g = [&]() { return hip_status(start_dyb_parts(dY, B, M, N, r, part, G, &rest, s)); };
+  auto run_g = [&]() {
+    const qlora_status e = start_g();
+    return e != QLORA_OK ? e : hip_status(launch_ride(rest, s));
+  };
   if (dX) {
     bf16_t* WdT = reinterpret_cast<bf16_t*>(ws_at(ws, L.wdt));
     const bf16_t* g = dY;
-    const bool late = dy_late(M, N);
-    if (r > 0 && !late && (st = run_g()) != QLORA_OK) return st;
-    if ((st = weight_t(W, W8, WdT, np, s)) != QLORA_OK) return st;
+    // G's last step rides with the dequantization, unless what that writes would
+    // push dY out of the last-level cache and G goes after it
+    const bool late = dy_late(M, N) && (np * K + M * N) * 2 > ((int64_t)256 << 20);
+    if (r > 0 && !late && (st = start_g()) != QLORA_OK) return st;
+    if ((st = weight_t(W, W8, WdT, np, r > 0 && !late ? &rest : nullptr, s)) != QLORA_OK) return st;
     if (np != N) {
       bf16_t* dyp = reinterpret_cast<bf16_t*>(ws_at(ws, L.dyp));
       if ((st = hip_status(launch_pad_rows(dY, M, N, dyp, np, s))) != QLORA_OK) return st;
@@ -868,7 +883,7 @@ qlora_status qlora_i8_quantize(const uint16_t* X, const qlora_i8_rows* q, void* 
   if (st != QLORA_OK) return st;
   if (!X) return QLORA_E_NULL;
   if (!aligned16(X)) return QLORA_E_ALIGN;
-  return hip_status(launch_quant_rows(X, q->rows, q->cols, q->codes, q->scale, (hipStream_t)stream));
+  return hip_status(launch_quant_rows(X, q->rows, q->cols, q->codes, q->scale, nullptr, (hipStream_t)stream));
 }
 
 qlora_status qlora_i8_dequant(const qlora_i8_rows* q, uint16_t* out, void* stream) {
@@ -914,8 +929,11 @@ qlora_status qlora_i8_linear_fwd(const qlora_i8_rows* W, const uint16_t* X, int6
   if (i8_prep_ok(M, K, r)) {
     st = hip_status(launch_i8_prep(X, M, K, A, r, dp, U, xq, sx, s));
   } else {
-    if (r > 0 && (st = hip_status(launch_xat_drop(X, A, M, K, r, dp, part, U, s))) != QLORA_OK) return st;
-    st = hip_status(launch_quant_rows(X, M, K, xq, sx, s));
+    Ride rest;
+    if (r > 0 && (st = hip_status(start_xat_drop(X, A, M, K, r, dp, part, U, &rest, s))) != QLORA_OK) return st;
+    const bool sum = r > 0 && rest.kind == kRideSum;
+    if (r > 0 && !sum && (st = hip_status(launch_ride(rest, s))) != QLORA_OK) return st;
+    st = hip_status(launch_quant_rows(X, M, K, xq, sx, sum ? &rest : nullptr, s));
   }
   if (st != QLORA_OK) return st;
   const float sc = r > 0 ? (float)((double)alpha / (double)r) : 0.0f;

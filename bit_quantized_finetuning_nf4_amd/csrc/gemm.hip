@@ -24,7 +24,7 @@
 #include "device.h"
 #include "kernels.h"
 #include "lds.h"
-#include "urows.h"
+#include "ride.h"
 
 namespace qlora {
 
@@ -529,28 +529,6 @@ __global__ __launch_bounds__(kThreads, 1) void adapter_grads_kernel(GradArgs p) 
                                 p.tiles_b, p.part_b, 0, p.drop);
 }
 
-// Elements i .. i + 3 of the splits' partials, summed in split order, times
-// scale; the loads of eight splits are issued together.
-__device__ __forceinline__ float4 sum_splits(const float* __restrict__ part, int splits, int64_t n, int64_t i,
-                                             float scale) {
-  float4 acc = *reinterpret_cast<const float4*>(part + i);
-  for (int s0 = 1; s0 < splits; s0 += 8) {
-    float4 v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      v[k] = *reinterpret_cast<const float4*>(part + (int64_t)min(s0 + k, splits - 1) * n + i);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const bool in = s0 + k < splits;   // selects, not branches: a branch would sink its load
-      acc.x = in ? acc.x + v[k].x : acc.x;
-      acc.y = in ? acc.y + v[k].y : acc.y;
-      acc.z = in ? acc.z + v[k].z : acc.z;
-      acc.w = in ? acc.w + v[k].w : acc.w;
-    }
-  }
-  return make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
-}
-
 __global__ __launch_bounds__(kThreads) void reduce_kernel(const float* __restrict__ part, int splits, int64_t n,
                                                           float scale, float* __restrict__ out_f32,
                                                           bf16_t* __restrict__ out_bf16,
@@ -566,25 +544,9 @@ __global__ __launch_bounds__(kThreads) void reduce_kernel(const float* __restric
   }
 }
 
-// What the bf16 h leaves of v; nothing where h is not finite (an infinity minus
-// itself would make the gradient NaN where its sum is infinite).
-__device__ __forceinline__ float rest_of(float v, uint32_t h) {
-  return (h & 0x7F80u) == 0x7F80u ? 0.0f : v - bf2f(h);
-}
-// The sum of the splits as three bf16 parts, n elements apart: each the bf16
-// rounding of what the parts before it left, together the fp32 sum.
-__global__ __launch_bounds__(kThreads) void reduce_parts_kernel(const float* __restrict__ part, int splits, int64_t n,
-                                                                bf16_t* __restrict__ out) {
-  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-  if (i >= n) return;
-  float4 v = sum_splits(part, splits, n, i, 1.0f);
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const uint2 p = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-    *reinterpret_cast<uint2*>(out + k * n + i) = p;
-    v = make_float4(rest_of(v.x, p.x & 0xFFFFu), rest_of(v.y, p.x >> 16), rest_of(v.z, p.y & 0xFFFFu),
-                    rest_of(v.w, p.y >> 16));
-  }
+template <int KIND>
+__global__ __launch_bounds__(256) void ride_kernel(Ride a) {
+  ride<KIND>(a, blockIdx.x);
 }
 
 // The reductions of dA and dB in one launch: elements [0, n0) of the
@@ -788,17 +750,6 @@ size_t u_part_bytes(int64_t M, int64_t K, int r) {
 
 namespace {
 
-template <bool DROP>
-__global__ __launch_bounds__(256) void u_rows_kernel(const bf16_t* __restrict__ X, int64_t M, int64_t K,
-                                                     const bf16_t* __restrict__ A, int r, bf16_t* __restrict__ U,
-                                                     DropArgs drop) {
-  u_rows<DROP>(X, M, K, A, r, blockIdx.x, U, drop);
-}
-
-}  // namespace
-
-namespace {
-
 template <int RP, bool QT, bool DROP>
 hipError_t wide_partials(const bf16_t* P, int64_t M, int64_t C, const bf16_t* Q, int r, const DropArgs& drop,
                          const Split& sp, float* part, hipStream_t st) {
@@ -813,32 +764,48 @@ hipError_t wide_partials(const bf16_t* P, int64_t M, int64_t C, const bf16_t* Q,
 
 }  // namespace
 
-hipError_t launch_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
-                           float* part, bf16_t* out, hipStream_t st) {
-  if (u_rows_ok(M, r)) {
-    hipLaunchKernelGGL((drop ? &u_rows_kernel<true> : &u_rows_kernel<false>), dim3((unsigned)u_rows_blocks(M, r)),
-                       dim3(256), 0, st, X, M, K, A, r, out, drop ? *drop : DropArgs{});
-    return hipGetLastError();
-  }
-  const Split sp = rows_split(M, K);
-  const DropArgs d = drop ? *drop : DropArgs{};
-  const hipError_t e = drop ? (r <= 64 ? wide_partials<64, false, true>(X, M, K, A, r, d, sp, part, st)
-                                       : wide_partials<128, false, true>(X, M, K, A, r, d, sp, part, st))
-                            : (r <= 64 ? wide_partials<64, false, false>(X, M, K, A, r, d, sp, part, st)
-                                       : wide_partials<128, false, false>(X, M, K, A, r, d, sp, part, st));
-  if (e != hipSuccess) return e;
-  return reduce(part, sp.splits, M * r, drop ? drop->scale : 1.0f, nullptr, out, nullptr, st);
+namespace {
+
+Ride sum_ride(RideKind kind, const float* part, const Split& sp, int64_t n, float scale, bf16_t* out) {
+  Ride d{};
+  d.kind = kind, d.blocks = (int)((n / 4 + 255) / 256);
+  d.part = part, d.splits = sp.splits, d.n = n, d.scale = scale, d.out = out;
+  return d;
 }
 
-hipError_t launch_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* out,
-                            hipStream_t st) {
+}  // namespace
+
+hipError_t start_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
+                          float* part, bf16_t* out, Ride* rest, hipStream_t st) {
+  const DropArgs d = drop ? *drop : DropArgs{};
+  if (u_rows_ok(M, r)) {
+    *rest = Ride{};
+    rest->kind = drop ? kRideRowsDrop : kRideRows, rest->blocks = u_rows_blocks(M, r);
+    rest->X = X, rest->A = A, rest->M = M, rest->K = K, rest->r = r, rest->drop = d, rest->out = out;
+    return hipSuccess;
+  }
+  const Split sp = rows_split(M, K);
+  *rest = sum_ride(kRideSum, part, sp, M * r, drop ? drop->scale : 1.0f, out);
+  return drop ? (r <= 64 ? wide_partials<64, false, true>(X, M, K, A, r, d, sp, part, st)
+                         : wide_partials<128, false, true>(X, M, K, A, r, d, sp, part, st))
+              : (r <= 64 ? wide_partials<64, false, false>(X, M, K, A, r, d, sp, part, st)
+                         : wide_partials<128, false, false>(X, M, K, A, r, d, sp, part, st));
+}
+
+hipError_t start_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* out,
+                           Ride* rest, hipStream_t st) {
   const Split sp = rows_split(M, N);
-  const hipError_t e = r <= 64 ? wide_partials<64, true, false>(dY, M, N, B, r, DropArgs{}, sp, part, st)
-                               : wide_partials<128, true, false>(dY, M, N, B, r, DropArgs{}, sp, part, st);
-  if (e != hipSuccess) return e;
-  const int64_t n = M * r;
-  hipLaunchKernelGGL(reduce_parts_kernel, dim3((unsigned)((n / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
-                     part, sp.splits, n, out);
+  *rest = sum_ride(kRideSum3, part, sp, M * r, 1.0f, out);
+  return r <= 64 ? wide_partials<64, true, false>(dY, M, N, B, r, DropArgs{}, sp, part, st)
+                 : wide_partials<128, true, false>(dY, M, N, B, r, DropArgs{}, sp, part, st);
+}
+
+hipError_t launch_ride(const Ride& a, hipStream_t st) {
+  auto* fn = a.kind == kRideRows       ? &ride_kernel<kRideRows>
+             : a.kind == kRideRowsDrop ? &ride_kernel<kRideRowsDrop>
+             : a.kind == kRideSum      ? &ride_kernel<kRideSum>
+                                       : &ride_kernel<kRideSum3>;
+  hipLaunchKernelGGL(fn, dim3((unsigned)a.blocks), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

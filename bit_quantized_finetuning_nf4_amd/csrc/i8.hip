@@ -9,7 +9,7 @@
 // Rows are padded with zeros to whole 128-byte lines (i8_row_bytes), which
 // the product kernels stream.
 #include "lds.h"
-#include "urows.h"
+#include "ride.h"
 
 namespace qlora {
 namespace {
@@ -121,12 +121,17 @@ __device__ __forceinline__ void quant_row(const bf16_t* __restrict__ X, int64_t 
   }
 }
 
-template <int TPR, int NCH>
+// SUM: the first sum.blocks workgroups add up the partials of U (ride.h).
+template <int TPR, int NCH, bool SUM>
 __global__ __launch_bounds__(256) void quant_rows_kernel(const bf16_t* __restrict__ X, int64_t M, int64_t K,
                                                          int64_t ld, int8_t* __restrict__ Q,
-                                                         float* __restrict__ scale) {
+                                                         float* __restrict__ scale, Ride sum) {
   __shared__ uint32_t wmax[4];
-  const int64_t m = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  if (SUM && (int)blockIdx.x < sum.blocks) {
+    ride<kRideSum>(sum, blockIdx.x);
+    return;
+  }
+  const int64_t m = ((int64_t)blockIdx.x - (SUM ? sum.blocks : 0)) * (256 / TPR) + threadIdx.x / TPR;
   if (TPR == 64 && m >= M) return;   // whole waves; TPR == 64 meets no barrier
   quant_row<TPR, NCH>(X, m, threadIdx.x % TPR, K, ld, Q, scale, wmax);
 }
@@ -165,11 +170,19 @@ __global__ __launch_bounds__(256) void i8_dequant_kernel(const int8_t* __restric
 // WdT [K x ldo] = deq(W)^T, columns N .. ldo - 1 zero (ldo = N rounded up to
 // 64): 64 x 64 tiles through LDS.  Reads 64 bytes of 64 rows, writes 128
 // bytes of 64 rows.
+// The first sum3.blocks workgroups (0: none) add up the partials of G (ride.h).
 __global__ __launch_bounds__(256) void i8_dequant_t_kernel(const int8_t* __restrict__ Q,
                                                            const float* __restrict__ scale, int64_t N, int64_t K,
-                                                           int64_t ld, bf16_t* __restrict__ out, int64_t ldo) {
+                                                           int64_t ld, bf16_t* __restrict__ out, int64_t ldo,
+                                                           int tiles_k, Ride sum3) {
   __shared__ __align__(16) uint32_t tile[64][33];   // [column][row pair], one word of padding
-  const int64_t k0 = (int64_t)blockIdx.x * 64, n0 = (int64_t)blockIdx.y * 64;
+  const int id = (int)blockIdx.x - sum3.blocks;
+  if (id < 0) {
+    ride<kRideSum3>(sum3, blockIdx.x);
+    return;
+  }
+  const int by = id / tiles_k;
+  const int64_t k0 = (int64_t)(id - by * tiles_k) * 64, n0 = (int64_t)by * 64;
   const int t = threadIdx.x;
   {
     // thread: row pair t / 8 (rows 2 p, 2 p + 1), 8 columns at 8 (t mod 8)
@@ -213,24 +226,26 @@ unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); 
 
 }  // namespace
 
-hipError_t launch_quant_rows(const bf16_t* X, int64_t M, int64_t K, int8_t* Q, float* scale, hipStream_t st) {
+hipError_t launch_quant_rows(const bf16_t* X, int64_t M, int64_t K, int8_t* Q, float* scale, const Ride* sum,
+                             hipStream_t st) {
   const int64_t ld = i8_row_bytes(K);
-  auto go = [&](auto* fn, int rows_per_block) {
-    hipLaunchKernelGGL(fn, dim3((unsigned)((M + rows_per_block - 1) / rows_per_block)), dim3(256), 0, st, X, M, K, ld, Q,
-                       scale);
+  const Ride d = sum ? *sum : Ride{};
+  auto go = [&](auto* fn, auto* fn_sum, int rows_per_block) {
+    hipLaunchKernelGGL((sum ? fn_sum : fn), dim3((unsigned)(d.blocks + (M + rows_per_block - 1) / rows_per_block)),
+                       dim3(256), 0, st, X, M, K, ld, Q, scale, d);
   };
   if (ld <= 1024)
-    go(&quant_rows_kernel<64, 1>, 4);
+    go(&quant_rows_kernel<64, 1, false>, &quant_rows_kernel<64, 1, true>, 4);
   else if (ld <= 4096)
-    go(&quant_rows_kernel<256, 1>, 1);
+    go(&quant_rows_kernel<256, 1, false>, &quant_rows_kernel<256, 1, true>, 1);
   else if (ld <= 8192)
-    go(&quant_rows_kernel<256, 2>, 1);
+    go(&quant_rows_kernel<256, 2, false>, &quant_rows_kernel<256, 2, true>, 1);
   else if (ld <= 16384)
-    go(&quant_rows_kernel<256, 4>, 1);
+    go(&quant_rows_kernel<256, 4, false>, &quant_rows_kernel<256, 4, true>, 1);
   else if (ld <= 32768)
-    go(&quant_rows_kernel<256, 8>, 1);
+    go(&quant_rows_kernel<256, 8, false>, &quant_rows_kernel<256, 8, true>, 1);
   else
-    go(&quant_rows_kernel<256, 0>, 1);
+    go(&quant_rows_kernel<256, 0, false>, &quant_rows_kernel<256, 0, true>, 1);
   return hipGetLastError();
 }
 
@@ -262,9 +277,11 @@ hipError_t launch_i8_dequant(const int8_t* Q, const float* scale, int64_t N, int
 }
 
 hipError_t launch_i8_dequant_t(const int8_t* Q, const float* scale, int64_t N, int64_t K, bf16_t* out, int64_t ldo,
-                               hipStream_t st) {
-  hipLaunchKernelGGL(i8_dequant_t_kernel, dim3((unsigned)((K + 63) / 64), (unsigned)((N + 63) / 64)), dim3(256), 0, st,
-                     Q, scale, N, K, i8_row_bytes(K), out, ldo);
+                               const Ride* sum3, hipStream_t st) {
+  const Ride d = sum3 ? *sum3 : Ride{};
+  const int tiles_k = (int)((K + 63) / 64);
+  hipLaunchKernelGGL(i8_dequant_t_kernel, dim3((unsigned)(d.blocks + tiles_k * ((N + 63) / 64))), dim3(256), 0, st, Q,
+                     scale, N, K, i8_row_bytes(K), out, ldo, tiles_k, d);
   return hipGetLastError();
 }
 

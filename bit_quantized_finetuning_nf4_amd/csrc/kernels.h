@@ -55,6 +55,12 @@ hipError_t launch_dequant(const uint8_t* codes, const uint8_t* absmax_q, const f
 hipError_t launch_dequant_t(const uint8_t* codes, const uint8_t* absmax_q, const float* group_scale, int64_t N,
                             int64_t K, int codebook, int absfmt, bf16_t* out, int64_t ldo, hipStream_t s);
 
+// launch_dequant of a whole weight (rest: kRideSum or kRideRowsDrop) and
+// launch_dequant_t (rest: kRideSum3) with an adapter product's last step.
+struct Ride;
+hipError_t launch_dequant_ride(const Nf4View& W, bf16_t* out, const Ride& rest, hipStream_t s);
+hipError_t launch_dequant_t_ride(const Nf4View& W, bf16_t* out, int64_t ldo, const Ride& rest, hipStream_t s);
+
 // Up to kDeqMax weights of one shape (N x K), one codebook and one absmax
 // format, dequantized by one launch: weight i to out + i out_gs, as
 // launch_dequant (N K weights) or, transposed, as launch_dequant_t.
@@ -122,12 +128,31 @@ hipError_t launch_grads(const bf16_t* Gm, const bf16_t* X, const bf16_t* dY, int
 // u_part_bytes for the first alone, adapter_part_bytes for all of them.
 size_t u_part_bytes(int64_t M, int64_t K, int r);
 size_t adapter_part_bytes(int64_t M, int64_t N, int64_t K, int r);
-// out [M x r] = drop(X) A^T.
-hipError_t launch_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
-                           float* part, bf16_t* out, hipStream_t st);
-// G = dY B as the sum of three bf16 matrices [M x r], one after the other.
-hipError_t launch_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* out,
-                            hipStream_t st);
+// The last step of such a product, left to the caller: workgroups of a launch
+// that neither reads nor writes what it does (ride.h), or launch_ride.
+enum RideKind : int { kRideSum, kRideSum3, kRideRows, kRideRowsDrop };
+struct Ride {
+  RideKind kind;
+  int blocks;                 // workgroups of 256
+  bf16_t* out;
+  const float* part;          // sums of partials
+  int splits;
+  int64_t n;
+  float scale;
+  const bf16_t *X, *A;        // U by rows
+  int64_t M, K;
+  int r;
+  DropArgs drop;
+};
+hipError_t launch_ride(const Ride& a, hipStream_t st);
+// out [M x r] = drop(X) A^T: all but *rest (kRideSum, kRideRows or
+// kRideRowsDrop).
+hipError_t start_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
+                          float* part, bf16_t* out, Ride* rest, hipStream_t st);
+// G = dY B as the sum of three bf16 matrices [M x r], one after the other: all
+// but *rest (kRideSum3).
+hipError_t start_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* out,
+                           Ride* rest, hipStream_t st);
 // dA [r x K] = scale G^T drop(X) with G3 as above, dB [N x r] = scale dY^T U.
 hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t* dY, const bf16_t* U, int64_t M,
                                 int64_t N, int64_t K, int r, const DropArgs* drop, float* part, float* dA, float* dB,
@@ -148,7 +173,9 @@ hipError_t launch_staged(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X
 inline int64_t i8_row_bytes(int64_t cols) { return (cols + 127) / 128 * 128; }
 constexpr int64_t kI8MaxCols = 131072;   // 127^2 cols fits a 32-bit sum
 // Q [M x i8_row_bytes(K)], scale [M] from X [M x K], K % 8 == 0.
-hipError_t launch_quant_rows(const bf16_t* X, int64_t M, int64_t K, int8_t* Q, float* scale, hipStream_t st);
+// sum: null, or a step of kRideSum to take along.
+hipError_t launch_quant_rows(const bf16_t* X, int64_t M, int64_t K, int8_t* Q, float* scale, const Ride* sum,
+                             hipStream_t st);
 // U [M x r] = drop(X) A^T (r may be 0, drop null) and X quantized, in one
 // launch, where i8_prep_ok.
 bool i8_prep_ok(int64_t M, int64_t K, int r);
@@ -156,8 +183,9 @@ hipError_t launch_i8_prep(const bf16_t* X, int64_t M, int64_t K, const bf16_t* A
                           bf16_t* U, int8_t* Q, float* scale, hipStream_t st);
 hipError_t launch_i8_dequant(const int8_t* Q, const float* scale, int64_t N, int64_t K, bf16_t* out, hipStream_t st);
 // out [K x ldo] = deq^T, ldo = N rounded up to 64, the columns past N zero.
+// sum3: null, or a step of kRideSum3 to take along.
 hipError_t launch_i8_dequant_t(const int8_t* Q, const float* scale, int64_t N, int64_t K, bf16_t* out, int64_t ldo,
-                               hipStream_t st);
+                               const Ride* sum3, hipStream_t st);
 // out [rows x ldo]: in [rows x cols] (null: nothing copied) and zero columns
 // cols .. ldo - 1.
 hipError_t launch_pad_rows(const bf16_t* in, int64_t rows, int64_t cols, bf16_t* out, int64_t ldo, hipStream_t st);

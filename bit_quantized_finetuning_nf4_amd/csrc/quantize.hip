@@ -12,6 +12,7 @@
 
 #include "device.h"
 #include "kernels.h"
+#include "ride.h"
 
 namespace qlora {
 
@@ -231,15 +232,10 @@ __global__ __launch_bounds__(256) void quantize_kernel(const bf16_t* __restrict_
 // Grid y selects one of the launch's weights (all of one shape): weight i
 // goes to out + i out_gs.
 template <int CB>
-__global__ __launch_bounds__(256) void dequant_kernel(DeqSrcs src, int64_t numel, int64_t nb, int absfmt,
-                                                      bf16_t* __restrict__ out, int64_t out_gs, int rev) {
-  const int wi = rev ? (int)gridDim.y - 1 - (int)blockIdx.y : (int)blockIdx.y;
-  const uint8_t* __restrict__ codes = src.codes[wi];
-  const uint8_t* __restrict__ absmax_q = src.absmax_q[wi];
-  const float* __restrict__ group_scale = src.group_scale[wi];
-  out += wi * out_gs;
-  const int64_t bx = rev ? (int64_t)gridDim.x - 1 - blockIdx.x : (int64_t)blockIdx.x;
-  const int64_t g = bx * blockDim.x + threadIdx.x;
+__device__ __forceinline__ void dequant_block(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ absmax_q,
+                                              const float* __restrict__ group_scale, int64_t numel, int64_t nb,
+                                              int absfmt, bf16_t* __restrict__ out, int64_t bx) {
+  const int64_t g = bx * 256 + threadIdx.x;
   const int64_t b = g >> 2;
   if (b >= nb) return;
   const float t = block_scale(absmax_q[b], group_scale[b / kGroupBlocks], absfmt);
@@ -267,6 +263,24 @@ __global__ __launch_bounds__(256) void dequant_kernel(DeqSrcs src, int64_t numel
     }
   }
 }
+template <int CB>
+__global__ __launch_bounds__(256) void dequant_kernel(DeqSrcs src, int64_t numel, int64_t nb, int absfmt,
+                                                      bf16_t* __restrict__ out, int64_t out_gs, int rev) {
+  const int wi = rev ? (int)gridDim.y - 1 - (int)blockIdx.y : (int)blockIdx.y;
+  dequant_block<CB>(src.codes[wi], src.absmax_q[wi], src.group_scale[wi], numel, nb, absfmt, out + wi * out_gs,
+                    rev ? (int64_t)gridDim.x - 1 - blockIdx.x : (int64_t)blockIdx.x);
+}
+// One weight, and the last step of an adapter's product in the first workgroups.
+template <int CB, int KIND>
+__global__ __launch_bounds__(256) void dequant_ride_kernel(Nf4View W, int64_t nb, bf16_t* __restrict__ out, int rev,
+                                                           Ride rest) {
+  const int id = (int)blockIdx.x - rest.blocks;
+  if (id < 0)
+    ride<KIND>(rest, blockIdx.x);
+  else
+    dequant_block<CB>(W.codes, W.absmax_q, W.group_scale, W.N * W.K, nb, W.absfmt, out,
+                      rev ? (int64_t)gridDim.x - rest.blocks - 1 - id : (int64_t)id);
+}
 
 // Transposed dequantization, WdT [K x N] = deq(W)^T for W [N x K] with
 // K % 64 == 0 (the dense backward multiplies by it).  A workgroup takes 64
@@ -282,18 +296,12 @@ __global__ __launch_bounds__(256) void dequant_kernel(DeqSrcs src, int64_t numel
 // weight i goes to the columns from i out_gs on.
 constexpr int kTrStride = 33;
 template <int CB>
-__global__ __launch_bounds__(256) void dequant_t_kernel(DeqSrcs src, int64_t N, int64_t K, int absfmt,
-                                                        bf16_t* __restrict__ out, int64_t ldo, int64_t out_gs,
-                                                        int rev) {
-  const int wi = rev ? (int)gridDim.z - 1 - (int)blockIdx.z : (int)blockIdx.z;
-  const uint8_t* __restrict__ codes = src.codes[wi];
-  const uint8_t* __restrict__ absmax_q = src.absmax_q[wi];
-  const float* __restrict__ group_scale = src.group_scale[wi];
-  out += wi * out_gs;
+__device__ __forceinline__ void dequant_t_block(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ absmax_q,
+                                                const float* __restrict__ group_scale, int64_t N, int64_t K, int absfmt,
+                                                bf16_t* __restrict__ out, int64_t ldo, int64_t bx, int64_t by) {
   __shared__ uint32_t tile[256 * kTrStride];
   const int t = threadIdx.x, rp = t & 31, cg = t >> 5;
-  const int64_t by = rev ? (int64_t)gridDim.y - 1 - blockIdx.y : (int64_t)blockIdx.y;
-  const int64_t n0 = by * 64, k0 = (int64_t)blockIdx.x * 256;
+  const int64_t n0 = by * 64, k0 = bx * 256;
   const int64_t kc = k0 + 32 * cg;
   if (kc < K) {
     uint4 c[2];
@@ -336,6 +344,26 @@ __global__ __launch_bounds__(256) void dequant_t_kernel(DeqSrcs src, int64_t N, 
       const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
       for (int e = 0; e < 8 && n0 + 8 * c + e < N; ++e) dst[e] = (bf16_t)(vw[e >> 1] >> (16 * (e & 1)));
     }
+  }
+}
+template <int CB>
+__global__ __launch_bounds__(256) void dequant_t_kernel(DeqSrcs src, int64_t N, int64_t K, int absfmt,
+                                                        bf16_t* __restrict__ out, int64_t ldo, int64_t out_gs,
+                                                        int rev) {
+  const int wi = rev ? (int)gridDim.z - 1 - (int)blockIdx.z : (int)blockIdx.z;
+  dequant_t_block<CB>(src.codes[wi], src.absmax_q[wi], src.group_scale[wi], N, K, absfmt, out + wi * out_gs, ldo,
+                      blockIdx.x, rev ? (int64_t)gridDim.y - 1 - blockIdx.y : (int64_t)blockIdx.y);
+}
+template <int CB>
+__global__ __launch_bounds__(256) void dequant_t_ride_kernel(Nf4View W, bf16_t* __restrict__ out, int64_t ldo,
+                                                             int tiles_k, int rev, Ride rest) {
+  const int id = (int)blockIdx.x - rest.blocks;
+  if (id < 0) {
+    ride<kRideSum3>(rest, blockIdx.x);
+  } else {
+    const int by = id / tiles_k, bx = id - by * tiles_k, rows = (int)((W.N + 63) / 64);
+    dequant_t_block<CB>(W.codes, W.absmax_q, W.group_scale, W.N, W.K, W.absfmt, out, ldo, bx,
+                        rev ? rows - 1 - by : by);
   }
 }
 
@@ -396,6 +424,32 @@ hipError_t launch_dequant_group(const DeqSrcs& src, int n, int64_t N, int64_t K,
     hipLaunchKernelGGL(fn, dim3((unsigned)((K + 255) / 256), (unsigned)((N + 63) / 64), (unsigned)n), dim3(256), 0,
                        s, src, N, K, absfmt, out, ldo, out_gs, rev);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_dequant_ride(const Nf4View& W, bf16_t* out, const Ride& rest, hipStream_t s) {
+  const int64_t numel = W.N * W.K, nb = (numel + kBlock - 1) / kBlock;
+  const int rev = numel * 2 > kLlcBytes ? 1 : 0;
+  auto go = [&](auto* sum, auto* rows) {
+    hipLaunchKernelGGL((rest.kind == kRideSum ? sum : rows), dim3((unsigned)(rest.blocks + (4 * nb + 255) / 256)),
+                       dim3(256), 0, s, W, nb, out, rev, rest);
+  };
+  if (W.codebook == kCbFp4)
+    go(&dequant_ride_kernel<kCbFp4, kRideSum>, &dequant_ride_kernel<kCbFp4, kRideRowsDrop>);
+  else if (W.codebook == kCbInt4)
+    go(&dequant_ride_kernel<kCbInt4, kRideSum>, &dequant_ride_kernel<kCbInt4, kRideRowsDrop>);
+  else
+    go(&dequant_ride_kernel<kCbNf4, kRideSum>, &dequant_ride_kernel<kCbNf4, kRideRowsDrop>);
+  return hipGetLastError();
+}
+
+hipError_t launch_dequant_t_ride(const Nf4View& W, bf16_t* out, int64_t ldo, const Ride& rest, hipStream_t s) {
+  const int rev = W.N * W.K * 2 > kLlcBytes ? 1 : 0;
+  const int tiles_k = (int)((W.K + 255) / 256);
+  auto* fn = W.codebook == kCbFp4 ? &dequant_t_ride_kernel<kCbFp4> : W.codebook == kCbInt4 ? &dequant_t_ride_kernel<kCbInt4>
+                                                                                          : &dequant_t_ride_kernel<kCbNf4>;
+  hipLaunchKernelGGL(fn, dim3((unsigned)(rest.blocks + tiles_k * ((W.N + 63) / 64))), dim3(256), 0, s, W, out, ldo,
+                     tiles_k, rev, rest);
   return hipGetLastError();
 }
 

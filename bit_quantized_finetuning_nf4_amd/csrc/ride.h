@@ -1,0 +1,64 @@
+// ride.h -- the last step of a small adapter product (U = drop(X) A^T, G = dY
+// B) as extra workgroups of the launch that comes next anyway, a
+// dequantization or a quantization, which neither reads the product nor is
+// read by it.  Alone such a step is a launch of 3-5 us that leaves most of the
+// card idle: the backward of 2048 x 4096 x 4096 at rank 64 takes 107 us with it
+// apart and 104 this way, the 8-bit forward 57 and 54, the NF4 forward of 256 x
+// 1024 x 1024 at rank 8 24.9 and 21.1.
+#pragma once
+#include "urows.h"
+
+namespace qlora {
+
+// Elements i .. i + 3 of the splits' partials, summed in split order, times
+// scale; the loads of eight splits are issued together.
+__device__ __forceinline__ float4 sum_splits(const float* __restrict__ part, int splits, int64_t n, int64_t i,
+                                             float scale) {
+  float4 acc = *reinterpret_cast<const float4*>(part + i);
+  for (int s0 = 1; s0 < splits; s0 += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      v[k] = *reinterpret_cast<const float4*>(part + (int64_t)min(s0 + k, splits - 1) * n + i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool in = s0 + k < splits;   // selects, not branches: a branch would sink its load
+      acc.x = in ? acc.x + v[k].x : acc.x;
+      acc.y = in ? acc.y + v[k].y : acc.y;
+      acc.z = in ? acc.z + v[k].z : acc.z;
+      acc.w = in ? acc.w + v[k].w : acc.w;
+    }
+  }
+  return make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
+}
+
+// What the bf16 h leaves of v; nothing where h is not finite (an infinity minus
+// itself would make the gradient NaN where its sum is infinite).
+__device__ __forceinline__ float rest_of(float v, uint32_t h) {
+  return (h & 0x7F80u) == 0x7F80u ? 0.0f : v - bf2f(h);
+}
+
+// Workgroup `block` (of a.blocks, 256 threads) of the step.
+//   kRideSum   bf16 of the splits' sum times scale
+//   kRideSum3  the sum as three bf16 parts, n elements apart: each the bf16
+//              rounding of what the parts before it left, together the fp32 sum
+//   kRideRows, kRideRowsDrop   U by rows (urows.h)
+template <int KIND>
+__device__ __forceinline__ void ride(const Ride& a, int block) {
+  if constexpr (KIND == kRideRows || KIND == kRideRowsDrop) {
+    u_rows<KIND == kRideRowsDrop>(a.X, a.M, a.K, a.A, a.r, block, a.out, a.drop);
+  } else {
+    const int64_t i = ((int64_t)block * 256 + threadIdx.x) * 4;
+    if (i >= a.n) return;
+    float4 v = sum_splits(a.part, a.splits, a.n, i, a.scale);
+#pragma unroll
+    for (int k = 0; k < (KIND == kRideSum3 ? 3 : 1); ++k) {
+      const uint2 p = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      *reinterpret_cast<uint2*>(a.out + k * a.n + i) = p;
+      v = make_float4(rest_of(v.x, p.x & 0xFFFFu), rest_of(v.y, p.x >> 16), rest_of(v.z, p.y & 0xFFFFu),
+                      rest_of(v.w, p.y >> 16));
+    }
+  }
+}
+
+}  // namespace qlora
