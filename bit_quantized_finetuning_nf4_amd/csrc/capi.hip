@@ -536,7 +536,7 @@ size_t qlora_workspace_bytes(qlora_op op, int64_t M, int64_t N, int64_t K, int32
       if (!group_sizes_ok(M, N, K, r, njobs)) return 0;
       return dense_split_bytes(K, (int64_t)njobs * N, M);
     case QLORA_OP_FWD_DROP:
-      if (M <= 0 || N <= 0 || K <= 0 || r <= 0 || r > kMaxRank) return 0;
+      if (M <= 0 || N <= 0 || K <= 0 || K % 64 != 0 || r <= 0 || r > kMaxRank) return 0;
       if (M > 0x7FFFFFFF / K || M > 0x7FFFFFFF / N) return 0;
       return std::max(drop_fwd_layout(M, N, K, r, drop_fwd_staged(M, N, K)).total,
                       fwd_layout(M, N, K, r, staged_ok(M, N, K)).total);
