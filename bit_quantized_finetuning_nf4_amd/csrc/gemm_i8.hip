@@ -12,6 +12,7 @@
 // the 32x32x16 bf16 one.  After the loop the sums become fp32 in the
 // registers that held them.
 #include <algorithm>
+#include <cmath>
 
 #include "dense_tile.h"
 
@@ -356,20 +357,51 @@ hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, int split
 
 }  // namespace
 
-// Up to 16 tokens: the streaming kernel, 16 channels per workgroup, or 32
-// where that still fills the card and there are enough tokens for their
-// second reading to cost (16 x 8192 x 8192: 17.8 against 19.9 us, 16 x 22016 x
-// 8192: 41 against 47; one token at 22016 x 8192: 37 against 34).  17 to 32
-// tokens: the same with two token groups, below 16384 channels (32 x 8192 x
-// 8192: 19.8 against 21.3 us on 64 x 64 tiles, 32 x 22016 x 8192: 54 against
-// 45).  More: tiles (64 x 4096 x 4096: 10.6 against 12.1 us), the small ones or
-// 256 x 64 FI; or whole rounds of 256 x 256 tiles and the rest of the channels
-// apart.
+// Up to 32 tokens: the streaming kernel, or tiles (split where that pays and
+// there is room), whichever is estimated to take less.  The streaming kernel
+// takes 16 channels a workgroup, or 32 where that still fills the card and
+// there are enough tokens for their second reading to cost; a round of
+// workgroups costs by its batches of lines, and whole rounds up to two (a
+// workgroup fills a CU), less than whole ones past that.  Neither goes below
+// the weight's bytes at 4.8 TB/s.  Measured in us at 57 sizes, where the choice
+// is within 0.7 % of the faster on the mean (tokens x channels x K, streaming
+// and tiles):
+//   1 x 22016 x 8192    34.5  44.8     16 x 8192 x 8192    17.7  20.6
+//   8 x 4096 x 16384    17.5  20.8     16 x 5120 x 13824   29.8  18.7
+//   16 x 4096 x 4096     6.5   8.7     1 x 256 x 22016     14.1   9.7
+//   24 x 4096 x 4096     7.4   9.1     32 x 5120 x 5120    25.8  11.4
+//   20 x 8192 x 2048     6.2   7.5     32 x 22016 x 8192   54.5  46.2
+namespace {
+
+constexpr int64_t kSkinnyTokens = 32;
+constexpr int kSplitCus = 256;   // the workspace is sized for it (choose_tile)
+
+double skinny_cost(int64_t M, int64_t N, int64_t lines, int cus) {
+  const bool wide = M > 8 && N >= 8192;   // 32 channels a workgroup
+  const double x = (double)((N + (wide ? 31 : 15)) / (wide ? 32 : 16)) / cus;
+  const double rounds = x <= (M > 8 && M <= 16 && wide ? 1.0 : 2.0) ? std::ceil(x) : 0.46 * (x + std::ceil(x));
+  const double l16 = (double)((lines + 15) / 16 * 16);
+  if (M > 16) return rounds * (wide ? 1.5 + 0.3 * l16 : 2.0 + 5.7 * (double)((lines + 31) / 32));
+  const double round = M <= 8 ? 2.2 + 0.073 * l16 : wide ? 0.5 + 0.26 * l16 : 2.4 + 0.113 * l16;
+  return std::max(rounds * round, (double)N * lines * 128.0 / 4.8e6 + 2.0);
+}
+bool use_skinny(int64_t M, int64_t N, int64_t lines, int cus, size_t part_bytes) {
+  if (M > kSkinnyTokens) return false;
+  const double cost = skinny_cost(M, N, lines, cus), least = (double)N * lines * 128.0 / 4.8e6 + 4.0;   // of tiles
+  return cost <= least || cost <= choose_tile(M, N, lines, cus, part_bytes).cost + 1.5;
+}
+
+}  // namespace
+
+// More tokens: tiles, the small ones or 256 x 64 FI; or whole rounds of 256 x
+// 256 tiles and the rest of the channels apart.
 hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, float* part, size_t part_bytes) {
-  if (g.M <= 16) return g.M > 8 && g.N >= 8192 ? launch_skinny<2, 1, 2>(g, st) : launch_skinny<1, 1, 2>(g, st);
-  if (g.M <= 32 && g.N < 16384) return g.N < 8192 ? launch_skinny<1, 2, 4>(g, st) : launch_skinny<2, 2, 2>(g, st);
   const int cus = device_cu_count();
   const int64_t lines = i8_row_bytes(g.K) / 128;
+  if (use_skinny(g.M, g.N, lines, cus, part ? part_bytes : 0)) {
+    if (g.M <= 16) return g.M > 8 && g.N >= 8192 ? launch_skinny<2, 1, 2>(g, st) : launch_skinny<1, 1, 2>(g, st);
+    return g.N < 8192 ? launch_skinny<1, 2, 4>(g, st) : launch_skinny<2, 2, 2>(g, st);
+  }
   auto part_of = [&](const TileChoice& c, int64_t n_begin, int64_t n_rows) {
     if (c.tm == 256)
       return c.tn == 256   ? launch_fi<4>(g, n_begin, n_rows, c.splits, part, st)
@@ -396,7 +428,8 @@ hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, float* part, size_t p
 }
 
 size_t i8_gemm_part_bytes(int64_t M, int64_t N, int64_t K) {
-  return M <= 32 ? 0 : tile_part_bytes(M, N, i8_row_bytes(K) / 128);
+  const int64_t lines = i8_row_bytes(K) / 128;
+  return use_skinny(M, N, lines, kSplitCus, (size_t)1 << 62) ? 0 : tile_part_bytes(M, N, lines);
 }
 
 }  // namespace qlora

@@ -81,6 +81,42 @@ def test_i8_forward(name, r):
     within(Y, ref, 1.01 * tol, "Y")
 
 
+# up to 32 tokens: the streaming kernel in its widths, batches whole and partial, rounds whole and partial; and where
+# tiles, split or not, take over
+FEW = [(1, 1024, 8072), (2, 6152, 8192), (7, 4096, 16264), (8, 8200, 1160), (9, 16392, 2048), (16, 8192, 8072),
+       (11, 28680, 640), (16, 4104, 1000), (17, 1000, 2968), (24, 4096, 4096), (32, 4104, 3000), (20, 8192, 1960),
+       (1, 256, 22016), (8, 13824, 5120), (16, 5120, 13824), (16, 264, 22016), (20, 512, 8192), (32, 1024, 1024),
+       (32, 5128, 5120), (24, 11008, 4096), (32, 16392, 4096)]
+
+
+@pytest.mark.parametrize("M,N,K", FEW)
+@pytest.mark.parametrize("r", [0, 40])
+def test_i8_forward_of_few_tokens(M, N, K, r):
+    print(f"[few i8] M{M} N{N} K{K} r{r}", flush=True)
+    rng = np.random.default_rng(M + N + r)
+    W, Wr = bf16(rng, (N, K), 0.02)
+    X, Xr = bf16(rng, (M, K))
+    (wc, ws), (xc, sx) = OI.i8_quantize(Wr), OI.i8_quantize(Xr)
+    main = OI.i8_matmul(xc, sx, wc, ws)
+    w = ops.i8_quantize(W)
+    # without a workspace nothing is split: the exact sum, the scales' product and their product rounded
+    within(ops.i8_matmul(ops.i8_quantize(X), w), main, 1.01 * (E + 3.01 * 2.0**-24) * np.abs(main), "matmul")
+    parts = 34 * 2.0**-24 * (np.abs(xc.astype(np.float64)) @ np.abs(wc.astype(np.float64)).T) * sx[:, None] * ws[None, :]
+    if r == 0:
+        within(ops.i8_linear_fwd(w, X), main, 1.01 * (E * np.abs(main) + parts), "Y")
+        return
+    A, Ar = bf16(rng, (r, K), 0.1)
+    B, Br = bf16(rng, (N, r), 0.1)
+    Y, U = ops.i8_linear_fwd(w, X, A, B, 16.0, save_u=True)
+    s, Ur = 16.0 / r, Xr @ Ar.T
+    u_err = K * F * (np.abs(Xr) @ np.abs(Ar).T)
+    within(U, Ur, 1.01 * (E * np.abs(Ur) + 2 * u_err), "U")
+    ref = main + s * (Ur @ Br.T)
+    tol = (E * np.abs(ref) + parts
+           + s * ((2.01 * E * np.abs(Ur) + 2 * u_err) @ np.abs(Br).T + (r + 34) * F * (np.abs(Ur) @ np.abs(Br).T)))
+    within(Y, ref, 1.01 * tol, "Y")
+
+
 @pytest.mark.parametrize("name", SIZES)
 def test_nf4_forward_under_dropout(name):
     M, N, lines = SIZES[name]
