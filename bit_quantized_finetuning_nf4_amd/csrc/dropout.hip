@@ -7,7 +7,7 @@
 // store each, kUnroll groups with their loads issued together, so that
 // the generator's products run while the loads are in flight.  4096 x 22016:
 // 65.5 us, 5.5 TB/s (a large copy reaches 4.8: part of the input is still in
-// the last-level cache from the call before); one row of 8192: 1.7 us, a launch.
+// the last-level cache from the call before); one row of 4096: 1.7 us, a launch.
 #include "rng.h"
 
 namespace qlora {
