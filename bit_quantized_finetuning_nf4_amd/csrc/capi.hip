@@ -926,7 +926,7 @@ qlora_status qlora_i8_linear_fwd(const qlora_i8_rows* W, const uint16_t* X, int6
   bf16_t* U = r > 0 ? (U_save ? U_save : reinterpret_cast<bf16_t*>(ws_at(ws, L.u))) : nullptr;
   const DropArgs* dp = active ? &d : nullptr;
   float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
-  if (i8_prep_ok(M, K, r)) {
+  if (i8_prep_ok(M, K, r, active)) {
     st = hip_status(launch_i8_prep(X, M, K, A, r, dp, U, xq, sx, s));
   } else {
     Ride rest;

@@ -750,7 +750,8 @@ size_t adapter_part_bytes(int64_t M, int64_t N, int64_t K, int r) {
 }
 
 size_t u_part_bytes(int64_t M, int64_t K, int r) {
-  return u_rows_ok(M, r) ? 0 : part_bytes(rows_split(M, K), M * r);
+  // (with or without the mask)
+  return u_rows_ok(M, K, r, true) && u_rows_ok(M, K, r, false) ? 0 : part_bytes(rows_split(M, K), M * r);
 }
 
 namespace {
@@ -783,7 +784,7 @@ Ride sum_ride(RideKind kind, const float* part, const Split& sp, int64_t n, floa
 hipError_t start_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
                           float* part, bf16_t* out, Ride* rest, hipStream_t st) {
   const DropArgs d = drop ? *drop : DropArgs{};
-  if (u_rows_ok(M, r)) {
+  if (u_rows_ok(M, K, r, drop != nullptr)) {
     *rest = Ride{};
     rest->kind = drop ? kRideRowsDrop : kRideRows, rest->blocks = u_rows_blocks(M, r);
     rest->X = X, rest->A = A, rest->M = M, rest->K = K, rest->r = r, rest->drop = d, rest->out = out;

@@ -254,7 +254,7 @@ hipError_t launch_quant_rows(const bf16_t* X, int64_t M, int64_t K, int8_t* Q, f
   return hipGetLastError();
 }
 
-bool i8_prep_ok(int64_t M, int64_t K, int r) { return u_rows_ok(M, r) && i8_row_bytes(K) <= 32768; }
+bool i8_prep_ok(int64_t M, int64_t K, int r, bool drop) { return u_rows_ok(M, K, r, drop) && i8_row_bytes(K) <= 32768; }
 
 hipError_t launch_i8_prep(const bf16_t* X, int64_t M, int64_t K, const bf16_t* A, int r, const DropArgs* drop,
                           bf16_t* U, int8_t* Q, float* scale, hipStream_t st) {

@@ -178,7 +178,7 @@ hipError_t launch_quant_rows(const bf16_t* X, int64_t M, int64_t K, int8_t* Q, f
                              hipStream_t st);
 // U [M x r] = drop(X) A^T (r may be 0, drop null) and X quantized, in one
 // launch, where i8_prep_ok.
-bool i8_prep_ok(int64_t M, int64_t K, int r);
+bool i8_prep_ok(int64_t M, int64_t K, int r, bool drop);
 hipError_t launch_i8_prep(const bf16_t* X, int64_t M, int64_t K, const bf16_t* A, int r, const DropArgs* drop,
                           bf16_t* U, int8_t* Q, float* scale, hipStream_t st);
 hipError_t launch_i8_dequant(const int8_t* Q, const float* scale, int64_t N, int64_t K, bf16_t* out, hipStream_t st);

@@ -1,7 +1,7 @@
 // urows.h -- U = drop(X) A^T for few tokens or a small rank, without partial
 // sums: a workgroup takes one rank row and up to four tokens and forms their
 // fp32 dot products, each thread over every 256th group of eight columns.  A
-// is read once per four tokens and X r times (from L2), so it pays while M r
+// is read once per four tokens and X r times (from L2), so it pays while M K r
 // is small; past that the MFMA product with split partials does (gemm.hip),
 // which is two launches.  Four tokens: with 16 a workgroup brings 256 KiB at K
 // = 8192 (16 tokens at rank 64 with their quantization and product: 15.8 us
@@ -78,10 +78,18 @@ __device__ __forceinline__ void u_rows(const bf16_t* __restrict__ X, int64_t M, 
 }
 
 inline int u_rows_blocks(int64_t M, int r) { return r * (int)((M + kURowTokens - 1) / kURowTokens); }
-// U with the tokens' quantization and a small product, in us, here and by
-// MFMA: 128 x 4096 at rank 64 15.2 and 20.0, 64 x 8192 at rank 128 21.1 and 27.7,
-// 512 x 4096 at rank 16 17.6 and 19.4; but 1024 x 4096 at rank 8 23.1 and 20.9,
-// 256 x 4096 at rank 64 under the mask 27.1 and 22.7.
-inline bool u_rows_ok(int64_t M, int r) { return M * r <= 8192 && M <= 512; }
+// Where that takes less than the MFMA product: a workgroup's loads, and under
+// the mask its Philox blocks, grow with M K r, the MFMA product's launch and
+// its walk along K do not.  Fitted to both at 170 sizes each, 1 to 512 tokens,
+// K 1024 to 22016, ranks 8 to 128, where it is within 0.1 % of the faster on
+// the mean.  With the tokens' quantization and a 64-channel product, in us,
+// here and by MFMA (then under the mask):
+//    16 x  4096 r  64  10.2 12.6 (10.9 14.3)    128 x  4096 r 64  15.6 15.6 (20.7 17.4)
+//     1 x 22016 r 128  15.6 22.5 (16.0 27.5)    256 x 12288 r 32  25.4 20.1 (37.9 23.7)
+//   512 x  1024 r   8   9.3 10.8 (10.0 11.9)    512 x 22016 r 16  45.5 28.7 (58.3 32.0)
+inline bool u_rows_ok(int64_t M, int64_t K, int r, bool drop) {
+  if (M > 512) return false;
+  return drop ? M * K * (r + 8) <= 14000000 + 2000 * K : M * K * (r + 10) <= 14000000 + 3400 * K;
+}
 
 }  // namespace qlora
