@@ -28,48 +28,61 @@
 namespace qlora {
 namespace {
 
-// The masked LoRA tail of a tile: acc += s drop'(T A) over tokens row0 .. and
-// columns col0 .., A [r x cols] read transposed, T [M x r], r <= 128.  All
-// chunks of the rank are in LDS (chunk c at 2 kOp c), so a 32 x 32 block's
-// product is summed in 16 registers of its own, masked, and added: the tile
-// keeps one set of accumulators.  Masked dX of 4096 x 22016 x 8192 at rank 64
-// 1221 us, 1.21 PFLOP/s; of 2048 x 4096 x 4096 69 us (one round of 256 x 128
-// tiles, 1.0 PFLOP/s).
-template <int FI, int NT>
-__device__ __forceinline__ void masked_tail(f32x16_t (&acc)[FI][4], const char* smem, float s,
-                                            const DropKey& key, int64_t cols, int64_t row0, int64_t col0) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1, lr = lane & 31;
+// The masked LoRA tail of a tile: acc += s drop'(T A), A [r x cols] read
+// transposed, T [M x r], r <= 128.  The nt chunks of the rank are in LDS (chunk c
+// at 2 kOp c), so the products of four 32 x 32 blocks at a time are summed in
+// registers of their own, masked by their bits (block 4 i + j of the wave at
+// bits + 1 KiB (4 i + j)), and added: the tile keeps one set of accumulators.
+// Masked dX of 4096 x 22016 x 8192 at rank 64 1.2 PFLOP/s; 2048 x 4096 x 4096
+// 69 us (one round of 256 x 128 tiles, 1.0 PFLOP/s).  With a block at a time,
+// its mask computed here, the whole backward of 3918 x 20856 x 800 at rank 128
+// took 438 us, 383 this way.
+template <int FI>
+__device__ __forceinline__ void masked_tail(f32x16_t (&acc)[FI][4], const char* smem, int nt, float s,
+                                            const char* bits) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1;
   const FragOffs fo = frag_offs(lane);
-  const int bm64 = wr * 128 * 64;
+  const char* tok = smem + kOp + wr * 128 * 64;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    bf16x8_t b[2 * NT];
+  for (int i = 0; i < FI; ++i) {   // four blocks at a time
+    f32x16_t y[4];
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      const char* tok = smem + c * 2 * kOp + kOp + bm64 + j * 2048;
-      b[2 * c] = rd16(tok + fo.o0);
-      b[2 * c + 1] = rd16(tok + fo.o1);
-    }
-    // Philox block of column col0 + 32 FI wc of the lane's token, M cols < 2^31
-    const uint32_t row_block =
-        (uint32_t)(row0 + 128 * wr + 32 * j + lr) * (uint32_t)(cols >> 3) + (uint32_t)((col0 + 32 * FI * wc) >> 3);
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int i = 0; i < FI; ++i) {
-      f32x16_t t;
+      for (int e = 0; e < 16; ++e) y[j][e] = 0.0f;
+    for (int c = 0; c < nt; ++c) {
+      bf16x8_t b0[4], b1[4], f0, f1;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) t[e] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        const char* a0 = smem + c * 2 * kOp + tr_off<512>(wc * FI + i);
-        bf16x8_t f0, f1;
-        tr_read2<2048, 2048>(a0, a0 + 16 * 512, f0, f1);
-        t = mfma32x32x16(f0, b[2 * c], t);
-        t = mfma32x32x16(f1, b[2 * c + 1], t);
+      for (int j = 0; j < 4; ++j) {
+        b0[j] = rd16(tok + c * 2 * kOp + j * 2048 + fo.o0);
+        b1[j] = rd16(tok + c * 2 * kOp + j * 2048 + fo.o1);
       }
-      mask_block(t, row_block + 4u * i, key);
+      const char* a0 = smem + c * 2 * kOp + tr_off<512>(wc * FI + i);
+      tr_read2<2048, 2048>(a0, a0 + 16 * 512, f0, f1);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(s, t[e], acc[i][j][e]);
-      __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
+      for (int j = 0; j < 4; ++j) y[j] = mfma32x32x16(f0, b0[j], y[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = mfma32x32x16(f1, b1[j], y[j]);
+    }
+    uint32_t keep[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      keep[j] = *reinterpret_cast<const uint32_t*>(bits + 1024 * (4 * i + j) + 4 * threadIdx.x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // back into the accumulator registers at once: the compiler would keep
+      // the sums in vector registers, and spill
+      float f[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) f[e] = fmaf(s, masked(y[j][e], keep[j], e), acc[i][j][e]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float v;
+        asm volatile("v_accvgpr_write_b32 %0, %1" : "=a"(v) : "v"(f[e]));
+        acc[i][j][e] = v;
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
@@ -170,11 +183,28 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
     F.b0[i] = rd16(smem + kPairOp + bm + i * 32 * 128 + po.o[0][0]);
   }
   // K % 64 == 0: whole pairs of 32-wide stages
+  // DR: the mask of the wave's block b = 4 i + j, a word per lane past the pair
+  // slots; only the thread that wrote it reads it
+  [[maybe_unused]] DropKey key;
+  [[maybe_unused]] uint32_t block00 = 0u, block_row = 0u;   // M N < 2^31
+  if constexpr (DR) {
+    key = drop_key(drop);
+    block_row = (uint32_t)(N >> 3);
+    block00 = (uint32_t)(m0 + 128 * wr + (lane & 31)) * block_row + (uint32_t)((n0 + 32 * FI * wc) >> 3);
+  }
+  [[maybe_unused]] auto put_bits = [&](int b) __attribute__((always_inline)) {
+    *reinterpret_cast<uint32_t*>(smem + kLdsPairs + 1024 * b + 4 * t) =
+        mask_bits(block00 + 32u * (uint32_t)(b & 3) * block_row + 4u * (uint32_t)(b >> 2), key);
+  };
   for (int pr = 0; pr < f.npair; ++pr) {
     char* cur = smem + (pr & 1) * kPairSlot;
     char* nxt = smem + ((pr & 1) ^ 1) * kPairSlot;
     __builtin_amdgcn_sched_barrier(0);
     dense_slots<MmBf16, FI, 0, 0>(cur, nxt, cur, f, pr, acc, F, am, bm, po);
+    if constexpr (DR) {
+      // one block's mask a pair, while the next pair's lines are on their way
+      if (tail && pr < 4 * FI) put_bits(pr);
+    }
     __builtin_amdgcn_sched_barrier(0);
     dense_slots<MmBf16, FI, 1, 0>(cur, nxt, cur, f, pr, acc, F, am, bm, po);
   }
@@ -182,6 +212,10 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
   QLORA_WAIT(0, 0);
   __builtin_amdgcn_s_barrier();
 
+  if constexpr (DR) {
+    if (tail)
+      for (int b = f.npair; b < 4 * FI; ++b) put_bits(b);   // a contraction of fewer pairs than blocks
+  }
   const FragOffs fo = frag_offs(lane);
   const int am64 = wc * 32 * FI * 64, bm64 = wr * 128 * 64;
   // acc += the chunk at buf (weights at buf, tokens at buf + kOp); the tokens
@@ -220,7 +254,7 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
   };
   if constexpr (DR) {
     if (tail) {
-      const int nt = r <= 32 ? 1 : r <= 64 ? 2 : 4;
+      const int nt = (r + 31) / 32;
       if constexpr (TD) {
         const TailSrc ts = tail_src();
         for (int c = 0; c < nt; ++c) tail_dma(smem + c * 2 * kOp, ts, c, f.w, lane);
@@ -233,13 +267,7 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
       }
       QLORA_WAIT(0, 0);
       __syncthreads();
-      const DropKey key = drop_key(drop);
-      if (nt == 1)
-        masked_tail<FI, 1>(acc, smem, s, key, N, m0, n0);
-      else if (nt == 2)
-        masked_tail<FI, 2>(acc, smem, s, key, N, m0, n0);
-      else
-        masked_tail<FI, 4>(acc, smem, s, key, N, m0, n0);
+      masked_tail<FI>(acc, smem, nt, s, smem + kLdsPairs);
     }
   } else if constexpr (TD) {
     if (tdma) {
@@ -323,13 +351,10 @@ hipError_t launch_fi(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, in
                      int64_t n_rows, hipStream_t st, const DropArgs* drop, int splits = 1, float* part = nullptr) {
   const int tiles_n = (int)((n_rows + 64 * FI - 1) / (64 * FI));
   const int tiles_m = (int)((M + kTile - 1) / kTile);
-  // masked_tail takes 1, 2 or 4 chunks: the fourth of rank 96 is zeroed through
-  // registers (by DMA its tokens would be the next rows', whose infinities times
-  // the weight side's zeros are NaN)
-  const bool td = tail_by_dma(N, M, r, ldu, gn, n_begin, tiles_n, 64 * FI) && !(drop && r == 96);
+  const bool td = tail_by_dma(N, M, r, ldu, gn, n_begin, tiles_n, 64 * FI);
   auto* fn = drop ? (td ? &bf16_fwd_kernel<FI, true, true> : &bf16_fwd_kernel<FI, false, true>)
                   : (td ? &bf16_fwd_kernel<FI, true, false> : &bf16_fwd_kernel<FI, false, false>);
-  const size_t lds = td && !drop ? kLdsDense : kLdsPairs;
+  const size_t lds = drop ? kLdsPairs + 4096 * FI : td ? kLdsDense : kLdsPairs;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
   if (e != hipSuccess) return e;
   const int npair = (int)(K >> 6);

@@ -205,7 +205,9 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
 #pragma unroll
         for (int j = 0; j < FJ; ++j) {
           const uint32_t m = (uint32_t)(m0 + 32 * (FJ * wr + j) + lr);
-          mask_block(y[i][j], m * (uint32_t)(N >> 3) + (uint32_t)((n0 + 32 * (FI * wc + i)) >> 3), key);
+          const uint32_t bits = mask_bits(m * (uint32_t)(N >> 3) + (uint32_t)((n0 + 32 * (FI * wc + i)) >> 3), key);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[i][j][e] = masked(y[i][j][e], bits, e);
         }
     }
   }

@@ -80,32 +80,34 @@ __device__ __forceinline__ u32x4_t drop8(u32x4_t v, uint64_t block, const DropKe
                  v.w & keep_halves(w.w, k.thr)};
 }
 
-
-// A 32-channel x 32-token block in the layout of a 32x32 MFMA (lane (lr, h):
-// token lr, channels 8 q + 4 h .. + 3 in elements 4 q ..), masked: block0 is
-// the Philox block of the token's first channel.  A lane holds half of a
-// block's eight elements and its two lane halves the two halves, so the lower
-// half computes the block of channel group 2 p, the upper one that of
-// 2 p + 1, and v_permlane32_swap hands each half its four elements of both.
-__device__ __forceinline__ void mask_block(f32x16_t& t, uint32_t block0, const DropKey& key) {
+// The mask of a 32-channel x 32-token block in the layout of a 32x32 MFMA (lane
+// (lr, h): token lr, channels 8 q + 4 h .. + 3 in elements 4 q ..), a bit per
+// element: element e at bit 8 + e / 2 + 16 (e mod 2).  block0 is the Philox
+// block of the token's first channel.  A lane holds half of a block's eight
+// elements and its two lane halves the two halves, so the lower half computes
+// the block of channel group 2 p, the upper one that of 2 p + 1, and
+// v_permlane32_swap hands each half its four elements of both.
+__device__ __forceinline__ uint32_t mask_bits(uint32_t block0, const DropKey& key) {
   const int h = (threadIdx.x >> 5) & 1;
-  const int thr = key.thr << 16;   // a half, as a signed number in the high bits
+  const short t = (short)(key.thr - 1);
+  uint32_t bits = 0u;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const u32x4_t x = philox(block0 + (uint32_t)(2 * p + h), key);
     const auto x0 = __builtin_amdgcn_permlane32_swap(x.x, x.z, false, false);
     const auto x1 = __builtin_amdgcn_permlane32_swap(x.y, x.w, false, false);
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int wd[2] = {(int)x0[g], (int)x1[g]};
+    for (int g = 0; g < 2; ++g)
 #pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const int e = 8 * p + 4 * g + 2 * d;
-        t[e] = (wd[d] << 16) >= thr ? t[e] : 0.0f;
-        t[e + 1] = wd[d] >= thr ? t[e + 1] : 0.0f;
+      for (int d = 0; d < 2; ++d) {   // the signs of both halves' differences, as in keep_halves
+        const s16x2_t v = __builtin_bit_cast(s16x2_t, d == 0 ? (uint32_t)x0[g] : (uint32_t)x1[g]);
+        bits = bits >> 1 | (__builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(s16x2_t{t, t}, v)) & 0x80008000u);
       }
-    }
   }
+  return bits;
+}
+__device__ __forceinline__ float masked(float v, uint32_t bits, int e) {
+  return u2f(f2u(v) & (uint32_t)__builtin_amdgcn_sbfe((int)bits, 8 + e / 2 + 16 * (e & 1), 1));
 }
 
 }  // namespace qlora
