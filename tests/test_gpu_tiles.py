@@ -27,7 +27,7 @@ SIZES = {
 
 
 @pytest.mark.parametrize("name", SIZES)
-@pytest.mark.parametrize("r,p", [(0, 0.0), (24, 0.0), (24, 0.3), (64, 0.1)])
+@pytest.mark.parametrize("r,p", [(0, 0.0), (24, 0.0), (24, 0.3), (64, 0.1), (96, 0.2), (128, 0.0), (128, 0.6)])
 def test_dx(name, r, p):
     M, K, lines = SIZES[name]
     N = 64 * lines
