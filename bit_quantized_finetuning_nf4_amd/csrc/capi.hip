@@ -792,17 +792,19 @@ qlora_status check_bwd(int64_t M, int64_t N, int64_t K, const uint16_t* X, const
   return QLORA_OK;
 }
 
-// deq(W)^T of either format: out [K x ldo], the columns past N zero; with G's
-// last step if there is one.
-qlora_status weight_t(const qlora_nf4_weight* W, const qlora_i8_rows* W8, bf16_t* out, int64_t ldo, const Ride* rest,
+// deq(W)^T of either format: out [K x ldo], the columns past N zero; with what
+// rides along (G's last step, padded rows).
+qlora_status weight_t(const qlora_nf4_weight* W, const qlora_i8_rows* W8, bf16_t* out, int64_t ldo, Ride rest,
                       hipStream_t s) {
   if (W8) return hip_status(launch_i8_dequant_t(W8->codes, W8->scale, W8->rows, W8->cols, out, ldo, rest, s));
   const int64_t N = W->rows, K = W->cols;
-  const qlora_status st = hip_status(
-      rest ? launch_dequant_t_ride(view(W), out, ldo, *rest, s)
-           : launch_dequant_t(W->codes, W->absmax_q, W->group_scale, N, K, W->codebook, W->absmax_format, out, ldo, s));
-  if (st != QLORA_OK || ldo == N) return st;
-  return hip_status(launch_pad_rows(nullptr, K, N, out, ldo, s));
+  if (ldo != N) {
+    rest.pad[1] = pad_rows(nullptr, K, N, out, ldo);
+    rest.blocks += rest.pad[1].blocks;
+  }
+  return hip_status(rest.blocks > 0 ? launch_dequant_t_ride(view(W), out, ldo, rest, s)
+                                    : launch_dequant_t(W->codes, W->absmax_q, W->group_scale, N, K, W->codebook,
+                                                       W->absmax_format, out, ldo, s));
 }
 
 // The staged backward's launches on validated arguments, for the weight W or
@@ -824,7 +826,8 @@ qlora_status run_bwd(const qlora_nf4_weight* W, const qlora_i8_rows* W8, int64_t
     if ((st = hip_status(launch_ride(rest, s))) != QLORA_OK) return st;
     U = Ud;
   }
-  Ride rest;
+  Ride rest{};
+  rest.kind = kRideSum3;
   auto start_g = [&]() { return hip_status(start_dyb_parts(dY, B, M, N, r, part, G, &rest, s)); };
   auto run_g = [&]() {
     const qlora_status e = start_g();
@@ -837,12 +840,13 @@ qlora_status run_bwd(const qlora_nf4_weight* W, const qlora_i8_rows* W8, int64_t
     // push dY out of the last-level cache and G goes after it
     const bool late = dy_late(M, N) && (np * K + M * N) * 2 > ((int64_t)256 << 20);
     if (r > 0 && !late && (st = start_g()) != QLORA_OK) return st;
-    if ((st = weight_t(W, W8, WdT, np, r > 0 && !late ? &rest : nullptr, s)) != QLORA_OK) return st;
     if (np != N) {
       bf16_t* dyp = reinterpret_cast<bf16_t*>(ws_at(ws, L.dyp));
-      if ((st = hip_status(launch_pad_rows(dY, M, N, dyp, np, s))) != QLORA_OK) return st;
+      rest.pad[0] = pad_rows(dY, M, N, dyp, np);
+      rest.blocks += rest.pad[0].blocks;
       g = dyp;
     }
+    if ((st = weight_t(W, W8, WdT, np, rest, s)) != QLORA_OK) return st;
     if (r > 0 && late && (st = run_g()) != QLORA_OK) return st;
     float* split = reinterpret_cast<float*>(ws_at(ws, L.split));
     st = hip_status(launch_staged(WdT, K, np, g, M, r > 0 ? G : nullptr, r > 0 ? A : nullptr, true, r, sc,

@@ -353,7 +353,7 @@ template <int RP, bool DB, int PARTS, bool DROP>
 __device__ __forceinline__ void cskinny(int block, int g, int groups, char* smem, const bf16_t* __restrict__ Big, int64_t M,
                                         int64_t C, int64_t ldb, int64_t big_gs, const bf16_t* __restrict__ Sm, int r,
                                         int lds, int64_t sm_gs, int stages_per_split, int tiles_c,
-                                        float* __restrict__ part, int64_t sm_part, const DropArgs& drop) {
+                                        float* __restrict__ part, int64_t sm_part, const DropArgs& drop, float scale) {
   static_assert(PARTS == 1 || (PARTS == 3 && !DB && RP <= 128), "three-part rank side: dA of one adapter");
   using S = ColShape<RP, PARTS>;
   constexpr int kRing = S::kRing, kAhead = S::kAhead;
@@ -490,13 +490,15 @@ __device__ __forceinline__ void cskinny(int block, int g, int groups, char* smem
         const int64_t c = c0 + 32 * w + 8 * q + 4 * h;
         if (j < r && c < C)
           *reinterpret_cast<float4*>(out + j * C + c) =
-              make_float4(acc[f][4 * q], acc[f][4 * q + 1], acc[f][4 * q + 2], acc[f][4 * q + 3]);
+              make_float4(acc[f][4 * q] * scale, acc[f][4 * q + 1] * scale, acc[f][4 * q + 2] * scale,
+                          acc[f][4 * q + 3] * scale);
       } else {               // D[j][c]: j = 32 f + 8 q + 4 h + 0..3, c = c0 + 32 w + lr -> dB[c][j..]
         const int j = 32 * f + 8 * q + 4 * h;
         const int64_t c = c0 + 32 * w + lr;
         if (j < r && c < C)
           *reinterpret_cast<float4*>(out + c * r + j) =
-              make_float4(acc[f][4 * q], acc[f][4 * q + 1], acc[f][4 * q + 2], acc[f][4 * q + 3]);
+              make_float4(acc[f][4 * q] * scale, acc[f][4 * q + 1] * scale, acc[f][4 * q + 2] * scale,
+                          acc[f][4 * q + 3] * scale);
       }
     }
 }
@@ -509,7 +511,7 @@ __global__ __launch_bounds__(kThreads, 1) void cskinny_kernel(const bf16_t* __re
                                                               float* __restrict__ part) {
   extern __shared__ __align__(16) char smem[];
   cskinny<RP, DB, 1, false>(blockIdx.x, blockIdx.y, gridDim.y, smem, Big, M, C, ldb, big_gs, Sm, r, lds, sm_gs,
-                            stages_per_split, tiles_c, part, 0, DropArgs{});
+                            stages_per_split, tiles_c, part, 0, DropArgs{}, 1.0f);
 }
 
 // Both gradients of one adapter in one launch, dA's workgroups first: apart
@@ -519,7 +521,8 @@ struct GradArgs {
   const bf16_t *X, *dY, *G3, *U;
   int64_t M, N, K;
   int r, sps_a, tiles_a, blocks_a, sps_b, tiles_b;
-  float *part_a, *part_b;
+  float *part_a, *part_b;   // dA, dB themselves where one split is all
+  float scale_a, scale_b;   // 1 where there are more
   DropArgs drop;
 };
 template <int RP, bool DROP>
@@ -528,10 +531,10 @@ __global__ __launch_bounds__(kThreads, 1) void adapter_grads_kernel(GradArgs p) 
   const int id = blockIdx.x;
   if (id < p.blocks_a)
     cskinny<RP, false, 3, DROP>(id, 0, 1, smem, p.X, p.M, p.K, p.K, 0, p.G3, p.r, p.r, 0, p.sps_a, p.tiles_a, p.part_a,
-                                p.M * p.r, p.drop);
+                                p.M * p.r, p.drop, p.scale_a);
   else
     cskinny<RP, true, 1, false>(id - p.blocks_a, 0, 1, smem, p.dY, p.M, p.N, p.N, 0, p.U, p.r, p.r, 0, p.sps_b,
-                                p.tiles_b, p.part_b, 0, p.drop);
+                                p.tiles_b, p.part_b, 0, p.drop, p.scale_b);
 }
 
 __global__ __launch_bounds__(kThreads) void reduce_kernel(const float* __restrict__ part, int splits, int64_t n,
@@ -830,7 +833,10 @@ hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t*
   const Split sa = cols_split(K, M), sb = cols_split(N, M);
   const int64_t na = (int64_t)r * K, nb = N * r;
   float* part_b = part + (part_bytes(sa, na) + 255) / 256 * 256 / sizeof(float);
-  const GradArgs p{X, dY, G3, U, M, N, K, r, sa.sps, sa.tiles, sa.tiles * sa.splits, sb.sps, sb.tiles, part, part_b,
+  const bool whole_a = sa.splits == 1, whole_b = sb.splits == 1;
+  const float scale_a = drop ? scale * drop->scale : scale;
+  const GradArgs p{X, dY, G3, U, M, N, K, r, sa.sps, sa.tiles, sa.tiles * sa.splits, sb.sps, sb.tiles,
+                   whole_a ? dA : part, whole_b ? dB : part_b, whole_a ? scale_a : 1.0f, whole_b ? scale : 1.0f,
                    drop ? *drop : DropArgs{}};
   auto* fn = r <= 64 ? (drop ? &adapter_grads_kernel<64, true> : &adapter_grads_kernel<64, false>)
                      : (drop ? &adapter_grads_kernel<128, true> : &adapter_grads_kernel<128, false>);
@@ -838,8 +844,10 @@ hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t*
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(fn, dim3(p.blocks_a + sb.tiles * sb.splits), dim3(kThreads), lds, st, p);
-  hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(((na + nb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
-                     part, sa.splits, na, dA, part_b, sb.splits, nb, dB, drop ? scale * drop->scale : scale, scale);
+  const int64_t ra = whole_a ? 0 : na, rb = whole_b ? 0 : nb;
+  if (ra + rb == 0) return hipGetLastError();
+  hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(((ra + rb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
+                     part, sa.splits, ra, dA, part_b, sb.splits, rb, dB, scale_a, scale);
   return hipGetLastError();
 }
 

@@ -175,15 +175,15 @@ __global__ __launch_bounds__(256) void i8_dequant_kernel(const int8_t* __restric
 // WdT [K x ldo] = deq(W)^T, columns N .. ldo - 1 zero (ldo = N rounded up to
 // 64): 64 x 64 tiles through LDS.  Reads 64 bytes of 64 rows, writes 128
 // bytes of 64 rows.
-// The first sum3.blocks workgroups (0: none) add up the partials of G (ride.h).
+// The first rest.blocks workgroups (0: none) do what rides along (ride.h).
 __global__ __launch_bounds__(256) void i8_dequant_t_kernel(const int8_t* __restrict__ Q,
                                                            const float* __restrict__ scale, int64_t N, int64_t K,
                                                            int64_t ld, bf16_t* __restrict__ out, int64_t ldo,
-                                                           int tiles_k, Ride sum3) {
+                                                           int tiles_k, Ride rest) {
   __shared__ __align__(16) uint32_t tile[64][33];   // [column][row pair], one word of padding
-  const int id = (int)blockIdx.x - sum3.blocks;
+  const int id = (int)blockIdx.x - rest.blocks;
   if (id < 0) {
-    ride<kRideSum3>(sum3, blockIdx.x);
+    ride<kRideSum3>(rest, blockIdx.x);
     return;
   }
   const int by = id / tiles_k;
@@ -212,19 +212,6 @@ __global__ __launch_bounds__(256) void i8_dequant_t_kernel(const int8_t* __restr
       *reinterpret_cast<uint4*>(out + (k0 + k) * ldo + n0 + 8 * c) =
           make_uint4(tile[k][4 * c], tile[k][4 * c + 1], tile[k][4 * c + 2], tile[k][4 * c + 3]);
   }
-}
-
-// out [rows x ldo] = in [rows x cols] with zero columns cols .. ldo - 1 (in
-// may be null: only the zero columns are written); cols, ldo % 8 == 0.
-__global__ __launch_bounds__(256) void pad_rows_kernel(const bf16_t* __restrict__ in, int64_t rows, int64_t cols,
-                                                       bf16_t* __restrict__ out, int64_t ldo) {
-  const int64_t c0 = in ? 0 : cols >> 3, per = (ldo >> 3) - c0;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= rows * per) return;
-  const int64_t m = id / per, g = c0 + id - m * per;
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (8 * g < cols) v = *reinterpret_cast<const uint4*>(in + m * cols + 8 * g);
-  *reinterpret_cast<uint4*>(out + m * ldo + 8 * g) = v;
 }
 
 unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); }
@@ -282,18 +269,10 @@ hipError_t launch_i8_dequant(const int8_t* Q, const float* scale, int64_t N, int
 }
 
 hipError_t launch_i8_dequant_t(const int8_t* Q, const float* scale, int64_t N, int64_t K, bf16_t* out, int64_t ldo,
-                               const Ride* sum3, hipStream_t st) {
-  const Ride d = sum3 ? *sum3 : Ride{};
+                               const Ride& rest, hipStream_t st) {
   const int tiles_k = (int)((K + 63) / 64);
-  hipLaunchKernelGGL(i8_dequant_t_kernel, dim3((unsigned)(d.blocks + tiles_k * ((N + 63) / 64))), dim3(256), 0, st, Q,
-                     scale, N, K, i8_row_bytes(K), out, ldo, tiles_k, d);
-  return hipGetLastError();
-}
-
-hipError_t launch_pad_rows(const bf16_t* in, int64_t rows, int64_t cols, bf16_t* out, int64_t ldo, hipStream_t st) {
-  const int64_t per = in ? ldo >> 3 : (ldo - cols) >> 3;
-  if (per == 0) return hipSuccess;
-  hipLaunchKernelGGL(pad_rows_kernel, dim3(blocks_of(rows * per)), dim3(256), 0, st, in, rows, cols, out, ldo);
+  hipLaunchKernelGGL(i8_dequant_t_kernel, dim3((unsigned)(rest.blocks + tiles_k * ((N + 63) / 64))), dim3(256), 0, st,
+                     Q, scale, N, K, i8_row_bytes(K), out, ldo, tiles_k, rest);
   return hipGetLastError();
 }
 

@@ -131,6 +131,17 @@ size_t adapter_part_bytes(int64_t M, int64_t N, int64_t K, int r);
 // The last step of such a product, left to the caller: workgroups of a launch
 // that neither reads nor writes what it does (ride.h), or launch_ride.
 enum RideKind : int { kRideSum, kRideSum3, kRideRows, kRideRowsDrop };
+// out [rows x ld]: in [rows x cols] (null: nothing copied) and zero columns
+// cols .. ld - 1; cols, ld % 8 == 0.
+struct PadRows {
+  const bf16_t* in;
+  bf16_t* out;
+  int64_t rows, cols, ld;
+  int blocks;
+};
+inline PadRows pad_rows(const bf16_t* in, int64_t rows, int64_t cols, bf16_t* out, int64_t ld) {
+  return PadRows{in, out, rows, cols, ld, (int)((rows * (in ? ld >> 3 : (ld - cols) >> 3) + 255) / 256)};
+}
 struct Ride {
   RideKind kind;
   int blocks;                 // workgroups of 256
@@ -143,6 +154,7 @@ struct Ride {
   int64_t M, K;
   int r;
   DropArgs drop;
+  PadRows pad[2];             // kRideSum3: padded copies, too
 };
 hipError_t launch_ride(const Ride& a, hipStream_t st);
 // out [M x r] = drop(X) A^T: all but *rest (kRideSum, kRideRows or
@@ -182,13 +194,10 @@ bool i8_prep_ok(int64_t M, int64_t K, int r, bool drop);
 hipError_t launch_i8_prep(const bf16_t* X, int64_t M, int64_t K, const bf16_t* A, int r, const DropArgs* drop,
                           bf16_t* U, int8_t* Q, float* scale, hipStream_t st);
 hipError_t launch_i8_dequant(const int8_t* Q, const float* scale, int64_t N, int64_t K, bf16_t* out, hipStream_t st);
-// out [K x ldo] = deq^T, ldo = N rounded up to 64, the columns past N zero.
-// sum3: null, or a step of kRideSum3 to take along.
+// out [K x ldo] = deq^T, ldo = N rounded up to 64, the columns past N zero;
+// rest: of kRideSum3, possibly empty.
 hipError_t launch_i8_dequant_t(const int8_t* Q, const float* scale, int64_t N, int64_t K, bf16_t* out, int64_t ldo,
-                               const Ride* sum3, hipStream_t st);
-// out [rows x ldo]: in [rows x cols] (null: nothing copied) and zero columns
-// cols .. ldo - 1.
-hipError_t launch_pad_rows(const bf16_t* in, int64_t rows, int64_t cols, bf16_t* out, int64_t ldo, hipStream_t st);
+                               const Ride& rest, hipStream_t st);
 
 // Y [M x N] = sx sw^T o (Xq Wq^T) + s U B^T (r may be 0).
 struct I8Gemm {

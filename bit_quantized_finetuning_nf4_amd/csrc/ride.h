@@ -1,5 +1,5 @@
 // ride.h -- the last step of a small adapter product (U = drop(X) A^T, G = dY
-// B) as extra workgroups of the launch that comes next anyway, a
+// B), and copies of rows padded to whole stages, as extra workgroups of the launch that comes next anyway, a
 // dequantization or a quantization, which neither reads the product nor is
 // read by it.  Alone such a step is a launch of 3-5 us that leaves most of the
 // card idle: the backward of 2048 x 4096 x 4096 at rank 64 takes 107 us with it
@@ -42,12 +42,28 @@ __device__ __forceinline__ float rest_of(float v, uint32_t h) {
 //   kRideSum   bf16 of the splits' sum times scale
 //   kRideSum3  the sum as three bf16 parts, n elements apart: each the bf16
 //              rounding of what the parts before it left, together the fp32 sum
+//              (the workgroups after those that pad rows)
 //   kRideRows, kRideRowsDrop   U by rows (urows.h)
+__device__ __forceinline__ void pad_block(const PadRows& p, int block) {
+  const int64_t c0 = p.in ? 0 : p.cols >> 3, per = (p.ld >> 3) - c0;
+  const int64_t id = (int64_t)block * 256 + threadIdx.x;
+  if (id >= p.rows * per) return;
+  const int64_t m = id / per, g = c0 + id - m * per;
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (8 * g < p.cols) v = *reinterpret_cast<const uint4*>(p.in + m * p.cols + 8 * g);
+  *reinterpret_cast<uint4*>(p.out + m * p.ld + 8 * g) = v;
+}
 template <int KIND>
 __device__ __forceinline__ void ride(const Ride& a, int block) {
   if constexpr (KIND == kRideRows || KIND == kRideRowsDrop) {
     u_rows<KIND == kRideRowsDrop>(a.X, a.M, a.K, a.A, a.r, block, a.out, a.drop);
   } else {
+    if constexpr (KIND == kRideSum3) {
+      if (block < a.pad[0].blocks) return pad_block(a.pad[0], block);
+      block -= a.pad[0].blocks;
+      if (block < a.pad[1].blocks) return pad_block(a.pad[1], block);
+      block -= a.pad[1].blocks;
+    }
     const int64_t i = ((int64_t)block * 256 + threadIdx.x) * 4;
     if (i >= a.n) return;
     float4 v = sum_splits(a.part, a.splits, a.n, i, a.scale);
