@@ -16,13 +16,15 @@
 // times, so it is taken from kStagedMinTokens tokens on, when the workspace
 // holds the bf16 weight.
 //   GEMV        : per job, 128 fp32 for u = A x | the device job table
-//   BWD_DROP, I8_BWD : G as three bf16 parts [M x r] each | U bf16 [M x r] |
+//   BWD_DROP, I8_BWD : s G as three bf16 parts [M x r] each | U bf16 [M x r] |
 //                 split partials | deq(W)^T bf16 [K x Np] | dY bf16 [M x Np]
 //                 when N % 64 != 0 (Np = N rounded up to 64, zero columns) |
 //                 the dense product's split partials, if it splits
 //   I8_FWD      : X as 8-bit rows [M x i8_row_bytes(K)] | their scales fp32
-//                 [M] | U bf16 [M x r] | split partials of X A^T, then of
-//                 the product
+//                 [M] | s U as two bf16 parts [M x r] each | split partials of
+//                 X A^T, then of the product
+//   FWD_DROP    : s U as above | split partials of U, then of the staged
+//                 product | deq(W) bf16 [N x K], if staged
 // qlora_linear_fwd_noalloc carves the FWD layout out of `scratch` below
 // instead of a caller workspace.
 #include <hip/hip_runtime.h>
@@ -149,9 +151,7 @@ FwdLayout fwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool staged) {
   return L;
 }
 
-// The forward under dropout: U | split partials of U, then of the staged
-// product | deq(W), if staged.  It is staged from kStagedMinTokens tokens on,
-// and below where the estimate says so: the fused kernel takes about 26 ns a
+// The forward under dropout is staged from kStagedMinTokens tokens on, and below where the estimate says so: the fused kernel takes about 26 ns a
 // column of K and round of 256 x 256 tiles (256 x 1024 x 1024: 31 us on four
 // workgroups, against 3 us to dequantize and 12 for 64 x 64 tiles; 263 x 16576
 // x 3968: about 100 us, against 35 and 80), the dequantization 2.5 bytes a
@@ -164,11 +164,11 @@ bool drop_fwd_staged(int64_t M, int64_t N, int64_t K) {
   return 4.0 + (double)N * (double)K * 2.5 / 4.4e6 + staged_cost(N, K, M) < 5.0 + rounds * 0.026 * (double)K;
 }
 struct DropFwdLayout {
-  size_t u, part, part_bytes, wd, total;
+  size_t t, part, part_bytes, wd, total;
 };
 DropFwdLayout drop_fwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool staged) {
   DropFwdLayout L{};
-  L.part = align_up((size_t)M * r * 2);
+  L.part = align_up((size_t)M * r * 2 * kTermParts);
   L.part_bytes = std::max(u_part_bytes(M, K, r), staged ? staged_part_bytes(N, K, M) : 0);
   L.wd = L.part + align_up(L.part_bytes);
   L.total = L.wd + (staged ? align_up((size_t)N * (size_t)K * 2) : 0);
@@ -240,7 +240,7 @@ DropBwdLayout drop_bwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool w
   DropBwdLayout L{};
   const int64_t np = up64(N);
   if (r > 0) {
-    L.u = align_up((size_t)M * r * 3 * 2);
+    L.u = align_up((size_t)M * r * 2 * kGradParts);
     L.part = L.u + align_up((size_t)M * r * 2);
     L.total = L.part + align_up(adapter_part_bytes(M, N, K, r));
   }
@@ -261,13 +261,13 @@ bool drop_bwd_ok(int64_t M, int64_t N, int64_t K) {
 }
 
 struct I8FwdLayout {
-  size_t xq, sx, u, part, part_bytes, total;
+  size_t xq, sx, t, part, part_bytes, total;
 };
 I8FwdLayout i8_fwd_layout(int64_t M, int64_t N, int64_t K, int32_t r) {
   I8FwdLayout L{};
   L.sx = align_up((size_t)M * (size_t)i8_row_bytes(K));
-  L.u = L.sx + align_up((size_t)M * sizeof(float));
-  L.part = L.u + align_up((size_t)M * r * 2);
+  L.t = L.sx + align_up((size_t)M * sizeof(float));
+  L.part = L.t + align_up((size_t)M * r * 2 * kTermParts);
   // the partials of U, then those of the product
   L.part_bytes = std::max(r > 0 ? u_part_bytes(M, K, r) : 0, i8_gemm_part_bytes(M, N, K));
   L.total = L.part + align_up(L.part_bytes);
@@ -758,17 +758,17 @@ qlora_status qlora_linear_fwd_drop(const qlora_nf4_weight* W, const uint16_t* X,
   if ((st = check_ws(ws, ws_bytes, L.total)) != QLORA_OK) return st;
   hipStream_t s = (hipStream_t)stream;
   const float sc = (float)((double)alpha / (double)r);
-  bf16_t* U = U_save ? U_save : reinterpret_cast<bf16_t*>(ws_at(ws, L.u));
+  bf16_t* T = reinterpret_cast<bf16_t*>(ws_at(ws, L.t));
   float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
   Ride rest;
-  if ((st = hip_status(start_xat_drop(X, A, M, K, r, &d, part, U, &rest, s))) != QLORA_OK) return st;
+  if ((st = hip_status(start_xat_drop(X, A, M, K, r, &d, part, U_save, T, sc, &rest, s))) != QLORA_OK) return st;
   if (!staged) {
     if ((st = hip_status(launch_ride(rest, s))) != QLORA_OK) return st;
-    return hip_status(launch_fwd(view(W), X, M, U, B, r, sc, Y, s));
+    return hip_status(launch_fwd(view(W), X, M, T, B, r, 1.0f, Y, s, kTermParts));
   }
   bf16_t* Wd = reinterpret_cast<bf16_t*>(ws_at(ws, L.wd));
   if ((st = hip_status(launch_dequant_ride(view(W), Wd, rest, s))) != QLORA_OK) return st;
-  return hip_status(launch_staged(Wd, N, K, X, M, U, B, false, r, sc, nullptr, Y, s, part, L.part_bytes));
+  return hip_status(launch_staged(Wd, N, K, X, M, T, B, false, r, nullptr, Y, s, part, L.part_bytes));
 }
 
 namespace {
@@ -817,18 +817,21 @@ qlora_status run_bwd(const qlora_nf4_weight* W, const qlora_i8_rows* W8, int64_t
   const int64_t np = up64(N);
   qlora_status st;
   const float sc = r > 0 ? (float)((double)alpha / (double)r) : 0.0f;
-  bf16_t* G = reinterpret_cast<bf16_t*>(ws_at(ws, L.g));   // its first part is G rounded to bf16
+  // what both dX and dA have of G: alpha / r, and 1 / (1 - p) under the mask
+  const float sg = drop ? sc * drop->scale : sc;
+  bf16_t* G = reinterpret_cast<bf16_t*>(ws_at(ws, L.g));   // dX takes its first kTermParts parts, dA all
   float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
   if (r > 0 && !U) {
     bf16_t* Ud = reinterpret_cast<bf16_t*>(ws_at(ws, L.u));
     Ride rest;
-    if ((st = hip_status(start_xat_drop(X, A, M, K, r, drop, part, Ud, &rest, s))) != QLORA_OK) return st;
+    if ((st = hip_status(start_xat_drop(X, A, M, K, r, drop, part, Ud, nullptr, 0.0f, &rest, s))) != QLORA_OK)
+      return st;
     if ((st = hip_status(launch_ride(rest, s))) != QLORA_OK) return st;
     U = Ud;
   }
   Ride rest{};
   rest.kind = kRideSum3;
-  auto start_g = [&]() { return hip_status(start_dyb_parts(dY, B, M, N, r, part, G, &rest, s)); };
+  auto start_g = [&]() { return hip_status(start_dyb_parts(dY, B, M, N, r, part, G, sg, &rest, s)); };
   auto run_g = [&]() {
     const qlora_status e = start_g();
     return e != QLORA_OK ? e : hip_status(launch_ride(rest, s));
@@ -849,7 +852,7 @@ qlora_status run_bwd(const qlora_nf4_weight* W, const qlora_i8_rows* W8, int64_t
     if ((st = weight_t(W, W8, WdT, np, rest, s)) != QLORA_OK) return st;
     if (r > 0 && late && (st = run_g()) != QLORA_OK) return st;
     float* split = reinterpret_cast<float*>(ws_at(ws, L.split));
-    st = hip_status(launch_staged(WdT, K, np, g, M, r > 0 ? G : nullptr, r > 0 ? A : nullptr, true, r, sc,
+    st = hip_status(launch_staged(WdT, K, np, g, M, r > 0 ? G : nullptr, r > 0 ? A : nullptr, true, r,
                                   r > 0 ? drop : nullptr, dX, s, split, L.split_bytes));
     if (st != QLORA_OK) return st;
   } else if (r > 0 && (st = run_g()) != QLORA_OK) {
@@ -905,7 +908,7 @@ qlora_status qlora_i8_matmul(const qlora_i8_rows* X, const qlora_i8_rows* W, uin
   if (X->cols != W->cols) return QLORA_E_SHAPE;
   if (!Y) return QLORA_E_NULL;
   if (!aligned16(Y)) return QLORA_E_ALIGN;
-  const I8Gemm g{W->codes, W->scale, W->rows, W->cols, X->codes, X->scale, X->rows, nullptr, nullptr, 0, 0.0f, Y};
+  const I8Gemm g{W->codes, W->scale, W->rows, W->cols, X->codes, X->scale, X->rows, nullptr, nullptr, 0, Y};
   return hip_status(launch_i8_gemm(g, (hipStream_t)stream, nullptr, 0));
 }
 
@@ -927,21 +930,22 @@ qlora_status qlora_i8_linear_fwd(const qlora_i8_rows* W, const uint16_t* X, int6
   hipStream_t s = (hipStream_t)stream;
   int8_t* xq = reinterpret_cast<int8_t*>(ws_at(ws, L.xq));
   float* sx = reinterpret_cast<float*>(ws_at(ws, L.sx));
-  bf16_t* U = r > 0 ? (U_save ? U_save : reinterpret_cast<bf16_t*>(ws_at(ws, L.u))) : nullptr;
+  bf16_t* T = r > 0 ? reinterpret_cast<bf16_t*>(ws_at(ws, L.t)) : nullptr;
+  const float sc = r > 0 ? (float)((double)alpha / (double)r) : 0.0f;
   const DropArgs* dp = active ? &d : nullptr;
   float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
   if (i8_prep_ok(M, K, r, active)) {
-    st = hip_status(launch_i8_prep(X, M, K, A, r, dp, U, xq, sx, s));
+    st = hip_status(launch_i8_prep(X, M, K, A, r, dp, U_save, T, sc, xq, sx, s));
   } else {
     Ride rest;
-    if (r > 0 && (st = hip_status(start_xat_drop(X, A, M, K, r, dp, part, U, &rest, s))) != QLORA_OK) return st;
+    if (r > 0 && (st = hip_status(start_xat_drop(X, A, M, K, r, dp, part, U_save, T, sc, &rest, s))) != QLORA_OK)
+      return st;
     const bool sum = r > 0 && rest.kind == kRideSum;
     if (r > 0 && !sum && (st = hip_status(launch_ride(rest, s))) != QLORA_OK) return st;
     st = hip_status(launch_quant_rows(X, M, K, xq, sx, sum ? &rest : nullptr, s));
   }
   if (st != QLORA_OK) return st;
-  const float sc = r > 0 ? (float)((double)alpha / (double)r) : 0.0f;
-  const I8Gemm g{W->codes, W->scale, N, K, xq, sx, M, U, B, r, sc, Y};
+  const I8Gemm g{W->codes, W->scale, N, K, xq, sx, M, T, B, r, Y};
   return hip_status(launch_i8_gemm(g, s, part, L.part_bytes));
 }
 

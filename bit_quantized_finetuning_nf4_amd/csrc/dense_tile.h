@@ -222,6 +222,28 @@ __device__ __forceinline__ void tail_load(TailRegs& R, const bf16_t* Bm, bool b_
     R.t[e] = u;
   }
 }
+// The same for one adapter whose T is kTermParts bf16 matrices [trows x r], as a
+// chunk of a rank of kTermParts r: ranks r .. are the second part's.
+__device__ __forceinline__ void tail_load_parts(TailRegs& R, const bf16_t* Bm, bool b_trans, int64_t rows, int r,
+                                                int64_t row0, int j0, const bf16_t* T, int64_t trows,
+                                                int64_t trow0) {
+  static_assert(kTermParts == 2);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int idx = threadIdx.x + kThreads * e;
+    const int row = idx >> 2, col = j0 + 8 * (idx & 3), part = col >= r ? 1 : 0, k = col - part * r;
+    R.w[e] = R.t[e] = make_uint4(0u, 0u, 0u, 0u);
+    if (!b_trans) {
+      if (k < r && row0 + row < rows) R.w[e] = *reinterpret_cast<const uint4*>(Bm + (row0 + row) * r + k);
+    } else {
+      const int j = j0 + (idx >> 5), kj = j >= r ? j - r : j;
+      const int64_t rr = row0 + 8 * (idx & 31);
+      if (kj < r && rr < rows) R.w[e] = *reinterpret_cast<const uint4*>(Bm + (int64_t)kj * rows + rr);
+    }
+    if (k < r && trow0 + row < trows)
+      R.t[e] = *reinterpret_cast<const uint4*>(T + (part * trows + trow0 + row) * r + k);
+  }
+}
 // The chunk into LDS: s T as a 64-byte-row tile at dst + kOp; the weights
 // at dst, as a 64-byte-row tile or, with b_trans, as a tile of 32 rank rows
 // x 256 weight rows (512-byte rows, 32-byte block b of rank row n at
@@ -243,8 +265,9 @@ __device__ __forceinline__ void tail_store(char* dst, const TailRegs& R, bool b_
 
 // The LoRA tail by DMA, for tiles inside one adapter group with the rank in
 // whole 32-wide chunks.  A chunk takes 32 KiB of LDS in the layouts of
-// tail_store, but the token half holds T itself (unscaled): s is applied to
-// each fragment as it is read, which rounds exactly as tail_store does.
+// tail_store, but the token half holds T itself (unscaled): s, where T does not
+// hold it, is applied to each fragment as it is read, which rounds exactly as
+// tail_store does.
 struct TailSrc {
   rsrc_t wr, tr;         // weight half (B, or A with b_trans), token half (T)
   int64_t n0, m0, rows;  // first weight row, first token row, weight rows (N)

@@ -321,10 +321,10 @@ __global__ __launch_bounds__(kWideThreads, 1) void rwide_kernel(const bf16_t* __
 // tokens.  Both tiles are rows m, read transposed.  DB = false stores dA
 // [r x C] (A operand = Big, D[c][j]: four consecutive c per lane); DB = true
 // stores dB [C x r] (A operand = Sm, D[j][c]: four consecutive j per lane).
-// PARTS = 3: the rank side is an fp32 matrix as a sum of three bf16 ones,
-// sm_part elements apart, all multiplied into the same sums (dA is fp32: one
-// bf16 G would leave it G's rounding of 2^-9, two 2^-18, above the sum's own
-// error).
+// PARTS = kGradParts: the rank side is an fp32 matrix as a sum of three bf16
+// ones, sm_part elements apart, all multiplied into the same sums (dA is fp32:
+// one bf16 G would leave it G's rounding of 2^-9, two 2^-18, above the sum's
+// own error).
 // DROP: Big is drop(Big).  A transposed fragment holds eight tokens of one
 // column, eight different Philox blocks, so the mask is applied in LDS
 // instead: each lane zeroes the dropped elements of the 16-byte pieces that
@@ -522,7 +522,7 @@ struct GradArgs {
   int64_t M, N, K;
   int r, sps_a, tiles_a, blocks_a, sps_b, tiles_b;
   float *part_a, *part_b;   // dA, dB themselves where one split is all
-  float scale_a, scale_b;   // 1 where there are more
+  float scale_b;            // 1 where there are more (dA's is in G's parts)
   DropArgs drop;
 };
 template <int RP, bool DROP>
@@ -531,7 +531,7 @@ __global__ __launch_bounds__(kThreads, 1) void adapter_grads_kernel(GradArgs p) 
   const int id = blockIdx.x;
   if (id < p.blocks_a)
     cskinny<RP, false, 3, DROP>(id, 0, 1, smem, p.X, p.M, p.K, p.K, 0, p.G3, p.r, p.r, 0, p.sps_a, p.tiles_a, p.part_a,
-                                p.M * p.r, p.drop, p.scale_a);
+                                p.M * p.r, p.drop, 1.0f);
   else
     cskinny<RP, true, 1, false>(id - p.blocks_a, 0, 1, smem, p.dY, p.M, p.N, p.N, 0, p.U, p.r, p.r, 0, p.sps_b,
                                 p.tiles_b, p.part_b, 0, p.drop, p.scale_b);
@@ -775,36 +775,38 @@ hipError_t wide_partials(const bf16_t* P, int64_t M, int64_t C, const bf16_t* Q,
 
 namespace {
 
-Ride sum_ride(RideKind kind, const float* part, const Split& sp, int64_t n, float scale, bf16_t* out) {
+Ride sum_ride(RideKind kind, const float* part, const Split& sp, int64_t n, float scale, bf16_t* out, bf16_t* parts,
+              float s) {
   Ride d{};
   d.kind = kind, d.blocks = (int)((n / 4 + 255) / 256);
-  d.part = part, d.splits = sp.splits, d.n = n, d.scale = scale, d.out = out;
+  d.part = part, d.splits = sp.splits, d.n = n, d.scale = scale, d.out = out, d.parts = parts, d.s = s;
   return d;
 }
 
 }  // namespace
 
 hipError_t start_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
-                          float* part, bf16_t* out, Ride* rest, hipStream_t st) {
+                          float* part, bf16_t* out, bf16_t* parts, float s, Ride* rest, hipStream_t st) {
   const DropArgs d = drop ? *drop : DropArgs{};
   if (u_rows_ok(M, K, r, drop != nullptr)) {
     *rest = Ride{};
     rest->kind = drop ? kRideRowsDrop : kRideRows, rest->blocks = u_rows_blocks(M, r);
-    rest->X = X, rest->A = A, rest->M = M, rest->K = K, rest->r = r, rest->drop = d, rest->out = out;
+    rest->X = X, rest->A = A, rest->M = M, rest->K = K, rest->r = r, rest->drop = d;
+    rest->out = out, rest->parts = parts, rest->s = s;
     return hipSuccess;
   }
   const Split sp = rows_split(M, K);
-  *rest = sum_ride(kRideSum, part, sp, M * r, drop ? drop->scale : 1.0f, out);
+  *rest = sum_ride(kRideSum, part, sp, M * r, drop ? drop->scale : 1.0f, out, parts, s);
   return drop ? (r <= 64 ? wide_partials<64, false, true>(X, M, K, A, r, d, sp, part, st)
                          : wide_partials<128, false, true>(X, M, K, A, r, d, sp, part, st))
               : (r <= 64 ? wide_partials<64, false, false>(X, M, K, A, r, d, sp, part, st)
                          : wide_partials<128, false, false>(X, M, K, A, r, d, sp, part, st));
 }
 
-hipError_t start_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* out,
-                           Ride* rest, hipStream_t st) {
+hipError_t start_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* parts,
+                           float s, Ride* rest, hipStream_t st) {
   const Split sp = rows_split(M, N);
-  *rest = sum_ride(kRideSum3, part, sp, M * r, 1.0f, out);
+  *rest = sum_ride(kRideSum3, part, sp, M * r, 1.0f, nullptr, parts, s);
   return r <= 64 ? wide_partials<64, true, false>(dY, M, N, B, r, DropArgs{}, sp, part, st)
                  : wide_partials<128, true, false>(dY, M, N, B, r, DropArgs{}, sp, part, st);
 }
@@ -834,10 +836,8 @@ hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t*
   const int64_t na = (int64_t)r * K, nb = N * r;
   float* part_b = part + (part_bytes(sa, na) + 255) / 256 * 256 / sizeof(float);
   const bool whole_a = sa.splits == 1, whole_b = sb.splits == 1;
-  const float scale_a = drop ? scale * drop->scale : scale;
   const GradArgs p{X, dY, G3, U, M, N, K, r, sa.sps, sa.tiles, sa.tiles * sa.splits, sb.sps, sb.tiles,
-                   whole_a ? dA : part, whole_b ? dB : part_b, whole_a ? scale_a : 1.0f, whole_b ? scale : 1.0f,
-                   drop ? *drop : DropArgs{}};
+                   whole_a ? dA : part, whole_b ? dB : part_b, whole_b ? scale : 1.0f, drop ? *drop : DropArgs{}};
   auto* fn = r <= 64 ? (drop ? &adapter_grads_kernel<64, true> : &adapter_grads_kernel<64, false>)
                      : (drop ? &adapter_grads_kernel<128, true> : &adapter_grads_kernel<128, false>);
   const int lds = r <= 64 ? grads_lds<64>() : grads_lds<128>();
@@ -847,7 +847,7 @@ hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t*
   const int64_t ra = whole_a ? 0 : na, rb = whole_b ? 0 : nb;
   if (ra + rb == 0) return hipGetLastError();
   hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(((ra + rb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
-                     part, sa.splits, ra, dA, part_b, sb.splits, rb, dB, scale_a, scale);
+                     part, sa.splits, ra, dA, part_b, sb.splits, rb, dB, 1.0f, scale);
   return hipGetLastError();
 }
 

@@ -28,18 +28,21 @@
 namespace qlora {
 namespace {
 
-// The masked LoRA tail of a tile: acc += s drop'(T A), A [r x cols] read
-// transposed, T [M x r], r <= 128.  The nt chunks of the rank are in LDS (chunk c
-// at 2 kOp c), so the products of four 32 x 32 blocks at a time are summed in
-// registers of their own, masked by their bits (block 4 i + j of the wave at
-// bits + 1 KiB (4 i + j)), and added: the tile keeps one set of accumulators.
+// Forms of the LoRA tail: T one matrix, scaled by s as it is read; or T as
+// kTermParts parts with s in them, the product as it is or masked.
+enum TailForm : int { kTailScaled = 0, kTailParts = 1, kTailPartsDrop = 2 };
+
+// Chunks of the masked LoRA tail of a tile: acc += drop'(T A), A [r x cols] read
+// transposed.  The nt <= 4 chunks are in LDS (chunk c at 2 kOp c), so the
+// products of four 32 x 32 blocks at a time are summed in registers of their
+// own, masked by their bits (block 4 i + j of the wave at bits + 1 KiB (4 i +
+// j)), and added: the tile keeps one set of accumulators.
 // Masked dX of 4096 x 22016 x 8192 at rank 64 1.2 PFLOP/s; 2048 x 4096 x 4096
 // 69 us (one round of 256 x 128 tiles, 1.0 PFLOP/s).  With a block at a time,
 // its mask computed here, the whole backward of 3918 x 20856 x 800 at rank 128
 // took 438 us, 383 this way.
 template <int FI>
-__device__ __forceinline__ void masked_tail(f32x16_t (&acc)[FI][4], const char* smem, int nt, float s,
-                                            const char* bits) {
+__device__ __forceinline__ void masked_tail(f32x16_t (&acc)[FI][4], const char* smem, int nt, const char* bits) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1;
   const FragOffs fo = frag_offs(lane);
   const char* tok = smem + kOp + wr * 128 * 64;
@@ -74,7 +77,7 @@ __device__ __forceinline__ void masked_tail(f32x16_t (&acc)[FI][4], const char* 
       // the sums in vector registers, and spill
       float f[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) f[e] = fmaf(s, masked(y[j][e], keep[j], e), acc[i][j][e]);
+      for (int e = 0; e < 16; ++e) f[e] = acc[i][j][e] + masked(y[j][e], keep[j], e);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -93,8 +96,9 @@ __device__ __forceinline__ void masked_tail(f32x16_t (&acc)[FI][4], const char* 
 // split p takes contraction pairs p pps .. (64-column pairs), split 0 alone
 // adds the LoRA tail, and each split stores its fp32 sums at part + p M N
 // ([M x N], row stride N) instead of Y.
-// DR: the LoRA tail masked by `drop` (dX: b_trans, one adapter, gn = N).
-template <int FI, bool TD, bool DR>
+// FORM kTailParts and kTailPartsDrop: U holds kTermParts parts, one adapter (gn
+// = N, ldu = r), s is not used; kTailPartsDrop: dX (b_trans), masked by `drop`.
+template <int FI, bool TD, int FORM>
 __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __restrict__ Wd, int64_t N, int64_t K,
                                                                const bf16_t* __restrict__ X, int64_t M,
                                                                const bf16_t* __restrict__ U,
@@ -102,6 +106,7 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
                                                                int ldu, int64_t gn, float s, bf16_t* __restrict__ Y,
                                                                int64_t n_begin, int tiles_n, int tiles_m, int pps,
                                                                float* __restrict__ part, DropArgs drop) {
+  constexpr bool DR = FORM == kTailPartsDrop;
   extern __shared__ __align__(16) char smem[];
   int tn, tm;
   int id = xcd_tile_id();
@@ -154,10 +159,10 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
   const bool tail = r > 0 && split == 0;
   const bool tdma = TD && !DR && tail;
   // (built where used, so nothing of it stays live through the main loop)
-  auto tail_src = [&]() __attribute__((always_inline)) {
+  auto tail_src = [&](int part) __attribute__((always_inline)) {
     TailSrc ts;
     ts.wr = make_rsrc(Bl, (uint32_t)(N * r * 2));
-    ts.tr = make_rsrc(U, (uint32_t)(M * ldu * 2));
+    ts.tr = make_rsrc(FORM == kTailScaled ? U : U + part * M * r, (uint32_t)(M * ldu * 2));
     ts.n0 = n0;
     ts.m0 = m0;
     ts.rows = N;
@@ -167,7 +172,12 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
     ts.bt = b_trans != 0;
     return ts;
   };
-  if (tdma) tail_dma(smem + kLdsPairs, tail_src(), 0, f.w, lane);   // chunk 0 past the pair slots
+  // chunk c of the parts, one part's chunks after the other's
+  [[maybe_unused]] auto part_dma = [&](char* dst, int c) __attribute__((always_inline)) {
+    const int nj = r / 32, part = c / nj;
+    tail_dma(dst, tail_src(part), c - part * nj, f.w, lane);
+  };
+  if (tdma) tail_dma(smem + kLdsPairs, tail_src(0), 0, f.w, lane);   // chunk 0 past the pair slots
   // pairs 0 and 1 into slots 0 and 1
 #pragma unroll
   for (int d = 0; d < 2 * FI + 8; ++d) {
@@ -254,40 +264,51 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
   };
   if constexpr (DR) {
     if (tail) {
-      const int nt = (r + 31) / 32;
-      if constexpr (TD) {
-        const TailSrc ts = tail_src();
-        for (int c = 0; c < nt; ++c) tail_dma(smem + c * 2 * kOp, ts, c, f.w, lane);
-      } else {
-        for (int c = 0; c < nt; ++c) {
-          TailRegs R;
-          tail_load(R, Bl, true, N, r, n0, 32 * c, 0, N, U, ldu, M, m0);
-          tail_store(smem + c * 2 * kOp, R, true, 1.0f);
+      // four chunks at a time through the pair slots
+      const int nt = (kTermParts * r + 31) / 32;
+      for (int b0 = 0; b0 < nt; b0 += 4) {
+        const int bn = min(4, nt - b0);
+        if (b0 > 0) __syncthreads();   // every wave is done with the batch before
+        for (int c = 0; c < bn; ++c) {
+          if constexpr (TD) {
+            part_dma(smem + c * 2 * kOp, b0 + c);
+          } else {
+            TailRegs R;
+            tail_load_parts(R, Bl, true, N, r, n0, 32 * (b0 + c), U, M, m0);
+            tail_store(smem + c * 2 * kOp, R, true, 1.0f);
+          }
         }
+        QLORA_WAIT(0, 0);
+        __syncthreads();
+        masked_tail<FI>(acc, smem, bn, smem + kLdsPairs);
       }
-      QLORA_WAIT(0, 0);
-      __syncthreads();
-      masked_tail<FI>(acc, smem, nt, s, smem + kLdsPairs);
     }
   } else if constexpr (TD) {
     if (tdma) {
       // chunk 0 landed before the drain above; chunks 1 .. go four at a time
       // into the pair slots, the first four while chunk 0 is multiplied
-      const TailSrc ts = tail_src();
-      const int nt = r / 32;
+      constexpr bool raw = FORM == kTailScaled;
+      const TailSrc ts = tail_src(0);
+      auto dma = [&](char* dst, int c) __attribute__((always_inline)) {
+        if constexpr (raw)
+          tail_dma(dst, ts, c, f.w, lane);
+        else
+          part_dma(dst, c);
+      };
+      const int nt = (raw ? 1 : kTermParts) * (r / 32);
       int b0 = 1, bn = min(4, nt - 1);
-      for (int c = 0; c < bn; ++c) tail_dma(smem + c * 2 * kOp, ts, b0 + c, f.w, lane);
-      tail_chunk(smem + kLdsPairs, true);
+      for (int c = 0; c < bn; ++c) dma(smem + c * 2 * kOp, b0 + c);
+      tail_chunk(smem + kLdsPairs, raw);
       while (bn > 0) {
         QLORA_WAIT(0, 0);
         __builtin_amdgcn_s_barrier();
-        for (int c = 0; c < bn; ++c) tail_chunk(smem + c * 2 * kOp, true);
+        for (int c = 0; c < bn; ++c) tail_chunk(smem + c * 2 * kOp, raw);
         b0 += bn;
         bn = min(4, nt - b0);
         if (bn > 0) {
           QLORA_WAIT(0, 0);
           __builtin_amdgcn_s_barrier();   // every wave is done with the batch's slots
-          for (int c = 0; c < bn; ++c) tail_dma(smem + c * 2 * kOp, ts, b0 + c, f.w, lane);
+          for (int c = 0; c < bn; ++c) dma(smem + c * 2 * kOp, b0 + c);
         }
       }
     }
@@ -301,19 +322,24 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
     // one barrier per chunk both publishes a chunk and retires the buffer
     // the next store overwrites (its readers finished before they stored
     // their part of the chunk in between).
+    // (With T in parts there is one adapter.)
     const int64_t g_last = (min(n0 + 64 * FI, N) - 1) / gn;
     const int nj = (r + 31) / 32;
-    const int nt = (int)(g_last - g0 + 1) * nj;
+    const int nt = FORM == kTailScaled ? (int)(g_last - g0 + 1) * nj : (kTermParts * r + 31) / 32;
     TailRegs R;
     auto load = [&](int t) {
-      const int64_t g = g0 + t / nj;
-      tail_load(R, Bl, b_trans != 0, N, r, n0, 32 * (t % nj), g * gn, min((g + 1) * gn, N), U + g * r, ldu, M,
-                m0);
+      if constexpr (FORM == kTailScaled) {
+        const int64_t g = g0 + t / nj;
+        tail_load(R, Bl, b_trans != 0, N, r, n0, 32 * (t % nj), g * gn, min((g + 1) * gn, N), U + g * r, ldu, M,
+                  m0);
+      } else {
+        tail_load_parts(R, Bl, b_trans != 0, N, r, n0, 32 * t, U, M, m0);
+      }
     };
     load(0);
     for (int t = 0; t < nt; ++t) {
       char* buf = smem + (t & 1) * 2 * kOp;
-      tail_store(buf, R, b_trans != 0, s);
+      tail_store(buf, R, b_trans != 0, FORM == kTailScaled ? s : 1.0f);
       if (t + 1 < nt) load(t + 1);
       __syncthreads();
       tail_chunk(buf, false);
@@ -348,13 +374,17 @@ bool tail_by_dma(int64_t N, int64_t M, int r, int ldu, int64_t gn, int64_t n_beg
 template <int FI>
 hipError_t launch_fi(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* U,
                      const bf16_t* B, bool b_trans, int r, int ldu, int64_t gn, float s, bf16_t* Y, int64_t n_begin,
-                     int64_t n_rows, hipStream_t st, const DropArgs* drop, int splits = 1, float* part = nullptr) {
+                     int64_t n_rows, hipStream_t st, TailForm form, const DropArgs* drop, int splits = 1,
+                     float* part = nullptr) {
   const int tiles_n = (int)((n_rows + 64 * FI - 1) / (64 * FI));
   const int tiles_m = (int)((M + kTile - 1) / kTile);
   const bool td = tail_by_dma(N, M, r, ldu, gn, n_begin, tiles_n, 64 * FI);
-  auto* fn = drop ? (td ? &bf16_fwd_kernel<FI, true, true> : &bf16_fwd_kernel<FI, false, true>)
-                  : (td ? &bf16_fwd_kernel<FI, true, false> : &bf16_fwd_kernel<FI, false, false>);
-  const size_t lds = drop ? kLdsPairs + 4096 * FI : td ? kLdsDense : kLdsPairs;
+  auto* fn = form == kTailPartsDrop ? (td ? &bf16_fwd_kernel<FI, true, kTailPartsDrop>
+                                          : &bf16_fwd_kernel<FI, false, kTailPartsDrop>)
+             : form == kTailParts
+                 ? (td ? &bf16_fwd_kernel<FI, true, kTailParts> : &bf16_fwd_kernel<FI, false, kTailParts>)
+                 : (td ? &bf16_fwd_kernel<FI, true, kTailScaled> : &bf16_fwd_kernel<FI, false, kTailScaled>);
+  const size_t lds = form == kTailPartsDrop ? kLdsPairs + 4096 * FI : td ? kLdsDense : kLdsPairs;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
   if (e != hipSuccess) return e;
   const int npair = (int)(K >> 6);
@@ -399,11 +429,11 @@ int best_fi(int64_t rows, int64_t tiles_m, int cus) {
 
 hipError_t launch_rows(int fi, const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M,
                        const bf16_t* U, const bf16_t* B, bool b_trans, int r, int ldu, int64_t gn, float s,
-                       bf16_t* Y, int64_t n_begin, hipStream_t st, const DropArgs* drop) {
+                       bf16_t* Y, int64_t n_begin, hipStream_t st, TailForm form, const DropArgs* drop) {
   const int64_t n_rows = N - n_begin;
-  if (fi == 3) return launch_fi<3>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_begin, n_rows, st, drop);
-  if (fi == 2) return launch_fi<2>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_begin, n_rows, st, drop);
-  return launch_fi<4>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_begin, n_rows, st, drop);
+  if (fi == 3) return launch_fi<3>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_begin, n_rows, st, form, drop);
+  if (fi == 2) return launch_fi<2>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_begin, n_rows, st, form, drop);
+  return launch_fi<4>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_begin, n_rows, st, form, drop);
 }
 
 }  // namespace
@@ -435,13 +465,13 @@ namespace {
 
 hipError_t launch_dense(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* U,
                         int ldu, const bf16_t* B, bool b_trans, int r, int64_t gn, float s, bf16_t* Y,
-                        hipStream_t st, float* part, size_t part_bytes, const DropArgs* drop) {
+                        hipStream_t st, float* part, size_t part_bytes, TailForm form, const DropArgs* drop) {
   const int cus = device_cu_count();
   const int64_t tiles_m = (M + kTile - 1) / kTile;
   const int64_t tiles_n = (N + kTile - 1) / kTile;
   const int sp = dense_splits(N, K, M, cus);
   if (sp > 1 && part != nullptr && part_bytes >= (size_t)sp * (size_t)M * (size_t)N * sizeof(float)) {
-    hipError_t e = launch_fi<4>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, 0, N, st, drop, sp, part);
+    hipError_t e = launch_fi<4>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, 0, N, st, form, drop, sp, part);
     if (e != hipSuccess) return e;
     const int64_t n = M * N;
     hipLaunchKernelGGL(split_sum_kernel, dim3((unsigned)((n / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
@@ -457,13 +487,13 @@ hipError_t launch_dense(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X,
       n_split = 0;   // nothing left over, or the remainder gains nothing from narrower tiles: one launch
   }
   if (n_split > 0) {
-    hipError_t e = launch_fi<4>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, 0, n_split, st, drop);
+    hipError_t e = launch_fi<4>(Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, 0, n_split, st, form, drop);
     if (e != hipSuccess) return e;
     // the remainder's tiles address rows from n_split on, in the same arrays
     return launch_rows(best_fi(N - n_split, tiles_m, cus), Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, n_split,
-                       st, drop);
+                       st, form, drop);
   }
-  return launch_rows(best_fi(N, tiles_m, cus), Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, 0, st, drop);
+  return launch_rows(best_fi(N, tiles_m, cus), Wd, N, K, X, M, U, B, b_trans, r, ldu, gn, s, Y, 0, st, form, drop);
 }
 
 }  // namespace
@@ -471,7 +501,7 @@ hipError_t launch_dense(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X,
 hipError_t launch_bf16_group(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* U,
                              int ldu, const bf16_t* B, bool b_trans, int r, int64_t gn, float s, bf16_t* Y,
                              hipStream_t st, float* part, size_t part_bytes) {
-  return launch_dense(Wd, N, K, X, M, U, ldu, B, b_trans, r, gn, s, Y, st, part, part_bytes, nullptr);
+  return launch_dense(Wd, N, K, X, M, U, ldu, B, b_trans, r, gn, s, Y, st, part, part_bytes, kTailScaled, nullptr);
 }
 
 hipError_t launch_bf16_fwd(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* U,
@@ -493,23 +523,24 @@ size_t staged_part_bytes(int64_t N, int64_t K, int64_t M) {
 double staged_cost(int64_t N, int64_t K, int64_t M) { return choose_tile(M, N, K / 64, kSplitCus, (size_t)1 << 62).cost; }
 
 hipError_t launch_staged(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* T,
-                         const bf16_t* B, bool b_trans, int r, float s, const DropArgs* drop, bf16_t* Y, hipStream_t st,
+                         const bf16_t* B, bool b_trans, int r, const DropArgs* drop, bf16_t* Y, hipStream_t st,
                          float* part, size_t part_bytes) {
-  const float sc = drop ? s * drop->scale : s;
+  const TailForm form = drop ? kTailPartsDrop : kTailParts;
   const TileChoice c = choose_tile(M, N, K / 64, device_cu_count(), part ? part_bytes : 0);
   if (c.tm < 256) {
     TileGemm t{};
-    t.W = Wd, t.X = X, t.N = N, t.row_bytes = 2 * K, t.M = M, t.T = T, t.B = B, t.r = r, t.s = sc, t.b_trans = b_trans;
+    t.W = Wd, t.X = X, t.N = N, t.row_bytes = 2 * K, t.M = M, t.T = T, t.B = B, t.r = r, t.b_trans = b_trans;
     t.dropped = drop != nullptr;
     if (drop) t.drop = *drop;
     t.Y = Y, t.part = part;
     return launch_tile(t, c, 0, N, st);
   }
   if (c.splits > 1) {
-    const hipError_t e = launch_fi<4>(Wd, N, K, X, M, T, B, b_trans, r, r, N, sc, Y, 0, N, st, drop, c.splits, part);
+    const hipError_t e = launch_fi<4>(Wd, N, K, X, M, T, B, b_trans, r, r, N, 1.0f, Y, 0, N, st, form, drop,
+                                      c.splits, part);
     return e != hipSuccess ? e : launch_split_sum(part, c.splits, M * N, Y, st);
   }
-  return launch_dense(Wd, N, K, X, M, T, r, B, b_trans, r, N, sc, Y, st, part, part_bytes, drop);
+  return launch_dense(Wd, N, K, X, M, T, r, B, b_trans, r, N, 1.0f, Y, st, part, part_bytes, form, drop);
 }
 
 }  // namespace qlora

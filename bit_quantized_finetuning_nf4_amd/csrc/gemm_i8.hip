@@ -1,7 +1,9 @@
 // gemm_i8.hip -- the product of 8-bit integers with one scale per token and
 // one per output channel, and the LoRA tail:
 //
-//   Y[m][n] = sx[m] sw[n] sum_k Xq[m][k] Wq[n][k] + s sum_j U[m][j] B[n][j]
+//   Y[m][n] = sx[m] sw[n] sum_k Xq[m][k] Wq[n][k] + sum_j T[m][j] B[n][j]
+//
+// with T = s U as kTermParts bf16 matrices.
 //
 // The sum over k is exact: products of integers up to 127 in 32-bit sums, no
 // overflow for K <= 131072 (127^2 K < 2^31).  It is rounded to fp32 when it
@@ -65,10 +67,9 @@ __device__ __forceinline__ void scale_tile(const i32x16_t (&acc)[FI][4], f32x16_
   }
 }
 
-// acc += the chunk at buf (weights at buf, tokens at buf + kOp; the tokens
-// scaled by s as they are read when `raw`).
+// acc += the chunk at buf (weights at buf, tokens at buf + kOp).
 template <int FI>
-__device__ __forceinline__ void tail_mul(f32x16_t (&acc)[FI][4], const char* buf, bool raw, float s) {
+__device__ __forceinline__ void tail_mul(f32x16_t (&acc)[FI][4], const char* buf) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1;
   const FragOffs fo = frag_offs(lane);
   const int am64 = wc * 32 * FI * 64, bm64 = wr * 128 * 64;
@@ -79,28 +80,26 @@ __device__ __forceinline__ void tail_mul(f32x16_t (&acc)[FI][4], const char* buf
 #pragma unroll
     for (int i = 0; i < FI; ++i) a[i] = rd16(buf + am64 + i * 2048 + o);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      b[i] = rd16(buf + kOp + bm64 + i * 2048 + o);
-      if (raw) b[i] = scale_frag(b[i], s);
-    }
+    for (int i = 0; i < 4; ++i) b[i] = rd16(buf + kOp + bm64 + i * 2048 + o);
     mfma_block<FI, 4>(acc, a, b);
   }
 }
 
-// acc += B (s U)^T over the rank, 32 at a time through 64-byte-row tiles, one
-// chunk loaded into registers while the one before is multiplied.
+// acc += B T^T over the ranks of the parts, 32 at a time through 64-byte-row
+// tiles, one chunk loaded into registers while the one before is multiplied.
 template <int FI>
-__device__ __forceinline__ void lora_tail(f32x16_t (&acc)[FI][4], const bf16_t* B, const bf16_t* U, int r, float s,
-                                          int64_t M, int64_t N, int64_t m0, int64_t n0, char* smem) {
-  const int nt = (r + 31) / 32;
+__device__ __forceinline__ void lora_tail(f32x16_t (&acc)[FI][4], const bf16_t* B, const bf16_t* T, int r, int64_t M,
+                                          int64_t N, int64_t m0, int64_t n0, char* smem) {
+  const int nt = (kTermParts * r + 31) / 32;
   TailRegs R;
-  tail_load(R, B, false, N, r, n0, 0, 0, N, U, r, M, m0);
+  auto load = [&](int c) { tail_load_parts(R, B, false, N, r, n0, 32 * c, T, M, m0); };
+  load(0);
   for (int c = 0; c < nt; ++c) {
     char* buf = smem + (c & 1) * 2 * kOp;
-    tail_store(buf, R, false, s);
-    if (c + 1 < nt) tail_load(R, B, false, N, r, n0, 32 * (c + 1), 0, N, U, r, M, m0);
+    tail_store(buf, R, false, 1.0f);
+    if (c + 1 < nt) load(c + 1);
     __syncthreads();
-    tail_mul<FI>(acc, buf, false, s);
+    tail_mul<FI>(acc, buf);
   }
 }
 
@@ -114,8 +113,8 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
                                                               const float* __restrict__ sw, int64_t N, int64_t ld,
                                                               const int8_t* __restrict__ Xq,
                                                               const float* __restrict__ sx, int64_t M,
-                                                              const bf16_t* __restrict__ U,
-                                                              const bf16_t* __restrict__ B, int r, float s,
+                                                              const bf16_t* __restrict__ T,
+                                                              const bf16_t* __restrict__ B, int r,
                                                               bf16_t* __restrict__ Y, int64_t n_begin, int tiles_n,
                                                               int tiles_m, int pps, float* __restrict__ part) {
   extern __shared__ __align__(16) char smem[];
@@ -185,29 +184,41 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
   // drain the DMAs still in flight (clamped re-loads) before reusing LDS
   QLORA_WAIT(0, 0);
   __builtin_amdgcn_s_barrier();
-  // TD: the rank's chunks (32 each, at most four) come into the pair slots
-  // while the sums become fp32
-  if (TD && tail) {
-    TailSrc ts;
-    ts.wr = make_rsrc(B, (uint32_t)(N * r * 2));
-    ts.tr = make_rsrc(U, (uint32_t)(M * r * 2));
-    ts.n0 = n0;
-    ts.m0 = m0;
-    ts.rows = N;
-    ts.r = ts.ld = r;
-    ts.col0 = 0;
-    ts.bt = false;
-    for (int c = 0; c < r / 32; ++c) tail_dma(smem + c * 2 * kOp, ts, c, f.w, lane);
-  }
+  // TD: the parts' chunks (32 ranks each) come into the pair slots, four at a
+  // time, the first four while the sums become fp32
+  const int nj = r / 32, nt = kTermParts * nj;
+  auto tail_batch = [&](int c0) __attribute__((always_inline)) {
+    for (int c = c0; c < min(c0 + 4, nt); ++c) {
+      const int pt = c / nj;
+      TailSrc ts;
+      ts.wr = make_rsrc(B, (uint32_t)(N * r * 2));
+      ts.tr = make_rsrc(T + pt * M * r, (uint32_t)(M * r * 2));
+      ts.n0 = n0;
+      ts.m0 = m0;
+      ts.rows = N;
+      ts.r = ts.ld = r;
+      ts.col0 = 0;
+      ts.bt = false;
+      tail_dma(smem + (c - c0) * 2 * kOp, ts, c - pt * nj, f.w, lane);
+    }
+  };
+  if (TD && tail) tail_batch(0);
   f32x16_t out[FI][4];
   scale_tile<FI>(acc, out, smem + kLdsPairs);
   if (tail) {
     if constexpr (TD) {
-      QLORA_WAIT(0, 0);
-      __builtin_amdgcn_s_barrier();
-      for (int c = 0; c < r / 32; ++c) tail_mul<FI>(out, smem + c * 2 * kOp, true, s);
+      for (int c0 = 0; c0 < nt; c0 += 4) {
+        if (c0 > 0) {
+          QLORA_WAIT(0, 0);
+          __builtin_amdgcn_s_barrier();   // every wave is done with the batch before
+          tail_batch(c0);
+        }
+        QLORA_WAIT(0, 0);
+        __builtin_amdgcn_s_barrier();
+        for (int c = c0; c < min(c0 + 4, nt); ++c) tail_mul<FI>(out, smem + (c - c0) * 2 * kOp);
+      }
     } else {
-      lora_tail<FI>(out, B, U, r, s, M, N, m0, n0, smem);
+      lora_tail<FI>(out, B, T, r, M, N, m0, n0, smem);
     }
   }
   if (part != nullptr)
@@ -242,8 +253,8 @@ __global__ __launch_bounds__(kSkWaves * 64, 1) void i8_skinny_kernel(const int8_
                                                                      const float* __restrict__ sw, int64_t N,
                                                                      int64_t ld, const int8_t* __restrict__ Xq,
                                                                      const float* __restrict__ sx, int64_t M,
-                                                                     const bf16_t* __restrict__ U,
-                                                                     const bf16_t* __restrict__ B, int r, float s,
+                                                                     const bf16_t* __restrict__ T,
+                                                                     const bf16_t* __restrict__ B, int r,
                                                                      bf16_t* __restrict__ Y) {
   __shared__ __align__(16) i32x4_t red[kSkWaves][R * MT][64];
   // the wave's number as a scalar: its branches must not mask lanes, which an
@@ -317,18 +328,19 @@ __global__ __launch_bounds__(kSkWaves * 64, 1) void i8_skinny_kernel(const int8_
     for (int v = 1; v < kSkWaves; ++v) t += red[v][blk][lane];
     const int64_t m = 16 * j + l, nrow = n0 + 16 * i, n = nrow + 4 * g;
     f32x4_t lo = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = 0; c < r; c += 32) {   // adapter: 16 channels x 16 tokens over the rank
-      const int k = c + 8 * g;
+    static_assert(kTermParts == 2);
+    for (int c = 0; c < kTermParts * r; c += 32) {   // adapter: 16 channels x 16 tokens over the ranks of both parts
+      const int kp = c + 8 * g, part = kp >= r ? 1 : 0, k = kp - part * r;
       bf16x8_t fb{}, fu{};
       if (k < r && nrow + l < N) fb = *reinterpret_cast<const bf16x8_t*>(B + (nrow + l) * r + k);
-      if (k < r && m < M) fu = *reinterpret_cast<const bf16x8_t*>(U + m * r + k);
+      if (k < r && m < M) fu = *reinterpret_cast<const bf16x8_t*>(T + (part * M + m) * r + k);
       lo = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fu, lo, 0, 0, 0);
     }
     if (m < M && n < N) {   // N % 8 == 0
       const float4 sc = *reinterpret_cast<const float4*>(sw + n);
       const float x = sx[m];
-      const float y0 = fmaf(s, lo[0], (float)t[0] * (x * sc.x)), y1 = fmaf(s, lo[1], (float)t[1] * (x * sc.y)),
-                  y2 = fmaf(s, lo[2], (float)t[2] * (x * sc.z)), y3 = fmaf(s, lo[3], (float)t[3] * (x * sc.w));
+      const float y0 = (float)t[0] * (x * sc.x) + lo[0], y1 = (float)t[1] * (x * sc.y) + lo[1],
+                  y2 = (float)t[2] * (x * sc.z) + lo[2], y3 = (float)t[3] * (x * sc.w) + lo[3];
       *reinterpret_cast<uint2*>(Y + m * N + n) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
     }
   }
@@ -337,15 +349,15 @@ __global__ __launch_bounds__(kSkWaves * 64, 1) void i8_skinny_kernel(const int8_
 template <int R, int MT, int UP>
 hipError_t launch_skinny(const I8Gemm& g, hipStream_t st) {
   hipLaunchKernelGGL((i8_skinny_kernel<R, MT, UP>), dim3((unsigned)((g.N + 16 * R - 1) / (16 * R))),
-                     dim3(kSkWaves * 64), 0, st, g.Wq, g.sw, g.N, i8_row_bytes(g.K), g.Xq, g.sx, g.M, g.U, g.B, g.r,
-                     g.s, g.Y);
+                     dim3(kSkWaves * 64), 0, st, g.Wq, g.sw, g.N, i8_row_bytes(g.K), g.Xq, g.sx, g.M, g.T, g.B, g.r,
+                     g.Y);
   return hipGetLastError();
 }
 
 template <int FI>
 hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, int splits, float* part, hipStream_t st) {
   const int tiles_n = (int)((n_rows + 64 * FI - 1) / (64 * FI)), tiles_m = (int)((g.M + kTile - 1) / kTile);
-  // the rank in whole chunks, U and B within 32-bit byte offsets
+  // the rank in whole chunks, T's parts and B within 32-bit byte offsets
   const bool td = g.r > 0 && g.r % 32 == 0 && g.M * g.r < ((int64_t)1 << 30) && g.N * g.r < ((int64_t)1 << 30);
   auto* fn = td ? &i8_gemm_kernel<FI, true> : &i8_gemm_kernel<FI, false>;
   constexpr size_t lds = kLdsPairs + kLdsScales;
@@ -353,7 +365,7 @@ hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, int split
   if (e != hipSuccess) return e;
   const int npair = (int)(i8_row_bytes(g.K) / 128);
   hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_m * splits), dim3(kThreads), lds, st, g.Wq, g.sw, g.N,
-                     i8_row_bytes(g.K), g.Xq, g.sx, g.M, g.U, g.B, g.r, g.s, g.Y, n_begin, tiles_n, tiles_m,
+                     i8_row_bytes(g.K), g.Xq, g.sx, g.M, g.T, g.B, g.r, g.Y, n_begin, tiles_n, tiles_m,
                      (npair + splits - 1) / splits, splits > 1 ? part : nullptr);
   if ((e = hipGetLastError()) != hipSuccess || splits == 1) return e;
   return launch_split_sum(part, splits, g.M * g.N, g.Y, st);
@@ -413,7 +425,7 @@ hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, float* part, size_t p
                            : launch_fi<2>(g, n_begin, n_rows, 1, nullptr, st);
     TileGemm t{};
     t.W = g.Wq, t.X = g.Xq, t.sw = g.sw, t.sx = g.sx, t.N = g.N, t.row_bytes = i8_row_bytes(g.K), t.M = g.M;
-    t.T = g.U, t.B = g.B, t.r = g.r, t.s = g.s, t.Y = g.Y, t.part = part;
+    t.T = g.T, t.B = g.B, t.r = g.r, t.Y = g.Y, t.part = part;
     return launch_tile(t, c, n_begin, n_rows, st);
   };
   const TileChoice one = choose_tile(g.M, g.N, lines, cus, part ? part_bytes : 0);

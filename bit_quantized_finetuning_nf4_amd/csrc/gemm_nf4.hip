@@ -349,7 +349,8 @@ template <int CB>
 __global__ __launch_bounds__(kThreads, 1) void nf4_fwd_r_kernel(Nf4View W, const bf16_t* __restrict__ X, int64_t M,
                                                                 const bf16_t* __restrict__ U,
                                                                 const bf16_t* __restrict__ Bl, int r, float s,
-                                                                bf16_t* __restrict__ Y, int tiles_n, int tiles_m) {
+                                                                bf16_t* __restrict__ Y, int tiles_n, int tiles_m,
+                                                                int parts) {
   extern __shared__ __align__(16) char smem[];
   int tn, tm;
   map_tile(tiles_n, tiles_m, tn, tm);
@@ -451,11 +452,14 @@ __global__ __launch_bounds__(kThreads, 1) void nf4_fwd_r_kernel(Nf4View W, const
   QLORA_WAIT(0, 0);
   __builtin_amdgcn_s_barrier();
   if (r > 0) {
-    // LoRA up-projection: acc += B (s U)^T over the rank, 32 at a time; the
-    // weight operand comes straight from B (rows of the lane, ranks 16h + 8kk)
-    for (int j0 = 0; j0 < r; j0 += 32) {
+    // LoRA up-projection: acc += B (s U)^T over the rank, 32 at a time, for each
+    // part of U; the weight operand comes straight from B (rows of the lane,
+    // ranks 16h + 8kk)
+    const int nj = (r + 31) / 32;
+    for (int c = 0; c < parts * nj; ++c) {
+      const int j0 = 32 * (c % nj);
       char* xb = smem;
-      tail_tokens(xb, U, M, r, m0, j0, s);
+      tail_tokens(xb, U + c / nj * M * r, M, r, m0, j0, s);
       bf16x8_t a[2][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -649,7 +653,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void nf4_fwd_n32_kernel(Nf4View W, c
                                                                     int64_t M, const bf16_t* __restrict__ U,
                                                                     const bf16_t* __restrict__ Bl, int r, float s,
                                                                     bf16_t* __restrict__ Y, int tiles_n, int tiles_m,
-                                                                    int tail_base) {
+                                                                    int tail_base, int parts) {
   extern __shared__ __align__(16) char smem[];
   int64_t n0, m0;
   if (tail_base < 0) {
@@ -742,10 +746,13 @@ __global__ __launch_bounds__(64 * WAVES, 1) void nf4_fwd_n32_kernel(Nf4View W, c
   __builtin_amdgcn_s_barrier();
 
   if (r > 0) {
-    // LoRA up-projection: acc += B (s U)^T over the rank, 32 at a time; the
-    // weight operand comes straight from B (row of the lane, ranks 16h + 8kk)
-    for (int j0 = 0; j0 < r; j0 += 32) {
-      tail_tokens8<64 * WAVES>(smem, U, M, r, m0, j0, s);
+    // LoRA up-projection: acc += B (s U)^T over the rank, 32 at a time, for each
+    // part of U; the weight operand comes straight from B (row of the lane,
+    // ranks 16h + 8kk)
+    const int nj = (r + 31) / 32;
+    for (int c = 0; c < parts * nj; ++c) {
+      const int j0 = 32 * (c % nj);
+      tail_tokens8<64 * WAVES>(smem, U + c / nj * M * r, M, r, m0, j0, s);
       bf16x8_t a[2];
       const int64_t n = n0 + 32 * f.w + lr;
 #pragma unroll
@@ -1394,7 +1401,7 @@ namespace {
 
 template <int CB>
 hipError_t launch_fwd_cb(const Nf4View& W, const bf16_t* X, int64_t M, const bf16_t* U, const bf16_t* B, int r,
-                        float s, bf16_t* Y, hipStream_t st) {
+                        float s, bf16_t* Y, hipStream_t st, int parts) {
   const int tiles_n = (int)((W.N + kTile - 1) / kTile);
   const int tiles_m = (int)((M + kTile - 1) / kTile);
   const int tiles = tiles_n * tiles_m;
@@ -1407,14 +1414,14 @@ hipError_t launch_fwd_cb(const Nf4View& W, const bf16_t* X, int64_t M, const bf1
   hipError_t e = allow_lds(reinterpret_cast<const void*>(&nf4_fwd_r_kernel<CB>), (int)kLdsFwdR);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(nf4_fwd_r_kernel<CB>, dim3(main_tiles), dim3(kThreads), kLdsFwdR, st, W, X, M, U, B, r, s, Y,
-                     tiles_n, tiles_m);
+                     tiles_n, tiles_m, parts);
   e = hipGetLastError();
   if (e != hipSuccess || main_tiles == tiles) return e;
   auto* tail = &nf4_fwd_n32_kernel<CB, 4>;
   e = allow_lds(reinterpret_cast<const void*>(tail), (int)kLdsFwdR);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(tail, dim3(2 * (tiles - main_tiles)), dim3(kThreads), kLdsFwdR, st, W, X, M, U, B, r, s, Y,
-                     tiles_n, tiles_m, main_tiles);
+                     tiles_n, tiles_m, main_tiles, parts);
   return hipGetLastError();
 }
 
@@ -1447,10 +1454,10 @@ hipError_t launch_dx_cb(const Nf4View& W, const bf16_t* dY, int64_t M, const bf1
 // The codebook is a template parameter of the kernels (its levels are
 // literals in the block-table code).
 hipError_t launch_fwd(const Nf4View& W, const bf16_t* X, int64_t M, const bf16_t* U, const bf16_t* B, int r,
-                      float s, bf16_t* Y, hipStream_t st) {
-  if (W.codebook == kCbFp4) return launch_fwd_cb<kCbFp4>(W, X, M, U, B, r, s, Y, st);
-  if (W.codebook == kCbInt4) return launch_fwd_cb<kCbInt4>(W, X, M, U, B, r, s, Y, st);
-  return launch_fwd_cb<kCbNf4>(W, X, M, U, B, r, s, Y, st);
+                      float s, bf16_t* Y, hipStream_t st, int parts) {
+  if (W.codebook == kCbFp4) return launch_fwd_cb<kCbFp4>(W, X, M, U, B, r, s, Y, st, parts);
+  if (W.codebook == kCbInt4) return launch_fwd_cb<kCbInt4>(W, X, M, U, B, r, s, Y, st, parts);
+  return launch_fwd_cb<kCbNf4>(W, X, M, U, B, r, s, Y, st, parts);
 }
 
 hipError_t launch_dx(const Nf4View& W, const bf16_t* dY, int64_t M, const bf16_t* G, const bf16_t* A, int r,

@@ -2,9 +2,11 @@
 // channels: Y = X W^T and the adapter's term, in tiles small enough to reach
 // every CU, for bf16 and for 8-bit operands.
 //
-//   forward   Y = X W^T + s U B^T           (B [N x r])
-//   dX        Y = X W^T + s (G A)           (A [r x N], W a transposed weight)
-//   dX under dropout                        (s G A masked as Y's own shape)
+//   forward   Y = X W^T + T B^T             (B [N x r], T = s U)
+//   dX        Y = X W^T + T A               (A [r x N], W a transposed weight, T = s G)
+//   dX under dropout                        (T A masked as Y's own shape)
+//
+// T comes as kTermParts bf16 matrices, summed as one of twice the rank.
 //
 // TM tokens x TN channels per workgroup, waves 2 x 2 over the tile, a ring of
 // NS stages of 128 bytes of all its rows, brought by buffer->LDS DMA.  The
@@ -125,8 +127,8 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
 
   // D[channel][token]: lane (lr, h): token lr, channels 8 q + 4 h .. of a
   // block.  The adapter's product is summed on its own (it is masked, or added
-  // to scaled integer sums), from global memory: 8 ranks per lane half and MFMA,
-  // the loads of the next 16 ranks of all blocks in flight meanwhile.
+  // to scaled integer sums), from global memory: 8 ranks of a part per lane half
+  // and MFMA, the loads of the next 16 ranks of all blocks in flight meanwhile.
   const int r = split == 0 ? g.r : 0;
   [[maybe_unused]] float x[FJ];
   [[maybe_unused]] float4 sc[FI][4];
@@ -150,8 +152,10 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
     constexpr int kB = TAIL == kTailFwd ? 4 : 8;   // words of a weight fragment as loaded
     uint32_t fb[2][FI][kB];
     u32x4_t fu[2][FJ];
+    static_assert(kTermParts == 2);
     auto load = [&](int c, int set) __attribute__((always_inline)) {
-      const int k = c + 8 * h;   // past the rank (r % 8 == 0), or the rows: zero
+      const int kp = c + 8 * h, part = kp >= r ? 1 : 0, k = kp - part * r;
+      const bf16_t* T = g.T + (part ? M * g.r : 0);   // past both parts (r % 8 == 0), or the rows: zero
 #pragma unroll
       for (int i = 0; i < FI; ++i) {
         const int64_t n = n0 + 32 * (FI * wc + i) + lr;
@@ -170,7 +174,7 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
       for (int j = 0; j < FJ; ++j) {
         const int64_t m = m0 + 32 * (FJ * wr + j) + lr;
         fu[set][j] = u32x4_t{0u, 0u, 0u, 0u};
-        if (k < r && m < M) fu[set][j] = *reinterpret_cast<const u32x4_t*>(g.T + m * g.r + k);
+        if (k < r && m < M) fu[set][j] = *reinterpret_cast<const u32x4_t*>(T + m * g.r + k);
       }
     };
     auto mul = [&](int set) __attribute__((always_inline)) {
@@ -190,7 +194,7 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
       }
     };
     load(0, 0);
-    for (int c = 0; c < r; c += 32) {
+    for (int c = 0; c < kTermParts * r; c += 32) {
       load(c + 16, 1);
       mul(0);
       load(c + 32, 0);
@@ -229,7 +233,7 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
           for (int e = 0; e < 4; ++e) {
             float a = (float)acc[i][j][4 * q + e];
             if constexpr (kI8) a *= x[j] * (e == 0 ? sc[i][q].x : e == 1 ? sc[i][q].y : e == 2 ? sc[i][q].z : sc[i][q].w);
-            v[e] = fmaf(g.s, y[i][j][4 * q + e], a);
+            v[e] = a + y[i][j][4 * q + e];
           }
           pack(smem + (32 * (FJ * wr + j) + lr) * kPitch + (32 * (FI * wc + i) + 8 * q + 4 * h) * kSize, v);
         }

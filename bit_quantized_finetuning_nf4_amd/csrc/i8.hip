@@ -147,13 +147,14 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const bf16_t* __restric
 template <int NCH, bool DROP>
 __global__ __launch_bounds__(256) void i8_prep_kernel(const bf16_t* __restrict__ X, int64_t M, int64_t K, int64_t ld,
                                                       const bf16_t* __restrict__ A, int r, int nu,
-                                                      bf16_t* __restrict__ U, int8_t* __restrict__ Q,
-                                                      float* __restrict__ scale, DropArgs drop) {
+                                                      bf16_t* __restrict__ U, bf16_t* __restrict__ parts, float s,
+                                                      int8_t* __restrict__ Q, float* __restrict__ scale,
+                                                      DropArgs drop) {
   __shared__ uint32_t wmax[4];
   if ((int)blockIdx.x >= nu)
     quant_row<256, NCH>(X, (int)blockIdx.x - nu, threadIdx.x, K, ld, Q, scale, wmax);
   else
-    u_rows<DROP>(X, M, K, A, r, blockIdx.x, U, drop);
+    u_rows<DROP>(X, M, K, A, r, blockIdx.x, U, parts, s, drop);
 }
 
 // deq = RNE_bf16(RN32(scale q)).
@@ -244,12 +245,12 @@ hipError_t launch_quant_rows(const bf16_t* X, int64_t M, int64_t K, int8_t* Q, f
 bool i8_prep_ok(int64_t M, int64_t K, int r, bool drop) { return u_rows_ok(M, K, r, drop) && i8_row_bytes(K) <= 32768; }
 
 hipError_t launch_i8_prep(const bf16_t* X, int64_t M, int64_t K, const bf16_t* A, int r, const DropArgs* drop,
-                          bf16_t* U, int8_t* Q, float* scale, hipStream_t st) {
+                          bf16_t* U, bf16_t* parts, float s, int8_t* Q, float* scale, hipStream_t st) {
   const int64_t ld = i8_row_bytes(K);
   const int nu = u_rows_blocks(M, r);
   auto go = [&](auto* fn) {
-    hipLaunchKernelGGL(fn, dim3((unsigned)(nu + M)), dim3(256), 0, st, X, M, K, ld, A, r, nu, U, Q, scale,
-                       drop ? *drop : DropArgs{});
+    hipLaunchKernelGGL(fn, dim3((unsigned)(nu + M)), dim3(256), 0, st, X, M, K, ld, A, r, nu, U, parts, s, Q,
+                       scale, drop ? *drop : DropArgs{});
   };
   if (ld <= 4096)
     drop ? go(&i8_prep_kernel<1, true>) : go(&i8_prep_kernel<1, false>);

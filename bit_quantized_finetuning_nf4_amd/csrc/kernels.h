@@ -73,9 +73,10 @@ struct DeqSrcs {
 hipError_t launch_dequant_group(const DeqSrcs& src, int n, int64_t N, int64_t K, int codebook, int absfmt,
                                 bool transposed, bf16_t* out, int64_t ldo, int64_t out_gs, hipStream_t s);
 
-// Y = X deq(W)^T + s * U * B^T  (U already holds X A^T in bf16; r may be 0)
+// Y = X deq(W)^T + s * U * B^T  (U already holds X A^T in bf16; r may be 0).
+// parts: U is the sum of that many matrices [M x r], one after the other.
 hipError_t launch_fwd(const Nf4View& W, const bf16_t* X, int64_t M, const bf16_t* U, const bf16_t* B,
-                      int r, float s, bf16_t* Y, hipStream_t st);
+                      int r, float s, bf16_t* Y, hipStream_t st, int parts = 1);
 
 // dX = dY deq(W) + s * G * A  (G = dY B in bf16; r may be 0)
 hipError_t launch_dx(const Nf4View& W, const bf16_t* dY, int64_t M, const bf16_t* G, const bf16_t* A,
@@ -142,10 +143,19 @@ struct PadRows {
 inline PadRows pad_rows(const bf16_t* in, int64_t rows, int64_t cols, bf16_t* out, int64_t ld) {
   return PadRows{in, out, rows, cols, ld, (int)((rows * (in ? ld >> 3 : (ld - cols) >> 3) + 255) / 256)};
 }
+//
+// What such a product gives: out [M x r] bf16 (may be null), and parts (may be
+// null), s times it as the sum of bf16 matrices [M x r], one after the other:
+// kTermParts of them, or (kRideSum3) kGradParts.  The dense products take the
+// adapter's side in that form: one bf16 would leave Y and dX an error of 2^-9
+// of the adapter's term, as large as the rounding of the result; two leave
+// 2^-17.  s is applied in fp32, before the split.
+constexpr int kTermParts = 2, kGradParts = 3;
 struct Ride {
   RideKind kind;
   int blocks;                 // workgroups of 256
-  bf16_t* out;
+  bf16_t *out, *parts;
+  float s;
   const float* part;          // sums of partials
   int splits;
   int64_t n;
@@ -157,27 +167,27 @@ struct Ride {
   PadRows pad[2];             // kRideSum3: padded copies, too
 };
 hipError_t launch_ride(const Ride& a, hipStream_t st);
-// out [M x r] = drop(X) A^T: all but *rest (kRideSum, kRideRows or
+// U = drop(X) A^T, to out and parts: all but *rest (kRideSum, kRideRows or
 // kRideRowsDrop).
 hipError_t start_xat_drop(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, const DropArgs* drop,
-                          float* part, bf16_t* out, Ride* rest, hipStream_t st);
-// G = dY B as the sum of three bf16 matrices [M x r], one after the other: all
-// but *rest (kRideSum3).
-hipError_t start_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* out,
-                           Ride* rest, hipStream_t st);
-// dA [r x K] = scale G^T drop(X) with G3 as above, dB [N x r] = scale dY^T U.
+                          float* part, bf16_t* out, bf16_t* parts, float s, Ride* rest, hipStream_t st);
+// s G = s dY B as kGradParts parts: all but *rest (kRideSum3).
+hipError_t start_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t N, int r, float* part, bf16_t* parts,
+                           float s, Ride* rest, hipStream_t st);
+// dA [r x K] = G^T drop(X) with G3 as above (s in it, and 1 / (1 - p) too),
+// dB [N x r] = scale dY^T U.
 hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t* dY, const bf16_t* U, int64_t M,
                                 int64_t N, int64_t K, int r, const DropArgs* drop, float* part, float* dA, float* dB,
                                 float scale, hipStream_t st);
 
-// launch_bf16_fwd on the small tiles or the 256-token kernels, whichever is
-// estimated faster: Y [M x N] = X Wd^T + s T B'^T, with b_trans and drop (may
-// be null) the adapter's term masked as the M x N tensor was (dX).  K % 64 ==
-// 0; part as for launch_bf16_fwd, staged_part_bytes are enough.
+// The small tiles or the 256-token kernels, whichever is estimated faster: Y
+// [M x N] = X Wd^T + T B'^T, T in kTermParts parts; with b_trans and drop (may
+// be null) the adapter's term masked as the M x N tensor was (dX), its scale in
+// T.  K % 64 == 0; part as for launch_bf16_fwd, staged_part_bytes are enough.
 size_t staged_part_bytes(int64_t N, int64_t K, int64_t M);
 double staged_cost(int64_t N, int64_t K, int64_t M);   // us, estimated
 hipError_t launch_staged(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* T,
-                         const bf16_t* B, bool b_trans, int r, float s, const DropArgs* drop, bf16_t* Y, hipStream_t st,
+                         const bf16_t* B, bool b_trans, int r, const DropArgs* drop, bf16_t* Y, hipStream_t st,
                          float* part, size_t part_bytes);
 
 // Rows of 8-bit integers with one scale each (i8.hip): bytes from one row to
@@ -188,18 +198,18 @@ constexpr int64_t kI8MaxCols = 131072;   // 127^2 cols fits a 32-bit sum
 // sum: null, or a step of kRideSum to take along.
 hipError_t launch_quant_rows(const bf16_t* X, int64_t M, int64_t K, int8_t* Q, float* scale, const Ride* sum,
                              hipStream_t st);
-// U [M x r] = drop(X) A^T (r may be 0, drop null) and X quantized, in one
-// launch, where i8_prep_ok.
+// U = drop(X) A^T, to U (may be null) and parts as above (r may be 0, drop
+// null), and X quantized, in one launch, where i8_prep_ok.
 bool i8_prep_ok(int64_t M, int64_t K, int r, bool drop);
 hipError_t launch_i8_prep(const bf16_t* X, int64_t M, int64_t K, const bf16_t* A, int r, const DropArgs* drop,
-                          bf16_t* U, int8_t* Q, float* scale, hipStream_t st);
+                          bf16_t* U, bf16_t* parts, float s, int8_t* Q, float* scale, hipStream_t st);
 hipError_t launch_i8_dequant(const int8_t* Q, const float* scale, int64_t N, int64_t K, bf16_t* out, hipStream_t st);
 // out [K x ldo] = deq^T, ldo = N rounded up to 64, the columns past N zero;
 // rest: of kRideSum3, possibly empty.
 hipError_t launch_i8_dequant_t(const int8_t* Q, const float* scale, int64_t N, int64_t K, bf16_t* out, int64_t ldo,
                                const Ride& rest, hipStream_t st);
 
-// Y [M x N] = sx sw^T o (Xq Wq^T) + s U B^T (r may be 0).
+// Y [M x N] = sx sw^T o (Xq Wq^T) + T B^T (r may be 0), T in kTermParts parts.
 struct I8Gemm {
   const int8_t* Wq;
   const float* sw;
@@ -207,10 +217,9 @@ struct I8Gemm {
   const int8_t* Xq;
   const float* sx;
   int64_t M;
-  const bf16_t* U;
+  const bf16_t* T;
   const bf16_t* B;
   int r;
-  float s;
   bf16_t* Y;
 };
 // part (part_bytes of fp32 scratch, may be null) lets shapes of few tiles split
@@ -220,8 +229,8 @@ hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, float* part, size_t p
 
 // Tiles of a middling product (gemm_tile.hip).  Rows of W [N] and X [M] are
 // row_bytes apart, whole 128-byte lines; sw and sx: 8-bit operands.  The
-// adapter's term: T [M x r] with B [N x r], or with b_trans A [r x N], masked
-// by `drop` if `dropped`.
+// adapter's term: T, kTermParts parts [M x r], with B [N x r], or with b_trans A
+// [r x N], masked by `drop` if `dropped`.
 struct TileGemm {
   const void* W;
   const void* X;
@@ -231,7 +240,6 @@ struct TileGemm {
   const bf16_t* T;
   const bf16_t* B;
   int r;
-  float s;
   bool b_trans, dropped;
   DropArgs drop;
   bf16_t* Y;

@@ -32,17 +32,13 @@ __device__ __forceinline__ float4 sum_splits(const float* __restrict__ part, int
   return make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
 }
 
-// What the bf16 h leaves of v; nothing where h is not finite (an infinity minus
-// itself would make the gradient NaN where its sum is infinite).
-__device__ __forceinline__ float rest_of(float v, uint32_t h) {
-  return (h & 0x7F80u) == 0x7F80u ? 0.0f : v - bf2f(h);
-}
-
 // Workgroup `block` (of a.blocks, 256 threads) of the step.
-//   kRideSum   bf16 of the splits' sum times scale
-//   kRideSum3  the sum as three bf16 parts, n elements apart: each the bf16
-//              rounding of what the parts before it left, together the fp32 sum
-//              (the workgroups after those that pad rows)
+//   kRideSum   v = the splits' sum times scale: bf16 of v to out, s v as two
+//              parts
+//   kRideSum3  s v as three parts, together its fp32 value (the workgroups
+//              after those that pad rows)
+// Parts lie n elements apart, each the bf16 rounding of what those before it
+// left.
 //   kRideRows, kRideRowsDrop   U by rows (urows.h)
 __device__ __forceinline__ void pad_block(const PadRows& p, int block) {
   const int64_t c0 = p.in ? 0 : p.cols >> 3, per = (p.ld >> 3) - c0;
@@ -56,7 +52,7 @@ __device__ __forceinline__ void pad_block(const PadRows& p, int block) {
 template <int KIND>
 __device__ __forceinline__ void ride(const Ride& a, int block) {
   if constexpr (KIND == kRideRows || KIND == kRideRowsDrop) {
-    u_rows<KIND == kRideRowsDrop>(a.X, a.M, a.K, a.A, a.r, block, a.out, a.drop);
+    u_rows<KIND == kRideRowsDrop>(a.X, a.M, a.K, a.A, a.r, block, a.out, a.parts, a.s, a.drop);
   } else {
     if constexpr (KIND == kRideSum3) {
       if (block < a.pad[0].blocks) return pad_block(a.pad[0], block);
@@ -67,10 +63,14 @@ __device__ __forceinline__ void ride(const Ride& a, int block) {
     const int64_t i = ((int64_t)block * 256 + threadIdx.x) * 4;
     if (i >= a.n) return;
     float4 v = sum_splits(a.part, a.splits, a.n, i, a.scale);
+    if (KIND == kRideSum && a.out)
+      *reinterpret_cast<uint2*>(a.out + i) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    if (!a.parts) return;
+    v = make_float4(v.x * a.s, v.y * a.s, v.z * a.s, v.w * a.s);
 #pragma unroll
-    for (int k = 0; k < (KIND == kRideSum3 ? 3 : 1); ++k) {
+    for (int k = 0; k < (KIND == kRideSum3 ? kGradParts : kTermParts); ++k) {
       const uint2 p = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-      *reinterpret_cast<uint2*>(a.out + k * a.n + i) = p;
+      *reinterpret_cast<uint2*>(a.parts + k * a.n + i) = p;
       v = make_float4(rest_of(v.x, p.x & 0xFFFFu), rest_of(v.y, p.x >> 16), rest_of(v.z, p.y & 0xFFFFu),
                       rest_of(v.w, p.y >> 16));
     }

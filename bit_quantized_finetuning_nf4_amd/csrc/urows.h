@@ -13,9 +13,16 @@ namespace qlora {
 
 constexpr int kURowTokens = 4;
 
+// What the bf16 h leaves of v; nothing where h is not finite (an infinity minus
+// itself would make the gradient NaN where its sum is infinite).
+__device__ __forceinline__ float rest_of(float v, uint32_t h) {
+  return (h & 0x7F80u) == 0x7F80u ? 0.0f : v - bf2f(h);
+}
+
 template <bool DROP>
 __device__ __forceinline__ void u_rows(const bf16_t* __restrict__ X, int64_t M, int64_t K, const bf16_t* __restrict__ A,
-                                       int r, int block, bf16_t* __restrict__ U, const DropArgs& drop) {
+                                       int r, int block, bf16_t* __restrict__ U, bf16_t* __restrict__ parts, float s,
+                                       const DropArgs& drop) {
   __shared__ float part[4][kURowTokens];
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
   const int j = block % r, m0 = block / r * kURowTokens;
@@ -73,7 +80,16 @@ __device__ __forceinline__ void u_rows(const bf16_t* __restrict__ X, int64_t M, 
   if (t < mt) {
     float v = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
     if constexpr (DROP) v *= drop.scale;
-    U[(int64_t)(m0 + t) * r + j] = (bf16_t)pack_bf16x2(v, 0.0f);
+    const int64_t o = (int64_t)(m0 + t) * r + j;
+    if (U) U[o] = (bf16_t)pack_bf16x2(v, 0.0f);
+    v *= s;
+#pragma unroll
+    for (int k = 0; k < kTermParts; ++k)
+      if (parts) {
+        const uint32_t p = pack_bf16x2(v, 0.0f) & 0xFFFFu;
+        parts[(int64_t)k * M * r + o] = (bf16_t)p;
+        v = rest_of(v, p);
+      }
   }
 }
 

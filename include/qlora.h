@@ -560,6 +560,8 @@ qlora_status qlora_dropout(const uint16_t* x, int64_t n, const qlora_drop* drop,
 
 /* qlora_linear_fwd with the adapter under dropout:
  *   Y = X deq(W)^T + s U B^T,  U = drop(X) A^T,  drop over X [M x K].
+ * Y takes s U as two bf16 parts of its fp32 sum (2^-17 of it is lost); only
+ * U_save is U rounded to bf16.
  * Arguments, paths and errors as qlora_linear_fwd; r > 0 and drop not NULL;
  * M r, N r and r K below 2^31 (QLORA_E_UNSUPPORTED otherwise, here and in the
  * backward).
@@ -574,8 +576,8 @@ qlora_status qlora_linear_fwd_drop(const qlora_nf4_weight* W, const uint16_t* X,
  *   dX = dY deq(W) + s drop'(G A),  G = dY B,  drop'(Z) masked and scaled as
  *                                   X was (NULL dX skips it);
  *   dA = s G^T drop(X),  dB = s dY^T U.
- * U_saved is the forward's U; NULL computes it again.  G is kept in fp32 for
- * dA (as three bf16 parts), in bf16 for dX.  Always staged, for
+ * U_saved is the forward's U; NULL computes it again.  s G enters dA as three
+ * bf16 parts (fp32's precision) and dX as the first two.  Always staged, for
  * any M: workspace qlora_workspace_bytes(QLORA_OP_BWD_DROP, M, N, K, r, 0),
  * which holds deq(W)^T.  K % 64 == 0, N % 8 == 0; with Np = N rounded up to
  * 64, Np K and M Np below 2^31 (QLORA_E_UNSUPPORTED otherwise). */
@@ -619,7 +621,8 @@ qlora_status qlora_i8_dequant(const qlora_i8_rows* q, uint16_t* out, void* strea
 qlora_status qlora_i8_matmul(const qlora_i8_rows* X, const qlora_i8_rows* W, uint16_t* Y, void* stream);
 
 /* Forward: Y [M x N] = Xq W^T (as qlora_i8_matmul, with X quantized per token
- * into the workspace) + s U B^T, U = drop(X) A^T (drop NULL: X A^T).  A, B,
+ * into the workspace) + s U B^T, U = drop(X) A^T (drop NULL: X A^T), with s U
+ * in two parts as for qlora_linear_fwd_drop.  A, B,
  * r, alpha, U_save as for qlora_linear_fwd; r == 0 gives the frozen layer
  * alone (drop must be NULL).  Any M >= 1; N % 8 == 0, K % 8 == 0.
  * Workspace: qlora_workspace_bytes(QLORA_OP_I8_FWD, M, N, K, r, 0). */
