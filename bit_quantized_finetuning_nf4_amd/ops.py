@@ -258,6 +258,18 @@ def _beside(t, like, name):
     return t
 
 
+def _whole(q: QuantizedWeight, like):
+    """The weight's arrays beside `like`, of their types and at least the sizes
+    that its rows and cols need."""
+    blocks = -(-q.rows * q.cols // BLOCKSIZE)
+    for t, dtype, n, name in ((q.codes, torch.uint8, -(-q.rows * q.cols // 2), "codes"),
+                              (q.absmax_q, torch.uint8, blocks, "absmax_q"),
+                              (q.group_scale, torch.float32, -(-blocks // GROUP_BLOCKS), "group_scale")):
+        _beside(_need(t, dtype, name), like, name)
+        if t.numel() < n:
+            raise ValueError(f"{name} holds {t.numel()} elements, a {q.rows} x {q.cols} weight has {n}")
+
+
 def _out(t, shape, dtype, like, name):
     """The caller's output checked, or a new one."""
     if t is None:
@@ -312,17 +324,15 @@ def linear_fwd(q: QuantizedWeight, X: torch.Tensor, A=None, B=None, alpha: float
     if r:
         _need(A, torch.bfloat16, "A", (r, q.cols))
         _need(B, torch.bfloat16, "B", (q.rows, r))
-    Y = out if out is not None else _empty(M, q.rows, dtype=torch.bfloat16, device=X.device)
-    U = None
-    if save_u and r:
-        U = u_out if u_out is not None else _empty(M, r, dtype=torch.bfloat16, device=X.device)
     if drop is not None:
         if path != "auto":
             raise ValueError("the forward under dropout takes the path that the library chooses")
         _on_current(X.device)
         _need(X, torch.bfloat16, "X", (M, q.cols))
-        for t, name in ((q.codes, "q"), (A, "A"), (B, "B"), (Y, "out"), (U, "u_out")):
-            _beside(t, X, name)
+        _beside(A, X, "A"), _beside(B, X, "B")
+        _whole(q, X)
+        Y = _out(out, (M, q.rows), torch.bfloat16, X, "out")
+        U = _out(u_out, (M, r), torch.bfloat16, X, "u_out") if save_u and r else None
         d = q.desc()
         ws = _ws_for(ws, workspace_bytes(_lib.QLORA_OP_FWD_DROP, M, q.rows, q.cols, r), X)
         dd = drop.desc(X.device)
@@ -330,6 +340,10 @@ def linear_fwd(q: QuantizedWeight, X: torch.Tensor, A=None, B=None, alpha: float
                                           ctypes.byref(dd), _ptr(Y), _ptr(U), *_ws_args(ws), _stream()),
               "qlora_linear_fwd_drop")
         return (Y, U) if save_u else Y
+    Y = out if out is not None else _empty(M, q.rows, dtype=torch.bfloat16, device=X.device)
+    U = None
+    if save_u and r:
+        U = u_out if u_out is not None else _empty(M, r, dtype=torch.bfloat16, device=X.device)
     nbytes = workspace_bytes(_op(path, _lib.QLORA_OP_FWD, _lib.QLORA_OP_FWD_FUSED), M, q.rows, q.cols, r)
     if ws is None:
         ws = workspace(nbytes, X.device)
@@ -376,8 +390,8 @@ def linear_bwd(q: QuantizedWeight, X: torch.Tensor, dY: torch.Tensor, A=None, B=
     if drop is not None:
         if path != "auto":
             raise ValueError("the backward under dropout has no fused path")
+        _whole(q, dY)
         d = q.desc()
-        _beside(q.codes, dY, "q")
         return _staged_bwd("qlora_linear_bwd_drop", _lib.QLORA_OP_BWD_DROP, d, q.rows, q.cols, X, dY, A, B, alpha, U,
                            drop, need_dx, dX, dA, dB, ws)
     M = dY.shape[0]
