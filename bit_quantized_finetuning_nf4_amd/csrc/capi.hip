@@ -151,12 +151,12 @@ FwdLayout fwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, bool staged) {
   return L;
 }
 
-// The forward under dropout is staged from kStagedMinTokens tokens on, and below where the estimate says so: the fused kernel takes about 26 ns a
-// column of K and round of 256 x 256 tiles (256 x 1024 x 1024: 31 us on four
-// workgroups, against 3 us to dequantize and 12 for 64 x 64 tiles; 263 x 16576
-// x 3968: about 100 us, against 35 and 80), the dequantization 2.5 bytes a
-// weight at 4.4 TB/s.  (Fixed rates, so that the workspace does not depend on
-// the device.)
+// The forward under dropout is staged from kStagedMinTokens tokens on, and below
+// where the estimate says so: the fused kernel takes about 26 ns a column of K
+// and round of 256 x 256 tiles (256 x 1024 x 1024: 31 us on four workgroups,
+// against 3 us to dequantize and 12 for 64 x 64 tiles; 263 x 16576 x 3968: about
+// 100 us, against 35 and 80), the dequantization 2.5 bytes a weight at 4.4 TB/s.
+// (Fixed rates, so that the workspace does not depend on the device.)
 bool drop_fwd_staged(int64_t M, int64_t N, int64_t K) {
   if (N > (int64_t)0x7FFFFFFF / K) return false;
   if (staged_ok(M, N, K)) return true;
@@ -946,7 +946,7 @@ qlora_status qlora_i8_linear_fwd(const qlora_i8_rows* W, const uint16_t* X, int6
   }
   if (st != QLORA_OK) return st;
   const I8Gemm g{W->codes, W->scale, N, K, xq, sx, M, T, B, r, Y};
-  return hip_status(launch_i8_gemm(g, s, part, L.part_bytes));
+  return hip_status(launch_i8_gemm(g, s, reinterpret_cast<int32_t*>(part), L.part_bytes));
 }
 
 qlora_status qlora_i8_linear_bwd(const qlora_i8_rows* W, const uint16_t* X, const uint16_t* dY, int64_t M,

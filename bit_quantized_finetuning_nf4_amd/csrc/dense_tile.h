@@ -301,12 +301,14 @@ __device__ __forceinline__ bf16x8_t scale_frag(bf16x8_t v, float s) {
   return __builtin_bit_cast(bf16x8_t, scale16(__builtin_bit_cast(uint4, v), s));
 }
 
-// fp32 sums of the tile (the lane layout of store_tile_lds): lane (lr, h) of
-// wave (wr, wc) holds token row0 + 128 wr + 32 j + lr, columns col0 + 32 FI
-// wc + 32 i + 8 q + 4 h + 0..3, stored as one 16-byte piece (cols % 4 == 0).
-template <int FI>
-__device__ __forceinline__ void store_tile_f32(const f32x16_t (&acc)[FI][4], float* out, int64_t ld, int64_t rows,
-                                               int64_t cols, int64_t row0, int64_t col0) {
+// The tile's sums as they are, fp32 or 32-bit integers (the lane layout of
+// store_tile_lds): lane (lr, h) of wave (wr, wc) holds token row0 + 128 wr + 32 j
+// + lr, columns col0 + 32 FI wc + 32 i + 8 q + 4 h + 0..3, stored as one 16-byte
+// piece (cols % 4 == 0).
+template <int FI, class ACC, class T>
+__device__ __forceinline__ void store_tile_parts(const ACC (&acc)[FI][4], T* out, int64_t ld, int64_t rows,
+                                                 int64_t cols, int64_t row0, int64_t col0) {
+  typedef T piece_t __attribute__((ext_vector_type(4)));
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1, lr = lane & 31, h = lane >> 5;
 #pragma unroll
   for (int i = 0; i < FI; ++i)
@@ -317,8 +319,8 @@ __device__ __forceinline__ void store_tile_f32(const f32x16_t (&acc)[FI][4], flo
       for (int q = 0; q < 4; ++q) {
         const int64_t col = col0 + 32 * FI * wc + 32 * i + 8 * q + 4 * h;
         if (row < rows && col < cols)
-          *reinterpret_cast<float4*>(out + row * ld + col) =
-              make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+          *reinterpret_cast<piece_t*>(out + row * ld + col) =
+              piece_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
       }
     }
 }

@@ -346,7 +346,7 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
     }
   }
   if (part != nullptr)
-    store_tile_f32<FI>(acc, part + (int64_t)split * M * N, N, M, N, m0, n0);
+    store_tile_parts<FI>(acc, part + (int64_t)split * M * N, N, M, N, m0, n0);
   else
     store_tile_lds<FI>(acc, Y, N, M, N, m0, n0, smem);
 }

@@ -6,7 +6,8 @@
 // with T = s U as kTermParts bf16 matrices.
 //
 // The sum over k is exact: products of integers up to 127 in 32-bit sums, no
-// overflow for K <= 131072 (127^2 K < 2^31).  It is rounded to fp32 when it
+// overflow for K <= 131072 (127^2 K < 2^31); a split contraction leaves its
+// parts as integers, which the sum kernel adds.  It is rounded to fp32 when it
 // is multiplied by the scales, and the adapter's product is added in fp32.
 //
 // The tile is the dense bf16 GEMM's (dense_tile.h): the operands stream the
@@ -105,8 +106,8 @@ __device__ __forceinline__ void lora_tail(f32x16_t (&acc)[FI][4], const bf16_t* 
 
 // Xq [M x ld], Wq [N x ld] bytes, whole 128-byte pairs; tiles of 64 FI channels
 // x 256 tokens from channel n_begin on.  part != null: the grid holds the tiles
-// once per split of the contraction, pps pairs each, split 0 with the adapter's
-// term, and their fp32 values go to part + split M N instead of Y.
+// once per split of the contraction, pps pairs each, and their integer sums go
+// to part + split M N, the rest being the sum kernel's.
 // TD: the LoRA tail by DMA.
 template <int FI, bool TD>
 __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __restrict__ Wq,
@@ -116,7 +117,7 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
                                                               const bf16_t* __restrict__ T,
                                                               const bf16_t* __restrict__ B, int r,
                                                               bf16_t* __restrict__ Y, int64_t n_begin, int tiles_n,
-                                                              int tiles_m, int pps, float* __restrict__ part) {
+                                                              int tiles_m, int pps, int32_t* __restrict__ part) {
   extern __shared__ __align__(16) char smem[];
   int tn, tm;
   const int id = xcd_tile_id(), split = id / (tiles_n * tiles_m), p0 = split * pps;
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-  const bool tail = r > 0 && split == 0;
+  const bool tail = r > 0;
   scales_dma(smem + kLdsPairs, sx, sw, M, N, m0, n0, f.w, lane);
 #pragma unroll
   for (int d = 0; d < 2 * FI + 8; ++d) {
@@ -184,6 +185,10 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
   // drain the DMAs still in flight (clamped re-loads) before reusing LDS
   QLORA_WAIT(0, 0);
   __builtin_amdgcn_s_barrier();
+  if (part != nullptr) {
+    store_tile_parts<FI>(acc, part + (int64_t)split * M * N, N, M, N, m0, n0);
+    return;
+  }
   // TD: the parts' chunks (32 ranks each) come into the pair slots, four at a
   // time, the first four while the sums become fp32
   const int nj = r / 32, nt = kTermParts * nj;
@@ -221,10 +226,118 @@ __global__ __launch_bounds__(kThreads, 1) void i8_gemm_kernel(const int8_t* __re
       lora_tail<FI>(out, B, T, r, M, N, m0, n0, smem);
     }
   }
-  if (part != nullptr)
-    store_tile_f32<FI>(out, part + (int64_t)split * M * N, N, M, N, m0, n0);
-  else
-    store_tile_lds<FI>(out, Y, N, M, N, m0, n0, smem);
+  store_tile_lds<FI>(out, Y, N, M, N, m0, n0, smem);
+}
+
+// Ranks k .. k + 7 of the two parts, counted as one rank of 2 r: of B's row (or
+// 0 where the row is past the end), and of T's.
+__device__ __forceinline__ bf16x8_t b_ranks(const bf16_t* __restrict__ B, int r, int64_t n, int64_t N, int kp) {
+  static_assert(kTermParts == 2);
+  const int k = kp >= r ? kp - r : kp;
+  bf16x8_t v{};
+  if (k < r && n < N) v = *reinterpret_cast<const bf16x8_t*>(B + n * r + k);
+  return v;
+}
+__device__ __forceinline__ bf16x8_t t_ranks(const bf16_t* __restrict__ T, int r, int64_t m, int64_t M, int kp) {
+  const int part = kp >= r ? 1 : 0, k = kp - part * r;
+  bf16x8_t v{};
+  if (k < r && m < M) v = *reinterpret_cast<const bf16x8_t*>(T + (part * M + m) * r + k);
+  return v;
+}
+// Channels n .. n + 3 of a token of scale x: the integer sums t, scaled, and the
+// adapter's, to its row at y.
+__device__ __forceinline__ void put4(i32x4_t t, f32x4_t lo, float4 sc, float x, bf16_t* __restrict__ y, int64_t n) {
+  const float y0 = (float)t[0] * (x * sc.x) + lo[0], y1 = (float)t[1] * (x * sc.y) + lo[1],
+              y2 = (float)t[2] * (x * sc.z) + lo[2], y3 = (float)t[3] * (x * sc.w) + lo[3];
+  *reinterpret_cast<uint2*>(y + n) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
+}
+
+// Y from the integer parts of a split product, 64 tokens x 64 channels a
+// workgroup: thread t adds the parts of channels 4 (t mod 16) .. of tokens t / 16
+// + 16 i, whole lines of the parts' and of Y's rows, the loads of S splits
+// together; the adapter's term comes from four 16x16 MFMA blocks per wave
+// through LDS meanwhile.  2048 x 4096 in two splits 27 us at rank 64 (read in the
+// MFMA's layout, 16 tokens' half lines per instruction, 36); what it adds to a sum
+// of fp32 parts, 13 us, the product saves in its own epilogue for the most part.
+template <int S>
+__global__ __launch_bounds__(kThreads) void i8_sum_kernel(const int32_t* __restrict__ part, int splits,
+                                                          const float* __restrict__ sw, int64_t N,
+                                                          const float* __restrict__ sx, int64_t M,
+                                                          const bf16_t* __restrict__ T, const bf16_t* __restrict__ B,
+                                                          int r, bf16_t* __restrict__ Y, int cols) {
+  constexpr int kPitch = 68;
+  __shared__ __align__(16) float term[64 * kPitch];
+  const int64_t m0 = (int64_t)(blockIdx.x / cols) * 64, n0 = (int64_t)(blockIdx.x % cols) * 64;
+  const int tok = threadIdx.x >> 4, ch = 4 * (threadIdx.x & 15);
+  // tokens and channels past the end re-read the last ones, never stored
+  const int64_t n = min(n0 + ch, N - 4);
+  i32x4_t t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = i32x4_t{0, 0, 0, 0};
+  for (int s0 = 0; s0 < splits; s0 += S) {
+    i32x4_t v[S][4];
+#pragma unroll
+    for (int k = 0; k < S; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t row = min(s0 + k, splits - 1) * M + min(m0 + tok + 16 * i, M - 1);
+        v[k][i] = *reinterpret_cast<const i32x4_t*>(part + row * N + n);
+      }
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      const int in = s0 + k < splits ? -1 : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] += v[k][i] & in;
+    }
+  }
+  if (r > 0) {
+    // wave w: tokens 32 (w / 2) .., channels 32 (w mod 2) ..
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane & 15, g = lane >> 4;
+    const int wm = 32 * (w >> 1), wn = 32 * (w & 1);
+    f32x4_t lo[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) lo[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < kTermParts * r; c += 64) {
+      bf16x8_t fb[2][2], fu[2][2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          fb[k][i] = b_ranks(B, r, n0 + wn + 16 * i + l, N, c + 32 * k + 8 * g);
+          fu[k][i] = t_ranks(T, r, m0 + wm + 16 * i + l, M, c + 32 * k + 8 * g);
+        }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            lo[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[k][i], fu[k][j], lo[i][j], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<f32x4_t*>(term + (wm + 16 * j + l) * kPitch + wn + 16 * i + 4 * g) = lo[i][j];
+    __syncthreads();
+  }
+  const float4 sc = *reinterpret_cast<const float4*>(sw + n);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t m = m0 + tok + 16 * i;
+    f32x4_t lo = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (r > 0) lo = *reinterpret_cast<const f32x4_t*>(term + (tok + 16 * i) * kPitch + ch);
+    if (m < M && n0 + ch < N) put4(t[i], lo, sc, sx[m], Y + m * N, n);   // N % 8 == 0
+  }
+}
+hipError_t launch_i8_sum(const I8Gemm& g, int splits, const int32_t* part, hipStream_t st) {
+  const int cols = (int)((g.N + 63) / 64);
+  auto* fn = splits <= 2 ? &i8_sum_kernel<2> : &i8_sum_kernel<4>;
+  hipLaunchKernelGGL(fn, dim3((unsigned)((g.M + 63) / 64 * cols)), dim3(kThreads), 0, st, part, splits, g.sw,
+                     g.N, g.sx, g.M, g.T, g.B, g.r, g.Y, cols);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -326,23 +439,13 @@ __global__ __launch_bounds__(kSkWaves * 64, 1) void i8_skinny_kernel(const int8_
     i32x4_t t = red[0][blk][lane];
 #pragma unroll
     for (int v = 1; v < kSkWaves; ++v) t += red[v][blk][lane];
-    const int64_t m = 16 * j + l, nrow = n0 + 16 * i, n = nrow + 4 * g;
+    const int64_t nrow = n0 + 16 * i, m = 16 * j + l;
     f32x4_t lo = {0.0f, 0.0f, 0.0f, 0.0f};
-    static_assert(kTermParts == 2);
-    for (int c = 0; c < kTermParts * r; c += 32) {   // adapter: 16 channels x 16 tokens over the ranks of both parts
-      const int kp = c + 8 * g, part = kp >= r ? 1 : 0, k = kp - part * r;
-      bf16x8_t fb{}, fu{};
-      if (k < r && nrow + l < N) fb = *reinterpret_cast<const bf16x8_t*>(B + (nrow + l) * r + k);
-      if (k < r && m < M) fu = *reinterpret_cast<const bf16x8_t*>(T + (part * M + m) * r + k);
-      lo = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fu, lo, 0, 0, 0);
-    }
-    if (m < M && n < N) {   // N % 8 == 0
-      const float4 sc = *reinterpret_cast<const float4*>(sw + n);
-      const float x = sx[m];
-      const float y0 = (float)t[0] * (x * sc.x) + lo[0], y1 = (float)t[1] * (x * sc.y) + lo[1],
-                  y2 = (float)t[2] * (x * sc.z) + lo[2], y3 = (float)t[3] * (x * sc.w) + lo[3];
-      *reinterpret_cast<uint2*>(Y + m * N + n) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
-    }
+    for (int c = 0; c < kTermParts * r; c += 32)   // adapter: 16 channels x 16 tokens over the ranks of both parts
+      lo = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b_ranks(B, r, nrow + l, N, c + 8 * g), t_ranks(T, r, m, M, c + 8 * g),
+                                                   lo, 0, 0, 0);
+    const int64_t n = nrow + 4 * g;
+    if (m < M && n < N) put4(t, lo, *reinterpret_cast<const float4*>(sw + n), sx[m], Y + m * N, n);   // N % 8 == 0
   }
 }
 
@@ -355,7 +458,7 @@ hipError_t launch_skinny(const I8Gemm& g, hipStream_t st) {
 }
 
 template <int FI>
-hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, int splits, float* part, hipStream_t st) {
+hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, int splits, int32_t* part, hipStream_t st) {
   const int tiles_n = (int)((n_rows + 64 * FI - 1) / (64 * FI)), tiles_m = (int)((g.M + kTile - 1) / kTile);
   // the rank in whole chunks, T's parts and B within 32-bit byte offsets
   const bool td = g.r > 0 && g.r % 32 == 0 && g.M * g.r < ((int64_t)1 << 30) && g.N * g.r < ((int64_t)1 << 30);
@@ -367,8 +470,7 @@ hipError_t launch_fi(const I8Gemm& g, int64_t n_begin, int64_t n_rows, int split
   hipLaunchKernelGGL(fn, dim3(tiles_n * tiles_m * splits), dim3(kThreads), lds, st, g.Wq, g.sw, g.N,
                      i8_row_bytes(g.K), g.Xq, g.sx, g.M, g.T, g.B, g.r, g.Y, n_begin, tiles_n, tiles_m,
                      (npair + splits - 1) / splits, splits > 1 ? part : nullptr);
-  if ((e = hipGetLastError()) != hipSuccess || splits == 1) return e;
-  return launch_split_sum(part, splits, g.M * g.N, g.Y, st);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -411,7 +513,7 @@ bool use_skinny(int64_t M, int64_t N, int64_t lines, int cus, size_t part_bytes)
 
 // More tokens: tiles, the small ones or 256 x 64 FI; or whole rounds of 256 x
 // 256 tiles and the rest of the channels apart.
-hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, float* part, size_t part_bytes) {
+hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, int32_t* part, size_t part_bytes) {
   const int cus = device_cu_count();
   const int64_t lines = i8_row_bytes(g.K) / 128;
   if (use_skinny(g.M, g.N, lines, cus, part ? part_bytes : 0)) {
@@ -428,6 +530,11 @@ hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, float* part, size_t p
     t.T = g.T, t.B = g.B, t.r = g.r, t.Y = g.Y, t.part = part;
     return launch_tile(t, c, n_begin, n_rows, st);
   };
+  // (a split one: of all channels)
+  auto whole = [&](const TileChoice& c) {
+    const hipError_t e = part_of(c, 0, g.N);
+    return e != hipSuccess || c.splits == 1 ? e : launch_i8_sum(g, c.splits, part, st);
+  };
   const TileChoice one = choose_tile(g.M, g.N, lines, cus, part ? part_bytes : 0);
   const int64_t tiles_m = (g.M + 255) / 256, tiles = tiles_m * ((g.N + 255) / 256);
   if (tiles > cus && cus % tiles_m == 0) {
@@ -440,7 +547,7 @@ hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, float* part, size_t p
       }
     }
   }
-  return part_of(one, 0, g.N);
+  return whole(one);
 }
 
 size_t i8_gemm_part_bytes(int64_t M, int64_t N, int64_t K) {

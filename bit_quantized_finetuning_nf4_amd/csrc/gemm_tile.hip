@@ -20,7 +20,8 @@
 // (57 from L2 alone), whatever the depth of the ring; without its MFMAs and
 // LDS reads the loop takes the same time.  So the tile is chosen by the bytes
 // that the busiest CU brings (choose_tile), and where even the smallest tiles
-// leave CUs idle the contraction is split, the fp32 parts added in order.
+// leave CUs idle the contraction is split: fp32 parts, added in order, or the
+// 32-bit integers as they are, whose sum stays exact (gemm_i8.hip).
 #include <algorithm>
 #include <type_traits>
 
@@ -129,7 +130,7 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
   // block.  The adapter's product is summed on its own (it is masked, or added
   // to scaled integer sums), from global memory: 8 ranks of a part per lane half
   // and MFMA, the loads of the next 16 ranks of all blocks in flight meanwhile.
-  const int r = split == 0 ? g.r : 0;
+  const int r = split == 0 && !(kI8 && g.part) ? g.r : 0;
   [[maybe_unused]] float x[FJ];
   [[maybe_unused]] float4 sc[FI][4];
   if constexpr (kI8) {
@@ -220,6 +221,11 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
   // registers is 64 pieces of lines, which L2 takes one at a time: with those,
   // and the adapter's loads a block at a time, 333 x 11008 x 4096 took 35.1 us
   // at rank 16 and 39.2 at rank 64, 30.4 and 31.3 this way)
+  auto value = [&](int i, int j, int q, int e) __attribute__((always_inline)) {
+    float a = (float)acc[i][j][4 * q + e];
+    if constexpr (kI8) a *= x[j] * (e == 0 ? sc[i][q].x : e == 1 ? sc[i][q].y : e == 2 ? sc[i][q].z : sc[i][q].w);
+    return a + y[i][j][4 * q + e];
+  };
   auto out = [&](auto* dst, int64_t row0, auto pack) __attribute__((always_inline)) {
     constexpr int kSize = (int)sizeof(*dst), kPitch = TN * kSize + 16, kRow = TN * kSize / 16;
 #pragma unroll
@@ -227,16 +233,8 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
 #pragma unroll
       for (int i = 0; i < FI; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float a = (float)acc[i][j][4 * q + e];
-            if constexpr (kI8) a *= x[j] * (e == 0 ? sc[i][q].x : e == 1 ? sc[i][q].y : e == 2 ? sc[i][q].z : sc[i][q].w);
-            v[e] = a + y[i][j][4 * q + e];
-          }
-          pack(smem + (32 * (FJ * wr + j) + lr) * kPitch + (32 * (FI * wc + i) + 8 * q + 4 * h) * kSize, v);
-        }
+        for (int q = 0; q < 4; ++q)
+          pack(smem + (32 * (FJ * wr + j) + lr) * kPitch + (32 * (FI * wc + i) + 8 * q + 4 * h) * kSize, i, j, q);
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < TM * kRow / kThreads; ++p) {
@@ -247,12 +245,19 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
     }
   };
   if (g.part)
-    out(g.part, (int64_t)split * M + m0, [](char* p, const float (&v)[4]) {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    out(static_cast<float*>(g.part), (int64_t)split * M + m0, [&](char* p, int i, int j, int q)
+                                                                  __attribute__((always_inline)) {
+      if constexpr (kI8)
+        *reinterpret_cast<int4*>(p) = make_int4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                                                acc[i][j][4 * q + 3]);
+      else
+        *reinterpret_cast<float4*>(p) = make_float4(value(i, j, q, 0), value(i, j, q, 1), value(i, j, q, 2),
+                                                    value(i, j, q, 3));
     });
   else
-    out(g.Y, m0, [](char* p, const float (&v)[4]) {
-      *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    out(g.Y, m0, [&](char* p, int i, int j, int q) __attribute__((always_inline)) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(value(i, j, q, 0), value(i, j, q, 1)),
+                                                pack_bf16x2(value(i, j, q, 2), value(i, j, q, 3)));
     });
 }
 
@@ -268,8 +273,8 @@ hipError_t launch(TileGemm g, int splits, int64_t n_begin, int64_t n_rows, hipSt
   p.sps = (lines + splits - 1) / splits;
   if (splits == 1) p.g.part = nullptr;
   hipLaunchKernelGGL(fn, dim3(p.tiles_n * p.tiles_m * splits), dim3(kThreads), lds, st, p);
-  if ((e = hipGetLastError()) != hipSuccess || splits == 1) return e;
-  return launch_split_sum(g.part, splits, g.M * g.N, g.Y, st);
+  if ((e = hipGetLastError()) != hipSuccess || splits == 1 || std::is_same<MM, MmI8>::value) return e;
+  return launch_split_sum(static_cast<const float*>(g.part), splits, g.M * g.N, g.Y, st);
 }
 
 template <class MM, int TAIL>
@@ -314,7 +319,7 @@ double full_round_cost(int64_t lines) { return round_cost(kShapes[6], lines); }
 //   40 x 840 x 19840     64x64 in eight splits 11.3, unsplit 34
 // Rings of two stages lose (151 us against 115 with four, 128 x 128 at 512 x
 // 8192 x 22016); past three or four nothing changes.  A split adds a launch and
-// its fp32 parts' way through memory (mostly the last-level cache).
+// its parts' way through memory (mostly the last-level cache).
 TileChoice choose_tile(int64_t M, int64_t N, int64_t lines, int cus, size_t part_bytes) {
   TileChoice best{0, 0, 1, 1e30};
   for (const Shape& t : kShapes) {

@@ -222,15 +222,17 @@ struct I8Gemm {
   int r;
   bf16_t* Y;
 };
-// part (part_bytes of fp32 scratch, may be null) lets shapes of few tiles split
-// their contraction; i8_gemm_part_bytes is enough.
+// part (part_bytes of scratch, may be null) lets shapes of few tiles split their
+// contraction into 32-bit integer parts; i8_gemm_part_bytes is enough.
 size_t i8_gemm_part_bytes(int64_t M, int64_t N, int64_t K);
-hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, float* part, size_t part_bytes);
+hipError_t launch_i8_gemm(const I8Gemm& g, hipStream_t st, int32_t* part, size_t part_bytes);
 
 // Tiles of a middling product (gemm_tile.hip).  Rows of W [N] and X [M] are
 // row_bytes apart, whole 128-byte lines; sw and sx: 8-bit operands.  The
 // adapter's term: T, kTermParts parts [M x r], with B [N x r], or with b_trans A
-// [r x N], masked by `drop` if `dropped`.
+// [r x N], masked by `drop` if `dropped`.  A split contraction leaves fp32 parts of everything in
+// `part`, which launch_tile adds up; of 8-bit operands the integer sums alone,
+// which the caller does.
 struct TileGemm {
   const void* W;
   const void* X;
@@ -243,7 +245,7 @@ struct TileGemm {
   bool b_trans, dropped;
   DropArgs drop;
   bf16_t* Y;
-  float* part;
+  void* part;
 };
 struct TileChoice {
   int tm, tn, splits;   // tm == 256: one of the 256-token kernels
