@@ -32,6 +32,15 @@ struct MmI8 {
   }
 };
 
+// An integer sum times the scales of its channel and token, in this order: an
+// integer times a number of any size loses no range downwards, and the scales'
+// own product would leave fp32's range where the result is inside it (an
+// infinity times a sum of 0 would be NaN, 2^-150 a 0 that no sum brings back).
+// What is left is a channel's scale past 2^97, whose product with a sum may
+// overflow before a small token scale is applied; mantissas and exponents apart
+// would mend that too, and cost 2-4 % of a product.
+__device__ __forceinline__ float scaled_sum(int t, float sw, float sx) { return (float)t * sw * sx; }
+
 constexpr int kPairOp = kTile * 128;                    // 32 KiB: 256 rows x 64 bf16 (two stages)
 constexpr int kPairSlot = 2 * kPairOp;                  // weight rows at 0, token rows at kPairOp
 constexpr size_t kLdsPairs = 2 * (size_t)kPairSlot;     // 128 KiB: two pair slots

@@ -55,7 +55,7 @@ __device__ __forceinline__ void scale_tile(const i32x16_t (&acc)[FI][4], f32x16_
       // vector registers, which spills
       float f[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) f[e] = (float)acc[i][j][e] * (x[j] * v[e >> 2][e & 3]);
+      for (int e = 0; e < 16; ++e) f[e] = scaled_sum(acc[i][j][e], v[e >> 2][e & 3], x[j]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -247,8 +247,8 @@ __device__ __forceinline__ bf16x8_t t_ranks(const bf16_t* __restrict__ T, int r,
 // Channels n .. n + 3 of a token of scale x: the integer sums t, scaled, and the
 // adapter's, to its row at y.
 __device__ __forceinline__ void put4(i32x4_t t, f32x4_t lo, float4 sc, float x, bf16_t* __restrict__ y, int64_t n) {
-  const float y0 = (float)t[0] * (x * sc.x) + lo[0], y1 = (float)t[1] * (x * sc.y) + lo[1],
-              y2 = (float)t[2] * (x * sc.z) + lo[2], y3 = (float)t[3] * (x * sc.w) + lo[3];
+  const float y0 = scaled_sum(t[0], sc.x, x) + lo[0], y1 = scaled_sum(t[1], sc.y, x) + lo[1],
+              y2 = scaled_sum(t[2], sc.z, x) + lo[2], y3 = scaled_sum(t[3], sc.w, x) + lo[3];
   *reinterpret_cast<uint2*>(y + n) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
 }
 

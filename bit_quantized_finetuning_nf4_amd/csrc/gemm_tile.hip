@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
   // and MFMA, the loads of the next 16 ranks of all blocks in flight meanwhile.
   const int r = split == 0 && !(kI8 && g.part) ? g.r : 0;
   [[maybe_unused]] float x[FJ];
-  [[maybe_unused]] float4 sc[FI][4];
+  [[maybe_unused]] f32x4_t sc[FI][4];
   if constexpr (kI8) {
 #pragma unroll
     for (int j = 0; j < FJ; ++j) x[j] = g.sx[min(m0 + 32 * (FJ * wr + j) + lr, M - 1)];
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
     for (int i = 0; i < FI; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q)   // N % 8 == 0
-        sc[i][q] = *reinterpret_cast<const float4*>(g.sw + min(n0 + 32 * (FI * wc + i) + 8 * q + 4 * h, N - 4));
+        sc[i][q] = *reinterpret_cast<const f32x4_t*>(g.sw + min(n0 + 32 * (FI * wc + i) + 8 * q + 4 * h, N - 4));
   }
   f32x16_t y[FI][FJ];
 #pragma unroll
@@ -222,9 +222,10 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs p) {
   // and the adapter's loads a block at a time, 333 x 11008 x 4096 took 35.1 us
   // at rank 16 and 39.2 at rank 64, 30.4 and 31.3 this way)
   auto value = [&](int i, int j, int q, int e) __attribute__((always_inline)) {
-    float a = (float)acc[i][j][4 * q + e];
-    if constexpr (kI8) a *= x[j] * (e == 0 ? sc[i][q].x : e == 1 ? sc[i][q].y : e == 2 ? sc[i][q].z : sc[i][q].w);
-    return a + y[i][j][4 * q + e];
+    if constexpr (kI8)
+      return scaled_sum(acc[i][j][4 * q + e], sc[i][q][e], x[j]) + y[i][j][4 * q + e];
+    else
+      return acc[i][j][4 * q + e] + y[i][j][4 * q + e];
   };
   auto out = [&](auto* dst, int64_t row0, auto pack) __attribute__((always_inline)) {
     constexpr int kSize = (int)sizeof(*dst), kPitch = TN * kSize + 16, kRow = TN * kSize / 16;

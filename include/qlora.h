@@ -616,7 +616,8 @@ qlora_status qlora_i8_quantize(const uint16_t* X, const qlora_i8_rows* q, void* 
 qlora_status qlora_i8_dequant(const qlora_i8_rows* q, uint16_t* out, void* stream);
 
 /* Y [M x N] = the product of quantized rows: bf16 of sx_m sw_n sum_k x w,
- * the sum in 32-bit integers.  For callers that quantize an input once and
+ * the sum in 32-bit integers, sw_n applied first (scales of W from 2^97 on,
+ * weights past 2^104, may overflow there).  For callers that quantize an input once and
  * multiply it by several weights.  W->rows % 8 == 0, M N below 2^31. */
 qlora_status qlora_i8_matmul(const qlora_i8_rows* X, const qlora_i8_rows* W, uint16_t* Y, void* stream);
 
