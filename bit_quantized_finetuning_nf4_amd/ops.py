@@ -225,7 +225,9 @@ class Dropout:
     counter-based generator; the same seed and offset give the same mask in
     the forward and the backward pass.  Give every layer and step its own
     offset.  step, when given, is an int64 or uint64 GPU tensor of one element
-    that is added to the offset when the kernels run (for captured graphs)."""
+    that is added to the offset when the kernels run (for captured graphs):
+    space the layers' offsets by more than the steps that will be taken (layer
+    << 32, say), or layer 1 at step t has the mask of layer 0 at step t + 1."""
     p: float
     seed: int
     offset: int = 0

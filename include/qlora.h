@@ -542,8 +542,12 @@ qlora_status qlora_gemv_run(const qlora_gemv_plan* plan, void* stream);
  * 1/2)) the element is kept where the half, read as a signed number, is at
  * least t - 32768, and scaled by 65536 / (65536 - t); a dropped element is 0
  * whatever it held (infinities and NaN included).  Two calls use the same
- * mask if and only if seed and offset (and the position) agree: give each
- * layer and step its own offset. */
+ * mask if and only if seed and offset (and the position) agree, the offset
+ * being offset + *step where step is given: give each layer and step its own.
+ * Offsets and steps lie on one line, so offsets 0, 1, 2 ... of the layers and a
+ * step that grows by one would give layer l at step t + 1 the mask of layer
+ * l + 1 at step t: space the layers' offsets by more than the steps that will be
+ * taken (layer << 32, say), or give each layer its own seed. */
 typedef struct {
   double p;              /* probability of dropping, in [0, 1)               */
   uint64_t seed;
