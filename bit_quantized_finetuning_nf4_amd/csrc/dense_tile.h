@@ -48,11 +48,8 @@ constexpr size_t kLdsDense = kLdsPairs + 2 * kOp;       // + 32 KiB: the first L
 constexpr int kDGroup = 4;                              // token tiles per tile group (tile order)
 
 // Pair slots hold two consecutive 32-wide stages (one 64-wide stage): rows of
-// 128 bytes, 16-byte chunk c of row r at position c ^ ((r >> 1) & 7), so the
-// 16 lanes of one read quarter (16 consecutive rows, one chunk) and a DMA
-// instruction's 64 lanes (8 whole rows) cover all 64 LDS banks.  Chunks
-// 0..3 are the even stage, 4..7 the odd one.
-__device__ __forceinline__ int pos128(int r, int c) { return r * 128 + 16 * (c ^ ((r >> 1) & 7)); }
+// 128 bytes in the layout of pos128.  Chunks 0..3 are the even stage, 4..7 the
+// odd one.
 
 // Tile order of the dense GEMMs.  The eight XCDs receive contiguous ranges of
 // tile ids (the hardware hands workgroups to XCDs round robin); ids run over

@@ -199,8 +199,6 @@ struct WideShape {
   static constexpr int kWait = (kWideAhead - 1) * (16 + kQDma) < 63 ? (kWideAhead - 1) * (16 + kQDma) : 63;
 };
 
-__device__ __forceinline__ int pos_line(int r, int c) { return r * 128 + 16 * (c ^ ((r >> 1) & 7)); }
-
 template <int RP, bool QT, bool DROP>
 __global__ __launch_bounds__(kWideThreads, 1) void rwide_kernel(const bf16_t* __restrict__ P, int64_t M, int64_t C,
                                                             const bf16_t* __restrict__ Q, int r, int stages_per_split,
@@ -275,11 +273,11 @@ __global__ __launch_bounds__(kWideThreads, 1) void rwide_kernel(const bf16_t* __
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       const int ch = 2 * kk + h;   // both operands: columns 16 kk + 8 h ..
-      bf16x8_t b = rd16(base + pos_line(32 * w + lr, ch));
+      bf16x8_t b = rd16(base + pos128(32 * w + lr, ch));
       bf16x8_t a[FJ];
       if constexpr (!QT) {
 #pragma unroll
-        for (int f = 0; f < FJ; ++f) a[f] = rd16(base + S::kP + pos_line(32 * f + lr, ch));
+        for (int f = 0; f < FJ; ++f) a[f] = rd16(base + S::kP + pos128(32 * f + lr, ch));
       } else {
         // transposed reads in asm blocks (see tr_read2)
         constexpr int O = 4 * 2 * RP;

@@ -24,6 +24,12 @@ __device__ __forceinline__ uint4 buf_load16(rsrc_t r, uint32_t voff, uint32_t so
   return make_uint4(v.x, v.y, v.z, v.w);
 }
 
+// Rows of 128 bytes (whole cache lines) in LDS: 16-byte chunk c of row r at
+// position c ^ ((r >> 1) & 7), so the 16 lanes of one read quarter (16
+// consecutive rows, one chunk) and a DMA instruction's 64 lanes (8 whole rows)
+// cover all 64 LDS banks.
+__device__ __forceinline__ int pos128(int r, int c) { return r * 128 + 16 * (c ^ ((r >> 1) & 7)); }
+
 // s_waitcnt with vmcnt = vm and lgkmcnt = lgkm (expcnt not waited).
 constexpr int wait_imm(int vm, int lgkm) { return (vm & 15) | ((vm >> 4) << 14) | (7 << 4) | (lgkm << 8); }
 #define QLORA_WAIT(vm, lgkm) __builtin_amdgcn_s_waitcnt(wait_imm((vm), (lgkm)))
