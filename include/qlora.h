@@ -565,7 +565,8 @@ qlora_status qlora_dropout(const uint16_t* x, int64_t n, const qlora_drop* drop,
 /* qlora_linear_fwd with the adapter under dropout:
  *   Y = X deq(W)^T + s U B^T,  U = drop(X) A^T,  drop over X [M x K].
  * Y takes s U as two bf16 parts of its fp32 sum (2^-17 of it is lost); only
- * U_save is U rounded to bf16.
+ * U_save is U rounded to bf16.  What an infinity in B (here), A (dX) or a kept
+ * X (dA) reaches is infinite or NaN: it meets every part.
  * Arguments, paths and errors as qlora_linear_fwd; r > 0 and drop not NULL;
  * M r, N r and r K below 2^31 (QLORA_E_UNSUPPORTED otherwise, here and in the
  * backward).

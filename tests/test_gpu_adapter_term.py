@@ -37,7 +37,7 @@ def term_tol(ref, T, W, r):
     return 1.001 * (E * np.abs(ref) + (2.0**-16 + 2 * 2.0**-24 + 2 * r * 2.0**-23) * (np.abs(T) @ np.abs(W)))
 
 
-def check_forward(run, rng, M, N, K, r, p):
+def check_forward(run, rng, M, N, K, r, p, alpha=ALPHA):
     X, Xr = ints(rng, (M, K))
     A, Ar = ints(rng, (r, K))
     B, Br = ints(rng, (N, r))
@@ -48,7 +48,7 @@ def check_forward(run, rng, M, N, K, r, p):
     Ur = S * (OD.keep_scale(p) if p > 0 else 1.0)
     Y, U = run(X, A, B, drop)
     within(U, Ur, 1.001 * (E + 2.0**-24) * np.abs(Ur), "U")
-    T = ALPHA / r * Ur
+    T = alpha / r * Ur
     within(Y, T @ Br.T, term_tol(T @ Br.T, T, Br.T, r), "Y")
 
 
@@ -133,3 +133,28 @@ def test_u_saved_or_not_gives_the_same():
         for fwd, w in ((ops.linear_fwd, ops.quantize(W)), (ops.i8_linear_fwd, ops.i8_quantize(W))):
             Y, U = fwd(w, X, A, B, ALPHA, save_u=True, drop=drop)
             assert torch.equal(fwd(w, X, A, B, ALPHA, drop=drop), Y)
+
+
+@pytest.mark.parametrize("M,N,K,r", [(5, 264, 512, 16), (300, 1032, 1088, 64), (1100, 520, 576, 24)])
+def test_alpha_of_zero_and_below(M, N, K, r):
+    rng = np.random.default_rng(M)
+    W = torch.from_numpy(rng.standard_normal((N, K)) * 0.02).to(torch.bfloat16).cuda()
+    X, dY = ints(rng, (M, K))[0], ints(rng, (M, N))[0]
+    A, B = ints(rng, (r, K))[0], ints(rng, (N, r))[0]
+    w = ops.i8_quantize(W)
+    drop = ops.Dropout(0.2, 3, 4)
+    assert torch.equal(ops.i8_linear_fwd(w, X, A, B, 0.0, drop=drop), ops.i8_linear_fwd(w, X))
+    none = ops.i8_linear_bwd(w, None, dY)[0]
+    U = torch.ones((M, r), dtype=torch.bfloat16, device="cuda")
+    dX, dA, dB = ops.i8_linear_bwd(w, X, dY, A, B, 0.0, U=U, drop=drop)
+    assert torch.equal(dX, none) and bool((dA == 0).all()) and bool((dB == 0).all())
+    # -alpha: the gradients with the other sign (each sum off by 3 M products' 2^-23 at most: a matrix instruction's
+    # rounding need not be the same for a sum and its negative), and the forward's term
+    plus, minus = (ops.i8_linear_bwd(w, X, dY, A, B, a, U=U, drop=drop) for a in (ALPHA, -ALPHA))
+    G = ALPHA / r * (dY.double().abs() @ B.double().abs())
+    assert bool(((plus[1] + minus[1]).abs() <= 2 * 3 * M * 2.0**-23 * (G.T @ X.double().abs()) * 1.3).all())
+    dB = ALPHA / r * (dY.double().abs().T @ U.double())
+    assert bool(((plus[2] + minus[2]).abs() <= 2 * M * 2.0**-23 * dB).all())
+    zero, q = ops.i8_quantize(torch.zeros_like(W)), ops.quantize(torch.zeros_like(W))
+    for fwd, z in ((ops.i8_linear_fwd, zero), (ops.linear_fwd, q)):
+        check_forward(lambda X, A, B, drop: fwd(z, X, A, B, -ALPHA, save_u=True, drop=drop), rng, M, N, K, r, 0.25, -ALPHA)

@@ -77,3 +77,37 @@ def test_same_bits_as_the_unsplit_product(name):
         X[2, 5] = float("inf")
     Y, want = ops.i8_linear_fwd(w, X), ops.i8_matmul(ops.i8_quantize(X), w)
     assert np.array_equal(torch_to_f64(Y), torch_to_f64(want), equal_nan=True)
+
+
+def test_split_products_captured_and_on_two_streams():
+    """Replays of a captured split product with eager calls between them, and two at once."""
+    rng = np.random.default_rng(5)
+    cases = []
+    for M, N, K, r in ((40, 840, 19840, 16), (65, 9280, 5760, 64), (195, 8512, 9088, 128)):
+        w = ops.i8_quantize(torch.randn((N, K), device="cuda").mul_(0.02).to(torch.bfloat16))
+        X, A, B = (to_gpu(rng.standard_normal(s)) for s in ((M, K), (r, K), (N, r)))
+        cases.append((w, X, A, B))
+    call = lambda c, **kw: ops.i8_linear_fwd(*c, 16.0, **kw)
+    want = [call(c) for c in cases]
+    torch.cuda.synchronize()
+    stream, other = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [torch.empty_like(y) for y in want]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        for c, o in zip(cases, outs):
+            call(c, out=o)
+    for _ in range(4):
+        for o in outs:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for c, o, y in zip(cases, outs, want):
+            assert torch.equal(o, y) and torch.equal(call(c), y)
+    for _ in range(4):
+        with torch.cuda.stream(stream):
+            a = [call(c) for c in cases]
+        with torch.cuda.stream(other):
+            b = [call(c) for c in reversed(cases)]
+        torch.cuda.synchronize()
+        for y, s, t in zip(want, a, reversed(b)):
+            assert torch.equal(s, y) and torch.equal(t, y)
