@@ -37,10 +37,11 @@ enum TailForm : int { kTailScaled = 0, kTailParts = 1, kTailPartsDrop = 2 };
 // products of four 32 x 32 blocks at a time are summed in registers of their
 // own, masked by their bits (block 4 i + j of the wave at bits + 1 KiB (4 i +
 // j)), and added: the tile keeps one set of accumulators.
-// Masked dX of 4096 x 22016 x 8192 at rank 64 1.2 PFLOP/s; 2048 x 4096 x 4096
-// 69 us (one round of 256 x 128 tiles, 1.0 PFLOP/s).  With a block at a time,
+// Masked dX of 4096 x 22016 x 8192 at rank 64 1.3 PFLOP/s; 2048 x 4096 x 4096
+// 68 us (one round of 256 x 128 tiles, 1.0 PFLOP/s).  With a block at a time,
 // its mask computed here, the whole backward of 3918 x 20856 x 800 at rank 128
-// took 438 us, 383 this way.
+// took 438 us, 383 this way (both with T in one part; the second adds 10 us
+// there, 1.6 to the 68 and 7 to the 1140 of the others).
 template <int FI>
 __device__ __forceinline__ void masked_tail(f32x16_t (&acc)[FI][4], const char* smem, int nt, const char* bits) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1;

@@ -15,7 +15,7 @@
 // the 32x32x16 bf16 one.  After the loop the sums become fp32 in the
 // registers that held them.  Bound by the lines a CU keeps in flight and by
 // power: 4096 x 22016 x 8192 at rank 64 runs at 2.2 POPS (five whole rounds of
-// 256 x 256 tiles 600 us and 1536 channels on 256 x 128 77 us); random operands
+// 256 x 256 tiles 590 us and 1536 channels on 256 x 128 79 us); random operands
 // in registers alone reach 3.4, the library's product of 16384^3 2.4.
 #include <algorithm>
 #include <cmath>
@@ -350,7 +350,7 @@ hipError_t launch_i8_sum(const I8Gemm& g, int splits, const int32_t* part, hipSt
 // bytes of 16 rows, the next one the other half of the same lines.  The
 // tokens come from L2 in the same layout.  Loads run one batch of UP lines
 // ahead of the products.  One token at 8192 x 8192: 13.8 us, 4.9 TB/s of
-// weight; 16 at 22016 x 8192: 41 us, 4.4 TB/s.
+// weight; 16 at 8192 x 8192: 17.3 us, 3.9 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kSkWaves = 8;
 

@@ -1,9 +1,9 @@
 // ride.h -- the last step of a small adapter product (U = drop(X) A^T, G = dY
-// B), and copies of rows padded to whole stages, as extra workgroups of the launch that comes next anyway, a
-// dequantization or a quantization, which neither reads the product nor is
-// read by it.  Alone such a step is a launch of 3-5 us that leaves most of the
-// card idle: the backward of 2048 x 4096 x 4096 at rank 64 takes 107 us with it
-// apart and 104 this way, the 8-bit forward 57 and 54, the NF4 forward of 256 x
+// B), and copies of rows padded to whole stages, as extra workgroups of the
+// launch that comes next anyway, a dequantization or a quantization, which
+// neither reads the product nor is read by it.  Alone such a step is a launch of
+// 3-5 us that leaves most of the card idle: the backward of 2048 x 4096 x 4096 at
+// rank 64 took 107 us with it apart and 104 this way, the NF4 forward of 256 x
 // 1024 x 1024 at rank 8 24.9 and 21.1.
 #pragma once
 #include "urows.h"

@@ -2,8 +2,9 @@
 // sums: a workgroup takes one rank row and up to four tokens and forms their
 // fp32 dot products, each thread over every 256th group of eight columns.  A
 // is read once per four tokens and X r times (from L2), so it pays while M K r
-// is small; past that the MFMA product with split partials does (gemm.hip),
-// which is two launches.  Four tokens: with 16 a workgroup brings 256 KiB at K
+// is small; past that the MFMA product with split partials does (gemm.hip), a
+// launch more, the partials' sum riding with the next one (ride.h) as this does.
+// Four tokens: with 16 a workgroup brings 256 KiB at K
 // = 8192 (16 tokens at rank 64 with their quantization and product: 15.8 us
 // with four, 19.1 with eight, 26 with 16, 22.6 by MFMA).
 #pragma once
