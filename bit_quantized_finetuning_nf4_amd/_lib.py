@@ -15,6 +15,7 @@ QLORA_OP_FWD, QLORA_OP_BWD, QLORA_OP_GEMV, QLORA_OP_LORA = 0, 1, 2, 3
 QLORA_OP_FWD_FUSED, QLORA_OP_BWD_FUSED = 4, 5
 QLORA_OP_GROUP_FWD, QLORA_OP_GROUP_BWD, QLORA_OP_GROUP_LORA, QLORA_OP_BF16_DX = 6, 7, 8, 9
 QLORA_OP_BWD_DROP, QLORA_OP_I8_FWD, QLORA_OP_I8_BWD, QLORA_OP_FWD_DROP = 10, 11, 12, 13
+QLORA_OP_GATED_FWD, QLORA_OP_GATED_BWD, QLORA_OP_MANY_FWD, QLORA_OP_GATED_MANY_FWD = 14, 15, 16, 17
 
 STATUS_NAMES = {
     0: "QLORA_OK", 1: "QLORA_E_NULL", 2: "QLORA_E_ALIGN", 3: "QLORA_E_SHAPE",
@@ -39,6 +40,7 @@ EXPORTS = [
     "qlora_dropout", "qlora_linear_fwd_drop", "qlora_linear_bwd_drop",
     "qlora_i8_row_bytes", "qlora_i8_quantize", "qlora_i8_dequant", "qlora_i8_matmul",
     "qlora_i8_linear_fwd", "qlora_i8_linear_bwd",
+    "qlora_gated_fwd", "qlora_gated_bwd", "qlora_many_fwd", "qlora_gated_many_fwd",
 ]
 QLORA_PAGED_LOAD, QLORA_PAGED_STORE = 1, 2
 
@@ -115,6 +117,20 @@ class I8RowsDesc(ctypes.Structure):
         ("cols", ctypes.c_int64),
         ("codes", ctypes.c_void_p),
         ("scale", ctypes.c_void_p),
+    ]
+
+
+class AdapterPoolDesc(ctypes.Structure):
+    """qlora_adapter_pool."""
+    _fields_ = [
+        ("slots", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("rank", ctypes.c_int32),
+        ("A", ctypes.c_void_p),
+        ("B", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("ranks", ctypes.c_void_p),
     ]
 
 
@@ -240,6 +256,15 @@ def lib():
     L.qlora_i8_linear_fwd.argtypes = [Q, vp, i64, vp, vp, i32, f32, D, vp, vp, vp, sz, vp]
     L.qlora_i8_linear_bwd.restype = ctypes.c_int
     L.qlora_i8_linear_bwd.argtypes = [Q, vp, vp, i64, vp, vp, i32, f32, vp, D, vp, vp, vp, vp, sz, vp]
+    P = ctypes.POINTER(AdapterPoolDesc)
+    L.qlora_gated_fwd.restype = ctypes.c_int
+    L.qlora_gated_fwd.argtypes = [Wg, vp, i64, vp, vp, i32, f32, i32, vp, vp, vp, vp, sz, vp]
+    L.qlora_gated_bwd.restype = ctypes.c_int
+    L.qlora_gated_bwd.argtypes = [Wg, vp, vp, vp, i64, vp, vp, i32, f32, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.qlora_many_fwd.restype = ctypes.c_int
+    L.qlora_many_fwd.argtypes = [W, vp, i64, P, vp, vp, vp, sz, vp]
+    L.qlora_gated_many_fwd.restype = ctypes.c_int
+    L.qlora_gated_many_fwd.argtypes = [Wg, vp, i64, P, vp, i32, vp, vp, sz, vp]
     _lib = L
     return L
 

@@ -25,6 +25,12 @@
 //                 X A^T, then of the product
 //   FWD_DROP    : s U as above | split partials of U, then of the staged
 //                 product | deq(W) bf16 [N x K], if staged
+//   GATED_FWD, MANY_FWD, GATED_MANY_FWD : scale A x fp32 [M x G R] | deq(W_g)
+//                 stacked [G N x K] | the frozen product's fp32 parts
+//   GATED_BWD   : s G as three bf16 parts [M x 2 r] each | U bf16 [M x 2 r] |
+//                 split partials | [dG | dP] bf16 [M x 2 Fp] (Fp = F rounded up
+//                 to 32, zero columns) | deq(W_g)^T side by side [K x 2 Fp] |
+//                 the dense product's split partials, if it splits
 // qlora_linear_fwd_noalloc carves the FWD layout out of `scratch` below
 // instead of a caller workspace.
 #include <hip/hip_runtime.h>
@@ -358,6 +364,58 @@ BwdLayout group_bwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, int32_t G
   return L;
 }
 
+// A gated block and the adapters of many requests: G weights N x K (1, or gate
+// and up) side by side, adapters of rank R for each (0: none).
+struct PoolLayout {
+  size_t t, wd, part, total;
+};
+PoolLayout pool_layout(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
+  PoolLayout L{};
+  L.wd = align_up((size_t)M * (size_t)(G * R) * sizeof(float));
+  L.part = L.wd + align_up((size_t)G * (size_t)N * (size_t)K * 2);
+  L.total = L.part + align_up(product_part_bytes(G * N, K, M));
+  return L;
+}
+// 32-bit byte offsets of the stack, X and the results, and (2^27) the thread
+// count of the pass that forms scale A x.
+bool pool_sizes_ok(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
+  if (M <= 0 || N <= 0 || K <= 0 || G < 1 || R < 0 || R > kMaxRank) return false;
+  if (N > (int64_t)0x7FFFFFFF / G / K || M > (int64_t)0x7FFFFFFF / K || M > (int64_t)0x7FFFFFFF / G / N) return false;
+  return R == 0 || M <= ((int64_t)1 << 27) / (G * R);
+}
+qlora_status check_pool_sizes(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
+  if (M <= 0 || M > 0x7FFFFFFF) return QLORA_E_SHAPE;
+  return pool_sizes_ok(M, N, K, R, G) ? QLORA_OK : QLORA_E_UNSUPPORTED;
+}
+
+struct GatedBwdLayout {
+  size_t g, u, part, dy, wdt, split, split_bytes, total;
+};
+int64_t up32(int64_t n) { return (n + 31) / 32 * 32; }
+GatedBwdLayout gated_bwd_layout(int64_t M, int64_t F, int64_t K, int32_t r, bool with_dx) {
+  GatedBwdLayout L{};
+  const int64_t fp = up32(F);
+  if (r > 0) {
+    L.u = align_up((size_t)M * 2 * r * 2 * kGradParts);
+    L.part = L.u + align_up((size_t)M * 2 * r * 2);
+    L.dy = L.part + align_up(std::max(std::max(skinny_partial_bytes(M, 2 * r, K, kXAt), group_dyb_part_bytes(M, F, r, 2)),
+                                      group_grads_part_bytes(M, F, K, r, 2)));
+  }
+  if (r > 0 || with_dx) L.total = L.wdt = L.dy + align_up((size_t)M * (size_t)(2 * fp) * 2);
+  if (with_dx) {
+    L.split = L.wdt + align_up((size_t)(2 * fp) * (size_t)K * 2);
+    L.split_bytes = staged_part_bytes(K, 2 * fp, M);
+    L.total = L.split + align_up(L.split_bytes);
+  }
+  return L;
+}
+bool gated_bwd_ok(int64_t M, int64_t F, int64_t K, int32_t r) {
+  if (M <= 0 || F <= 0 || K <= 0 || r < 0 || r > kMaxRank || F > 0x3FFFFFF) return false;
+  const int64_t n = 2 * up32(F);
+  if (n > (int64_t)0x7FFFFFFF / K || n > (int64_t)0x7FFFFFFF / M || M > (int64_t)0x7FFFFFFF / K || n / 64 > 65535) return false;
+  return r == 0 || (skinny_cols_ok(K) && skinny_cols_ok(n) && std::max(M, std::max(n, K)) <= (int64_t)0x7FFFFFFF / (2 * r));
+}
+
 qlora_status check_ws(void* ws, size_t ws_bytes, size_t need) {
   if (ws_bytes < need) return QLORA_E_WORKSPACE;
   if (need > 0 && !ws) return QLORA_E_NULL;
@@ -549,6 +607,14 @@ size_t qlora_workspace_bytes(qlora_op op, int64_t M, int64_t N, int64_t K, int32
           r > kMaxRank)
         return 0;
       return i8_fwd_layout(M, N, K, r).total;
+    case QLORA_OP_GATED_FWD:
+    case QLORA_OP_GATED_MANY_FWD:
+    case QLORA_OP_MANY_FWD: {
+      const int32_t G = op == QLORA_OP_MANY_FWD ? 1 : 2;
+      return K > 0 && K % 64 == 0 && pool_sizes_ok(M, N, K, r, G) ? pool_layout(M, N, K, r, G).total : 0;
+    }
+    case QLORA_OP_GATED_BWD:
+      return gated_bwd_ok(M, N, K, r) && K % 64 == 0 ? gated_bwd_layout(M, N, K, r, true).total : 0;
   }
   return 0;
 }
@@ -1118,6 +1184,139 @@ qlora_status qlora_group_bwd(const qlora_nf4_weight* W, int32_t G, const uint16_
       return st;
   }
   return group_grads(X, dY, U, Gm, M, N, K, r, G, alpha, dA, dB, part, s);
+}
+
+namespace {
+
+// Y = [act of] the G weights' products with the pool's term, on validated
+// arguments.
+qlora_status run_pool(const qlora_nf4_weight* W, const PoolView& p, const uint16_t* X, int64_t M, int act, uint16_t* Y,
+                      uint16_t* GU, uint16_t* U, void* ws, hipStream_t s) {
+  const int64_t N = W[0].rows, K = W[0].cols;
+  const PoolLayout L = pool_layout(M, N, K, p.R, p.G);
+  float* T = reinterpret_cast<float*>(ws_at(ws, L.t));
+  bf16_t* Wd = reinterpret_cast<bf16_t*>(ws_at(ws, L.wd));
+  float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
+  qlora_status st;
+  if (p.R > 0 && (st = hip_status(launch_pool_down(p, X, M, K, T, U, s))) != QLORA_OK) return st;
+  if ((st = group_dequant(W, p.G, false, Wd, s)) != QLORA_OK) return st;
+  int splits = 1;
+  if ((st = hip_status(launch_product_parts(Wd, p.G * N, K, X, M, part, &splits, s))) != QLORA_OK) return st;
+  return hip_status(launch_pool_finish(p, part, splits, M, N, T, act, Y, GU, s));
+}
+
+bool act_ok(int32_t act) { return act == QLORA_ACT_SILU || act == QLORA_ACT_GELU; }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A pool beside weights of `rows` rows in all and K columns.
+qlora_status check_pool(const qlora_adapter_pool* p, const int32_t* ids, int64_t rows, int64_t K) {
+  if (!p || !ids) return QLORA_E_NULL;
+  if (p->slots <= 0 || p->rows != rows || p->cols != K) return QLORA_E_SHAPE;
+  if (p->slots > QLORA_MAX_SLOTS || p->rank <= 0 || p->rank > kMaxRank || p->rank % 8 != 0) return QLORA_E_UNSUPPORTED;
+  if (!p->A || !p->B || !p->scale) return QLORA_E_NULL;
+  if (!aligned16(p->A) || !aligned16(p->B) || !aligned4(p->scale) || !aligned4(p->ranks) || !aligned4(ids))
+    return QLORA_E_ALIGN;
+  return QLORA_OK;
+}
+PoolView pool_view(const qlora_adapter_pool* p, const int32_t* ids, int G) {
+  return PoolView{p->A, p->B, p->scale, p->ranks, ids, 0.0f, (int)p->slots, p->rank, G};
+}
+
+qlora_status pool_fwd(const qlora_nf4_weight* W, int32_t G, const uint16_t* X, int64_t M, const qlora_adapter_pool* pool,
+                      const int32_t* ids, int32_t act, uint16_t* Y, void* ws, size_t ws_bytes, void* stream) {
+  qlora_status st = check_group_weights(W, G);
+  if (st != QLORA_OK) return st;
+  const int64_t N = W[0].rows, K = W[0].cols;
+  if ((st = check_pool(pool, ids, G * N, K)) != QLORA_OK) return st;
+  if ((st = check_pool_sizes(M, N, K, pool->rank, G)) != QLORA_OK) return st;
+  if (!X || !Y) return QLORA_E_NULL;
+  if (!aligned16(X) || !aligned16(Y)) return QLORA_E_ALIGN;
+  if (!act_ok(act)) return QLORA_E_UNSUPPORTED;
+  if ((st = check_ws(ws, ws_bytes, pool_layout(M, N, K, pool->rank, G).total)) != QLORA_OK) return st;
+  return run_pool(W, pool_view(pool, ids, G), X, M, act, Y, nullptr, nullptr, ws, (hipStream_t)stream);
+}
+
+}  // namespace
+
+qlora_status qlora_many_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, const qlora_adapter_pool* pool,
+                            const int32_t* ids, uint16_t* Y, void* ws, size_t ws_bytes, void* stream) {
+  return pool_fwd(W, 1, X, M, pool, ids, QLORA_ACT_SILU, Y, ws, ws_bytes, stream);
+}
+
+qlora_status qlora_gated_many_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M,
+                                  const qlora_adapter_pool* pool, const int32_t* ids, int32_t act, uint16_t* H, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  return pool_fwd(W, 2, X, M, pool, ids, act, H, ws, ws_bytes, stream);
+}
+
+qlora_status qlora_gated_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, const uint16_t* A,
+                             const uint16_t* B, int32_t r, float alpha, int32_t act, uint16_t* H, uint16_t* GU_save,
+                             uint16_t* U_save, void* ws, size_t ws_bytes, void* stream) {
+  qlora_status st = check_group_weights(W, 2);
+  if (st != QLORA_OK) return st;
+  if ((st = check_rank(r, A, B)) != QLORA_OK) return st;
+  const int64_t N = W[0].rows, K = W[0].cols;
+  if ((st = check_pool_sizes(M, N, K, r, 2)) != QLORA_OK) return st;
+  if (!X || !H) return QLORA_E_NULL;
+  if (!aligned16(X) || !aligned16(H) || !aligned16(GU_save) || !aligned16(U_save)) return QLORA_E_ALIGN;
+  if (!act_ok(act)) return QLORA_E_UNSUPPORTED;
+  if ((st = check_ws(ws, ws_bytes, pool_layout(M, N, K, r, 2).total)) != QLORA_OK) return st;
+  const PoolView p{A, B, nullptr, nullptr, nullptr, lora_s(alpha, r), 1, r, 2};
+  return run_pool(W, p, X, M, act, H, GU_save, r > 0 ? U_save : nullptr, ws, (hipStream_t)stream);
+}
+
+qlora_status qlora_gated_bwd(const qlora_nf4_weight* W, const uint16_t* X, const uint16_t* dH, const uint16_t* GU,
+                             int64_t M, const uint16_t* A, const uint16_t* B, int32_t r, float alpha, int32_t act,
+                             const uint16_t* U_saved, uint16_t* dX, float* dA, float* dB, void* ws, size_t ws_bytes,
+                             void* stream) {
+  qlora_status st = check_group_weights(W, 2);
+  if (st != QLORA_OK) return st;
+  if ((st = check_rank(r, A, B)) != QLORA_OK) return st;
+  const int64_t F = W[0].rows, K = W[0].cols, fp = up32(F);
+  if (M <= 0 || M > 0x7FFFFFFF) return QLORA_E_SHAPE;
+  if (!gated_bwd_ok(M, F, K, r) || !act_ok(act)) return QLORA_E_UNSUPPORTED;
+  if (!dH || !GU) return QLORA_E_NULL;
+  if (!aligned16(dH) || !aligned16(GU) || !aligned16(dX) || !aligned16(U_saved)) return QLORA_E_ALIGN;
+  if (r > 0) {
+    if (!dA || !dB || !X) return QLORA_E_NULL;
+    if (!aligned16(dA) || !aligned16(dB) || !aligned16(X)) return QLORA_E_ALIGN;
+  } else if (dA || dB) {
+    return QLORA_E_SHAPE;   // no adapter, no adapter gradients
+  }
+  const GatedBwdLayout L = gated_bwd_layout(M, F, K, r, dX != nullptr);
+  if ((st = check_ws(ws, ws_bytes, L.total)) != QLORA_OK) return st;
+  if (r == 0 && !dX) return QLORA_OK;
+  hipStream_t s = (hipStream_t)stream;
+  bf16_t* G3 = reinterpret_cast<bf16_t*>(ws_at(ws, L.g));
+  float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
+  bf16_t* dY = reinterpret_cast<bf16_t*>(ws_at(ws, L.dy));
+  bf16_t* WdT = dX ? reinterpret_cast<bf16_t*>(ws_at(ws, L.wdt)) : nullptr;
+  const float sc = lora_s(alpha, r);
+  const bf16_t* U = U_saved;
+  if (r > 0 && !U) {
+    bf16_t* Ud = reinterpret_cast<bf16_t*>(ws_at(ws, L.u));
+    if ((st = hip_status(launch_xat(X, A, M, K, 2 * r, part, Ud, nullptr, 1.0f, s))) != QLORA_OK) return st;
+    U = Ud;
+  }
+  if ((st = hip_status(launch_gated_grad(dH, GU, M, F, fp, act, dY, WdT, K, s))) != QLORA_OK) return st;
+  if (r > 0) {
+    Ride rest;
+    if ((st = hip_status(start_dyb_parts_group(dY, 2 * fp, B, M, F, r, 2, part, G3, sc, &rest, s))) != QLORA_OK) return st;
+    if ((st = hip_status(launch_ride(rest, s))) != QLORA_OK) return st;
+  }
+  if (dX) {
+    for (int g = 0; g < 2; ++g)
+      if ((st = hip_status(launch_dequant_t(W[g].codes, W[g].absmax_q, W[g].group_scale, F, K, W[g].codebook,
+                                            W[g].absmax_format, WdT + g * fp, 2 * fp, s))) != QLORA_OK)
+        return st;
+    if ((st = hip_status(launch_staged(WdT, K, 2 * fp, dY, M, r > 0 ? G3 : nullptr, r > 0 ? A : nullptr, true, 2 * r,
+                                       nullptr, dX, s, reinterpret_cast<float*>(ws_at(ws, L.split)), L.split_bytes))) !=
+        QLORA_OK)
+      return st;
+  }
+  if (r == 0) return QLORA_OK;
+  return hip_status(launch_adapter_grads_group(G3, X, dY, 2 * fp, fp, U, M, F, K, r, 2, part, dA, dB, sc, s));
 }
 
 qlora_status qlora_group_dequant(const qlora_nf4_weight* W, int32_t G, uint16_t* Wd_out, void* stream) {

@@ -535,6 +535,32 @@ __global__ __launch_bounds__(kThreads, 1) void adapter_grads_kernel(GradArgs p) 
                                 p.tiles_b, p.part_b, 0, p.drop, p.scale_b);
 }
 
+// The same of G stacked adapters: dA [G r x K] as one product of rank G r where
+// that is at most RPA, else as G of rank r (ga of ra ranks), dB per adapter.
+struct GroupGradArgs {
+  const bf16_t *X, *dY, *G3, *U;
+  int64_t M, N, K, ldy, dy_gs;
+  int r, G, ga, ra, sps_a, tiles_a, blocks_a, sps_b, tiles_b, blocks_b;   // blocks: of one of ga (G) products
+  float *part_a, *part_b;
+  float scale_b;
+};
+template <int RPA, int RPB>
+__global__ __launch_bounds__(kThreads, 1) void group_grads_kernel(GroupGradArgs p) {
+  extern __shared__ __align__(16) char smem[];
+  const int ld = p.G * p.r;
+  int id = blockIdx.x;
+  if (id < p.ga * p.blocks_a) {
+    const int g = id / p.blocks_a;
+    cskinny<RPA, false, 3, false>(id - g * p.blocks_a, g, p.ga, smem, p.X, p.M, p.K, p.K, 0, p.G3, p.ra, ld, p.ra,
+                                  p.sps_a, p.tiles_a, p.part_a, p.M * ld, DropArgs{}, 1.0f);
+  } else {
+    id -= p.ga * p.blocks_a;
+    const int g = id / p.blocks_b;
+    cskinny<RPB, true, 1, false>(id - g * p.blocks_b, g, p.G, smem, p.dY, p.M, p.N, p.ldy, p.dy_gs, p.U, p.r, ld, p.r,
+                                 p.sps_b, p.tiles_b, p.part_b, 0, DropArgs{}, p.scale_b);
+  }
+}
+
 __global__ __launch_bounds__(kThreads) void reduce_kernel(const float* __restrict__ part, int splits, int64_t n,
                                                           float scale, float* __restrict__ out_f32,
                                                           bf16_t* __restrict__ out_bf16,
@@ -624,7 +650,7 @@ struct RowArgs {
 };
 
 template <int RP, bool QT>
-hipError_t run_rows(const RowArgs& a, float* part, float scale, bf16_t* out, bf16_t* out2, hipStream_t st) {
+hipError_t row_partials(const RowArgs& a, float* part, hipStream_t st) {
   const Split sp = split_for((a.M + 127) / 128, a.C, 256);
   auto* fn = &rskinny_kernel<RP, QT>;
   const size_t lds = (size_t)kRing * RowShape<RP, QT>::kStage;
@@ -632,8 +658,13 @@ hipError_t run_rows(const RowArgs& a, float* part, float scale, bf16_t* out, bf1
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits, a.G), dim3(kThreads), lds, st, a.P, a.M, a.C, a.ldp, a.p_gs, a.Q,
                      a.r, a.q_gs, sp.sps, sp.tiles, a.ldo, part);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  return reduce(part, sp.splits, a.M * a.ldo, scale, nullptr, out, out2, st);
+  return hipGetLastError();
+}
+template <int RP, bool QT>
+hipError_t run_rows(const RowArgs& a, float* part, float scale, bf16_t* out, bf16_t* out2, hipStream_t st) {
+  const hipError_t e = row_partials<RP, QT>(a, part, st);
+  if (e != hipSuccess) return e;
+  return reduce(part, split_for((a.M + 127) / 128, a.C, 256).splits, a.M * a.ldo, scale, nullptr, out, out2, st);
 }
 
 // Token contraction over G groups (grid y): group g reads Big + g big_gs
@@ -809,6 +840,17 @@ hipError_t start_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t
                  : wide_partials<128, true, false>(dY, M, N, B, r, DropArgs{}, sp, part, st);
 }
 
+size_t group_dyb_part_bytes(int64_t M, int64_t N, int r, int G) {
+  return part_bytes(split_for((M + 127) / 128, N, 256), M * G * r);
+}
+
+hipError_t start_dyb_parts_group(const bf16_t* dY, int64_t ldy, const bf16_t* B, int64_t M, int64_t N, int r, int G,
+                                 float* part, bf16_t* parts, float s, Ride* rest, hipStream_t st) {
+  const RowArgs a{dY, M, N, ldy, ldy / G, B, r, N * r, G, G * r};
+  *rest = sum_ride(kRideSum3, part, split_for((M + 127) / 128, N, 256), M * G * r, 1.0f, nullptr, parts, s);
+  return r <= 64 ? row_partials<64, true>(a, part, st) : row_partials<128, true>(a, part, st);
+}
+
 hipError_t launch_ride(const Ride& a, hipStream_t st) {
   auto* fn = a.kind == kRideRows       ? &ride_kernel<kRideRows>
              : a.kind == kRideRowsDrop ? &ride_kernel<kRideRowsDrop>
@@ -846,6 +888,54 @@ hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t*
   if (ra + rb == 0) return hipGetLastError();
   hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(((ra + rb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
                      part, sa.splits, ra, dA, part_b, sb.splits, rb, dB, 1.0f, scale);
+  return hipGetLastError();
+}
+
+// Splits of G products of C columns each.
+namespace {
+Split group_cols_split(int G, int64_t C, int64_t M) {
+  Split s = fill_split(G * ((C + 127) / 128), M, 32, 4, 512);
+  s.tiles /= G;
+  return s;
+}
+struct GroupGrads {
+  int ga, ra;
+  Split a, b;
+  int64_t na, nb;
+};
+GroupGrads group_grads_of(int64_t M, int64_t N, int64_t K, int r, int G) {
+  GroupGrads g{};
+  g.ga = G * r <= 128 ? 1 : G, g.ra = G * r / g.ga;
+  g.a = group_cols_split(g.ga, K, M), g.b = group_cols_split(G, N, M);
+  g.na = (int64_t)G * r * K, g.nb = (int64_t)G * N * r;
+  return g;
+}
+}  // namespace
+
+size_t group_grads_part_bytes(int64_t M, int64_t N, int64_t K, int r, int G) {
+  const GroupGrads g = group_grads_of(M, N, K, r, G);
+  return (part_bytes(g.a, g.na) + 255) / 256 * 256 + part_bytes(g.b, g.nb);
+}
+
+hipError_t launch_adapter_grads_group(const bf16_t* G3, const bf16_t* X, const bf16_t* dY, int64_t ldy, int64_t dy_gs,
+                                      const bf16_t* U, int64_t M, int64_t N, int64_t K, int r, int G, float* part,
+                                      float* dA, float* dB, float scale, hipStream_t st) {
+  const GroupGrads g = group_grads_of(M, N, K, r, G);
+  float* part_b = part + (part_bytes(g.a, g.na) + 255) / 256 * 256 / sizeof(float);
+  const bool whole_a = g.a.splits == 1, whole_b = g.b.splits == 1;
+  const GroupGradArgs p{X, dY, G3, U, M, N, K, ldy, dy_gs, r, G, g.ga, g.ra, g.a.sps, g.a.tiles, g.a.tiles * g.a.splits,
+                        g.b.sps, g.b.tiles, g.b.tiles * g.b.splits, whole_a ? dA : part, whole_b ? dB : part_b,
+                        whole_b ? scale : 1.0f};
+  auto* fn = g.ra <= 64 ? (r <= 64 ? &group_grads_kernel<64, 64> : &group_grads_kernel<64, 128>)
+                        : (r <= 64 ? &group_grads_kernel<128, 64> : &group_grads_kernel<128, 128>);
+  const int lds = g.ra <= 64 && r <= 64 ? grads_lds<64>() : std::max(grads_lds<64>(), grads_lds<128>());
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(fn, dim3(p.ga * p.blocks_a + G * p.blocks_b), dim3(kThreads), lds, st, p);
+  const int64_t ra = whole_a ? 0 : g.na, rb = whole_b ? 0 : g.nb;
+  if (ra + rb == 0) return hipGetLastError();
+  hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(((ra + rb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
+                     part, g.a.splits, ra, dA, part_b, g.b.splits, rb, dB, 1.0f, scale);
   return hipGetLastError();
 }
 

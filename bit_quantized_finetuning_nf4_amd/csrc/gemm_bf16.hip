@@ -523,6 +523,25 @@ size_t staged_part_bytes(int64_t N, int64_t K, int64_t M) {
 
 double staged_cost(int64_t N, int64_t K, int64_t M) { return choose_tile(M, N, K / 64, kSplitCus, (size_t)1 << 62).cost; }
 
+// Of the tiles below 256 tokens, on a card of kSplitCus CUs: the parts' number
+// has to be the one that the caller sized its workspace for.
+namespace {
+TileChoice parts_tile(int64_t N, int64_t K, int64_t M) {
+  return choose_tile(M, N, K / 64, kSplitCus, (size_t)1 << 62, true);
+}
+}  // namespace
+size_t product_part_bytes(int64_t N, int64_t K, int64_t M) {
+  return (size_t)parts_tile(N, K, M).splits * (size_t)M * (size_t)N * sizeof(float);
+}
+hipError_t launch_product_parts(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, float* part,
+                                int* splits, hipStream_t st) {
+  const TileChoice c = parts_tile(N, K, M);
+  TileGemm t{};
+  t.W = Wd, t.X = X, t.N = N, t.row_bytes = 2 * K, t.M = M, t.part = part, t.keep = true;
+  *splits = c.splits;
+  return launch_tile(t, c, 0, N, st);
+}
+
 hipError_t launch_staged(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* T,
                          const bf16_t* B, bool b_trans, int r, const DropArgs* drop, bf16_t* Y, hipStream_t st,
                          float* part, size_t part_bytes) {

@@ -273,9 +273,9 @@ hipError_t launch(TileGemm g, int splits, int64_t n_begin, int64_t n_rows, hipSt
   TileArgs p{g, n_begin, (int)((n_rows + TN - 1) / TN), (int)((g.M + TM - 1) / TM), 0};
   const int lines = (int)(g.row_bytes / 128);
   p.sps = (lines + splits - 1) / splits;
-  if (splits == 1) p.g.part = nullptr;
+  if (splits == 1 && !g.keep) p.g.part = nullptr;
   hipLaunchKernelGGL(fn, dim3(p.tiles_n * p.tiles_m * splits), dim3(kThreads), lds, st, p);
-  if ((e = hipGetLastError()) != hipSuccess || splits == 1 || std::is_same<MM, MmI8>::value) return e;
+  if ((e = hipGetLastError()) != hipSuccess || splits == 1 || g.keep || std::is_same<MM, MmI8>::value) return e;
   return launch_split_sum(static_cast<const float*>(g.part), splits, g.M * g.N, g.Y, st);
 }
 
@@ -322,9 +322,10 @@ double full_round_cost(int64_t lines) { return round_cost(kShapes[6], lines); }
 // Rings of two stages lose (151 us against 115 with four, 128 x 128 at 512 x
 // 8192 x 22016); past three or four nothing changes.  A split adds a launch and
 // its parts' way through memory (mostly the last-level cache).
-TileChoice choose_tile(int64_t M, int64_t N, int64_t lines, int cus, size_t part_bytes) {
+TileChoice choose_tile(int64_t M, int64_t N, int64_t lines, int cus, size_t part_bytes, bool small) {
   TileChoice best{0, 0, 1, 1e30};
   for (const Shape& t : kShapes) {
+    if (small && t.tm == 256) break;
     const int64_t tiles = (M + t.tm - 1) / t.tm * ((N + t.tn - 1) / t.tn);
     for (int want = 1; want <= (t.tm == 256 && t.tn != 256 ? 1 : kMaxSplits); ++want) {
       if (want > 1 && (int64_t)want * kMinLines > lines) break;

@@ -186,9 +186,49 @@ hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t*
 // T.  K % 64 == 0; part as for launch_bf16_fwd, staged_part_bytes are enough.
 size_t staged_part_bytes(int64_t N, int64_t K, int64_t M);
 double staged_cost(int64_t N, int64_t K, int64_t M);   // us, estimated
+// X Wd^T alone as *splits fp32 parts [M x N].  product_part_bytes are enough.
+size_t product_part_bytes(int64_t N, int64_t K, int64_t M);
+hipError_t launch_product_parts(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, float* part,
+                                int* splits, hipStream_t st);
 hipError_t launch_staged(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* T,
                          const bf16_t* B, bool b_trans, int r, const DropArgs* drop, bf16_t* Y, hipStream_t st,
                          float* part, size_t part_bytes);
+
+// The same of G stacked adapters of rank r (a gated block's two): columns g N ..
+// of dY [M x ldy] and B + g N r give columns g r .. of G's parts [M x G r].
+size_t group_dyb_part_bytes(int64_t M, int64_t N, int r, int G);
+hipError_t start_dyb_parts_group(const bf16_t* dY, int64_t ldy, const bf16_t* B, int64_t M, int64_t N, int r, int G,
+                                 float* part, bf16_t* parts, float s, Ride* rest, hipStream_t st);
+// dA [G r x K] and dB [G N x r] (group g: columns g dy_gs .. of dY, g r .. of U).
+size_t group_grads_part_bytes(int64_t M, int64_t N, int64_t K, int r, int G);
+hipError_t launch_adapter_grads_group(const bf16_t* G3, const bf16_t* X, const bf16_t* dY, int64_t ldy, int64_t dy_gs,
+                                      const bf16_t* U, int64_t M, int64_t N, int64_t K, int r, int G, float* part,
+                                      float* dA, float* dB, float scale, hipStream_t st);
+
+// The adapters of a call: S slots of rank R for each of G weights side by side,
+// A [S x G R x K], B [S x G N x R]; token m takes slot ids[m] (ids null: slot 0),
+// none where that is no slot.  scale null: s; rank null: R for all (pool.h).
+struct PoolView {
+  const bf16_t *A, *B;
+  const float* scale;
+  const int32_t* rank;
+  const int32_t* ids;
+  float s;
+  int slots, R, G;   // R == 0: no adapters
+};
+// T [M x G R] fp32, the ranks past a slot's own left as they were; U (may be
+// null) the same without the scale, in bf16.  (pool.hip)
+hipError_t launch_pool_down(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* T, bf16_t* U,
+                            hipStream_t st);
+// Y [M x N] from `splits` fp32 parts [M x G N] of the frozen products and the
+// adapters' term; G == 2: act(first) second, and the two themselves to GU
+// [M x 2 N] (may be null).
+hipError_t launch_pool_finish(const PoolView& p, const float* part, int splits, int64_t M, int64_t N, const float* T,
+                              int act, bf16_t* Y, bf16_t* GU, hipStream_t st);
+// dY [M x 2 Fp] = [dG | dP] of a gated block (gated.hip), zero from column F of
+// each half on, as Wt [K x 2 Fp] is made (may be null).
+hipError_t launch_gated_grad(const bf16_t* dH, const bf16_t* GU, int64_t M, int64_t F, int64_t Fp, int act, bf16_t* dY,
+                             bf16_t* Wt, int64_t K, hipStream_t st);
 
 // Rows of 8-bit integers with one scale each (i8.hip): bytes from one row to
 // the next, and the passes over them.
@@ -246,13 +286,15 @@ struct TileGemm {
   DropArgs drop;
   bf16_t* Y;
   void* part;
+  bool keep;   // leave the fp32 parts, of one split too, to the caller
 };
 struct TileChoice {
   int tm, tn, splits;   // tm == 256: one of the 256-token kernels
   double cost;          // us, estimated
 };
 double full_round_cost(int64_t lines);   // of 256 x 256 tiles
-TileChoice choose_tile(int64_t M, int64_t N, int64_t lines, int cus, size_t part_bytes);
+// small: of the tiles below 256 tokens.
+TileChoice choose_tile(int64_t M, int64_t N, int64_t lines, int cus, size_t part_bytes, bool small = false);
 size_t tile_part_bytes(int64_t M, int64_t N, int64_t lines);
 hipError_t launch_tile(const TileGemm& g, const TileChoice& c, int64_t n_begin, int64_t n_rows, hipStream_t st);
 // Y [n] bf16 = the sum of the splits' fp32 parts, in order.

@@ -13,7 +13,7 @@ import torch
 
 from . import _lib
 from . import debug as _debug
-from ._lib import DropDesc, I8RowsDesc
+from ._lib import AdapterPoolDesc, DropDesc, I8RowsDesc
 from ._lib import GemvJobDesc, GemvPlanDesc, Nf4WeightDesc, PagedLayoutDesc, PagedTensorDesc, lib
 from ._lib import check as _check_status
 
@@ -620,6 +620,150 @@ def group_bwd(qs: Sequence[QuantizedWeight], X: torch.Tensor, dY: torch.Tensor, 
                                 _stream()),
           "qlora_group_bwd")
     return dX, dA, dB
+
+
+# qlora_act values
+ACTS = {"silu": 0, "gelu": 1}
+
+
+def _act(name):
+    if name not in ACTS:
+        raise ValueError(f"unknown activation {name!r}: one of {sorted(ACTS)}")
+    return ACTS[name]
+
+
+def _pair(qs, like):
+    """(descriptors, F, K) of a block's gate and up weights."""
+    if len(qs) != 2:
+        raise ValueError(f"a gated block has two weights, gate and up, got {len(qs)}")
+    for q in qs:
+        _whole(q, like)
+    return _group_descs(qs), qs[0].rows, qs[0].cols
+
+
+def gated_fwd(qs: Sequence[QuantizedWeight], X: torch.Tensor, A=None, B=None, alpha: float = 0.0, act: str = "silu",
+              save: bool = False, out=None, gu_out=None, u_out=None, ws=None):
+    """H = act(G) * P of a gated block: qs its gate and up weights [F x K], G
+    and P their products with X and the stacked adapters A [2r x K], B [2F x r]
+    (as group_fwd).  act is "silu" or "gelu" (the tanh form).  Returns H
+    [M x F], or with save (H, GU, U) for gated_bwd: GU [M x 2F] = [G | P] and
+    U [M x 2r] (None without adapters), in bf16."""
+    _need(X, torch.bfloat16, "X")
+    _on_current(X.device)
+    descs, F, K = _pair(qs, X)
+    M = X.shape[0]
+    _need(X, torch.bfloat16, "X", (M, K))
+    r = _pair_rank(A, B, F, K, X)
+    H = _out(out, (M, F), torch.bfloat16, X, "out")
+    GU = _out(gu_out, (M, 2 * F), torch.bfloat16, X, "gu_out") if save else None
+    U = _out(u_out, (M, 2 * r), torch.bfloat16, X, "u_out") if save and r else None
+    ws = _ws_for(ws, workspace_bytes(_lib.QLORA_OP_GATED_FWD, M, F, K, r), X)
+    check(lib().qlora_gated_fwd(descs, _ptr(X), M, _ptr(A), _ptr(B), r, float(alpha), _act(act), _ptr(H), _ptr(GU),
+                                _ptr(U), *_ws_args(ws), _stream()), "qlora_gated_fwd")
+    return (H, GU, U) if save else H
+
+
+def _pair_rank(A, B, F, K, like):
+    """The rank of a pair's stacked adapters, checked (0 without)."""
+    if A is None:
+        return 0
+    if A.dim() != 2 or A.shape[0] % 2:
+        raise ValueError(f"A must be the two adapters' stacked, got shape {tuple(A.shape)}")
+    r = A.shape[0] // 2
+    if r:
+        _beside(_need(A, torch.bfloat16, "A", (2 * r, K)), like, "A")
+        _beside(_need(B, torch.bfloat16, "B", (2 * F, r)), like, "B")
+    return r
+
+
+def gated_bwd(qs: Sequence[QuantizedWeight], X, dH: torch.Tensor, GU: torch.Tensor, A=None, B=None, alpha: float = 0.0,
+              act: str = "silu", U: Optional[torch.Tensor] = None, need_dx: bool = True, dX=None, dA=None, dB=None,
+              ws=None):
+    """Backward of gated_fwd from dH [M x F] and its GU (and U; computed again
+    when not given).  Returns (dX [M x K] bf16 or None, dA [2r x K] fp32, dB
+    [2F x r] fp32) (the last two None without adapters)."""
+    _need(dH, torch.bfloat16, "dH")
+    _on_current(dH.device)
+    descs, F, K = _pair(qs, dH)
+    M = dH.shape[0]
+    _need(dH, torch.bfloat16, "dH", (M, F))
+    _beside(_need(GU, torch.bfloat16, "GU", (M, 2 * F)), dH, "GU")
+    r = _pair_rank(A, B, F, K, dH)
+    if r:
+        _beside(_need(X, torch.bfloat16, "X", (M, K)), dH, "X")
+        if U is not None:
+            _beside(_need(U, torch.bfloat16, "U", (M, 2 * r)), dH, "U")
+        dA = _out(dA, (2 * r, K), torch.float32, dH, "dA")
+        dB = _out(dB, (2 * F, r), torch.float32, dH, "dB")
+    else:
+        X = U = dA = dB = None
+    dX = _out(dX, (M, K), torch.bfloat16, dH, "dX") if need_dx else None
+    ws = _ws_for(ws, workspace_bytes(_lib.QLORA_OP_GATED_BWD, M, F, K, r), dH)
+    check(lib().qlora_gated_bwd(descs, _ptr(X), _ptr(dH), _ptr(GU), M, _ptr(A) if r else None, _ptr(B) if r else None, r,
+                                float(alpha), _act(act), _ptr(U), _ptr(dX), _ptr(dA), _ptr(dB), *_ws_args(ws),
+                                _stream()), "qlora_gated_bwd")
+    return dX, dA, dB
+
+
+@dataclass
+class AdapterPool:
+    """The adapters of many requests, in slots of one rank R: A [S, R, K] and B
+    [S, N, R] beside one weight; [S, 2R, K] and [S, 2F, R] beside a gated
+    block's two.  scale [S] is alpha / r of each; rank [S] (int32, optional)
+    the slot's own rank where it is below R, the rest up to a multiple of
+    eight being zeros.  A slot may be filled anew between calls, or between the
+    replays of a captured graph."""
+    A: torch.Tensor
+    B: torch.Tensor
+    scale: torch.Tensor
+    rank: Optional[torch.Tensor] = None
+
+    def desc(self, groups=1) -> AdapterPoolDesc:
+        A, B = self.A, self.B
+        if A.dim() != 3 or B.dim() != 3:
+            raise ValueError(f"a pool's A and B have three dimensions, got {tuple(A.shape)} and {tuple(B.shape)}")
+        S, rows, R = B.shape
+        _need(A, torch.bfloat16, "A", (S, groups * R, A.shape[2]))
+        _beside(_need(B, torch.bfloat16, "B"), A, "B")
+        _beside(_need(self.scale, torch.float32, "scale", (S,)), A, "scale")
+        if self.rank is not None:
+            _beside(_need(self.rank, torch.int32, "rank", (S,)), A, "rank")
+        return AdapterPoolDesc(S, rows, A.shape[2], R, A.data_ptr(), B.data_ptr(), self.scale.data_ptr(),
+                               _ptr(self.rank))
+
+
+def _many(name, op, descs, N, K, groups, X, pool, ids, act, out, ws):
+    M = X.shape[0]
+    _need(X, torch.bfloat16, "X", (M, K))
+    p = pool.desc(groups)
+    _beside(pool.A, X, "pool")
+    _beside(_need(ids, torch.int32, "ids", (M,)), X, "ids")
+    Y = _out(out, (M, N), torch.bfloat16, X, "out")
+    ws = _ws_for(ws, workspace_bytes(op, M, N, K, p.rank), X)
+    check(getattr(lib(), name)(descs, _ptr(X), M, ctypes.byref(p), _ptr(ids), *act, _ptr(Y), *_ws_args(ws), _stream()),
+          name)
+    return Y
+
+
+def many_fwd(q: QuantizedWeight, X: torch.Tensor, pool: AdapterPool, ids: torch.Tensor, out=None, ws=None):
+    """Y [M x N]: token m's product with the weight, and with the adapter in
+    slot ids[m] (int32) of the pool; an id outside the pool is no adapter."""
+    _need(X, torch.bfloat16, "X")
+    _on_current(X.device)
+    _whole(q, X)
+    d = q.desc()
+    return _many("qlora_many_fwd", _lib.QLORA_OP_MANY_FWD, ctypes.byref(d), q.rows, q.cols, 1, X, pool, ids, (), out, ws)
+
+
+def gated_many_fwd(qs: Sequence[QuantizedWeight], X: torch.Tensor, pool: AdapterPool, ids: torch.Tensor,
+                   act: str = "silu", out=None, ws=None):
+    """H [M x F] of a gated block (gated_fwd) with a pool's adapters, as
+    many_fwd."""
+    _need(X, torch.bfloat16, "X")
+    _on_current(X.device)
+    descs, F, K = _pair(qs, X)
+    return _many("qlora_gated_many_fwd", _lib.QLORA_OP_GATED_MANY_FWD, descs, F, K, 2, X, pool, ids, (_act(act),), out,
+                 ws)
 
 
 @dataclass

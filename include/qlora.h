@@ -99,7 +99,12 @@ typedef enum {
   QLORA_OP_BWD_DROP = 10,  /* qlora_linear_bwd_drop                          */
   QLORA_OP_I8_FWD = 11,    /* qlora_i8_linear_fwd                            */
   QLORA_OP_I8_BWD = 12,    /* qlora_i8_linear_bwd                            */
-  QLORA_OP_FWD_DROP = 13   /* qlora_linear_fwd_drop (room for the staged path) */
+  QLORA_OP_FWD_DROP = 13,  /* qlora_linear_fwd_drop (room for the staged path) */
+  QLORA_OP_GATED_FWD = 14, /* qlora_gated_fwd (N = rows of one weight)       */
+  QLORA_OP_GATED_BWD = 15, /* qlora_gated_bwd (N = rows of one weight)       */
+  QLORA_OP_MANY_FWD = 16,  /* qlora_many_fwd (r = the pool's rank)           */
+  QLORA_OP_GATED_MANY_FWD = 17   /* qlora_gated_many_fwd (N = rows of one
+                              weight, r = the pool's rank)                   */
 } qlora_op;
 
 /* A quantized weight: host struct holding device pointers.
@@ -644,6 +649,85 @@ qlora_status qlora_i8_linear_bwd(const qlora_i8_rows* W, const uint16_t* X, cons
                                  const uint16_t* A, const uint16_t* B, int32_t r, float alpha,
                                  const uint16_t* U_saved, const qlora_drop* drop, uint16_t* dX, float* dA, float* dB,
                                  void* ws, size_t ws_bytes, void* stream);
+
+/* ---- The gated feed-forward block ------------------------------------------
+ * The gate and up projections of a feed-forward block read one input and are
+ * joined by an activation (the layer sets' gate and up linears are such a
+ * pair).  W points to their two weights, gate then up, both [F x K]:
+ *   H = act(G) o P,  G = X deq(W_0)^T + s U_0 B_0^T,  P = X deq(W_1)^T +
+ *   s U_1 B_1^T,  [U_0 | U_1] = X A^T,
+ * with the two adapters stacked as for qlora_group_fwd, A [2 r x K] and
+ * B [2 F x r], s = RN32(alpha / r); r == 0 (A = B = NULL): none.  G, P and s U
+ * are not rounded before H, which is rounded once.  Any M >= 1; K % 64 == 0,
+ * F % 8 == 0; 2 F K, M K and 2 M F below 2^31, 2 M r at most 2^27
+ * (QLORA_E_UNSUPPORTED otherwise); QLORA_E_SHAPE where the weights differ in
+ * shape.  The two may have different codebooks. */
+typedef enum {
+  QLORA_ACT_SILU = 0,   /* x / (1 + exp(-x))                                   */
+  QLORA_ACT_GELU = 1    /* x / 2 (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3)))   */
+} qlora_act;
+
+/* H [M x F] bf16 (overwritten).  For the backward: GU_save (nullable) receives
+ * [G | P] [M x 2 F] and U_save (nullable) [U_0 | U_1] [M x 2 r], in bf16.
+ * Workspace: qlora_workspace_bytes(QLORA_OP_GATED_FWD, M, F, K, r, 0). */
+qlora_status qlora_gated_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, const uint16_t* A,
+                             const uint16_t* B, int32_t r, float alpha, int32_t act, uint16_t* H, uint16_t* GU_save,
+                             uint16_t* U_save, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward, from dH [M x F] and the forward's GU:
+ *   dG = dH o P o act'(G) and dP = dH o act(G), rounded to fp32 and from there
+ *   to bf16, as the gradient of a projection's output is in every backward here;
+ *   dX [M x K] = sum_g (dY_g deq(W_g) + s (dY_g B_g) A_g) for dY = (dG, dP)
+ *   (bf16, overwritten; NULL skips it);
+ *   dA [2 r x K] = s [dG B_0 | dP B_1]^T X, dB [2 F x r] with dB_g = s dY_g^T
+ *   U_g (fp32, overwritten; the sums s dY_g B_g enter dA with fp32's precision).
+ * U_saved is the forward's U; NULL computes it again.  r == 0: dA and dB NULL.
+ * With Fp = F rounded up to 32: 2 Fp K, 2 Fp M and M K below 2^31, 2 Fp at most
+ * 2^22; with r > 0 K and 2 Fp below 2^24 and 2 r times M, K or 2 Fp below 2^31.
+ * Workspace: qlora_workspace_bytes(QLORA_OP_GATED_BWD, M, F, K, r, 0). */
+qlora_status qlora_gated_bwd(const qlora_nf4_weight* W, const uint16_t* X, const uint16_t* dH, const uint16_t* GU,
+                             int64_t M, const uint16_t* A, const uint16_t* B, int32_t r, float alpha, int32_t act,
+                             const uint16_t* U_saved, uint16_t* dX, float* dA, float* dB, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* ---- Adapters of many requests ---------------------------------------------
+ * Adapters are small beside the frozen weight that they were trained on, so
+ * one copy of it serves requests of many of them at once.  A pool holds S of
+ * them in slots of one rank; each token names its slot.  Everything in the pool
+ * is device memory that the kernels read when they run: a captured graph
+ * follows a slot that is filled anew, or other ids. */
+#define QLORA_MAX_SLOTS 65536
+typedef struct {
+  int64_t slots;          /* S, 1 to QLORA_MAX_SLOTS                           */
+  int64_t rows;           /* N of the weight; 2 F for a gated block            */
+  int64_t cols;           /* K                                                 */
+  int32_t rank;           /* R of every slot: R % 8 == 0, 8 to 128             */
+  const uint16_t* A;      /* [S x R x K]; [S x 2 R x K], gate's ranks then up's */
+  const uint16_t* B;      /* [S x rows x R]                                    */
+  const float* scale;     /* [S], alpha / r of the slot's adapter              */
+  const int32_t* ranks;   /* nullable [S]: the slot's own rank, at most R (0:
+                             none); ranks past it, rounded up to eight, are not
+                             read: zeros where it is not a multiple of eight   */
+} qlora_adapter_pool;
+
+/* Y [M x N] (bf16, overwritten): y_m = deq(W) x_m + scale_a B_a (A_a x_m) with
+ * a = ids[m]; an id outside 0 .. S - 1 is no adapter.  ids [M], 4-byte aligned,
+ * in any order; tokens of one slot next to each other read it less often.
+ * scale A x is not rounded in between.  Any M >= 1; K % 64 == 0, N % 8 == 0;
+ * N K, M K and M N below 2^31, M R at most 2^27 (QLORA_E_UNSUPPORTED
+ * otherwise).  A slot that no id names is not read; what its scale, A or B hold
+ * does not matter.
+ * Workspace: qlora_workspace_bytes(QLORA_OP_MANY_FWD, M, N, K, R, 0). */
+qlora_status qlora_many_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, const qlora_adapter_pool* pool,
+                            const int32_t* ids, uint16_t* Y, void* ws, size_t ws_bytes, void* stream);
+
+/* qlora_gated_fwd (without what it saves) with the adapters of a pool of rows
+ * 2 F, a slot holding those of gate and up, both of its rank.  Sizes as for
+ * qlora_gated_fwd with r = R.
+ * Workspace: qlora_workspace_bytes(QLORA_OP_GATED_MANY_FWD, M, F, K, R, 0). */
+qlora_status qlora_gated_many_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M,
+                                  const qlora_adapter_pool* pool, const int32_t* ids, int32_t act, uint16_t* H, void* ws,
+                                  size_t ws_bytes, void* stream);
 
 /* ---- Serialized quantized weights -------------------------------------
  * An adapter is trained against one exact quantized base weight: the pages
