@@ -369,11 +369,15 @@ BwdLayout group_bwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, int32_t G
 struct PoolLayout {
   size_t t, wd, part, total;
 };
+constexpr int64_t kStreamTokens = 64;
 PoolLayout pool_layout(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
   PoolLayout L{};
-  L.wd = align_up((size_t)M * (size_t)(G * R) * sizeof(float));
+  L.wd = L.part = align_up((size_t)M * (size_t)(G * R) * sizeof(float));
+  size_t part = (size_t)M * (size_t)(G * N) * sizeof(float);
+  if (M <= kStreamTokens) part *= (size_t)stream_plan(N, K, M, G).splits;
+  // (two codebooks: staged for any M)
   L.part = L.wd + align_up((size_t)G * (size_t)N * (size_t)K * 2);
-  L.total = L.part + align_up(product_part_bytes(G * N, K, M));
+  L.total = L.part + align_up(std::max(part, product_part_bytes(G * N, K, M)));
   return L;
 }
 // 32-bit byte offsets of the stack, X and the results, and (2^27) the thread
@@ -1198,9 +1202,14 @@ qlora_status run_pool(const qlora_nf4_weight* W, const PoolView& p, const uint16
   bf16_t* Wd = reinterpret_cast<bf16_t*>(ws_at(ws, L.wd));
   float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
   qlora_status st;
+  int splits = 1;
+  if (M <= kStreamTokens && W[0].codebook == W[p.G - 1].codebook) {
+    const Nf4View v[2] = {view(&W[0]), view(&W[p.G - 1])};
+    if ((st = hip_status(launch_stream(v, X, M, p, T, U, part, &splits, s))) != QLORA_OK) return st;
+    return hip_status(launch_pool_finish(p, part, splits, M, N, T, act, Y, GU, s));
+  }
   if (p.R > 0 && (st = hip_status(launch_pool_down(p, X, M, K, T, U, s))) != QLORA_OK) return st;
   if ((st = group_dequant(W, p.G, false, Wd, s)) != QLORA_OK) return st;
-  int splits = 1;
   if ((st = hip_status(launch_product_parts(Wd, p.G * N, K, X, M, part, &splits, s))) != QLORA_OK) return st;
   return hip_status(launch_pool_finish(p, part, splits, M, N, T, act, Y, GU, s));
 }

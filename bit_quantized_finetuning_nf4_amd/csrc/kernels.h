@@ -220,6 +220,14 @@ struct PoolView {
 // null) the same without the scale, in bf16.  (pool.hip)
 hipError_t launch_pool_down(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* T, bf16_t* U,
                             hipStream_t st);
+// The G frozen products of few tokens (one codebook) as *splits fp32 parts [M x
+// G N], and T as above in the same launch.  (stream.hip)
+struct StreamPlan {
+  int nt, tiles, tokens, spans, splits;
+};
+StreamPlan stream_plan(int64_t N, int64_t K, int64_t M, int G);
+hipError_t launch_stream(const Nf4View* W, const bf16_t* X, int64_t M, const PoolView& pool, float* T, bf16_t* U,
+                         float* part, int* splits, hipStream_t st);
 // Y [M x N] from `splits` fp32 parts [M x G N] of the frozen products and the
 // adapters' term; G == 2: act(first) second, and the two themselves to GU
 // [M x 2 N] (may be null).

@@ -8,43 +8,15 @@
 // for every token is a pool of one slot.
 #include <algorithm>
 
+#include "downs.h"
 #include "gate.h"
-#include "lds.h"
-#include "pool.h"
 
 namespace qlora {
 namespace {
 
-// T [M x G R] fp32: a workgroup takes one token and eight of its slot's rank
-// rows, two a wave, in fp32 dot products.  U (may be null) is A_a x_m in bf16.
 __global__ __launch_bounds__(256) void pool_down_kernel(PoolView p, const bf16_t* __restrict__ X, int64_t M, int64_t K,
                                                         float* __restrict__ T, bf16_t* __restrict__ U) {
-  const int GR = p.G * p.R, per = GR / 8;
-  const int64_t m = blockIdx.x / per;
-  const int j0 = (int)(blockIdx.x - m * per) * 8, t = threadIdx.x, lane = t & 63, w = t >> 6;
-  const int a = slot_of(p, m);
-  if (a < 0 || j0 % p.R >= rank_of(p, a)) return;
-  const bf16_t* A = p.A + ((int64_t)a * GR + j0 + 2 * w) * K;
-  const bf16_t* x = X + m * K;
-  float s0 = 0.0f, s1 = 0.0f;
-  for (int64_t k = 8 * lane; k < K; k += 512) {
-    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + k), a0 = *reinterpret_cast<const u32x4_t*>(A + k),
-                  a1 = *reinterpret_cast<const u32x4_t*>(A + K + k);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float lo = bf2f(v[e] & 0xFFFFu), hi = bf2f(v[e] >> 16);
-      s0 = fmaf(bf2f(a0[e] & 0xFFFFu), lo, s0), s0 = fmaf(bf2f(a0[e] >> 16), hi, s0);
-      s1 = fmaf(bf2f(a1[e] & 0xFFFFu), lo, s1), s1 = fmaf(bf2f(a1[e] >> 16), hi, s1);
-    }
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) s0 += __shfl_xor(s0, o), s1 += __shfl_xor(s1, o);
-  if (lane < 2) {
-    const float v = lane ? s1 : s0;
-    const int64_t o = m * GR + j0 + 2 * w + lane;
-    T[o] = v * scale_of(p, a);
-    if (U) U[o] = (bf16_t)pack_bf16x2(v, 0.0f);
-  }
+  pool_down<4>(p, X, M, K, T, U, blockIdx.x);
 }
 
 // A thread takes one column of the result and TB tokens: the splits' parts in
@@ -113,7 +85,7 @@ __global__ __launch_bounds__(256) void pool_finish_kernel(PoolView p, const floa
 
 hipError_t launch_pool_down(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* T, bf16_t* U,
                             hipStream_t st) {
-  hipLaunchKernelGGL(pool_down_kernel, dim3((unsigned)(M * (p.G * p.R / 8))), dim3(256), 0, st, p, X, M, K, T, U);
+  hipLaunchKernelGGL(pool_down_kernel, dim3((unsigned)pool_down_blocks(p, M, 4)), dim3(256), 0, st, p, X, M, K, T, U);
   return hipGetLastError();
 }
 
