@@ -367,14 +367,18 @@ BwdLayout group_bwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, int32_t G
 // A gated block and the adapters of many requests: G weights N x K (1, or gate
 // and up) side by side, adapters of rank R for each (0: none).
 struct PoolLayout {
-  size_t t, wd, part, total;
+  size_t t, counts, wd, part, total;
 };
 constexpr int64_t kStreamTokens = 64;
 PoolLayout pool_layout(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
   PoolLayout L{};
-  L.wd = L.part = align_up((size_t)M * (size_t)(G * R) * sizeof(float));
-  size_t part = (size_t)M * (size_t)(G * N) * sizeof(float);
-  if (M <= kStreamTokens) part *= (size_t)stream_plan(N, K, M, G).splits;
+  size_t part = 0;
+  L.counts = L.wd = align_up((size_t)M * (size_t)(G * R) * sizeof(float));
+  if (M <= kStreamTokens) {
+    const StreamPlan s = stream_plan(N, K, M, G, R);
+    L.wd = L.counts + align_up((size_t)s.all_tiles * sizeof(int32_t));
+    part = (size_t)s.slots * (size_t)M * (size_t)(G * N) * sizeof(float);
+  }
   // (two codebooks: staged for any M)
   L.part = L.wd + align_up((size_t)G * (size_t)N * (size_t)K * 2);
   L.total = L.part + align_up(std::max(part, product_part_bytes(G * N, K, M)));
@@ -1202,16 +1206,18 @@ qlora_status run_pool(const qlora_nf4_weight* W, const PoolView& p, const uint16
   bf16_t* Wd = reinterpret_cast<bf16_t*>(ws_at(ws, L.wd));
   float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
   qlora_status st;
-  int splits = 1;
   if (M <= kStreamTokens && W[0].codebook == W[p.G - 1].codebook) {
     const Nf4View v[2] = {view(&W[0]), view(&W[p.G - 1])};
-    if ((st = hip_status(launch_stream(v, X, M, p, T, U, part, &splits, s))) != QLORA_OK) return st;
-    return hip_status(launch_pool_finish(p, part, splits, M, N, T, act, Y, GU, s));
+    const StreamPlan plan = stream_plan(N, K, M, p.G, p.R);
+    int32_t* counts = reinterpret_cast<int32_t*>(ws_at(ws, L.counts));
+    if ((st = hip_status(launch_stream(v, X, M, p, plan, T, U, part, counts, s))) != QLORA_OK) return st;
+    return hip_status(launch_pool_finish(p, part, 0, counts, &plan.line, M, N, T, act, Y, GU, s));
   }
+  int splits = 1;
   if (p.R > 0 && (st = hip_status(launch_pool_down(p, X, M, K, T, U, s))) != QLORA_OK) return st;
   if ((st = group_dequant(W, p.G, false, Wd, s)) != QLORA_OK) return st;
   if ((st = hip_status(launch_product_parts(Wd, p.G * N, K, X, M, part, &splits, s))) != QLORA_OK) return st;
-  return hip_status(launch_pool_finish(p, part, splits, M, N, T, act, Y, GU, s));
+  return hip_status(launch_pool_finish(p, part, splits, nullptr, nullptr, M, N, T, act, Y, GU, s));
 }
 
 bool act_ok(int32_t act) { return act == QLORA_ACT_SILU || act == QLORA_ACT_GELU; }

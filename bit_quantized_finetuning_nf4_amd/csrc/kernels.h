@@ -220,19 +220,50 @@ struct PoolView {
 // null) the same without the scale, in bf16.  (pool.hip)
 hipError_t launch_pool_down(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* T, bf16_t* U,
                             hipStream_t st);
-// The G frozen products of few tokens (one codebook) as *splits fp32 parts [M x
-// G N], and T as above in the same launch.  (stream.hip)
-struct StreamPlan {
-  int nt, tiles, tokens, spans, splits;
+// The work of a streamed product (stream.hip), shared out to `wgs` workgroups:
+// `downs` tasks, task i to workgroup i wgs / downs, and tiles x spans units, in
+// order, so many to each that with a task's cost (down_cost, a unit's being
+// kUnitCost) the sums are even.  Where a workgroup may have more than a task,
+// or few units, down_cost is 0: as many units to each.  Every workgroup has a
+// unit; cost wgs < 2^32.
+constexpr int kStreamRows = 256;
+constexpr uint32_t kUnitCost = 8;
+struct StreamLine {
+  uint32_t tiles, spans, downs, down_cost, cost, wgs, block;   // tiles of one weight and token block; tokens of a block
+  // the first unit of workgroup w, and its first task
+  __host__ __device__ uint32_t unit(uint32_t w) const { return (w * cost / wgs - task(w) * down_cost) / kUnitCost; }
+  __host__ __device__ uint32_t task(uint32_t w) const { return (w * downs + wgs - 1) / wgs; }
+  // the workgroup of a unit: unit(w) is off an even share by less than a task
+  __host__ __device__ uint32_t of(uint32_t u) const {
+    uint32_t w = min_(u * kUnitCost * wgs / (cost - downs * down_cost), wgs - 1);
+    while (unit(w) > u) --w;
+    while (w + 1 < wgs && unit(w + 1) <= u) ++w;
+    return w;
+  }
+  // the first workgroup of a tile
+  __host__ __device__ uint32_t first(uint32_t tile) const { return of(tile * spans); }
+
+ private:
+  static __host__ __device__ uint32_t min_(uint32_t a, uint32_t b) { return a < b ? a : b; }
 };
-StreamPlan stream_plan(int64_t N, int64_t K, int64_t M, int G);
-hipError_t launch_stream(const Nf4View* W, const bf16_t* X, int64_t M, const PoolView& pool, float* T, bf16_t* U,
-                         float* part, int* splits, hipStream_t st);
-// Y [M x N] from `splits` fp32 parts [M x G N] of the frozen products and the
-// adapters' term; G == 2: act(first) second, and the two themselves to GU
-// [M x 2 N] (may be null).
-hipError_t launch_pool_finish(const PoolView& p, const float* part, int splits, int64_t M, int64_t N, const float* T,
-                              int act, bf16_t* Y, bf16_t* GU, hipStream_t st);
+struct StreamPlan {
+  int nt, slots;   // slots: parts of a tile at most
+  int tt;          // tokens of a task
+  int all_tiles;   // of all weights and token blocks
+  StreamLine line;
+};
+StreamPlan stream_plan(int64_t N, int64_t K, int64_t M, int G, int R);
+// The G frozen products (one codebook) as parts [slots][M][G N], counts[t] of
+// those of tile t (token block, weight, kStreamRows rows), and T as above in the
+// same launch.
+hipError_t launch_stream(const Nf4View* W, const bf16_t* X, int64_t M, const PoolView& pool, const StreamPlan& plan,
+                         float* T, bf16_t* U, float* part, int32_t* counts, hipStream_t st);
+// Y [M x N] from fp32 parts [M x G N] of the frozen products, `splits` of them or
+// (counts not null) as launch_stream leaves them, and the adapters' term; G ==
+// 2: act(first) second, and the two themselves to GU [M x 2 N] (may be null).
+hipError_t launch_pool_finish(const PoolView& p, const float* part, int splits, const int32_t* counts,
+                              const StreamLine* line, int64_t M, int64_t N, const float* T, int act, bf16_t* Y,
+                              bf16_t* GU, hipStream_t st);
 // dY [M x 2 Fp] = [dG | dP] of a gated block (gated.hip), zero from column F of
 // each half on, as Wt [K x 2 Fp] is made (may be null).
 hipError_t launch_gated_grad(const bf16_t* dH, const bf16_t* GU, int64_t M, int64_t F, int64_t Fp, int act, bf16_t* dY,
