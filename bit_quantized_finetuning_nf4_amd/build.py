@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqlora.so")
 SOURCES = ["quantize.hip", "gemm.hip", "gemm_nf4.hip", "gemm_bf16.hip", "dropout.hip", "i8.hip", "gemm_i8.hip", "gemm_tile.hip",
-           "gated.hip", "pool.hip", "stream.hip", "gemv.hip", "optim.hip", "paged.hip", "capi.hip", "qtensor.cpp"]
+           "gated.hip", "pool.hip", "gemm_pool.hip", "stream.hip", "gemv.hip", "optim.hip", "paged.hip", "capi.hip", "qtensor.cpp"]
 ARCH = "gfx950"
 
 

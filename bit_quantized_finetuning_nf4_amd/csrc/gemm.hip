@@ -840,6 +840,16 @@ hipError_t start_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t
                  : wide_partials<128, true, false>(dY, M, N, B, r, DropArgs{}, sp, part, st);
 }
 
+hipError_t start_xat_parts(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, float* part, bf16_t* out,
+                           bf16_t* parts, float s, Ride* rest, hipStream_t st) {
+  const RowArgs a{X, M, K, K, 0, A, r, 0, 1, r};
+  *rest = sum_ride(kRideSum, part, split_for((M + 127) / 128, K, 256), M * r, 1.0f, out, parts, s);
+  if (r <= 64) return row_partials<64, false>(a, part, st);
+  if (r <= 128) return row_partials<128, false>(a, part, st);
+  if (r <= 192) return row_partials<192, false>(a, part, st);
+  return row_partials<256, false>(a, part, st);
+}
+
 size_t group_dyb_part_bytes(int64_t M, int64_t N, int r, int G) {
   return part_bytes(split_for((M + 127) / 128, N, 256), M * G * r);
 }

@@ -523,22 +523,31 @@ size_t staged_part_bytes(int64_t N, int64_t K, int64_t M) {
 
 double staged_cost(int64_t N, int64_t K, int64_t M) { return choose_tile(M, N, K / 64, kSplitCus, (size_t)1 << 62).cost; }
 
-// Of the tiles below 256 tokens, on a card of kSplitCus CUs: the parts' number
-// has to be the one that the caller sized its workspace for.
+// The tiles of a product whose sums are left as fp32 parts, on a card of kSplitCus
+// CUs: the parts' number has to be the one that the caller sized its workspace
+// for.  Tiles of 256 tokens only in a split contraction.
 namespace {
 TileChoice parts_tile(int64_t N, int64_t K, int64_t M) {
-  return choose_tile(M, N, K / 64, kSplitCus, (size_t)1 << 62, true);
+  const TileChoice c = choose_tile(M, N, K / 64, kSplitCus, (size_t)1 << 62);
+  return c.tm == 256 && c.splits == 1 ? choose_tile(M, N, K / 64, kSplitCus, (size_t)1 << 62, true) : c;
 }
 }  // namespace
+bool dense_tiles(int64_t N, int64_t K, int64_t M) {
+  const TileChoice c = choose_tile(M, N, K / 64, kSplitCus, (size_t)1 << 62);
+  return c.tm == 256 && c.splits == 1;
+}
 size_t product_part_bytes(int64_t N, int64_t K, int64_t M) {
   return (size_t)parts_tile(N, K, M).splits * (size_t)M * (size_t)N * sizeof(float);
 }
 hipError_t launch_product_parts(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, float* part,
                                 int* splits, hipStream_t st) {
   const TileChoice c = parts_tile(N, K, M);
+  *splits = c.splits;
+  if (c.tm == 256)
+    return launch_fi<4>(Wd, N, K, X, M, nullptr, nullptr, false, 0, 0, N, 0.0f, nullptr, 0, N, st, kTailParts, nullptr,
+                        c.splits, part);
   TileGemm t{};
   t.W = Wd, t.X = X, t.N = N, t.row_bytes = 2 * K, t.M = M, t.part = part, t.keep = true;
-  *splits = c.splits;
   return launch_tile(t, c, 0, N, st);
 }
 

@@ -63,13 +63,13 @@ __device__ __forceinline__ void map_tile(int tiles_c, int tiles_r, int& tc, int&
 // 32 partial cache lines each.  Instead each lane puts its 8-byte pieces
 // into LDS rows of U 8-byte units (unit u of row R at u ^ (R & SM): the 32
 // rows of one write instruction fall on different banks, and with U a
-// multiple of 16 and SM < 16, or U a multiple of 32, the unit stays inside
-// its row), then the workgroup writes the tile out row by row, 16 bytes per
+// multiple of 16 and SM < 16, or U a multiple of 32, or U a multiple of 8 and SM
+// < 8, the unit stays inside its row), then the workgroup writes the tile out row by row, 16 bytes per
 // lane, a wave instruction covering whole rows.  Units c, c + 1 (c even) sit
 // at the aligned pair (c ^ s) & ~1, swapped when s is odd.
 template <int U, int SM>
 __device__ __forceinline__ void lds_put4(char* smem, int R, int u, float x0, float x1, float x2, float x3) {
-  static_assert(U % 32 == 0 || (U % 16 == 0 && SM < 16), "the swizzle must stay inside the row");
+  static_assert(U % 32 == 0 || (U % 16 == 0 && SM < 16) || (U % 8 == 0 && SM < 8), "the swizzle must stay inside the row");
   *reinterpret_cast<u32x2_t*>(smem + (R * U + (u ^ (R & SM))) * 8) = u32x2_t{pack_bf16x2(x0, x1), pack_bf16x2(x2, x3)};
 }
 // The tile's 256 rows out: row R to out + (row0 + R) ld + col0 .. (4 U

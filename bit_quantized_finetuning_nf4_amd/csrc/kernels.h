@@ -186,6 +186,8 @@ hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t*
 // T.  K % 64 == 0; part as for launch_bf16_fwd, staged_part_bytes are enough.
 size_t staged_part_bytes(int64_t N, int64_t K, int64_t M);
 double staged_cost(int64_t N, int64_t K, int64_t M);   // us, estimated
+// Whether the 256-token tiles are estimated the fastest, unsplit.
+bool dense_tiles(int64_t N, int64_t K, int64_t M);
 // X Wd^T alone as *splits fp32 parts [M x N].  product_part_bytes are enough.
 size_t product_part_bytes(int64_t N, int64_t K, int64_t M);
 hipError_t launch_product_parts(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, float* part,
@@ -264,6 +266,33 @@ hipError_t launch_stream(const Nf4View* W, const bf16_t* X, int64_t M, const Poo
 hipError_t launch_pool_finish(const PoolView& p, const float* part, int splits, const int32_t* counts,
                               const StreamLine* line, int64_t M, int64_t N, const float* T, int act, bf16_t* Y,
                               bf16_t* GU, hipStream_t st);
+// The products of many tokens with the adapters' term, and of a gated block's two
+// weights with its activation, from a dequantized stack (gemm_pool.hip): G == 1
+// Wd [N x K]; G == 2 rows in turns of pool_turn, N rounded up to kPoolRows of
+// each, as launch_dequant_pair leaves them.  T: kTermParts parts [M x G R].
+struct PoolGemm {
+  const bf16_t* Wd;
+  int64_t N, K, M;
+  const bf16_t *X, *T;
+  PoolView pool;
+  int act;
+  bf16_t *Y, *GU;
+};
+constexpr int64_t kPoolRows = 32;
+inline int64_t pool_stack_rows(int64_t N, int G) { return G == 1 ? N : (N + kPoolRows - 1) / kPoolRows * kPoolRows * 2; }
+int pool_turn(int64_t N, int64_t M, int G);
+hipError_t launch_pool_gemm(const PoolGemm& g, hipStream_t st);
+// T's parts [M x G R] of a pool's adapters, through `part` (pool_u_part_bytes).
+size_t pool_u_part_bytes(int64_t M, int64_t K, int GR);
+hipError_t launch_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* part, bf16_t* parts,
+                         hipStream_t st);
+// Of one adapter, r <= 256: parts of s X A^T, and X A^T in bf16 to out (may be
+// null); all but *rest (kRideSum).  part: skinny_partial_bytes(M, r, K, kXAt).
+hipError_t start_xat_parts(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, float* part, bf16_t* out,
+                           bf16_t* parts, float s, Ride* rest, hipStream_t st);
+// Two weights N x K as one stack in turns of `turn` rows; those past N are left
+// as they were.  N K < 2^31.
+hipError_t launch_dequant_pair(const Nf4View* W, int turn, bf16_t* out, hipStream_t st);
 // dY [M x 2 Fp] = [dG | dP] of a gated block (gated.hip), zero from column F of
 // each half on, as Wt [K x 2 Fp] is made (may be null).
 hipError_t launch_gated_grad(const bf16_t* dH, const bf16_t* GU, int64_t M, int64_t F, int64_t Fp, int act, bf16_t* dY,

@@ -270,6 +270,26 @@ __global__ __launch_bounds__(256) void dequant_kernel(DeqSrcs src, int64_t numel
   dequant_block<CB>(src.codes[wi], src.absmax_q[wi], src.group_scale[wi], numel, nb, absfmt, out + wi * out_gs,
                     rev ? (int64_t)gridDim.x - 1 - blockIdx.x : (int64_t)blockIdx.x);
 }
+// A gated block's two weights as one stack: the y-th `turn` rows of weight z to
+// rows (2 y + z) turn ..
+template <int CB>
+__global__ __launch_bounds__(256) void dequant_pair_kernel(DeqSrcs src, int64_t N, int64_t K, int absfmt0, int absfmt1,
+                                                           bf16_t* __restrict__ out, int turn, int z0,
+                                                           int rev) {
+  const int z = z0 + (int)blockIdx.z;
+  const int64_t y = rev ? (int64_t)gridDim.y - 1 - blockIdx.y : (int64_t)blockIdx.y;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) << 4, e0 = y * turn * K + i;   // 16 weights a thread
+  if (i >= turn * K || e0 >= N * K) return;
+  const int64_t b = e0 >> 6;   // K % 64 == 0
+  const Nf4Table T = make_table<CB>(block_scale(src.absmax_q[z][b], src.group_scale[z][b / kGroupBlocks], z ? absfmt1 : absfmt0));
+  const uint2 c = *reinterpret_cast<const uint2*>(src.codes[z] + (e0 >> 1));
+  uint32_t o[8];
+  dequant8(c.x, T, o);
+  dequant8(c.y, T, o + 4);
+  uint4* dst = reinterpret_cast<uint4*>(out + (2 * y + z) * turn * K + i);
+  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
 // One weight, and the last step of an adapter's product in the first workgroups.
 template <int CB, int KIND>
 __global__ __launch_bounds__(256) void dequant_ride_kernel(Nf4View W, int64_t nb, bf16_t* __restrict__ out, int rev,
@@ -451,6 +471,24 @@ hipError_t launch_dequant_t_ride(const Nf4View& W, bf16_t* out, int64_t ldo, con
   hipLaunchKernelGGL(fn, dim3((unsigned)(rest.blocks + tiles_k * ((W.N + 63) / 64))), dim3(256), 0, s, W, out, ldo,
                      tiles_k, rev, rest);
   return hipGetLastError();
+}
+
+hipError_t launch_dequant_pair(const Nf4View* W, int turn, bf16_t* out, hipStream_t st) {
+  const int64_t N = W[0].N, K = W[0].K;
+  DeqSrcs src{};
+  for (int g = 0; g < 2; ++g) src.codes[g] = W[g].codes, src.absmax_q[g] = W[g].absmax_q, src.group_scale[g] = W[g].group_scale;
+  const int rev = 4 * N * K > kLlcBytes ? 1 : 0;
+  const int both = W[0].codebook == W[1].codebook ? 2 : 1;   // one launch, or one for each codebook
+  for (int z = 0; z < 2; z += both) {
+    auto* fn = W[z].codebook == kCbFp4   ? &dequant_pair_kernel<kCbFp4>
+               : W[z].codebook == kCbInt4 ? &dequant_pair_kernel<kCbInt4>
+                                          : &dequant_pair_kernel<kCbNf4>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)((turn * K / 16 + 255) / 256), (unsigned)((N + turn - 1) / turn), both), dim3(256), 0, st, src, N,
+                       K, W[0].absfmt, W[1].absfmt, out, turn, z, rev);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_dequant(const uint8_t* codes, const uint8_t* absmax_q, const float* group_scale,

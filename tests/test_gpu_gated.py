@@ -105,7 +105,9 @@ def check_fwd(qs, Ws, X, A, B, alpha, name, label):
 
 SHAPES = [(1, 8, 64, 8), (1, 256, 1024, 64), (2, 40, 128, 0), (5, 136, 192, 24), (16, 264, 512, 16), (17, 64, 320, 8),
           (32, 96, 256, 128), (33, 520, 64, 64), (63, 72, 448, 40), (130, 200, 256, 32), (257, 328, 128, 16),
-          (300, 1032, 576, 72), (1024, 512, 256, 64), (1030, 2056, 320, 8)]
+          (300, 1032, 576, 72), (1024, 512, 256, 64), (1030, 2056, 320, 8),
+          # tiles of 256 tokens: ragged tokens, features and ranks
+          (1999, 2104, 256, 24), (2050, 2056, 192, 128), (1024, 4104, 256, 64), (4100, 1032, 256, 0), (2300, 2184, 128, 8)]
 
 
 @pytest.mark.parametrize("M,N,K,r", SHAPES)

@@ -91,7 +91,9 @@ def spread_ids(rng, M, S, kind):
 
 SHAPES = [(1, 8, 64, 1, 8), (1, 520, 1024, 4, 64), (2, 40, 128, 3, 16), (7, 136, 192, 9, 24), (16, 264, 512, 16, 16),
           (17, 72, 320, 5, 128), (32, 96, 256, 40, 8), (33, 520, 64, 7, 64), (65, 64, 448, 12, 40), (130, 200, 256, 3, 32),
-          (300, 1032, 576, 20, 16), (1030, 520, 320, 8, 64)]
+          (300, 1032, 576, 20, 16), (1030, 520, 320, 8, 64),
+          # tiles of 256 tokens
+          (1999, 4208, 256, 5, 24), (2050, 4104, 192, 300, 8), (1024, 8208, 256, 12, 64), (4100, 2056, 128, 2, 128)]
 
 
 @pytest.mark.parametrize("M,N,K,S,R", SHAPES)
@@ -101,7 +103,8 @@ def test_many(M, N, K, S, R, kind):
     check(M, N, K, S, R, spread_ids(np.random.default_rng(M), M, S, kind), M + N)
 
 
-@pytest.mark.parametrize("M,N,K,S,R", [s for s in SHAPES if s[0] in (1, 7, 32, 65, 300, 1030)])
+@pytest.mark.parametrize("M,N,K,S,R", [s for s in SHAPES if s[0] in (1, 7, 32, 65, 300, 1030)] +
+                         [(1999, 2104, 256, 5, 24), (2050, 2056, 192, 300, 8), (1024, 4104, 256, 12, 64), (2300, 2184, 64, 3, 128)])
 @pytest.mark.parametrize("kind", ["runs", "outside"])
 @pytest.mark.parametrize("name", ["silu", "gelu"])
 def test_gated_many(M, N, K, S, R, kind, name):
@@ -119,18 +122,26 @@ def test_ranks_of_their_own(M, G):
     check(M, 136, 192, 8, 64, np.sort(rng.integers(0, 8, M)), 4, ranks, G)
 
 
+@pytest.mark.parametrize("G", [1, 2])
+def test_ranks_of_their_own_in_large_tiles(G):
+    ranks = [64, 8, 3, 0, 40, -5, 17, 200]
+    rng = np.random.default_rng(G)
+    check(1999, 4208 // G // 8 * 8, 128, 8, 64, rng.integers(0, 8, 1999), 5, ranks, G)
+    check(1999, 4208 // G // 8 * 8, 128, 8, 64, np.sort(rng.integers(-1, 9, 1999)), 6, ranks, G)
+
+
 @pytest.mark.parametrize("M", [3, 70])
 @pytest.mark.parametrize("codebook,fmt", [("fp4", "linear"), ("int4", "fp8"), ("nf4", "fp8")])
 def test_codebooks(M, codebook, fmt):
     check(M, 72, 320, 3, 16, np.arange(M) % 3, 5, codebook=codebook, absmax_format=fmt)
 
 
-@pytest.mark.parametrize("M", [5, 300])
-def test_what_no_token_names_is_not_read(M):
+@pytest.mark.parametrize("M,N", [(5, 136), (300, 136), (2000, 4104)])
+def test_what_no_token_names_is_not_read(M, N):
     rng = np.random.default_rng(9)
-    q, _ = weight(rng, 136, 128)
+    q, _ = weight(rng, N, 128)
     X = bf16(rng, (M, 128))[0]
-    p, *_ = make_pool(rng, 4, 16, 136, 128)
+    p, *_ = make_pool(rng, 4, 16, N, 128)
     ids = torch.from_numpy(np.where(np.arange(M) % 2 == 0, 1, 3).astype(np.int32)).cuda()
     want = ops.many_fwd(q, X, p, ids)
     for t in (p.A, p.B, p.scale):
@@ -171,10 +182,10 @@ def test_neighbours_and_workspace():
     assert torch.equal(*got) and torch.isfinite(got[0].float()).all()
 
 
-@pytest.mark.parametrize("M", [2, 33, 300])
-def test_captured_call_follows_ids_and_slots(M):
+@pytest.mark.parametrize("M,N", [(2, 136), (33, 136), (300, 136), (2000, 4104)])
+def test_captured_call_follows_ids_and_slots(M, N):
     rng = np.random.default_rng(7)
-    N, K, S, R = 136, 128, 4, 16
+    K, S, R = 128, 4, 16
     q, _ = weight(rng, N, K)
     qs = [weight(rng, N, K)[0] for _ in range(2)]
     X = bf16(rng, (M, K))[0]
