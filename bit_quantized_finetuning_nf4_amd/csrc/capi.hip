@@ -366,28 +366,30 @@ BwdLayout group_bwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, int32_t G
 
 // A gated block and the adapters of many requests: G weights N x K (1, or gate
 // and up) side by side, adapters of rank R for each (0: none).
-// Three ways, by the number of tokens: the codes streamed (up to kStreamTokens,
-// of one codebook); the weights dequantized, and the product in small tiles whose
+// Three ways, by the number of tokens: the codes streamed (up to kStreamTokens);
+// the weights dequantized, and the product in small tiles whose
 // sums the adapters join in a pass of their own; or (dense) in 256-token tiles
 // that take it all.
 constexpr int64_t kStreamTokens = 64;
 enum PoolPath { kPoolStream, kPoolTiles, kPoolDense };
-PoolPath pool_path(int64_t M, int64_t N, int64_t K, int32_t G, bool one_codebook) {
-  if (M <= kStreamTokens && one_codebook) return kPoolStream;
+PoolPath pool_path(int64_t M, int64_t N, int64_t K, int32_t G) {
+  if (M <= kStreamTokens) return kPoolStream;
   return dense_tiles(G * N, K, M) ? kPoolDense : kPoolTiles;
 }
 struct PoolLayout {
+  PoolPath path;
   size_t t, counts, wd, part, total;
 };
-PoolLayout pool_layout(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G, PoolPath path) {
+PoolLayout pool_layout(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
   PoolLayout L{};
+  L.path = pool_path(M, N, K, G);
   const size_t mr = (size_t)M * (size_t)(G * R);
-  if (path == kPoolStream) {
+  if (L.path == kPoolStream) {
     const StreamPlan s = stream_plan(N, K, M, G, R);
     L.counts = align_up(mr * sizeof(float));
     L.part = L.wd = L.counts + align_up((size_t)s.all_tiles * sizeof(int32_t));
     L.total = L.part + align_up((size_t)s.slots * (size_t)M * (size_t)(G * N) * sizeof(float));
-  } else if (path == kPoolTiles) {
+  } else if (L.path == kPoolTiles) {
     L.wd = L.counts = align_up(mr * sizeof(float));
     L.part = L.wd + align_up((size_t)G * (size_t)N * (size_t)K * 2);
     L.total = L.part + align_up(product_part_bytes(G * N, K, M));
@@ -396,14 +398,9 @@ PoolLayout pool_layout(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G, Po
     L.part = L.wd + align_up((size_t)pool_stack_rows(N, G) * (size_t)K * 2);
     L.total = L.part;
     if (R > 0)
-      L.total += align_up(std::max(pool_u_part_bytes(M, K, G * R), skinny_partial_bytes(M, G * R, K, kXAt)));
+      L.total += align_up(std::max(pool_u_part_bytes(M, K, G * R), xat_part_bytes(M, K, G * R)));
   }
   return L;
-}
-// What is asked of the caller: room for weights of one codebook or two.
-size_t pool_bytes(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
-  return std::max(pool_layout(M, N, K, R, G, pool_path(M, N, K, G, true)).total,
-                  pool_layout(M, N, K, R, G, pool_path(M, N, K, G, false)).total);
 }
 // 32-bit byte offsets of the stack, X, the results, a slot's B (2^31) and scale A x
 // (2^29).
@@ -641,7 +638,7 @@ size_t qlora_workspace_bytes(qlora_op op, int64_t M, int64_t N, int64_t K, int32
     case QLORA_OP_GATED_MANY_FWD:
     case QLORA_OP_MANY_FWD: {
       const int32_t G = op == QLORA_OP_MANY_FWD ? 1 : 2;
-      return K > 0 && K % 64 == 0 && pool_sizes_ok(M, N, K, r, G) ? pool_bytes(M, N, K, r, G) : 0;
+      return K > 0 && K % 64 == 0 && pool_sizes_ok(M, N, K, r, G) ? pool_layout(M, N, K, r, G).total : 0;
     }
     case QLORA_OP_GATED_BWD:
       return gated_bwd_ok(M, N, K, r) && K % 64 == 0 ? gated_bwd_layout(M, N, K, r, true).total : 0;
@@ -1220,23 +1217,21 @@ namespace {
 
 // Y = [act of] the G weights' products with the pool's term, on validated
 // arguments.
-qlora_status run_pool(const qlora_nf4_weight* W, const PoolView& p, const uint16_t* X, int64_t M, int act, uint16_t* Y,
-                      uint16_t* GU, uint16_t* U, void* ws, hipStream_t s) {
+qlora_status run_pool(const qlora_nf4_weight* W, const PoolView& p, const PoolLayout& L, const uint16_t* X, int64_t M,
+                      int act, uint16_t* Y, uint16_t* GU, uint16_t* U, void* ws, hipStream_t s) {
   const int64_t N = W[0].rows, K = W[0].cols;
-  const PoolPath path = pool_path(M, N, K, p.G, W[0].codebook == W[p.G - 1].codebook);
-  const PoolLayout L = pool_layout(M, N, K, p.R, p.G, path);
   float* T = reinterpret_cast<float*>(ws_at(ws, L.t));
   bf16_t* Wd = reinterpret_cast<bf16_t*>(ws_at(ws, L.wd));
   float* part = reinterpret_cast<float*>(ws_at(ws, L.part));
   const Nf4View v[2] = {view(&W[0]), view(&W[p.G - 1])};
   qlora_status st;
-  if (path == kPoolStream) {
+  if (L.path == kPoolStream) {
     const StreamPlan plan = stream_plan(N, K, M, p.G, p.R);
     int32_t* counts = reinterpret_cast<int32_t*>(ws_at(ws, L.counts));
     if ((st = hip_status(launch_stream(v, X, M, p, plan, T, U, part, counts, s))) != QLORA_OK) return st;
     return hip_status(launch_pool_finish(p, part, 0, counts, &plan.line, M, N, T, act, Y, GU, s));
   }
-  if (path == kPoolTiles) {
+  if (L.path == kPoolTiles) {
     int splits = 1;
     if (p.R > 0 && (st = hip_status(launch_pool_down(p, X, M, K, T, U, s))) != QLORA_OK) return st;
     if ((st = group_dequant(W, p.G, false, Wd, s)) != QLORA_OK) return st;
@@ -1244,14 +1239,14 @@ qlora_status run_pool(const qlora_nf4_weight* W, const PoolView& p, const uint16
     return hip_status(launch_pool_finish(p, part, splits, nullptr, nullptr, M, N, T, act, Y, GU, s));
   }
   bf16_t* parts = reinterpret_cast<bf16_t*>(T);
-  if (p.R > 0 && p.ids) {
-    if ((st = hip_status(launch_pool_u(p, X, M, K, part, parts, s))) != QLORA_OK) return st;
-  } else if (p.R > 0) {
-    Ride rest;
-    if ((st = hip_status(start_xat_parts(X, p.A, M, K, p.G * p.R, part, U, parts, p.s, &rest, s))) != QLORA_OK) return st;
-    if ((st = hip_status(launch_ride(rest, s))) != QLORA_OK) return st;
+  Ride rest{};
+  rest.kind = kRideSum;
+  if (p.R > 0) {
+    st = hip_status(p.ids ? start_pool_u(p, X, M, K, part, parts, &rest, s)
+                          : start_xat_parts(X, p.A, M, K, p.G * p.R, part, U, parts, p.s, &rest, s));
+    if (st != QLORA_OK) return st;
   }
-  st = p.G == 2 ? hip_status(launch_dequant_pair(v, pool_turn(N, M, 2), Wd, s)) : group_dequant(W, 1, false, Wd, s);
+  st = hip_status(p.G == 2 ? launch_dequant_pair(v, pool_turn(N, M, 2), Wd, rest, s) : launch_dequant_ride(v[0], Wd, rest, s));
   if (st != QLORA_OK) return st;
   return hip_status(launch_pool_gemm(PoolGemm{Wd, N, K, M, X, parts, p, act, Y, GU}, s));
 }
@@ -1284,8 +1279,9 @@ qlora_status pool_fwd(const qlora_nf4_weight* W, int32_t G, const uint16_t* X, i
   if (!X || !Y) return QLORA_E_NULL;
   if (!aligned16(X) || !aligned16(Y)) return QLORA_E_ALIGN;
   if (!act_ok(act)) return QLORA_E_UNSUPPORTED;
-  if ((st = check_ws(ws, ws_bytes, pool_bytes(M, N, K, pool->rank, G))) != QLORA_OK) return st;
-  return run_pool(W, pool_view(pool, ids, G), X, M, act, Y, nullptr, nullptr, ws, (hipStream_t)stream);
+  const PoolLayout L = pool_layout(M, N, K, pool->rank, G);
+  if ((st = check_ws(ws, ws_bytes, L.total)) != QLORA_OK) return st;
+  return run_pool(W, pool_view(pool, ids, G), L, X, M, act, Y, nullptr, nullptr, ws, (hipStream_t)stream);
 }
 
 }  // namespace
@@ -1312,9 +1308,10 @@ qlora_status qlora_gated_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64
   if (!X || !H) return QLORA_E_NULL;
   if (!aligned16(X) || !aligned16(H) || !aligned16(GU_save) || !aligned16(U_save)) return QLORA_E_ALIGN;
   if (!act_ok(act)) return QLORA_E_UNSUPPORTED;
-  if ((st = check_ws(ws, ws_bytes, pool_bytes(M, N, K, r, 2))) != QLORA_OK) return st;
+  const PoolLayout L = pool_layout(M, N, K, r, 2);
+  if ((st = check_ws(ws, ws_bytes, L.total)) != QLORA_OK) return st;
   const PoolView p{A, B, nullptr, nullptr, nullptr, lora_s(alpha, r), 1, r, 2};
-  return run_pool(W, p, X, M, act, H, GU_save, r > 0 ? U_save : nullptr, ws, (hipStream_t)stream);
+  return run_pool(W, p, L, X, M, act, H, GU_save, r > 0 ? U_save : nullptr, ws, (hipStream_t)stream);
 }
 
 qlora_status qlora_gated_bwd(const qlora_nf4_weight* W, const uint16_t* X, const uint16_t* dH, const uint16_t* GU,
@@ -1351,16 +1348,14 @@ qlora_status qlora_gated_bwd(const qlora_nf4_weight* W, const uint16_t* X, const
     U = Ud;
   }
   if ((st = hip_status(launch_gated_grad(dH, GU, M, F, fp, act, dY, WdT, K, s))) != QLORA_OK) return st;
-  if (r > 0) {
-    Ride rest;
-    if ((st = hip_status(start_dyb_parts_group(dY, 2 * fp, B, M, F, r, 2, part, G3, sc, &rest, s))) != QLORA_OK) return st;
-    if ((st = hip_status(launch_ride(rest, s))) != QLORA_OK) return st;
-  }
+  Ride rest{};
+  rest.kind = kRideSum3;
+  if (r > 0 && (st = hip_status(start_dyb_parts_group(dY, 2 * fp, B, M, F, r, 2, part, G3, sc, &rest, s))) != QLORA_OK)
+    return st;
+  if (!dX && (st = hip_status(launch_ride(rest, s))) != QLORA_OK) return st;
   if (dX) {
-    for (int g = 0; g < 2; ++g)
-      if ((st = hip_status(launch_dequant_t(W[g].codes, W[g].absmax_q, W[g].group_scale, F, K, W[g].codebook,
-                                            W[g].absmax_format, WdT + g * fp, 2 * fp, s))) != QLORA_OK)
-        return st;
+    const Nf4View v[2] = {view(&W[0]), view(&W[1])};
+    if ((st = hip_status(launch_dequant_t_pair(v, WdT, fp, rest, s))) != QLORA_OK) return st;
     if ((st = hip_status(launch_staged(WdT, K, 2 * fp, dY, M, r > 0 ? G3 : nullptr, r > 0 ? A : nullptr, true, 2 * r,
                                        nullptr, dX, s, reinterpret_cast<float*>(ws_at(ws, L.split)), L.split_bytes))) !=
         QLORA_OK)

@@ -71,6 +71,10 @@ template <int CB>
 __device__ __forceinline__ uint32_t cb_thresh_bits(int i) {
   return CB == kCbNf4 ? kNf4ThreshBits[i] : CB == kCbFp4 ? kFp4ThreshBits[i] : kInt4ThreshBits[i];
 }
+// The same for a codebook known at run time (uniform).
+__device__ __forceinline__ uint32_t cb_level_bits(int cb, int i) {
+  return cb == kCbNf4 ? kNf4LevelBits[i] : cb == kCbFp4 ? kFp4LevelBits[i] : kInt4LevelBits[i];
+}
 // The code of an all-zero block: the lowest index of a zero level.
 template <int CB>
 constexpr uint32_t cb_zero_code() { return CB == kCbInt4 ? 8u : 7u; }

@@ -199,26 +199,31 @@ struct WideShape {
   static constexpr int kWait = (kWideAhead - 1) * (16 + kQDma) < 63 ? (kWideAhead - 1) * (16 + kQDma) : 63;
 };
 
+// Grid y: groups of stacked adapters, group g of columns g p_gs .. of P (rows of
+// stride ldp), Q + g q_gs, and columns g r .. of the [M x ldo] result.
 template <int RP, bool QT, bool DROP>
 __global__ __launch_bounds__(kWideThreads, 1) void rwide_kernel(const bf16_t* __restrict__ P, int64_t M, int64_t C,
-                                                            const bf16_t* __restrict__ Q, int r, int stages_per_split,
+                                                            int64_t ldp, int64_t p_gs, const bf16_t* __restrict__ Q,
+                                                            int r, int64_t q_gs, int ldo, int stages_per_split,
                                                             int tiles_m, float* __restrict__ part, DropArgs drop) {
   using S = WideShape<RP>;
   extern __shared__ __align__(16) char smem[];
   const int tm = blockIdx.x % tiles_m, sp = blockIdx.x / tiles_m;
+  P += blockIdx.y * p_gs;
+  Q += blockIdx.y * q_gs;
   const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, lr = lane & 31, h = lane >> 5;
   const int64_t m0 = (int64_t)tm * 128;
   const int nst = (int)((C + 63) / 64);
   const int s0 = sp * stages_per_split, s1 = min(nst, s0 + stages_per_split);   // no split is empty
   // P rows of this tile only (rows past M read as zero); Q whole
-  const rsrc_t pr = make_rsrc(P + m0 * C, (uint32_t)(min((int64_t)128, M - m0) * C * 2));
+  const rsrc_t pr = make_rsrc(P + m0 * ldp, (uint32_t)(((min((int64_t)128, M - m0) - 1) * ldp + C) * 2));
   const rsrc_t qr = make_rsrc(Q, (uint32_t)((int64_t)r * C * 2));
   if (w == 4) {   // the wave that brings the stages
     uint32_t po[16], qo[S::kQDma];
 #pragma unroll
     for (int q = 0; q < 16; ++q) {   // rows 8 q .. + 7 of P
       const int row = 8 * q + (lane >> 3);
-      po[q] = (uint32_t)(row * C * 2 + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+      po[q] = (uint32_t)(row * ldp * 2 + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
     }
 #pragma unroll
     for (int q = 0; q < S::kQDma; ++q) {   // 1 KiB pieces of the stage's Q tile
@@ -298,7 +303,7 @@ __global__ __launch_bounds__(kWideThreads, 1) void rwide_kernel(const bf16_t* __
     slot = slot == kWideRing - 1 ? 0 : slot + 1;
   }
   // D[j][m]: lane (lr, h) holds m = m0 + 32 w + lr, j = 32 f + 8 q + 4 h + 0..3
-  float* out = part + (int64_t)sp * M * r;
+  float* out = part + (int64_t)sp * M * ldo + (int64_t)blockIdx.y * r;
   const int64_t m = m0 + 32 * w + lr;
   if (m < M) {
 #pragma unroll
@@ -307,7 +312,7 @@ __global__ __launch_bounds__(kWideThreads, 1) void rwide_kernel(const bf16_t* __
       for (int q = 0; q < 4; ++q) {
         const int j = 32 * f + 8 * q + 4 * h;
         if (j < r)
-          *reinterpret_cast<float4*>(out + m * r + j) =
+          *reinterpret_cast<float4*>(out + m * ldo + j) =
               make_float4(acc[f][4 * q], acc[f][4 * q + 1], acc[f][4 * q + 2], acc[f][4 * q + 3]);
       }
   }
@@ -650,7 +655,7 @@ struct RowArgs {
 };
 
 template <int RP, bool QT>
-hipError_t row_partials(const RowArgs& a, float* part, hipStream_t st) {
+hipError_t run_rows(const RowArgs& a, float* part, float scale, bf16_t* out, bf16_t* out2, hipStream_t st) {
   const Split sp = split_for((a.M + 127) / 128, a.C, 256);
   auto* fn = &rskinny_kernel<RP, QT>;
   const size_t lds = (size_t)kRing * RowShape<RP, QT>::kStage;
@@ -658,13 +663,8 @@ hipError_t row_partials(const RowArgs& a, float* part, hipStream_t st) {
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits, a.G), dim3(kThreads), lds, st, a.P, a.M, a.C, a.ldp, a.p_gs, a.Q,
                      a.r, a.q_gs, sp.sps, sp.tiles, a.ldo, part);
-  return hipGetLastError();
-}
-template <int RP, bool QT>
-hipError_t run_rows(const RowArgs& a, float* part, float scale, bf16_t* out, bf16_t* out2, hipStream_t st) {
-  const hipError_t e = row_partials<RP, QT>(a, part, st);
-  if (e != hipSuccess) return e;
-  return reduce(part, split_for((a.M + 127) / 128, a.C, 256).splits, a.M * a.ldo, scale, nullptr, out, out2, st);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  return reduce(part, sp.splits, a.M * a.ldo, scale, nullptr, out, out2, st);
 }
 
 // Token contraction over G groups (grid y): group g reads Big + g big_gs
@@ -789,15 +789,20 @@ size_t u_part_bytes(int64_t M, int64_t K, int r) {
 namespace {
 
 template <int RP, bool QT, bool DROP>
-hipError_t wide_partials(const bf16_t* P, int64_t M, int64_t C, const bf16_t* Q, int r, const DropArgs& drop,
-                         const Split& sp, float* part, hipStream_t st) {
+hipError_t wide_partials(const RowArgs& a, const DropArgs& drop, const Split& sp, float* part, hipStream_t st) {
   auto* fn = &rwide_kernel<RP, QT, DROP>;
   const size_t lds = (size_t)kWideRing * WideShape<RP>::kStage;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits), dim3(kWideThreads), lds, st, P, M, C, Q, r, sp.sps, sp.tiles,
-                     part, drop);
+  hipLaunchKernelGGL(fn, dim3(sp.tiles * sp.splits, a.G), dim3(kWideThreads), lds, st, a.P, a.M, a.C, a.ldp, a.p_gs, a.Q,
+                     a.r, a.q_gs, a.ldo, sp.sps, sp.tiles, part, drop);
   return hipGetLastError();
+}
+// Of one adapter, P [M x C].
+template <int RP, bool QT, bool DROP>
+hipError_t wide_partials(const bf16_t* P, int64_t M, int64_t C, const bf16_t* Q, int r, const DropArgs& drop,
+                         const Split& sp, float* part, hipStream_t st) {
+  return wide_partials<RP, QT, DROP>(RowArgs{P, M, C, C, 0, Q, r, 0, 1, r}, drop, sp, part, st);
 }
 
 }  // namespace
@@ -840,25 +845,39 @@ hipError_t start_dyb_parts(const bf16_t* dY, const bf16_t* B, int64_t M, int64_t
                  : wide_partials<128, true, false>(dY, M, N, B, r, DropArgs{}, sp, part, st);
 }
 
+// The splits of G such products in one launch.
+namespace {
+Split group_rows_split(int G, int64_t M, int64_t C) {
+  Split s = fill_split(G * ((M + 127) / 128), C, 64, 2, 256);
+  s.tiles /= G;
+  return s;
+}
+int xat_groups(int r) { return r <= 128 ? 1 : 2; }   // r % 16 == 0 past 128: two adapters' stacked
+}  // namespace
+
+size_t xat_part_bytes(int64_t M, int64_t K, int r) { return part_bytes(group_rows_split(xat_groups(r), M, K), M * r); }
+
 hipError_t start_xat_parts(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, float* part, bf16_t* out,
                            bf16_t* parts, float s, Ride* rest, hipStream_t st) {
-  const RowArgs a{X, M, K, K, 0, A, r, 0, 1, r};
-  *rest = sum_ride(kRideSum, part, split_for((M + 127) / 128, K, 256), M * r, 1.0f, out, parts, s);
-  if (r <= 64) return row_partials<64, false>(a, part, st);
-  if (r <= 128) return row_partials<128, false>(a, part, st);
-  if (r <= 192) return row_partials<192, false>(a, part, st);
-  return row_partials<256, false>(a, part, st);
+  const int G = xat_groups(r), rg = r / G;
+  const Split sp = group_rows_split(G, M, K);
+  const RowArgs a{X, M, K, K, 0, A, rg, (int64_t)rg * K, G, r};
+  *rest = sum_ride(kRideSum, part, sp, M * r, 1.0f, out, parts, s);
+  return rg <= 64 ? wide_partials<64, false, false>(a, DropArgs{}, sp, part, st)
+                  : wide_partials<128, false, false>(a, DropArgs{}, sp, part, st);
 }
 
 size_t group_dyb_part_bytes(int64_t M, int64_t N, int r, int G) {
-  return part_bytes(split_for((M + 127) / 128, N, 256), M * G * r);
+  return part_bytes(group_rows_split(G, M, N), M * G * r);
 }
 
 hipError_t start_dyb_parts_group(const bf16_t* dY, int64_t ldy, const bf16_t* B, int64_t M, int64_t N, int r, int G,
                                  float* part, bf16_t* parts, float s, Ride* rest, hipStream_t st) {
+  const Split sp = group_rows_split(G, M, N);
   const RowArgs a{dY, M, N, ldy, ldy / G, B, r, N * r, G, G * r};
-  *rest = sum_ride(kRideSum3, part, split_for((M + 127) / 128, N, 256), M * G * r, 1.0f, nullptr, parts, s);
-  return r <= 64 ? row_partials<64, true>(a, part, st) : row_partials<128, true>(a, part, st);
+  *rest = sum_ride(kRideSum3, part, sp, M * G * r, 1.0f, nullptr, parts, s);
+  return r <= 64 ? wide_partials<64, true, false>(a, DropArgs{}, sp, part, st)
+                 : wide_partials<128, true, false>(a, DropArgs{}, sp, part, st);
 }
 
 hipError_t launch_ride(const Ride& a, hipStream_t st) {

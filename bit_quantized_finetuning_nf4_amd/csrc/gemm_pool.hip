@@ -481,8 +481,8 @@ size_t pool_u_part_bytes(int64_t M, int64_t K, int GR) {
   return (size_t)u_split(M, K).splits * (size_t)M * (size_t)GR * sizeof(float);
 }
 
-hipError_t launch_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* part, bf16_t* parts,
-                         hipStream_t st) {
+hipError_t start_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* part, bf16_t* parts, Ride* rest,
+                        hipStream_t st) {
   const USplit s = u_split(M, K);
   const int GR = p.G * p.R, rp = GR <= 64 ? 64 : 128;
   auto* fn = rp == 64 ? &pool_u_kernel<64> : &pool_u_kernel<128>;
@@ -491,11 +491,11 @@ hipError_t launch_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t 
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(fn, dim3(s.tiles * s.splits, (GR + rp - 1) / rp, p.slots > 1 ? 2 : 1), dim3(kUThreads), lds, st, p, X,
                      M, K, s.sps, s.tiles, part);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  Ride rest{};
-  rest.kind = kRideSum, rest.blocks = (int)((M * GR / 4 + 255) / 256);
-  rest.part = part, rest.splits = s.splits, rest.n = M * GR, rest.scale = 1.0f, rest.parts = parts, rest.s = 1.0f;
-  return launch_ride(rest, st);
+  // (of tokens and ranks without an adapter the sums mean nothing, and are not read)
+  *rest = Ride{};
+  rest->kind = kRideSum, rest->blocks = (int)((M * GR / 4 + 255) / 256);
+  rest->part = part, rest->splits = s.splits, rest->n = M * GR, rest->scale = 1.0f, rest->parts = parts, rest->s = 1.0f;
+  return hipGetLastError();
 }
 
 int pool_turn(int64_t N, int64_t M, int G) { return G == 2 && pool_tiles(N, M, G, device_cu_count()).fi == 3 ? 16 : 32; }

@@ -251,11 +251,12 @@ struct StreamLine {
 struct StreamPlan {
   int nt, slots;   // slots: parts of a tile at most
   int tt;          // tokens of a task
+  int alone;       // tasks of workgroups of their own, after line.wgs others (line.downs is 0)
   int all_tiles;   // of all weights and token blocks
   StreamLine line;
 };
 StreamPlan stream_plan(int64_t N, int64_t K, int64_t M, int G, int R);
-// The G frozen products (one codebook) as parts [slots][M][G N], counts[t] of
+// The G frozen products as parts [slots][M][G N], counts[t] of
 // those of tile t (token block, weight, kStreamRows rows), and T as above in the
 // same launch.
 hipError_t launch_stream(const Nf4View* W, const bf16_t* X, int64_t M, const PoolView& pool, const StreamPlan& plan,
@@ -282,17 +283,22 @@ constexpr int64_t kPoolRows = 32;
 inline int64_t pool_stack_rows(int64_t N, int G) { return G == 1 ? N : (N + kPoolRows - 1) / kPoolRows * kPoolRows * 2; }
 int pool_turn(int64_t N, int64_t M, int G);
 hipError_t launch_pool_gemm(const PoolGemm& g, hipStream_t st);
-// T's parts [M x G R] of a pool's adapters, through `part` (pool_u_part_bytes).
+// T's parts [M x G R] of a pool's adapters, through `part` (pool_u_part_bytes): all
+// but *rest (kRideSum).
 size_t pool_u_part_bytes(int64_t M, int64_t K, int GR);
-hipError_t launch_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* part, bf16_t* parts,
-                         hipStream_t st);
-// Of one adapter, r <= 256: parts of s X A^T, and X A^T in bf16 to out (may be
-// null); all but *rest (kRideSum).  part: skinny_partial_bytes(M, r, K, kXAt).
+hipError_t start_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* part, bf16_t* parts, Ride* rest,
+                        hipStream_t st);
+// The same of one adapter, or of two of rank r / 2 stacked (r <= 256): parts of s
+// X A^T, and X A^T in bf16 to out (may be null).
+size_t xat_part_bytes(int64_t M, int64_t K, int r);
 hipError_t start_xat_parts(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, float* part, bf16_t* out,
                            bf16_t* parts, float s, Ride* rest, hipStream_t st);
 // Two weights N x K as one stack in turns of `turn` rows; those past N are left
-// as they were.  N K < 2^31.
-hipError_t launch_dequant_pair(const Nf4View* W, int turn, bf16_t* out, hipStream_t st);
+// as they were.  N K < 2^31.  With *rest of kRideSum, possibly empty.
+hipError_t launch_dequant_pair(const Nf4View* W, int turn, bf16_t* out, const Ride& rest, hipStream_t st);
+// The two transposed, weight z to columns z half .. of out [K x 2 half]; those past
+// N of each are left as they were.  rest: of kRideSum3, possibly empty.
+hipError_t launch_dequant_t_pair(const Nf4View* W, bf16_t* out, int64_t half, const Ride& rest, hipStream_t st);
 // dY [M x 2 Fp] = [dG | dP] of a gated block (gated.hip), zero from column F of
 // each half on, as Wt [K x 2 Fp] is made (may be null).
 hipError_t launch_gated_grad(const bf16_t* dH, const bf16_t* GU, int64_t M, int64_t F, int64_t Fp, int act, bf16_t* dY,

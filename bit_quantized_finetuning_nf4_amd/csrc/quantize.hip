@@ -272,16 +272,24 @@ __global__ __launch_bounds__(256) void dequant_kernel(DeqSrcs src, int64_t numel
 }
 // A gated block's two weights as one stack: the y-th `turn` rows of weight z to
 // rows (2 y + z) turn ..
+// (The first workgroups: the last step of the adapters' product.)
+struct PairArgs {
+  DeqSrcs src;
+  int64_t N, K;
+  int absfmt[2], turn, z0, rev, bx, by;   // workgroups of a turn, turns
+};
 template <int CB>
-__global__ __launch_bounds__(256) void dequant_pair_kernel(DeqSrcs src, int64_t N, int64_t K, int absfmt0, int absfmt1,
-                                                           bf16_t* __restrict__ out, int turn, int z0,
-                                                           int rev) {
-  const int z = z0 + (int)blockIdx.z;
-  const int64_t y = rev ? (int64_t)gridDim.y - 1 - blockIdx.y : (int64_t)blockIdx.y;
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) << 4, e0 = y * turn * K + i;   // 16 weights a thread
+__global__ __launch_bounds__(256) void dequant_pair_kernel(PairArgs p, bf16_t* __restrict__ out, Ride rest) {
+  int id = (int)blockIdx.x - rest.blocks;
+  if (id < 0) return ride<kRideSum>(rest, blockIdx.x);
+  const DeqSrcs& src = p.src;
+  const int64_t N = p.N, K = p.K;
+  const int turn = p.turn, row = id / p.bx, x = id - row * p.bx, z = p.z0 + row / p.by;
+  const int64_t y = p.rev ? p.by - 1 - row % p.by : row % p.by;
+  const int64_t i = ((int64_t)x * 256 + threadIdx.x) << 4, e0 = y * turn * K + i;   // 16 weights a thread
   if (i >= turn * K || e0 >= N * K) return;
   const int64_t b = e0 >> 6;   // K % 64 == 0
-  const Nf4Table T = make_table<CB>(block_scale(src.absmax_q[z][b], src.group_scale[z][b / kGroupBlocks], z ? absfmt1 : absfmt0));
+  const Nf4Table T = make_table<CB>(block_scale(src.absmax_q[z][b], src.group_scale[z][b / kGroupBlocks], p.absfmt[z]));
   const uint2 c = *reinterpret_cast<const uint2*>(src.codes[z] + (e0 >> 1));
   uint32_t o[8];
   dequant8(c.x, T, o);
@@ -387,6 +395,21 @@ __global__ __launch_bounds__(256) void dequant_t_ride_kernel(Nf4View W, bf16_t* 
   }
 }
 
+// A gated block's two weights transposed side by side, columns z half .. of out
+// [K x 2 half].
+template <int CB>
+__global__ __launch_bounds__(256) void dequant_t_pair_kernel(PairArgs p, bf16_t* __restrict__ out, int64_t half,
+                                                             Ride rest) {
+  const int id = (int)blockIdx.x - rest.blocks;
+  if (id < 0) {
+    ride<kRideSum3>(rest, blockIdx.x);
+  } else {
+    const int row = id / p.bx, bx = id - row * p.bx, z = p.z0 + row / p.by, by = row % p.by;
+    dequant_t_block<CB>(p.src.codes[z], p.src.absmax_q[z], p.src.group_scale[z], p.N, p.K, p.absfmt[z], out + z * half,
+                        2 * half, bx, p.rev ? p.by - 1 - by : by);
+  }
+}
+
 // Kernels whose dynamic-LDS limit has been raised, per device: the
 // attribute call costs a few microseconds of host time, which per-token
 // decode loops and small products would pay on every launch.
@@ -473,18 +496,46 @@ hipError_t launch_dequant_t_ride(const Nf4View& W, bf16_t* out, int64_t ldo, con
   return hipGetLastError();
 }
 
-hipError_t launch_dequant_pair(const Nf4View* W, int turn, bf16_t* out, hipStream_t st) {
+hipError_t launch_dequant_pair(const Nf4View* W, int turn, bf16_t* out, const Ride& rest, hipStream_t st) {
   const int64_t N = W[0].N, K = W[0].K;
-  DeqSrcs src{};
-  for (int g = 0; g < 2; ++g) src.codes[g] = W[g].codes, src.absmax_q[g] = W[g].absmax_q, src.group_scale[g] = W[g].group_scale;
-  const int rev = 4 * N * K > kLlcBytes ? 1 : 0;
+  PairArgs p{};
+  for (int g = 0; g < 2; ++g)
+    p.src.codes[g] = W[g].codes, p.src.absmax_q[g] = W[g].absmax_q, p.src.group_scale[g] = W[g].group_scale,
+    p.absfmt[g] = W[g].absfmt;
+  p.N = N, p.K = K, p.turn = turn, p.rev = 4 * N * K > kLlcBytes ? 1 : 0;
+  p.bx = (int)((turn * K / 16 + 255) / 256), p.by = (int)((N + turn - 1) / turn);
   const int both = W[0].codebook == W[1].codebook ? 2 : 1;   // one launch, or one for each codebook
   for (int z = 0; z < 2; z += both) {
+    p.z0 = z;
+    Ride r = rest;
+    if (z > 0) r.blocks = 0;
     auto* fn = W[z].codebook == kCbFp4   ? &dequant_pair_kernel<kCbFp4>
                : W[z].codebook == kCbInt4 ? &dequant_pair_kernel<kCbInt4>
                                           : &dequant_pair_kernel<kCbNf4>;
-    hipLaunchKernelGGL(fn, dim3((unsigned)((turn * K / 16 + 255) / 256), (unsigned)((N + turn - 1) / turn), both), dim3(256), 0, st, src, N,
-                       K, W[0].absfmt, W[1].absfmt, out, turn, z, rev);
+    hipLaunchKernelGGL(fn, dim3((unsigned)(r.blocks + both * p.bx * p.by)), dim3(256), 0, st, p, out, r);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_dequant_t_pair(const Nf4View* W, bf16_t* out, int64_t half, const Ride& rest, hipStream_t st) {
+  const int64_t N = W[0].N, K = W[0].K;
+  PairArgs p{};
+  for (int g = 0; g < 2; ++g)
+    p.src.codes[g] = W[g].codes, p.src.absmax_q[g] = W[g].absmax_q, p.src.group_scale[g] = W[g].group_scale,
+    p.absfmt[g] = W[g].absfmt;
+  p.N = N, p.K = K, p.rev = 4 * N * K > kLlcBytes ? 1 : 0;
+  p.bx = (int)((K + 255) / 256), p.by = (int)((N + 63) / 64);
+  const int both = W[0].codebook == W[1].codebook ? 2 : 1;
+  for (int z = 0; z < 2; z += both) {
+    p.z0 = z;
+    Ride r = rest;
+    if (z > 0) r.blocks = 0;
+    auto* fn = W[z].codebook == kCbFp4   ? &dequant_t_pair_kernel<kCbFp4>
+               : W[z].codebook == kCbInt4 ? &dequant_t_pair_kernel<kCbInt4>
+                                          : &dequant_t_pair_kernel<kCbNf4>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)(r.blocks + both * p.bx * p.by)), dim3(256), 0, st, p, out, half, r);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -59,7 +59,7 @@ struct StreamArgs {
   const bf16_t* X;
   float* part;            // [slots][M][G N]
   int32_t* counts;        // parts of each tile
-  int G, absfmt[2];
+  int G, codebook[2], absfmt[2];
   StreamLine line;
   PoolView pool;          // R > 0: T [M x G R], U
   int tt;                 // tokens of a task
@@ -95,22 +95,25 @@ __device__ __forceinline__ float q8_fast(uint32_t byte) {
 template <int NT>
 constexpr int kSimdWaves = NT == 4 ? 2 : 4;
 
-template <int CB, int NT>
+template <int NT>
 __global__ __launch_bounds__(kThreads, kSimdWaves<NT>) void stream_kernel(StreamArgs p) {
   using S = XShape<NT>;
   extern __shared__ __align__(16) char smem[];   // no static LDS: addressed from 0
   const StreamLine& L = p.line;
-  const uint32_t wg = blockIdx.x, u0 = L.unit(wg), u1 = L.unit(wg + 1);
+  const uint32_t wg = blockIdx.x;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6, c = lane & 15, g = lane >> 4;
-  if (L.downs > 0) {
+  {
     float* red = reinterpret_cast<float*>(smem);
-    const uint32_t i1 = L.task(wg + 1);
+    const bool alone = wg >= L.wgs;   // a workgroup for one task
+    const uint32_t i0 = alone ? wg - L.wgs : L.task(wg), i1 = alone ? i0 + 1 : L.task(wg + 1);
     uint32_t turn = 0;
-    for (uint32_t i = L.task(wg); i < i1; ++i)
+    for (uint32_t i = i0; i < i1; ++i)
       turn += p.tt == 1 ? pool_down<kWaves, 1>(p.pool, p.X, p.M, p.K, p.T, p.U, i, turn, red)
                         : pool_down<kWaves, 4>(p.pool, p.X, p.M, p.K, p.T, p.U, i, turn, red);
+    if (alone) return;
     if (turn > 0) lds_barrier();   // the last task's sums have been read
   }
+  const uint32_t u0 = L.unit(wg), u1 = L.unit(wg + 1);
   const int64_t K = p.K, N = p.N;
   const uint32_t nblk = (uint32_t)(K >> 6), row_bytes = (uint32_t)(K >> 1);
 
@@ -216,13 +219,17 @@ __global__ __launch_bounds__(kThreads, kSimdWaves<NT>) void stream_kernel(Stream
   set_tile(at);
   load_codes(at.s);
   load_scales(at.s >> 2);
-  {   // the table: entry e of lane column l at 256 e + 8 l; e & 15 = 2 w + (lane >> 5), e >> 4 = i
+  // the table: entry e of lane column l at 256 e + 8 l; e & 15 = 2 w + (lane >> 5),
+  // e >> 4 = i
+  auto build = [&](int cb) __attribute__((always_inline)) {
     const int wu = __builtin_amdgcn_readfirstlane(w);
-    const uint32_t l0 = cb_level_bits<CB>(2 * wu), l1 = cb_level_bits<CB>(2 * wu + 1);
+    const uint32_t l0 = cb_level_bits(cb, 2 * wu), l1 = cb_level_bits(cb, 2 * wu + 1);
     const uint32_t lov = lane < 32 ? l0 : l1, to = (uint32_t)(2 * wu + (lane >> 5)) * 256u + 8u * (uint32_t)(lane & 31);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) *(lds_u64*)(size_t)(to + 4096u * i) = u32x2_t{lov, cb_level_bits<CB>(i)};
-  }
+    for (int i = 0; i < 16; ++i) *(lds_u64*)(size_t)(to + 4096u * i) = u32x2_t{lov, cb_level_bits(cb, i)};
+  };
+  int cb = p.codebook[at.in / L.tiles];
+  build(cb);
   put_x(0);
   load_x();
   const uint32_t col = 8u * (uint32_t)(lane & 31);
@@ -277,9 +284,13 @@ __global__ __launch_bounds__(kThreads, kSimdWaves<NT>) void stream_kernel(Stream
     }
     __builtin_amdgcn_sched_barrier(0);
     const bool last = u + 1 == u1, leave = last || here.s + 1 == L.spans;
+    int cb_next = cb;
     if (!last) {
       next(at);
-      if (leave) set_tile(at);
+      if (leave) {
+        set_tile(at);
+        cb_next = p.codebook[at.in / L.tiles];
+      }
       load_codes(at.s);
       if (leave || (at.s & 3u) == 0) load_scales(at.s >> 2);
     }
@@ -346,6 +357,12 @@ __global__ __launch_bounds__(kThreads, kSimdWaves<NT>) void stream_kernel(Stream
           acc[k][nt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         }
       }
+      if (cb_next != cb) {   // on to the other weight, of another codebook
+        cb = cb_next;
+        lds_barrier();
+        build(cb);
+        lds_barrier();
+      }
     }
   }
 }
@@ -362,11 +379,17 @@ StreamPlan stream_plan(int64_t N, int64_t K, int64_t M, int G, int R) {
   L.spans = (uint32_t)((K + kSpan - 1) / kSpan);
   L.block = 16 * s.nt;
   const uint32_t units = L.tiles * (uint32_t)G * (uint32_t)((M + L.block - 1) / L.block) * L.spans;
-  L.wgs = std::min<uint32_t>(s.nt == 4 ? 256 : 512, units);
-  // (units are below 2^21: G N K and M K below 2^31, M at most 256)
-  s.tt = pool_down_tasks(G * R, M, 1) > (int)L.wgs ? 4 : 1;
+  const uint32_t slots = s.nt == 4 ? 256 : 512;
+  L.wgs = std::min<uint32_t>(slots, units);
+  // (units are below 2^21: G N K and M K below 2^31, M at most 64)
+  s.tt = pool_down_tasks(G * R, M, 1) > (int)slots ? 4 : 1;
   L.downs = R > 0 ? (uint32_t)pool_down_tasks(G * R, M, s.tt) : 0;
   L.down_cost = 10;   // about a unit and a quarter
+  s.alone = 0;
+  // tasks in workgroups of their own where there is room, or where those that are
+  // left need no more units each
+  if (L.downs <= slots / 4 && (units + slots - 1) / slots == (units + slots - L.downs - 1) / (slots - L.downs))
+    L.wgs = std::min<uint32_t>(slots - L.downs, units), s.alone = (int)L.downs, L.downs = 0;
   L.cost = L.downs * L.down_cost + units * kUnitCost;
   if (L.downs > L.wgs || L.cost / L.wgs < L.down_cost + 2 * kUnitCost) L.down_cost = 0, L.cost = units * kUnitCost;
   L.wgs = std::min<uint32_t>(L.wgs, 0xFFFFFFFFu / std::max(L.cost, L.downs));   // products in 32 bits
@@ -382,25 +405,19 @@ hipError_t launch_stream(const Nf4View* W, const bf16_t* X, int64_t M, const Poo
   StreamArgs a{};
   for (int g = 0; g < pool.G; ++g) {
     a.w.codes[g] = W[g].codes, a.w.absmax_q[g] = W[g].absmax_q, a.w.group_scale[g] = W[g].group_scale;
-    a.absfmt[g] = W[g].absfmt;
+    a.codebook[g] = W[g].codebook, a.absfmt[g] = W[g].absfmt;
   }
   a.N = W[0].N, a.K = W[0].K, a.M = M, a.X = X, a.part = part, a.counts = counts, a.G = pool.G;
   a.line = s.line, a.pool = pool, a.tt = s.tt, a.T = T, a.U = U;
   auto go = [&](auto* fn, int lds) {
     const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(fn, dim3(s.line.wgs), dim3(kThreads), lds, st, a);
+    hipLaunchKernelGGL(fn, dim3(s.line.wgs + s.alone), dim3(kThreads), lds, st, a);
     return hipGetLastError();
   };
-  auto by_tokens = [&](auto cb) {
-    constexpr int CB = decltype(cb)::value;
-    return s.nt == 1   ? go(&stream_kernel<CB, 1>, XShape<1>::kLds)
-           : s.nt == 2 ? go(&stream_kernel<CB, 2>, XShape<2>::kLds)
-                       : go(&stream_kernel<CB, 4>, XShape<4>::kLds);
-  };
-  if (W[0].codebook == kCbFp4) return by_tokens(std::integral_constant<int, kCbFp4>{});
-  if (W[0].codebook == kCbInt4) return by_tokens(std::integral_constant<int, kCbInt4>{});
-  return by_tokens(std::integral_constant<int, kCbNf4>{});
+  return s.nt == 1   ? go(&stream_kernel<1>, XShape<1>::kLds)
+         : s.nt == 2 ? go(&stream_kernel<2>, XShape<2>::kLds)
+                     : go(&stream_kernel<4>, XShape<4>::kLds);
 }
 
 }  // namespace qlora

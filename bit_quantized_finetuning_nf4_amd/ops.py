@@ -260,6 +260,14 @@ def _beside(t, like, name):
     return t
 
 
+def _is(t, dtype, shape, like, name):
+    """_need and _beside in one look, for calls whose host time counts: the
+    checks' own messages where it fails."""
+    if t is None or t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_contiguous():
+        _beside(_need(t, dtype, name, shape), like, name)
+    return t.data_ptr()
+
+
 def _whole(q: QuantizedWeight, like):
     """The weight's arrays beside `like`, of their types and at least the sizes
     that its rows and cols need."""
@@ -281,7 +289,7 @@ def _out(t, shape, dtype, like, name):
 
 def _ws_for(ws, nbytes, like):
     if ws is None:
-        return workspace(nbytes, like.device)
+        return _debug.empty((nbytes,), torch.uint8, like.device) if nbytes else None
     return _beside(_need(ws, torch.uint8, "ws"), like, "ws")
 
 
@@ -652,14 +660,14 @@ def gated_fwd(qs: Sequence[QuantizedWeight], X: torch.Tensor, A=None, B=None, al
     _on_current(X.device)
     descs, F, K = _pair(qs, X)
     M = X.shape[0]
-    _need(X, torch.bfloat16, "X", (M, K))
+    x = _is(X, torch.bfloat16, (M, K), X, "X")
     r = _pair_rank(A, B, F, K, X)
     H = _out(out, (M, F), torch.bfloat16, X, "out")
     GU = _out(gu_out, (M, 2 * F), torch.bfloat16, X, "gu_out") if save else None
     U = _out(u_out, (M, 2 * r), torch.bfloat16, X, "u_out") if save and r else None
     ws = _ws_for(ws, workspace_bytes(_lib.QLORA_OP_GATED_FWD, M, F, K, r), X)
-    check(lib().qlora_gated_fwd(descs, _ptr(X), M, _ptr(A), _ptr(B), r, float(alpha), _act(act), _ptr(H), _ptr(GU),
-                                _ptr(U), *_ws_args(ws), _stream()), "qlora_gated_fwd")
+    check(lib().qlora_gated_fwd(descs, x, M, _ptr(A) if r else None, _ptr(B) if r else None, r, float(alpha), _act(act),
+                                H.data_ptr(), _ptr(GU), _ptr(U), *_ws_args(ws), _stream()), "qlora_gated_fwd")
     return (H, GU, U) if save else H
 
 
@@ -671,8 +679,8 @@ def _pair_rank(A, B, F, K, like):
         raise ValueError(f"A must be the two adapters' stacked, got shape {tuple(A.shape)}")
     r = A.shape[0] // 2
     if r:
-        _beside(_need(A, torch.bfloat16, "A", (2 * r, K)), like, "A")
-        _beside(_need(B, torch.bfloat16, "B", (2 * F, r)), like, "B")
+        _is(A, torch.bfloat16, (2 * r, K), like, "A")
+        _is(B, torch.bfloat16, (2 * F, r), like, "B")
     return r
 
 
@@ -722,26 +730,25 @@ class AdapterPool:
         A, B = self.A, self.B
         if A.dim() != 3 or B.dim() != 3:
             raise ValueError(f"a pool's A and B have three dimensions, got {tuple(A.shape)} and {tuple(B.shape)}")
+        if not A.is_cuda:
+            raise ValueError("A must be a GPU tensor (no CPU path)")
         S, rows, R = B.shape
-        _need(A, torch.bfloat16, "A", (S, groups * R, A.shape[2]))
-        _beside(_need(B, torch.bfloat16, "B"), A, "B")
-        _beside(_need(self.scale, torch.float32, "scale", (S,)), A, "scale")
-        if self.rank is not None:
-            _beside(_need(self.rank, torch.int32, "rank", (S,)), A, "rank")
-        return AdapterPoolDesc(S, rows, A.shape[2], R, A.data_ptr(), B.data_ptr(), self.scale.data_ptr(),
-                               _ptr(self.rank))
+        K = A.shape[2]
+        return AdapterPoolDesc(S, rows, K, R, _is(A, torch.bfloat16, (S, groups * R, K), A, "A"),
+                               _is(B, torch.bfloat16, (S, rows, R), A, "B"),
+                               _is(self.scale, torch.float32, (S,), A, "scale"),
+                               None if self.rank is None else _is(self.rank, torch.int32, (S,), A, "rank"))
 
 
 def _many(name, op, descs, N, K, groups, X, pool, ids, act, out, ws):
     M = X.shape[0]
-    _need(X, torch.bfloat16, "X", (M, K))
+    x = _is(X, torch.bfloat16, (M, K), X, "X")
     p = pool.desc(groups)
     _beside(pool.A, X, "pool")
-    _beside(_need(ids, torch.int32, "ids", (M,)), X, "ids")
+    i = _is(ids, torch.int32, (M,), X, "ids")
     Y = _out(out, (M, N), torch.bfloat16, X, "out")
     ws = _ws_for(ws, workspace_bytes(op, M, N, K, p.rank), X)
-    check(getattr(lib(), name)(descs, _ptr(X), M, ctypes.byref(p), _ptr(ids), *act, _ptr(Y), *_ws_args(ws), _stream()),
-          name)
+    check(getattr(lib(), name)(descs, x, M, ctypes.byref(p), i, *act, Y.data_ptr(), *_ws_args(ws), _stream()), name)
     return Y
 
 
