@@ -44,7 +44,6 @@ __device__ __forceinline__ float scaled_sum(int t, float sw, float sx) { return 
 constexpr int kPairOp = kTile * 128;                    // 32 KiB: 256 rows x 64 bf16 (two stages)
 constexpr int kPairSlot = 2 * kPairOp;                  // weight rows at 0, token rows at kPairOp
 constexpr size_t kLdsPairs = 2 * (size_t)kPairSlot;     // 128 KiB: two pair slots
-constexpr size_t kLdsDense = kLdsPairs + 2 * kOp;       // + 32 KiB: the first LoRA tail chunk
 constexpr int kDGroup = 4;                              // token tiles per tile group (tile order)
 
 // Pair slots hold two consecutive 32-wide stages (one 64-wide stage): rows of
@@ -191,6 +190,127 @@ __device__ __forceinline__ void dense_slots(const char* cur, const char* nxt, ch
   if constexpr (X < 8 * FI) {
     dense_slot<MM, FI, X, HF>(cur, nxt, fill, f, pair, acc, F, am, bm, po);
     dense_slots<MM, FI, HF, X + 1>(cur, nxt, fill, f, pair, acc, F, am, bm, po);
+  }
+}
+
+// The same loop through a ring of five half slots of 32 KiB, one operand of a pair
+// each: pair p's weight rows are half 2 p, its token rows half 2 p + 1, and half q
+// is in slot q mod 5.  Two pair slots leave the last lines of a pair a quarter of a
+// pair's time to arrive; here, once a pair has been read, its two slots take the
+// token rows of the pair after next and the weight rows of the one behind it, spread
+// over the whole next pair, and the last lines that a barrier waits for have half a
+// pair's time: the wave's 2 FI weight loads issued after them stay in flight.
+// 4096 x 8192 x 22016 1.94 -> 1.56 cycles a matrix cycle (0.65 -> 0.81 of the time in
+// the matrix units), 1200 -> 1138 us; 333 x 22016 x 4096 95 -> 82.  A loop that waits
+// for no load at all takes the same: the rest is issue, and the clock, which falls
+// as the units fill.  It needs all of the LDS: for kernels that keep nothing else
+// there.
+constexpr size_t kLdsHalves = 5 * (size_t)kPairOp;
+// Load d of the group that follows the barrier of pair p (8 of token rows, 2 FI of
+// weight rows), in matrix instructions after it.
+template <int FI>
+constexpr int half_off(int d) { return d * 16 * FI / (2 * FI + 8); }
+template <int FI>
+__device__ __forceinline__ void half_dma(char* dst, const DenseOps& f, bool wrow, int pair, int q) {
+  const uint32_t soff = (uint32_t)min(pair, f.npair - 1) * 128u;
+  char* dd = dst + 8 * (4 * q + f.w) * 128;
+  if (wrow)
+    dma16(f.wr_, dd, f.wo[q], soff);
+  else
+    dma16(f.xr, dd, f.xo[q], soff);
+}
+template <int FI>
+__device__ __forceinline__ void group_dma(char* dx, char* dw, const DenseOps& f, int p, int d) {
+  if (d < 8)
+    half_dma<FI>(dx, f, false, p + 2, d);
+  else
+    half_dma<FI>(dw, f, true, p + 3, d - 8);
+}
+// Where halves 2 p .. 2 p + 4 are.
+struct Halves {
+  char* s[5];
+};
+// dense_slot, the halves of pair `pair` at c.s[0] and c.s[1], the next at c.s[2] and
+// c.s[3].
+template <class MM, int FI, int X, int HF>
+__device__ __forceinline__ void half_slot(const Halves& c, const DenseOps& f, int pair, typename MM::acc_t (&acc)[FI][4],
+                                          Frags& F, int am, int bm, const PairOffs& po) {
+  constexpr int H = 4 * FI;
+  constexpr int kk = X / H, y = X % H, i = y >> 2, j = y & 3;
+  if constexpr (HF == 1 && X == H) {
+    QLORA_WAIT(2 * FI, 0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if constexpr (kk == 0)
+    acc[i][j] = MM::mma(F.a0[i], F.b0[j], acc[i][j]);
+  else
+    acc[i][j] = MM::mma(F.a1[i], F.b1[j], acc[i][j]);
+#pragma unroll
+  for (int q = 0; q < FI + 4; ++q) {
+    if (rd_slot<FI>(q) != y) continue;
+    const bool isA = q == 0 || q >= 5;
+    const int fr = q == 0 ? 0 : q >= 5 ? q - 4 : q - 1;
+    const bool nxt = kk == 1 && HF == 1;
+    const int o = kk == 0 ? po.o[HF][1] : po.o[HF ^ 1][0];
+    const char* base = c.s[(nxt ? 2 : 0) + (isA ? 0 : 1)] + (isA ? am : bm) + fr * 32 * 128 + o;
+    if (isA) {
+      if (kk == 0) F.a1[fr] = rd16(base); else F.a0[fr] = rd16(base);
+    } else {
+      if (kk == 0) F.b1[fr] = rd16(base); else F.b0[fr] = rd16(base);
+    }
+  }
+  constexpr int off = HF == 0 ? H + X : X < H ? 3 * H + X : X - H;
+#pragma unroll
+  for (int d = 0; d < 2 * FI + 8; ++d)
+    if (half_off<FI>(d) == off) {
+      if constexpr (HF == 1 && X >= H)
+        group_dma<FI>(c.s[0], c.s[1], f, pair, d);
+      else
+        group_dma<FI>(c.s[3], c.s[4], f, pair - 1, d);
+    }
+  __builtin_amdgcn_sched_barrier(0);
+}
+template <class MM, int FI, int HF, int X>
+__device__ __forceinline__ void half_slots(const Halves& c, const DenseOps& f, int pair, typename MM::acc_t (&acc)[FI][4],
+                                           Frags& F, int am, int bm, const PairOffs& po) {
+  if constexpr (X < 8 * FI) {
+    half_slot<MM, FI, X, HF>(c, f, pair, acc, F, am, bm, po);
+    half_slots<MM, FI, HF, X + 1>(c, f, pair, acc, F, am, bm, po);
+  }
+}
+
+// The whole loop: every pair's products into acc.  Ends with the clamped loads past
+// the last pair still in flight.
+template <class MM, int FI>
+__device__ __forceinline__ void dense_halves(char* smem, const DenseOps& f, typename MM::acc_t (&acc)[FI][4], Frags& F,
+                                             int am, int bm, const PairOffs& po) {
+  Halves c;
+#pragma unroll
+  for (int q = 0; q < 5; ++q) c.s[q] = smem + q * kPairOp;
+#pragma unroll
+  for (int q = 0; q < 2 * FI; ++q) half_dma<FI>(c.s[0], f, true, 0, q);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) half_dma<FI>(c.s[1], f, false, 0, q);
+#pragma unroll
+  for (int q = 0; q < 2 * FI; ++q) half_dma<FI>(c.s[2], f, true, 1, q);
+  // as far as the pair before the first would have come
+  constexpr int kBefore = (4 * FI * (2 * FI + 8) + 16 * FI - 1) / (16 * FI);
+#pragma unroll
+  for (int d = 0; d < kBefore; ++d) group_dma<FI>(c.s[3], c.s[4], f, -1, d);
+  QLORA_WAIT(2 * FI + kBefore, 0);   // pair 0 has landed
+  __builtin_amdgcn_s_barrier();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < FI) F.a0[i] = rd16(c.s[0] + am + i * 32 * 128 + po.o[0][0]);
+    F.b0[i] = rd16(c.s[1] + bm + i * 32 * 128 + po.o[0][0]);
+  }
+  for (int pr = 0; pr < f.npair; ++pr) {
+    __builtin_amdgcn_sched_barrier(0);
+    half_slots<MM, FI, 0, 0>(c, f, pr, acc, F, am, bm, po);
+    __builtin_amdgcn_sched_barrier(0);
+    half_slots<MM, FI, 1, 0>(c, f, pr, acc, F, am, bm, po);
+    c = Halves{{c.s[2], c.s[3], c.s[4], c.s[0], c.s[1]}};
   }
 }
 

@@ -11,8 +11,8 @@
 // sub-tile (tokens 128 wr.., weight rows 128 wc..) in 256 accumulator
 // registers, bf16 MFMA 32x32x16 with fp32 accumulation.  The contraction runs
 // in pairs of 32-wide stages: a pair (64 columns: one 128-byte line of every
-// row) comes into one of two LDS pair slots by buffer->LDS DMA, each
-// instruction moving 8 whole rows, one pair ahead; one barrier per pair.
+// row) comes into LDS by buffer->LDS DMA, each instruction moving 8 whole rows,
+// one pair ahead and more (dense_tile.h); one barrier per pair.
 //
 //   dX        the same kernel on deq(W)^T: dX = dY (W^T)^T + s G (A^T)^T,
 //             with A read column-wise in the LoRA tail;
@@ -178,21 +178,7 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
     const int nj = r / 32, part = c / nj;
     tail_dma(dst, tail_src(part), c - part * nj, f.w, lane);
   };
-  if (tdma) tail_dma(smem + kLdsPairs, tail_src(0), 0, f.w, lane);   // chunk 0 past the pair slots
-  // pairs 0 and 1 into slots 0 and 1
-#pragma unroll
-  for (int d = 0; d < 2 * FI + 8; ++d) {
-    pair_dma<FI>(smem, f, 0, d);
-    pair_dma<FI>(smem + kPairSlot, f, 1, d);
-  }
-  QLORA_WAIT(0, 0);
-  __builtin_amdgcn_s_barrier();
   Frags F;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i < FI) F.a0[i] = rd16(smem + am + i * 32 * 128 + po.o[0][0]);
-    F.b0[i] = rd16(smem + kPairOp + bm + i * 32 * 128 + po.o[0][0]);
-  }
   // K % 64 == 0: whole pairs of 32-wide stages
   // DR: the mask of the wave's block b = 4 i + j, a word per lane past the pair
   // slots; only the thread that wrote it reads it
@@ -207,17 +193,32 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
     *reinterpret_cast<uint32_t*>(smem + kLdsPairs + 1024 * b + 4 * t) =
         mask_bits(block00 + 32u * (uint32_t)(b & 3) * block_row + 4u * (uint32_t)(b >> 2), key);
   };
-  for (int pr = 0; pr < f.npair; ++pr) {
-    char* cur = smem + (pr & 1) * kPairSlot;
-    char* nxt = smem + ((pr & 1) ^ 1) * kPairSlot;
-    __builtin_amdgcn_sched_barrier(0);
-    dense_slots<MmBf16, FI, 0, 0>(cur, nxt, cur, f, pr, acc, F, am, bm, po);
-    if constexpr (DR) {
+  if constexpr (DR) {
+    // the masks need LDS of their own: two pair slots, pairs 0 and 1 first
+#pragma unroll
+    for (int d = 0; d < 2 * FI + 8; ++d) {
+      pair_dma<FI>(smem, f, 0, d);
+      pair_dma<FI>(smem + kPairSlot, f, 1, d);
+    }
+    QLORA_WAIT(0, 0);
+    __builtin_amdgcn_s_barrier();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < FI) F.a0[i] = rd16(smem + am + i * 32 * 128 + po.o[0][0]);
+      F.b0[i] = rd16(smem + kPairOp + bm + i * 32 * 128 + po.o[0][0]);
+    }
+    for (int pr = 0; pr < f.npair; ++pr) {
+      char* cur = smem + (pr & 1) * kPairSlot;
+      char* nxt = smem + ((pr & 1) ^ 1) * kPairSlot;
+      __builtin_amdgcn_sched_barrier(0);
+      dense_slots<MmBf16, FI, 0, 0>(cur, nxt, cur, f, pr, acc, F, am, bm, po);
       // one block's mask a pair, while the next pair's lines are on their way
       if (tail && pr < 4 * FI) put_bits(pr);
+      __builtin_amdgcn_sched_barrier(0);
+      dense_slots<MmBf16, FI, 1, 0>(cur, nxt, cur, f, pr, acc, F, am, bm, po);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    dense_slots<MmBf16, FI, 1, 0>(cur, nxt, cur, f, pr, acc, F, am, bm, po);
+  } else {
+    dense_halves<MmBf16, FI>(smem, f, acc, F, am, bm, po);
   }
   // drain the DMAs still in flight (clamped re-loads) before reusing LDS
   QLORA_WAIT(0, 0);
@@ -286,31 +287,25 @@ __global__ __launch_bounds__(kThreads, 1) void bf16_fwd_kernel(const bf16_t* __r
     }
   } else if constexpr (TD) {
     if (tdma) {
-      // chunk 0 landed before the drain above; chunks 1 .. go four at a time
-      // into the pair slots, the first four while chunk 0 is multiplied
+      // five chunks at a time, each in a half slot
       constexpr bool raw = FORM == kTailScaled;
       const TailSrc ts = tail_src(0);
-      auto dma = [&](char* dst, int c) __attribute__((always_inline)) {
-        if constexpr (raw)
-          tail_dma(dst, ts, c, f.w, lane);
-        else
-          part_dma(dst, c);
-      };
       const int nt = (raw ? 1 : kTermParts) * (r / 32);
-      int b0 = 1, bn = min(4, nt - 1);
-      for (int c = 0; c < bn; ++c) dma(smem + c * 2 * kOp, b0 + c);
-      tail_chunk(smem + kLdsPairs, raw);
-      while (bn > 0) {
+      for (int b0 = 0; b0 < nt; b0 += 5) {
+        const int bn = min(5, nt - b0);
+        if (b0 > 0) {
+          QLORA_WAIT(0, 0);
+          __builtin_amdgcn_s_barrier();   // every wave is done with the batch before
+        }
+        for (int c = 0; c < bn; ++c) {
+          if constexpr (raw)
+            tail_dma(smem + c * 2 * kOp, ts, b0 + c, f.w, lane);
+          else
+            part_dma(smem + c * 2 * kOp, b0 + c);
+        }
         QLORA_WAIT(0, 0);
         __builtin_amdgcn_s_barrier();
         for (int c = 0; c < bn; ++c) tail_chunk(smem + c * 2 * kOp, raw);
-        b0 += bn;
-        bn = min(4, nt - b0);
-        if (bn > 0) {
-          QLORA_WAIT(0, 0);
-          __builtin_amdgcn_s_barrier();   // every wave is done with the batch's slots
-          for (int c = 0; c < bn; ++c) dma(smem + c * 2 * kOp, b0 + c);
-        }
       }
     }
   } else if (tail) {
@@ -385,7 +380,7 @@ hipError_t launch_fi(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, in
              : form == kTailParts
                  ? (td ? &bf16_fwd_kernel<FI, true, kTailParts> : &bf16_fwd_kernel<FI, false, kTailParts>)
                  : (td ? &bf16_fwd_kernel<FI, true, kTailScaled> : &bf16_fwd_kernel<FI, false, kTailScaled>);
-  const size_t lds = form == kTailPartsDrop ? kLdsPairs + 4096 * FI : td ? kLdsDense : kLdsPairs;
+  const size_t lds = form == kTailPartsDrop ? kLdsPairs + 4096 * FI : kLdsHalves;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)lds);
   if (e != hipSuccess) return e;
   const int npair = (int)(K >> 6);

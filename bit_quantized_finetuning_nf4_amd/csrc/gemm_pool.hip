@@ -131,27 +131,8 @@ __global__ __launch_bounds__(kThreads, 1) void pool_gemm_kernel(PoolGemmArgs p) 
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-#pragma unroll
-  for (int d = 0; d < 2 * FI + 8; ++d) {
-    pair_dma<FI>(smem, f, 0, d);
-    pair_dma<FI>(smem + kPairSlot, f, 1, d);
-  }
-  QLORA_WAIT(0, 0);
-  __builtin_amdgcn_s_barrier();
   Frags F;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i < FI) F.a0[i] = rd16(smem + am + i * 32 * 128 + po.o[0][0]);
-    F.b0[i] = rd16(smem + kPairOp + bm + i * 32 * 128 + po.o[0][0]);
-  }
-  for (int pr = 0; pr < f.npair; ++pr) {
-    char* cur = smem + (pr & 1) * kPairSlot;
-    char* nxt = smem + ((pr & 1) ^ 1) * kPairSlot;
-    __builtin_amdgcn_sched_barrier(0);
-    dense_slots<MmBf16, FI, 0, 0>(cur, nxt, cur, f, pr, acc, F, am, bm, po);
-    __builtin_amdgcn_sched_barrier(0);
-    dense_slots<MmBf16, FI, 1, 0>(cur, nxt, cur, f, pr, acc, F, am, bm, po);
-  }
+  dense_halves<MmBf16, FI>(smem, f, acc, F, am, bm, po);
   QLORA_WAIT(0, 0);   // the clamped re-loads still in flight
   __builtin_amdgcn_s_barrier();
 
@@ -314,10 +295,10 @@ __global__ __launch_bounds__(kThreads, 1) void pool_gemm_kernel(PoolGemmArgs p) 
 template <int FI, int G, bool POOL>
 hipError_t launch_tiles(const PoolGemm& g, int64_t rows, int64_t n_begin, int64_t n_rows, hipStream_t st) {
   auto* fn = &pool_gemm_kernel<FI, G, POOL>;
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)kLdsPairs);
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)kLdsHalves);
   if (e != hipSuccess) return e;
   PoolGemmArgs p{g, rows, n_begin, (int)((n_rows + 64 * FI - 1) / (64 * FI)), (int)((g.M + kTile - 1) / kTile)};
-  hipLaunchKernelGGL(fn, dim3(p.tiles_n * p.tiles_m), dim3(kThreads), kLdsPairs, st, p);
+  hipLaunchKernelGGL(fn, dim3(p.tiles_n * p.tiles_m), dim3(kThreads), kLdsHalves, st, p);
   return hipGetLastError();
 }
 template <int G, bool POOL>
