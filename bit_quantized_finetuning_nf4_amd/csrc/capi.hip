@@ -392,7 +392,9 @@ PoolLayout pool_layout(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
   } else if (L.path == kPoolTiles) {
     L.wd = L.counts = align_up(mr * sizeof(float));
     L.part = L.wd + align_up((size_t)G * (size_t)N * (size_t)K * 2);
-    L.total = L.part + align_up(product_part_bytes(G * N, K, M));
+    size_t bytes = product_part_bytes(G * N, K, M);
+    if (R > 0) bytes = std::max(bytes, std::max(pool_u_part_bytes(M, K, G * R), xat_part_bytes(M, K, G * R)));
+    L.total = L.part + align_up(bytes);
   } else {
     L.wd = L.counts = align_up(mr * 2 * kTermParts);
     L.part = L.wd + align_up((size_t)pool_stack_rows(N, G) * (size_t)K * 2);
@@ -1229,26 +1231,27 @@ qlora_status run_pool(const qlora_nf4_weight* W, const PoolView& p, const PoolLa
     const StreamPlan plan = stream_plan(N, K, M, p.G, p.R);
     int32_t* counts = reinterpret_cast<int32_t*>(ws_at(ws, L.counts));
     if ((st = hip_status(launch_stream(v, X, M, p, plan, T, U, part, counts, s))) != QLORA_OK) return st;
-    return hip_status(launch_pool_finish(p, part, 0, counts, &plan.line, M, N, T, act, Y, GU, s));
+    return hip_status(launch_pool_finish(p, part, plan.slots, counts, &plan.line, M, N, T, act, Y, GU, s));
   }
-  if (L.path == kPoolTiles) {
-    int splits = 1;
-    if (p.R > 0 && (st = hip_status(launch_pool_down(p, X, M, K, T, U, s))) != QLORA_OK) return st;
-    if ((st = group_dequant(W, p.G, false, Wd, s)) != QLORA_OK) return st;
-    if ((st = hip_status(launch_product_parts(Wd, p.G * N, K, X, M, part, &splits, s))) != QLORA_OK) return st;
-    return hip_status(launch_pool_finish(p, part, splits, nullptr, nullptr, M, N, T, act, Y, GU, s));
-  }
-  bf16_t* parts = reinterpret_cast<bf16_t*>(T);
+  // T as bf16 parts for the dense tiles, as it is for the finish; its last step rides in
+  // the dequantization.  (The product's parts may lie where T's were.)
+  const bool dense = L.path == kPoolDense;
+  bf16_t* Tparts = dense ? reinterpret_cast<bf16_t*>(T) : nullptr;
+  float* Tfull = dense ? nullptr : T;
   Ride rest{};
   rest.kind = kRideSum;
   if (p.R > 0) {
-    st = hip_status(p.ids ? start_pool_u(p, X, M, K, part, parts, &rest, s)
-                          : start_xat_parts(X, p.A, M, K, p.G * p.R, part, U, parts, p.s, &rest, s));
+    st = hip_status(p.ids ? start_pool_u(p, X, M, K, part, Tparts, Tfull, &rest, s)
+                          : start_xat_parts(X, p.A, M, K, p.G * p.R, part, U, Tparts, Tfull, p.s, &rest, s));
     if (st != QLORA_OK) return st;
   }
-  st = hip_status(p.G == 2 ? launch_dequant_pair(v, pool_turn(N, M, 2), Wd, rest, s) : launch_dequant_ride(v[0], Wd, rest, s));
+  const int64_t turn = dense ? pool_turn(N, M, 2) : N;
+  st = hip_status(p.G == 2 ? launch_dequant_pair(v, (int)turn, Wd, rest, s) : launch_dequant_ride(v[0], Wd, rest, s));
   if (st != QLORA_OK) return st;
-  return hip_status(launch_pool_gemm(PoolGemm{Wd, N, K, M, X, parts, p, act, Y, GU}, s));
+  if (dense) return hip_status(launch_pool_gemm(PoolGemm{Wd, N, K, M, X, Tparts, p, act, Y, GU}, s));
+  int splits = 1;
+  if ((st = hip_status(launch_product_parts(Wd, p.G * N, K, X, M, part, &splits, s))) != QLORA_OK) return st;
+  return hip_status(launch_pool_finish(p, part, splits, nullptr, nullptr, M, N, T, act, Y, GU, s));
 }
 
 bool act_ok(int32_t act) { return act == QLORA_ACT_SILU || act == QLORA_ACT_GELU; }

@@ -858,11 +858,12 @@ int xat_groups(int r) { return r <= 128 ? 1 : 2; }   // r % 16 == 0 past 128: tw
 size_t xat_part_bytes(int64_t M, int64_t K, int r) { return part_bytes(group_rows_split(xat_groups(r), M, K), M * r); }
 
 hipError_t start_xat_parts(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, float* part, bf16_t* out,
-                           bf16_t* parts, float s, Ride* rest, hipStream_t st) {
+                           bf16_t* parts, float* T, float s, Ride* rest, hipStream_t st) {
   const int G = xat_groups(r), rg = r / G;
   const Split sp = group_rows_split(G, M, K);
   const RowArgs a{X, M, K, K, 0, A, rg, (int64_t)rg * K, G, r};
   *rest = sum_ride(kRideSum, part, sp, M * r, 1.0f, out, parts, s);
+  rest->full = T;
   return rg <= 64 ? wide_partials<64, false, false>(a, DropArgs{}, sp, part, st)
                   : wide_partials<128, false, false>(a, DropArgs{}, sp, part, st);
 }

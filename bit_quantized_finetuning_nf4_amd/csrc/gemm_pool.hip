@@ -462,8 +462,8 @@ size_t pool_u_part_bytes(int64_t M, int64_t K, int GR) {
   return (size_t)u_split(M, K).splits * (size_t)M * (size_t)GR * sizeof(float);
 }
 
-hipError_t start_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* part, bf16_t* parts, Ride* rest,
-                        hipStream_t st) {
+hipError_t start_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* part, bf16_t* parts, float* T,
+                        Ride* rest, hipStream_t st) {
   const USplit s = u_split(M, K);
   const int GR = p.G * p.R, rp = GR <= 64 ? 64 : 128;
   auto* fn = rp == 64 ? &pool_u_kernel<64> : &pool_u_kernel<128>;
@@ -475,7 +475,7 @@ hipError_t start_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K
   // (of tokens and ranks without an adapter the sums mean nothing, and are not read)
   *rest = Ride{};
   rest->kind = kRideSum, rest->blocks = (int)((M * GR / 4 + 255) / 256);
-  rest->part = part, rest->splits = s.splits, rest->n = M * GR, rest->scale = 1.0f, rest->parts = parts, rest->s = 1.0f;
+  rest->part = part, rest->splits = s.splits, rest->n = M * GR, rest->scale = 1.0f, rest->parts = parts, rest->full = T, rest->s = 1.0f;
   return hipGetLastError();
 }
 

@@ -155,6 +155,7 @@ struct Ride {
   RideKind kind;
   int blocks;                 // workgroups of 256
   bf16_t *out, *parts;
+  float* full;                // kRideSum: s times the sum in fp32 (may be null)
   float s;
   const float* part;          // sums of partials
   int splits;
@@ -218,10 +219,6 @@ struct PoolView {
   float s;
   int slots, R, G;   // R == 0: no adapters
 };
-// T [M x G R] fp32, the ranks past a slot's own left as they were; U (may be
-// null) the same without the scale, in bf16.  (pool.hip)
-hipError_t launch_pool_down(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* T, bf16_t* U,
-                            hipStream_t st);
 // The work of a streamed product (stream.hip), shared out to `wgs` workgroups:
 // `downs` tasks, task i to workgroup i wgs / downs, and tiles x spans units, in
 // order, so many to each that with a task's cost (down_cost, a unit's being
@@ -262,7 +259,7 @@ StreamPlan stream_plan(int64_t N, int64_t K, int64_t M, int G, int R);
 hipError_t launch_stream(const Nf4View* W, const bf16_t* X, int64_t M, const PoolView& pool, const StreamPlan& plan,
                          float* T, bf16_t* U, float* part, int32_t* counts, hipStream_t st);
 // Y [M x N] from fp32 parts [M x G N] of the frozen products, `splits` of them or
-// (counts not null) as launch_stream leaves them, and the adapters' term; G ==
+// (counts not null) as launch_stream leaves them, `splits` of a tile at most, and the adapters' term; G ==
 // 2: act(first) second, and the two themselves to GU [M x 2 N] (may be null).
 hipError_t launch_pool_finish(const PoolView& p, const float* part, int splits, const int32_t* counts,
                               const StreamLine* line, int64_t M, int64_t N, const float* T, int act, bf16_t* Y,
@@ -283,16 +280,16 @@ constexpr int64_t kPoolRows = 32;
 inline int64_t pool_stack_rows(int64_t N, int G) { return G == 1 ? N : (N + kPoolRows - 1) / kPoolRows * kPoolRows * 2; }
 int pool_turn(int64_t N, int64_t M, int G);
 hipError_t launch_pool_gemm(const PoolGemm& g, hipStream_t st);
-// T's parts [M x G R] of a pool's adapters, through `part` (pool_u_part_bytes): all
-// but *rest (kRideSum).
+// T [M x G R] of a pool's adapters, as parts or in fp32 (T; either may be null),
+// through `part` (pool_u_part_bytes): all but *rest (kRideSum).
 size_t pool_u_part_bytes(int64_t M, int64_t K, int GR);
-hipError_t start_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* part, bf16_t* parts, Ride* rest,
-                        hipStream_t st);
-// The same of one adapter, or of two of rank r / 2 stacked (r <= 256): parts of s
-// X A^T, and X A^T in bf16 to out (may be null).
+hipError_t start_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* part, bf16_t* parts, float* T,
+                        Ride* rest, hipStream_t st);
+// The same of one adapter, or of two of rank r / 2 stacked (r <= 256): s X A^T, and
+// X A^T in bf16 to out (may be null).
 size_t xat_part_bytes(int64_t M, int64_t K, int r);
 hipError_t start_xat_parts(const bf16_t* X, const bf16_t* A, int64_t M, int64_t K, int r, float* part, bf16_t* out,
-                           bf16_t* parts, float s, Ride* rest, hipStream_t st);
+                           bf16_t* parts, float* T, float s, Ride* rest, hipStream_t st);
 // Two weights N x K as one stack in turns of `turn` rows; those past N are left
 // as they were.  N K < 2^31.  With *rest of kRideSum, possibly empty.
 hipError_t launch_dequant_pair(const Nf4View* W, int turn, bf16_t* out, const Ride& rest, hipStream_t st);

@@ -14,28 +14,48 @@
 namespace qlora {
 namespace {
 
-__global__ __launch_bounds__(256) void pool_down_kernel(PoolView p, const bf16_t* __restrict__ X, int64_t M, int64_t K,
-                                                        float* __restrict__ T, bf16_t* __restrict__ U) {
-  __shared__ float red[2 * 4 * 16];
-  pool_down<4, 4>(p, X, M, K, T, U, blockIdx.x, 0, red);
-}
-
 // A thread takes one column of the result and TB tokens: the parts in order,
-// then its row of B times each token's T (uniform: scalar loads), a run of tokens
-// of one slot sharing the row.  LINE: the parts of a streamed product, TB dividing
-// its blocks of tokens.  Mostly latency: the loads of kR ranks of B and of kP
-// parts are issued together.
+// then its row of B times each token's T, the tokens of one slot sharing the row.
+// LINE: the parts of a streamed product, at most `splits` of them, TB dividing its
+// blocks of tokens.  Mostly latency: T comes through LDS (as scalar loads, rank
+// after rank, it took 2-4 us), and T, kR ranks of B and kP parts are asked for
+// together, before it is known how many parts and ranks there are; what there is
+// not is never used.
 template <int G, int TB, bool LINE>
 __global__ __launch_bounds__(256) void pool_finish_kernel(PoolView p, const float* __restrict__ part, int splits,
                                                           const int32_t* __restrict__ counts, StreamLine line, int64_t M,
                                                           int64_t N, const float* __restrict__ T, int act,
                                                           bf16_t* __restrict__ Y, bf16_t* __restrict__ GU) {
+  __shared__ __align__(16) float ts[TB * G * 128];   // [TB][G R]
   const uint32_t width = blockDim.x;   // columns: 64 or 256
   const uint32_t tiles = (uint32_t)((N + width - 1) / width), bm = blockIdx.x / tiles, bn = blockIdx.x - bm * tiles;
   const int64_t n = (int64_t)bn * width + threadIdx.x, m0 = (int64_t)bm * TB, GN = G * N;
   const int GR = G * p.R, mt = (int)min((int64_t)TB, M - m0);
   const int64_t nc = min(n, N - 1);
-  constexpr int kR = TB == 1 ? 64 : 32, kP = TB == 1 ? 8 : TB == 2 ? 4 : LINE ? 2 : 1;
+  constexpr int kR = TB == 1 ? 64 : 32, kP = TB == 1 ? 8 : TB == 2 ? 4 : 2;
+  const uint32_t quads = (uint32_t)(mt * GR) / 4;
+  u32x4_t tv = u32x4_t{0u, 0u, 0u, 0u};
+  const u32x4_t* t4 = reinterpret_cast<const u32x4_t*>(T + m0 * GR);
+  if (threadIdx.x < quads) tv = t4[threadIdx.x];
+  // the slots of the tokens, and those not yet done
+  int a[TB];
+  uint32_t left = 0u;
+#pragma unroll
+  for (int i = 0; i < TB; ++i) {
+    a[i] = p.R > 0 ? slot_of(p, min(m0 + i, M - 1)) : -1;
+    if (a[i] >= 0 && i < mt) left |= 1u << i;
+  }
+  // ranks j0 .. of the rows of slot s
+  u32x4_t v[G][kR / 8];
+  auto load_b = [&](int s, int j0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int q = 0; q < kR / 8; ++q)
+        if (j0 + 8 * q < p.R)
+          v[g][q] = *reinterpret_cast<const u32x4_t*>(p.B + ((int64_t)s * GN + g * N + nc) * p.R + j0 + 8 * q);
+  };
+  if (p.R > 0) load_b(max(a[0], 0), 0);
   int cnt[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
@@ -45,75 +65,60 @@ __global__ __launch_bounds__(256) void pool_finish_kernel(PoolView p, const floa
       cnt[g] = counts[((uint32_t)m0 / line.block * G + g) * line.tiles + (bn * width) / kStreamRows];
     }
   }
-  float acc[G][TB];
+  float acc[G][TB], x[G][kP][TB];
+  auto load_parts = [&](int g, int s0) __attribute__((always_inline)) {
+    const float* src = part + m0 * GN + g * N + nc;
 #pragma unroll
-  for (int g = 0; g < G; ++g)
+    for (int k = 0; k < kP; ++k)
 #pragma unroll
-    for (int i = 0; i < TB; ++i) acc[g][i] = 0.0f;
-  // the term of tokens i0 .. i1 - 1, of slot a and rank r: ranks j0 ..
-  u32x4_t v[G][kR / 8];
-  auto load_b = [&](int a, int r, int j0) __attribute__((always_inline)) {
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int q = 0; q < kR / 8; ++q) {
-        v[g][q] = u32x4_t{0u, 0u, 0u, 0u};
-        if (j0 + 8 * q < r)
-          v[g][q] = *reinterpret_cast<const u32x4_t*>(p.B + ((int64_t)a * GN + g * N + nc) * p.R + j0 + 8 * q);
-      }
+      for (int i = 0; i < TB; ++i)
+        x[g][k][i] = src[((int64_t)min(s0 + k, splits - 1) * M + min(i, mt - 1)) * GN];
   };
-  auto term = [&](int i0, int i1, int r, int j0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int q = 0; q < kR / 8; ++q) {
-        if (j0 + 8 * q >= r) break;
-        float w[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[2 * e] = bf2f(v[g][q][e] & 0xFFFFu), w[2 * e + 1] = bf2f(v[g][q][e] >> 16);
-#pragma unroll
-        for (int i = 0; i < TB; ++i)
-          if (i >= i0 && i < i1) {
-            const float* t = T + (m0 + i) * GR + g * p.R + j0 + 8 * q;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[g][i] = fmaf(w[e], t[e], acc[g][i]);
-          }
-      }
-  };
-  // the first slot's rows are asked for before the parts
-  int a = p.R > 0 ? slot_of(p, m0) : -1, r = a < 0 ? 0 : rank_of(p, a);
-  load_b(max(a, 0), r, 0);
+  for (int g = 0; g < G; ++g) load_parts(g, 0);
+  if (threadIdx.x < quads) *reinterpret_cast<u32x4_t*>(ts + 4 * threadIdx.x) = tv;
+  for (uint32_t e = threadIdx.x + width; e < quads; e += width) *reinterpret_cast<u32x4_t*>(ts + 4 * e) = t4[e];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const float* src = part + m0 * GN + g * N + nc;
+#pragma unroll
+    for (int i = 0; i < TB; ++i) acc[g][i] = 0.0f;
     for (int s0 = 0; s0 < cnt[g]; s0 += kP) {
-      float x[kP][TB];
+      if (s0 > 0) load_parts(g, s0);
 #pragma unroll
       for (int k = 0; k < kP; ++k)
 #pragma unroll
-        for (int i = 0; i < TB; ++i) {
-          x[k][i] = 0.0f;
-          if (s0 + k < cnt[g] && i < mt) x[k][i] = src[((int64_t)(s0 + k) * M + i) * GN];
-        }
-#pragma unroll
-      for (int k = 0; k < kP; ++k)
-#pragma unroll
-        for (int i = 0; i < TB; ++i) acc[g][i] += x[k][i];
+        for (int i = 0; i < TB; ++i) acc[g][i] = s0 + k < cnt[g] ? acc[g][i] + x[g][k][i] : acc[g][i];
     }
   }
-  if (p.R > 0) {
-    for (int i0 = 0;;) {
-      int i1 = i0 + 1;
-      while (i1 < mt && slot_of(p, m0 + i1) == a) ++i1;
-      term(i0, i1, r, 0);
-      for (int j0 = kR; j0 < r; j0 += kR) {
-        load_b(a, r, j0);
-        term(i0, i1, r, j0);
-      }
-      if ((i0 = i1) >= mt) break;
-      a = slot_of(p, m0 + i0), r = a < 0 ? 0 : rank_of(p, a);
-      load_b(max(a, 0), r, 0);
+  __syncthreads();
+  for (bool first = true; left != 0u; first = false) {
+    const int lead = __builtin_ctz(left), s = slot_of(p, m0 + lead), r = rank_of(p, s);
+    uint32_t set = 0u;   // the tokens of this slot
+#pragma unroll
+    for (int i = 0; i < TB; ++i) set |= a[i] == s ? 1u << i : 0u;
+    set &= left;
+    for (int j0 = 0; j0 < r; j0 += kR) {
+      if (!first || lead > 0 || j0 > 0) load_b(s, j0);
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int q = 0; q < kR / 8; ++q) {
+          if (j0 + 8 * q >= r) break;
+          float w[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[2 * e] = bf2f(v[g][q][e] & 0xFFFFu), w[2 * e + 1] = bf2f(v[g][q][e] >> 16);
+#pragma unroll
+          for (int i = 0; i < TB; ++i)
+            if (set >> i & 1u) {
+              const float4* t = reinterpret_cast<const float4*>(ts + i * GR + g * p.R + j0 + 8 * q);
+              const float4 t0 = t[0], t1 = t[1];
+              const float y[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) acc[g][i] = fmaf(w[e], y[e], acc[g][i]);
+            }
+        }
     }
+    left &= ~set;
   }
   if (n >= N) return;
 #pragma unroll
@@ -133,13 +138,6 @@ __global__ __launch_bounds__(256) void pool_finish_kernel(PoolView p, const floa
 }
 
 }  // namespace
-
-hipError_t launch_pool_down(const PoolView& p, const bf16_t* X, int64_t M, int64_t K, float* T, bf16_t* U,
-                            hipStream_t st) {
-  hipLaunchKernelGGL(pool_down_kernel, dim3((unsigned)pool_down_tasks(p.G * p.R, M, 4)), dim3(256), 0, st, p, X, M, K, T,
-                     U);
-  return hipGetLastError();
-}
 
 // After a streamed product a thread takes as few tokens as fill the card.
 hipError_t launch_pool_finish(const PoolView& p, const float* part, int splits, const int32_t* counts,

@@ -33,8 +33,8 @@ __device__ __forceinline__ float4 sum_splits(const float* __restrict__ part, int
 }
 
 // Workgroup `block` (of a.blocks, 256 threads) of the step.
-//   kRideSum   v = the splits' sum times scale: bf16 of v to out, s v as two
-//              parts
+//   kRideSum   v = the splits' sum times scale: bf16 of v to out, s v as it is or
+//              as two parts
 //   kRideSum3  s v as three parts, together its fp32 value (the workgroups
 //              after those that pad rows)
 // Parts lie n elements apart, each the bf16 rounding of what those before it
@@ -65,8 +65,9 @@ __device__ __forceinline__ void ride(const Ride& a, int block) {
     float4 v = sum_splits(a.part, a.splits, a.n, i, a.scale);
     if (KIND == kRideSum && a.out)
       *reinterpret_cast<uint2*>(a.out + i) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-    if (!a.parts) return;
     v = make_float4(v.x * a.s, v.y * a.s, v.z * a.s, v.w * a.s);
+    if (KIND == kRideSum && a.full) *reinterpret_cast<float4*>(a.full + i) = v;
+    if (!a.parts) return;
 #pragma unroll
     for (int k = 0; k < (KIND == kRideSum3 ? kGradParts : kTermParts); ++k) {
       const uint2 p = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
