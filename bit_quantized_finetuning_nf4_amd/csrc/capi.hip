@@ -1356,16 +1356,17 @@ qlora_status qlora_gated_bwd(const qlora_nf4_weight* W, const uint16_t* X, const
   if (r > 0 && (st = hip_status(start_dyb_parts_group(dY, 2 * fp, B, M, F, r, 2, part, G3, sc, &rest, s))) != QLORA_OK)
     return st;
   if (!dX && (st = hip_status(launch_ride(rest, s))) != QLORA_OK) return st;
+  SplitSum left{};   // dX's, to go with dA's and dB's
   if (dX) {
     const Nf4View v[2] = {view(&W[0]), view(&W[1])};
     if ((st = hip_status(launch_dequant_t_pair(v, WdT, fp, rest, s))) != QLORA_OK) return st;
     if ((st = hip_status(launch_staged(WdT, K, 2 * fp, dY, M, r > 0 ? G3 : nullptr, r > 0 ? A : nullptr, true, 2 * r,
-                                       nullptr, dX, s, reinterpret_cast<float*>(ws_at(ws, L.split)), L.split_bytes))) !=
-        QLORA_OK)
+                                       nullptr, dX, s, reinterpret_cast<float*>(ws_at(ws, L.split)), L.split_bytes,
+                                       r > 0 ? &left : nullptr))) != QLORA_OK)
       return st;
   }
   if (r == 0) return QLORA_OK;
-  return hip_status(launch_adapter_grads_group(G3, X, dY, 2 * fp, fp, U, M, F, K, r, 2, part, dA, dB, sc, s));
+  return hip_status(launch_adapter_grads_group(G3, X, dY, 2 * fp, fp, U, M, F, K, r, 2, part, dA, dB, sc, left, s));
 }
 
 qlora_status qlora_group_dequant(const qlora_nf4_weight* W, int32_t G, uint16_t* Wd_out, void* stream) {

@@ -588,12 +588,22 @@ __global__ __launch_bounds__(256) void ride_kernel(Ride a) {
 
 // The reductions of dA and dB in one launch: elements [0, n0) of the
 // output are out0 (partials at part0, splits0 of them), the next n1 are out1
-// (part1, splits1); each sums its splits in order, as reduce_kernel does.
+// (part1, splits1); each sums its splits in order, as reduce_kernel does.  The
+// first left_blocks workgroups: the sum that dX's product left (a gated block's
+// backward of 256 x 1024 x 1024 at rank 8: one launch of 3 us less).
 __global__ __launch_bounds__(kThreads) void reduce2_kernel(const float* __restrict__ part0, int splits0, int64_t n0,
                                                            float* __restrict__ out0,
                                                            const float* __restrict__ part1, int splits1, int64_t n1,
-                                                           float* __restrict__ out1, float scale, float scale1) {
-  int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+                                                           float* __restrict__ out1, float scale, float scale1,
+                                                           SplitSum left, int left_blocks) {
+  if ((int)blockIdx.x < left_blocks) {
+    const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (i >= left.n) return;
+    const float4 v = sum_splits(left.part, left.splits, left.n, i, 1.0f);
+    *reinterpret_cast<uint2*>(left.out + i) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    return;
+  }
+  int64_t i = ((int64_t)(blockIdx.x - left_blocks) * kThreads + threadIdx.x) * 4;
   const float* part = part0;
   float* out = out0;
   int splits = splits0;
@@ -745,7 +755,7 @@ hipError_t launch_grads(const bf16_t* Gm, const bf16_t* X, const bf16_t* dY, int
   if (e != hipSuccess) return e;
   const int64_t na = (int64_t)ra * K, nb = (int64_t)G * N * r;
   hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(((na + nb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
-                     part, sa, na, dA, part_b, sb, nb, dB, scale, scale);
+                     part, sa, na, dA, part_b, sb, nb, dB, scale, scale, SplitSum{}, 0);
   return hipGetLastError();
 }
 
@@ -917,7 +927,7 @@ hipError_t launch_adapter_grads(const bf16_t* G3, const bf16_t* X, const bf16_t*
   const int64_t ra = whole_a ? 0 : na, rb = whole_b ? 0 : nb;
   if (ra + rb == 0) return hipGetLastError();
   hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(((ra + rb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
-                     part, sa.splits, ra, dA, part_b, sb.splits, rb, dB, 1.0f, scale);
+                     part, sa.splits, ra, dA, part_b, sb.splits, rb, dB, 1.0f, scale, SplitSum{}, 0);
   return hipGetLastError();
 }
 
@@ -949,7 +959,7 @@ size_t group_grads_part_bytes(int64_t M, int64_t N, int64_t K, int r, int G) {
 
 hipError_t launch_adapter_grads_group(const bf16_t* G3, const bf16_t* X, const bf16_t* dY, int64_t ldy, int64_t dy_gs,
                                       const bf16_t* U, int64_t M, int64_t N, int64_t K, int r, int G, float* part,
-                                      float* dA, float* dB, float scale, hipStream_t st) {
+                                      float* dA, float* dB, float scale, const SplitSum& left, hipStream_t st) {
   const GroupGrads g = group_grads_of(M, N, K, r, G);
   float* part_b = part + (part_bytes(g.a, g.na) + 255) / 256 * 256 / sizeof(float);
   const bool whole_a = g.a.splits == 1, whole_b = g.b.splits == 1;
@@ -963,9 +973,10 @@ hipError_t launch_adapter_grads_group(const bf16_t* G3, const bf16_t* X, const b
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(fn, dim3(p.ga * p.blocks_a + G * p.blocks_b), dim3(kThreads), lds, st, p);
   const int64_t ra = whole_a ? 0 : g.na, rb = whole_b ? 0 : g.nb;
-  if (ra + rb == 0) return hipGetLastError();
-  hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(((ra + rb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
-                     part, g.a.splits, ra, dA, part_b, g.b.splits, rb, dB, 1.0f, scale);
+  const int lb = left.splits > 0 ? (int)((left.n / 4 + kThreads - 1) / kThreads) : 0;
+  if (ra + rb == 0 && lb == 0) return hipGetLastError();
+  hipLaunchKernelGGL(reduce2_kernel, dim3((unsigned)(lb + ((ra + rb) / 4 + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
+                     part, g.a.splits, ra, dA, part_b, g.b.splits, rb, dB, 1.0f, scale, left, lb);
   return hipGetLastError();
 }
 

@@ -548,7 +548,7 @@ hipError_t launch_product_parts(const bf16_t* Wd, int64_t N, int64_t K, const bf
 
 hipError_t launch_staged(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* T,
                          const bf16_t* B, bool b_trans, int r, const DropArgs* drop, bf16_t* Y, hipStream_t st,
-                         float* part, size_t part_bytes) {
+                         float* part, size_t part_bytes, SplitSum* rest) {
   const TailForm form = drop ? kTailPartsDrop : kTailParts;
   const TileChoice c = choose_tile(M, N, K / 64, device_cu_count(), part ? part_bytes : 0);
   if (c.tm < 256) {
@@ -557,12 +557,15 @@ hipError_t launch_staged(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X
     t.dropped = drop != nullptr;
     if (drop) t.drop = *drop;
     t.Y = Y, t.part = part;
+    t.keep = rest && c.splits > 1;
+    if (t.keep) *rest = SplitSum{part, c.splits, M * N, Y};
     return launch_tile(t, c, 0, N, st);
   }
   if (c.splits > 1) {
     const hipError_t e = launch_fi<4>(Wd, N, K, X, M, T, B, b_trans, r, r, N, 1.0f, Y, 0, N, st, form, drop,
                                       c.splits, part);
-    return e != hipSuccess ? e : launch_split_sum(part, c.splits, M * N, Y, st);
+    if (rest) *rest = SplitSum{part, c.splits, M * N, Y};
+    return e != hipSuccess || rest ? e : launch_split_sum(part, c.splits, M * N, Y, st);
   }
   return launch_dense(Wd, N, K, X, M, T, r, B, b_trans, r, N, 1.0f, Y, st, part, part_bytes, form, drop);
 }

@@ -193,20 +193,28 @@ bool dense_tiles(int64_t N, int64_t K, int64_t M);
 size_t product_part_bytes(int64_t N, int64_t K, int64_t M);
 hipError_t launch_product_parts(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, float* part,
                                 int* splits, hipStream_t st);
+// rest (may be null): the sum of a split contraction's parts is left to the caller.
+struct SplitSum {
+  const float* part;
+  int splits;   // 0: nothing left
+  int64_t n;
+  bf16_t* out;
+};
 hipError_t launch_staged(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, const bf16_t* T,
                          const bf16_t* B, bool b_trans, int r, const DropArgs* drop, bf16_t* Y, hipStream_t st,
-                         float* part, size_t part_bytes);
+                         float* part, size_t part_bytes, SplitSum* rest = nullptr);
 
 // The same of G stacked adapters of rank r (a gated block's two): columns g N ..
 // of dY [M x ldy] and B + g N r give columns g r .. of G's parts [M x G r].
 size_t group_dyb_part_bytes(int64_t M, int64_t N, int r, int G);
 hipError_t start_dyb_parts_group(const bf16_t* dY, int64_t ldy, const bf16_t* B, int64_t M, int64_t N, int r, int G,
                                  float* part, bf16_t* parts, float s, Ride* rest, hipStream_t st);
-// dA [G r x K] and dB [G N x r] (group g: columns g dy_gs .. of dY, g r .. of U).
+// dA [G r x K] and dB [G N x r] (group g: columns g dy_gs .. of dY, g r .. of U),
+// and the sum that another product left.
 size_t group_grads_part_bytes(int64_t M, int64_t N, int64_t K, int r, int G);
 hipError_t launch_adapter_grads_group(const bf16_t* G3, const bf16_t* X, const bf16_t* dY, int64_t ldy, int64_t dy_gs,
                                       const bf16_t* U, int64_t M, int64_t N, int64_t K, int r, int G, float* part,
-                                      float* dA, float* dB, float scale, hipStream_t st);
+                                      float* dA, float* dB, float scale, const SplitSum& left, hipStream_t st);
 
 // The adapters of a call: S slots of rank R for each of G weights side by side,
 // A [S x G R x K], B [S x G N x R]; token m takes slot ids[m] (ids null: slot 0),
