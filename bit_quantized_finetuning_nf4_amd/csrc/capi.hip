@@ -1277,6 +1277,7 @@ qlora_status pool_fwd(const qlora_nf4_weight* W, int32_t G, const uint16_t* X, i
   qlora_status st = check_group_weights(W, G);
   if (st != QLORA_OK) return st;
   const int64_t N = W[0].rows, K = W[0].cols;
+  if (M <= 0) return QLORA_E_SHAPE;   // before the pointers: no tokens have no ids
   if ((st = check_pool(pool, ids, G * N, K)) != QLORA_OK) return st;
   if ((st = check_pool_sizes(M, N, K, pool->rank, G)) != QLORA_OK) return st;
   if (!X || !Y) return QLORA_E_NULL;
