@@ -386,7 +386,7 @@ PoolLayout pool_layout(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
   const size_t mr = (size_t)M * (size_t)(G * R);
   if (L.path == kPoolStream) {
     const StreamPlan s = stream_plan(N, K, M, G, R);
-    L.counts = align_up(mr * sizeof(float));
+    L.counts = align_up(s.downs.slices * mr * sizeof(float));
     L.part = L.wd = L.counts + align_up((size_t)s.all_tiles * sizeof(int32_t));
     L.total = L.part + align_up((size_t)s.slots * (size_t)M * (size_t)(G * N) * sizeof(float));
   } else if (L.path == kPoolTiles) {
@@ -1230,8 +1230,9 @@ qlora_status run_pool(const qlora_nf4_weight* W, const PoolView& p, const PoolLa
   if (L.path == kPoolStream) {
     const StreamPlan plan = stream_plan(N, K, M, p.G, p.R);
     int32_t* counts = reinterpret_cast<int32_t*>(ws_at(ws, L.counts));
-    if ((st = hip_status(launch_stream(v, X, M, p, plan, T, U, part, counts, s))) != QLORA_OK) return st;
-    return hip_status(launch_pool_finish(p, part, plan.slots, counts, &plan.line, M, N, T, act, Y, GU, s));
+    if ((st = hip_status(launch_stream(v, X, M, p, plan, T, part, counts, s))) != QLORA_OK) return st;
+    return hip_status(launch_pool_finish(p, part, plan.slots, counts, &plan.line, M, N, T, (int)plan.downs.slices,
+                                         p.scale ? 1.0f : p.s, U, act, Y, GU, s));
   }
   // T as bf16 parts for the dense tiles, as it is for the finish; its last step rides in
   // the dequantization.  (The product's parts may lie where T's were.)
@@ -1251,7 +1252,7 @@ qlora_status run_pool(const qlora_nf4_weight* W, const PoolView& p, const PoolLa
   if (dense) return hip_status(launch_pool_gemm(PoolGemm{Wd, N, K, M, X, Tparts, p, act, Y, GU}, s));
   int splits = 1;
   if ((st = hip_status(launch_product_parts(Wd, p.G * N, K, X, M, part, &splits, s))) != QLORA_OK) return st;
-  return hip_status(launch_pool_finish(p, part, splits, nullptr, nullptr, M, N, T, act, Y, GU, s));
+  return hip_status(launch_pool_finish(p, part, splits, nullptr, nullptr, M, N, T, 1, 1.0f, nullptr, act, Y, GU, s));
 }
 
 bool act_ok(int32_t act) { return act == QLORA_ACT_SILU || act == QLORA_ACT_GELU; }

@@ -227,51 +227,55 @@ struct PoolView {
   float s;
   int slots, R, G;   // R == 0: no adapters
 };
-// The work of a streamed product (stream.hip), shared out to `wgs` workgroups:
-// `downs` tasks, task i to workgroup i wgs / downs, and tiles x spans units, in
-// order, so many to each that with a task's cost (down_cost, a unit's being
-// kUnitCost) the sums are even.  Where a workgroup may have more than a task,
-// or few units, down_cost is 0: as many units to each.  Every workgroup has a
-// unit; cost wgs < 2^32.
+// The work of a streamed product (stream.hip): units, `spans` of them to a tile,
+// shared out evenly to `wgs` workgroups in order; units x wgs < 2^32.
 constexpr int kStreamRows = 256;
-constexpr uint32_t kUnitCost = 8;
 struct StreamLine {
-  uint32_t tiles, spans, downs, down_cost, cost, wgs, block;   // tiles of one weight and token block; tokens of a block
-  // the first unit of workgroup w, and its first task
-  __host__ __device__ uint32_t unit(uint32_t w) const { return (w * cost / wgs - task(w) * down_cost) / kUnitCost; }
-  __host__ __device__ uint32_t task(uint32_t w) const { return (w * downs + wgs - 1) / wgs; }
-  // the workgroup of a unit: unit(w) is off an even share by less than a task
-  __host__ __device__ uint32_t of(uint32_t u) const {
-    uint32_t w = min_(u * kUnitCost * wgs / (cost - downs * down_cost), wgs - 1);
-    while (unit(w) > u) --w;
-    while (w + 1 < wgs && unit(w + 1) <= u) ++w;
-    return w;
-  }
+  uint32_t tiles, spans, units, wgs, block;   // tiles of one weight and token block; tokens of a block
+  // the first unit of workgroup w, and the workgroup of unit u
+  __host__ __device__ uint32_t unit(uint32_t w) const { return w * units / wgs; }
+  __host__ __device__ uint32_t of(uint32_t u) const { return ((u + 1) * wgs - 1) / units; }
   // the first workgroup of a tile
   __host__ __device__ uint32_t first(uint32_t tile) const { return of(tile * spans); }
-
- private:
-  static __host__ __device__ uint32_t min_(uint32_t a, uint32_t b) { return a < b ? a : b; }
+};
+// The adapters' first half as tasks of waves (downs.h): `slices` of K, `cols` wide;
+// done by `wgs` workgroups: others than the product's, those that have one unit
+// less than the rest (`least`), or all of them.
+constexpr int kMaxSlices = 4;
+enum StreamTasks : int { kTasksApart, kTasksLight, kTasksAll };
+struct StreamDowns {
+  uint32_t tasks, slices, cols, wgs, least;
+  int tt;   // tokens of a task
+  StreamTasks where;
+  // the number of workgroup w among them, or -1
+  __host__ __device__ int index(const StreamLine& l, uint32_t w) const {
+    if (where == kTasksApart) return w < l.wgs ? -1 : (int)(w - l.wgs);
+    if (where == kTasksAll) return (int)w;
+    const uint32_t u = l.unit(w);
+    return l.unit(w + 1) - u == least ? (int)(w - (u - w * least)) : -1;   // less those before it that have one more
+  }
 };
 struct StreamPlan {
   int nt, slots;   // slots: parts of a tile at most
-  int tt;          // tokens of a task
-  int alone;       // tasks of workgroups of their own, after line.wgs others (line.downs is 0)
   int all_tiles;   // of all weights and token blocks
   StreamLine line;
+  StreamDowns downs;
 };
 StreamPlan stream_plan(int64_t N, int64_t K, int64_t M, int G, int R);
 // The G frozen products as parts [slots][M][G N], counts[t] of
-// those of tile t (token block, weight, kStreamRows rows), and T as above in the
-// same launch.
+// those of tile t (token block, weight, kStreamRows rows), and T as parts
+// [downs.slices][M][G R], with the scales of a pool that has them, in the same
+// launch.
 hipError_t launch_stream(const Nf4View* W, const bf16_t* X, int64_t M, const PoolView& pool, const StreamPlan& plan,
-                         float* T, bf16_t* U, float* part, int32_t* counts, hipStream_t st);
+                         float* T, float* part, int32_t* counts, hipStream_t st);
 // Y [M x N] from fp32 parts [M x G N] of the frozen products, `splits` of them or
 // (counts not null) as launch_stream leaves them, `splits` of a tile at most, and the adapters' term; G ==
 // 2: act(first) second, and the two themselves to GU [M x 2 N] (may be null).
+// T [M x G R] is scale times the sum of `slices` parts, that sum in bf16 to U (may
+// be null).
 hipError_t launch_pool_finish(const PoolView& p, const float* part, int splits, const int32_t* counts,
-                              const StreamLine* line, int64_t M, int64_t N, const float* T, int act, bf16_t* Y,
-                              bf16_t* GU, hipStream_t st);
+                              const StreamLine* line, int64_t M, int64_t N, const float* T, int slices, float scale,
+                              bf16_t* U, int act, bf16_t* Y, bf16_t* GU, hipStream_t st);
 // The products of many tokens with the adapters' term, and of a gated block's two
 // weights with its activation, from a dequantized stack (gemm_pool.hip): G == 1
 // Wd [N x K]; G == 2 rows in turns of pool_turn, N rounded up to kPoolRows of

@@ -8,8 +8,9 @@
 // for every token is a pool of one slot.
 #include <algorithm>
 
-#include "downs.h"
 #include "gate.h"
+#include "lds.h"
+#include "pool.h"
 
 namespace qlora {
 namespace {
@@ -17,15 +18,16 @@ namespace {
 // A thread takes one column of the result and TB tokens: the parts in order,
 // then its row of B times each token's T, the tokens of one slot sharing the row.
 // LINE: the parts of a streamed product, at most `splits` of them, TB dividing its
-// blocks of tokens.  Mostly latency: T comes through LDS (as scalar loads, rank
+// blocks of tokens, and T in `slices` parts; else T in one.  Mostly latency: T comes through LDS (as scalar loads, rank
 // after rank, it took 2-4 us), and T, kR ranks of B and kP parts are asked for
 // together, before it is known how many parts and ranks there are; what there is
 // not is never used.
 template <int G, int TB, bool LINE>
 __global__ __launch_bounds__(256) void pool_finish_kernel(PoolView p, const float* __restrict__ part, int splits,
                                                           const int32_t* __restrict__ counts, StreamLine line, int64_t M,
-                                                          int64_t N, const float* __restrict__ T, int act,
-                                                          bf16_t* __restrict__ Y, bf16_t* __restrict__ GU) {
+                                                          int64_t N, const float* __restrict__ T, int slices, float scale,
+                                                          bf16_t* __restrict__ U, int act, bf16_t* __restrict__ Y,
+                                                          bf16_t* __restrict__ GU) {
   __shared__ __align__(16) float ts[TB * G * 128];   // [TB][G R]
   const uint32_t width = blockDim.x;   // columns: 64 or 256
   const uint32_t tiles = (uint32_t)((N + width - 1) / width), bm = blockIdx.x / tiles, bn = blockIdx.x - bm * tiles;
@@ -34,9 +36,14 @@ __global__ __launch_bounds__(256) void pool_finish_kernel(PoolView p, const floa
   const int64_t nc = min(n, N - 1);
   constexpr int kR = TB == 1 ? 64 : 32, kP = TB == 1 ? 8 : TB == 2 ? 4 : 2;
   const uint32_t quads = (uint32_t)(mt * GR) / 4;
-  u32x4_t tv = u32x4_t{0u, 0u, 0u, 0u};
-  const u32x4_t* t4 = reinterpret_cast<const u32x4_t*>(T + m0 * GR);
-  if (threadIdx.x < quads) tv = t4[threadIdx.x];
+  // T: four of a row at a time, its parts in order
+  auto load_t = [&](uint32_t e, float4 (&v)[kMaxSlices]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < kMaxSlices; ++k)
+      if (LINE || k == 0) v[k] = *reinterpret_cast<const float4*>(T + ((int64_t)min(k, slices - 1) * M + m0) * GR + 4 * e);
+  };
+  float4 tv[kMaxSlices];
+  if (threadIdx.x < quads) load_t(threadIdx.x, tv);
   // the slots of the tokens, and those not yet done
   int a[TB];
   uint32_t left = 0u;
@@ -76,8 +83,20 @@ __global__ __launch_bounds__(256) void pool_finish_kernel(PoolView p, const floa
   };
 #pragma unroll
   for (int g = 0; g < G; ++g) load_parts(g, 0);
-  if (threadIdx.x < quads) *reinterpret_cast<u32x4_t*>(ts + 4 * threadIdx.x) = tv;
-  for (uint32_t e = threadIdx.x + width; e < quads; e += width) *reinterpret_cast<u32x4_t*>(ts + 4 * e) = t4[e];
+  auto put_t = [&](uint32_t e, const float4 (&v)[kMaxSlices]) __attribute__((always_inline)) {
+    float4 t = v[0];
+#pragma unroll
+    for (int k = 1; k < kMaxSlices; ++k)
+      if (LINE && k < slices) t = make_float4(t.x + v[k].x, t.y + v[k].y, t.z + v[k].z, t.w + v[k].w);
+    *reinterpret_cast<float4*>(ts + 4 * e) = make_float4(t.x * scale, t.y * scale, t.z * scale, t.w * scale);
+    if (U && bn == 0)
+      *reinterpret_cast<uint2*>(U + m0 * GR + 4 * e) = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+  };
+  if (threadIdx.x < quads) put_t(threadIdx.x, tv);
+  for (uint32_t e = threadIdx.x + width; e < quads; e += width) {
+    load_t(e, tv);
+    put_t(e, tv);
+  }
 #pragma unroll
   for (int g = 0; g < G; ++g) {
 #pragma unroll
@@ -141,13 +160,13 @@ __global__ __launch_bounds__(256) void pool_finish_kernel(PoolView p, const floa
 
 // After a streamed product a thread takes as few tokens as fill the card.
 hipError_t launch_pool_finish(const PoolView& p, const float* part, int splits, const int32_t* counts,
-                              const StreamLine* line, int64_t M, int64_t N, const float* T, int act, bf16_t* Y,
-                              bf16_t* GU, hipStream_t st) {
+                              const StreamLine* line, int64_t M, int64_t N, const float* T, int slices, float scale,
+                              bf16_t* U, int act, bf16_t* Y, bf16_t* GU, hipStream_t st) {
   const int64_t tiles = (N + 255) / 256;
   const unsigned width = tiles * M < 1024 ? 64 : 256;
   auto go = [&](auto* fn, int tb) {
-    hipLaunchKernelGGL(fn, dim3((unsigned)((N + width - 1) / width * ((M + tb - 1) / tb))), dim3(width), 0, st, p, part, splits, counts,
-                       line ? *line : StreamLine{}, M, N, T, act, Y, GU);
+    hipLaunchKernelGGL(fn, dim3((unsigned)((N + width - 1) / width * ((M + tb - 1) / tb))), dim3(width), 0, st, p, part, splits,
+                       counts, line ? *line : StreamLine{}, M, N, T, slices, scale, U, act, Y, GU);
     return hipGetLastError();
   };
   const int tb = !line ? 8 : tiles * M >= 4 * 1024 ? 4 : tiles * M >= 2 * 1024 ? 2 : 1;

@@ -1,16 +1,16 @@
 // stream.hip -- the frozen product of few tokens, X deq(W_g)^T for G 4-bit
 // weights side by side, as fp32 parts; the adapters and what follows are the
-// next launch's (pool.hip).  Their first half, scale_a A_a x, is done by the same
-// launch.
+// next launch's (pool.hip).  Their first half, A_a x, is done by the same launch.
 //
 // A weight enters the product as the value that it stands for, RNE_bf16(RN32(L
 // t)): the sums have no other error than fp32's.
 //
 //   * Work.  A unit is 256 rows of the stack by 256 columns (a span), for 16 NT
-//     tokens.  The units, tile by tile, and the adapters' tasks before them lie
-//     on a line that the workgroups share out evenly (StreamLine): each writes
-//     one part for each tile that its stretch touches, and a tile's parts are
-//     those of consecutive workgroups.  Two workgroups share a CU.
+//     tokens.  The units lie on a line, tile by tile, that the workgroups share
+//     out evenly (StreamLine): each writes one part for each tile that its stretch
+//     touches, and a tile's parts are those of consecutive workgroups.  Two
+//     workgroups share a CU.  The adapters' tasks go to workgroups that have fewer
+//     units, or none, before these.
 //   * Codes.  Eight waves take two sets of 16 rows each.  Of a set's span a lane
 //     loads 16 bytes twice, each load over eight whole 128-byte lines (loads over
 //     sixteen rows stall in the vector L1's address translation); an exchange
@@ -28,6 +28,7 @@
 //   * x in LDS, a span or half of one at a time, the next one's loads and stores
 //     beside the products, one barrier each.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "downs.h"
@@ -61,10 +62,9 @@ struct StreamArgs {
   int32_t* counts;        // parts of each tile
   int G, codebook[2], absfmt[2];
   StreamLine line;
-  PoolView pool;          // R > 0: T [M x G R], U
-  int tt;                 // tokens of a task
+  PoolView pool;          // R > 0: T
+  StreamDowns downs;
   float* T;
-  bf16_t* U;
 };
 
 __device__ __forceinline__ f32x4_t mfma16x16x32(const bf16x8_t& a, const bf16x8_t& b, const f32x4_t& c) {
@@ -102,16 +102,17 @@ __global__ __launch_bounds__(kThreads, kSimdWaves<NT>) void stream_kernel(Stream
   const StreamLine& L = p.line;
   const uint32_t wg = blockIdx.x;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6, c = lane & 15, g = lane >> 4;
-  {
-    float* red = reinterpret_cast<float*>(smem);
-    const bool alone = wg >= L.wgs;   // a workgroup for one task
-    const uint32_t i0 = alone ? wg - L.wgs : L.task(wg), i1 = alone ? i0 + 1 : L.task(wg + 1);
-    uint32_t turn = 0;
-    for (uint32_t i = i0; i < i1; ++i)
-      turn += p.tt == 1 ? pool_down<kWaves, 1>(p.pool, p.X, p.M, p.K, p.T, p.U, i, turn, red)
-                        : pool_down<kWaves, 4>(p.pool, p.X, p.M, p.K, p.T, p.U, i, turn, red);
-    if (alone) return;
-    if (turn > 0) lds_barrier();   // the last task's sums have been read
+  if (p.downs.tasks > 0) {
+    const int at = p.downs.index(L, wg);
+    if (at >= 0)
+      for (uint32_t i = (uint32_t)__builtin_amdgcn_readfirstlane(w) * p.downs.wgs + (uint32_t)at; i < p.downs.tasks;
+           i += kWaves * p.downs.wgs) {
+        if (p.downs.tt == 1)
+          pool_down<1>(p.pool, p.X, p.M, p.K, p.T, i, p.downs.slices, p.downs.cols);
+        else
+          pool_down<4>(p.pool, p.X, p.M, p.K, p.T, i, p.downs.slices, p.downs.cols);
+      }
+    if (wg >= L.wgs) return;
   }
   const uint32_t u0 = L.unit(wg), u1 = L.unit(wg + 1);
   const int64_t K = p.K, N = p.N;
@@ -378,41 +379,62 @@ StreamPlan stream_plan(int64_t N, int64_t K, int64_t M, int G, int R) {
   L.tiles = (uint32_t)((N + kStreamRows - 1) / kStreamRows);
   L.spans = (uint32_t)((K + kSpan - 1) / kSpan);
   L.block = 16 * s.nt;
-  const uint32_t units = L.tiles * (uint32_t)G * (uint32_t)((M + L.block - 1) / L.block) * L.spans;
-  const uint32_t slots = s.nt == 4 ? 256 : 512;
-  L.wgs = std::min<uint32_t>(slots, units);
-  // (units are below 2^21: G N K and M K below 2^31, M at most 64)
-  s.tt = pool_down_tasks(G * R, M, 1) > (int)slots ? 4 : 1;
-  L.downs = R > 0 ? (uint32_t)pool_down_tasks(G * R, M, s.tt) : 0;
-  L.down_cost = 10;   // about a unit and a quarter
-  s.alone = 0;
-  // tasks in workgroups of their own where there is room, or where those that are
-  // left need no more units each
-  if (L.downs <= slots / 4 && (units + slots - 1) / slots == (units + slots - L.downs - 1) / (slots - L.downs))
-    L.wgs = std::min<uint32_t>(slots - L.downs, units), s.alone = (int)L.downs, L.downs = 0;
-  L.cost = L.downs * L.down_cost + units * kUnitCost;
-  if (L.downs > L.wgs || L.cost / L.wgs < L.down_cost + 2 * kUnitCost) L.down_cost = 0, L.cost = units * kUnitCost;
-  L.wgs = std::min<uint32_t>(L.wgs, 0xFFFFFFFFu / std::max(L.cost, L.downs));   // products in 32 bits
-  if (L.downs > L.wgs) L.down_cost = 0, L.cost = units * kUnitCost;
-  const uint32_t least = (L.cost / L.wgs - L.down_cost) / kUnitCost;
+  // (below 2^21: G N K and M K below 2^31, M at most 64)
+  L.units = L.tiles * (uint32_t)G * (uint32_t)((M + L.block - 1) / L.block) * L.spans;
+  L.wgs = std::min<uint32_t>(s.nt == 4 ? 256 : 512, L.units);
+  const uint32_t least = L.units / L.wgs;
   s.slots = (int)((L.spans + least - 2) / least + 1);
-  s.all_tiles = (int)(units / L.spans);
+  s.all_tiles = (int)(L.units / L.spans);
+  // The tasks go where they cost least: a task takes about `per` + 3 turns of 512
+  // columns, a unit ten of them, and what fits beside the other workgroups' units
+  // is free.
+  StreamDowns& d = s.downs;
+  d.slices = 1, d.least = least;
+  if (R > 0) {
+    const uint32_t most = s.nt == 4 ? 256 : 512;
+    const int64_t rows = (K + 511) / 512;
+    d.tt = pool_down_tasks(G * R, M, 1) > (int64_t)kWaves * most ? 4 : 1;
+    const int64_t n = pool_down_tasks(G * R, M, d.tt);
+    const uint32_t rest = L.units % L.wgs, wgs[3] = {most - L.wgs, rest > 0 ? L.wgs - rest : 0, L.wgs};
+    const int64_t free[3] = {10 * (int64_t)least, 10, 0};
+    int64_t best = INT64_MAX;
+    for (int c = 0; c < 3; ++c) {
+      const int64_t waves = (int64_t)kWaves * wgs[c];
+      if (waves == 0) continue;
+      const int64_t want = std::max<int64_t>(1, std::min(std::min<int64_t>(kMaxSlices, rows), waves / n));
+      const int64_t per = (rows + want - 1) / want, slices = (rows + per - 1) / per, tasks = n * slices;
+      const int64_t cost = std::max<int64_t>(0, (tasks + waves - 1) / waves * (per + 3) - free[c]);
+      if (cost >= best) continue;
+      best = cost;
+      d.where = (StreamTasks)c, d.wgs = (uint32_t)std::min<int64_t>(wgs[c], tasks);
+      d.slices = (uint32_t)slices, d.cols = (uint32_t)(512 * per), d.tasks = (uint32_t)tasks;
+      if (c != kTasksApart) d.wgs = wgs[c];
+    }
+  }
   return s;
 }
 
 hipError_t launch_stream(const Nf4View* W, const bf16_t* X, int64_t M, const PoolView& pool, const StreamPlan& s, float* T,
-                         bf16_t* U, float* part, int32_t* counts, hipStream_t st) {
+                         float* part, int32_t* counts, hipStream_t st) {
   StreamArgs a{};
   for (int g = 0; g < pool.G; ++g) {
     a.w.codes[g] = W[g].codes, a.w.absmax_q[g] = W[g].absmax_q, a.w.group_scale[g] = W[g].group_scale;
     a.codebook[g] = W[g].codebook, a.absfmt[g] = W[g].absfmt;
   }
   a.N = W[0].N, a.K = W[0].K, a.M = M, a.X = X, a.part = part, a.counts = counts, a.G = pool.G;
-  a.line = s.line, a.pool = pool, a.tt = s.tt, a.T = T, a.U = U;
+  a.line = s.line, a.pool = pool, a.downs = s.downs, a.T = T;
+  // the kernel's table is addressed from 0: the compiler may have put nothing there
+  static std::atomic<uint32_t> looked{0u};
   auto go = [&](auto* fn, int lds) {
-    const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
+    hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(fn, dim3(s.line.wgs + s.alone), dim3(kThreads), lds, st, a);
+    if (!(looked.load(std::memory_order_relaxed) & (uint32_t)s.nt)) {
+      hipFuncAttributes at{};
+      if ((e = hipFuncGetAttributes(&at, reinterpret_cast<const void*>(fn))) != hipSuccess) return e;
+      if (at.sharedSizeBytes != 0) return hipErrorInvalidKernelFile;
+      looked.fetch_or((uint32_t)s.nt, std::memory_order_relaxed);
+    }
+    hipLaunchKernelGGL(fn, dim3(s.line.wgs + (s.downs.where == kTasksApart ? s.downs.wgs : 0)), dim3(kThreads), lds, st, a);
     return hipGetLastError();
   };
   return s.nt == 1   ? go(&stream_kernel<1>, XShape<1>::kLds)
