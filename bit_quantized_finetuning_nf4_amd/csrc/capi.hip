@@ -366,11 +366,15 @@ BwdLayout group_bwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, int32_t G
 
 // A gated block and the adapters of many requests: G weights N x K (1, or gate
 // and up) side by side, adapters of rank R for each (0: none).
-// Three ways, by the number of tokens: the codes streamed (up to kStreamTokens);
-// the weights dequantized, and the product in small tiles whose
-// sums the adapters join in a pass of their own; or (dense) in 256-token tiles
-// that take it all.
-constexpr int64_t kStreamTokens = 64;
+// Three ways, by the number of tokens: the codes streamed, once for every 64
+// tokens (up to kStreamTokens); the weights dequantized, and the product in small
+// tiles whose sums the adapters join in a pass of their own; or (dense) in
+// 256-token tiles that take it all.
+// Streamed and dequantized, kernels' times: two weights of 22016 x 8192 with 128
+// tokens 215 and 485 us, 256 tokens 395 and 530; 8192 x 8192 47 and 100, 81 and
+// 104; two of 11008 x 4096 63 and 110, 108 and 112.  With 320 tokens the two meet
+// (104 and 113, 134 and 133).
+constexpr int64_t kStreamTokens = 256;
 enum PoolPath { kPoolStream, kPoolTiles, kPoolDense };
 PoolPath pool_path(int64_t M, int64_t N, int64_t K, int32_t G) {
   if (M <= kStreamTokens) return kPoolStream;
