@@ -165,20 +165,21 @@ hipError_t launch_pool_finish(const PoolView& p, const float* part, int splits, 
   const int64_t tiles = (N + 255) / 256;
   const unsigned width = tiles * M < 1024 ? 64 : 256;
   auto go = [&](auto* fn, int tb) {
-    hipLaunchKernelGGL(fn, dim3((unsigned)((N + width - 1) / width * ((M + tb - 1) / tb))), dim3(width), 0, st, p, part, splits,
-                       counts, line ? *line : StreamLine{}, M, N, T, slices, scale, U, act, Y, GU);
+    hipLaunchKernelGGL(fn, dim3((unsigned)((N + width - 1) / width * ((M + tb - 1) / tb))), dim3(width), 0, st, p, part,
+                       splits, counts, line ? *line : StreamLine{}, M, N, T, slices, scale, U, act, Y, GU);
     return hipGetLastError();
   };
-  const int tb = !line ? 8 : tiles * M >= 4 * 1024 ? 4 : tiles * M >= 2 * 1024 ? 2 : 1;
+  const int64_t work = tiles * M / 1024;
+  if (!line) return p.G == 1 ? go(&pool_finish_kernel<1, 8, false>, 8) : go(&pool_finish_kernel<2, 8, false>, 8);
   if (p.G == 1)
-    return tb == 8   ? go(&pool_finish_kernel<1, 8, false>, 8)
-           : tb == 4 ? go(&pool_finish_kernel<1, 4, true>, 4)
-           : tb == 2 ? go(&pool_finish_kernel<1, 2, true>, 2)
-                     : go(&pool_finish_kernel<1, 1, true>, 1);
-  return tb == 8   ? go(&pool_finish_kernel<2, 8, false>, 8)
-         : tb == 4 ? go(&pool_finish_kernel<2, 4, true>, 4)
-         : tb == 2 ? go(&pool_finish_kernel<2, 2, true>, 2)
-                   : go(&pool_finish_kernel<2, 1, true>, 1);
+    return work >= 8   ? go(&pool_finish_kernel<1, 8, true>, 8)
+           : work >= 4 ? go(&pool_finish_kernel<1, 4, true>, 4)
+           : work >= 2 ? go(&pool_finish_kernel<1, 2, true>, 2)
+                       : go(&pool_finish_kernel<1, 1, true>, 1);
+  return work >= 8   ? go(&pool_finish_kernel<2, 8, true>, 8)
+         : work >= 4 ? go(&pool_finish_kernel<2, 4, true>, 4)
+         : work >= 2 ? go(&pool_finish_kernel<2, 2, true>, 2)
+                     : go(&pool_finish_kernel<2, 1, true>, 1);
 }
 
 }  // namespace qlora
