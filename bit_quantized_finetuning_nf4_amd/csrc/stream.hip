@@ -91,7 +91,7 @@ __device__ __forceinline__ float q8_fast(uint32_t byte) {
   return fmaf(fmaf(-255.0f, r, q), c, r);
 }
 
-// Waves a SIMD: four, or two with the registers to read a step ahead.
+// Waves a SIMD: four, or two with the registers to read ahead.
 template <int NT>
 constexpr int kSimdWaves = NT == 4 ? 2 : 4;
 
@@ -243,14 +243,10 @@ __global__ __launch_bounds__(kThreads, kSimdWaves<NT>) void stream_kernel(Stream
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[k][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   uint32_t stage = 0;
-  // Two waves a SIMD: a step's table and x reads one step ahead.  Four: a set's at
-  // a time, the other waves hide their latency.
+  // Two waves a SIMD: the table and x read one set ahead of the products.  Four: a
+  // set's at a time, the other waves hide their latency.
   constexpr bool kAhead = kSimdWaves<NT> == 2;
   constexpr uint32_t kSel[4] = {0x0C0C0400u, 0x0C0C0500u, 0x0C0C0600u, 0x0C0C0700u};
-  struct Step {
-    u32x2_t l[kSets][4];
-    bf16x8_t x[NT];
-  } step[kAhead ? 2 : 1];
 
   for (uint32_t u = u0; u < u1; ++u) {
     const At here = at;
@@ -296,20 +292,6 @@ __global__ __launch_bounds__(kThreads, kSimdWaves<NT>) void stream_kernel(Stream
       if (leave || (at.s & 3u) == 0) load_scales(at.s >> 2);
     }
     __builtin_amdgcn_sched_barrier(0);
-    auto read_x = [&](Step& r, int d, uint32_t xb) __attribute__((always_inline)) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        r.x[n] = __builtin_bit_cast(bf16x8_t, *(const lds_u128*)(size_t)(xa[d] + xb + 16u * n * S::kRow));
-    };
-    auto read_l = [&](Step& r, int k, int j, int d) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r.l[k][i] = *(const lds_u64*)(size_t)perm(V[k][j][d], col, kSel[i]);
-    };
-    auto read = [&](Step& r, int j, int d, uint32_t xb) __attribute__((always_inline)) {
-      read_x(r, d, xb);
-#pragma unroll
-      for (int k = 0; k < kSets; ++k) read_l(r, k, j, d);
-    };
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (S::kCols < kSpan || j == 0) {
@@ -319,22 +301,38 @@ __global__ __launch_bounds__(kThreads, kSimdWaves<NT>) void stream_kernel(Stream
         ++stage;
       }
       const uint32_t xb = ((stage - 1) & 1) * S::kBytes + (S::kCols == kSpan ? 256u * j : 0u);
+      bf16x8_t x[kAhead ? 2 : 1][NT];
+      u32x2_t l[kAhead ? 2 : kSets][4];
+      auto read_x = [&](int d) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          x[kAhead ? d & 1 : 0][n] = __builtin_bit_cast(bf16x8_t, *(const lds_u128*)(size_t)(xa[d] + xb + 16u * n * S::kRow));
+      };
+      auto read_l = [&](int d, int k) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[kAhead ? k & 1 : k][i] = *(const lds_u64*)(size_t)perm(V[k][j][d], col, kSel[i]);
+      };
+      if constexpr (kAhead) {
+        read_x(0);
+        read_l(0, 0);
+      }
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        Step& cur = kAhead ? step[d & 1] : step[0];
-        if constexpr (kAhead) {
-          if (d == 0) read(cur, j, d, xb);
-          if (d < 3) read(step[(d + 1) & 1], j, d + 1, xb);
-        } else {
-          read_x(cur, d, xb);
-        }
+        if constexpr (!kAhead) read_x(d);
 #pragma unroll
         for (int k = 0; k < kSets; ++k) {
-          if constexpr (!kAhead) read_l(cur, k, j, d);
-          if (!kAhead || k == 0) __builtin_amdgcn_sched_barrier(0);
-          const bf16x8_t b = weights8(cur.l[k], ts[k][j]);
+          if constexpr (!kAhead) {
+            read_l(d, k);
+          } else if (k + 1 < kSets) {
+            read_l(d, k + 1);
+          } else if (d < 3) {
+            read_x(d + 1);
+            read_l(d + 1, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          const bf16x8_t b = weights8(l[kAhead ? k & 1 : k], ts[k][j]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) acc[k][n] = mfma16x16x32(cur.x[n], b, acc[k][n]);
+          for (int n = 0; n < NT; ++n) acc[k][n] = mfma16x16x32(x[kAhead ? d & 1 : 0][n], b, acc[k][n]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }

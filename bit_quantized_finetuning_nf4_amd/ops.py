@@ -275,8 +275,9 @@ def _whole(q: QuantizedWeight, like):
     for t, dtype, n, name in ((q.codes, torch.uint8, -(-q.rows * q.cols // 2), "codes"),
                               (q.absmax_q, torch.uint8, blocks, "absmax_q"),
                               (q.group_scale, torch.float32, -(-blocks // GROUP_BLOCKS), "group_scale")):
-        _beside(_need(t, dtype, name), like, name)
-        if t.numel() < n:
+        if (t is None or not t.is_cuda or t.dtype != dtype or t.device != like.device or not t.is_contiguous() or
+                t.numel() < n):
+            _beside(_need(t, dtype, name), like, name)
             raise ValueError(f"{name} holds {t.numel()} elements, a {q.rows} x {q.cols} weight has {n}")
 
 
