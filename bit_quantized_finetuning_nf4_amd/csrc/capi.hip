@@ -368,8 +368,8 @@ BwdLayout group_bwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, int32_t G
 // and up) side by side, adapters of rank R for each (0: none).
 // Three ways, by the number of tokens: the codes streamed, once for every 64
 // tokens (up to kStreamTokens); the weights dequantized, and the product in small
-// tiles whose sums the adapters join in a pass of their own; or (dense) in
-// 256-token tiles that take it all.
+// tiles, or in splits, whose sums the adapters join in a pass of their own; or
+// (dense) in 256-token tiles that take it all.
 // Streamed and dequantized, kernels' times: two weights of 22016 x 8192 with 128
 // tokens 215 and 485 us, 256 tokens 395 and 530; 8192 x 8192 47 and 100, 81 and
 // 104; two of 11008 x 4096 63 and 110, 108 and 112.  With 320 tokens the two meet
@@ -403,8 +403,7 @@ PoolLayout pool_layout(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
     L.wd = L.counts = align_up(mr * 2 * kTermParts);
     L.part = L.wd + align_up((size_t)pool_stack_rows(N, G) * (size_t)K * 2);
     L.total = L.part;
-    if (R > 0)
-      L.total += align_up(std::max(pool_u_part_bytes(M, K, G * R), xat_part_bytes(M, K, G * R)));
+    if (R > 0) L.total += align_up(std::max(pool_u_part_bytes(M, K, G * R), xat_part_bytes(M, K, G * R)));
   }
   return L;
 }
@@ -414,7 +413,7 @@ bool pool_sizes_ok(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
   if (M <= 0 || N <= 0 || K <= 0 || G < 1 || R < 0 || R > kMaxRank) return false;
   if (N > (int64_t)1 << 30 || pool_stack_rows(N, G) > (int64_t)0x7FFFFFFF / K || M > (int64_t)0x7FFFFFFF / K || M > (int64_t)0x7FFFFFFF / G / N) return false;
   if (G == 2 && (N + 15) / 16 > 65535) return false;   // the stack's dequantization
-  return R == 0 || (M <= ((int64_t)1 << 27) / (G * R) && N < ((int64_t)1 << 30) / R && skinny_cols_ok(K));
+  return R == 0 || (pool_term_ok(M, N, R, G) && skinny_cols_ok(K));
 }
 qlora_status check_pool_sizes(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
   if (M <= 0 || M > 0x7FFFFFFF) return QLORA_E_SHAPE;
@@ -422,7 +421,7 @@ qlora_status check_pool_sizes(int64_t M, int64_t N, int64_t K, int32_t R, int32_
 }
 
 struct GatedBwdLayout {
-  size_t g, u, part, dy, wdt, split, split_bytes, total;
+  size_t g, u, part, at, dy, wdt, split, split_bytes, total;
 };
 int64_t up32(int64_t n) { return (n + 31) / 32 * 32; }
 GatedBwdLayout gated_bwd_layout(int64_t M, int64_t F, int64_t K, int32_t r, bool with_dx) {
@@ -431,8 +430,9 @@ GatedBwdLayout gated_bwd_layout(int64_t M, int64_t F, int64_t K, int32_t r, bool
   if (r > 0) {
     L.u = align_up((size_t)M * 2 * r * 2 * kGradParts);
     L.part = L.u + align_up((size_t)M * 2 * r * 2);
-    L.dy = L.part + align_up(std::max(std::max(skinny_partial_bytes(M, 2 * r, K, kXAt), group_dyb_part_bytes(M, F, r, 2)),
+    L.at = L.part + align_up(std::max(std::max(skinny_partial_bytes(M, 2 * r, K, kXAt), group_dyb_part_bytes(M, F, r, 2)),
                                       group_grads_part_bytes(M, F, K, r, 2)));
+    L.dy = L.at + align_up((size_t)K * 2 * r * 2);
   }
   if (r > 0 || with_dx) L.total = L.wdt = L.dy + align_up((size_t)M * (size_t)(2 * fp) * 2);
   if (with_dx) {
@@ -441,6 +441,15 @@ GatedBwdLayout gated_bwd_layout(int64_t M, int64_t F, int64_t K, int32_t r, bool
     L.total = L.split + align_up(L.split_bytes);
   }
   return L;
+}
+// Splits of dX's product in 256-token tiles (1: none), or 0 where other tiles are better.
+int dx_splits(int64_t M, int64_t N, int64_t K, size_t part_bytes) {
+  const int cus = device_cu_count();
+  const TileChoice c = choose_tile(M, N, K / 64, cus, part_bytes);
+  if (c.tm != 256) return 0;
+  if (c.splits > 1) return c.splits;
+  const int n = dense_splits(N, K, M, cus);
+  return n > 1 && part_bytes >= (size_t)n * (size_t)M * (size_t)N * sizeof(float) ? n : 1;
 }
 bool gated_bwd_ok(int64_t M, int64_t F, int64_t K, int32_t r) {
   if (M <= 0 || F <= 0 || K <= 0 || r < 0 || r > kMaxRank || F > 0x3FFFFFF) return false;
@@ -1250,10 +1259,10 @@ qlora_status run_pool(const qlora_nf4_weight* W, const PoolView& p, const PoolLa
                           : start_xat_parts(X, p.A, M, K, p.G * p.R, part, U, Tparts, Tfull, p.s, &rest, s));
     if (st != QLORA_OK) return st;
   }
-  const int64_t turn = dense ? pool_turn(N, M, 2) : N;
-  st = hip_status(p.G == 2 ? launch_dequant_pair(v, (int)turn, Wd, rest, s) : launch_dequant_ride(v[0], Wd, rest, s));
+  const int turn = dense ? (int)kPoolTurn : (int)N;
+  st = hip_status(p.G == 2 ? launch_dequant_pair(v, turn, Wd, rest, s) : launch_dequant_ride(v[0], Wd, rest, s));
   if (st != QLORA_OK) return st;
-  if (dense) return hip_status(launch_pool_gemm(PoolGemm{Wd, N, K, M, X, Tparts, p, act, Y, GU}, s));
+  if (dense) return hip_status(launch_pool_gemm(PoolGemm{Wd, N, K, M, X, Tparts, p, act, Y, GU, nullptr, 1}, s));
   int splits = 1;
   if ((st = hip_status(launch_product_parts(Wd, p.G * N, K, X, M, part, &splits, s))) != QLORA_OK) return st;
   return hip_status(launch_pool_finish(p, part, splits, nullptr, nullptr, M, N, T, 1, 1.0f, nullptr, act, Y, GU, s));
@@ -1356,7 +1365,10 @@ qlora_status qlora_gated_bwd(const qlora_nf4_weight* W, const uint16_t* X, const
     if ((st = hip_status(launch_xat(X, A, M, K, 2 * r, part, Ud, nullptr, 1.0f, s))) != QLORA_OK) return st;
     U = Ud;
   }
-  if ((st = hip_status(launch_gated_grad(dH, GU, M, F, fp, act, dY, WdT, K, s))) != QLORA_OK) return st;
+  // dX in 256-token tiles: their term takes A^T
+  const int tiles = dX && (r == 0 || pool_term_ok(M, K, 2 * r, 1)) ? dx_splits(M, K, 2 * fp, L.split_bytes) : 0;
+  bf16_t* At = tiles > 0 && r > 0 ? reinterpret_cast<bf16_t*>(ws_at(ws, L.at)) : nullptr;
+  if ((st = hip_status(launch_gated_grad(dH, GU, M, F, fp, act, dY, WdT, K, A, 2 * r, At, s))) != QLORA_OK) return st;
   Ride rest{};
   rest.kind = kRideSum3;
   if (r > 0 && (st = hip_status(start_dyb_parts_group(dY, 2 * fp, B, M, F, r, 2, part, G3, sc, &rest, s))) != QLORA_OK)
@@ -1366,10 +1378,18 @@ qlora_status qlora_gated_bwd(const qlora_nf4_weight* W, const uint16_t* X, const
   if (dX) {
     const Nf4View v[2] = {view(&W[0]), view(&W[1])};
     if ((st = hip_status(launch_dequant_t_pair(v, WdT, fp, rest, s))) != QLORA_OK) return st;
-    if ((st = hip_status(launch_staged(WdT, K, 2 * fp, dY, M, r > 0 ? G3 : nullptr, r > 0 ? A : nullptr, true, 2 * r,
-                                       nullptr, dX, s, reinterpret_cast<float*>(ws_at(ws, L.split)), L.split_bytes,
-                                       r > 0 ? &left : nullptr))) != QLORA_OK)
-      return st;
+    float* split = reinterpret_cast<float*>(ws_at(ws, L.split));
+    if (tiles > 0) {
+      const PoolView term{nullptr, At, nullptr, nullptr, nullptr, 1.0f, 1, 2 * r, 1};
+      left = SplitSum{split, tiles > 1 ? tiles : 0, M * K, dX};
+      st = hip_status(launch_pool_gemm(
+          PoolGemm{WdT, K, 2 * fp, M, dY, G3, term, act, dX, nullptr, tiles > 1 ? split : nullptr, tiles}, s));
+      if (st == QLORA_OK && r == 0 && tiles > 1) st = hip_status(launch_split_sum(split, tiles, M * K, dX, s));
+    } else {
+      st = hip_status(launch_staged(WdT, K, 2 * fp, dY, M, r > 0 ? G3 : nullptr, r > 0 ? A : nullptr, true, 2 * r, nullptr,
+                                    dX, s, split, L.split_bytes, r > 0 ? &left : nullptr));
+    }
+    if (st != QLORA_OK) return st;
   }
   if (r == 0) return QLORA_OK;
   return hip_status(launch_adapter_grads_group(G3, X, dY, 2 * fp, fp, U, M, F, K, r, 2, part, dA, dB, sc, left, s));

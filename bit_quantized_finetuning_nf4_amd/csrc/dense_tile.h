@@ -314,6 +314,116 @@ __device__ __forceinline__ void dense_halves(char* smem, const DenseOps& f, type
   }
 }
 
+// The ring of half slots with 16 x 16 x 32 matrix instructions: a wave's 2 FI
+// fragments of 16 weight rows by 8 of 16 tokens, a stage of 32 columns at a time.
+// Slot X = 8 m + n of a stage is fragments (m, n).  Reads during a stage: at slot 0 its
+// own last weight fragment; from slot 8 on the next stage's: token fragments into
+// the other set, weight fragment m into the registers that slot 8 m + 7 was the
+// last to use.  The odd stage's slot 8 waits for the next pair.
+// The matrix units take as many cycles as with 32 x 32 x 16, but an accumulator is
+// read and written half as often a product, and what is not spent so is clock:
+// 4096 x 8192 x 22016 1155 -> 1073 us (1.80 and 1.85 million cycles), 4096 x 44032
+// x 8192 2250 -> 2095.
+struct Frags16 {
+  bf16x8_t a[8], b[2][8];
+};
+// c += a b in place, in accumulation registers: with the builtin the compiler moves
+// them about, 200 moves a pair.  It knows nothing of the instruction's latencies,
+// then: operands come from loads, or (READY false) an instruction may have written
+// them just before; what is not another product of c waits for mfma_done.
+template <bool READY = true>
+__device__ __forceinline__ void mfma_acc(const bf16x8_t& a, const bf16x8_t& b, f32x4_t& c) {
+  if constexpr (READY)
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  else
+    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mfma_done() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+template <int FI>
+constexpr int quad_off(int d) { return d * 32 * FI / (2 * FI + 8); }
+template <int FI>
+constexpr int quad_rd(int q) { return 8 + q * (16 * FI - 10) / 8; }
+template <int FI, int X, int HF>
+__device__ __forceinline__ void quad_slot(const Halves& c, const DenseOps& f, int pair, f32x4_t (&acc)[2 * FI][8], Frags16& F,
+                                          int am, int bm, const int (&o)[2]) {
+  constexpr int NA = 2 * FI, S = 8 * NA, m = X / 8, n = X % 8;
+  if constexpr (HF == 1 && X == 8) {
+    QLORA_WAIT(2 * FI, 0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  mfma_acc(F.a[m], F.b[HF][n], acc[m][n]);
+  if constexpr (X == 0) F.a[NA - 1] = rd16(c.s[0] + am + (NA - 1) * 16 * 128 + o[HF]);
+  constexpr int w = HF == 0 ? 0 : 2;   // the next stage's halves
+  if constexpr (n == 3 && m > 0) F.a[m - 1] = rd16(c.s[w] + am + (m - 1) * 16 * 128 + o[HF ^ 1]);
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (quad_rd<FI>(q) == X) F.b[HF ^ 1][q] = rd16(c.s[w + 1] + bm + q * 16 * 128 + o[HF ^ 1]);
+  constexpr int off = HF == 0 ? S - 8 + X : X < 8 ? 2 * S - 8 + X : X - 8;   // from the barrier on
+#pragma unroll
+  for (int d = 0; d < 2 * FI + 8; ++d)
+    if (quad_off<FI>(d) == off) {
+      if constexpr (HF == 1 && X >= 8)
+        group_dma<FI>(c.s[0], c.s[1], f, pair, d);
+      else
+        group_dma<FI>(c.s[3], c.s[4], f, pair - 1, d);
+    }
+  __builtin_amdgcn_sched_barrier(0);
+}
+template <int FI, int HF, int X>
+__device__ __forceinline__ void quad_slots(const Halves& c, const DenseOps& f, int pair, f32x4_t (&acc)[2 * FI][8], Frags16& F,
+                                           int am, int bm, const int (&o)[2]) {
+  if constexpr (X < 16 * FI) {
+    quad_slot<FI, X, HF>(c, f, pair, acc, F, am, bm, o);
+    quad_slots<FI, HF, X + 1>(c, f, pair, acc, F, am, bm, o);
+  }
+}
+// Loads of a group that come before its pair's last slot.
+template <int FI>
+constexpr int quads_before() {
+  int n = 0;
+  for (int d = 0; d < 2 * FI + 8; ++d) n += quad_off<FI>(d) < 16 * FI - 8;
+  return n;
+}
+// The whole loop, as dense_halves.
+template <int FI>
+__device__ __forceinline__ void dense_quads(char* smem, const DenseOps& f, f32x4_t (&acc)[2 * FI][8], int am, int bm,
+                                            const int (&o)[2]) {
+  Halves c;
+#pragma unroll
+  for (int q = 0; q < 5; ++q) c.s[q] = smem + q * kPairOp;
+#pragma unroll
+  for (int q = 0; q < 2 * FI; ++q) half_dma<FI>(c.s[0], f, true, 0, q);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) half_dma<FI>(c.s[1], f, false, 0, q);
+#pragma unroll
+  for (int q = 0; q < 2 * FI; ++q) half_dma<FI>(c.s[2], f, true, 1, q);
+  constexpr int kBefore = quads_before<FI>();
+#pragma unroll
+  for (int d = 0; d < kBefore; ++d) group_dma<FI>(c.s[3], c.s[4], f, -1, d);
+  QLORA_WAIT(2 * FI + kBefore, 0);   // pair 0 has landed
+  __builtin_amdgcn_s_barrier();
+  mfma_done();
+  Frags16 F;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (i < 2 * FI - 1) F.a[i] = rd16(c.s[0] + am + i * 16 * 128 + o[0]);
+    F.b[0][i] = rd16(c.s[1] + bm + i * 16 * 128 + o[0]);
+  }
+  for (int pr = 0; pr < f.npair; ++pr) {
+    __builtin_amdgcn_sched_barrier(0);
+    quad_slots<FI, 0, 0>(c, f, pr, acc, F, am, bm, o);
+    __builtin_amdgcn_sched_barrier(0);
+    quad_slots<FI, 1, 0>(c, f, pr, acc, F, am, bm, o);
+    c = Halves{{c.s[2], c.s[3], c.s[4], c.s[0], c.s[1]}};
+  }
+  mfma_done();
+}
+
 // One 32-wide chunk of the LoRA tail, in registers: the weight half
 // B'[row0 + row, j0 ..] (zero past the rank, and for rows outside [lo, hi))
 // and the token half T[trow0 + row, j0 + 8 c ..] (T is trows x rank with

@@ -14,14 +14,27 @@ namespace {
 
 // A thread takes eight columns of a token.  dY [M x 2 Fp], Fp = F rounded up to
 // 32: columns F .. Fp of both halves are zero, as are those of Wt [K x 2 Fp]
-// (may be null), whose contraction they pad.
+// (may be null), whose contraction they pad.  The last threads transpose A [r x K],
+// eight ranks of a column each.
 __global__ __launch_bounds__(256) void gated_grad_kernel(const bf16_t* __restrict__ dH, const bf16_t* __restrict__ GU,
                                                          int64_t M, int64_t F, int64_t Fp, int act,
-                                                         bf16_t* __restrict__ dY, bf16_t* __restrict__ Wt, int64_t K) {
+                                                         bf16_t* __restrict__ dY, bf16_t* __restrict__ Wt, int64_t K,
+                                                         const bf16_t* __restrict__ A, int r, bf16_t* __restrict__ At) {
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, per = Fp >> 3;
   if (id >= M * per) {
-    const int64_t z = id - M * per, pieces = (Fp - F) >> 3;
-    if (!Wt || z >= 2 * K * pieces) return;
+    const int64_t pieces = (Fp - F) >> 3, pads = Wt ? 2 * K * pieces : 0;
+    int64_t z = id - M * per;
+    if (z >= pads) {
+      z -= pads;
+      const int64_t j = z / K, k = z - j * K;
+      if (!At || j >= r / 8) return;
+      uint32_t v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = A[(8 * j + e) * K + k];
+      *reinterpret_cast<uint4*>(At + k * r + 8 * j) =
+          make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+      return;
+    }
     const int64_t k = z / (2 * pieces), q = z - k * 2 * pieces, half = q / pieces;
     *reinterpret_cast<uint4*>(Wt + k * 2 * Fp + half * Fp + F + 8 * (q - half * pieces)) = make_uint4(0u, 0u, 0u, 0u);
     return;
@@ -60,10 +73,10 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(const bf16_t* __restric
 }  // namespace
 
 hipError_t launch_gated_grad(const bf16_t* dH, const bf16_t* GU, int64_t M, int64_t F, int64_t Fp, int act, bf16_t* dY,
-                             bf16_t* Wt, int64_t K, hipStream_t st) {
-  const int64_t n = M * (Fp >> 3) + (Wt ? 2 * K * ((Fp - F) >> 3) : 0);
+                             bf16_t* Wt, int64_t K, const bf16_t* A, int r, bf16_t* At, hipStream_t st) {
+  const int64_t n = M * (Fp >> 3) + (Wt ? 2 * K * ((Fp - F) >> 3) : 0) + (At ? K * (r / 8) : 0);
   hipLaunchKernelGGL(gated_grad_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, dH, GU, M, F, Fp, act, dY,
-                     Wt, K);
+                     Wt, K, A, r, At);
   return hipGetLastError();
 }
 

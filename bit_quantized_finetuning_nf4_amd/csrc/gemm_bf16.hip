@@ -520,7 +520,7 @@ double staged_cost(int64_t N, int64_t K, int64_t M) { return choose_tile(M, N, K
 
 // The tiles of a product whose sums are left as fp32 parts, on a card of kSplitCus
 // CUs: the parts' number has to be the one that the caller sized its workspace
-// for.  Tiles of 256 tokens only in a split contraction.
+// for.  Tiles of 256 tokens only in a split contraction (gemm_pool.hip).
 namespace {
 TileChoice parts_tile(int64_t N, int64_t K, int64_t M) {
   const TileChoice c = choose_tile(M, N, K / 64, kSplitCus, (size_t)1 << 62);
@@ -538,9 +538,11 @@ hipError_t launch_product_parts(const bf16_t* Wd, int64_t N, int64_t K, const bf
                                 int* splits, hipStream_t st) {
   const TileChoice c = parts_tile(N, K, M);
   *splits = c.splits;
-  if (c.tm == 256)
-    return launch_fi<4>(Wd, N, K, X, M, nullptr, nullptr, false, 0, 0, N, 0.0f, nullptr, 0, N, st, kTailParts, nullptr,
-                        c.splits, part);
+  if (c.tm == 256) {
+    PoolGemm g{};
+    g.Wd = Wd, g.N = N, g.K = K, g.M = M, g.X = X, g.pool.G = 1, g.part = part, g.splits = c.splits;
+    return launch_pool_gemm(g, st);
+  }
   TileGemm t{};
   t.W = Wd, t.X = X, t.N = N, t.row_bytes = 2 * K, t.M = M, t.part = part, t.keep = true;
   return launch_tile(t, c, 0, N, st);

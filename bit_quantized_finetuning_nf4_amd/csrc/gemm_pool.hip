@@ -5,17 +5,19 @@
 //   Y = X Wd^T + T B^T          T = scale_a A_a x of the token's slot, B = B_a
 //   H = act(G) o P              of a block's two weights, both so
 //
-// Wd: the dequantized weight; of a gated block's two, rows in turns, gate then
-// up: of 32, where a wave's fragments come in pairs, 2 i and 2 i + 1 the same
-// features of both; of 16, where it has three, each half of both.  Either way
-// the two meet in a lane's registers.  The main loop is the dense GEMM's
-// (dense_tile.h): 256 x 64 FI tiles, both operands by buffer->LDS DMA.
+// Wd: the dequantized weight; of a gated block's two, 16 rows of gate and 16 of up
+// in turn: a wave's fragments 2 i and 2 i + 1 are the same features of both, and the
+// two meet in a lane's registers.  The main loop is dense_quads (dense_tile.h): 256 x
+// 64 FI tiles, both operands by buffer->LDS DMA.  A contraction in splits (of
+// one weight, with one adapter or none) leaves fp32 sums, the adapter's steps shared
+// out to the splits.
 //
 // The adapters' term follows from global memory, T as kTermParts bf16 parts: for
-// each slot among the tile's tokens the ranks 16 at a time, the next ones' loads in
+// each slot among the tile's tokens the ranks 32 at a time, the next ones' loads in
 // flight, the tokens of other slots zero.  Tokens of one slot next to each other
 // (prompts) make it one pass or two of a tile.
 #include <algorithm>
+#include <type_traits>
 
 #include "dense_tile.h"
 #include "gate.h"
@@ -24,11 +26,15 @@
 namespace qlora {
 namespace {
 
+__device__ __forceinline__ f32x4_t mfma16x16x32(const bf16x8_t& a, const bf16x8_t& b, const f32x4_t& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
 struct PoolGemmArgs {
   PoolGemm g;
   int64_t rows;            // of the stack
   int64_t n_begin;
-  int tiles_n, tiles_m;
+  int tiles_n, tiles_m, splits, pps;   // pps: pairs of a split
 };
 
 // The slots among TOKENS tokens from m0 on, each once, in the order of their
@@ -66,45 +72,21 @@ __device__ __forceinline__ int tile_slots(const PoolView& p, int64_t m0, int64_t
   return count;
 }
 
-// Rows of a turn of gate or up: see above.
-template <int FI>
-constexpr int kTurn = FI == 3 ? 16 : 32;
-
-// The tile's 256 rows of one result's 32 FI columns: value(f, j, e) of the wave's f-th
-// 16 features, e 0 .. 7: features 8 (e / 4) + 4 h + e % 4 of them.
-template <int FI, class F>
-__device__ __forceinline__ void store_half(const F& value, bf16_t* out, int64_t ld, int64_t rows, int64_t cols, int64_t row0,
-                                           int64_t col0, char* smem) {
-  constexpr int U = 8 * FI, SM = FI == 4 ? 31 : FI == 3 ? 7 : 15;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wr = w >> 1, wc = w & 1, lr = lane & 31, h = lane >> 5;
-  lds_free_for_output();
-#pragma unroll
-  for (int f = 0; f < FI; ++f)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        lds_put4<U, SM>(smem, wr * 128 + 32 * j + lr, wc * 4 * FI + 4 * f + 2 * q + h, value(f, j, 4 * q),
-                        value(f, j, 4 * q + 1), value(f, j, 4 * q + 2), value(f, j, 4 * q + 3));
-  __syncthreads();
-  lds_tile_out<U, SM>(smem, out, ld, rows, cols, row0, col0);
-}
-
 template <int FI, int G, bool POOL>
 __global__ __launch_bounds__(kThreads, 1) void pool_gemm_kernel(PoolGemmArgs p) {
-  constexpr bool kHalves = G == 2 && kTurn<FI> == 16;   // a fragment holds both weights' rows
   extern __shared__ __align__(16) char smem[];
   const PoolGemm& a = p.g;
   int tn, tm;
-  map_tile_grouped(xcd_tile_id(), p.tiles_n, p.tiles_m, tn, tm);
+  const int id = xcd_tile_id(), split = id / (p.tiles_n * p.tiles_m), p0 = split * p.pps;
+  map_tile_grouped(id - split * p.tiles_n * p.tiles_m, p.tiles_n, p.tiles_m, tn, tm);
   const int64_t n0 = p.n_begin + (int64_t)tn * 64 * FI, m0 = (int64_t)tm * kTile;
   const int64_t K = a.K, M = a.M, N = a.N;
-  const int t = threadIdx.x, lane = t & 63, wv = t >> 6, wr = wv >> 1, wc = wv & 1, lr = lane & 31, h = lane >> 5;
+  const int t = threadIdx.x, lane = t & 63, wv = t >> 6, wr = wv >> 1, wc = wv & 1, l16 = lane & 15, lg = lane >> 4;
 
   DenseOps f;
   f.w = __builtin_amdgcn_readfirstlane(wv);
   __builtin_assume(f.w >= 0 && f.w < 4);
-  f.npair = (int)(K >> 6);
+  f.npair = min((int)(K >> 6) - p0, p.pps);
   f.wr_ = make_rsrc(a.Wd, (uint32_t)(p.rows * K * 2));
   f.xr = make_rsrc(a.X, (uint32_t)(M * K * 2));
   {
@@ -113,108 +95,101 @@ __global__ __launch_bounds__(kThreads, 1) void pool_gemm_kernel(PoolGemmArgs p) 
     for (int q = 0; q < 8; ++q) {
       // rows past the end re-read the last row: never stored
       const int row = 8 * (4 * q + f.w) + (lane >> 3);
-      if (q < 2 * FI) f.wo[q] = (uint32_t)(min(n0 + row, p.rows - 1) * K * 2 + c * 16);
-      f.xo[q] = (uint32_t)(min(m0 + row, M - 1) * K * 2 + c * 16);
+      if (q < 2 * FI) f.wo[q] = (uint32_t)(min(n0 + row, p.rows - 1) * K * 2 + p0 * 128 + c * 16);
+      f.xo[q] = (uint32_t)(min(m0 + row, M - 1) * K * 2 + p0 * 128 + c * 16);
     }
   }
-  PairOffs po;
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) po.o[hf][kk] = pos128(lr, 4 * hf + 2 * kk + h);
+  const int o[2] = {pos128(l16, lg), pos128(l16, 4 + lg)};
   const int am = wc * 32 * FI * 128, bm = wr * 128 * 128;
-
-  f32x16_t acc[FI][4];
+  constexpr int NA = 2 * FI;
+  f32x4_t acc[NA][8];
 #pragma unroll
-  for (int i = 0; i < FI; ++i)
+  for (int i = 0; i < NA; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  Frags F;
-  dense_halves<MmBf16, FI>(smem, f, acc, F, am, bm, po);
+    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  dense_quads<FI>(smem, f, acc, am, bm, o);
   QLORA_WAIT(0, 0);   // the clamped re-loads still in flight
   __builtin_amdgcn_s_barrier();
 
   if (a.pool.R > 0) {
     const PoolView& pl = a.pool;
+    const int first = POOL ? 0 : 32 * split, step = 32 * p.splits;   // one adapter's steps go round the splits
     const int GR = G * pl.R;
     int* ids = reinterpret_cast<int*>(smem);
     int* list = ids + kTile;
     const int slots = POOL ? tile_slots<kTile>(pl, m0, M, ids) : 1;
-    int mine[4];   // the slots of the lane's tokens
+    int mine[8];   // the slots of the lane's tokens
 #pragma unroll
-    for (int j = 0; j < 4; ++j) mine[j] = POOL ? ids[128 * wr + 32 * j + lr] : (m0 + 128 * wr + 32 * j + lr < M ? 0 : -1);
+    for (int j = 0; j < 8; ++j) {
+      const int at = 128 * wr + 16 * j + l16;
+      mine[j] = POOL ? ids[at] : (m0 + at < M ? 0 : -1);
+    }
     // the lane's rows of B (of one weight) and of T: byte offsets, past the end zero
-    constexpr int FG = kHalves ? FI : FI / G;
+    constexpr int FG = NA / G;
     constexpr uint32_t kNone = 0x80000000u;   // and no array reaches it (M G R at most 2^27, N R below 2^30)
     static_assert(kTermParts == 2);
-    uint32_t brow[FG], trow[4];
+    uint32_t brow[FG], trow[8];
 #pragma unroll
     for (int i = 0; i < FG; ++i) {
-      const int64_t row = n0 + 32 * (FI * wc + (kHalves ? 1 : G) * i) + lr;
-      const int64_t n = G == 1 ? row : kHalves ? (row >> 5) * 16 + (lr & 15) : (row >> 6) * 32 + lr;
-      brow[i] = n < N ? (uint32_t)(n * pl.R + 8 * h) * 2u : kNone;
+      const int64_t row = n0 + 32 * FI * wc + 16 * G * i;
+      const int64_t n = (G == 1 ? row : row >> 1) + l16;
+      brow[i] = n < N ? (uint32_t)(n * pl.R + 8 * lg) * 2u : kNone;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) trow[j] = (uint32_t)(min(m0 + 128 * wr + 32 * j + lr, M - 1) * GR + 8 * h) * 2u;
+    for (int j = 0; j < 8; ++j) trow[j] = (uint32_t)(min(m0 + 128 * wr + 16 * j + l16, M - 1) * GR + 8 * lg) * 2u;
     const uint32_t part = (uint32_t)(M * GR) * 2u, bytes = (uint32_t)(N * pl.R) * 2u;
     const rsrc_t tr = make_rsrc(a.T, 2 * part);
-    // a step: 16 ranks of one weight's fragments
+    // a step: 32 ranks of one weight's fragments, by half of the tokens at a time
     u32x4_t b[2][FG], x[2][2][4];
-    auto load = [&](int set, int slot, int r, int g, int k0) __attribute__((always_inline)) {
+    auto load_b = [&](int t, int slot, int r, int g, int k0) __attribute__((always_inline)) {
       const rsrc_t br = make_rsrc(pl.B + ((int64_t)slot * G + g) * N * pl.R, bytes);
-      const bool in = k0 + 8 * h < r;
+      const bool in = k0 + 8 * lg < r;
 #pragma unroll
       for (int i = 0; i < FG; ++i)
-        b[set][i] = __builtin_bit_cast(
-            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(br, in && (!kHalves || lr >> 4 == g) ? brow[i] : kNone, 2 * k0, 0));
+        b[t][i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(br, in ? brow[i] : kNone, 2 * k0, 0));
+    };
+    auto load_x = [&](int h2, int slot, int r, int g, int k0) __attribute__((always_inline)) {
+      const bool in = k0 + 8 * lg < r;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t o = in && mine[j] == slot ? trow[j] : kNone;
+        const uint32_t at = in && mine[4 * h2 + j] == slot ? trow[4 * h2 + j] : kNone;
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          x[set][e][j] = __builtin_bit_cast(
-              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(tr, o, 2 * (k0 + g * pl.R) + (e ? part : 0u), 0));
+          x[h2][e][j] = __builtin_bit_cast(
+              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(tr, at, 2 * (k0 + g * pl.R) + (e ? part : 0u), 0));
       }
     };
     // Tokens of other slots have zeros, which an infinity or a NaN of this slot's B
     // would still reach.  A step that holds one, in a wave whose tokens are not all
     // the slot's, is left out and comes in a second turn, summed apart and given to
     // the slot's own tokens alone.
-    auto apart = [&](int set, bool mixed) __attribute__((always_inline)) {
+    auto apart = [&](int t, bool mixed) __attribute__((always_inline)) {
       bool found = false;
       if (POOL && mixed) {
 #pragma unroll
         for (int i = 0; i < FG; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            found |= (b[set][i][e] & 0x7F80u) == 0x7F80u || (b[set][i][e] & 0x7F800000u) == 0x7F800000u;
+            found |= (b[t][i][e] & 0x7F80u) == 0x7F80u || (b[t][i][e] & 0x7F800000u) == 0x7F800000u;
         found = __any(found);
       }
       return found;
     };
     bool again = false;
-    auto at = [](int i, int g) { return G == 1 || kHalves ? i : 2 * i + g; };
-    auto mul = [&](int set, int g, bool mixed) __attribute__((always_inline)) {
-      if (apart(set, mixed)) {
-        again = true;
-        return;
-      }
+    auto mul = [&](int t, int h2, int g) __attribute__((always_inline)) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int i = 0; i < FG; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            acc[at(i, g)][j] = mfma32x32x16(__builtin_bit_cast(bf16x8_t, b[set][i]),
-                                            __builtin_bit_cast(bf16x8_t, x[set][e][j]), acc[at(i, g)][j]);
+            mfma_acc<false>(__builtin_bit_cast(bf16x8_t, b[t][i]), __builtin_bit_cast(bf16x8_t, x[h2][e][j]), acc[G * i + g][4 * h2 + j]);
     };
     // Whether the wave has tokens of the slot, and others.
     auto present = [&](int slot, bool& mixed) __attribute__((always_inline)) {
       bool some = mine[0] == slot, all = some;
 #pragma unroll
-      for (int j = 1; j < 4; ++j) some = some || mine[j] == slot, all = all && mine[j] == slot;
+      for (int j = 1; j < 8; ++j) some = some || mine[j] == slot, all = all && mine[j] == slot;
       mixed = !__all(all);
       return (bool)__any(some);
     };
@@ -223,72 +198,106 @@ __global__ __launch_bounds__(kThreads, 1) void pool_gemm_kernel(PoolGemmArgs p) 
       bool mixed = false;
       if (POOL && !present(slot, mixed)) continue;
       const int r = POOL ? rank_of(pl, slot) : pl.R;
-      if (r == 0) continue;
-      load(0, slot, r, 0, 0);
-      for (int k0 = 0; k0 < r; k0 += G == 1 ? 32 : 16) {
-        load(1, slot, r, G - 1, G == 1 ? k0 + 16 : k0);
-        mul(0, 0, mixed);
-        load(0, slot, r, 0, G == 1 ? k0 + 32 : k0 + 16);
-        mul(1, G - 1, mixed);
-      }
+      if (first >= r) continue;
+      load_b(0, slot, r, 0, first);
+      load_x(0, slot, r, 0, first);
+      for (int k0 = first; k0 < r; k0 += step)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const int t = G == 1 ? 0 : g, gn = g + 1 < G ? g + 1 : 0, kn = g + 1 < G ? k0 : k0 + step;
+          load_x(1, slot, r, g, k0);
+          const bool skip = apart(t, mixed);
+          again = again || skip;
+          if (!skip) mul(t, 0, g);
+          if (G == 2) load_b(t ^ 1, slot, r, gn, kn);
+          load_x(0, slot, r, gn, kn);
+          if (!skip) mul(t, 1, g);
+          if (G == 1) load_b(0, slot, r, gn, kn);
+        }
     }
+    mfma_done();
     if (POOL && again) {
       for (int e = 0; e < slots; ++e) {
         const int slot = __builtin_amdgcn_readfirstlane(list[e]);
         bool mixed;
         if (!present(slot, mixed)) continue;
         const int r = rank_of(pl, slot);
-        for (int k0 = 0; k0 < r; k0 += 16)
+        for (int k0 = 0; k0 < r; k0 += 32)
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            load(0, slot, r, g, k0);
+            load_b(0, slot, r, g, k0);
             if (!apart(0, mixed)) continue;
 #pragma unroll
-            for (int i = 0; i < FG; ++i)
+            for (int h2 = 0; h2 < 2; ++h2) {
+              load_x(h2, slot, r, g, k0);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                f32x16_t& to = acc[at(i, g)][j];
-                const bf16x8_t w = __builtin_bit_cast(bf16x8_t, b[0][i]);
-                f32x16_t y;
+              for (int i = 0; i < FG; ++i)
 #pragma unroll
-                for (int v = 0; v < 16; ++v) y[v] = 0.0f;
-                y = mfma32x32x16(w, __builtin_bit_cast(bf16x8_t, x[0][1][j]),
-                                 mfma32x32x16(w, __builtin_bit_cast(bf16x8_t, x[0][0][j]), y));
-                const bool own = mine[j] == slot;
-                // back into the accumulator registers at once (or the compiler keeps
-                // the sums in vector registers, and spills)
-                float f16[16];
+                for (int j = 0; j < 4; ++j) {
+                  f32x4_t& to = acc[G * i + g][4 * h2 + j];
+                  const bf16x8_t w = __builtin_bit_cast(bf16x8_t, b[0][i]);
+                  f32x4_t y = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                  y = mfma16x16x32(w, __builtin_bit_cast(bf16x8_t, x[h2][1][j]),
+                                   mfma16x16x32(w, __builtin_bit_cast(bf16x8_t, x[h2][0][j]), y));
+                  const bool own = mine[4 * h2 + j] == slot;
 #pragma unroll
-                for (int v = 0; v < 16; ++v) f16[v] = own ? to[v] + y[v] : to[v];
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                  float u;
-                  asm volatile("v_accvgpr_write_b32 %0, %1" : "=a"(u) : "v"(f16[v]));
-                  to[v] = u;
+                  for (int v = 0; v < 4; ++v) to[v] = own ? to[v] + y[v] : to[v];
                 }
-                __builtin_amdgcn_sched_barrier(0);
-              }
+            }
           }
       }
     }
   }
-  if constexpr (G == 1) {
-    store_tile_lds<FI>(acc, a.Y, N, M, N, m0, n0, smem);
-  } else {
-    const int64_t c0 = n0 >> 1;
-    auto gate = [&](int f, int j, int e) { return kHalves ? acc[f][j][e] : acc[f & ~1][j][8 * (f & 1) + e]; };
-    auto up = [&](int f, int j, int e) { return kHalves ? acc[f][j][8 + e] : acc[f | 1][j][8 * (f & 1) + e]; };
-    if (a.GU) {
-      store_half<FI>(gate, a.GU, 2 * N, M, N, m0, c0, smem);
-      store_half<FI>(up, a.GU + N, 2 * N, M, N, m0, c0, smem);
+  if constexpr (G == 1 && !POOL) {
+    if (a.part) {   // the sums as they are, [M x N] of each split
+#pragma unroll
+      for (int m = 0; m < NA; ++m)
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const int64_t row = m0 + 128 * wr + 16 * n + l16, col = n0 + 32 * FI * wc + 16 * m + 4 * lg;
+          if (row < M && col < N)   // N % 8 == 0
+            *reinterpret_cast<f32x4_t*>(a.part + ((int64_t)split * M + row) * N + col) = acc[m][n];
+        }
+      return;
     }
+  }
+  // Out through LDS: lane (l16, lg) of fragments (m, n) has token 16 n + l16, features 4
+  // lg .. of 16 m.
+  auto store = [&](auto&& value, auto per, bf16_t* out, int64_t ld, int64_t c0) __attribute__((always_inline)) {
+    constexpr int P = decltype(per)::value;   // fragments of 16 features a wave stores
+    constexpr int U = 8 * P, SM = U % 32 == 0 ? 31 : U % 16 == 0 ? 15 : 7;
+    lds_free_for_output();
+#pragma unroll
+    for (int m = 0; m < P; ++m)
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const f32x4_t v = value(m, n);
+        lds_put4<U, SM>(smem, wr * 128 + 16 * n + l16, wc * 4 * P + 4 * m + lg, v[0], v[1], v[2], v[3]);
+      }
+    __syncthreads();
+    lds_tile_out<U, SM>(smem, out, ld, M, N, m0, c0);
+  };
+  if constexpr (G == 1) {
+    store([&](int m, int n) { return acc[m][n]; }, std::integral_constant<int, NA>{}, a.Y, N, n0);
+  } else {
+    const std::integral_constant<int, FI> half{};
+    const int64_t c0 = n0 >> 1;
+    if (a.GU) {
+      store([&](int m, int n) { return acc[2 * m][n]; }, half, a.GU, 2 * N, c0);
+      store([&](int m, int n) { return acc[2 * m + 1][n]; }, half, a.GU + N, 2 * N, c0);
+    }
+    auto h = [&](auto act) __attribute__((always_inline)) {
+      store([&](int m, int n) {
+        f32x4_t v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = act_of<decltype(act)::value>(acc[2 * m][n][e]) * acc[2 * m + 1][n][e];
+        return v;
+      }, half, a.Y, N, c0);
+    };
     if (a.act == kActSilu)
-      store_half<FI>([&](int f, int j, int e) { return act_of<kActSilu>(gate(f, j, e)) * up(f, j, e); }, a.Y, N, M, N, m0, c0,
-                     smem);
+      h(std::integral_constant<int, kActSilu>{});
     else
-      store_half<FI>([&](int f, int j, int e) { return act_of<kActGelu>(gate(f, j, e)) * up(f, j, e); }, a.Y, N, M, N, m0, c0,
-                     smem);
+      h(std::integral_constant<int, kActGelu>{});
   }
 }
 
@@ -297,8 +306,9 @@ hipError_t launch_tiles(const PoolGemm& g, int64_t rows, int64_t n_begin, int64_
   auto* fn = &pool_gemm_kernel<FI, G, POOL>;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)kLdsHalves);
   if (e != hipSuccess) return e;
-  PoolGemmArgs p{g, rows, n_begin, (int)((n_rows + 64 * FI - 1) / (64 * FI)), (int)((g.M + kTile - 1) / kTile)};
-  hipLaunchKernelGGL(fn, dim3(p.tiles_n * p.tiles_m), dim3(kThreads), kLdsHalves, st, p);
+  PoolGemmArgs p{g, rows, n_begin, (int)((n_rows + 64 * FI - 1) / (64 * FI)), (int)((g.M + kTile - 1) / kTile), g.part ? g.splits : 1, 0};
+  p.pps = ((int)(g.K >> 6) + p.splits - 1) / p.splits;
+  hipLaunchKernelGGL(fn, dim3(p.tiles_n * p.tiles_m * p.splits), dim3(kThreads), kLdsHalves, st, p);
   return hipGetLastError();
 }
 template <int G, bool POOL>
@@ -310,6 +320,7 @@ hipError_t launch_fi(int fi, const PoolGemm& g, int64_t rows, int64_t n_begin, i
 
 // Rounds of the card that `rows` rows in tiles of 64 fi take, in rounds of 256-row
 // tiles, the narrower ones' extra reads charged as for the plain dense product.
+int64_t pool_rows(int64_t N, int G) { return G == 1 ? N : (N + kPoolTurn - 1) / kPoolTurn * 2 * kPoolTurn; }
 double rounds(int64_t rows, int64_t tiles_m, int fi, int cus) {
   const int64_t tiles = (rows + 64 * fi - 1) / (64 * fi) * tiles_m;
   return (double)((tiles + cus - 1) / cus) * fi / 4.0 * (fi == 4 ? 1.0 : fi == 3 ? 1.06 : 1.12);
@@ -326,11 +337,10 @@ PoolTiles pool_tiles(int64_t N, int64_t M, int G, int cus) {
   PoolTiles best{0, 4};
   double least = 1e30;
   for (int fi = 4; fi >= 2; --fi) {
-    const int turn = fi == 3 ? 16 : 32;
-    const int64_t rows = G == 1 ? N : (N + turn - 1) / turn * 2 * turn;
+    const int64_t rows = pool_rows(N, G);
     const int64_t round = std::max<int64_t>(1, cus / tiles_m) * kTile;   // rows of a round of 256-row tiles
     for (int k = 0; k < 2; ++k) {
-      const int64_t whole = k == 0 || (G == 2 && fi == 3) || fi == 4 || tiles_m > cus ? 0 : rows / round * round;
+      const int64_t whole = k == 0 || fi == 4 || tiles_m > cus ? 0 : rows / round * round;
       const double cost = (double)(whole / round) + (rows > whole ? rounds(rows - whole, tiles_m, fi, cus) : 0.0);
       if (cost < least) least = cost, best = PoolTiles{whole, fi};
     }
@@ -479,18 +489,17 @@ hipError_t start_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K
   return hipGetLastError();
 }
 
-int pool_turn(int64_t N, int64_t M, int G) { return G == 2 && pool_tiles(N, M, G, device_cu_count()).fi == 3 ? 16 : 32; }
-
 hipError_t launch_pool_gemm(const PoolGemm& g, hipStream_t st) {
   const int G = g.pool.G;
+  const bool many = g.pool.ids != nullptr && g.pool.R > 0;
+  if (g.part && (G != 1 || many)) return hipErrorInvalidValue;
   const PoolTiles p = pool_tiles(g.N, g.M, G, device_cu_count());
-  const int turn = p.fi == 3 ? 16 : 32;
-  const int64_t rows = G == 1 ? g.N : (g.N + turn - 1) / turn * 2 * turn;
+  const int64_t rows = pool_rows(g.N, G);
   auto go = [&](int fi, int64_t begin, int64_t n) {
-    const bool many = g.pool.ids != nullptr && g.pool.R > 0;
     if (G == 1) return many ? launch_fi<1, true>(fi, g, rows, begin, n, st) : launch_fi<1, false>(fi, g, rows, begin, n, st);
     return many ? launch_fi<2, true>(fi, g, rows, begin, n, st) : launch_fi<2, false>(fi, g, rows, begin, n, st);
   };
+  if (g.part) return go(4, 0, rows);
   if (p.whole > 0) {
     const hipError_t e = go(4, 0, p.whole);
     if (e != hipSuccess || p.whole >= rows) return e;

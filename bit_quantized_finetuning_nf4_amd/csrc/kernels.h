@@ -189,6 +189,8 @@ size_t staged_part_bytes(int64_t N, int64_t K, int64_t M);
 double staged_cost(int64_t N, int64_t K, int64_t M);   // us, estimated
 // Whether the 256-token tiles are estimated the fastest, unsplit.
 bool dense_tiles(int64_t N, int64_t K, int64_t M);
+// Splits of a dense product of few 256-token tiles and a long contraction (1: none).
+int dense_splits(int64_t N, int64_t K, int64_t M, int cus);
 // X Wd^T alone as *splits fp32 parts [M x N].  product_part_bytes are enough.
 size_t product_part_bytes(int64_t N, int64_t K, int64_t M);
 hipError_t launch_product_parts(const bf16_t* Wd, int64_t N, int64_t K, const bf16_t* X, int64_t M, float* part,
@@ -278,8 +280,9 @@ hipError_t launch_pool_finish(const PoolView& p, const float* part, int splits, 
                               bf16_t* U, int act, bf16_t* Y, bf16_t* GU, hipStream_t st);
 // The products of many tokens with the adapters' term, and of a gated block's two
 // weights with its activation, from a dequantized stack (gemm_pool.hip): G == 1
-// Wd [N x K]; G == 2 rows in turns of pool_turn, N rounded up to kPoolRows of
-// each, as launch_dequant_pair leaves them.  T: kTermParts parts [M x G R].
+// Wd [N x K]; G == 2 kPoolTurn rows of each in turn, N rounded up to kPoolRows of
+// each, as launch_dequant_pair leaves them.  T: kTermParts parts [M x G R].  part
+// not null (G == 1, one adapter or none): the sum as `splits` fp32 parts [M x N].
 struct PoolGemm {
   const bf16_t* Wd;
   int64_t N, K, M;
@@ -287,10 +290,15 @@ struct PoolGemm {
   PoolView pool;
   int act;
   bf16_t *Y, *GU;
+  float* part;
+  int splits;
 };
-constexpr int64_t kPoolRows = 32;
+constexpr int64_t kPoolRows = 32, kPoolTurn = 16;
 inline int64_t pool_stack_rows(int64_t N, int G) { return G == 1 ? N : (N + kPoolRows - 1) / kPoolRows * kPoolRows * 2; }
-int pool_turn(int64_t N, int64_t M, int G);
+// 32-bit offsets of T and of a slot's B, R ranks of G weights each.
+inline bool pool_term_ok(int64_t M, int64_t N, int64_t R, int G) {
+  return M <= ((int64_t)1 << 27) / (G * R) && N < ((int64_t)1 << 30) / R;
+}
 hipError_t launch_pool_gemm(const PoolGemm& g, hipStream_t st);
 // T [M x G R] of a pool's adapters, as parts or in fp32 (T; either may be null),
 // through `part` (pool_u_part_bytes): all but *rest (kRideSum).
@@ -309,9 +317,10 @@ hipError_t launch_dequant_pair(const Nf4View* W, int turn, bf16_t* out, const Ri
 // N of each are left as they were.  rest: of kRideSum3, possibly empty.
 hipError_t launch_dequant_t_pair(const Nf4View* W, bf16_t* out, int64_t half, const Ride& rest, hipStream_t st);
 // dY [M x 2 Fp] = [dG | dP] of a gated block (gated.hip), zero from column F of
-// each half on, as Wt [K x 2 Fp] is made (may be null).
+// each half on, as Wt [K x 2 Fp] is made (may be null); and At [K x r] = A^T (may be
+// null, r % 8 == 0).
 hipError_t launch_gated_grad(const bf16_t* dH, const bf16_t* GU, int64_t M, int64_t F, int64_t Fp, int act, bf16_t* dY,
-                             bf16_t* Wt, int64_t K, hipStream_t st);
+                             bf16_t* Wt, int64_t K, const bf16_t* A, int r, bf16_t* At, hipStream_t st);
 
 // Rows of 8-bit integers with one scale each (i8.hip): bytes from one row to
 // the next, and the passes over them.
