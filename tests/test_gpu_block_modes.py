@@ -232,3 +232,16 @@ def test_tokens_of_two_to_the_31():
         # T may enter as two bf16 parts, 2^-17 of it
         tol = E * want.abs() + 1.01 * ((K + R) * F + 2.0**-17) * size
         assert ((Y[at:at + 40].double() - want).abs() <= tol).all(), at
+
+
+# (tokens, features, K, rank): 256-token tiles for dX, whole and in a split contraction
+@pytest.mark.parametrize("M,N,K,r", [(2050, 104, 8192, 24), (2050, 200, 4160, 0), (1040, 4104, 4160, 72), (1040, 4104, 4096, 0),
+                                     (2050, 4104, 2048, 128)])
+def test_backward_in_large_tiles(M, N, K, r):
+    print(f"[gated_bwd] M={M} F={N} K={K} r={r}", flush=True)
+    qs, Ws, X, A, B, rng = block(M, M, N, K, r)
+    check_bwd(qs, Ws, X, A, B, 16.0, "silu", rng, "large tiles")
+
+
+def test_many_in_a_split_contraction():
+    check(1030, 4104, 8192, 6, 40, spread_ids(np.random.default_rng(3), 1030, 6, "outside"), 3)
