@@ -1,6 +1,7 @@
 // dense_tile.h -- the main loop and the LoRA-tail staging of the dense GEMMs
 // (gfx950): 256 x 64 FI output tiles, both operands streamed as rows of
-// 128-byte lines through two LDS pair slots by buffer->LDS DMA.
+// 128-byte lines through LDS by buffer->LDS DMA: two pair slots (dense_slots), or a
+// ring of five half slots (dense_halves, dense_quads), which takes all of the LDS.
 //
 // The loop moves bytes: a pair is 128 bytes of every row, 64 bf16 or 128
 // 8-bit integers, and a fragment is 16 bytes of a row.  The operation MM

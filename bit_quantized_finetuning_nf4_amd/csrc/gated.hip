@@ -4,7 +4,7 @@
 //
 // from the saved projections GU = [G | P] (bf16), side by side in 16 bits as
 // the backward products read them.  10 bytes an element and about 45 fp64
-// operations (gate.h says why 64 bits).
+// operations (gate.h says why 64 bits): 2048 x 13824 60-67 us, 4.2-4.7 TB/s, memory.
 #include "gate.h"
 #include "kernels.h"
 #include "lds.h"

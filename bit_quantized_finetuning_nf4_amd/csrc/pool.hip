@@ -22,6 +22,9 @@ namespace {
 // after rank, it took 2-4 us), and T, kR ranks of B and kP parts are asked for
 // together, before it is known how many parts and ranks there are; what there is
 // not is never used.
+// 1 x 2 x 11008, rank 64 4.0 us; 32 tokens of as many slots of rank 16 beside 2 x
+// 22016 rows 13 (17 MB of parts, 45 of B: 4.8 TB/s); 777 tokens mixed over 7 slots of
+// rank 64, three parts of 5120 columns 25: the rows of B again for every eight tokens.
 template <int G, int TB, bool LINE>
 __global__ __launch_bounds__(256) void pool_finish_kernel(PoolView p, const float* __restrict__ part, int splits,
                                                           const int32_t* __restrict__ counts, StreamLine line, int64_t M,

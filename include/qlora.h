@@ -657,9 +657,11 @@ qlora_status qlora_i8_linear_bwd(const qlora_i8_rows* W, const uint16_t* X, cons
  *   H = act(G) o P,  G = X deq(W_0)^T + s U_0 B_0^T,  P = X deq(W_1)^T +
  *   s U_1 B_1^T,  [U_0 | U_1] = X A^T,
  * with the two adapters stacked as for qlora_group_fwd, A [2 r x K] and
- * B [2 F x r], s = RN32(alpha / r); r == 0 (A = B = NULL): none.  G, P and s U
- * are not rounded before H, which is rounded once.  Any M >= 1; K % 64 == 0,
- * F % 8 == 0; 2 F K, M K and 2 M F below 2^31, 2 M r at most 2^27
+ * B [2 F x r], s = RN32(alpha / r); r == 0 (A = B = NULL): none.  G and P are
+ * not rounded before H, which is rounded once; s U is not either, or (from some
+ * hundred tokens on) enters as the sum of two bf16, 2^-17 of it.  Any M >= 1;
+ * K % 64 == 0, F % 8 == 0; with Fp = F rounded up to 32, 2 Fp K, M K and 2 M F
+ * below 2^31; with r > 0 2 M r at most 2^27, F r below 2^30 and K below 2^24
  * (QLORA_E_UNSUPPORTED otherwise); QLORA_E_SHAPE where the weights differ in
  * shape.  The two may have different codebooks. */
 typedef enum {
@@ -682,8 +684,8 @@ qlora_status qlora_gated_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64
  *   dA [2 r x K] = s [dG B_0 | dP B_1]^T X, dB [2 F x r] with dB_g = s dY_g^T
  *   U_g (fp32, overwritten; the sums s dY_g B_g enter dA with fp32's precision).
  * U_saved is the forward's U; NULL computes it again.  r == 0: dA and dB NULL.
- * With Fp = F rounded up to 32: 2 Fp K, 2 Fp M and M K below 2^31, 2 Fp at most
- * 2^22; with r > 0 K and 2 Fp below 2^24 and 2 r times M, K or 2 Fp below 2^31.
+ * 2 Fp K, 2 Fp M and M K below 2^31, 2 Fp below 2^22; with r > 0 K below 2^24 and
+ * 2 r times M, K or 2 Fp below 2^31.
  * Workspace: qlora_workspace_bytes(QLORA_OP_GATED_BWD, M, F, K, r, 0). */
 qlora_status qlora_gated_bwd(const qlora_nf4_weight* W, const uint16_t* X, const uint16_t* dH, const uint16_t* GU,
                              int64_t M, const uint16_t* A, const uint16_t* B, int32_t r, float alpha, int32_t act,
@@ -706,17 +708,17 @@ typedef struct {
   const uint16_t* B;      /* [S x rows x R]                                    */
   const float* scale;     /* [S], alpha / r of the slot's adapter              */
   const int32_t* ranks;   /* nullable [S]: the slot's own rank, at most R (0:
-                             none); ranks past it, rounded up to eight, are not
-                             read: zeros where it is not a multiple of eight   */
+                             none); what lies past it, rounded up to eight, does
+                             not matter: zeros where it is no multiple of eight */
 } qlora_adapter_pool;
 
 /* Y [M x N] (bf16, overwritten): y_m = deq(W) x_m + scale_a B_a (A_a x_m) with
  * a = ids[m]; an id outside 0 .. S - 1 is no adapter.  ids [M], 4-byte aligned,
  * in any order; tokens of one slot next to each other read it less often.
- * scale A x is not rounded in between.  Any M >= 1; K % 64 == 0, N % 8 == 0;
- * N K, M K and M N below 2^31, M R at most 2^27 (QLORA_E_UNSUPPORTED
- * otherwise).  A slot that no id names is not read; what its scale, A or B hold
- * does not matter.
+ * scale A x is as exact as s U above.  Any M >= 1; K % 64 == 0, N % 8 == 0;
+ * N K, M K and M N below 2^31, M R at most 2^27, N R below 2^30, K below 2^24
+ * (QLORA_E_UNSUPPORTED otherwise).  What a slot holds that no id names does not
+ * matter, and infinities and NaN of one slot reach its own tokens alone.
  * Workspace: qlora_workspace_bytes(QLORA_OP_MANY_FWD, M, N, K, R, 0). */
 qlora_status qlora_many_fwd(const qlora_nf4_weight* W, const uint16_t* X, int64_t M, const qlora_adapter_pool* pool,
                             const int32_t* ids, uint16_t* Y, void* ws, size_t ws_bytes, void* stream);
