@@ -695,22 +695,21 @@ def gated_bwd(qs: Sequence[QuantizedWeight], X, dH: torch.Tensor, GU: torch.Tens
     _on_current(dH.device)
     descs, F, K = _pair(qs, dH)
     M = dH.shape[0]
-    _need(dH, torch.bfloat16, "dH", (M, F))
-    _beside(_need(GU, torch.bfloat16, "GU", (M, 2 * F)), dH, "GU")
+    h = _is(dH, torch.bfloat16, (M, F), dH, "dH")
+    gu = _is(GU, torch.bfloat16, (M, 2 * F), dH, "GU")
     r = _pair_rank(A, B, F, K, dH)
+    x = u = None
     if r:
-        _beside(_need(X, torch.bfloat16, "X", (M, K)), dH, "X")
-        if U is not None:
-            _beside(_need(U, torch.bfloat16, "U", (M, 2 * r)), dH, "U")
+        x = _is(X, torch.bfloat16, (M, K), dH, "X")
+        u = None if U is None else _is(U, torch.bfloat16, (M, 2 * r), dH, "U")
         dA = _out(dA, (2 * r, K), torch.float32, dH, "dA")
         dB = _out(dB, (2 * F, r), torch.float32, dH, "dB")
     else:
-        X = U = dA = dB = None
+        dA = dB = None
     dX = _out(dX, (M, K), torch.bfloat16, dH, "dX") if need_dx else None
     ws = _ws_for(ws, workspace_bytes(_lib.QLORA_OP_GATED_BWD, M, F, K, r), dH)
-    check(lib().qlora_gated_bwd(descs, _ptr(X), _ptr(dH), _ptr(GU), M, _ptr(A) if r else None, _ptr(B) if r else None, r,
-                                float(alpha), _act(act), _ptr(U), _ptr(dX), _ptr(dA), _ptr(dB), *_ws_args(ws),
-                                _stream()), "qlora_gated_bwd")
+    check(lib().qlora_gated_bwd(descs, x, h, gu, M, _ptr(A) if r else None, _ptr(B) if r else None, r, float(alpha),
+                                _act(act), u, _ptr(dX), _ptr(dA), _ptr(dB), *_ws_args(ws), _stream()), "qlora_gated_bwd")
     return dX, dA, dB
 
 
