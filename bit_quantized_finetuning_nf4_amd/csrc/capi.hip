@@ -371,10 +371,10 @@ BwdLayout group_bwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, int32_t G
 // tiles, or in splits, whose sums the adapters join in a pass of their own; or
 // (dense) in 256-token tiles that take it all.
 // Streamed and dequantized, kernels' times: two weights of 22016 x 8192 with 128
-// tokens 215 and 485 us, 256 tokens 395 and 530; 8192 x 8192 47 and 100, 81 and
-// 104; two of 11008 x 4096 63 and 110, 108 and 112.  With 320 tokens the two meet
-// (104 and 113, 134 and 133).
-constexpr int64_t kStreamTokens = 256;
+// tokens 215 and 485 us, 320 tokens 503 and 600, 384 tokens 573 and 608; 8192 x
+// 8192 46 and 100, 105 and 118, 121 and 122; two of 11008 x 4096 61 and 110, 134
+// and 134, 155 and 134; 5120 x 13824 at rank 64 64 and 110, 141 and 138, 159 and 137.
+constexpr int64_t kStreamTokens = 320;
 enum PoolPath { kPoolStream, kPoolTiles, kPoolDense };
 PoolPath pool_path(int64_t M, int64_t N, int64_t K, int32_t G) {
   if (M <= kStreamTokens) return kPoolStream;

@@ -384,7 +384,7 @@ StreamPlan stream_plan(int64_t N, int64_t K, int64_t M, int G, int R) {
   L.tiles = (uint32_t)((N + kStreamRows - 1) / kStreamRows);
   L.spans = (uint32_t)((K + kSpan - 1) / kSpan);
   L.block = 16 * s.nt;
-  // (below 2^20: G N K and M K below 2^31, M at most 256)
+  // (below 2^20: G N K and M K below 2^31, M at most 320)
   L.units = L.tiles * (uint32_t)G * (uint32_t)((M + L.block - 1) / L.block) * L.spans;
   L.wgs = std::min<uint32_t>(s.nt == 4 ? 256 : 512, L.units);
   const uint32_t least = L.units / L.wgs;
