@@ -411,8 +411,8 @@ PoolLayout pool_layout(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
 // (2^29).
 bool pool_sizes_ok(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {
   if (M <= 0 || N <= 0 || K <= 0 || G < 1 || R < 0 || R > kMaxRank) return false;
-  if (N > (int64_t)1 << 30 || pool_stack_rows(N, G) > (int64_t)0x7FFFFFFF / K || M > (int64_t)0x7FFFFFFF / K || M > (int64_t)0x7FFFFFFF / G / N) return false;
-  if (G == 2 && (N + 15) / 16 > 65535) return false;   // the stack's dequantization
+  const int64_t top = 0x7FFFFFFF;
+  if (N > (int64_t)1 << 30 || pool_stack_rows(N, G) > top / K || M > top / K || M > top / G / N) return false;
   return R == 0 || (pool_term_ok(M, N, R, G) && skinny_cols_ok(K));
 }
 qlora_status check_pool_sizes(int64_t M, int64_t N, int64_t K, int32_t R, int32_t G) {

@@ -190,7 +190,8 @@ __global__ __launch_bounds__(kThreads, 1) void pool_gemm_kernel(PoolGemmArgs p) 
         for (int i = 0; i < FG; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mfma_acc<false>(__builtin_bit_cast(bf16x8_t, b[t][i]), __builtin_bit_cast(bf16x8_t, x[h2][e][j]), acc[G * i + g][4 * h2 + j]);
+            mfma_acc<false>(__builtin_bit_cast(bf16x8_t, b[t][i]), __builtin_bit_cast(bf16x8_t, x[h2][e][j]),
+                            acc[G * i + g][4 * h2 + j]);
     };
     // Whether the wave has tokens of the slot, and others.
     auto present = [&](int slot, bool& mixed) __attribute__((always_inline)) {
@@ -313,7 +314,8 @@ hipError_t launch_tiles(const PoolGemm& g, int64_t rows, int64_t n_begin, int64_
   auto* fn = &pool_gemm_kernel<FI, G, POOL>;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), (int)kLdsHalves);
   if (e != hipSuccess) return e;
-  PoolGemmArgs p{g, rows, n_begin, (int)((n_rows + 64 * FI - 1) / (64 * FI)), (int)((g.M + kTile - 1) / kTile), g.part ? g.splits : 1, 0};
+  PoolGemmArgs p{g, rows, n_begin, (int)((n_rows + 64 * FI - 1) / (64 * FI)), (int)((g.M + kTile - 1) / kTile),
+                 g.part ? g.splits : 1, 0};
   p.pps = ((int)(g.K >> 6) + p.splits - 1) / p.splits;
   hipLaunchKernelGGL(fn, dim3(p.tiles_n * p.tiles_m * p.splits), dim3(kThreads), kLdsHalves, st, p);
   return hipGetLastError();
@@ -493,7 +495,8 @@ hipError_t start_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K
   // (of tokens and ranks without an adapter the sums mean nothing, and are not read)
   *rest = Ride{};
   rest->kind = kRideSum, rest->blocks = (int)((M * GR / 4 + 255) / 256);
-  rest->part = part, rest->splits = s.splits, rest->n = M * GR, rest->scale = 1.0f, rest->parts = parts, rest->full = T, rest->s = 1.0f;
+  rest->part = part, rest->splits = s.splits, rest->n = M * GR, rest->scale = rest->s = 1.0f;
+  rest->parts = parts, rest->full = T;
   return hipGetLastError();
 }
 

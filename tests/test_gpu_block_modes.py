@@ -245,3 +245,21 @@ def test_backward_in_large_tiles(M, N, K, r):
 
 def test_many_in_a_split_contraction():
     check(1030, 4104, 8192, 6, 40, spread_ids(np.random.default_rng(3), 1030, 6, "outside"), 3)
+
+
+def test_a_block_of_a_million_features():
+    """More rows than a grid's second dimension could count; the first and last 256 are what they are alone."""
+    M, N, K = 330, 1200128, 64   # 256 x 4688
+    torch.manual_seed(2)
+    qs = [big_weight(N, K) for _ in range(2)]
+    X = bf16(np.random.default_rng(2), (M, K), 0.5)[0]
+    H, GU, _ = ops.gated_fwd(qs, X, save=True)
+    for at in (0, N - 256):
+        for g, q in enumerate(qs):
+            one = ops.QuantizedWeight(256, K, q.codes[at * 32:(at + 256) * 32].clone(), q.absmax_q[at:at + 256].clone(),
+                                      q.group_scale[at // 256:at // 256 + 1].clone())
+            W = ops.dequant(one).view(256, K).double()
+            want, size = X.double() @ W.T, X.double().abs() @ W.abs().T
+            got = GU[:, g * N + at:g * N + at + 256].double()
+            assert ((got - want).abs() <= E * want.abs() + 1.01 * K * F * size).all(), (g, at)
+    assert torch.isfinite(H).all()
