@@ -490,8 +490,12 @@ hipError_t start_pool_u(const PoolView& p, const bf16_t* X, int64_t M, int64_t K
   const int lds = rp == 64 ? UShape<64>::kLds : UShape<128>::kLds;
   hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(s.tiles * s.splits, (GR + rp - 1) / rp, p.slots > 1 ? 2 : 1), dim3(kUThreads), lds, st, p, X,
-                     M, K, s.sps, s.tiles, part);
+  // The slots of a tile go round the grid's third dimension: two workgroups, or as
+  // many more as CUs would have nothing to do (393 tokens of 15 slots mixed, K 832: 42
+  // us with two, 14 with sixteen).
+  const int ranks = (GR + rp - 1) / rp, idle = 256 / (s.tiles * s.splits * ranks);
+  const int turns = std::min(p.slots, std::max(2, std::min(16, idle)));
+  hipLaunchKernelGGL(fn, dim3(s.tiles * s.splits, ranks, turns), dim3(kUThreads), lds, st, p, X, M, K, s.sps, s.tiles, part);
   // (of tokens and ranks without an adapter the sums mean nothing, and are not read)
   *rest = Ride{};
   rest->kind = kRideSum, rest->blocks = (int)((M * GR / 4 + 255) / 256);

@@ -161,7 +161,9 @@ __global__ __launch_bounds__(256) void pool_finish_kernel(PoolView p, const floa
 
 }  // namespace
 
-// After a streamed product a thread takes as few tokens as fill the card.
+// After a streamed product a thread takes as few tokens as fill the card, and more
+// at higher ranks, whose rows of B weigh more than the parts: 209 tokens of 2256
+// features at rank 128 17.7 us with one token, 11.6 with four.
 hipError_t launch_pool_finish(const PoolView& p, const float* part, int splits, const int32_t* counts,
                               const StreamLine* line, int64_t M, int64_t N, const float* T, int slices, float scale,
                               bf16_t* U, int act, bf16_t* Y, bf16_t* GU, hipStream_t st) {
@@ -172,7 +174,7 @@ hipError_t launch_pool_finish(const PoolView& p, const float* part, int splits, 
                        splits, counts, line ? *line : StreamLine{}, M, N, T, slices, scale, U, act, Y, GU);
     return hipGetLastError();
   };
-  const int64_t work = tiles * M / 1024;
+  const int64_t work = tiles * M * std::max(1, p.G * p.R / 32) / 1024;
   if (!line) return p.G == 1 ? go(&pool_finish_kernel<1, 8, false>, 8) : go(&pool_finish_kernel<2, 8, false>, 8);
   if (p.G == 1)
     return work >= 8   ? go(&pool_finish_kernel<1, 8, true>, 8)
