@@ -263,3 +263,11 @@ def test_a_block_of_a_million_features():
             got = GU[:, g * N + at:g * N + at + 256].double()
             assert ((got - want).abs() <= E * want.abs() + 1.01 * K * F * size).all(), (g, at)
     assert torch.isfinite(H).all()
+
+
+@pytest.mark.parametrize("K", [64, 128, 192, 320, 448, 576, 1088, 1216])
+@pytest.mark.parametrize("N", [8, 24, 32, 40, 104, 264])
+def test_rows_whose_block_codes_share_words(N, K):
+    """K / 64 of 1 to 19 block codes a row, at every place in a word, the array ending inside one or not."""
+    for M in (1, 20, 40):
+        check(M, N, K, 3, 8, np.arange(M) % 4 - 1, M + N + K)
