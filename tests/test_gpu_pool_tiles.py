@@ -11,9 +11,10 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from bit_quantized_finetuning_nf4_amd import ops
-from tests.test_gpu_gated import bf16, block, check_bwd, check_fwd, weight
-from tests.test_gpu_many import check, make_pool, spread_ids
+from tests.test_gpu_gated import E, bf16, block, check_bwd, check_fwd, weight, within
+from tests.test_gpu_many import check, make_pool, reference, spread_ids
 
 pytestmark = pytest.mark.gpu
 
@@ -167,3 +168,18 @@ def test_streams_in_small_tiles():
     for i, outs in got:
         for a, b in zip(want[i], outs):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M,N,K,S,R", [(7, 136, 192, 6, 24), (300, 72, 128, 6, 64), (400, 136, 128, 6, 16),
+                                       (1999, 4208, 64, 6, 40)])
+def test_the_oracles_tokens(M, N, K, S, R):
+    """Against oracle.many_fwd, ranks and ids outside the pool included; its error is that of the same sums."""
+    rng = np.random.default_rng(M)
+    q, W = weight(rng, N, K)
+    X = bf16(rng, (M, K), 0.3)
+    ranks = [R, 8, 3, 0, -5, 200]
+    p, A, B, scale = make_pool(rng, S, R, N, K, ranks=ranks)
+    ids = spread_ids(rng, M, S, "outside").astype(np.int32)
+    want = oracle.many_fwd(W, X[1], A, B, scale, ids, np.array(ranks))
+    _, err = reference([W], X[1], A, B, scale, ids)
+    within(ops.many_fwd(q, X[0], p, torch.from_numpy(ids).cuda()), want, E * np.abs(want) + 1.01 * err, "many")
