@@ -656,7 +656,8 @@ def gated_fwd(qs: Sequence[QuantizedWeight], X: torch.Tensor, A=None, B=None, al
     and P their products with X and the stacked adapters A [2r x K], B [2F x r]
     (as group_fwd).  act is "silu" or "gelu" (the tanh form).  Returns H
     [M x F], or with save (H, GU, U) for gated_bwd: GU [M x 2F] = [G | P] and
-    U [M x 2r] (None without adapters), in bf16."""
+    U [M x 2r] (None without adapters), in bf16.  The adapters' input is not
+    dropped out: linear_fwd(drop=), one linear at a time, is for that."""
     _need(X, torch.bfloat16, "X")
     _on_current(X.device)
     descs, F, K = _pair(qs, X)

@@ -663,7 +663,10 @@ qlora_status qlora_i8_linear_bwd(const qlora_i8_rows* W, const uint16_t* X, cons
  * K % 64 == 0, F % 8 == 0; with Fp = F rounded up to 32, 2 Fp K, M K and 2 M F
  * below 2^31; with r > 0 2 M r at most 2^27, F r below 2^30 and K below 2^24
  * (QLORA_E_UNSUPPORTED otherwise); QLORA_E_SHAPE where the weights differ in
- * shape.  The two may have different codebooks. */
+ * shape.  The two may have different codebooks.  There is no dropout of the
+ * adapters' input in this block, in either direction, nor with a pool: a block
+ * trained under it takes its two linears one by one (qlora_linear_fwd_drop and
+ * qlora_linear_bwd_drop). */
 typedef enum {
   QLORA_ACT_SILU = 0,   /* x / (1 + exp(-x))                                   */
   QLORA_ACT_GELU = 1    /* x / 2 (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3)))   */
