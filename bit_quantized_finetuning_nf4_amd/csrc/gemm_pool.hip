@@ -15,7 +15,13 @@
 // The adapters' term follows from global memory, T as kTermParts bf16 parts: for
 // each slot among the tile's tokens the ranks 32 at a time, the next ones' loads in
 // flight, the tokens of other slots zero.  Tokens of one slot next to each other
-// (prompts) make it one pass or two of a tile.
+// (prompts) make it one pass or two of a tile; the time grows with the slots of a
+// tile, here and in T's kernel below (4096 tokens through 8192 x 8192 at rank 16:
+// eight prompts 443 us, eight slots in turn 607, a slot to every token 4030; two of
+// 22016 x 8192: 2270, 2600, 8570).  With a pool the 256-row tile's term has more live
+// values than registers: 88 (one weight) and 133 (two) go to scratch and are read
+// back in it; with one adapter and one weight 32 rest there during the term.  The
+// main loop has none.
 //
 // 4096 x 8192 x 22016 with the adapters of eight prompts 1060 us (1.39 PFLOP/s), two
 // weights of 22016 x 8192 and 4096 tokens, activation and saved projections
@@ -335,8 +341,10 @@ double rounds(int64_t rows, int64_t tiles_m, int fi, int cus) {
   return (double)((tiles + cus - 1) / cus) * fi / 4.0 * (fi == 4 ? 1.0 : fi == 3 ? 1.06 : 1.12);
 }
 // The first `whole` rows in 256-row tiles, whole rounds of them, the others in
-// tiles of 64 fi: what takes the least time.  A gated block's rows come in one
-// kind of turn, so fi 3 is for all of them or none.
+// tiles of 64 fi: what takes the least time.  A gated block's rows come in turns of
+// 32 (16 of each weight), and a tile may begin at any of them: every fi fits after
+// whole rounds.  Two weights of 22016 x 8192 and 4096 tokens: 40960 rows in ten
+// rounds, then 3072 in tiles of 192.
 struct PoolTiles {
   int64_t whole;
   int fi;
@@ -365,7 +373,8 @@ PoolTiles pool_tiles(int64_t N, int64_t M, int G, int cus) {
 // tokens.  Stages of 64 columns, one 128-byte line of every row, in a ring of four
 // that a fifth wave fills (a CU keeps about 90 lines in flight, and their issue
 // stalls there).  4096 x 22016 of eight prompts at rank 64 76 us (180 MB at 2.4 TB/s),
-// 1200 x 5120 x 2 at rank 32 19: bound by those lines.
+// 1200 x 5120 x 2 at rank 32 19: bound by those lines.  Each slot of a tile is a pass
+// over its tokens' columns, all 128 multiplied.
 // ---------------------------------------------------------------------------
 namespace {
 

@@ -755,7 +755,9 @@ def _many(name, op, descs, N, K, groups, X, pool, ids, act, out, ws):
 
 def many_fwd(q: QuantizedWeight, X: torch.Tensor, pool: AdapterPool, ids: torch.Tensor, out=None, ws=None):
     """Y [M x N]: token m's product with the weight, and with the adapter in
-    slot ids[m] (int32) of the pool; an id outside the pool is no adapter."""
+    slot ids[m] (int32) of the pool; an id outside the pool is no adapter.
+    Past 320 tokens the time grows with the slots among neighbouring tokens:
+    put the tokens of one slot next to each other."""
     _need(X, torch.bfloat16, "X")
     _on_current(X.device)
     _whole(q, X)
