@@ -30,10 +30,13 @@
 //
 // One token through two weights of 22016 x 8192 50 us (186 MB at 3.7 TB/s), of 11008 x
 // 4096 20, through 4096 x 4096 7.5: 5-7 us to start (table, first codes, the
-// adapters' loads) and then 4.0-4.6 TB/s, what reads alone reach here.  32 tokens
-// 70: x's lines come with the codes', half as many; 64 tokens 104, as many.  The
-// vector units are busy 43 % of the time at 32 tokens, LDS 28 %.  Units of 512 rows, which
-// halve x's share, took as long at 32 tokens and longer at 64 (more to start with).
+// adapters' loads) and then 4.0-4.6 TB/s.  That is what launches this short reach;
+// the decode kernel (gemv.hip) reads the same codes at 5.6-5.7 TB/s over a pass of
+// 35 GB.  32 tokens 70: x's lines come with the codes', half as many; 64 tokens 104, as
+// many.  The vector units are busy 43 % of the time at 32 tokens, LDS 28 %; the
+// kernel of 32 tokens is at its 128 registers, and seven more are read back from
+// scratch in the unit loop.  Units of 512 rows, which halve x's share, took as long at
+// 32 tokens and longer at 64 (more to start with).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
