@@ -25,8 +25,14 @@
 //                 X A^T, then of the product
 //   FWD_DROP    : s U as above | split partials of U, then of the staged
 //                 product | deq(W) bf16 [N x K], if staged
-//   GATED_FWD, MANY_FWD, GATED_MANY_FWD : scale A x fp32 [M x G R] | deq(W_g)
-//                 stacked [G N x K] | the frozen product's fp32 parts
+//   GATED_FWD, MANY_FWD, GATED_MANY_FWD, by the way that the call takes:
+//     streamed  : A x as fp32 parts of K's slices [slices][M x G R] (a pool's with
+//                 its scales) | the number of each tile's parts, int32 | the
+//                 frozen products' fp32 parts [slots][M x G N]
+//     small tiles or splits : scale A x fp32 [M x G R] | deq(W_g) stacked [G N x
+//                 K] | first the fp32 parts of A x, then those of the product
+//     256-token tiles : scale A x as two bf16 parts [M x G R] each | deq(W_g), of
+//                 two weights in turns of 16 rows | the fp32 parts of A x
 //   GATED_BWD   : s G as three bf16 parts [M x 2 r] each | U bf16 [M x 2 r] |
 //                 split partials | [dG | dP] bf16 [M x 2 Fp] (Fp = F rounded up
 //                 to 32, zero columns) | deq(W_g)^T side by side [K x 2 Fp] |
@@ -374,6 +380,12 @@ BwdLayout group_bwd_layout(int64_t M, int64_t N, int64_t K, int32_t r, int32_t G
 // tokens 215 and 485 us, 320 tokens 503 and 600, 384 tokens 573 and 608; 8192 x
 // 8192 46 and 100, 105 and 118, 121 and 122; two of 11008 x 4096 61 and 110, 134
 // and 134, 155 and 134; 5120 x 13824 at rank 64 64 and 110, 141 and 138, 159 and 137.
+// One number for every shape is a compromise: a pool's rank weighs on the streamed
+// way, whose adapters are vector products (calls with eight slots, us: 5120 x 13824
+// with 320 tokens 103 and 119 at rank 8, 133 and 129 at 64, 165 and 142 at 128; two
+// of 11008 x 4096 137 and 154, 184 and 173, 227 and 193, and with 256 tokens at rank
+// 128 184 and 167), and small weights would gain from it for longer (1024 x 1024 with
+// 384 tokens 19 and 28, 4096 x 4096 at rank 8 41 and 51).
 constexpr int64_t kStreamTokens = 320;
 enum PoolPath { kPoolStream, kPoolTiles, kPoolDense };
 PoolPath pool_path(int64_t M, int64_t N, int64_t K, int32_t G) {
