@@ -201,7 +201,7 @@ def decode_batch_study(jobs, layers, r, alpha, passes, dev):
 # the device code of each kernel whose traffic is reported: its source file
 # and the device headers it includes
 KERNEL_SOURCES = {"fwd_kernel": ["gemm_nf4.hip", "gemm_common.h"], "dx_kernel": ["gemm_nf4.hip", "gemm_common.h"],
-                  "dense_gemm": ["gemm_bf16.hip", "gemm_common.h"],
+                  "dense_gemm": ["gemm_bf16.hip", "dense_tile.h", "gemm_common.h"],
                   "quantize_kernel": ["quantize.hip"], "gemv_kernel": ["gemv.hip"],
                   "dequant_kernel": ["quantize.hip"], "dequant_t_kernel": ["quantize.hip"]}
 DEVICE_HEADERS = ["device.h", "lds.h"]
