@@ -202,7 +202,9 @@ __device__ __forceinline__ void dense_slots(const char* cur, const char* nxt, ch
 // over the whole next pair, and the last lines that a barrier waits for have half a
 // pair's time: the wave's 2 FI weight loads issued after them stay in flight.
 // 4096 x 8192 x 22016 1.94 -> 1.56 cycles a matrix cycle (0.65 -> 0.81 of the time in
-// the matrix units), 1200 -> 1138 us; 333 x 22016 x 4096 95 -> 82.  A loop that waits
+// the matrix units), 1200 -> 1138 us; 333 x 22016 x 4096 95 -> 82; the eight grouped
+// products of the 65B layer set (gemm_bf16.hip), both in turn on one card, 1323 -> 1374
+// TFLOP/s, the clock falling from 1.78 to 1.67 GHz.  A loop that waits
 // for no load at all takes the same: the rest is issue, and the clock, which falls
 // as the units fill.  It needs all of the LDS: for kernels that keep nothing else
 // there.
