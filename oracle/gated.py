@@ -26,13 +26,14 @@ from .group import group_bwd, group_fwd
 def act(x, name):
     """act(x) and act'(x)."""
     x = np.asarray(x, dtype=np.float64)
+    # (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)), which keeps its digits where tanh z is next to -1
+    p, dp = x, 1.0
+    if name != "silu":
+        c = 2.0 * math.sqrt(2.0 / math.pi)
+        p, dp = c * (x + 0.044715 * x**3), c * (1.0 + 3 * 0.044715 * x * x)
     with np.errstate(over="ignore"):
-        if name == "silu":
-            s = 1.0 / (1.0 + np.exp(-x))
-            return x * s, s + x * s * (1.0 - s)
-        c = math.sqrt(2.0 / math.pi)
-        t = np.tanh(c * (x + 0.044715 * x**3))
-        return 0.5 * x * (1.0 + t), 0.5 * (1.0 + t) + 0.5 * x * (1.0 - t * t) * c * (1.0 + 3 * 0.044715 * x * x)
+        s, rest = 1.0 / (1.0 + np.exp(-p)), 1.0 / (1.0 + np.exp(p))
+    return x * s, s + x * s * rest * dp
 
 
 def gated_fwd(Wds, X, A, B, alpha, name):
