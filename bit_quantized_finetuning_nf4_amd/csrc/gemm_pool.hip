@@ -344,7 +344,7 @@ double rounds(int64_t rows, int64_t tiles_m, int fi, int cus) {
 // tiles of 64 fi: what takes the least time.  A gated block's rows come in turns of
 // 32 (16 of each weight), and a tile may begin at any of them: every fi fits after
 // whole rounds.  Two weights of 22016 x 8192 and 4096 tokens: 40960 rows in ten
-// rounds, then 3072 in tiles of 192.
+// rounds, then the rest in tiles of 192.
 struct PoolTiles {
   int64_t whole;
   int fi;
